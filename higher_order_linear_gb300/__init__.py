@@ -16,7 +16,16 @@ from .hla2 import (  # noqa: F401
     hla2_forward_noalloc,
     hla2_forward_plan,
     hla2_forward_workspace,
+    hla2_gated_scan,
+    hla2_gated_scan_backward,
+    hla2_gated_scan_carry_len,
+    hla2_gated_scan_workspace,
+    hla2_gated_step,
     hla2_last_error_detail,
+    hla2_rmsnorm,
+    hla2_rmsnorm_backward,
+    hla2_rmsnorm_q8,
+    hla2_rotary,
     hla2_scan,
     hla2_state_to_pform,
     hla2_step,

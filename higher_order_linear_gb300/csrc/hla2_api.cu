@@ -201,6 +201,8 @@ void prof_commit(const PhaseEvents& pe) {
 }
 }  // namespace
 
+int sm_count() { return current_sm_count(); }
+
 void note_launches(int n) { g_launches.fetch_add(n, std::memory_order_relaxed); }
 
 int set_error(int code, const char* fmt, ...) {

@@ -20,6 +20,9 @@ enum DeviceError : int {
 // Address of this device's status word (looked up once per device).
 int* device_status_word();
 
+// SM count of the current device (queried once per device).
+int sm_count();
+
 // Counts kernel launches issued by the library (for instrumentation).
 void note_launches(int n);
 

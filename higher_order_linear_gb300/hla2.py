@@ -100,6 +100,28 @@ def lib() -> ctypes.CDLL:
             L.hla2_decay_forward.restype = i
             L.hla2_decay_step.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, ctypes.c_float, vp]
             L.hla2_decay_step.restype = i
+            ll, f, pll, pi = ctypes.c_longlong, ctypes.c_float, ctypes.POINTER(ctypes.c_longlong), ctypes.POINTER(i)
+            L.hla2_gated_scan_workspace.argtypes = [i, i, i, i]
+            L.hla2_gated_scan_workspace.restype = sz
+            L.hla2_gated_scan_carry_len.argtypes = [i, i]
+            L.hla2_gated_scan_carry_len.restype = sz
+            L.hla2_gated_scan.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, pll, i, i, i, i, vp, sz, vp]
+            L.hla2_gated_scan.restype = i
+            L.hla2_gated_scan_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, pll, i, i, i, i, vp,
+                                                   sz, vp]
+            L.hla2_gated_scan_backward.restype = i
+            L.hla2_gated_step.argtypes = [vp, vp, vp, vp, vp, i, i, pll, i, i, i, i, vp]
+            L.hla2_gated_step.restype = i
+            L.hla2_rmsnorm.argtypes = [vp, vp, vp, vp, vp, ll, i, ll, ll, ll, ll, f, i, i, i, vp]
+            L.hla2_rmsnorm.restype = i
+            L.hla2_rmsnorm_q8.argtypes = [vp, vp, vp, vp, vp, vp, ll, i, ll, ll, ll, ll, f, i, i, vp]
+            L.hla2_rmsnorm_q8.restype = i
+            L.hla2_rmsnorm_backward_workspace.argtypes = [ll, i]
+            L.hla2_rmsnorm_backward_workspace.restype = sz
+            L.hla2_rmsnorm_backward.argtypes = [vp, vp, vp, vp, vp, vp, ll, i, pll, f, i, i, i, vp, sz, vp]
+            L.hla2_rmsnorm_backward.restype = i
+            L.hla2_rotary.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, pi, i, i, pll, i, vp]
+            L.hla2_rotary.restype = i
             _lib = L
         return _lib
 
@@ -505,3 +527,449 @@ def hla2_decay_step(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: to
                     o: torch.Tensor | None = None, normalized: bool = False, stream=None) -> torch.Tensor:
     """One decayed decode step on the compact state [n, d*d + d*dv + d] (S|P|p, in place)."""
     return _step("hla2_decay_step", state, q, k, v, o, normalized, stream, pform_record_len, gamma=gamma)
+
+
+# ------------------------------------------------ around the attention layer ----
+# The gated linear recurrence, the root-mean-square norm and the rotary
+# positions.  Their tensors may be strided (the last dimension contiguous).
+_GATE_FORMS = {"sigmoid": 0, "decay": 1}
+
+
+class _NoGuard:
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_NO_GUARD = _NoGuard()
+
+
+def _guard(dev: torch.device, stream):
+    """Makes ``dev`` current, and ``stream`` (when given) too, so that what the
+    call allocates belongs to the stream it is used on.  Free of cost in the
+    common case."""
+    if stream is None:
+        return _NO_GUARD if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    return torch.cuda.stream(stream)
+
+
+def _operand(t, name: str, device=None, dtype=None, shape=None, dense=False) -> None:
+    """Checks of one operand of the calls below, before anything is allocated or launched."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the inputs on {device}")
+    if dense and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _last_dense(t: torch.Tensor, name: str) -> None:
+    if t.stride(-1) != 1 and t.shape[-1] != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+
+
+def _no_overlap(t: torch.Tensor, name: str) -> None:
+    """An output must not hold one element in two places."""
+    if any(st == 0 and n > 1 for st, n in zip(t.stride(), t.shape)):
+        raise ValueError(f"{name} must not be an expanded tensor")
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _out_like(t: torch.Tensor, dtype: torch.dtype) -> torch.Tensor:
+    """A new tensor of t's shape: t's memory order where t is dense in some order, else row-major."""
+    return torch.empty_like(t, dtype=dtype)
+
+
+def hla2_gated_scan_workspace(B: int, H: int, T: int, d: int) -> int:
+    return int(lib().hla2_gated_scan_workspace(B, H, T, d))
+
+
+def hla2_gated_scan_carry_len(T: int, d: int) -> int:
+    """Floats per head of the ``carry`` that a forward keeps for its backward."""
+    return int(lib().hla2_gated_scan_carry_len(T, d))
+
+
+def _gated_inputs(X, G, form, reset):
+    """Checks shared by the scan and its backward; returns (B, H, T, d, dtype code, form code, shared)."""
+    _operand(X, "X")
+    _operand(G, "G")
+    if X.dim() != 4 or (G.shape != X.shape and G.shape != X.shape[:3]):
+        raise ValueError("expected X [B,H,T,d] and G [B,H,T,d] or [B,H,T]")
+    if X.dtype != G.dtype:
+        raise ValueError(f"X and G must share a dtype (got {X.dtype}, {G.dtype})")
+    code = _dtype_code(X)
+    if form not in _GATE_FORMS:
+        raise ValueError(f"unknown gate form {form!r}: one of {sorted(_GATE_FORMS)}")
+    _operand(G, "G", X.device)
+    B, H, T, d = X.shape
+    shared = G.dim() == 3
+    _last_dense(X, "X")
+    if not shared:
+        _last_dense(G, "G")
+    if reset is not None:
+        if not isinstance(reset, torch.Tensor) or reset.dtype not in (torch.bool, torch.uint8):
+            raise ValueError("reset must be a bool or uint8 tensor")
+        _operand(reset, "reset", X.device, shape=(B, T), dense=True)
+    return B, H, T, d, code, _GATE_FORMS[form], shared
+
+
+def _gated_work(workspace, B, H, T, d, dev):
+    if workspace is not None:
+        return workspace, workspace.numel() * workspace.element_size()
+    need = hla2_gated_scan_workspace(B, H, T, d)
+    if need:
+        workspace = torch.empty(need, device=dev, dtype=torch.uint8)
+    return workspace, need
+
+
+def _strides(*tensors):
+    """The first three strides of each tensor (zeros for None), as the C entries take them."""
+    flat = []
+    for t in tensors:
+        flat += (0, 0, 0) if t is None else t.stride()[:3]
+    return (ctypes.c_longlong * len(flat))(*flat)
+
+
+def hla2_gated_scan(X: torch.Tensor, G: torch.Tensor, O: torch.Tensor | None = None, form: str = "sigmoid",
+                    reset: torch.Tensor | None = None, state_in: torch.Tensor | None = None,
+                    state_out: torch.Tensor | None = None, carry: torch.Tensor | None = None,
+                    out_dtype: torch.dtype = torch.float32, workspace: torch.Tensor | None = None,
+                    stream=None) -> torch.Tensor:
+    """Gated linear recurrence h_t = a_t h_{t-1} + u_t along the tokens of each
+    head: X [B,H,T,d], G [B,H,T,d] or [B,H,T] (one gate for a head's channels),
+    fp32 or bf16 -> O [B,H,T,d] of ``out_dtype`` (or O's own dtype).
+
+    ``form`` "sigmoid": a = sigmoid(G), u = (1 - a) X;  "decay": a = G, u = X.
+    ``reset`` [B,T] bool: a document begins there (h_{t-1} counts as zero).
+    ``state_in`` / ``state_out`` [B,H,d] fp32: h before and after.
+    ``carry`` [B,H,hla2_gated_scan_carry_len(T, d)] fp32 keeps what
+    hla2_gated_scan_backward needs."""
+    B, H, T, d, code, fcode, shared = _gated_inputs(X, G, form, reset)
+    dev = X.device
+    if O is not None:
+        _operand(O, "O", dev, shape=X.shape)
+        out_dtype = O.dtype
+        _last_dense(O, "O")
+        _no_overlap(O, "O")
+    if out_dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"unsupported output dtype {out_dtype}")
+    if state_in is not None:
+        _operand(state_in, "state_in", dev, torch.float32, (B, H, d), dense=True)
+    if state_out is not None:
+        _operand(state_out, "state_out", dev, torch.float32, (B, H, d), dense=True)
+    if carry is not None:
+        _operand(carry, "carry", dev, torch.float32, (B, H, hla2_gated_scan_carry_len(T, d)), dense=True)
+    if workspace is not None:
+        _operand(workspace, "workspace", dev, dense=True)
+    _cuda_device(X, "X")
+    with _guard(dev, stream):
+        if O is None:
+            O = _out_like(X, out_dtype)
+        workspace, nws = _gated_work(workspace, B, H, T, d, dev)
+        rc = lib().hla2_gated_scan(X.data_ptr(), G.data_ptr(), _ptr(reset), _ptr(state_in), O.data_ptr(),
+                                   _ptr(state_out), _ptr(carry), B, H, T, d, _strides(X, G, O), fcode, int(shared),
+                                   code, 1 if out_dtype == torch.bfloat16 else 0, _ptr(workspace), nws,
+                                   _stream(stream))
+    _check(rc, "hla2_gated_scan")
+    return O
+
+
+def hla2_gated_scan_backward(X: torch.Tensor, G: torch.Tensor, dO: torch.Tensor, carry: torch.Tensor,
+                             form: str = "sigmoid", reset: torch.Tensor | None = None,
+                             dstate_out: torch.Tensor | None = None, dX: torch.Tensor | None = None,
+                             dG: torch.Tensor | None = None, dstate_in: torch.Tensor | None = None,
+                             workspace: torch.Tensor | None = None, stream=None):
+    """Gradients (dX, dG) of hla2_gated_scan over the same X, G, ``form`` and
+    ``reset``; ``carry`` is what that call kept.  dO [B,H,T,d] is the gradient
+    of O, ``dstate_out`` that of state_out; ``dstate_in`` [B,H,d] fp32 receives
+    that of state_in.  A shared gate's dG [B,H,T] is summed over the channels."""
+    B, H, T, d, code, fcode, shared = _gated_inputs(X, G, form, reset)
+    dev = X.device
+    _operand(dO, "dO", dev, shape=X.shape)
+    ocode = _dtype_code(dO)
+    _last_dense(dO, "dO")
+    _operand(carry, "carry", dev, torch.float32, (B, H, hla2_gated_scan_carry_len(T, d)), dense=True)
+    for t, name, like in ((dX, "dX", X), (dG, "dG", G)):
+        if t is not None:
+            _operand(t, name, dev, like.dtype, like.shape)
+            if t.dim() == 4:
+                _last_dense(t, name)
+            _no_overlap(t, name)
+    for t, name in ((dstate_out, "dstate_out"), (dstate_in, "dstate_in")):
+        if t is not None:
+            _operand(t, name, dev, torch.float32, (B, H, d), dense=True)
+    if workspace is not None:
+        _operand(workspace, "workspace", dev, dense=True)
+    _cuda_device(X, "X")
+    with _guard(dev, stream):
+        if dX is None:
+            dX = _out_like(X, X.dtype)
+        if dG is None:
+            dG = _out_like(G, G.dtype)
+        workspace, nws = _gated_work(workspace, B, H, T, d, dev)
+        rc = lib().hla2_gated_scan_backward(X.data_ptr(), G.data_ptr(), _ptr(reset), carry.data_ptr(), dO.data_ptr(),
+                                            _ptr(dstate_out), dX.data_ptr(), dG.data_ptr(), _ptr(dstate_in), B, H, T,
+                                            d, _strides(X, G, dO, dX, dG), fcode, int(shared), code, ocode,
+                                            _ptr(workspace), nws, _stream(stream))
+    _check(rc, "hla2_gated_scan_backward")
+    return dX, dG
+
+
+def hla2_gated_step(state: torch.Tensor, x: torch.Tensor, g: torch.Tensor, o: torch.Tensor | None = None,
+                    form: str = "sigmoid", out_dtype: torch.dtype = torch.float32,
+                    state_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """One token of the recurrence for n heads: state [n,d] fp32, x [n,d] and
+    g [n,d] or [n] (fp32 or bf16) -> o [n,d].  The state is updated in place,
+    or left and the new one written to ``state_out``."""
+    _operand(x, "x")
+    if x.dim() != 2:
+        raise ValueError("hla2_gated_step: expected x [n,d]")
+    n, d = x.shape
+    dev = x.device
+    _operand(g, "g", dev)
+    shared = g.dim() == 1
+    if g.shape != x.shape and g.shape != x.shape[:1]:
+        raise ValueError("hla2_gated_step: expected g [n,d] or [n]")
+    if g.dtype != x.dtype:
+        raise ValueError(f"x and g must share a dtype (got {x.dtype}, {g.dtype})")
+    code = _dtype_code(x)
+    if form not in _GATE_FORMS:
+        raise ValueError(f"unknown gate form {form!r}: one of {sorted(_GATE_FORMS)}")
+    _last_dense(x, "x")
+    if not shared:
+        _last_dense(g, "g")
+    _operand(state, "state", dev, torch.float32, x.shape, dense=True)
+    if state_out is not None:
+        _operand(state_out, "state_out", dev, torch.float32, x.shape, dense=True)
+    if o is not None:
+        _operand(o, "o", dev, shape=x.shape)
+        _last_dense(o, "o")
+        _no_overlap(o, "o")
+        out_dtype = o.dtype
+    if out_dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"unsupported output dtype {out_dtype}")
+    _cuda_device(x, "x")
+    with _guard(dev, stream):
+        if o is None:
+            o = torch.empty((n, d), device=dev, dtype=out_dtype)
+        ld = (ctypes.c_longlong * 3)(x.stride(0), g.stride(0), o.stride(0))
+        rc = lib().hla2_gated_step(state.data_ptr(), x.data_ptr(), g.data_ptr(), o.data_ptr(), _ptr(state_out), n, d,
+                                   ld, _GATE_FORMS[form], int(shared), code, 1 if out_dtype == torch.bfloat16 else 0,
+                                   _stream(stream))
+    _check(rc, "hla2_gated_step")
+    return o
+
+
+def _rows(t: torch.Tensor, name: str):
+    """(row stride) of a tensor whose leading dimensions run through its rows with one stride."""
+    C = t.shape[-1]
+    if t.is_contiguous():
+        return C
+    _last_dense(t, name)
+    ld, expect = None, None
+    for n, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if n == 1:
+            continue
+        if ld is None:
+            ld, expect = st, st * n
+        elif st == expect:
+            expect = st * n
+        else:
+            raise ValueError(f"{name}: its rows must have one stride")
+    if ld is None:
+        return C
+    if ld < C:
+        raise ValueError(f"{name}: its rows overlap")
+    return ld
+
+
+def _norm_inputs(X, weight, residual, eps):
+    """Checks shared by the norms; returns (rows, C, dtype code, weight dtype code)."""
+    _operand(X, "X")
+    if X.dim() < 1:
+        raise ValueError("X must have at least one dimension")
+    code = _dtype_code(X)
+    C = X.shape[-1]
+    rows = X.numel() // C if C else 0
+    wcode = 0
+    if weight is not None:
+        _operand(weight, "weight", X.device, shape=(C,), dense=True)
+        wcode = _dtype_code(weight)
+    if residual is not None:
+        _operand(residual, "residual", X.device, X.dtype, X.shape)
+    if not eps >= 0:
+        raise ValueError("eps must not be negative")
+    return rows, C, code, wcode
+
+
+def _norm_outputs(X, residual, S):
+    """The row strides of X, residual and S; S is wanted with a residual."""
+    ldx = _rows(X, "X")
+    ldr = _rows(residual, "residual") if residual is not None else 0
+    if S is not None:
+        _operand(S, "S", X.device, X.dtype, X.shape)
+        _rows(S, "S")
+    return ldx, ldr
+
+
+def hla2_rmsnorm(X: torch.Tensor, weight: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+                 Y: torch.Tensor | None = None, S: torch.Tensor | None = None, eps: float = 1e-6,
+                 out_dtype: torch.dtype | None = None, stream=None):
+    """Root-mean-square norm of the rows of t = X (+ residual):
+    Y = t / sqrt(mean(t^2) + eps) * weight.  X [..., C] fp32 or bf16, weight [C].
+    Returns (Y, S): Y of ``out_dtype`` (X's by default), S = t in X's dtype,
+    the new residual stream (None without a residual unless S is given)."""
+    rows, C, code, wcode = _norm_inputs(X, weight, residual, eps)
+    dev = X.device
+    ldx, ldr = _norm_outputs(X, residual, S)
+    if Y is not None:
+        _operand(Y, "Y", dev, shape=X.shape)
+        out_dtype = Y.dtype
+        _rows(Y, "Y")
+    elif out_dtype is None:
+        out_dtype = X.dtype
+    if out_dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"unsupported output dtype {out_dtype}")
+    _cuda_device(X, "X")
+    with _guard(dev, stream):
+        if Y is None:
+            Y = torch.empty(X.shape, device=dev, dtype=out_dtype)
+        if S is None and residual is not None:
+            S = torch.empty(X.shape, device=dev, dtype=X.dtype)
+        rc = lib().hla2_rmsnorm(X.data_ptr(), _ptr(residual), _ptr(weight), _ptr(S), Y.data_ptr(), rows, C, ldx, ldr,
+                                _rows(S, "S") if S is not None else 0, _rows(Y, "Y"), eps, code, wcode,
+                                1 if out_dtype == torch.bfloat16 else 0, _stream(stream))
+    _check(rc, "hla2_rmsnorm")
+    return Y, S
+
+
+def hla2_rmsnorm_q8(X: torch.Tensor, weight: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+                    Q: torch.Tensor | None = None, scale: torch.Tensor | None = None, S: torch.Tensor | None = None,
+                    eps: float = 1e-6, stream=None):
+    """The norm of hla2_rmsnorm with an 8-bit output: returns (Q, scale, S), Q
+    [..., C] float8_e4m3fn and scale [...] fp32 with Y = Q * scale (scale =
+    max|Y| / 448 of the row, 1 for a row of zeros)."""
+    rows, C, code, wcode = _norm_inputs(X, weight, residual, eps)
+    dev = X.device
+    ldx, ldr = _norm_outputs(X, residual, S)
+    if Q is not None:
+        _operand(Q, "Q", dev, torch.float8_e4m3fn, X.shape)
+        _rows(Q, "Q")
+    if scale is not None:
+        _operand(scale, "scale", dev, torch.float32, X.shape[:-1], dense=True)
+    _cuda_device(X, "X")
+    with _guard(dev, stream):
+        if Q is None:
+            Q = torch.empty(X.shape, device=dev, dtype=torch.float8_e4m3fn)
+        if scale is None:
+            scale = torch.empty(X.shape[:-1], device=dev, dtype=torch.float32)
+        if S is None and residual is not None:
+            S = torch.empty(X.shape, device=dev, dtype=X.dtype)
+        rc = lib().hla2_rmsnorm_q8(X.data_ptr(), _ptr(residual), _ptr(weight), _ptr(S), Q.data_ptr(), scale.data_ptr(),
+                                   rows, C, ldx, ldr, _rows(S, "S") if S is not None else 0, _rows(Q, "Q"), eps, code,
+                                   wcode, _stream(stream))
+    _check(rc, "hla2_rmsnorm_q8")
+    return Q, scale, S
+
+
+def hla2_rmsnorm_backward(S: torch.Tensor, dY: torch.Tensor, weight: torch.Tensor | None = None,
+                          dS: torch.Tensor | None = None, dX: torch.Tensor | None = None, eps: float = 1e-6,
+                          workspace: torch.Tensor | None = None, stream=None):
+    """Gradients of the norm at t = S (what the forward kept, or X without a
+    residual): dX (of X and of the residual; ``dS``, the gradient that reaches
+    the residual stream, is added) in S's dtype, and dW [C] fp32 (None without
+    a weight)."""
+    rows, C, code, wcode = _norm_inputs(S, weight, dS, eps)
+    dev = S.device
+    _operand(dY, "dY", dev, shape=S.shape)
+    ycode = _dtype_code(dY)
+    lds, ldy = _rows(S, "S"), _rows(dY, "dY")
+    ldd = _rows(dS, "dS") if dS is not None else 0
+    if dX is not None:
+        _operand(dX, "dX", dev, S.dtype, S.shape)
+        _rows(dX, "dX")
+    if workspace is not None:
+        _operand(workspace, "workspace", dev, dense=True)
+    _cuda_device(S, "S")
+    with _guard(dev, stream):
+        if dX is None:
+            dX = torch.empty(S.shape, device=dev, dtype=S.dtype)
+        dW, nws = None, 0
+        if weight is not None:
+            dW = torch.empty((C,), device=dev, dtype=torch.float32)
+            if workspace is None:
+                workspace = torch.empty(int(lib().hla2_rmsnorm_backward_workspace(rows, C)), device=dev,
+                                        dtype=torch.uint8)
+            nws = workspace.numel() * workspace.element_size()
+        ld = (ctypes.c_longlong * 4)(lds, ldy, ldd, _rows(dX, "dX"))
+        rc = lib().hla2_rmsnorm_backward(S.data_ptr(), dY.data_ptr(), _ptr(weight), _ptr(dS), dX.data_ptr(), _ptr(dW),
+                                         rows, C, ld, eps, code, wcode, ycode, _ptr(workspace), nws, _stream(stream))
+    _check(rc, "hla2_rmsnorm_backward")
+    return dX, dW
+
+
+def hla2_rotary(Q: torch.Tensor, pos: torch.Tensor, freq: torch.Tensor, sections, K: torch.Tensor | None = None,
+                OQ: torch.Tensor | None = None, OK: torch.Tensor | None = None, interleaved: bool = False,
+                inverse: bool = False, stream=None):
+    """Rotary positions with several axes: pair p of each head's first
+    2 * len(freq) channels turns by pos[axis of p] * freq[p] (``inverse``: back,
+    which is the gradient).  Q [B,H,T,d], K [B,HK,T,d] fp32 or bf16; pos int32
+    [axes,B,T] or [axes,T]; freq fp32 [pairs]; ``sections``: how many pairs
+    follow each axis, in order.  Pairs are (p, p + pairs), or (2p, 2p + 1) when
+    ``interleaved``.  OQ and OK may be Q and K.  Returns (OQ, OK)."""
+    _operand(Q, "Q")
+    if Q.dim() != 4:
+        raise ValueError("expected Q [B,H,T,d]")
+    code = _dtype_code(Q)
+    B, H, T, d = Q.shape
+    dev = Q.device
+    HK = 0
+    if K is not None:
+        _operand(K, "K", dev, Q.dtype)
+        if K.dim() != 4 or K.shape[0] != B or K.shape[2:] != Q.shape[2:]:
+            raise ValueError("expected K [B,HK,T,d] with Q's B, T and d")
+        HK = K.shape[1]
+        _last_dense(K, "K")
+    elif OK is not None:
+        raise ValueError("OK without K")
+    _last_dense(Q, "Q")
+    sections = tuple(int(s) for s in sections)
+    axes = len(sections)
+    _operand(pos, "pos", dev, torch.int32)
+    if pos.shape != (axes, B, T) and pos.shape != (axes, T):
+        raise ValueError(f"pos has shape {tuple(pos.shape)}, expected {(axes, B, T)} or {(axes, T)}")
+    _last_dense(pos, "pos")
+    _operand(freq, "freq", dev, torch.float32, dense=True)
+    if freq.dim() != 1 or sum(sections) != freq.numel():
+        raise ValueError(f"freq must hold one frequency for each of the sections' {sum(sections)} pairs")
+    for o, name, like in ((OQ, "OQ", Q), (OK, "OK", K)):
+        if o is not None:
+            _operand(o, name, dev, like.dtype, like.shape)
+            _last_dense(o, name)
+            _no_overlap(o, name)
+    _cuda_device(Q, "Q")
+    with _guard(dev, stream):
+        if OQ is None:
+            OQ = _out_like(Q, Q.dtype)
+        if OK is None and K is not None:
+            OK = _out_like(K, K.dtype)
+        st = [*Q.stride()[:3], *OQ.stride()[:3]]
+        st += (*K.stride()[:3], *OK.stride()[:3]) if K is not None else (0,) * 6
+        st += (pos.stride(0), pos.stride(1) if pos.dim() == 3 else 0)
+        rc = lib().hla2_rotary(Q.data_ptr(), OQ.data_ptr(), _ptr(K), _ptr(OK), pos.data_ptr(), freq.data_ptr(), B, H,
+                               HK, T, d, 2 * freq.numel(), axes, (ctypes.c_int * axes)(*sections),
+                               int(bool(interleaved)), int(bool(inverse)), (ctypes.c_longlong * 14)(*st), code,
+                               _stream(stream))
+    _check(rc, "hla2_rotary")
+    return OQ, OK

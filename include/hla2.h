@@ -350,6 +350,140 @@ HLA2_API int hla2_decay_forward_path(int d, int dv, int dtype, int normalized, i
 HLA2_API int hla2_decay_step(float* state, const float* q, const float* k, const float* v, float* o,
                              int n, int d, int dv, int normalized, float gamma, hla2_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Operators around the attention layer (no counterpart on the pages): a
+ * gated linear recurrence, a root-mean-square norm and rotary positions.
+ *
+ * Unlike the calls above, their tensors may be strided: every stride is in
+ * elements, the last dimension is contiguous, and pointers need only their
+ * element's alignment (16-byte alignment of base and strides picks the wide
+ * accesses).  A NULL strides argument means dense tensors.
+ * ------------------------------------------------------------------------ */
+
+enum { HLA2_GATE_SIGMOID = 0, HLA2_GATE_DECAY = 1 };
+
+/*
+ * Gated linear recurrence along the tokens of each head and channel,
+ *   h_t = a_t h_{t-1} + u_t,   o_t = h_t,
+ *   form HLA2_GATE_SIGMOID: a_t = 1 / (1 + exp(-g_t)), u_t = (1 - a_t) x_t;
+ *   form HLA2_GATE_DECAY:   a_t = g_t, u_t = x_t.
+ *
+ *   X          [B][H][T][d], dtype.
+ *   G          [B][H][T][d], or [B][H][T] when gate_shared (one gate for all
+ *              channels of a head), dtype.
+ *   reset      optional [B][T] bytes: where nonzero, h_{t-1} counts as zero
+ *              (a document begins at t), even when it is inf or NaN.
+ *   state_in   optional [B][H][d] fp32, h before the first token (else zero).
+ *   O          [B][H][T][d], out_dtype.
+ *   state_out  optional [B][H][d] fp32, h after the last token.
+ *   carry      optional [B][H][hla2_gated_scan_carry_len(T, d)] fp32: the
+ *              states entering each tile of tokens, kept for the backward.
+ *   strides    NULL, or nine values: X (b, h, t), G (b, h, t), O (b, h, t).
+ *   workspace  hla2_gated_scan_workspace(...) bytes, 16-byte aligned, not
+ *              initialised; NULL when that is 0.  It serves one call at a time.
+ * All sums are fp32.  Tokens are joined in a fixed order: the same call gives
+ * the same bits.  |a_t| is meant to be at most 1; with larger decays the
+ * product of the decays of a run of 32768 tokens must stay finite.
+ * Errors: HLA2_ERR_INVALID, HLA2_ERR_UNSUPPORTED (d > 128, B*H > 65535,
+ * unknown form or type), HLA2_ERR_WORKSPACE, HLA2_ERR_LAUNCH.
+ */
+HLA2_API size_t hla2_gated_scan_workspace(int B, int H, int T, int d);
+HLA2_API size_t hla2_gated_scan_carry_len(int T, int d);
+HLA2_API int hla2_gated_scan(const void* X, const void* G, const unsigned char* reset, const float* state_in, void* O,
+                             float* state_out, float* carry, int B, int H, int T, int d, const long long* strides,
+                             int form, int gate_shared, int dtype, int out_dtype, void* workspace, size_t ws_bytes,
+                             hla2_stream_t stream);
+
+/*
+ * Gradients of hla2_gated_scan.  With lam_t = dO_t + a_{t+1} lam_{t+1}
+ * (dstate_out added at the last token; a_{t+1} counts as zero at a reset):
+ *   decay:   dX = lam,            dG = lam h_{t-1};
+ *   sigmoid: dX = (1 - a) lam,    dG = lam a (1 - a) (h_{t-1} - x);
+ *   dstate_in = a_0 lam_0.
+ *   carry       as written by the forward over the same X, G, reset, state_in.
+ *   dO          [B][H][T][d], out_dtype.      dstate_out  optional [B][H][d] fp32.
+ *   dX, dG      like X and G (dtype); a shared gate's dG is the sum over the
+ *               head's channels.              dstate_in   optional [B][H][d] fp32.
+ *   strides     NULL, or fifteen values: X, G, dO, dX, dG (b, h, t each).
+ * Workspace and errors as for the forward.
+ */
+HLA2_API int hla2_gated_scan_backward(const void* X, const void* G, const unsigned char* reset, const float* carry,
+                                      const void* dO, const float* dstate_out, void* dX, void* dG, float* dstate_in,
+                                      int B, int H, int T, int d, const long long* strides, int form, int gate_shared,
+                                      int dtype, int out_dtype, void* workspace, size_t ws_bytes,
+                                      hla2_stream_t stream);
+
+/*
+ * One token of the recurrence for n heads: h = a state + u, o = h.
+ *   state [n][d] fp32;  x [n][d], g [n][d] (or [n] when gate_shared), dtype;
+ *   o [n][d], out_dtype;  state_out [n][d] fp32, or NULL to update in place.
+ *   ld: row strides of x, g and o, or NULL for dense; the states are dense.
+ * Errors as for the forward (n <= 0: HLA2_ERR_INVALID).
+ */
+HLA2_API int hla2_gated_step(float* state, const void* x, const void* g, void* o, float* state_out, int n, int d,
+                             const long long* ld, int form, int gate_shared, int dtype, int out_dtype,
+                             hla2_stream_t stream);
+
+/*
+ * Root-mean-square norm of rows, with the residual's addition:
+ *   t = X + R,   Y = t / sqrt(mean(t^2) + eps) * W.
+ *   X, R  [rows][C] dtype (R optional);   W  [C], wdtype (NULL: ones);
+ *   S     t rounded to dtype, the new residual stream (optional, may be X or R);
+ *   Y     [rows][C] out_dtype.
+ *   ldx, ldr, lds, ldy: row strides in elements, at least C.
+ * The norm is taken of t before its rounding.  Sums are fp32.
+ * Errors: HLA2_ERR_INVALID, HLA2_ERR_UNSUPPORTED (C > 16384, types).
+ */
+HLA2_API int hla2_rmsnorm(const void* X, const void* R, const void* W, void* S, void* Y, long long rows, int C,
+                          long long ldx, long long ldr, long long lds, long long ldy, float eps, int dtype,
+                          int wdtype, int out_dtype, hla2_stream_t stream);
+
+/*
+ * The same norm with an 8-bit output: row r of Y is stored as
+ *   Q = e4m3(Y / scale[r]) (round to nearest even, saturating),
+ *   scale[r] = max|Y_r| / 448, or 1 for a row of zeros.
+ * A row that holds NaN or inf has a NaN or infinite scale and NaN in those places.
+ *   Q [rows][C] bytes, row stride ldq;  scale [rows] fp32.
+ */
+HLA2_API int hla2_rmsnorm_q8(const void* X, const void* R, const void* W, void* S, void* Q, float* scale,
+                             long long rows, int C, long long ldx, long long ldr, long long lds, long long ldq,
+                             float eps, int dtype, int wdtype, hla2_stream_t stream);
+
+/*
+ * Gradients of hla2_rmsnorm at the stored t (S of the forward; X without a
+ * residual).  With n = t rstd and rstd = 1 / sqrt(mean(t^2) + eps):
+ *   dX = rstd (W dY - n mean(W dY n)) + dS    (the gradient of X and of R),
+ *   dW = sum over rows of dY n.
+ *   S, dS, dX [rows][C] dtype (dS optional: the gradient that reaches the
+ *   residual stream);  dY [rows][C] out_dtype;  dW [C] fp32 (optional).
+ *   ld: row strides of S, dY, dS, dX, or NULL for dense.
+ *   workspace  hla2_rmsnorm_backward_workspace(rows, C) bytes, needed with dW.
+ */
+HLA2_API size_t hla2_rmsnorm_backward_workspace(long long rows, int C);
+HLA2_API int hla2_rmsnorm_backward(const void* S, const void* dY, const void* W, const void* dS, void* dX, float* dW,
+                                   long long rows, int C, const long long* ld, float eps, int dtype, int wdtype,
+                                   int out_dtype, void* workspace, size_t ws_bytes, hla2_stream_t stream);
+
+/*
+ * Rotary positions with several axes, on queries and (optionally) keys.
+ * Pair p of a head's first `rot` channels turns by
+ *   angle = pos[axis(p)][b][t] * freq[p]   (radians),
+ * where the first sections[0] pairs follow axis 0, the next sections[1] axis 1
+ * and so on: (x, y) -> (x cos - y sin, x sin + y cos), or the inverse turn,
+ * which is also the gradient, when `inverse`.  Channels from rot on are copied.
+ *   Q, OQ  [B][H][T][d];  K, OK  [B][HK][T][d] (NULL, HK = 0: none); dtype.
+ *          An output may be its input.
+ *   pos    int32, [naxes][B][T];  freq  [rot/2] fp32.
+ *   sections  naxes (1..4) positive counts on the host, adding up to rot/2.
+ *   interleaved  pair p is channels (2p, 2p + 1); else (p, p + rot/2).
+ *   strides   NULL, or fourteen values: Q, OQ, K, OK (b, h, t each), pos (axis, b).
+ * The angle is reduced exactly (its error does not grow with the position).
+ * Errors: HLA2_ERR_INVALID, HLA2_ERR_UNSUPPORTED (d > 128, types).
+ */
+HLA2_API int hla2_rotary(const void* Q, void* OQ, const void* K, void* OK, const int* pos, const float* freq, int B,
+                         int H, int HK, int T, int d, int rot, int naxes, const int* sections, int interleaved,
+                         int inverse, const long long* strides, int dtype, hla2_stream_t stream);
+
 /*
  * Copies the calling host thread's last error reason (NUL-terminated,
  * truncated to n bytes) into buf.  Returns the length of the full message.
