@@ -12,12 +12,46 @@
 // Gradient, lam_t = dh_t + a_{t+1} lam_{t+1}:
 //   decay:   dx = lam,    dg = lam h_{t-1}
 //   sigmoid: dx = z lam,  dg = z (1 - z) lam (h_{t-1} - x)
+//
+// One pass over the data.  A run of tokens maps the state before it to the
+// state after it by h -> A h + X, and such maps compose, so a tile of tokens
+// can be read once, long before the state that enters it is known:
+//   - a block holds a tile in registers: a thread 4 channels of kTok tokens, a
+//     "run"; the runs' maps are composed in shared memory;
+//   - the tile's map goes to the workspace; the state that enters the tile is
+//     the state that entered its super-group of 128 tiles, passed through the
+//     maps of the groups of 8 tiles, then of the tiles, before it; warps of their
+//     own do this, so that no thread holds its tokens and these maps at once;
+//   - every thread then walks its tokens again, from registers, from the state
+//     that enters its run.
+// Tiles are taken by ticket, all heads' first tiles first, so whoever waits
+// waits for a tile that a running block holds.  Which maps are composed, and in
+// which order, depends on the tile's place alone: the same call gives the same
+// bits, whatever the timing.  The last tile of a group publishes the group's
+// map and the last of a super-group the state after it, so a tile reads at most
+// 22 maps and one state, and the only chain along the sequence has one link for
+// each 128 tiles.
+#include <map>
+#include <mutex>
+
 #include "hla2_layer.cuh"
 
 namespace hla2 {
 namespace {
 
-constexpr int kTile = 64;  // tokens between two kept states
+constexpr int kTok = 8;         // tokens of a thread's run
+constexpr int kCh = 4;          // channels of a thread
+constexpr int kData = 256;      // threads that hold a tile
+constexpr int kGroup = 8;       // tiles to a group
+constexpr int kSuper = 16;      // groups to a super-group
+constexpr unsigned long long kGateWaitNs = 2000000000ull;  // bounded waits: 2 s
+
+// Lanes that share a token: they cover 4 channels each, d <= 4 lanes.
+__host__ __device__ constexpr int lanes_of(int d) { return d <= 64 ? 16 : 32; }
+// Tokens of a tile: a state is kept for the gradient at the start of each.
+__host__ __device__ constexpr int tile_of(int lanes) { return kData / lanes * kTok; }
+// Threads of a block: those that hold the tile, and a warp for each 32 channels that joins tiles.
+__host__ __device__ constexpr int block_threads(int lanes) { return kData + lanes * kCh; }
 
 struct GateParams {
     const void *x, *g, *dout;
@@ -27,6 +61,12 @@ struct GateParams {
     float *state_out, *dstate_in, *carry;
     int B, H, T, d;
     long long sx[3], sg[3], so[3], sdo[3], sdx[3], sdg[3];
+    // workspace (null for one tile): see Lookback
+    unsigned* words;
+    float* maps;
+    int tiles, out_bf16;
+    unsigned total;  // rows * tiles
+    int* status;
 };
 
 // z = 1 - a of the sigmoid gate
@@ -35,81 +75,446 @@ __device__ __forceinline__ float keep_out(float g) {
     return isinf(e) ? 1.f : __fdividef(e, 1.f + e);
 }
 
-template <typename T, typename TO, bool SIG, bool SHARED>
-__global__ void __launch_bounds__(128) gated_simple_kernel(const GateParams p) {
-    const int c = threadIdx.x, b = blockIdx.x / p.H, hd = blockIdx.x % p.H;
-    if (c >= p.d) return;
-    const long long row = (long long)blockIdx.x * p.d + c;
-    const int tiles = (p.T + kTile - 1) / kTile;
-    const T* x = static_cast<const T*>(p.x) + b * p.sx[0] + hd * p.sx[1] + c;
-    const T* g = static_cast<const T*>(p.g) + b * p.sg[0] + hd * p.sg[1] + (SHARED ? 0 : c);
-    TO* o = static_cast<TO*>(p.o) + b * p.so[0] + hd * p.so[1] + c;
-    float h = p.state_in ? p.state_in[row] : 0.f;
-    for (int t = 0; t < p.T; ++t) {
-        if (p.carry && t % kTile == 0) p.carry[((long long)blockIdx.x * tiles + t / kTile) * p.d + c] = h;
-        if (p.reset && p.reset[(long long)b * p.T + t]) h = 0.f;
-        const float xv = to_f32(x[t * p.sx[2]]), gv = to_f32(g[t * p.sg[2]]);
-        h = SIG ? fmaf(keep_out(gv), xv - h, h) : fmaf(gv, h, xv);
-        o[t * p.so[2]] = from_f32<TO>(h);
-    }
-    if (p.state_out) p.state_out[row] = h;
+// ---- maps h -> A h + X -------------------------------------------------------
+// A run that holds a reset forgets what entered it: its A is -0, which nothing
+// else is (products that are zero are made +0), and then only X counts.
+__device__ __forceinline__ float cut() { return __uint_as_float(0x80000000u); }
+__device__ __forceinline__ bool is_cut(float A) { return __float_as_uint(A) == 0x80000000u; }
+__device__ __forceinline__ float pass(float2 m, float h) { return is_cut(m.x) ? m.y : fmaf(m.x, h, m.y); }
+// first `a`, then `b`
+__device__ __forceinline__ float2 then(float2 a, float2 b) {
+    return make_float2(is_cut(b.x) || is_cut(a.x) ? cut() : a.x * b.x + 0.f, pass(b, a.y));
 }
 
-template <typename T, typename TO, bool SIG, bool SHARED>
-__global__ void __launch_bounds__(128) gated_simple_bwd_kernel(const GateParams p) {
-    __shared__ float before[kTile][128];  // h_{t-1} of this tile's tokens
-    __shared__ float part[128];
-    const int c = threadIdx.x, b = blockIdx.x / p.H, hd = blockIdx.x % p.H;
-    const bool in = c < p.d;
-    const long long row = (long long)blockIdx.x * p.d + c;
-    const int tiles = (p.T + kTile - 1) / kTile;
-    const int cc = in ? c : 0;
-    const T* x = static_cast<const T*>(p.x) + b * p.sx[0] + hd * p.sx[1] + cc;
-    const T* g = static_cast<const T*>(p.g) + b * p.sg[0] + hd * p.sg[1] + (SHARED ? 0 : cc);
-    const TO* dout = static_cast<const TO*>(p.dout) + b * p.sdo[0] + hd * p.sdo[1] + cc;
-    T* dx = static_cast<T*>(p.dx) + b * p.sdx[0] + hd * p.sdx[1] + cc;
-    T* dg = static_cast<T*>(p.dg) + b * p.sdg[0] + hd * p.sdg[1] + (SHARED ? 0 : cc);
-    float mu = in && p.dstate_out ? p.dstate_out[row] : 0.f;  // a_{t+1} lam_{t+1}
-    for (int tile = tiles - 1; tile >= 0; --tile) {
-        const int t0 = tile * kTile, t1 = min(p.T, t0 + kTile);
-        float h = in ? p.carry[((long long)blockIdx.x * tiles + tile) * p.d + c] : 0.f;
-        for (int t = t0; t < t1; ++t) {
-            if (p.reset && p.reset[(long long)b * p.T + t]) h = 0.f;
-            before[t - t0][c] = h;
-            const float xv = to_f32(x[t * p.sx[2]]), gv = to_f32(g[t * p.sg[2]]);
-            h = SIG ? fmaf(keep_out(gv), xv - h, h) : fmaf(gv, h, xv);
-        }
-        for (int t = t1 - 1; t >= t0; --t) {
-            const float xv = to_f32(x[t * p.sx[2]]), gv = to_f32(g[t * p.sg[2]]), hb = before[t - t0][c];
-            const float lam = to_f32(dout[t * p.sdo[2]]) + mu;
-            float gx, gg, a;
-            if (SIG) {
-                const float z = keep_out(gv);
-                a = 1.f - z;
-                gx = z * lam;
-                gg = gx * a * (hb - xv);
-            } else {
-                a = gv;
-                gx = lam;
-                gg = lam * hb;
-            }
-            mu = (p.reset && p.reset[(long long)b * p.T + t]) ? 0.f : a * lam;
-            if (in) dx[t * p.sdx[2]] = from_f32<T>(gx);
-            if (SHARED) {
-                __syncthreads();
-                part[c] = in ? gg : 0.f;
-                __syncthreads();
-                if (c == 0) {
-                    float s = 0.f;
-                    for (int i = 0; i < p.d; ++i) s += part[i];
-                    dg[t * p.sdg[2]] = from_f32<T>(s);
+// ---- the workspace -----------------------------------------------------------
+// words: [0] ticket, [1] a wait ran out, then a flag for each (row, tile, warp),
+// (row, group, warp) and (row, super-group, warp): zeroed before the launch.
+// maps: tile maps, group maps (float2 for each of the row's channels), states
+// that enter the super-groups (float).  A warp holds 32 channels of the maps and
+// reads only what the same warp of other blocks published.
+struct Lookback {
+    int rows, tiles, groups, supers, cb;  // cb: channels of a map, 32 to a warp
+    __host__ __device__ Lookback(int rows, int tiles, int cb)
+        : rows(rows), tiles(tiles), groups((tiles + kGroup - 1) / kGroup),
+          supers((groups + kSuper - 1) / kSuper), cb(cb) {}
+    __host__ __device__ size_t warps() const { return (size_t)cb / 32; }
+    __host__ __device__ size_t tile_flag(int r, int t) const { return 2 + ((size_t)r * tiles + t) * warps(); }
+    __host__ __device__ size_t group_flag(int r, int g) const {
+        return tile_flag(rows, 0) + ((size_t)r * groups + g) * warps();
+    }
+    __host__ __device__ size_t super_flag(int r, int s) const {
+        return group_flag(rows, 0) + ((size_t)r * supers + s) * warps();
+    }
+    __host__ __device__ size_t words() const { return super_flag(rows, 0); }
+    __host__ __device__ size_t tile_map(int r, int t) const { return ((size_t)r * tiles + t) * cb * 2; }
+    __host__ __device__ size_t group_map(int r, int g) const {
+        return tile_map(rows, 0) + ((size_t)r * groups + g) * cb * 2;
+    }
+    __host__ __device__ size_t super_state(int r, int s) const {
+        return group_map(rows, 0) + ((size_t)r * supers + s) * cb;
+    }
+    __host__ __device__ size_t floats() const { return super_state(rows, 0); }
+};
+
+__device__ __forceinline__ unsigned ld_acquire(const unsigned* p) {
+    unsigned v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_release(unsigned* p, unsigned v) {
+    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+__device__ __forceinline__ unsigned long long gate_timer() {
+    unsigned long long t;
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+    return t;
+}
+
+// Waits until the flag of every lane that has one is set (at most 2 s, then this
+// call's results are void: the status word says so, and every later wait of the
+// call gives up at once).
+__device__ __forceinline__ void wait_flags(const GateParams& p, const unsigned* flag) {
+    bool ok = flag == nullptr || ld_acquire(flag) != 0;
+    if (!__all_sync(0xffffffffu, ok)) {
+        const unsigned long long t0 = gate_timer();
+        bool give_up = false;
+        while (!__all_sync(0xffffffffu, ok)) {
+            if (!ok) ok = ld_acquire(flag) != 0;
+            if (!ok && (gate_timer() - t0 > kGateWaitNs || *(volatile unsigned*)(p.words + 1) != 0)) give_up = true;
+            if (__any_sync(0xffffffffu, give_up)) {
+                if ((threadIdx.x & 31) == 0) {
+                    atomicExch(p.words + 1, 1u);
+                    atomicExch(p.status, (int)kDevWaitTimeout);
                 }
-            } else if (in) {
-                dg[t * p.sdg[2]] = from_f32<T>(gg);
+                break;
             }
         }
     }
-    if (in && p.dstate_in) p.dstate_in[row] = mu;
+    __syncwarp();
+}
+
+// One warp's part for its 32 channels: publishes the tile's map `m`, returns the
+// state that enters the tile.  `start`: the state that enters the sequence.
+// `n` counts tiles in the order of the walk.  Every lane calls it.
+__device__ __forceinline__ float enter_tile(const GateParams& p, const Lookback& lb, int row, int n, int warp, float2 m,
+                                            float start) {
+    const int lane = threadIdx.x & 31, ch = warp * 32 + lane;
+    const int g = n / kGroup, s = g / kSuper;
+    const int nt = n % kGroup, ng = g % kSuper;  // tiles before this one in its group, groups before it in the super-group
+    const bool ends_group = nt == kGroup - 1, ends_super = ends_group && ng == kSuper - 1;
+    float* maps = p.maps;
+    if (n + 1 < lb.tiles) {
+        *reinterpret_cast<float2*>(maps + lb.tile_map(row, n) + 2 * ch) = m;
+        __syncwarp();
+        if (lane == 0) st_release(p.words + lb.tile_flag(row, n) + warp, 1u);
+    }
+    // the tiles of the group first: the group's map waits for nothing else
+    wait_flags(p, lane < nt ? p.words + lb.tile_flag(row, n - nt + lane) + warp : nullptr);
+    float2 w[kGroup - 1];
+#pragma unroll
+    for (int i = 0; i < kGroup - 1; ++i)
+        if (i < nt) w[i] = __ldcg(reinterpret_cast<const float2*>(maps + lb.tile_map(row, n - nt + i) + 2 * ch));
+    if (ends_group && n + 1 < lb.tiles) {
+        float2 all = w[0];
+#pragma unroll
+        for (int i = 1; i < kGroup - 1; ++i) all = then(all, w[i]);
+        all = then(all, m);
+        *reinterpret_cast<float2*>(maps + lb.group_map(row, g) + 2 * ch) = all;
+        __syncwarp();
+        if (lane == 0) st_release(p.words + lb.group_flag(row, g) + warp, 1u);
+    }
+    if (ng > 0 || s > 0)
+        wait_flags(p, lane < ng              ? p.words + lb.group_flag(row, g - ng + lane) + warp
+                      : lane == ng && s > 0 ? p.words + lb.super_flag(row, s) + warp
+                                            : nullptr);
+    float h = s > 0 ? __ldcg(maps + lb.super_state(row, s) + ch) : start;
+    float2 v[kSuper / 2];
+#pragma unroll
+    for (int half = 0; half < kSuper; half += kSuper / 2) {
+#pragma unroll
+        for (int i = 0; i < kSuper / 2; ++i)
+            if (half + i < ng)
+                v[i] = __ldcg(reinterpret_cast<const float2*>(maps + lb.group_map(row, g - ng + half + i) + 2 * ch));
+#pragma unroll
+        for (int i = 0; i < kSuper / 2; ++i)
+            if (half + i < ng) h = pass(v[i], h);
+    }
+#pragma unroll
+    for (int i = 0; i < kGroup - 1; ++i)
+        if (i < nt) h = pass(w[i], h);
+    if (ends_super && n + 1 < lb.tiles) {
+        maps[lb.super_state(row, s + 1) + ch] = pass(m, h);
+        __syncwarp();
+        if (lane == 0) st_release(p.words + lb.super_flag(row, s + 1) + warp, 1u);
+    }
+    return h;
+}
+
+// The tiles of a block, by ticket where tiles wait for one another.  The
+// joining warps take the next ticket between the two barriers of a tile.
+struct Tickets {
+    unsigned* words;
+    unsigned* slot;  // shared
+    __device__ unsigned first() {
+        if (!words) return blockIdx.x;
+        if (threadIdx.x == 0) *slot = atomicAdd(words, 1u);
+        __syncthreads();
+        return *slot;
+    }
+    __device__ unsigned take(unsigned k) { return words ? atomicAdd(words, 1u) : k + gridDim.x; }
+};
+
+// Loads a run: x and gates of tokens [0, nt), the bits of its resets.
+template <typename T, bool SHARED, bool VEC>
+struct Run {
+    Lane<T, kCh, VEC> x[kTok];
+    Lane<T, SHARED ? 1 : kCh, VEC && !SHARED> g[kTok];
+    unsigned resets;
+    __device__ __forceinline__ void load(const GateParams& p, int b, int hd, int t0, int c, int nc, int nt) {
+        const T* xp = static_cast<const T*>(p.x) + b * p.sx[0] + hd * p.sx[1] + t0 * p.sx[2] + c;
+        const T* gp = static_cast<const T*>(p.g) + b * p.sg[0] + hd * p.sg[1] + t0 * p.sg[2] + (SHARED ? 0 : c);
+#pragma unroll
+        for (int i = 0; i < kTok; ++i)
+            if (i < nt) {
+                x[i].load(xp + i * p.sx[2], nc);
+                g[i].load(gp + i * p.sg[2], SHARED ? 1 : nc);
+            }
+        resets = 0;
+        if (p.reset) {
+            const unsigned char* rp = p.reset + (long long)b * p.T + t0;
+#pragma unroll
+            for (int i = 0; i < kTok; ++i)
+                if (i < nt && rp[i]) resets |= 1u << i;
+        }
+    }
+    __device__ __forceinline__ bool reset(int i) const { return (resets >> i) & 1u; }
+};
+
+// ---- forward -----------------------------------------------------------------
+// LANES x 4 channels to a token, kData / LANES runs of kTok tokens to a tile.
+template <typename T, bool SIG, bool SHARED, int LANES, bool VEC>
+__global__ void __launch_bounds__(block_threads(LANES), sizeof(T) == 2 ? 2 : 1)
+gated_scan_kernel(const GateParams p) {
+    constexpr int CB = LANES * kCh, RUNS = kData / LANES, TILE = RUNS * kTok, NG = SHARED ? 1 : kCh;
+    __shared__ float2 runs[RUNS][CB];  // maps of the runs, then of what is before each in the tile
+    __shared__ float entering[CB];
+    __shared__ unsigned slot;
+    const int rows = p.B * p.H;
+    const Lookback lb(rows, p.tiles, CB);
+    Tickets tickets{p.words, &slot};
+    unsigned k = tickets.first();
+    if (threadIdx.x >= kData) {  // joins the tiles: one thread to a channel
+        const int ch = threadIdx.x - kData;
+        while (k < p.total) {
+            const int n = (int)(k / (unsigned)rows), row = (int)(k - (unsigned)n * (unsigned)rows);
+            float h = p.state_in && ch < p.d ? p.state_in[(long long)row * p.d + ch] : 0.f;
+            __syncthreads();  // the runs' maps are there
+            if (ch == 0) slot = tickets.take(k);
+            float2 m = make_float2(1.f, 0.f);
+#pragma unroll 8
+            for (int r = 0; r < RUNS; ++r) {
+                const float2 f = runs[r][ch];
+                runs[r][ch] = m;
+                m = then(m, f);
+            }
+            if (p.words) h = enter_tile(p, lb, row, n, ch >> 5, m, h);
+            entering[ch] = h;
+            if (p.carry && ch < p.d) p.carry[((long long)row * p.tiles + n) * p.d + ch] = h;
+            __syncthreads();  // what enters each run is there
+            k = slot;
+        }
+        return;
+    }
+    const int lane = threadIdx.x % LANES, run = threadIdx.x / LANES;
+    const int c = lane * kCh, nc = p.d - c;
+    while (k < p.total) {
+        const int n = (int)(k / (unsigned)rows), row = (int)(k - (unsigned)n * (unsigned)rows);
+        const int b = row / p.H, hd = row - b * p.H;
+        const int t0 = n * TILE + run * kTok;
+        const int nt = nc > 0 ? min(kTok, p.T - t0) : 0;  // tokens of this thread, none where <= 0
+        Run<T, SHARED, VEC> in;
+        in.load(p, b, hd, t0, c, nc, nt);
+        float gate[kTok][NG];  // z of the sigmoid, a of the decay
+        float A[kCh], X[kCh];
+#pragma unroll
+        for (int j = 0; j < kCh; ++j) { A[j] = 1.f; X[j] = 0.f; }
+#pragma unroll
+        for (int i = 0; i < kTok; ++i)
+            if (i < nt) {
+#pragma unroll
+                for (int j = 0; j < NG; ++j) gate[i][j] = SIG ? keep_out(in.g[i].get(j)) : in.g[i].get(j);
+#pragma unroll
+                for (int j = 0; j < kCh; ++j) {
+                    const float ga = gate[i][SHARED ? 0 : j], xv = in.x[i].get(j);
+                    if (in.reset(i)) X[j] = 0.f;
+                    X[j] = SIG ? fmaf(ga, xv - X[j], X[j]) : fmaf(ga, X[j], xv);
+                    A[j] = SIG ? fmaf(-ga, A[j], A[j]) : ga * A[j];
+                }
+            }
+#pragma unroll
+        for (int j = 0; j < kCh; ++j) runs[run][c + j] = make_float2(in.resets ? cut() : A[j] + 0.f, X[j]);
+        __syncthreads();
+        __syncthreads();
+        k = slot;
+        if (nt > 0) {
+            float h[kCh];
+#pragma unroll
+            for (int j = 0; j < kCh; ++j) h[j] = pass(runs[run][c + j], entering[c + j]);
+            const long long off = b * p.so[0] + hd * p.so[1] + t0 * p.so[2] + c;
+#pragma unroll
+            for (int i = 0; i < kTok; ++i)
+                if (i < nt) {
+#pragma unroll
+                    for (int j = 0; j < kCh; ++j) {
+                        const float ga = gate[i][SHARED ? 0 : j], xv = in.x[i].get(j);
+                        if (in.reset(i)) h[j] = 0.f;
+                        h[j] = SIG ? fmaf(ga, xv - h[j], h[j]) : fmaf(ga, h[j], xv);
+                    }
+                    if (p.out_bf16) {
+                        Lane<bf16, kCh, VEC> ov;
+                        ov.set(h);
+                        ov.store(static_cast<bf16*>(p.o) + off + i * p.so[2], nc);
+                    } else {
+                        Lane<float, kCh, VEC> ov;
+                        ov.set(h);
+                        ov.store(static_cast<float*>(p.o) + off + i * p.so[2], nc);
+                    }
+                }
+            if (p.state_out && t0 + nt == p.T) {
+#pragma unroll
+                for (int j = 0; j < kCh; ++j)
+                    if (j < nc) p.state_out[(long long)row * p.d + c + j] = h[j];
+            }
+        }
+    }
+}
+
+// ---- gradient ----------------------------------------------------------------
+// The same walk from the last tile to the first for mu_t = a_t lam_t, the part of
+// the gradient that reaches h_{t-1}: mu_t = a_t (dh_t + mu_{t+1}), so a run maps
+// the mu behind it to the mu before it by the same A and a Y of its own.  The
+// states inside the tile are formed anew, from the kept state that enters it; a
+// thread's h_{t-1} wait in shared memory until its way back.
+template <typename T, typename TO, bool SIG, bool SHARED, int LANES, bool VEC>
+__global__ void __launch_bounds__(block_threads(LANES), sizeof(T) == 2 ? 2 : 1)
+gated_scan_bwd_kernel(const GateParams p) {
+    constexpr int CB = LANES * kCh, RUNS = kData / LANES, TILE = RUNS * kTok, NG = SHARED ? 1 : kCh;
+    __shared__ float2 fwd[RUNS][CB];   // maps of h; .x becomes the state that enters the run
+    __shared__ float2 back[RUNS][CB];  // maps of mu, then of what is behind each run in the tile
+    __shared__ float entering[CB];
+    __shared__ unsigned slot;
+    extern __shared__ float4 before[];  // [kTok][kData]: h_{t-1}
+    const int rows = p.B * p.H;
+    const Lookback lb(rows, p.tiles, CB);
+    Tickets tickets{p.words, &slot};
+    unsigned k = tickets.first();
+    if (threadIdx.x >= kData) {
+        const int ch = threadIdx.x - kData;
+        while (k < p.total) {
+            const int n = (int)(k / (unsigned)rows), row = (int)(k - (unsigned)n * (unsigned)rows);
+            float mu = 0.f, h = 0.f;
+            if (ch < p.d) {
+                if (p.dstate_out) mu = p.dstate_out[(long long)row * p.d + ch];
+                h = p.carry[((long long)row * p.tiles + (p.tiles - 1 - n)) * p.d + ch];
+            }
+            __syncthreads();
+            if (ch == 0) slot = tickets.take(k);
+            float2 m = make_float2(1.f, 0.f);
+#pragma unroll 8
+            for (int r = RUNS - 1; r >= 0; --r) {
+                const float2 f = back[r][ch];
+                back[r][ch] = m;
+                m = then(m, f);
+            }
+#pragma unroll 8
+            for (int r = 0; r < RUNS; ++r) {
+                const float2 f = fwd[r][ch];
+                fwd[r][ch].x = h;
+                h = pass(f, h);
+            }
+            if (p.words) mu = enter_tile(p, lb, row, n, ch >> 5, m, mu);
+            entering[ch] = mu;
+            __syncthreads();
+            k = slot;
+        }
+        return;
+    }
+    const int tid = threadIdx.x, lane = tid % LANES, run = tid / LANES;
+    const int c = lane * kCh, nc = p.d - c;
+    while (k < p.total) {
+        const int n = (int)(k / (unsigned)rows), row = (int)(k - (unsigned)n * (unsigned)rows);
+        const int b = row / p.H, hd = row - b * p.H;
+        const int t0 = (p.tiles - 1 - n) * TILE + run * kTok;
+        const int nt = nc > 0 ? min(kTok, p.T - t0) : 0;
+        Run<T, SHARED, VEC> in;
+        in.load(p, b, hd, t0, c, nc, nt);
+        Lane<TO, kCh, VEC> dh[kTok];
+        const TO* up = static_cast<const TO*>(p.dout) + b * p.sdo[0] + hd * p.sdo[1] + t0 * p.sdo[2] + c;
+#pragma unroll
+        for (int i = 0; i < kTok; ++i)
+            if (i < nt) dh[i].load(up + i * p.sdo[2], nc);
+        float gate[kTok][NG];
+        float A[kCh], X[kCh], Y[kCh];
+#pragma unroll
+        for (int j = 0; j < kCh; ++j) { A[j] = 1.f; X[j] = 0.f; Y[j] = 0.f; }
+#pragma unroll
+        for (int i = 0; i < kTok; ++i)
+            if (i < nt) {
+#pragma unroll
+                for (int j = 0; j < NG; ++j) gate[i][j] = SIG ? keep_out(in.g[i].get(j)) : in.g[i].get(j);
+#pragma unroll
+                for (int j = 0; j < kCh; ++j) {
+                    const float ga = gate[i][SHARED ? 0 : j], xv = in.x[i].get(j);
+                    if (in.reset(i)) X[j] = 0.f;
+                    X[j] = SIG ? fmaf(ga, xv - X[j], X[j]) : fmaf(ga, X[j], xv);
+                    A[j] = SIG ? fmaf(-ga, A[j], A[j]) : ga * A[j];
+                }
+            }
+#pragma unroll
+        for (int i = kTok - 1; i >= 0; --i)
+            if (i < nt) {
+#pragma unroll
+                for (int j = 0; j < kCh; ++j) {
+                    const float ga = gate[i][SHARED ? 0 : j], lam = dh[i].get(j) + Y[j];
+                    Y[j] = in.reset(i) ? 0.f : SIG ? fmaf(-ga, lam, lam) : ga * lam;
+                }
+            }
+#pragma unroll
+        for (int j = 0; j < kCh; ++j) {
+            const float a = in.resets ? cut() : A[j] + 0.f;
+            fwd[run][c + j] = make_float2(a, X[j]);
+            back[run][c + j] = make_float2(a, Y[j]);
+        }
+        __syncthreads();
+        __syncthreads();
+        k = slot;
+        float mu[kCh];
+        if (nt > 0) {
+            float h[kCh];
+#pragma unroll
+            for (int j = 0; j < kCh; ++j) {
+                h[j] = fwd[run][c + j].x;
+                mu[j] = pass(back[run][c + j], entering[c + j]);
+            }
+#pragma unroll
+            for (int i = 0; i < kTok; ++i)
+                if (i < nt) {
+#pragma unroll
+                    for (int j = 0; j < kCh; ++j)
+                        if (in.reset(i)) h[j] = 0.f;
+                    before[i * kData + tid] = make_float4(h[0], h[1], h[2], h[3]);
+#pragma unroll
+                    for (int j = 0; j < kCh; ++j) {
+                        const float ga = gate[i][SHARED ? 0 : j], xv = in.x[i].get(j);
+                        h[j] = SIG ? fmaf(ga, xv - h[j], h[j]) : fmaf(ga, h[j], xv);
+                    }
+                }
+        }
+        T* dxp = static_cast<T*>(p.dx) + b * p.sdx[0] + hd * p.sdx[1] + t0 * p.sdx[2] + c;
+        T* dgp = static_cast<T*>(p.dg) + b * p.sdg[0] + hd * p.sdg[1] + t0 * p.sdg[2] + (SHARED ? 0 : c);
+#pragma unroll
+        for (int i = kTok - 1; i >= 0; --i) {
+            float gx[kCh], gg[kCh];
+            const bool live = i < nt;
+            if (live) {
+                const float4 hb4 = before[i * kData + tid];
+                const float hb[kCh] = {hb4.x, hb4.y, hb4.z, hb4.w};
+#pragma unroll
+                for (int j = 0; j < kCh; ++j) {
+                    const float ga = gate[i][SHARED ? 0 : j], lam = dh[i].get(j) + mu[j];
+                    if (SIG) {
+                        gx[j] = ga * lam;
+                        gg[j] = fmaf(-ga, gx[j], gx[j]) * (hb[j] - in.x[i].get(j));
+                        mu[j] = in.reset(i) ? 0.f : fmaf(-ga, lam, lam);
+                    } else {
+                        gx[j] = lam;
+                        gg[j] = lam * hb[j];
+                        mu[j] = in.reset(i) ? 0.f : ga * lam;
+                    }
+                }
+                Lane<T, kCh, VEC> ov;
+                ov.set(gx);
+                ov.store(dxp + i * p.sdx[2], nc);
+            }
+            if (SHARED) {  // the sum over the token's channels
+                float s = 0.f;
+#pragma unroll
+                for (int j = 0; j < kCh; ++j) s += live && j < nc ? gg[j] : 0.f;
+#pragma unroll
+                for (int w = LANES / 2; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
+                if (live && lane == 0) dgp[i * p.sdg[2]] = from_f32<T>(s);
+            } else if (live) {
+                Lane<T, kCh, VEC> ov;
+                ov.set(gg);
+                ov.store(dgp + i * p.sdg[2], nc);
+            }
+        }
+        if (p.dstate_in && t0 == 0 && nt > 0) {
+#pragma unroll
+            for (int j = 0; j < kCh; ++j)
+                if (j < nc) p.dstate_in[(long long)row * p.d + c + j] = mu[j];
+        }
+    }
 }
 
 // One token: a read and a write of the state and of the token's n d values are
@@ -164,6 +569,7 @@ int check_gated(const char* what, int B, int H, int T, int d, int form, int dtyp
     if (form != HLA2_GATE_SIGMOID && form != HLA2_GATE_DECAY) return set_error(HLA2_ERR_UNSUPPORTED, "%s: unknown form %d", what, form);
     if (!known_dtype(dtype) || !known_dtype(out_dtype))
         return set_error(HLA2_ERR_UNSUPPORTED, "%s: unknown dtype %d or output dtype %d", what, dtype, out_dtype);
+    if (T > (1 << 30) || (long long)B * H * T > (1LL << 33)) return set_error(HLA2_ERR_UNSUPPORTED, "%s: problem too large", what);
     return HLA2_OK;
 }
 
@@ -176,17 +582,78 @@ void take_strides(long long (&s)[3], const long long* strides, int i, int H, int
     }
 }
 
+
+// The workspace of one direction: flags first, then the maps (16-byte aligned).
+size_t lookback_bytes(int rows, int tiles, int cb) {
+    if (tiles <= 1) return 0;
+    const Lookback lb(rows, tiles, cb);
+    return ((lb.words() * 4 + 15) & ~size_t(15)) + lb.floats() * 4;
+}
+
+// Blocks of a kernel that fit the device at once, at most one to a tile.  What
+// an SM holds is asked once for each kernel and device.
+cudaError_t persistent_blocks(const void* kernel, int threads, size_t smem, unsigned total, unsigned* blocks) {
+    static std::mutex mu;
+    static std::map<std::pair<const void*, int>, unsigned> known;
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev)) return e;
+    unsigned fit = 0;
+    {
+        std::lock_guard<std::mutex> lk(mu);
+        auto it = known.find({kernel, dev});
+        if (it != known.end()) fit = it->second;
+    }
+    if (!fit) {
+        if (smem)
+            if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem))
+                return e;
+        int per_sm = 0;
+        if (cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem)) return e;
+        fit = (unsigned)(per_sm > 0 ? per_sm : 1) * (unsigned)sm_count();
+        std::lock_guard<std::mutex> lk(mu);
+        known[{kernel, dev}] = fit;
+    }
+    *blocks = total < fit ? total : fit;
+    return cudaSuccess;
+}
+
+// Carves the workspace and zeroes its flags.
+cudaError_t begin_lookback(GateParams& p, int cb, void* workspace, cudaStream_t s) {
+    p.total = (unsigned)((long long)p.B * p.H * p.tiles);
+    if (p.tiles <= 1) return cudaSuccess;
+    const Lookback lb(p.B * p.H, p.tiles, cb);
+    p.words = static_cast<unsigned*>(workspace);
+    p.maps = reinterpret_cast<float*>(static_cast<char*>(workspace) + ((lb.words() * 4 + 15) & ~size_t(15)));
+    p.status = device_status_word();
+    return cudaMemsetAsync(p.words, 0, lb.words() * 4, s);
+}
+
+template <int N>
+using Int = std::integral_constant<int, N>;
+
+template <typename F>
+cudaError_t by_lanes(int d, bool vec, F&& f) {
+    using std::false_type;
+    using std::true_type;
+    if (d <= 64) return vec ? f(Int<16>{}, true_type{}) : f(Int<16>{}, false_type{});
+    return vec ? f(Int<32>{}, true_type{}) : f(Int<32>{}, false_type{});
+}
+
 }  // namespace
 }  // namespace hla2
 
 extern "C" size_t hla2_gated_scan_workspace(int B, int H, int T, int d) {
-    (void)B; (void)H; (void)T; (void)d;
-    return 0;
+    using namespace hla2;
+    if (B <= 0 || H <= 0 || T <= 0 || d <= 0 || d > 128 || (long long)B * H > 65535) return 0;
+    const int lanes = lanes_of(d), rows = B * H;
+    return (lookback_bytes(rows, (T + tile_of(lanes) - 1) / tile_of(lanes), lanes * kCh) + 255) & ~size_t(255);
 }
 
 extern "C" size_t hla2_gated_scan_carry_len(int T, int d) {
-    if (T <= 0 || d <= 0) return 0;
-    return (size_t)((T + hla2::kTile - 1) / hla2::kTile) * d;
+    using namespace hla2;
+    if (T <= 0 || d <= 0 || d > 128) return 0;
+    const int kept = tile_of(lanes_of(d));
+    return (size_t)((T + kept - 1) / kept) * d;
 }
 
 extern "C" int hla2_gated_scan(const void* X, const void* G, const unsigned char* reset, const float* state_in, void* O,
@@ -204,18 +671,32 @@ extern "C" int hla2_gated_scan(const void* X, const void* G, const unsigned char
     const size_t need = hla2_gated_scan_workspace(B, H, T, d);
     if (need && (!workspace || ws_bytes < need))
         return set_error(HLA2_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", what, ws_bytes, need);
+    if (need && reinterpret_cast<uintptr_t>(workspace) % 16)
+        return set_error(HLA2_ERR_INVALID, "%s: workspace not 16-byte aligned", what);
     GateParams p{};
     p.x = X; p.g = G; p.reset = reset; p.state_in = state_in; p.o = O; p.state_out = state_out; p.carry = carry;
     p.B = B; p.H = H; p.T = T; p.d = d;
     take_strides(p.sx, strides, 0, H, T, d);
     take_strides(p.sg, strides, 1, H, T, gate_shared ? 1 : d);
     take_strides(p.so, strides, 2, H, T, d);
+    const int lanes = lanes_of(d), tile = tile_of(lanes);
+    p.tiles = (T + tile - 1) / tile;
+    const bool vec = d % kCh == 0 && aligned_to(X, es, p.sx, 3, kCh * es) && aligned_to(O, os, p.so, 3, kCh * os) &&
+                     (gate_shared || aligned_to(G, es, p.sg, 3, kCh * es));
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = by_types(dtype, out_dtype, [&](auto tin, auto tout) {
+    cudaError_t e = begin_lookback(p, lanes * kCh, workspace, s);
+    p.out_bf16 = out_dtype == HLA2_DTYPE_BF16;
+    if (e == cudaSuccess) e = by_types(dtype, HLA2_DTYPE_F32, [&](auto tin, auto) {
         return by_form(form, gate_shared, [&](auto sig, auto shared) {
-            gated_simple_kernel<decltype(tin), decltype(tout), decltype(sig)::value, decltype(shared)::value>
-                <<<B * H, 128, 0, s>>>(p);
-            return cudaGetLastError();
+            return by_lanes(d, vec, [&](auto ln, auto v) {
+                constexpr int threads = block_threads(decltype(ln)::value);
+                auto kernel = gated_scan_kernel<decltype(tin), decltype(sig)::value, decltype(shared)::value,
+                                                decltype(ln)::value, decltype(v)::value>;
+                unsigned blocks = 0;
+                if (cudaError_t e2 = persistent_blocks(reinterpret_cast<const void*>(kernel), threads, 0, p.total, &blocks)) return e2;
+                kernel<<<blocks, threads, 0, s>>>(p);
+                return cudaGetLastError();
+            });
         });
     });
     note_launches(1);
@@ -239,6 +720,8 @@ extern "C" int hla2_gated_scan_backward(const void* X, const void* G, const unsi
     const size_t need = hla2_gated_scan_workspace(B, H, T, d);
     if (need && (!workspace || ws_bytes < need))
         return set_error(HLA2_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", what, ws_bytes, need);
+    if (need && reinterpret_cast<uintptr_t>(workspace) % 16)
+        return set_error(HLA2_ERR_INVALID, "%s: workspace not 16-byte aligned", what);
     GateParams p{};
     p.x = X; p.g = G; p.reset = reset; p.carry = const_cast<float*>(carry); p.dout = dO; p.dstate_out = dstate_out;
     p.dx = dX; p.dg = dG; p.dstate_in = dstate_in;
@@ -248,12 +731,25 @@ extern "C" int hla2_gated_scan_backward(const void* X, const void* G, const unsi
     take_strides(p.sdo, strides, 2, H, T, d);
     take_strides(p.sdx, strides, 3, H, T, d);
     take_strides(p.sdg, strides, 4, H, T, gate_shared ? 1 : d);
+    const int lanes = lanes_of(d), tile = tile_of(lanes);
+    p.tiles = (T + tile - 1) / tile;
+    const bool vec = d % kCh == 0 && aligned_to(X, es, p.sx, 3, kCh * es) && aligned_to(dX, es, p.sdx, 3, kCh * es) &&
+                     aligned_to(dO, os, p.sdo, 3, kCh * os) &&
+                     (gate_shared || (aligned_to(G, es, p.sg, 3, kCh * es) && aligned_to(dG, es, p.sdg, 3, kCh * es)));
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = by_types(dtype, out_dtype, [&](auto tin, auto tout) {
+    cudaError_t e = begin_lookback(p, lanes * kCh, workspace, s);
+    if (e == cudaSuccess) e = by_types(dtype, out_dtype, [&](auto tin, auto tout) {
         return by_form(form, gate_shared, [&](auto sig, auto shared) {
-            gated_simple_bwd_kernel<decltype(tin), decltype(tout), decltype(sig)::value, decltype(shared)::value>
-                <<<B * H, 128, 0, s>>>(p);
-            return cudaGetLastError();
+            return by_lanes(d, vec, [&](auto ln, auto v) {
+                auto kernel = gated_scan_bwd_kernel<decltype(tin), decltype(tout), decltype(sig)::value,
+                                                    decltype(shared)::value, decltype(ln)::value, decltype(v)::value>;
+                constexpr int threads = block_threads(decltype(ln)::value);
+                constexpr size_t smem = (size_t)kTok * kData * sizeof(float4);
+                unsigned blocks = 0;
+                if (cudaError_t e2 = persistent_blocks(reinterpret_cast<const void*>(kernel), threads, smem, p.total, &blocks)) return e2;
+                kernel<<<blocks, threads, smem, s>>>(p);
+                return cudaGetLastError();
+            });
         });
     });
     note_launches(1);
