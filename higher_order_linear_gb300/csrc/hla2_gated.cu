@@ -62,8 +62,7 @@ struct GateParams {
     int B, H, T, d;
     long long sx[3], sg[3], so[3], sdo[3], sdx[3], sdg[3];
     // workspace (null for one tile): see Lookback
-    unsigned* words;
-    float* maps;
+    unsigned long long* words;
     int tiles, out_bf16;
     unsigned total;  // rows * tiles
     int* status;
@@ -87,141 +86,129 @@ __device__ __forceinline__ float2 then(float2 a, float2 b) {
 }
 
 // ---- the workspace -----------------------------------------------------------
-// words: [0] ticket, [1] a wait ran out, then a flag for each (row, tile, warp),
-// (row, group, warp) and (row, super-group, warp): zeroed before the launch.
-// maps: tile maps, group maps (float2 for each of the row's channels), states
-// that enter the super-groups (float).  A warp holds 32 channels of the maps and
-// reads only what the same warp of other blocks published.
+// A ticket word and a word that says that a wait ran out; then the maps of the
+// tiles and of the groups (A, X for each of a row's channels), then the states
+// that enter the super-groups (h, 0).  Each pair is one 64-bit word, written and
+// read whole, so it is its own flag: the words are set to all ones before the
+// launch, which no pair is (arithmetic gives one NaN, 0x7fffffff), and whoever
+// needs one reads it until it is something else.
 struct Lookback {
-    int rows, tiles, groups, supers, cb;  // cb: channels of a map, 32 to a warp
+    int rows, tiles, groups, supers, cb;  // cb: channels of a map
     __host__ __device__ Lookback(int rows, int tiles, int cb)
         : rows(rows), tiles(tiles), groups((tiles + kGroup - 1) / kGroup),
           supers((groups + kSuper - 1) / kSuper), cb(cb) {}
-    __host__ __device__ size_t warps() const { return (size_t)cb / 32; }
-    __host__ __device__ size_t tile_flag(int r, int t) const { return 2 + ((size_t)r * tiles + t) * warps(); }
-    __host__ __device__ size_t group_flag(int r, int g) const {
-        return tile_flag(rows, 0) + ((size_t)r * groups + g) * warps();
-    }
-    __host__ __device__ size_t super_flag(int r, int s) const {
-        return group_flag(rows, 0) + ((size_t)r * supers + s) * warps();
-    }
-    __host__ __device__ size_t words() const { return super_flag(rows, 0); }
-    __host__ __device__ size_t tile_map(int r, int t) const { return ((size_t)r * tiles + t) * cb * 2; }
-    __host__ __device__ size_t group_map(int r, int g) const {
-        return tile_map(rows, 0) + ((size_t)r * groups + g) * cb * 2;
-    }
+    __host__ __device__ size_t tile_map(int r, int t) const { return 1 + ((size_t)r * tiles + t) * cb; }
+    __host__ __device__ size_t group_map(int r, int g) const { return tile_map(rows, 0) + ((size_t)r * groups + g) * cb; }
     __host__ __device__ size_t super_state(int r, int s) const {
         return group_map(rows, 0) + ((size_t)r * supers + s) * cb;
     }
-    __host__ __device__ size_t floats() const { return super_state(rows, 0); }
+    __host__ __device__ size_t words() const { return super_state(rows, 0); }
 };
 
-__device__ __forceinline__ unsigned ld_acquire(const unsigned* p) {
-    unsigned v;
-    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+using u64 = unsigned long long;
+constexpr u64 kNothing = ~0ull;
+
+__device__ __forceinline__ u64 ld_word(const u64* p) {
+    u64 v;
+    asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
     return v;
 }
-__device__ __forceinline__ void st_release(unsigned* p, unsigned v) {
-    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+__device__ __forceinline__ void st_pair(u64* p, float2 m) {
+    u64 v = ((u64)__float_as_uint(m.y) << 32) | __float_as_uint(m.x);
+    if (v == kNothing) v = 0x7fffffff7fffffffull;
+    asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
 }
-__device__ __forceinline__ unsigned long long gate_timer() {
-    unsigned long long t;
+__device__ __forceinline__ float2 as_pair(u64 v) {
+    return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
+}
+__device__ __forceinline__ u64 gate_timer() {
+    u64 t;
     asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
     return t;
 }
 
-// Waits until the flag of every lane that has one is set (at most 2 s, then this
-// call's results are void: the status word says so, and every later wait of the
-// call gives up at once).
-__device__ __forceinline__ void wait_flags(const GateParams& p, const unsigned* flag) {
-    bool ok = flag == nullptr || ld_acquire(flag) != 0;
-    if (!__all_sync(0xffffffffu, ok)) {
-        const unsigned long long t0 = gate_timer();
-        bool give_up = false;
-        while (!__all_sync(0xffffffffu, ok)) {
-            if (!ok) ok = ld_acquire(flag) != 0;
-            if (!ok && (gate_timer() - t0 > kGateWaitNs || *(volatile unsigned*)(p.words + 1) != 0)) give_up = true;
-            if (__any_sync(0xffffffffu, give_up)) {
-                if ((threadIdx.x & 31) == 0) {
-                    atomicExch(p.words + 1, 1u);
-                    atomicExch(p.status, (int)kDevWaitTimeout);
-                }
-                break;
+// Reads w[i] = p[i * step] for i < n until every one is there.  Gives up after
+// 2 s: then this call's results are void, the status word says so, and every
+// later wait of the call ends at once.
+template <int N>
+__device__ __forceinline__ void read_words(const GateParams& p, const u64* src, size_t step, int n, u64 (&w)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = i < n ? ld_word(src + i * step) : 0;
+    u64 t0 = 0;
+    while (true) {
+        bool all = true;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (w[i] == kNothing) {
+                w[i] = ld_word(src + i * step);
+                all = all && w[i] != kNothing;
             }
+        if (all) return;
+        const u64 now = gate_timer();
+        if (t0 == 0) t0 = now;
+        unsigned* const run_out = reinterpret_cast<unsigned*>(p.words) + 1;
+        if (now - t0 > kGateWaitNs || *(volatile unsigned*)run_out != ~0u) {
+            atomicExch(run_out, 0u);
+            atomicExch(p.status, (int)kDevWaitTimeout);
+            return;
         }
     }
-    __syncwarp();
 }
 
-// One warp's part for its 32 channels: publishes the tile's map `m`, returns the
+// One thread's part, for its channel: publishes the tile's map `m`, returns the
 // state that enters the tile.  `start`: the state that enters the sequence.
-// `n` counts tiles in the order of the walk.  Every lane calls it.
-__device__ __forceinline__ float enter_tile(const GateParams& p, const Lookback& lb, int row, int n, int warp, float2 m,
+// `n` counts tiles in the order of the walk.
+__device__ __forceinline__ float enter_tile(const GateParams& p, const Lookback& lb, int row, int n, int ch, float2 m,
                                             float start) {
-    const int lane = threadIdx.x & 31, ch = warp * 32 + lane;
     const int g = n / kGroup, s = g / kSuper;
     const int nt = n % kGroup, ng = g % kSuper;  // tiles before this one in its group, groups before it in the super-group
-    const bool ends_group = nt == kGroup - 1, ends_super = ends_group && ng == kSuper - 1;
-    float* maps = p.maps;
-    if (n + 1 < lb.tiles) {
-        *reinterpret_cast<float2*>(maps + lb.tile_map(row, n) + 2 * ch) = m;
-        __syncwarp();
-        if (lane == 0) st_release(p.words + lb.tile_flag(row, n) + warp, 1u);
-    }
+    const bool last = n + 1 == lb.tiles, ends_group = nt == kGroup - 1, ends_super = ends_group && ng == kSuper - 1;
+    if (!last) st_pair(p.words + lb.tile_map(row, n) + ch, m);
     // the tiles of the group first: the group's map waits for nothing else
-    wait_flags(p, lane < nt ? p.words + lb.tile_flag(row, n - nt + lane) + warp : nullptr);
-    float2 w[kGroup - 1];
+    u64 w[kGroup - 1];
+    read_words(p, p.words + lb.tile_map(row, n - nt) + ch, lb.cb, nt, w);
+    if (ends_group && !last) {
+        float2 all = as_pair(w[0]);
 #pragma unroll
-    for (int i = 0; i < kGroup - 1; ++i)
-        if (i < nt) w[i] = __ldcg(reinterpret_cast<const float2*>(maps + lb.tile_map(row, n - nt + i) + 2 * ch));
-    if (ends_group && n + 1 < lb.tiles) {
-        float2 all = w[0];
-#pragma unroll
-        for (int i = 1; i < kGroup - 1; ++i) all = then(all, w[i]);
-        all = then(all, m);
-        *reinterpret_cast<float2*>(maps + lb.group_map(row, g) + 2 * ch) = all;
-        __syncwarp();
-        if (lane == 0) st_release(p.words + lb.group_flag(row, g) + warp, 1u);
+        for (int i = 1; i < kGroup - 1; ++i) all = then(all, as_pair(w[i]));
+        st_pair(p.words + lb.group_map(row, g) + ch, then(all, m));
     }
-    if (ng > 0 || s > 0)
-        wait_flags(p, lane < ng              ? p.words + lb.group_flag(row, g - ng + lane) + warp
-                      : lane == ng && s > 0 ? p.words + lb.super_flag(row, s) + warp
-                                            : nullptr);
-    float h = s > 0 ? __ldcg(maps + lb.super_state(row, s) + ch) : start;
-    float2 v[kSuper / 2];
+    float h = start;
+    if (s > 0) {
+        u64 v[1];
+        read_words(p, p.words + lb.super_state(row, s) + ch, 0, 1, v);
+        h = as_pair(v[0]).x;
+    }
 #pragma unroll
     for (int half = 0; half < kSuper; half += kSuper / 2) {
+        u64 v[kSuper / 2];
+        const int here = min(ng - half, kSuper / 2);
+        if (here > 0) {
+            read_words(p, p.words + lb.group_map(row, g - ng + half) + ch, lb.cb, here, v);
 #pragma unroll
-        for (int i = 0; i < kSuper / 2; ++i)
-            if (half + i < ng)
-                v[i] = __ldcg(reinterpret_cast<const float2*>(maps + lb.group_map(row, g - ng + half + i) + 2 * ch));
-#pragma unroll
-        for (int i = 0; i < kSuper / 2; ++i)
-            if (half + i < ng) h = pass(v[i], h);
+            for (int i = 0; i < kSuper / 2; ++i)
+                if (i < here) h = pass(as_pair(v[i]), h);
+        }
     }
 #pragma unroll
     for (int i = 0; i < kGroup - 1; ++i)
-        if (i < nt) h = pass(w[i], h);
-    if (ends_super && n + 1 < lb.tiles) {
-        maps[lb.super_state(row, s + 1) + ch] = pass(m, h);
-        __syncwarp();
-        if (lane == 0) st_release(p.words + lb.super_flag(row, s + 1) + warp, 1u);
-    }
+        if (i < nt) h = pass(as_pair(w[i]), h);
+    if (ends_super && !last) st_pair(p.words + lb.super_state(row, s + 1) + ch, make_float2(pass(m, h), 0.f));
     return h;
 }
 
 // The tiles of a block, by ticket where tiles wait for one another.  The
 // joining warps take the next ticket between the two barriers of a tile.
 struct Tickets {
-    unsigned* words;
+    unsigned* word;  // starts at ~0
     unsigned* slot;  // shared
     __device__ unsigned first() {
-        if (!words) return blockIdx.x;
-        if (threadIdx.x == 0) *slot = atomicAdd(words, 1u);
+        if (!word) return blockIdx.x;
+        if (threadIdx.x == 0) *slot = atomicAdd(word, 1u) + 1u;
         __syncthreads();
         return *slot;
     }
-    __device__ unsigned take(unsigned k) { return words ? atomicAdd(words, 1u) : k + gridDim.x; }
+    __device__ unsigned take(unsigned k) { return word ? atomicAdd(word, 1u) + 1u : k + gridDim.x; }
 };
 
 // Loads a run: x and gates of tokens [0, nt), the bits of its resets.
@@ -261,7 +248,7 @@ gated_scan_kernel(const GateParams p) {
     __shared__ unsigned slot;
     const int rows = p.B * p.H;
     const Lookback lb(rows, p.tiles, CB);
-    Tickets tickets{p.words, &slot};
+    Tickets tickets{reinterpret_cast<unsigned*>(p.words), &slot};
     unsigned k = tickets.first();
     if (threadIdx.x >= kData) {  // joins the tiles: one thread to a channel
         const int ch = threadIdx.x - kData;
@@ -277,7 +264,7 @@ gated_scan_kernel(const GateParams p) {
                 runs[r][ch] = m;
                 m = then(m, f);
             }
-            if (p.words) h = enter_tile(p, lb, row, n, ch >> 5, m, h);
+            if (p.words) h = enter_tile(p, lb, row, n, ch, m, h);
             entering[ch] = h;
             if (p.carry && ch < p.d) p.carry[((long long)row * p.tiles + n) * p.d + ch] = h;
             __syncthreads();  // what enters each run is there
@@ -366,7 +353,7 @@ gated_scan_bwd_kernel(const GateParams p) {
     extern __shared__ float4 before[];  // [kTok][kData]: h_{t-1}
     const int rows = p.B * p.H;
     const Lookback lb(rows, p.tiles, CB);
-    Tickets tickets{p.words, &slot};
+    Tickets tickets{reinterpret_cast<unsigned*>(p.words), &slot};
     unsigned k = tickets.first();
     if (threadIdx.x >= kData) {
         const int ch = threadIdx.x - kData;
@@ -392,7 +379,7 @@ gated_scan_bwd_kernel(const GateParams p) {
                 fwd[r][ch].x = h;
                 h = pass(f, h);
             }
-            if (p.words) mu = enter_tile(p, lb, row, n, ch >> 5, m, mu);
+            if (p.words) mu = enter_tile(p, lb, row, n, ch, m, mu);
             entering[ch] = mu;
             __syncthreads();
             k = slot;
@@ -583,11 +570,9 @@ void take_strides(long long (&s)[3], const long long* strides, int i, int H, int
 }
 
 
-// The workspace of one direction: flags first, then the maps (16-byte aligned).
 size_t lookback_bytes(int rows, int tiles, int cb) {
     if (tiles <= 1) return 0;
-    const Lookback lb(rows, tiles, cb);
-    return ((lb.words() * 4 + 15) & ~size_t(15)) + lb.floats() * 4;
+    return Lookback(rows, tiles, cb).words() * 8;
 }
 
 // Blocks of a kernel that fit the device at once, at most one to a tile.  What
@@ -617,15 +602,13 @@ cudaError_t persistent_blocks(const void* kernel, int threads, size_t smem, unsi
     return cudaSuccess;
 }
 
-// Carves the workspace and zeroes its flags.
+// Sets the workspace's words to "nothing yet".
 cudaError_t begin_lookback(GateParams& p, int cb, void* workspace, cudaStream_t s) {
     p.total = (unsigned)((long long)p.B * p.H * p.tiles);
     if (p.tiles <= 1) return cudaSuccess;
-    const Lookback lb(p.B * p.H, p.tiles, cb);
-    p.words = static_cast<unsigned*>(workspace);
-    p.maps = reinterpret_cast<float*>(static_cast<char*>(workspace) + ((lb.words() * 4 + 15) & ~size_t(15)));
+    p.words = static_cast<unsigned long long*>(workspace);
     p.status = device_status_word();
-    return cudaMemsetAsync(p.words, 0, lb.words() * 4, s);
+    return cudaMemsetAsync(p.words, 0xff, Lookback(p.B * p.H, p.tiles, cb).words() * 8, s);
 }
 
 template <int N>
