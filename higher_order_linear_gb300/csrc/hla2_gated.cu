@@ -31,216 +31,15 @@
 // map and the last of a super-group the state after it, so a tile reads at most
 // 22 maps and one state, and the only chain along the sequence has one link for
 // each 128 tiles.
-#include <map>
-#include <mutex>
-
-#include "hla2_layer.cuh"
+#include "hla2_gated.cuh"
 
 namespace hla2 {
 namespace {
 
-constexpr int kTok = 8;         // tokens of a thread's run
-constexpr int kCh = 4;          // channels of a thread
-constexpr int kData = 256;      // threads that hold a tile
-constexpr int kGroup = 8;       // tiles to a group
-constexpr int kSuper = 16;      // groups to a super-group
-constexpr unsigned long long kGateWaitNs = 2000000000ull;  // bounded waits: 2 s
-
-// Lanes that share a token: they cover 4 channels each, d <= 4 lanes.
-__host__ __device__ constexpr int lanes_of(int d) { return d <= 64 ? 16 : 32; }
-// Tokens of a tile: a state is kept for the gradient at the start of each.
-__host__ __device__ constexpr int tile_of(int lanes) { return kData / lanes * kTok; }
-// Threads of a block: those that hold the tile, and a warp for each 32 channels that joins tiles.
-__host__ __device__ constexpr int block_threads(int lanes) { return kData + lanes * kCh; }
-
-struct GateParams {
-    const void *x, *g, *dout;
-    const unsigned char* reset;
-    const float *state_in, *dstate_out;
-    void *o, *dx, *dg;
-    float *state_out, *dstate_in, *carry;
-    int B, H, T, d;
-    long long sx[3], sg[3], so[3], sdo[3], sdx[3], sdg[3];
-    // workspace (null for one tile): see Lookback
-    unsigned long long* words;
-    int tiles, out_bf16;
-    unsigned total;  // rows * tiles
-    int* status;
-};
-
-// z = 1 - a of the sigmoid gate
-__device__ __forceinline__ float keep_out(float g) {
-    const float e = __expf(-g);
-    return isinf(e) ? 1.f : __fdividef(e, 1.f + e);
-}
-
-// ---- maps h -> A h + X -------------------------------------------------------
-// A run that holds a reset forgets what entered it: its A is -0, which nothing
-// else is (products that are zero are made +0), and then only X counts.
-__device__ __forceinline__ float cut() { return __uint_as_float(0x80000000u); }
-__device__ __forceinline__ bool is_cut(float A) { return __float_as_uint(A) == 0x80000000u; }
-__device__ __forceinline__ float pass(float2 m, float h) { return is_cut(m.x) ? m.y : fmaf(m.x, h, m.y); }
-// first `a`, then `b`
-__device__ __forceinline__ float2 then(float2 a, float2 b) {
-    return make_float2(is_cut(b.x) || is_cut(a.x) ? cut() : a.x * b.x + 0.f, pass(b, a.y));
-}
-
-// ---- the workspace -----------------------------------------------------------
-// A ticket word and a word that says that a wait ran out; then the maps of the
-// tiles and of the groups (A, X for each of a row's channels), then the states
-// that enter the super-groups (h, 0).  Each pair is one 64-bit word, written and
-// read whole, so it is its own flag: the words are set to all ones before the
-// launch, which no pair is (arithmetic gives one NaN, 0x7fffffff), and whoever
-// needs one reads it until it is something else.
-struct Lookback {
-    int rows, tiles, groups, supers, cb;  // cb: channels of a map
-    __host__ __device__ Lookback(int rows, int tiles, int cb)
-        : rows(rows), tiles(tiles), groups((tiles + kGroup - 1) / kGroup),
-          supers((groups + kSuper - 1) / kSuper), cb(cb) {}
-    __host__ __device__ size_t tile_map(int r, int t) const { return 1 + ((size_t)r * tiles + t) * cb; }
-    __host__ __device__ size_t group_map(int r, int g) const { return tile_map(rows, 0) + ((size_t)r * groups + g) * cb; }
-    __host__ __device__ size_t super_state(int r, int s) const {
-        return group_map(rows, 0) + ((size_t)r * supers + s) * cb;
-    }
-    __host__ __device__ size_t words() const { return super_state(rows, 0); }
-};
-
-using u64 = unsigned long long;
-constexpr u64 kNothing = ~0ull;
-
-__device__ __forceinline__ u64 ld_word(const u64* p) {
-    u64 v;
-    asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
-    return v;
-}
-__device__ __forceinline__ void st_pair(u64* p, float2 m) {
-    u64 v = ((u64)__float_as_uint(m.y) << 32) | __float_as_uint(m.x);
-    if (v == kNothing) v = 0x7fffffff7fffffffull;
-    asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
-}
-__device__ __forceinline__ float2 as_pair(u64 v) {
-    return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
-}
-__device__ __forceinline__ u64 gate_timer() {
-    u64 t;
-    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-    return t;
-}
-
-// Reads w[i] = p[i * step] for i < n until every one is there.  Gives up after
-// 2 s: then this call's results are void, the status word says so, and every
-// later wait of the call ends at once.
-template <int N>
-__device__ __forceinline__ void read_words(const GateParams& p, const u64* src, size_t step, int n, u64 (&w)[N]) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) w[i] = i < n ? ld_word(src + i * step) : 0;
-    u64 t0 = 0;
-    while (true) {
-        bool all = true;
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (w[i] == kNothing) {
-                w[i] = ld_word(src + i * step);
-                all = all && w[i] != kNothing;
-            }
-        if (all) return;
-        const u64 now = gate_timer();
-        if (t0 == 0) t0 = now;
-        unsigned* const run_out = reinterpret_cast<unsigned*>(p.words) + 1;
-        if (now - t0 > kGateWaitNs || *(volatile unsigned*)run_out != ~0u) {
-            atomicExch(run_out, 0u);
-            atomicExch(p.status, (int)kDevWaitTimeout);
-            return;
-        }
-    }
-}
-
-// One thread's part, for its channel: publishes the tile's map `m`, returns the
-// state that enters the tile.  `start`: the state that enters the sequence.
-// `n` counts tiles in the order of the walk.
-__device__ __forceinline__ float enter_tile(const GateParams& p, const Lookback& lb, int row, int n, int ch, float2 m,
-                                            float start) {
-    const int g = n / kGroup, s = g / kSuper;
-    const int nt = n % kGroup, ng = g % kSuper;  // tiles before this one in its group, groups before it in the super-group
-    const bool last = n + 1 == lb.tiles, ends_group = nt == kGroup - 1, ends_super = ends_group && ng == kSuper - 1;
-    if (!last) st_pair(p.words + lb.tile_map(row, n) + ch, m);
-    // the tiles of the group first: the group's map waits for nothing else
-    u64 w[kGroup - 1];
-    read_words(p, p.words + lb.tile_map(row, n - nt) + ch, lb.cb, nt, w);
-    if (ends_group && !last) {
-        float2 all = as_pair(w[0]);
-#pragma unroll
-        for (int i = 1; i < kGroup - 1; ++i) all = then(all, as_pair(w[i]));
-        st_pair(p.words + lb.group_map(row, g) + ch, then(all, m));
-    }
-    float h = start;
-    if (s > 0) {
-        u64 v[1];
-        read_words(p, p.words + lb.super_state(row, s) + ch, 0, 1, v);
-        h = as_pair(v[0]).x;
-    }
-#pragma unroll
-    for (int half = 0; half < kSuper; half += kSuper / 2) {
-        u64 v[kSuper / 2];
-        const int here = min(ng - half, kSuper / 2);
-        if (here > 0) {
-            read_words(p, p.words + lb.group_map(row, g - ng + half) + ch, lb.cb, here, v);
-#pragma unroll
-            for (int i = 0; i < kSuper / 2; ++i)
-                if (i < here) h = pass(as_pair(v[i]), h);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < kGroup - 1; ++i)
-        if (i < nt) h = pass(as_pair(w[i]), h);
-    if (ends_super && !last) st_pair(p.words + lb.super_state(row, s + 1) + ch, make_float2(pass(m, h), 0.f));
-    return h;
-}
-
-// The tiles of a block, by ticket where tiles wait for one another.  The
-// joining warps take the next ticket between the two barriers of a tile.
-struct Tickets {
-    unsigned* word;  // starts at ~0
-    unsigned* slot;  // shared
-    __device__ unsigned first() {
-        if (!word) return blockIdx.x;
-        if (threadIdx.x == 0) *slot = atomicAdd(word, 1u) + 1u;
-        __syncthreads();
-        return *slot;
-    }
-    __device__ unsigned take(unsigned k) { return word ? atomicAdd(word, 1u) + 1u : k + gridDim.x; }
-};
-
-// Loads a run: x and gates of tokens [0, nt), the bits of its resets.
-template <typename T, bool SHARED, bool VEC>
-struct Run {
-    Lane<T, kCh, VEC> x[kTok];
-    Lane<T, SHARED ? 1 : kCh, VEC && !SHARED> g[kTok];
-    unsigned resets;
-    __device__ __forceinline__ void load(const GateParams& p, int b, int hd, int t0, int c, int nc, int nt) {
-        const T* xp = static_cast<const T*>(p.x) + b * p.sx[0] + hd * p.sx[1] + t0 * p.sx[2] + c;
-        const T* gp = static_cast<const T*>(p.g) + b * p.sg[0] + hd * p.sg[1] + t0 * p.sg[2] + (SHARED ? 0 : c);
-#pragma unroll
-        for (int i = 0; i < kTok; ++i)
-            if (i < nt) {
-                x[i].load(xp + i * p.sx[2], nc);
-                g[i].load(gp + i * p.sg[2], SHARED ? 1 : nc);
-            }
-        resets = 0;
-        if (p.reset) {
-            const unsigned char* rp = p.reset + (long long)b * p.T + t0;
-#pragma unroll
-            for (int i = 0; i < kTok; ++i)
-                if (i < nt && rp[i]) resets |= 1u << i;
-        }
-    }
-    __device__ __forceinline__ bool reset(int i) const { return (resets >> i) & 1u; }
-};
-
 // ---- forward -----------------------------------------------------------------
 // LANES x 4 channels to a token, kData / LANES runs of kTok tokens to a tile.
-template <typename T, bool SIG, bool SHARED, int LANES, bool VEC>
-__global__ void __launch_bounds__(block_threads(LANES), sizeof(T) == 2 ? 2 : 1)
+template <typename T, bool SIG, bool SHARED, int LANES>
+__global__ void __launch_bounds__(block_threads(LANES), 1)
 gated_scan_kernel(const GateParams p) {
     constexpr int CB = LANES * kCh, RUNS = kData / LANES, TILE = RUNS * kTok, NG = SHARED ? 1 : kCh;
     __shared__ float2 runs[RUNS][CB];  // maps of the runs, then of what is before each in the tile
@@ -264,7 +63,10 @@ gated_scan_kernel(const GateParams p) {
                 runs[r][ch] = m;
                 m = then(m, f);
             }
-            if (p.words) h = enter_tile(p, lb, row, n, ch, m, h);
+            if (p.words) {
+                publish_tile(p, lb, row, n, ch, m);
+                h = enter_tile(p, lb, row, n, ch, m, h);
+            }
             entering[ch] = h;
             if (p.carry && ch < p.d) p.carry[((long long)row * p.tiles + n) * p.d + ch] = h;
             __syncthreads();  // what enters each run is there
@@ -279,7 +81,7 @@ gated_scan_kernel(const GateParams p) {
         const int b = row / p.H, hd = row - b * p.H;
         const int t0 = n * TILE + run * kTok;
         const int nt = nc > 0 ? min(kTok, p.T - t0) : 0;  // tokens of this thread, none where <= 0
-        Run<T, SHARED, VEC> in;
+        Run<T, SHARED, false> in;
         in.load(p, b, hd, t0, c, nc, nt);
         float gate[kTok][NG];  // z of the sigmoid, a of the decay
         float A[kCh], X[kCh];
@@ -318,11 +120,11 @@ gated_scan_kernel(const GateParams p) {
                         h[j] = SIG ? fmaf(ga, xv - h[j], h[j]) : fmaf(ga, h[j], xv);
                     }
                     if (p.out_bf16) {
-                        Lane<bf16, kCh, VEC> ov;
+                        Lane<bf16, kCh, false> ov;
                         ov.set(h);
                         ov.store(static_cast<bf16*>(p.o) + off + i * p.so[2], nc);
                     } else {
-                        Lane<float, kCh, VEC> ov;
+                        Lane<float, kCh, false> ov;
                         ov.set(h);
                         ov.store(static_cast<float*>(p.o) + off + i * p.so[2], nc);
                     }
@@ -336,172 +138,301 @@ gated_scan_kernel(const GateParams p) {
     }
 }
 
-// ---- gradient ----------------------------------------------------------------
-// The same walk from the last tile to the first for mu_t = a_t lam_t, the part of
-// the gradient that reaches h_{t-1}: mu_t = a_t (dh_t + mu_{t+1}), so a run maps
-// the mu behind it to the mu before it by the same A and a Y of its own.  The
-// states inside the tile are formed anew, from the kept state that enters it; a
-// thread's h_{t-1} wait in shared memory until its way back.
-template <typename T, typename TO, bool SIG, bool SHARED, int LANES, bool VEC>
-__global__ void __launch_bounds__(block_threads(LANES), sizeof(T) == 2 ? 2 : 1)
-gated_scan_bwd_kernel(const GateParams p) {
-    constexpr int CB = LANES * kCh, RUNS = kData / LANES, TILE = RUNS * kTok, NG = SHARED ? 1 : kCh;
-    __shared__ float2 fwd[RUNS][CB];   // maps of h; .x becomes the state that enters the run
-    __shared__ float2 back[RUNS][CB];  // maps of mu, then of what is behind each run in the tile
-    __shared__ float entering[CB];
-    __shared__ unsigned slot;
-    extern __shared__ float4 before[];  // [kTok][kData]: h_{t-1}
+
+// ---- the pipelined forward -----------------------------------------------------
+// One block to an SM and a ring of tiles in shared memory, so that several tiles
+// of a block wait for the states that enter them while others are loaded,
+// mapped and written.  Warps have one role each and meet on mbarriers:
+//   loader   takes tickets and loads tiles of x (and gates) by bulk tensor copies;
+//   mappers  form the maps of the tile's runs, compose and publish the tile's map;
+//   joiners  (kJoin groups, every kJoin-th tile each) find the state that enters
+//            the tile and from it the state that enters each run;
+//   writers  walk the runs again and write the outputs.
+// Every wait is bounded in time, as in the other kernels of this library.
+constexpr int kJoin = 3;
+
+template <typename T, bool SHARED, int LANES>
+struct PipeLayout {
+    static constexpr int CB = LANES * kCh, RUNS = kData / LANES, TILE = RUNS * kTok;
+    static constexpr uint32_t kTileBytes = TILE * CB * sizeof(T);  // of x, and of the gates
+    static constexpr uint32_t kMaps = RUNS * CB * 8;
+    static constexpr uint32_t kStage = kTileBytes * (SHARED ? 1 : 2) + kMaps;
+    static constexpr int kStages = 225 * 1024 / kStage > 8 ? 8 : 225 * 1024 / kStage;
+    static constexpr uint32_t kBytes = kStage * kStages + 128;  // and alignment to 128 bytes
+    static constexpr int kThreads = 32 + kData + kJoin * CB + kData;
+};
+
+__device__ __forceinline__ void mbar_arrive(uint32_t a) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(a) : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t mbar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(mbar)
+        : "memory");
+}
+
+// four channels of one token in shared memory, as fp32
+__device__ __forceinline__ void four(const float* p, float (&v)[4]) {
+    const float4 a = *reinterpret_cast<const float4*>(p);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+}
+__device__ __forceinline__ void four(const bf16* p, float (&v)[4]) {
+    const uint2 a = *reinterpret_cast<const uint2*>(p);
+    v[0] = __uint_as_float(a.x << 16); v[1] = __uint_as_float(a.x & 0xffff0000u);
+    v[2] = __uint_as_float(a.y << 16); v[3] = __uint_as_float(a.y & 0xffff0000u);
+}
+
+template <typename T, bool SIG, bool SHARED, int LANES>
+__global__ void __launch_bounds__(PipeLayout<T, SHARED, LANES>::kThreads, 1)
+gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mg, const GateParams p) {
+    using LY = PipeLayout<T, SHARED, LANES>;
+    constexpr int CB = LY::CB, RUNS = LY::RUNS, TILE = LY::TILE, S = LY::kStages;
+    constexpr unsigned kEnd = 0xffffffffu;
+    extern __shared__ __align__(128) unsigned char raw[];
+    __shared__ __align__(8) unsigned long long bars[5 * S];
+    static_assert(S >= kJoin, "the ends of the tickets take a stage for each group of joiners");
+    __shared__ unsigned tile_of_stage[S], reset_bits[S][RUNS];
+    __shared__ float2 total[S][CB];
+    __shared__ volatile int abort_flag;
+    unsigned char* const base = raw + ((128u - (smem_u32(raw) & 127u)) & 127u);
+    const int tid = threadIdx.x, warp = tid >> 5;
+    auto full = [&](int s) { return smem_u32(&bars[s]); };            // the tile is loaded
+    auto mapped = [&](int s) { return smem_u32(&bars[S + s]); };      // its runs' maps and its own are there
+    auto joined = [&](int s) { return smem_u32(&bars[2 * S + s]); };  // the states that enter its runs are there
+    auto empty = [&](int s) { return smem_u32(&bars[3 * S + s]); };   // its outputs are written
+    auto runs = [&](int s) { return smem_u32(&bars[4 * S + s]); };    // every mapper's runs are mapped
+    auto sx = [&](int s) { return reinterpret_cast<T*>(base + (size_t)s * LY::kStage); };
+    auto sg = [&](int s) { return reinterpret_cast<T*>(base + (size_t)s * LY::kStage + LY::kTileBytes); };
+    auto maps = [&](int s) {
+        return reinterpret_cast<float2*>(base + (size_t)s * LY::kStage + LY::kTileBytes * (SHARED ? 1 : 2));
+    };
+    if (tid == 0) {
+        abort_flag = 0;
+        for (int s = 0; s < S; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(mapped(s), CB / 32);
+            mbar_init(joined(s), CB / 32);
+            mbar_init(empty(s), kData / 32);
+            mbar_init(runs(s), kData / 32);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+        if (abort_flag) return false;
+        if (mbar_try(bar, parity)) return true;
+        const unsigned long long t0 = globaltimer();
+        while (!mbar_try(bar, parity)) {
+            if (abort_flag) return false;
+            if (globaltimer() - t0 > 2 * kGateWaitNs) {  // longer than the joiners' own waits
+                abort_flag = 1;
+                atomicExch(p.status, (int)kDevWaitTimeout);
+                return false;
+            }
+        }
+        return true;
+    };
     const int rows = p.B * p.H;
     const Lookback lb(rows, p.tiles, CB);
-    Tickets tickets{reinterpret_cast<unsigned*>(p.words), &slot};
-    unsigned k = tickets.first();
-    if (threadIdx.x >= kData) {
-        const int ch = threadIdx.x - kData;
-        while (k < p.total) {
-            const int n = (int)(k / (unsigned)rows), row = (int)(k - (unsigned)n * (unsigned)rows);
-            float mu = 0.f, h = 0.f;
-            if (ch < p.d) {
-                if (p.dstate_out) mu = p.dstate_out[(long long)row * p.d + ch];
-                h = p.carry[((long long)row * p.tiles + (p.tiles - 1 - n)) * p.d + ch];
+    auto place = [&](unsigned k, int& n, int& row, int& b, int& hd) {
+        n = (int)(k / (unsigned)rows);
+        row = (int)(k - (unsigned)n * (unsigned)rows);
+        b = row / p.H;
+        hd = row - b * p.H;
+    };
+    int n, row, b, hd;
+
+    if (warp == 0) {  // loader
+        if (tid != 0) return;
+        Tickets tickets{reinterpret_cast<unsigned*>(p.words), nullptr};
+        LoadLedger<S> loads(full(0));
+        unsigned k = p.words ? tickets.take(0) : blockIdx.x;
+        int ends = 0;
+        for (unsigned i = 0; ends < kJoin; ++i) {
+            const int s = (int)(i % S);
+            if (!wait(empty(s), ((i / S) & 1u) ^ 1u)) break;
+            if (k >= p.total) {  // one end to each group of joiners
+                tile_of_stage[s] = kEnd;
+                mbar_arrive(full(s));
+                ++ends;
+                continue;
             }
-            __syncthreads();
-            if (ch == 0) slot = tickets.take(k);
-            float2 m = make_float2(1.f, 0.f);
-#pragma unroll 8
-            for (int r = RUNS - 1; r >= 0; --r) {
-                const float2 f = back[r][ch];
-                back[r][ch] = m;
-                m = then(m, f);
-            }
-#pragma unroll 8
-            for (int r = 0; r < RUNS; ++r) {
-                const float2 f = fwd[r][ch];
-                fwd[r][ch].x = h;
-                h = pass(f, h);
-            }
-            if (p.words) mu = enter_tile(p, lb, row, n, ch, m, mu);
-            entering[ch] = mu;
-            __syncthreads();
-            k = slot;
+            tile_of_stage[s] = k;
+            place(k, n, row, b, hd);
+            loads.note(s);
+            mbar_expect_tx(full(s), (uint32_t)(TILE * p.d * sizeof(T)) * (SHARED ? 1u : 2u));
+            tma_load_4d(smem_u32(sx(s)), &mx, 0, n * TILE, hd, b, full(s));
+            if (!SHARED) tma_load_4d(smem_u32(sg(s)), &mg, 0, n * TILE, hd, b, full(s));
+            k = tickets.take(k);
         }
+        if (abort_flag && !loads.settle()) atomicExch(p.status, (int)kDevWaitTimeout);
         return;
     }
-    const int tid = threadIdx.x, lane = tid % LANES, run = tid / LANES;
-    const int c = lane * kCh, nc = p.d - c;
-    while (k < p.total) {
-        const int n = (int)(k / (unsigned)rows), row = (int)(k - (unsigned)n * (unsigned)rows);
-        const int b = row / p.H, hd = row - b * p.H;
-        const int t0 = (p.tiles - 1 - n) * TILE + run * kTok;
-        const int nt = nc > 0 ? min(kTok, p.T - t0) : 0;
-        Run<T, SHARED, VEC> in;
-        in.load(p, b, hd, t0, c, nc, nt);
-        Lane<TO, kCh, VEC> dh[kTok];
-        const TO* up = static_cast<const TO*>(p.dout) + b * p.sdo[0] + hd * p.sdo[1] + t0 * p.sdo[2] + c;
+    if (warp >= 1 + kData / 32 && warp < 1 + kData / 32 + kJoin * (CB / 32)) {  // joiners
+        const int j = (warp - 1 - kData / 32) / (CB / 32);
+        const int ch = tid - 32 - kData - j * CB;
+        for (unsigned i = (unsigned)j;; i += kJoin) {
+            const int s = (int)(i % S);
+            if (!wait(mapped(s), (i / S) & 1u)) return;
+            const unsigned k = tile_of_stage[s];
+            if (k != kEnd) {
+                place(k, n, row, b, hd);
+                float h = p.state_in && ch < p.d ? p.state_in[(long long)row * p.d + ch] : 0.f;
+                if (p.words) h = enter_tile(p, lb, row, n, ch, total[s][ch], h);
+                if (p.carry && ch < p.d) p.carry[((long long)row * p.tiles + n) * p.d + ch] = h;
+                float2* m = maps(s) + ch;
 #pragma unroll
-        for (int i = 0; i < kTok; ++i)
-            if (i < nt) dh[i].load(up + i * p.sdo[2], nc);
-        float gate[kTok][NG];
-        float A[kCh], X[kCh], Y[kCh];
-#pragma unroll
-        for (int j = 0; j < kCh; ++j) { A[j] = 1.f; X[j] = 0.f; Y[j] = 0.f; }
-#pragma unroll
-        for (int i = 0; i < kTok; ++i)
-            if (i < nt) {
-#pragma unroll
-                for (int j = 0; j < NG; ++j) gate[i][j] = SIG ? keep_out(in.g[i].get(j)) : in.g[i].get(j);
-#pragma unroll
-                for (int j = 0; j < kCh; ++j) {
-                    const float ga = gate[i][SHARED ? 0 : j], xv = in.x[i].get(j);
-                    if (in.reset(i)) X[j] = 0.f;
-                    X[j] = SIG ? fmaf(ga, xv - X[j], X[j]) : fmaf(ga, X[j], xv);
-                    A[j] = SIG ? fmaf(-ga, A[j], A[j]) : ga * A[j];
+                for (int r = 0; r < RUNS; ++r) {
+                    const float2 f = m[r * CB];
+                    m[r * CB].x = h;
+                    h = pass(f, h);
                 }
             }
-#pragma unroll
-        for (int i = kTok - 1; i >= 0; --i)
-            if (i < nt) {
-#pragma unroll
-                for (int j = 0; j < kCh; ++j) {
-                    const float ga = gate[i][SHARED ? 0 : j], lam = dh[i].get(j) + Y[j];
-                    Y[j] = in.reset(i) ? 0.f : SIG ? fmaf(-ga, lam, lam) : ga * lam;
-                }
-            }
-#pragma unroll
-        for (int j = 0; j < kCh; ++j) {
-            const float a = in.resets ? cut() : A[j] + 0.f;
-            fwd[run][c + j] = make_float2(a, X[j]);
-            back[run][c + j] = make_float2(a, Y[j]);
-        }
-        __syncthreads();
-        __syncthreads();
-        k = slot;
-        float mu[kCh];
-        if (nt > 0) {
-            float h[kCh];
-#pragma unroll
-            for (int j = 0; j < kCh; ++j) {
-                h[j] = fwd[run][c + j].x;
-                mu[j] = pass(back[run][c + j], entering[c + j]);
-            }
-#pragma unroll
-            for (int i = 0; i < kTok; ++i)
-                if (i < nt) {
-#pragma unroll
-                    for (int j = 0; j < kCh; ++j)
-                        if (in.reset(i)) h[j] = 0.f;
-                    before[i * kData + tid] = make_float4(h[0], h[1], h[2], h[3]);
-#pragma unroll
-                    for (int j = 0; j < kCh; ++j) {
-                        const float ga = gate[i][SHARED ? 0 : j], xv = in.x[i].get(j);
-                        h[j] = SIG ? fmaf(ga, xv - h[j], h[j]) : fmaf(ga, h[j], xv);
-                    }
-                }
-        }
-        T* dxp = static_cast<T*>(p.dx) + b * p.sdx[0] + hd * p.sdx[1] + t0 * p.sdx[2] + c;
-        T* dgp = static_cast<T*>(p.dg) + b * p.sdg[0] + hd * p.sdg[1] + t0 * p.sdg[2] + (SHARED ? 0 : c);
-#pragma unroll
-        for (int i = kTok - 1; i >= 0; --i) {
-            float gx[kCh], gg[kCh];
-            const bool live = i < nt;
-            if (live) {
-                const float4 hb4 = before[i * kData + tid];
-                const float hb[kCh] = {hb4.x, hb4.y, hb4.z, hb4.w};
-#pragma unroll
-                for (int j = 0; j < kCh; ++j) {
-                    const float ga = gate[i][SHARED ? 0 : j], lam = dh[i].get(j) + mu[j];
-                    if (SIG) {
-                        gx[j] = ga * lam;
-                        gg[j] = fmaf(-ga, gx[j], gx[j]) * (hb[j] - in.x[i].get(j));
-                        mu[j] = in.reset(i) ? 0.f : fmaf(-ga, lam, lam);
-                    } else {
-                        gx[j] = lam;
-                        gg[j] = lam * hb[j];
-                        mu[j] = in.reset(i) ? 0.f : ga * lam;
-                    }
-                }
-                Lane<T, kCh, VEC> ov;
-                ov.set(gx);
-                ov.store(dxp + i * p.sdx[2], nc);
-            }
-            if (SHARED) {  // the sum over the token's channels
-                float s = 0.f;
-#pragma unroll
-                for (int j = 0; j < kCh; ++j) s += live && j < nc ? gg[j] : 0.f;
-#pragma unroll
-                for (int w = LANES / 2; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-                if (live && lane == 0) dgp[i * p.sdg[2]] = from_f32<T>(s);
-            } else if (live) {
-                Lane<T, kCh, VEC> ov;
-                ov.set(gg);
-                ov.store(dgp + i * p.sdg[2], nc);
-            }
-        }
-        if (p.dstate_in && t0 == 0 && nt > 0) {
-#pragma unroll
-            for (int j = 0; j < kCh; ++j)
-                if (j < nc) p.dstate_in[(long long)row * p.d + c + j] = mu[j];
+            __syncwarp();
+            if ((tid & 31) == 0) mbar_arrive(joined(s));
+            if (k == kEnd) return;
         }
     }
+    const bool mapper = warp < 1 + kData / 32;
+    const int at = mapper ? tid - 32 : tid - (LY::kThreads - kData);
+    const int lane = at % LANES, run = at / LANES;
+    const int c = lane * kCh, nc = p.d - c;
+    constexpr int NG = SHARED ? 1 : kCh;
+    int ends = 0;
+    for (unsigned i = 0;; ++i) {
+        const int s = (int)(i % S);
+        const uint32_t phase = (i / S) & 1u;
+        if (!mapper && !wait(joined(s), phase)) return;
+        if (!wait(full(s), phase)) return;
+        const unsigned k = tile_of_stage[s];
+        if (k == kEnd) {
+            if (!mapper) return;
+            if (at < CB && (tid & 31) == 0) mbar_arrive(mapped(s));
+            if (++ends == kJoin) return;
+            continue;
+        }
+        place(k, n, row, b, hd);
+        const int t0 = n * TILE + run * kTok;
+        const int nt = nc > 0 ? min(kTok, p.T - t0) : 0;
+        const T* xs = sx(s) + run * kTok * p.d + c;
+        const T* gs = sg(s) + run * kTok * p.d + c;
+        const T* gp = static_cast<const T*>(p.g) + b * p.sg[0] + hd * p.sg[1] + t0 * p.sg[2];
+        float gl[SHARED ? kTok : 1];
+        if (SHARED) {
+#pragma unroll
+            for (int i2 = 0; i2 < kTok; ++i2)
+                if (i2 < nt) gl[i2] = to_f32(gp[i2 * p.sg[2]]);
+        }
+        auto gates = [&](int i2, float (&ga)[NG]) {
+            if constexpr (SHARED) {
+                ga[0] = SIG ? keep_out(gl[i2]) : gl[i2];
+            } else {
+                four(gs + i2 * p.d, ga);
+                if (SIG) {
+#pragma unroll
+                    for (int j = 0; j < kCh; ++j) ga[j] = keep_out(ga[j]);
+                }
+            }
+        };
+        if (mapper) {
+            unsigned resets = 0;
+            if (p.reset) {
+                const unsigned char* rp = p.reset + (long long)b * p.T + t0;
+#pragma unroll
+                for (int i2 = 0; i2 < kTok; ++i2)
+                    if (i2 < min(kTok, p.T - t0) && rp[i2]) resets |= 1u << i2;
+                if (lane == 0) reset_bits[s][run] = resets;
+            }
+            float A[kCh], X[kCh];
+#pragma unroll
+            for (int j = 0; j < kCh; ++j) { A[j] = 1.f; X[j] = 0.f; }
+#pragma unroll
+            for (int i2 = 0; i2 < kTok; ++i2)
+                if (i2 < nt) {
+                    float xv[kCh], ga[NG];
+                    four(xs + i2 * p.d, xv);
+                    gates(i2, ga);
+#pragma unroll
+                    for (int j = 0; j < kCh; ++j) {
+                        const float z = ga[SHARED ? 0 : j];
+                        if ((resets >> i2) & 1u) X[j] = 0.f;
+                        X[j] = SIG ? fmaf(z, xv[j] - X[j], X[j]) : fmaf(z, X[j], xv[j]);
+                        A[j] = SIG ? fmaf(-z, A[j], A[j]) : z * A[j];
+                    }
+                }
+            float4* m4 = reinterpret_cast<float4*>(maps(s) + run * CB + c);
+#pragma unroll
+            for (int j = 0; j < kCh; ++j) A[j] = resets ? cut() : A[j] + 0.f;
+            m4[0] = make_float4(A[0], X[0], A[1], X[1]);
+            m4[1] = make_float4(A[2], X[2], A[3], X[3]);
+            __syncwarp();
+            if ((tid & 31) == 0) mbar_arrive(runs(s));
+            if (at < CB) {  // one channel of the tile's map
+                if (!wait(runs(s), phase)) return;
+                float2 m = maps(s)[at];
+#pragma unroll
+                for (int r = 1; r < RUNS; ++r) m = then(m, maps(s)[r * CB + at]);
+                if (p.words) publish_tile(p, lb, row, n, at, m);
+                total[s][at] = m;
+                __syncwarp();
+                if ((tid & 31) == 0) mbar_arrive(mapped(s));
+            }
+        } else {
+            const unsigned resets = p.reset ? reset_bits[s][run] : 0u;
+            float h[kCh];
+            const float4* m4 = reinterpret_cast<const float4*>(maps(s) + run * CB + c);
+            const float4 lo = m4[0], hi = m4[1];
+            h[0] = lo.x; h[1] = lo.z; h[2] = hi.x; h[3] = hi.z;
+            const long long off = b * p.so[0] + hd * p.so[1] + t0 * p.so[2] + c;
+#pragma unroll
+            for (int i2 = 0; i2 < kTok; ++i2)
+                if (i2 < nt) {
+                    float xv[kCh], ga[NG];
+                    four(xs + i2 * p.d, xv);
+                    gates(i2, ga);
+#pragma unroll
+                    for (int j = 0; j < kCh; ++j) {
+                        const float z = ga[SHARED ? 0 : j];
+                        if ((resets >> i2) & 1u) h[j] = 0.f;
+                        h[j] = SIG ? fmaf(z, xv[j] - h[j], h[j]) : fmaf(z, h[j], xv[j]);
+                    }
+                    if (p.out_bf16) {
+                        Lane<bf16, kCh, true> ov;
+                        ov.set(h);
+                        ov.store(static_cast<bf16*>(p.o) + off + i2 * p.so[2], nc);
+                    } else {
+                        Lane<float, kCh, true> ov;
+                        ov.set(h);
+                        ov.store(static_cast<float*>(p.o) + off + i2 * p.so[2], nc);
+                    }
+                }
+            __syncwarp();
+            if ((tid & 31) == 0) mbar_arrive(empty(s));
+            if (p.state_out && nt > 0 && t0 + nt == p.T)
+                *reinterpret_cast<float4*>(p.state_out + (long long)row * p.d + c) = make_float4(h[0], h[1], h[2], h[3]);
+        }
+    }
+}
+
+// A map of a strided [B][H][T][d] tensor, box of TILE tokens; false where its
+// strides or address do not allow bulk tensor copies.
+bool gate_map(CUtensorMap* m, const void* base, int es, const long long (&s)[3], int B, int H, int T, int d, int tile) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn || (reinterpret_cast<uintptr_t>(base) & 15u) || (d * es) % 16) return false;
+    const int sizes[3] = {T, H, B};
+    const long long st[3] = {s[2], s[1], s[0]};
+    cuuint64_t strides[3];
+    for (int i = 0; i < 3; ++i) {
+        strides[i] = (cuuint64_t)(sizes[i] == 1 ? (long long)d * es : st[i] * es);  // a single index needs none
+        if (sizes[i] > 1 && (st[i] <= 0 || (st[i] * es) % 16 || st[i] * es >= (1LL << 40))) return false;
+    }
+    const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)T, (cuuint64_t)H, (cuuint64_t)B};
+    const cuuint32_t box[4] = {(cuuint32_t)d, (cuuint32_t)tile, 1, 1}, step[4] = {1, 1, 1, 1};
+    return fn(m, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4,
+              const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
 }
 
 // One token: a read and a write of the state and of the token's n d values are
@@ -535,92 +466,6 @@ __global__ void __launch_bounds__(256) gated_step_kernel(const float* state, con
     ov.store(o + row * ldo + c, N);
 }
 
-template <typename F>
-cudaError_t by_types(int dtype, int out_dtype, F&& f) {
-    if (dtype == HLA2_DTYPE_BF16) return out_dtype == HLA2_DTYPE_BF16 ? f(bf16{}, bf16{}) : f(bf16{}, float{});
-    return out_dtype == HLA2_DTYPE_BF16 ? f(float{}, bf16{}) : f(float{}, float{});
-}
-template <typename F>
-cudaError_t by_form(int form, int shared, F&& f) {
-    using std::false_type;
-    using std::true_type;
-    if (form == HLA2_GATE_SIGMOID) return shared ? f(true_type{}, true_type{}) : f(true_type{}, false_type{});
-    return shared ? f(false_type{}, true_type{}) : f(false_type{}, false_type{});
-}
-
-int check_gated(const char* what, int B, int H, int T, int d, int form, int dtype, int out_dtype) {
-    if (B <= 0 || H <= 0 || T <= 0 || d <= 0)
-        return set_error(HLA2_ERR_INVALID, "%s: sizes must be positive (B=%d H=%d T=%d d=%d)", what, B, H, T, d);
-    if (d > 128) return set_error(HLA2_ERR_UNSUPPORTED, "%s: d=%d: this build supports d <= 128", what, d);
-    if ((long long)B * H > 65535) return set_error(HLA2_ERR_UNSUPPORTED, "%s: B*H=%lld exceeds 65535", what, (long long)B * H);
-    if (form != HLA2_GATE_SIGMOID && form != HLA2_GATE_DECAY) return set_error(HLA2_ERR_UNSUPPORTED, "%s: unknown form %d", what, form);
-    if (!known_dtype(dtype) || !known_dtype(out_dtype))
-        return set_error(HLA2_ERR_UNSUPPORTED, "%s: unknown dtype %d or output dtype %d", what, dtype, out_dtype);
-    if (T > (1 << 30) || (long long)B * H * T > (1LL << 33)) return set_error(HLA2_ERR_UNSUPPORTED, "%s: problem too large", what);
-    return HLA2_OK;
-}
-
-// strides of operand i of `strides`, or those of a dense [B][H][T][d] (or [B][H][T]) tensor
-void take_strides(long long (&s)[3], const long long* strides, int i, int H, int T, int d) {
-    if (strides) {
-        for (int k = 0; k < 3; ++k) s[k] = strides[3 * i + k];
-    } else {
-        s[0] = (long long)H * T * d; s[1] = (long long)T * d; s[2] = d;
-    }
-}
-
-
-size_t lookback_bytes(int rows, int tiles, int cb) {
-    if (tiles <= 1) return 0;
-    return Lookback(rows, tiles, cb).words() * 8;
-}
-
-// Blocks of a kernel that fit the device at once, at most one to a tile.  What
-// an SM holds is asked once for each kernel and device.
-cudaError_t persistent_blocks(const void* kernel, int threads, size_t smem, unsigned total, unsigned* blocks) {
-    static std::mutex mu;
-    static std::map<std::pair<const void*, int>, unsigned> known;
-    int dev = 0;
-    if (cudaError_t e = cudaGetDevice(&dev)) return e;
-    unsigned fit = 0;
-    {
-        std::lock_guard<std::mutex> lk(mu);
-        auto it = known.find({kernel, dev});
-        if (it != known.end()) fit = it->second;
-    }
-    if (!fit) {
-        if (smem)
-            if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem))
-                return e;
-        int per_sm = 0;
-        if (cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem)) return e;
-        fit = (unsigned)(per_sm > 0 ? per_sm : 1) * (unsigned)sm_count();
-        std::lock_guard<std::mutex> lk(mu);
-        known[{kernel, dev}] = fit;
-    }
-    *blocks = total < fit ? total : fit;
-    return cudaSuccess;
-}
-
-// Sets the workspace's words to "nothing yet".
-cudaError_t begin_lookback(GateParams& p, int cb, void* workspace, cudaStream_t s) {
-    p.total = (unsigned)((long long)p.B * p.H * p.tiles);
-    if (p.tiles <= 1) return cudaSuccess;
-    p.words = static_cast<unsigned long long*>(workspace);
-    p.status = device_status_word();
-    return cudaMemsetAsync(p.words, 0xff, Lookback(p.B * p.H, p.tiles, cb).words() * 8, s);
-}
-
-template <int N>
-using Int = std::integral_constant<int, N>;
-
-template <typename F>
-cudaError_t by_lanes(int d, bool vec, F&& f) {
-    using std::false_type;
-    using std::true_type;
-    if (d <= 64) return vec ? f(Int<16>{}, true_type{}) : f(Int<16>{}, false_type{});
-    return vec ? f(Int<32>{}, true_type{}) : f(Int<32>{}, false_type{});
-}
 
 }  // namespace
 }  // namespace hla2
@@ -664,73 +509,31 @@ extern "C" int hla2_gated_scan(const void* X, const void* G, const unsigned char
     take_strides(p.so, strides, 2, H, T, d);
     const int lanes = lanes_of(d), tile = tile_of(lanes);
     p.tiles = (T + tile - 1) / tile;
-    const bool vec = d % kCh == 0 && aligned_to(X, es, p.sx, 3, kCh * es) && aligned_to(O, os, p.so, 3, kCh * os) &&
-                     (gate_shared || aligned_to(G, es, p.sg, 3, kCh * es));
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = begin_lookback(p, lanes * kCh, workspace, s);
     p.out_bf16 = out_dtype == HLA2_DTYPE_BF16;
+    CUtensorMap mx{}, mg{};
+    const bool pipe = gate_map(&mx, X, es, p.sx, B, H, T, d, tile) &&
+                      (gate_shared || gate_map(&mg, G, es, p.sg, B, H, T, d, tile)) && d % kCh == 0 &&
+                      aligned_to(O, os, p.so, 3, kCh * os) && aligned_to(state_out, 4, nullptr, 0, 16);
     if (e == cudaSuccess) e = by_types(dtype, HLA2_DTYPE_F32, [&](auto tin, auto) {
         return by_form(form, gate_shared, [&](auto sig, auto shared) {
-            return by_lanes(d, vec, [&](auto ln, auto v) {
-                constexpr int threads = block_threads(decltype(ln)::value);
-                auto kernel = gated_scan_kernel<decltype(tin), decltype(sig)::value, decltype(shared)::value,
-                                                decltype(ln)::value, decltype(v)::value>;
+            return by_lanes(d, [&](auto ln) {
+                using T_ = decltype(tin);
+                constexpr bool SIG = decltype(sig)::value, SHARED = decltype(shared)::value;
+                constexpr int LANES = decltype(ln)::value;
                 unsigned blocks = 0;
-                if (cudaError_t e2 = persistent_blocks(reinterpret_cast<const void*>(kernel), threads, 0, p.total, &blocks)) return e2;
-                kernel<<<blocks, threads, 0, s>>>(p);
-                return cudaGetLastError();
-            });
-        });
-    });
-    note_launches(1);
-    if (e != cudaSuccess) return set_error(HLA2_ERR_LAUNCH, "%s: %s", what, cudaGetErrorString(e));
-    return HLA2_OK;
-}
-
-extern "C" int hla2_gated_scan_backward(const void* X, const void* G, const unsigned char* reset, const float* carry,
-                                        const void* dO, const float* dstate_out, void* dX, void* dG, float* dstate_in,
-                                        int B, int H, int T, int d, const long long* strides, int form, int gate_shared,
-                                        int dtype, int out_dtype, void* workspace, size_t ws_bytes,
-                                        hla2_stream_t stream) {
-    using namespace hla2;
-    const char* what = "gated_scan_backward";
-    if (int rc = check_gated(what, B, H, T, d, form, dtype, out_dtype)) return rc;
-    if (!X || !G || !carry || !dO || !dX || !dG) return set_error(HLA2_ERR_INVALID, "%s: null pointer", what);
-    const int es = dtype_size(dtype), os = dtype_size(out_dtype);
-    if (!aligned_elem(X, es) || !aligned_elem(G, es) || !aligned_elem(dX, es) || !aligned_elem(dG, es) ||
-        !aligned_elem(dO, os) || !aligned_elem(carry, 4) || !aligned_elem(dstate_out, 4) || !aligned_elem(dstate_in, 4))
-        return set_error(HLA2_ERR_INVALID, "%s: pointer not aligned to its element", what);
-    const size_t need = hla2_gated_scan_workspace(B, H, T, d);
-    if (need && (!workspace || ws_bytes < need))
-        return set_error(HLA2_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", what, ws_bytes, need);
-    if (need && reinterpret_cast<uintptr_t>(workspace) % 16)
-        return set_error(HLA2_ERR_INVALID, "%s: workspace not 16-byte aligned", what);
-    GateParams p{};
-    p.x = X; p.g = G; p.reset = reset; p.carry = const_cast<float*>(carry); p.dout = dO; p.dstate_out = dstate_out;
-    p.dx = dX; p.dg = dG; p.dstate_in = dstate_in;
-    p.B = B; p.H = H; p.T = T; p.d = d;
-    take_strides(p.sx, strides, 0, H, T, d);
-    take_strides(p.sg, strides, 1, H, T, gate_shared ? 1 : d);
-    take_strides(p.sdo, strides, 2, H, T, d);
-    take_strides(p.sdx, strides, 3, H, T, d);
-    take_strides(p.sdg, strides, 4, H, T, gate_shared ? 1 : d);
-    const int lanes = lanes_of(d), tile = tile_of(lanes);
-    p.tiles = (T + tile - 1) / tile;
-    const bool vec = d % kCh == 0 && aligned_to(X, es, p.sx, 3, kCh * es) && aligned_to(dX, es, p.sdx, 3, kCh * es) &&
-                     aligned_to(dO, os, p.sdo, 3, kCh * os) &&
-                     (gate_shared || (aligned_to(G, es, p.sg, 3, kCh * es) && aligned_to(dG, es, p.sdg, 3, kCh * es)));
-    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e = begin_lookback(p, lanes * kCh, workspace, s);
-    if (e == cudaSuccess) e = by_types(dtype, out_dtype, [&](auto tin, auto tout) {
-        return by_form(form, gate_shared, [&](auto sig, auto shared) {
-            return by_lanes(d, vec, [&](auto ln, auto v) {
-                auto kernel = gated_scan_bwd_kernel<decltype(tin), decltype(tout), decltype(sig)::value,
-                                                    decltype(shared)::value, decltype(ln)::value, decltype(v)::value>;
-                constexpr int threads = block_threads(decltype(ln)::value);
-                constexpr size_t smem = (size_t)kTok * kData * sizeof(float4);
-                unsigned blocks = 0;
-                if (cudaError_t e2 = persistent_blocks(reinterpret_cast<const void*>(kernel), threads, smem, p.total, &blocks)) return e2;
-                kernel<<<blocks, threads, smem, s>>>(p);
+                if (pipe) {
+                    using LY = PipeLayout<T_, SHARED, LANES>;
+                    auto kernel = gated_pipe_kernel<T_, SIG, SHARED, LANES>;
+                    if (cudaError_t e2 = persistent_blocks(reinterpret_cast<const void*>(kernel), LY::kThreads, LY::kBytes, p.total, &blocks)) return e2;
+                    kernel<<<blocks, LY::kThreads, LY::kBytes, s>>>(mx, mg, p);
+                } else {
+                    constexpr int threads = block_threads(LANES);
+                    auto kernel = gated_scan_kernel<T_, SIG, SHARED, LANES>;
+                    if (cudaError_t e2 = persistent_blocks(reinterpret_cast<const void*>(kernel), threads, 0, p.total, &blocks)) return e2;
+                    kernel<<<blocks, threads, 0, s>>>(p);
+                }
                 return cudaGetLastError();
             });
         });

@@ -1,0 +1,307 @@
+// hla2_gated.cuh -- what the forward (hla2_gated.cu) and the gradient
+// (hla2_gated_bwd.cu) of the gated linear recurrence share: the maps of runs of
+// tokens, how tiles are joined through the workspace, and the host side.
+#pragma once
+
+#include <map>
+#include <mutex>
+
+#include "hla2_layer.cuh"
+#include "hla2_tc_common.cuh"
+
+namespace hla2 {
+namespace {
+
+constexpr int kTok = 8;         // tokens of a run
+constexpr int kCh = 4;          // channels of a thread
+constexpr int kData = 256;      // threads that share a tile: one to a run and four channels
+constexpr int kGroup = 8;       // tiles to a group
+constexpr int kSuper = 16;      // groups to a super-group
+constexpr unsigned long long kGateWaitNs = 2000000000ull;  // bounded waits: 2 s
+
+// Lanes that share a token: they cover 4 channels each, d <= 4 lanes.
+__host__ __device__ constexpr int lanes_of(int d) { return d <= 64 ? 16 : 32; }
+// Tokens of a tile: a state is kept for the gradient at the start of each.
+__host__ __device__ constexpr int tile_of(int lanes) { return kData / lanes * kTok; }
+// Threads of a block of the register kernels: those that hold the tile, and a warp for each 32 channels that joins tiles.
+__host__ __device__ constexpr int block_threads(int lanes) { return kData + lanes * kCh; }
+
+struct GateParams {
+    const void *x, *g, *dout;
+    const unsigned char* reset;
+    const float *state_in, *dstate_out;
+    void *o, *dx, *dg;
+    float *state_out, *dstate_in, *carry;
+    int B, H, T, d;
+    long long sx[3], sg[3], so[3], sdo[3], sdx[3], sdg[3];
+    // workspace (null for one tile): see Lookback
+    unsigned long long* words;
+    int tiles, out_bf16;
+    unsigned total;  // rows * tiles
+    int* status;
+};
+
+// z = 1 - a of the sigmoid gate
+__device__ __forceinline__ float keep_out(float g) {
+    const float e = __expf(-g);
+    return isinf(e) ? 1.f : __fdividef(e, 1.f + e);
+}
+
+// ---- maps h -> A h + X -------------------------------------------------------
+// A run that holds a reset forgets what entered it: its A is -0, which nothing
+// else is (products that are zero are made +0), and then only X counts.
+__device__ __forceinline__ float cut() { return __uint_as_float(0x80000000u); }
+__device__ __forceinline__ bool is_cut(float A) { return __float_as_uint(A) == 0x80000000u; }
+__device__ __forceinline__ float pass(float2 m, float h) { return is_cut(m.x) ? m.y : fmaf(m.x, h, m.y); }
+// first `a`, then `b`
+__device__ __forceinline__ float2 then(float2 a, float2 b) {
+    return make_float2(is_cut(b.x) || is_cut(a.x) ? cut() : a.x * b.x + 0.f, pass(b, a.y));
+}
+
+// ---- the workspace -----------------------------------------------------------
+// A ticket word and a word that says that a wait ran out; then the maps of the
+// tiles and of the groups (A, X for each of a row's channels), then the states
+// that enter the super-groups (h, 0).  Each pair is one 64-bit word, written and
+// read whole, so it is its own flag: the words are set to all ones before the
+// launch, which no pair is (arithmetic gives one NaN, 0x7fffffff), and whoever
+// needs one reads it until it is something else.
+struct Lookback {
+    int rows, tiles, groups, supers, cb;  // cb: channels of a map
+    __host__ __device__ Lookback(int rows, int tiles, int cb)
+        : rows(rows), tiles(tiles), groups((tiles + kGroup - 1) / kGroup),
+          supers((groups + kSuper - 1) / kSuper), cb(cb) {}
+    __host__ __device__ size_t tile_map(int r, int t) const { return 1 + ((size_t)r * tiles + t) * cb; }
+    __host__ __device__ size_t group_map(int r, int g) const { return tile_map(rows, 0) + ((size_t)r * groups + g) * cb; }
+    __host__ __device__ size_t super_state(int r, int s) const {
+        return group_map(rows, 0) + ((size_t)r * supers + s) * cb;
+    }
+    __host__ __device__ size_t words() const { return super_state(rows, 0); }
+};
+
+using u64 = unsigned long long;
+constexpr u64 kNothing = ~0ull;
+
+__device__ __forceinline__ u64 ld_word(const u64* p) {
+    u64 v;
+    asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_pair(u64* p, float2 m) {
+    u64 v = ((u64)__float_as_uint(m.y) << 32) | __float_as_uint(m.x);
+    if (v == kNothing) v = 0x7fffffff7fffffffull;
+    asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
+}
+__device__ __forceinline__ float2 as_pair(u64 v) {
+    return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
+}
+__device__ __forceinline__ u64 gate_timer() {
+    u64 t;
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+    return t;
+}
+
+// Reads w[i] = p[i * step] for i < n until every one is there.  Gives up after
+// 2 s: then this call's results are void, the status word says so, and every
+// later wait of the call ends at once.
+template <int N>
+__device__ __forceinline__ void read_words(const GateParams& p, const u64* src, size_t step, int n, u64 (&w)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = i < n ? ld_word(src + i * step) : 0;
+    u64 t0 = 0;
+    while (true) {
+        bool all = true;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (w[i] == kNothing) {
+                w[i] = ld_word(src + i * step);
+                all = all && w[i] != kNothing;
+            }
+        if (all) return;
+        const u64 now = gate_timer();
+        if (t0 == 0) t0 = now;
+        unsigned* const run_out = reinterpret_cast<unsigned*>(p.words) + 1;
+        if (now - t0 > kGateWaitNs || *(volatile unsigned*)run_out != ~0u) {
+            atomicExch(run_out, 0u);
+            atomicExch(p.status, (int)kDevWaitTimeout);
+            return;
+        }
+    }
+}
+
+// Publishes one channel of a tile's map.  `n` counts tiles in the order of the walk.
+__device__ __forceinline__ void publish_tile(const GateParams& p, const Lookback& lb, int row, int n, int ch, float2 m) {
+    if (n + 1 < lb.tiles) st_pair(p.words + lb.tile_map(row, n) + ch, m);
+}
+
+// The state that enters the tile, for one channel, after publish_tile of its map
+// `m`; also publishes the map of the group, or the state after the super-group,
+// that the tile ends.  `start`: the state that enters the sequence.
+__device__ __forceinline__ float enter_tile(const GateParams& p, const Lookback& lb, int row, int n, int ch, float2 m,
+                                            float start) {
+    const int g = n / kGroup, s = g / kSuper;
+    const int nt = n % kGroup, ng = g % kSuper;  // tiles before this one in its group, groups before it in the super-group
+    const bool last = n + 1 == lb.tiles, ends_group = nt == kGroup - 1, ends_super = ends_group && ng == kSuper - 1;
+    // the tiles of the group first: the group's map waits for nothing else
+    u64 w[kGroup - 1];
+    read_words(p, p.words + lb.tile_map(row, n - nt) + ch, lb.cb, nt, w);
+    if (ends_group && !last) {
+        float2 all = as_pair(w[0]);
+#pragma unroll
+        for (int i = 1; i < kGroup - 1; ++i) all = then(all, as_pair(w[i]));
+        st_pair(p.words + lb.group_map(row, g) + ch, then(all, m));
+    }
+    float h = start;
+    if (s > 0) {
+        u64 v[1];
+        read_words(p, p.words + lb.super_state(row, s) + ch, 0, 1, v);
+        h = as_pair(v[0]).x;
+    }
+#pragma unroll
+    for (int half = 0; half < kSuper; half += kSuper / 2) {
+        u64 v[kSuper / 2];
+        const int here = min(ng - half, kSuper / 2);
+        if (here > 0) {
+            read_words(p, p.words + lb.group_map(row, g - ng + half) + ch, lb.cb, here, v);
+#pragma unroll
+            for (int i = 0; i < kSuper / 2; ++i)
+                if (i < here) h = pass(as_pair(v[i]), h);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kGroup - 1; ++i)
+        if (i < nt) h = pass(as_pair(w[i]), h);
+    if (ends_super && !last) st_pair(p.words + lb.super_state(row, s + 1) + ch, make_float2(pass(m, h), 0.f));
+    return h;
+}
+
+// The tiles of a block, by ticket where tiles wait for one another.  The
+// joining warps take the next ticket between the two barriers of a tile.
+struct Tickets {
+    unsigned* word;  // starts at ~0
+    unsigned* slot;  // shared
+    __device__ unsigned first() {
+        if (!word) return blockIdx.x;
+        if (threadIdx.x == 0) *slot = atomicAdd(word, 1u) + 1u;
+        __syncthreads();
+        return *slot;
+    }
+    __device__ unsigned take(unsigned k) { return word ? atomicAdd(word, 1u) + 1u : k + gridDim.x; }
+};
+
+// Loads a run: x and gates of tokens [0, nt), the bits of its resets.
+template <typename T, bool SHARED, bool VEC>
+struct Run {
+    Lane<T, kCh, VEC> x[kTok];
+    Lane<T, SHARED ? 1 : kCh, VEC && !SHARED> g[kTok];
+    unsigned resets;
+    __device__ __forceinline__ void load(const GateParams& p, int b, int hd, int t0, int c, int nc, int nt) {
+        const T* xp = static_cast<const T*>(p.x) + b * p.sx[0] + hd * p.sx[1] + t0 * p.sx[2] + c;
+        const T* gp = static_cast<const T*>(p.g) + b * p.sg[0] + hd * p.sg[1] + t0 * p.sg[2] + (SHARED ? 0 : c);
+#pragma unroll
+        for (int i = 0; i < kTok; ++i)
+            if (i < nt) {
+                x[i].load(xp + i * p.sx[2], nc);
+                g[i].load(gp + i * p.sg[2], SHARED ? 1 : nc);
+            }
+        resets = 0;
+        if (p.reset) {
+            const unsigned char* rp = p.reset + (long long)b * p.T + t0;
+#pragma unroll
+            for (int i = 0; i < kTok; ++i)
+                if (i < nt && rp[i]) resets |= 1u << i;
+        }
+    }
+    __device__ __forceinline__ bool reset(int i) const { return (resets >> i) & 1u; }
+};
+
+// ------------------------------------------------------------ host side ----
+template <typename F>
+cudaError_t by_types(int dtype, int out_dtype, F&& f) {
+    if (dtype == HLA2_DTYPE_BF16) return out_dtype == HLA2_DTYPE_BF16 ? f(bf16{}, bf16{}) : f(bf16{}, float{});
+    return out_dtype == HLA2_DTYPE_BF16 ? f(float{}, bf16{}) : f(float{}, float{});
+}
+template <typename F>
+cudaError_t by_form(int form, int shared, F&& f) {
+    using std::false_type;
+    using std::true_type;
+    if (form == HLA2_GATE_SIGMOID) return shared ? f(true_type{}, true_type{}) : f(true_type{}, false_type{});
+    return shared ? f(false_type{}, true_type{}) : f(false_type{}, false_type{});
+}
+
+int check_gated(const char* what, int B, int H, int T, int d, int form, int dtype, int out_dtype) {
+    if (B <= 0 || H <= 0 || T <= 0 || d <= 0)
+        return set_error(HLA2_ERR_INVALID, "%s: sizes must be positive (B=%d H=%d T=%d d=%d)", what, B, H, T, d);
+    if (d > 128) return set_error(HLA2_ERR_UNSUPPORTED, "%s: d=%d: this build supports d <= 128", what, d);
+    if ((long long)B * H > 65535) return set_error(HLA2_ERR_UNSUPPORTED, "%s: B*H=%lld exceeds 65535", what, (long long)B * H);
+    if (form != HLA2_GATE_SIGMOID && form != HLA2_GATE_DECAY) return set_error(HLA2_ERR_UNSUPPORTED, "%s: unknown form %d", what, form);
+    if (!known_dtype(dtype) || !known_dtype(out_dtype))
+        return set_error(HLA2_ERR_UNSUPPORTED, "%s: unknown dtype %d or output dtype %d", what, dtype, out_dtype);
+    if (T > (1 << 30) || (long long)B * H * T > (1LL << 33)) return set_error(HLA2_ERR_UNSUPPORTED, "%s: problem too large", what);
+    return HLA2_OK;
+}
+
+// strides of operand i of `strides`, or those of a dense [B][H][T][d] (or [B][H][T]) tensor
+void take_strides(long long (&s)[3], const long long* strides, int i, int H, int T, int d) {
+    if (strides) {
+        for (int k = 0; k < 3; ++k) s[k] = strides[3 * i + k];
+    } else {
+        s[0] = (long long)H * T * d; s[1] = (long long)T * d; s[2] = d;
+    }
+}
+
+
+size_t lookback_bytes(int rows, int tiles, int cb) {
+    if (tiles <= 1) return 0;
+    return Lookback(rows, tiles, cb).words() * 8;
+}
+
+// Blocks of a kernel that fit the device at once, at most one to a tile.  What
+// an SM holds is asked once for each kernel and device.
+cudaError_t persistent_blocks(const void* kernel, int threads, size_t smem, unsigned total, unsigned* blocks) {
+    static std::mutex mu;
+    static std::map<std::pair<const void*, int>, unsigned> known;
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev)) return e;
+    unsigned fit = 0;
+    {
+        std::lock_guard<std::mutex> lk(mu);
+        auto it = known.find({kernel, dev});
+        if (it != known.end()) fit = it->second;
+    }
+    if (!fit) {
+        if (smem)
+            if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem))
+                return e;
+        int per_sm = 0;
+        if (cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem)) return e;
+        fit = (unsigned)(per_sm > 0 ? per_sm : 1) * (unsigned)sm_count();
+        std::lock_guard<std::mutex> lk(mu);
+        known[{kernel, dev}] = fit;
+    }
+    *blocks = total < fit ? total : fit;
+    return cudaSuccess;
+}
+
+// Sets the workspace's words to "nothing yet".
+cudaError_t begin_lookback(GateParams& p, int cb, void* workspace, cudaStream_t s) {
+    p.total = (unsigned)((long long)p.B * p.H * p.tiles);
+    p.status = device_status_word();
+    if (p.tiles <= 1) return cudaSuccess;
+    p.words = static_cast<unsigned long long*>(workspace);
+    return cudaMemsetAsync(p.words, 0xff, Lookback(p.B * p.H, p.tiles, cb).words() * 8, s);
+}
+
+template <int N>
+using Int = std::integral_constant<int, N>;
+
+template <typename F>
+cudaError_t by_lanes(int d, F&& f) {
+    return lanes_of(d) == 16 ? f(Int<16>{}) : f(Int<32>{});
+}
+template <typename F>
+cudaError_t by_bool(bool v, F&& f) {
+    return v ? f(std::true_type{}) : f(std::false_type{});
+}
+
+}  // namespace
+}  // namespace hla2
