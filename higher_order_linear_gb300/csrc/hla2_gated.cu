@@ -347,20 +347,24 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
             float A[kCh], X[kCh];
 #pragma unroll
             for (int j = 0; j < kCh; ++j) { A[j] = 1.f; X[j] = 0.f; }
+            auto walk = [&](auto plain) {  // plain: a whole run without resets
 #pragma unroll
-            for (int i2 = 0; i2 < kTok; ++i2)
-                if (i2 < nt) {
-                    float xv[kCh], ga[NG];
-                    four(xs + i2 * p.d, xv);
-                    gates(i2, ga);
+                for (int i2 = 0; i2 < kTok; ++i2)
+                    if (plain || i2 < nt) {
+                        float xv[kCh], ga[NG];
+                        four(xs + i2 * p.d, xv);
+                        gates(i2, ga);
 #pragma unroll
-                    for (int j = 0; j < kCh; ++j) {
-                        const float z = ga[SHARED ? 0 : j];
-                        if ((resets >> i2) & 1u) X[j] = 0.f;
-                        X[j] = SIG ? fmaf(z, xv[j] - X[j], X[j]) : fmaf(z, X[j], xv[j]);
-                        A[j] = SIG ? fmaf(-z, A[j], A[j]) : z * A[j];
+                        for (int j = 0; j < kCh; ++j) {
+                            const float z = ga[SHARED ? 0 : j];
+                            if (!plain && ((resets >> i2) & 1u)) X[j] = 0.f;
+                            X[j] = SIG ? fmaf(z, xv[j] - X[j], X[j]) : fmaf(z, X[j], xv[j]);
+                            A[j] = SIG ? fmaf(-z, A[j], A[j]) : z * A[j];
+                        }
                     }
-                }
+            };
+            if (nt == kTok && resets == 0) walk(std::true_type{});
+            else walk(std::false_type{});
             float4* m4 = reinterpret_cast<float4*>(maps(s) + run * CB + c);
 #pragma unroll
             for (int j = 0; j < kCh; ++j) A[j] = resets ? cut() : A[j] + 0.f;
@@ -385,28 +389,31 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
             const float4 lo = m4[0], hi = m4[1];
             h[0] = lo.x; h[1] = lo.z; h[2] = hi.x; h[3] = hi.z;
             const long long off = b * p.so[0] + hd * p.so[1] + t0 * p.so[2] + c;
+            auto walk = [&](auto plain, auto* o) {
 #pragma unroll
-            for (int i2 = 0; i2 < kTok; ++i2)
-                if (i2 < nt) {
-                    float xv[kCh], ga[NG];
-                    four(xs + i2 * p.d, xv);
-                    gates(i2, ga);
+                for (int i2 = 0; i2 < kTok; ++i2)
+                    if (plain || i2 < nt) {
+                        float xv[kCh], ga[NG];
+                        four(xs + i2 * p.d, xv);
+                        gates(i2, ga);
 #pragma unroll
-                    for (int j = 0; j < kCh; ++j) {
-                        const float z = ga[SHARED ? 0 : j];
-                        if ((resets >> i2) & 1u) h[j] = 0.f;
-                        h[j] = SIG ? fmaf(z, xv[j] - h[j], h[j]) : fmaf(z, h[j], xv[j]);
-                    }
-                    if (p.out_bf16) {
-                        Lane<bf16, kCh, true> ov;
+                        for (int j = 0; j < kCh; ++j) {
+                            const float z = ga[SHARED ? 0 : j];
+                            if (!plain && ((resets >> i2) & 1u)) h[j] = 0.f;
+                            h[j] = SIG ? fmaf(z, xv[j] - h[j], h[j]) : fmaf(z, h[j], xv[j]);
+                        }
+                        Lane<std::remove_pointer_t<decltype(o)>, kCh, true> ov;
                         ov.set(h);
-                        ov.store(static_cast<bf16*>(p.o) + off + i2 * p.so[2], nc);
-                    } else {
-                        Lane<float, kCh, true> ov;
-                        ov.set(h);
-                        ov.store(static_cast<float*>(p.o) + off + i2 * p.so[2], nc);
+                        ov.store(o + off + i2 * p.so[2], nc);
                     }
-                }
+            };
+            if (nt == kTok && resets == 0) {
+                if (p.out_bf16) walk(std::true_type{}, static_cast<bf16*>(p.o));
+                else walk(std::true_type{}, static_cast<float*>(p.o));
+            } else if (nt > 0) {
+                if (p.out_bf16) walk(std::false_type{}, static_cast<bf16*>(p.o));
+                else walk(std::false_type{}, static_cast<float*>(p.o));
+            }
             __syncwarp();
             if ((tid & 31) == 0) mbar_arrive(empty(s));
             if (p.state_out && nt > 0 && t0 + nt == p.T)

@@ -41,10 +41,17 @@ struct GateParams {
     int* status;
 };
 
-// z = 1 - a of the sigmoid gate
+// z = 1 - a = 1 / (1 + e^g) of the sigmoid gate: 1 where e^g is zero, 0 where it is
+// inf, NaN for NaN.  The power of two and the reciprocal are the approximate
+// instructions (2 ulp and 1 ulp) without their handling of subnormal numbers,
+// which the sum with 1 swallows; a z below 2^-126 becomes 0.
 __device__ __forceinline__ float keep_out(float g) {
-    const float e = __expf(-g);
-    return isinf(e) ? 1.f : __fdividef(e, 1.f + e);
+    constexpr float kLog2e = 1.4426950408889634f;
+    const float t = g * kLog2e;
+    float e, z;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(z) : "f"(1.f + e));
+    return z;
 }
 
 // ---- maps h -> A h + X -------------------------------------------------------
