@@ -65,7 +65,9 @@ gated_scan_kernel(const GateParams p) {
             }
             if (p.words) {
                 publish_tile(p, lb, row, n, ch, m);
-                h = enter_tile(p, lb, row, n, ch, m, h);
+                publish_group(p, lb, row, n, ch, m);
+                h = enter_tile(p, lb, row, n, ch, h);
+                publish_state(p, lb, row, n, ch, pass(m, h));
             }
             entering[ch] = h;
             if (p.carry && ch < p.d) p.carry[((long long)row * p.tiles + n) * p.d + ch] = h;
@@ -145,11 +147,14 @@ gated_scan_kernel(const GateParams p) {
 // mapped and written.  Warps have one role each and meet on mbarriers:
 //   loader   takes tickets and loads tiles of x (and gates) by bulk tensor copies;
 //   mappers  form the maps of the tile's runs, compose and publish the tile's map;
-//   joiners  (kJoin groups, every kJoin-th tile each) find the state that enters
+//   joiners  (kJoin sets, every kJoin-th tile each) find the state that enters
 //            the tile and from it the state that enters each run;
+//   groupers publish the maps of the groups that the block's tiles end: warps of
+//            their own, so that no group's map waits behind a joiner's waits;
 //   writers  walk the runs again and write the outputs.
 // Every wait is bounded in time, as in the other kernels of this library.
-constexpr int kJoin = 3;
+constexpr int kJoin = 2;
+constexpr int kAhead = 1;
 
 template <typename T, bool SHARED, int LANES>
 struct PipeLayout {
@@ -159,7 +164,7 @@ struct PipeLayout {
     static constexpr uint32_t kStage = kTileBytes * (SHARED ? 1 : 2) + kMaps;
     static constexpr int kStages = 225 * 1024 / kStage > 8 ? 8 : 225 * 1024 / kStage;
     static constexpr uint32_t kBytes = kStage * kStages + 128;  // and alignment to 128 bytes
-    static constexpr int kThreads = 32 + kData + kJoin * CB + kData;
+    static constexpr int kThreads = 32 + kData + kJoin * CB + CB + kData;
 };
 
 __device__ __forceinline__ void mbar_arrive(uint32_t a) {
@@ -170,6 +175,12 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
         "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
         ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(mbar)
         : "memory");
+}
+
+__device__ __forceinline__ void tma_prefetch_l2_4d(const CUtensorMap* map, int x, int y, int z, int w) {
+    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global [%0, {%1, %2, %3, %4}];"
+                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w)
+                 : "memory");
 }
 
 // four channels of one token in shared memory, as fp32
@@ -190,7 +201,7 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
     constexpr int CB = LY::CB, RUNS = LY::RUNS, TILE = LY::TILE, S = LY::kStages;
     constexpr unsigned kEnd = 0xffffffffu;
     extern __shared__ __align__(128) unsigned char raw[];
-    __shared__ __align__(8) unsigned long long bars[5 * S];
+    __shared__ __align__(8) unsigned long long bars[6 * S];
     static_assert(S >= kJoin, "the ends of the tickets take a stage for each group of joiners");
     __shared__ unsigned tile_of_stage[S], reset_bits[S][RUNS];
     __shared__ float2 total[S][CB];
@@ -201,6 +212,7 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
     auto mapped = [&](int s) { return smem_u32(&bars[S + s]); };      // its runs' maps and its own are there
     auto joined = [&](int s) { return smem_u32(&bars[2 * S + s]); };  // the states that enter its runs are there
     auto empty = [&](int s) { return smem_u32(&bars[3 * S + s]); };   // its outputs are written
+    auto known = [&](int s) { return smem_u32(&bars[5 * S + s]); };   // the stage's next tile is known
     auto runs = [&](int s) { return smem_u32(&bars[4 * S + s]); };    // every mapper's runs are mapped
     auto sx = [&](int s) { return reinterpret_cast<T*>(base + (size_t)s * LY::kStage); };
     auto sg = [&](int s) { return reinterpret_cast<T*>(base + (size_t)s * LY::kStage + LY::kTileBytes); };
@@ -213,8 +225,9 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
             mbar_init(full(s), 1);
             mbar_init(mapped(s), CB / 32);
             mbar_init(joined(s), CB / 32);
-            mbar_init(empty(s), kData / 32);
+            mbar_init(empty(s), kData / 32 + CB / 32);
             mbar_init(runs(s), kData / 32);
+            mbar_init(known(s), 1);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -247,24 +260,41 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
         if (tid != 0) return;
         Tickets tickets{reinterpret_cast<unsigned*>(p.words), nullptr};
         LoadLedger<S> loads(full(0));
-        unsigned k = p.words ? tickets.take(0) : blockIdx.x;
+        // tickets taken ahead, their tiles on the way to L2
+        unsigned ahead[kAhead + 1];
+        auto take = [&](unsigned last, bool first) -> unsigned {
+            const unsigned k = first && !p.words ? blockIdx.x : tickets.take(last);
+            if (kAhead > 0 && k < p.total) {
+                place(k, n, row, b, hd);
+                tma_prefetch_l2_4d(&mx, 0, n * TILE, hd, b);
+                if (!SHARED) tma_prefetch_l2_4d(&mg, 0, n * TILE, hd, b);
+            }
+            return k;
+        };
+#pragma unroll
+        for (int i = 0; i <= kAhead; ++i) ahead[i] = take(i > 0 ? ahead[i > 0 ? i - 1 : 0] : 0u, i == 0);
         int ends = 0;
         for (unsigned i = 0; ends < kJoin; ++i) {
             const int s = (int)(i % S);
+            const unsigned k = ahead[0];
             if (!wait(empty(s), ((i / S) & 1u) ^ 1u)) break;
             if (k >= p.total) {  // one end to each group of joiners
                 tile_of_stage[s] = kEnd;
+                mbar_arrive(known(s));
                 mbar_arrive(full(s));
                 ++ends;
                 continue;
             }
             tile_of_stage[s] = k;
+            mbar_arrive(known(s));
             place(k, n, row, b, hd);
             loads.note(s);
             mbar_expect_tx(full(s), (uint32_t)(TILE * p.d * sizeof(T)) * (SHARED ? 1u : 2u));
             tma_load_4d(smem_u32(sx(s)), &mx, 0, n * TILE, hd, b, full(s));
             if (!SHARED) tma_load_4d(smem_u32(sg(s)), &mg, 0, n * TILE, hd, b, full(s));
-            k = tickets.take(k);
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) ahead[j] = ahead[j + 1];
+            ahead[kAhead] = take(ahead[kAhead], false);
         }
         if (abort_flag && !loads.settle()) atomicExch(p.status, (int)kDevWaitTimeout);
         return;
@@ -274,13 +304,15 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
         const int ch = tid - 32 - kData - j * CB;
         for (unsigned i = (unsigned)j;; i += kJoin) {
             const int s = (int)(i % S);
-            if (!wait(mapped(s), (i / S) & 1u)) return;
+            if (!wait(known(s), (i / S) & 1u)) return;
             const unsigned k = tile_of_stage[s];
             if (k != kEnd) {
                 place(k, n, row, b, hd);
                 float h = p.state_in && ch < p.d ? p.state_in[(long long)row * p.d + ch] : 0.f;
-                if (p.words) h = enter_tile(p, lb, row, n, ch, total[s][ch], h);
+                if (p.words) h = enter_tile(p, lb, row, n, ch, h);  // while the tile is loaded and mapped
                 if (p.carry && ch < p.d) p.carry[((long long)row * p.tiles + n) * p.d + ch] = h;
+                if (!wait(mapped(s), (i / S) & 1u)) return;
+                if (p.words) publish_state(p, lb, row, n, ch, pass(total[s][ch], h));
                 float2* m = maps(s) + ch;
 #pragma unroll
                 for (int r = 0; r < RUNS; ++r) {
@@ -292,6 +324,20 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
             __syncwarp();
             if ((tid & 31) == 0) mbar_arrive(joined(s));
             if (k == kEnd) return;
+        }
+    }
+    if (warp >= 1 + kData / 32 && warp < 1 + kData / 32 + (kJoin + 1) * (CB / 32)) {  // groupers
+        const int ch = tid - 32 - kData - kJoin * CB;
+        for (unsigned i = 0;; ++i) {
+            const int s = (int)(i % S);
+            if (!wait(mapped(s), (i / S) & 1u)) return;
+            const unsigned k = tile_of_stage[s];
+            if (k == kEnd) return;
+            const float2 m = total[s][ch];
+            __syncwarp();
+            if ((tid & 31) == 0) mbar_arrive(empty(s));
+            place(k, n, row, b, hd);
+            if (p.words) publish_group(p, lb, row, n, ch, m);
         }
     }
     const bool mapper = warp < 1 + kData / 32;

@@ -16,7 +16,7 @@ constexpr int kTok = 8;         // tokens of a run
 constexpr int kCh = 4;          // channels of a thread
 constexpr int kData = 256;      // threads that share a tile: one to a run and four channels
 constexpr int kGroup = 8;       // tiles to a group
-constexpr int kSuper = 16;      // groups to a super-group
+constexpr int kSuper = 4;       // groups to a super-group
 constexpr unsigned long long kGateWaitNs = 2000000000ull;  // bounded waits: 2 s
 
 // Lanes that share a token: they cover 4 channels each, d <= 4 lanes.
@@ -107,15 +107,19 @@ __device__ __forceinline__ u64 gate_timer() {
     return t;
 }
 
-// Reads w[i] = p[i * step] for i < n until every one is there.  Gives up after
-// 2 s: then this call's results are void, the status word says so, and every
-// later wait of the call ends at once.
+// Reads w[i] = src[i * step] for i < n.
 template <int N>
-__device__ __forceinline__ void read_words(const GateParams& p, const u64* src, size_t step, int n, u64 (&w)[N]) {
+__device__ __forceinline__ void ask_words(const u64* src, size_t step, int n, u64 (&w)[N]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) w[i] = i < n ? ld_word(src + i * step) : 0;
+}
+// Reads those that were not there again until every one is.  Gives up after 2 s:
+// then this call's results are void, the status word says so, and every later
+// wait of the call ends at once.
+template <int N>
+__device__ __forceinline__ void wait_words(const GateParams& p, const u64* src, size_t step, u64 (&w)[N]) {
     u64 t0 = 0;
-    while (true) {
+    for (unsigned tries = 1;; ++tries) {
         bool all = true;
 #pragma unroll
         for (int i = 0; i < N; ++i)
@@ -124,13 +128,15 @@ __device__ __forceinline__ void read_words(const GateParams& p, const u64* src, 
                 all = all && w[i] != kNothing;
             }
         if (all) return;
-        const u64 now = gate_timer();
-        if (t0 == 0) t0 = now;
-        unsigned* const run_out = reinterpret_cast<unsigned*>(p.words) + 1;
-        if (now - t0 > kGateWaitNs || *(volatile unsigned*)run_out != ~0u) {
-            atomicExch(run_out, 0u);
-            atomicExch(p.status, (int)kDevWaitTimeout);
-            return;
+        if (tries % 64 == 0) {
+            const u64 now = gate_timer();
+            if (t0 == 0) t0 = now;
+            unsigned* const run_out = reinterpret_cast<unsigned*>(p.words) + 1;
+            if (now - t0 > kGateWaitNs || *(volatile unsigned*)run_out != ~0u) {
+                atomicExch(run_out, 0u);
+                atomicExch(p.status, (int)kDevWaitTimeout);
+                return;
+            }
         }
     }
 }
@@ -140,45 +146,50 @@ __device__ __forceinline__ void publish_tile(const GateParams& p, const Lookback
     if (n + 1 < lb.tiles) st_pair(p.words + lb.tile_map(row, n) + ch, m);
 }
 
-// The state that enters the tile, for one channel, after publish_tile of its map
-// `m`; also publishes the map of the group, or the state after the super-group,
-// that the tile ends.  `start`: the state that enters the sequence.
-__device__ __forceinline__ float enter_tile(const GateParams& p, const Lookback& lb, int row, int n, int ch, float2 m,
+// Publishes one channel of the map of the group that tile n ends, if it ends one.
+__device__ __forceinline__ void publish_group(const GateParams& p, const Lookback& lb, int row, int n, int ch, float2 m) {
+    if (kSuper == 1 || n % kGroup != kGroup - 1 || n + 1 == lb.tiles) return;
+    u64 w[kGroup - 1];
+    const u64* const tiles = p.words + lb.tile_map(row, n - (kGroup - 1)) + ch;
+    ask_words(tiles, lb.cb, kGroup - 1, w);
+    wait_words(p, tiles, lb.cb, w);
+    float2 all = as_pair(w[0]);
+#pragma unroll
+    for (int i = 1; i < kGroup - 1; ++i) all = then(all, as_pair(w[i]));
+    st_pair(p.words + lb.group_map(row, n / kGroup) + ch, then(all, m));
+}
+
+// The state that enters the tile, for one channel.  `start`: the state that enters
+// the sequence.
+__device__ __forceinline__ float enter_tile(const GateParams& p, const Lookback& lb, int row, int n, int ch,
                                             float start) {
     const int g = n / kGroup, s = g / kSuper;
     const int nt = n % kGroup, ng = g % kSuper;  // tiles before this one in its group, groups before it in the super-group
-    const bool last = n + 1 == lb.tiles, ends_group = nt == kGroup - 1, ends_super = ends_group && ng == kSuper - 1;
-    // the tiles of the group first: the group's map waits for nothing else
-    u64 w[kGroup - 1];
-    read_words(p, p.words + lb.tile_map(row, n - nt) + ch, lb.cb, nt, w);
-    if (ends_group && !last) {
-        float2 all = as_pair(w[0]);
+    u64 w[kGroup - 1], v[kSuper > 1 ? kSuper - 1 : 1], u[1];
+    const u64* const state = p.words + lb.super_state(row, s) + ch;
+    const u64* const groups = p.words + lb.group_map(row, g - ng) + ch;
+    const u64* const tiles = p.words + lb.tile_map(row, n - nt) + ch;
+    ask_words(state, 0, s > 0 ? 1 : 0, u);
+    ask_words(groups, lb.cb, ng, v);
+    ask_words(tiles, lb.cb, nt, w);
+    wait_words(p, state, 0, u);
+    wait_words(p, groups, lb.cb, v);
+    wait_words(p, tiles, lb.cb, w);
+    float h = s > 0 ? as_pair(u[0]).x : start;
 #pragma unroll
-        for (int i = 1; i < kGroup - 1; ++i) all = then(all, as_pair(w[i]));
-        st_pair(p.words + lb.group_map(row, g) + ch, then(all, m));
-    }
-    float h = start;
-    if (s > 0) {
-        u64 v[1];
-        read_words(p, p.words + lb.super_state(row, s) + ch, 0, 1, v);
-        h = as_pair(v[0]).x;
-    }
-#pragma unroll
-    for (int half = 0; half < kSuper; half += kSuper / 2) {
-        u64 v[kSuper / 2];
-        const int here = min(ng - half, kSuper / 2);
-        if (here > 0) {
-            read_words(p, p.words + lb.group_map(row, g - ng + half) + ch, lb.cb, here, v);
-#pragma unroll
-            for (int i = 0; i < kSuper / 2; ++i)
-                if (i < here) h = pass(as_pair(v[i]), h);
-        }
-    }
+    for (int i = 0; i < kSuper - 1; ++i)
+        if (i < ng) h = pass(as_pair(v[i]), h);
 #pragma unroll
     for (int i = 0; i < kGroup - 1; ++i)
         if (i < nt) h = pass(as_pair(w[i]), h);
-    if (ends_super && !last) st_pair(p.words + lb.super_state(row, s + 1) + ch, make_float2(pass(m, h), 0.f));
     return h;
+}
+
+// Publishes the state `h` after tile n where the tile ends a super-group.
+__device__ __forceinline__ void publish_state(const GateParams& p, const Lookback& lb, int row, int n, int ch, float h) {
+    constexpr int kLong = kGroup * kSuper;
+    if (n % kLong == kLong - 1 && n + 1 < lb.tiles)
+        st_pair(p.words + lb.super_state(row, n / kLong + 1) + ch, make_float2(h, 0.f));
 }
 
 // The tiles of a block, by ticket where tiles wait for one another.  The

@@ -41,14 +41,20 @@ gated_scan_bwd_kernel(const GateParams p) {
                 back[r][ch] = m;
                 m = then(m, f);
             }
-            if (p.words) publish_tile(p, lb, row, n, ch, m);
+            if (p.words) {
+                publish_tile(p, lb, row, n, ch, m);
+                publish_group(p, lb, row, n, ch, m);
+            }
 #pragma unroll 8
             for (int r = 0; r < RUNS; ++r) {
                 const float2 f = fwd[r][ch];
                 fwd[r][ch].x = h;
                 h = pass(f, h);
             }
-            if (p.words) mu = enter_tile(p, lb, row, n, ch, m, mu);
+            if (p.words) {
+                mu = enter_tile(p, lb, row, n, ch, mu);
+                publish_state(p, lb, row, n, ch, pass(m, mu));
+            }
             entering[ch] = mu;
             __syncthreads();
             k = slot;

@@ -532,7 +532,13 @@ def hla2_decay_step(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: to
 # ------------------------------------------------ around the attention layer ----
 # The gated linear recurrence, the root-mean-square norm and the rotary
 # positions.  Their tensors may be strided (the last dimension contiguous).
+# A decoding step makes these calls on a few kilobytes, where the call itself is
+# the cost: each first asks in one expression whether the arguments are the
+# ordinary ones, and only otherwise goes through the checks one by one.
 _GATE_FORMS = {"sigmoid": 0, "decay": 1}
+_CODES = {torch.float32: HLA2_DTYPE_F32, torch.bfloat16: HLA2_DTYPE_BF16}
+_F32 = torch.float32
+_LL3, _LL4, _LL9, _LL14, _LL15 = (ctypes.c_longlong * n for n in (3, 4, 9, 14, 15))
 
 
 class _NoGuard:
@@ -548,17 +554,21 @@ _NO_GUARD = _NoGuard()
 
 def _guard(dev: torch.device, stream):
     """Makes ``dev`` current, and ``stream`` (when given) too, so that what the
-    call allocates belongs to the stream it is used on.  Free of cost in the
-    common case."""
+    call allocates belongs to the stream it is used on."""
     if stream is None:
-        return _NO_GUARD if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+        return _NO_GUARD if torch._C._cuda_getDevice() == dev.index else torch.cuda.device(dev)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=dev)
     return torch.cuda.stream(stream)
 
 
+def _raw(dev: torch.device, stream) -> int:
+    """The stream's handle; the current stream of ``dev`` by default."""
+    return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else _stream(stream)
+
+
 def _operand(t, name: str, device=None, dtype=None, shape=None, dense=False) -> None:
-    """Checks of one operand of the calls below, before anything is allocated or launched."""
+    """Checks of one operand, before anything is allocated or launched."""
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a tensor")
     if dtype is not None and t.dtype != dtype:
@@ -582,13 +592,22 @@ def _no_overlap(t: torch.Tensor, name: str) -> None:
         raise ValueError(f"{name} must not be an expanded tensor")
 
 
+def _output(t, name: str, dev, dtype, shape) -> None:
+    _operand(t, name, dev, dtype, shape)
+    if t.dim():
+        _last_dense(t, name)
+    _no_overlap(t, name)
+
+
+def _out_code(dtype) -> int:
+    code = _CODES.get(dtype)
+    if code is None:
+        raise ValueError(f"unsupported output dtype {dtype}")
+    return code
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
-
-
-def _out_like(t: torch.Tensor, dtype: torch.dtype) -> torch.Tensor:
-    """A new tensor of t's shape: t's memory order where t is dense in some order, else row-major."""
-    return torch.empty_like(t, dtype=dtype)
 
 
 def hla2_gated_scan_workspace(B: int, H: int, T: int, d: int) -> int:
@@ -624,21 +643,21 @@ def _gated_inputs(X, G, form, reset):
     return B, H, T, d, code, _GATE_FORMS[form], shared
 
 
-def _gated_work(workspace, B, H, T, d, dev):
+def _gated_optional(dev, B, H, T, d, carry, workspace, **states):
+    for name, t in states.items():
+        if t is not None:
+            _operand(t, name, dev, _F32, (B, H, d), dense=True)
+    if carry is not None:
+        _operand(carry, "carry", dev, _F32, (B, H, hla2_gated_scan_carry_len(T, d)), dense=True)
+    if workspace is not None:
+        _operand(workspace, "workspace", dev, dense=True)
+
+
+def _gated_work(L, workspace, B, H, T, d, dev):
     if workspace is not None:
         return workspace, workspace.numel() * workspace.element_size()
-    need = hla2_gated_scan_workspace(B, H, T, d)
-    if need:
-        workspace = torch.empty(need, device=dev, dtype=torch.uint8)
-    return workspace, need
-
-
-def _strides(*tensors):
-    """The first three strides of each tensor (zeros for None), as the C entries take them."""
-    flat = []
-    for t in tensors:
-        flat += (0, 0, 0) if t is None else t.stride()[:3]
-    return (ctypes.c_longlong * len(flat))(*flat)
+    need = L.hla2_gated_scan_workspace(B, H, T, d)
+    return (torch.empty(need, device=dev, dtype=torch.uint8) if need else None), need
 
 
 def hla2_gated_scan(X: torch.Tensor, G: torch.Tensor, O: torch.Tensor | None = None, form: str = "sigmoid",
@@ -648,7 +667,8 @@ def hla2_gated_scan(X: torch.Tensor, G: torch.Tensor, O: torch.Tensor | None = N
                     stream=None) -> torch.Tensor:
     """Gated linear recurrence h_t = a_t h_{t-1} + u_t along the tokens of each
     head: X [B,H,T,d], G [B,H,T,d] or [B,H,T] (one gate for a head's channels),
-    fp32 or bf16 -> O [B,H,T,d] of ``out_dtype`` (or O's own dtype).
+    fp32 or bf16 -> O [B,H,T,d] of ``out_dtype`` (or O's own dtype), in X's
+    memory order when it is not given.
 
     ``form`` "sigmoid": a = sigmoid(G), u = (1 - a) X;  "decay": a = G, u = X.
     ``reset`` [B,T] bool: a document begins there (h_{t-1} counts as zero).
@@ -658,30 +678,23 @@ def hla2_gated_scan(X: torch.Tensor, G: torch.Tensor, O: torch.Tensor | None = N
     B, H, T, d, code, fcode, shared = _gated_inputs(X, G, form, reset)
     dev = X.device
     if O is not None:
-        _operand(O, "O", dev, shape=X.shape)
+        _output(O, "O", dev, None, X.shape)
         out_dtype = O.dtype
-        _last_dense(O, "O")
-        _no_overlap(O, "O")
-    if out_dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"unsupported output dtype {out_dtype}")
-    if state_in is not None:
-        _operand(state_in, "state_in", dev, torch.float32, (B, H, d), dense=True)
-    if state_out is not None:
-        _operand(state_out, "state_out", dev, torch.float32, (B, H, d), dense=True)
-    if carry is not None:
-        _operand(carry, "carry", dev, torch.float32, (B, H, hla2_gated_scan_carry_len(T, d)), dense=True)
-    if workspace is not None:
-        _operand(workspace, "workspace", dev, dense=True)
+    ocode = _out_code(out_dtype)
+    if not (state_in is state_out is carry is workspace is None):
+        _gated_optional(dev, B, H, T, d, carry, workspace, state_in=state_in, state_out=state_out)
     _cuda_device(X, "X")
+    L = _lib or lib()
     with _guard(dev, stream):
         if O is None:
-            O = _out_like(X, out_dtype)
-        workspace, nws = _gated_work(workspace, B, H, T, d, dev)
-        rc = lib().hla2_gated_scan(X.data_ptr(), G.data_ptr(), _ptr(reset), _ptr(state_in), O.data_ptr(),
-                                   _ptr(state_out), _ptr(carry), B, H, T, d, _strides(X, G, O), fcode, int(shared),
-                                   code, 1 if out_dtype == torch.bfloat16 else 0, _ptr(workspace), nws,
-                                   _stream(stream))
-    _check(rc, "hla2_gated_scan")
+            O = torch.empty_like(X, dtype=out_dtype)
+        workspace, nws = _gated_work(L, workspace, B, H, T, d, dev)
+        rc = L.hla2_gated_scan(X.data_ptr(), G.data_ptr(), _ptr(reset), _ptr(state_in), O.data_ptr(),
+                               _ptr(state_out), _ptr(carry), B, H, T, d,
+                               _LL9(*X.stride()[:3], *G.stride()[:3], *O.stride()[:3]), fcode, shared, code, ocode,
+                               _ptr(workspace), nws, _raw(dev, stream))
+    if rc:
+        _check(rc, "hla2_gated_scan")
     return O
 
 
@@ -699,31 +712,53 @@ def hla2_gated_scan_backward(X: torch.Tensor, G: torch.Tensor, dO: torch.Tensor,
     _operand(dO, "dO", dev, shape=X.shape)
     ocode = _dtype_code(dO)
     _last_dense(dO, "dO")
-    _operand(carry, "carry", dev, torch.float32, (B, H, hla2_gated_scan_carry_len(T, d)), dense=True)
-    for t, name, like in ((dX, "dX", X), (dG, "dG", G)):
-        if t is not None:
-            _operand(t, name, dev, like.dtype, like.shape)
-            if t.dim() == 4:
-                _last_dense(t, name)
-            _no_overlap(t, name)
-    for t, name in ((dstate_out, "dstate_out"), (dstate_in, "dstate_in")):
-        if t is not None:
-            _operand(t, name, dev, torch.float32, (B, H, d), dense=True)
-    if workspace is not None:
-        _operand(workspace, "workspace", dev, dense=True)
+    _operand(carry, "carry", dev, _F32)
+    if dX is not None:
+        _output(dX, "dX", dev, X.dtype, X.shape)
+    if dG is not None:
+        _operand(dG, "dG", dev, G.dtype, G.shape)
+        if not shared:
+            _last_dense(dG, "dG")
+        _no_overlap(dG, "dG")
+    _gated_optional(dev, B, H, T, d, carry, workspace, dstate_out=dstate_out, dstate_in=dstate_in)
     _cuda_device(X, "X")
+    L = _lib or lib()
     with _guard(dev, stream):
         if dX is None:
-            dX = _out_like(X, X.dtype)
+            dX = torch.empty_like(X)
         if dG is None:
-            dG = _out_like(G, G.dtype)
-        workspace, nws = _gated_work(workspace, B, H, T, d, dev)
-        rc = lib().hla2_gated_scan_backward(X.data_ptr(), G.data_ptr(), _ptr(reset), carry.data_ptr(), dO.data_ptr(),
-                                            _ptr(dstate_out), dX.data_ptr(), dG.data_ptr(), _ptr(dstate_in), B, H, T,
-                                            d, _strides(X, G, dO, dX, dG), fcode, int(shared), code, ocode,
-                                            _ptr(workspace), nws, _stream(stream))
-    _check(rc, "hla2_gated_scan_backward")
+            dG = torch.empty_like(G)
+        workspace, nws = _gated_work(L, workspace, B, H, T, d, dev)
+        rc = L.hla2_gated_scan_backward(X.data_ptr(), G.data_ptr(), _ptr(reset), carry.data_ptr(), dO.data_ptr(),
+                                        _ptr(dstate_out), dX.data_ptr(), dG.data_ptr(), _ptr(dstate_in), B, H, T, d,
+                                        _LL15(*X.stride()[:3], *G.stride()[:3], *dO.stride()[:3], *dX.stride()[:3],
+                                              *dG.stride()[:3]), fcode, shared, code, ocode, _ptr(workspace), nws,
+                                        _raw(dev, stream))
+    if rc:
+        _check(rc, "hla2_gated_scan_backward")
     return dX, dG
+
+
+def _gated_step_checks(state, x, g, o, state_out):
+    _operand(x, "x")
+    if x.dim() != 2:
+        raise ValueError("hla2_gated_step: expected x [n,d]")
+    dev = x.device
+    _operand(g, "g", dev)
+    if g.shape != x.shape and g.shape != x.shape[:1]:
+        raise ValueError("hla2_gated_step: expected g [n,d] or [n]")
+    if g.dtype != x.dtype:
+        raise ValueError(f"x and g must share a dtype (got {x.dtype}, {g.dtype})")
+    _dtype_code(x)
+    _last_dense(x, "x")
+    if g.dim() == 2:
+        _last_dense(g, "g")
+    _operand(state, "state", dev, _F32, x.shape, dense=True)
+    if state_out is not None:
+        _operand(state_out, "state_out", dev, _F32, x.shape, dense=True)
+    if o is not None:
+        _output(o, "o", dev, None, x.shape)
+    _cuda_device(x, "x")
 
 
 def hla2_gated_step(state: torch.Tensor, x: torch.Tensor, g: torch.Tensor, o: torch.Tensor | None = None,
@@ -732,50 +767,36 @@ def hla2_gated_step(state: torch.Tensor, x: torch.Tensor, g: torch.Tensor, o: to
     """One token of the recurrence for n heads: state [n,d] fp32, x [n,d] and
     g [n,d] or [n] (fp32 or bf16) -> o [n,d].  The state is updated in place,
     or left and the new one written to ``state_out``."""
-    _operand(x, "x")
-    if x.dim() != 2:
-        raise ValueError("hla2_gated_step: expected x [n,d]")
-    n, d = x.shape
-    dev = x.device
-    _operand(g, "g", dev)
-    shared = g.dim() == 1
-    if g.shape != x.shape and g.shape != x.shape[:1]:
-        raise ValueError("hla2_gated_step: expected g [n,d] or [n]")
-    if g.dtype != x.dtype:
-        raise ValueError(f"x and g must share a dtype (got {x.dtype}, {g.dtype})")
-    code = _dtype_code(x)
-    if form not in _GATE_FORMS:
+    shape, dt, dev = x.shape, x.dtype, x.device
+    if not (x.is_cuda and x.is_contiguous() and len(shape) == 2 and dt in _CODES and o is None and
+            g.shape == shape and g.dtype is dt and g.device == dev and g.is_contiguous() and
+            state.shape == shape and state.dtype is _F32 and state.device == dev and state.is_contiguous() and
+            (state_out is None or (state_out.shape == shape and state_out.dtype is _F32 and
+                                   state_out.device == dev and state_out.is_contiguous()))):
+        _gated_step_checks(state, x, g, o, state_out)
+    fcode = _GATE_FORMS.get(form)
+    if fcode is None:
         raise ValueError(f"unknown gate form {form!r}: one of {sorted(_GATE_FORMS)}")
-    _last_dense(x, "x")
-    if not shared:
-        _last_dense(g, "g")
-    _operand(state, "state", dev, torch.float32, x.shape, dense=True)
-    if state_out is not None:
-        _operand(state_out, "state_out", dev, torch.float32, x.shape, dense=True)
-    if o is not None:
-        _operand(o, "o", dev, shape=x.shape)
-        _last_dense(o, "o")
-        _no_overlap(o, "o")
-        out_dtype = o.dtype
-    if out_dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"unsupported output dtype {out_dtype}")
-    _cuda_device(x, "x")
+    ocode = _out_code(out_dtype if o is None else o.dtype)
+    n, d = shape
+    L = _lib or lib()
     with _guard(dev, stream):
         if o is None:
-            o = torch.empty((n, d), device=dev, dtype=out_dtype)
-        ld = (ctypes.c_longlong * 3)(x.stride(0), g.stride(0), o.stride(0))
-        rc = lib().hla2_gated_step(state.data_ptr(), x.data_ptr(), g.data_ptr(), o.data_ptr(), _ptr(state_out), n, d,
-                                   ld, _GATE_FORMS[form], int(shared), code, 1 if out_dtype == torch.bfloat16 else 0,
-                                   _stream(stream))
-    _check(rc, "hla2_gated_step")
+            o = torch.empty(shape, device=dev, dtype=out_dtype)
+        rc = L.hla2_gated_step(state.data_ptr(), x.data_ptr(), g.data_ptr(), o.data_ptr(),
+                               None if state_out is None else state_out.data_ptr(), n, d,
+                               _LL3(x.stride(0), g.stride(0), o.stride(0)), fcode, g.dim() == 1, _CODES[dt], ocode,
+                               _raw(dev, stream))
+    if rc:
+        _check(rc, "hla2_gated_step")
     return o
 
 
-def _rows(t: torch.Tensor, name: str):
-    """(row stride) of a tensor whose leading dimensions run through its rows with one stride."""
-    C = t.shape[-1]
+def _rows(t: torch.Tensor, name: str) -> int:
+    """The row stride of a tensor whose leading dimensions run through its rows with one stride."""
     if t.is_contiguous():
-        return C
+        return t.shape[-1]
+    C = t.shape[-1]
     _last_dense(t, name)
     ld, expect = None, None
     for n, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
@@ -794,33 +815,46 @@ def _rows(t: torch.Tensor, name: str):
     return ld
 
 
-def _norm_inputs(X, weight, residual, eps):
-    """Checks shared by the norms; returns (rows, C, dtype code, weight dtype code)."""
+def _norm_checks(X, weight, residual, eps):
+    """The checks of the norms' inputs, one by one."""
     _operand(X, "X")
     if X.dim() < 1:
         raise ValueError("X must have at least one dimension")
-    code = _dtype_code(X)
-    C = X.shape[-1]
-    rows = X.numel() // C if C else 0
-    wcode = 0
+    _dtype_code(X)
     if weight is not None:
-        _operand(weight, "weight", X.device, shape=(C,), dense=True)
-        wcode = _dtype_code(weight)
+        _operand(weight, "weight", X.device, shape=X.shape[-1:], dense=True)
+        _dtype_code(weight)
     if residual is not None:
         _operand(residual, "residual", X.device, X.dtype, X.shape)
     if not eps >= 0:
         raise ValueError("eps must not be negative")
-    return rows, C, code, wcode
+    _rows(X, "X")
+    if residual is not None:
+        _rows(residual, "residual")
 
 
-def _norm_outputs(X, residual, S):
-    """The row strides of X, residual and S; S is wanted with a residual."""
-    ldx = _rows(X, "X")
-    ldr = _rows(residual, "residual") if residual is not None else 0
-    if S is not None:
-        _operand(S, "S", X.device, X.dtype, X.shape)
-        _rows(S, "S")
-    return ldx, ldr
+def _norm_inputs(X, weight, residual, eps):
+    """Returns (rows, C, dtype code, weight pointer, weight dtype code, row strides of X and the residual)."""
+    shape, dt, dev = X.shape, X.dtype, X.device
+    if not (len(shape) and dt in _CODES and eps >= 0 and X.is_contiguous() and
+            (weight is None or (weight.dtype in _CODES and weight.shape == shape[-1:] and weight.device == dev and
+                                weight.is_contiguous())) and
+            (residual is None or (residual.dtype is dt and residual.shape == shape and residual.device == dev and
+                                  residual.is_contiguous()))):
+        _norm_checks(X, weight, residual, eps)
+    C = shape[-1]
+    return (X.numel() // C if C else 0, C, _CODES[dt], None if weight is None else weight.data_ptr(),
+            0 if weight is None else _CODES[weight.dtype], _rows(X, "X"),
+            0 if residual is None else _rows(residual, "residual"))
+
+
+def _norm_stream(X, residual, S):
+    """The residual stream's new tensor (wanted with a residual) and its row stride."""
+    if S is None:
+        if residual is None:
+            return None, 0
+        return torch.empty(X.shape, device=X.device, dtype=X.dtype), X.shape[-1]
+    return S, _rows(S, "S")
 
 
 def hla2_rmsnorm(X: torch.Tensor, weight: torch.Tensor | None = None, residual: torch.Tensor | None = None,
@@ -830,27 +864,27 @@ def hla2_rmsnorm(X: torch.Tensor, weight: torch.Tensor | None = None, residual: 
     Y = t / sqrt(mean(t^2) + eps) * weight.  X [..., C] fp32 or bf16, weight [C].
     Returns (Y, S): Y of ``out_dtype`` (X's by default), S = t in X's dtype,
     the new residual stream (None without a residual unless S is given)."""
-    rows, C, code, wcode = _norm_inputs(X, weight, residual, eps)
+    rows, C, code, wptr, wcode, ldx, ldr = _norm_inputs(X, weight, residual, eps)
     dev = X.device
-    ldx, ldr = _norm_outputs(X, residual, S)
     if Y is not None:
-        _operand(Y, "Y", dev, shape=X.shape)
-        out_dtype = Y.dtype
+        _output(Y, "Y", dev, None, X.shape)
         _rows(Y, "Y")
+        out_dtype = Y.dtype
     elif out_dtype is None:
         out_dtype = X.dtype
-    if out_dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"unsupported output dtype {out_dtype}")
+    ocode = _out_code(out_dtype)
+    if S is not None:
+        _output(S, "S", dev, X.dtype, X.shape)
     _cuda_device(X, "X")
+    L = _lib or lib()
     with _guard(dev, stream):
         if Y is None:
             Y = torch.empty(X.shape, device=dev, dtype=out_dtype)
-        if S is None and residual is not None:
-            S = torch.empty(X.shape, device=dev, dtype=X.dtype)
-        rc = lib().hla2_rmsnorm(X.data_ptr(), _ptr(residual), _ptr(weight), _ptr(S), Y.data_ptr(), rows, C, ldx, ldr,
-                                _rows(S, "S") if S is not None else 0, _rows(Y, "Y"), eps, code, wcode,
-                                1 if out_dtype == torch.bfloat16 else 0, _stream(stream))
-    _check(rc, "hla2_rmsnorm")
+        S, lds = _norm_stream(X, residual, S)
+        rc = L.hla2_rmsnorm(X.data_ptr(), _ptr(residual), wptr, _ptr(S), Y.data_ptr(), rows, C, ldx, ldr, lds,
+                            _rows(Y, "Y"), eps, code, wcode, ocode, _raw(dev, stream))
+    if rc:
+        _check(rc, "hla2_rmsnorm")
     return Y, S
 
 
@@ -860,26 +894,27 @@ def hla2_rmsnorm_q8(X: torch.Tensor, weight: torch.Tensor | None = None, residua
     """The norm of hla2_rmsnorm with an 8-bit output: returns (Q, scale, S), Q
     [..., C] float8_e4m3fn and scale [...] fp32 with Y = Q * scale (scale =
     max|Y| / 448 of the row, 1 for a row of zeros)."""
-    rows, C, code, wcode = _norm_inputs(X, weight, residual, eps)
+    rows, C, code, wptr, wcode, ldx, ldr = _norm_inputs(X, weight, residual, eps)
     dev = X.device
-    ldx, ldr = _norm_outputs(X, residual, S)
     if Q is not None:
-        _operand(Q, "Q", dev, torch.float8_e4m3fn, X.shape)
+        _output(Q, "Q", dev, torch.float8_e4m3fn, X.shape)
         _rows(Q, "Q")
     if scale is not None:
-        _operand(scale, "scale", dev, torch.float32, X.shape[:-1], dense=True)
+        _operand(scale, "scale", dev, _F32, X.shape[:-1], dense=True)
+    if S is not None:
+        _output(S, "S", dev, X.dtype, X.shape)
     _cuda_device(X, "X")
+    L = _lib or lib()
     with _guard(dev, stream):
         if Q is None:
             Q = torch.empty(X.shape, device=dev, dtype=torch.float8_e4m3fn)
         if scale is None:
-            scale = torch.empty(X.shape[:-1], device=dev, dtype=torch.float32)
-        if S is None and residual is not None:
-            S = torch.empty(X.shape, device=dev, dtype=X.dtype)
-        rc = lib().hla2_rmsnorm_q8(X.data_ptr(), _ptr(residual), _ptr(weight), _ptr(S), Q.data_ptr(), scale.data_ptr(),
-                                   rows, C, ldx, ldr, _rows(S, "S") if S is not None else 0, _rows(Q, "Q"), eps, code,
-                                   wcode, _stream(stream))
-    _check(rc, "hla2_rmsnorm_q8")
+            scale = torch.empty(X.shape[:-1], device=dev, dtype=_F32)
+        S, lds = _norm_stream(X, residual, S)
+        rc = L.hla2_rmsnorm_q8(X.data_ptr(), _ptr(residual), wptr, _ptr(S), Q.data_ptr(), scale.data_ptr(), rows, C,
+                               ldx, ldr, lds, _rows(Q, "Q"), eps, code, wcode, _raw(dev, stream))
+    if rc:
+        _check(rc, "hla2_rmsnorm_q8")
     return Q, scale, S
 
 
@@ -890,33 +925,64 @@ def hla2_rmsnorm_backward(S: torch.Tensor, dY: torch.Tensor, weight: torch.Tenso
     residual): dX (of X and of the residual; ``dS``, the gradient that reaches
     the residual stream, is added) in S's dtype, and dW [C] fp32 (None without
     a weight)."""
-    rows, C, code, wcode = _norm_inputs(S, weight, dS, eps)
+    rows, C, code, wptr, wcode, lds, ldd = _norm_inputs(S, weight, dS, eps)
     dev = S.device
     _operand(dY, "dY", dev, shape=S.shape)
     ycode = _dtype_code(dY)
-    lds, ldy = _rows(S, "S"), _rows(dY, "dY")
-    ldd = _rows(dS, "dS") if dS is not None else 0
+    ldy = _rows(dY, "dY")
     if dX is not None:
-        _operand(dX, "dX", dev, S.dtype, S.shape)
+        _output(dX, "dX", dev, S.dtype, S.shape)
         _rows(dX, "dX")
     if workspace is not None:
         _operand(workspace, "workspace", dev, dense=True)
     _cuda_device(S, "S")
+    L = _lib or lib()
     with _guard(dev, stream):
         if dX is None:
             dX = torch.empty(S.shape, device=dev, dtype=S.dtype)
         dW, nws = None, 0
         if weight is not None:
-            dW = torch.empty((C,), device=dev, dtype=torch.float32)
+            dW = torch.empty((C,), device=dev, dtype=_F32)
             if workspace is None:
-                workspace = torch.empty(int(lib().hla2_rmsnorm_backward_workspace(rows, C)), device=dev,
-                                        dtype=torch.uint8)
+                workspace = torch.empty(L.hla2_rmsnorm_backward_workspace(rows, C), device=dev, dtype=torch.uint8)
             nws = workspace.numel() * workspace.element_size()
-        ld = (ctypes.c_longlong * 4)(lds, ldy, ldd, _rows(dX, "dX"))
-        rc = lib().hla2_rmsnorm_backward(S.data_ptr(), dY.data_ptr(), _ptr(weight), _ptr(dS), dX.data_ptr(), _ptr(dW),
-                                         rows, C, ld, eps, code, wcode, ycode, _ptr(workspace), nws, _stream(stream))
-    _check(rc, "hla2_rmsnorm_backward")
+        rc = L.hla2_rmsnorm_backward(S.data_ptr(), dY.data_ptr(), wptr, _ptr(dS), dX.data_ptr(), _ptr(dW), rows, C,
+                                     _LL4(lds, ldy, ldd, _rows(dX, "dX")), eps, code, wcode, ycode, _ptr(workspace),
+                                     nws, _raw(dev, stream))
+    if rc:
+        _check(rc, "hla2_rmsnorm_backward")
     return dX, dW
+
+
+def _rotary_checks(Q, pos, freq, sections, K, OQ, OK):
+    """The checks of the rotary call, one by one."""
+    _operand(Q, "Q")
+    if Q.dim() != 4:
+        raise ValueError("expected Q [B,H,T,d]")
+    _dtype_code(Q)
+    B, _, T, _ = Q.shape
+    dev = Q.device
+    _last_dense(Q, "Q")
+    if K is not None:
+        _operand(K, "K", dev, Q.dtype)
+        if K.dim() != 4 or K.shape[0] != B or K.shape[2:] != Q.shape[2:]:
+            raise ValueError("expected K [B,HK,T,d] with Q's B, T and d")
+        _last_dense(K, "K")
+    elif OK is not None:
+        raise ValueError("OK without K")
+    axes = len(sections)
+    _operand(pos, "pos", dev, torch.int32)
+    if pos.shape != (axes, B, T) and pos.shape != (axes, T):
+        raise ValueError(f"pos has shape {tuple(pos.shape)}, expected {(axes, B, T)} or {(axes, T)}")
+    _last_dense(pos, "pos")
+    _operand(freq, "freq", dev, _F32, dense=True)
+    if freq.dim() != 1 or sum(sections) != freq.numel():
+        raise ValueError(f"freq must hold one frequency for each of the sections' {sum(sections)} pairs")
+    if OQ is not None:
+        _output(OQ, "OQ", dev, Q.dtype, Q.shape)
+    if OK is not None:
+        _output(OK, "OK", dev, K.dtype, K.shape)
+    _cuda_device(Q, "Q")
 
 
 def hla2_rotary(Q: torch.Tensor, pos: torch.Tensor, freq: torch.Tensor, sections, K: torch.Tensor | None = None,
@@ -927,49 +993,30 @@ def hla2_rotary(Q: torch.Tensor, pos: torch.Tensor, freq: torch.Tensor, sections
     which is the gradient).  Q [B,H,T,d], K [B,HK,T,d] fp32 or bf16; pos int32
     [axes,B,T] or [axes,T]; freq fp32 [pairs]; ``sections``: how many pairs
     follow each axis, in order.  Pairs are (p, p + pairs), or (2p, 2p + 1) when
-    ``interleaved``.  OQ and OK may be Q and K.  Returns (OQ, OK)."""
-    _operand(Q, "Q")
-    if Q.dim() != 4:
-        raise ValueError("expected Q [B,H,T,d]")
-    code = _dtype_code(Q)
+    ``interleaved``.  OQ and OK may be Q and K; those not given take the memory
+    order of their input.  Returns (OQ, OK)."""
+    sections = tuple(sections)
+    _rotary_checks(Q, pos, freq, sections, K, OQ, OK)
     B, H, T, d = Q.shape
-    dev = Q.device
-    HK = 0
-    if K is not None:
-        _operand(K, "K", dev, Q.dtype)
-        if K.dim() != 4 or K.shape[0] != B or K.shape[2:] != Q.shape[2:]:
-            raise ValueError("expected K [B,HK,T,d] with Q's B, T and d")
-        HK = K.shape[1]
-        _last_dense(K, "K")
-    elif OK is not None:
-        raise ValueError("OK without K")
-    _last_dense(Q, "Q")
-    sections = tuple(int(s) for s in sections)
-    axes = len(sections)
-    _operand(pos, "pos", dev, torch.int32)
-    if pos.shape != (axes, B, T) and pos.shape != (axes, T):
-        raise ValueError(f"pos has shape {tuple(pos.shape)}, expected {(axes, B, T)} or {(axes, T)}")
-    _last_dense(pos, "pos")
-    _operand(freq, "freq", dev, torch.float32, dense=True)
-    if freq.dim() != 1 or sum(sections) != freq.numel():
-        raise ValueError(f"freq must hold one frequency for each of the sections' {sum(sections)} pairs")
-    for o, name, like in ((OQ, "OQ", Q), (OK, "OK", K)):
-        if o is not None:
-            _operand(o, name, dev, like.dtype, like.shape)
-            _last_dense(o, name)
-            _no_overlap(o, name)
-    _cuda_device(Q, "Q")
+    dev, axes = Q.device, len(sections)
+    L = _lib or lib()
     with _guard(dev, stream):
         if OQ is None:
-            OQ = _out_like(Q, Q.dtype)
-        if OK is None and K is not None:
-            OK = _out_like(K, K.dtype)
-        st = [*Q.stride()[:3], *OQ.stride()[:3]]
-        st += (*K.stride()[:3], *OK.stride()[:3]) if K is not None else (0,) * 6
-        st += (pos.stride(0), pos.stride(1) if pos.dim() == 3 else 0)
-        rc = lib().hla2_rotary(Q.data_ptr(), OQ.data_ptr(), _ptr(K), _ptr(OK), pos.data_ptr(), freq.data_ptr(), B, H,
-                               HK, T, d, 2 * freq.numel(), axes, (ctypes.c_int * axes)(*sections),
-                               int(bool(interleaved)), int(bool(inverse)), (ctypes.c_longlong * 14)(*st), code,
-                               _stream(stream))
-    _check(rc, "hla2_rotary")
+            OQ = torch.empty_like(Q)
+        sq, so, sp = Q.stride(), OQ.stride(), pos.stride()
+        pb = sp[1] if len(sp) == 3 else 0
+        if K is None:
+            HK, pk, po = 0, None, None
+            st = _LL14(sq[0], sq[1], sq[2], so[0], so[1], so[2], 0, 0, 0, 0, 0, 0, sp[0], pb)
+        else:
+            if OK is None:
+                OK = torch.empty_like(K)
+            HK, pk, po = K.shape[1], K.data_ptr(), OK.data_ptr()
+            sk, sl = K.stride(), OK.stride()
+            st = _LL14(sq[0], sq[1], sq[2], so[0], so[1], so[2], sk[0], sk[1], sk[2], sl[0], sl[1], sl[2], sp[0], pb)
+        rc = L.hla2_rotary(Q.data_ptr(), OQ.data_ptr(), pk, po, pos.data_ptr(), freq.data_ptr(), B, H, HK, T, d,
+                           2 * freq.numel(), axes, (ctypes.c_int * axes)(*sections), bool(interleaved), bool(inverse),
+                           st, _CODES[Q.dtype], _raw(dev, stream))
+    if rc:
+        _check(rc, "hla2_rotary")
     return OQ, OK
