@@ -28,7 +28,7 @@ struct NormParams {
     float* scale;
     long long rows, ldx, ldr, lds, ldy;
     int C, wdtype;
-    float eps;
+    float eps, inv_c;
 };
 
 // Sum over the TPR threads of a row (TPR a power of two).  Threads of a row are
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(block_of(TPR)) rmsnorm_kernel(const NormParams
     }
     row_reduce<TPR>(ss, m, Q8, sh_a, sh_m);
     if (!live) return;
-    const float rstd = 1.f / sqrtf(ss / (float)p.C + p.eps);
+    const float rstd = rsqrtf(fmaf(ss, p.inv_c, p.eps));  // 2 ulp; a root and a quotient took 30 instructions a row
     if constexpr (Q8) {
         const float top = __uint_as_float(m) * rstd;
         const float scale = top == 0.f ? 1.f : top / 448.f;
@@ -215,7 +215,7 @@ cudaError_t pick_norm(const NormParams& p, bool vec, cudaStream_t s) {
     if (C <= 1024) return launch_norm<T, OUT, 128, 1>(p, vec, s);
     if (C <= 2048) return launch_norm<T, OUT, 256, 1>(p, vec, s);
     if (C <= 4096) return launch_norm<T, OUT, 256, 2>(p, vec, s);
-    if (C <= 8192) return launch_norm<T, OUT, 512, 2>(p, vec, s);
+    if (C <= 8192) return launch_norm<T, OUT, 256, 4>(p, vec, s);
     return launch_norm<T, OUT, 512, 4>(p, vec, s);
 }
 
@@ -231,7 +231,7 @@ struct NormBwdParams {
     float *dw, *part;  // part: [groups][C]
     long long rows, ldt, lddy, ldds, lddx;
     int C, wdtype;
-    float eps;
+    float eps, inv_c;
 };
 
 template <int TPR>
@@ -265,57 +265,67 @@ __global__ void __launch_bounds__(block_of(TPR)) rmsnorm_bwd_kernel(const NormBw
     const int lane = threadIdx.x % TPR;
     const long long group = (long long)blockIdx.x * kRows + threadIdx.x / TPR;
     const long long groups = (long long)gridDim.x * kRows;
-    float acc[NV][8];
+    // a thread's columns are the same in every row: so are its weights
+    float w[NV][8], acc[NV][8];
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
+    for (int v = 0; v < NV; ++v) {
+        const int c = (v * TPR + lane) * 8, n = p.C - c;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[v][j] = 0.f;
-
-    const long long trips = (p.rows + groups - 1) / groups;  // the same for every thread of the block
-    for (long long k = 0; k < trips; ++k) {
-        const long long row = k * groups + group;
+        for (int j = 0; j < 8; ++j) w[v][j] = acc[v][j] = 0.f;
+        if (n > 0) load_weight<VEC>(p.w, p.wdtype, c, n, w[v]);
+    }
+    Lane<T, 8, VEC> tv[NV], sv[NV];
+    Lane<TY, 8, VEC> yv[NV];
+    auto load = [&](long long row) {
+        const T* t = static_cast<const T*>(p.t) + row * p.ldt;
+        const TY* dy = static_cast<const TY*>(p.dy) + row * p.lddy;
+        const T* ds = static_cast<const T*>(p.ds) + row * p.ldds;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int c = (v * TPR + lane) * 8, n = p.C - c;
+            if (n > 0) {
+                tv[v].load(t + c, n);
+                yv[v].load(dy + c, n);
+                if (p.ds) sv[v].load(ds + c, n);
+            }
+        }
+    };
+    const int trips = (int)((p.rows + groups - 1) / groups);  // the same for every thread of the block
+    long long row = group;
+    for (int k = 0; k < trips; ++k, row += groups) {
         const bool live = row < p.rows;
-        Lane<T, 8, VEC> tv[NV], sv[NV];
-        Lane<TY, 8, VEC> yv[NV];
+        if (live) load(row);
         float a = 0.f, b = 0.f;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const int c = (v * TPR + lane) * 8, n = p.C - c;
+            const int n = p.C - (v * TPR + lane) * 8;
             if (live && n > 0) {
-                tv[v].load(static_cast<const T*>(p.t) + row * p.ldt + c, n);
-                yv[v].load(static_cast<const TY*>(p.dy) + row * p.lddy + c, n);
-                if (p.ds) sv[v].load(static_cast<const T*>(p.ds) + row * p.ldds + c, n);
-            }
-        }
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const int c = (v * TPR + lane) * 8, n = p.C - c;
-            if (live && n > 0) {
-                float w[8];
-                load_weight<VEC>(p.w, p.wdtype, c, n, w);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const float t = tv[v].get(j);
                     a = fmaf(t, t, a);
-                    b = fmaf(w[j] * yv[v].get(j), t, b);
+                    b = fmaf(w[v][j] * yv[v].get(j), t, b);
                 }
             }
         }
         row_sum2<TPR>(a, b, sh, phase);
         if (!live) continue;
-        const float rstd = 1.f / sqrtf(a / (float)p.C + p.eps);
-        const float back = rstd * rstd * (b / (float)p.C);  // rstd mean(w dy n) = rstd^2 mean(w dy t)
+        const float rstd = rsqrtf(fmaf(a, p.inv_c, p.eps));
+        const float back = rstd * rstd * rstd * (b * p.inv_c);  // rstd mean(w dy n) n = this times t
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int c = (v * TPR + lane) * 8, n = p.C - c;
             if (n > 0) {
-                float w[8], dx[8];
-                load_weight<VEC>(p.w, p.wdtype, c, n, w);
+                float dx[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float t = tv[v].get(j), dy = yv[v].get(j);
-                    dx[j] = rstd * (w[j] * dy - t * back) + (p.ds ? sv[v].get(j) : 0.f);
-                    acc[v][j] = fmaf(dy * rstd, t, acc[v][j]);
+                    const float t = tv[v].get(j), dy = rstd * yv[v].get(j);
+                    dx[j] = fmaf(w[v][j], dy, -(t * back));
+                    acc[v][j] = fmaf(dy, t, acc[v][j]);
+                }
+                if (p.ds) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) dx[j] += sv[v].get(j);
                 }
                 tv[v].set(dx);
                 tv[v].store(static_cast<T*>(p.dx) + row * p.lddx + c, n);
@@ -333,8 +343,8 @@ __global__ void __launch_bounds__(block_of(TPR)) rmsnorm_bwd_kernel(const NormBw
 }
 
 // dw[c] = sum of the groups' partial sums, in order: a warp's lanes take 32
-// columns, the block's warps every eighth group.
-constexpr int kFoldWarps = 8;
+// columns, the block's 32 warps every 32nd group.
+constexpr int kFoldWarps = 32;
 __global__ void __launch_bounds__(kFoldWarps * 32) fold_columns_kernel(const float* __restrict__ part,
                                                                       float* __restrict__ dw, int groups, int C) {
     __shared__ float sh[kFoldWarps][32];
@@ -353,22 +363,24 @@ __global__ void __launch_bounds__(kFoldWarps * 32) fold_columns_kernel(const flo
     }
 }
 
-// Blocks of the gradient's grid: at most four to an SM, at most one for each run of rows.
+// Blocks of the gradient's grid: what an SM holds, at most one for each run of rows.
+constexpr int kBwdThreadsPerSM = 1024;
 struct BwdPlan {
     int tpr, nv, rows_per_block, blocks;
 };
 BwdPlan bwd_plan(long long rows, int C) {
     BwdPlan b;
     if (C <= 64) { b.tpr = 8; b.nv = 1; }
-    else if (C <= 128) { b.tpr = 16; b.nv = 1; }
-    else if (C <= 256) { b.tpr = 32; b.nv = 1; }
-    else if (C <= 1024) { b.tpr = 128; b.nv = 1; }
-    else if (C <= 2048) { b.tpr = 256; b.nv = 1; }
-    else if (C <= 4096) { b.tpr = 512; b.nv = 1; }
+    else if (C <= 128) { b.tpr = 8; b.nv = 2; }
+    else if (C <= 256) { b.tpr = 16; b.nv = 2; }
+    else if (C <= 512) { b.tpr = 32; b.nv = 2; }
+    else if (C <= 1024) { b.tpr = 64; b.nv = 2; }
+    else if (C <= 2048) { b.tpr = 128; b.nv = 2; }
+    else if (C <= 4096) { b.tpr = 256; b.nv = 2; }
     else if (C <= 8192) { b.tpr = 512; b.nv = 2; }
     else { b.tpr = 512; b.nv = 4; }
     b.rows_per_block = block_of(b.tpr) / b.tpr;
-    const long long most = (long long)sm_count() * (1024 / block_of(b.tpr));
+    const long long most = (long long)sm_count() * (kBwdThreadsPerSM / block_of(b.tpr));
     const long long need = (rows + b.rows_per_block - 1) / b.rows_per_block;
     b.blocks = (int)(need < most ? need : most);
     return b;
@@ -386,11 +398,12 @@ template <typename T, typename TY>
 cudaError_t pick_bwd(const NormBwdParams& p, const BwdPlan& b, bool vec, cudaStream_t s) {
     switch (b.tpr * 8 + b.nv) {
         case 8 * 8 + 1: return launch_bwd<T, TY, 8, 1>(p, b.blocks, vec, s);
-        case 16 * 8 + 1: return launch_bwd<T, TY, 16, 1>(p, b.blocks, vec, s);
-        case 32 * 8 + 1: return launch_bwd<T, TY, 32, 1>(p, b.blocks, vec, s);
-        case 128 * 8 + 1: return launch_bwd<T, TY, 128, 1>(p, b.blocks, vec, s);
-        case 256 * 8 + 1: return launch_bwd<T, TY, 256, 1>(p, b.blocks, vec, s);
-        case 512 * 8 + 1: return launch_bwd<T, TY, 512, 1>(p, b.blocks, vec, s);
+        case 8 * 8 + 2: return launch_bwd<T, TY, 8, 2>(p, b.blocks, vec, s);
+        case 16 * 8 + 2: return launch_bwd<T, TY, 16, 2>(p, b.blocks, vec, s);
+        case 32 * 8 + 2: return launch_bwd<T, TY, 32, 2>(p, b.blocks, vec, s);
+        case 64 * 8 + 2: return launch_bwd<T, TY, 64, 2>(p, b.blocks, vec, s);
+        case 128 * 8 + 2: return launch_bwd<T, TY, 128, 2>(p, b.blocks, vec, s);
+        case 256 * 8 + 2: return launch_bwd<T, TY, 256, 2>(p, b.blocks, vec, s);
         case 512 * 8 + 2: return launch_bwd<T, TY, 512, 2>(p, b.blocks, vec, s);
         default: return launch_bwd<T, TY, 512, 4>(p, b.blocks, vec, s);
     }
@@ -420,7 +433,7 @@ int norm_common(const char* what, const void* X, const void* R, const void* W, v
         return set_error(HLA2_ERR_INVALID, "%s: a row stride below C=%d or a pointer not aligned to its element", what, C);
     const bool vec = C % 8 == 0 && row_vec(X, ldx, es, 16) && row_vec(R, ldr, es, 16) && row_vec(S, lds, es, 16) &&
                      row_vec(Y, ldy, os, out == kOutE4M3 ? 8 : 16) && reinterpret_cast<uintptr_t>(W) % 16 == 0;
-    NormParams p{X, R, W, S, Y, scale, rows, ldx, ldr, lds, ldy, C, wdtype, eps};
+    NormParams p{X, R, W, S, Y, scale, rows, ldx, ldr, lds, ldy, C, wdtype, eps, 1.f / (float)C};
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (dtype == HLA2_DTYPE_BF16)
@@ -483,7 +496,7 @@ extern "C" int hla2_rmsnorm_backward(const void* S, const void* dY, const void* 
     const bool vec = C % 8 == 0 && row_vec(S, ld[0], es, 16) && row_vec(dY, ld[1], os, 16) &&
                      row_vec(dS, ld[2], es, 16) && row_vec(dX, ld[3], es, 16) &&
                      reinterpret_cast<uintptr_t>(W) % 16 == 0;
-    NormBwdParams p{S, dY, W, dS, dX, dW, static_cast<float*>(workspace), rows, ld[0], ld[1], ld[2], ld[3], C, wdtype, eps};
+    NormBwdParams p{S, dY, W, dS, dX, dW, static_cast<float*>(workspace), rows, ld[0], ld[1], ld[2], ld[3], C, wdtype, eps, 1.f / (float)C};
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (dtype == HLA2_DTYPE_BF16)

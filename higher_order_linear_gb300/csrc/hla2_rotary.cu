@@ -11,7 +11,12 @@
 // channels and its partners at a time: 65536 tokens x 32 heads need 4M sines
 // instead of 134M.  It walks the heads (or the tokens) in the order in which
 // they lie in memory: a walk that has all blocks at the same head of different
-// tokens, 4 KB apart, reached 0.54 of the copy bandwidth.
+// tokens, 4 KB apart, reached 0.54 of the copy bandwidth.  For the same reason a
+// block takes about 64 KB of Q and K, one row in flight to a thread and eight
+// blocks to an SM: few addresses, close together.  65536 tokens x 32 heads x 128
+// in 16 bits (1.07 GB): 168 us, 0.94 of the copy bandwidth; with 16 and 32 tokens
+// to a block (128 and 256 KB) 172 and 184 us, with two and four rows in flight
+// (and 32 tokens) 197 and 228 us.
 //
 // The angle is reduced in revolutions: freq / (2 pi) is carried as a sum of two
 // fp32 numbers, its product with the position as a sum of two more (the
@@ -26,8 +31,8 @@ namespace hla2 {
 namespace {
 
 constexpr int kRotThreads = 256;
-constexpr int kRotRows = 4;     // rows (a head of a token) whose loads a thread has in flight
-constexpr int kRotTokens = 32;  // tokens to a block, at most
+constexpr int kRotTokens = 32;         // tokens to a block, at most
+constexpr int kRotBytes = 64 * 1024;   // of Q and K to a block, about
 
 struct RotParams {
     const void *q, *k;
@@ -72,7 +77,7 @@ __device__ __forceinline__ void turn_of(int ps, float f, float& si, float& co) {
 }
 
 template <typename T, int V, bool IL>
-__global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_constant__ RotParams p) {
+__global__ void __launch_bounds__(kRotThreads, V == 8 ? 8 : 1) rotary_kernel(const __grid_constant__ RotParams p) {
     constexpr bool VEC = V > 1;
     extern __shared__ __align__(16) unsigned char raw[];
     // where each token's heads are: element offsets of Q, OQ, K, OK
@@ -105,22 +110,16 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
         if (p.head_inner) { tok = (int)(r / (unsigned)heads); h = (int)(r - (unsigned)tok * (unsigned)heads); }
         else { h = (int)(r / (unsigned)nt); tok = (int)(r - (unsigned)h * (unsigned)nt); }
     };
-    Lane<T, V, VEC> x[kRotRows], y[kRotRows];
-    auto load = [&](unsigned r0) {
-#pragma unroll
-        for (int i = 0; i < kRotRows; ++i) {
-            const unsigned r = r0 + i * groups;
-            if (r < rows) {
-                int tok, h;
-                locate(r, tok, h);
-                const T* s = h < p.H ? static_cast<const T*>(p.q) + at[0][tok] + h * p.sq[1]
-                                     : static_cast<const T*>(p.k) + at[2][tok] + (h - p.H) * p.sk[1];
-                if (n0 > 0) x[i].load(s + c0, n0);
-                if (n1 > 0) y[i].load(s + c1, n1);
-            }
-        }
+    Lane<T, V, VEC> x, y;
+    auto load = [&](unsigned r) {
+        int tok, h;
+        locate(r, tok, h);
+        const T* s = h < p.H ? static_cast<const T*>(p.q) + at[0][tok] + h * p.sq[1]
+                             : static_cast<const T*>(p.k) + at[2][tok] + (h - p.H) * p.sk[1];
+        if (n0 > 0) x.load(s + c0, n0);
+        if (n1 > 0) y.load(s + c1, n1);
     };
-    const bool works = group < groups;
+    const bool works = group < groups && (unsigned)group < rows;
     if (works) load(group);  // on its way while the sines are taken
 
     // sines: 4 pairs' cosines (or sines) are one 16-byte word; a token's words lie
@@ -144,51 +143,46 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
     }
     __syncthreads();
     if (!works) return;
-    for (unsigned r0 = group; r0 < rows; r0 += kRotRows * groups) {
-        if (r0 != (unsigned)group) load(r0);
+    for (unsigned r = group; r < rows; r += groups) {
+        if (r != (unsigned)group) load(r);
+        int tok, h;
+        locate(r, tok, h);
+        if (turns) {
+            float co[V], si[V];
+            if constexpr (VEC) {
 #pragma unroll
-        for (int i = 0; i < kRotRows; ++i) {
-            const unsigned r = r0 + i * groups;
-            if (r >= rows) break;
-            int tok, h;
-            locate(r, tok, h);
-            if (turns) {
-                float co[V], si[V];
-                if constexpr (VEC) {
-#pragma unroll
-                    for (int q = 0; q < V / 4; ++q) {
-                        const float4 c4 = *reinterpret_cast<const float4*>(table + entry(tok, p0 + 4 * q, 0));
-                        const float4 s4 = *reinterpret_cast<const float4*>(table + entry(tok, p0 + 4 * q, 1));
-                        co[4 * q] = c4.x; co[4 * q + 1] = c4.y; co[4 * q + 2] = c4.z; co[4 * q + 3] = c4.w;
-                        si[4 * q] = s4.x; si[4 * q + 1] = s4.y; si[4 * q + 2] = s4.z; si[4 * q + 3] = s4.w;
-                    }
-                } else {
-                    co[0] = table[entry(tok, p0, 0)];
-                    si[0] = table[entry(tok, p0, 1)];
+                for (int q = 0; q < V / 4; ++q) {
+                    const float4 c4 = *reinterpret_cast<const float4*>(table + entry(tok, p0 + 4 * q, 0));
+                    const float4 s4 = *reinterpret_cast<const float4*>(table + entry(tok, p0 + 4 * q, 1));
+                    co[4 * q] = c4.x; co[4 * q + 1] = c4.y; co[4 * q + 2] = c4.z; co[4 * q + 3] = c4.w;
+                    si[4 * q] = s4.x; si[4 * q + 1] = s4.y; si[4 * q + 2] = s4.z; si[4 * q + 3] = s4.w;
                 }
-                float u[V], v[V];
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    if (IL && VEC) {  // pair j: elements 2j, 2j + 1 of the 2 V channels
-                        const float a = 2 * j < V ? x[i].get((2 * j) % V) : y[i].get((2 * j) % V);
-                        const float c = 2 * j < V ? x[i].get((2 * j + 1) % V) : y[i].get((2 * j + 1) % V);
-                        const float r0 = a * co[j] - c * si[j], r1 = a * si[j] + c * co[j];
-                        if (2 * j < V) { u[(2 * j) % V] = r0; u[(2 * j + 1) % V] = r1; }
-                        else { v[(2 * j) % V] = r0; v[(2 * j + 1) % V] = r1; }
-                    } else {
-                        const float a = x[i].get(j), c = y[i].get(j);
-                        u[j] = a * co[j] - c * si[j];
-                        v[j] = a * si[j] + c * co[j];
-                    }
-                }
-                x[i].set(u);
-                y[i].set(v);
+            } else {
+                co[0] = table[entry(tok, p0, 0)];
+                si[0] = table[entry(tok, p0, 1)];
             }
-            T* o = h < p.H ? static_cast<T*>(p.oq) + at[1][tok] + h * p.soq[1]
-                           : static_cast<T*>(p.ok) + at[3][tok] + (h - p.H) * p.sok[1];
-            if (n0 > 0) x[i].store(o + c0, n0);
-            if (n1 > 0) y[i].store(o + c1, n1);
+            float u[V], v[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                if (IL && VEC) {  // pair j: elements 2j, 2j + 1 of the 2 V channels
+                    const float a = 2 * j < V ? x.get((2 * j) % V) : y.get((2 * j) % V);
+                    const float c = 2 * j < V ? x.get((2 * j + 1) % V) : y.get((2 * j + 1) % V);
+                    const float r0 = a * co[j] - c * si[j], r1 = a * si[j] + c * co[j];
+                    if (2 * j < V) { u[(2 * j) % V] = r0; u[(2 * j + 1) % V] = r1; }
+                    else { v[(2 * j) % V] = r0; v[(2 * j + 1) % V] = r1; }
+                } else {
+                    const float a = x.get(j), c = y.get(j);
+                    u[j] = a * co[j] - c * si[j];
+                    v[j] = a * si[j] + c * co[j];
+                }
+            }
+            x.set(u);
+            y.set(v);
         }
+        T* o = h < p.H ? static_cast<T*>(p.oq) + at[1][tok] + h * p.soq[1]
+                       : static_cast<T*>(p.ok) + at[3][tok] + (h - p.H) * p.sok[1];
+        if (n0 > 0) x.store(o + c0, n0);
+        if (n1 > 0) y.store(o + c1, n1);
     }
 }
 
@@ -197,8 +191,9 @@ cudaError_t launch_rotary(RotParams& p, bool interleaved, int sms, cudaStream_t 
     const int pairs = p.rot / 2, rest = p.d - p.rot;
     p.slots = pairs / V + (rest + 2 * V - 1) / (2 * V);
     p.total = (long long)p.B * p.T;
-    // as many tokens to a block as leave four blocks to an SM
     p.tokens = kRotTokens;
+    while (p.tokens > 1 && (long long)p.tokens * (p.H + p.HK) * p.d * sizeof(T) > kRotBytes) p.tokens /= 2;
+    // and as few as leave four blocks to an SM
     while (p.tokens > 1 && (p.total + p.tokens - 1) / p.tokens < 4LL * sms) p.tokens /= 2;
     const unsigned blocks = (unsigned)((p.total + p.tokens - 1) / p.tokens);
     const size_t smem = (size_t)p.tokens * pairs * 8;
