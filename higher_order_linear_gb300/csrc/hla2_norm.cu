@@ -222,9 +222,10 @@ cudaError_t pick_norm(const NormParams& p, bool vec, cudaStream_t s) {
 // ------------------------------------------------------------- gradient ----
 //   n = t rstd;  dx = rstd (w dy - n mean(w dy n)) + ds;  dw = sum_rows dy n.
 // The row stays in registers between its two sums (t^2 and w dy t) and dx.
-// The column sums of dw are kept in registers over all the rows a group of
-// threads walks; each group leaves its partial sums in the workspace and a
-// second kernel adds them in order, so the result does not depend on timing.
+// The column sums of dw are kept in registers over all the rows that a group of
+// threads walks; a block adds those of its groups in order and leaves them in the
+// workspace, and a second kernel adds the blocks' in order, so the result does
+// not depend on timing.
 struct NormBwdParams {
     const void *t, *dy, *w, *ds;
     void* dx;
@@ -234,6 +235,12 @@ struct NormBwdParams {
     float eps, inv_c;
 };
 
+// Threads of a block of the gradient, and blocks to an SM: 64 registers to a
+// thread hold a row's 8 elements of t, dy and ds, the weights, the column sums
+// and the next row's loads.
+constexpr int bwd_block(int tpr) { return tpr > 256 ? tpr : 256; }
+constexpr int bwd_blocks(int tpr) { return 1024 / bwd_block(tpr); }
+
 template <int TPR>
 __device__ __forceinline__ void row_sum2(float& a, float& b, float2* sh, int& phase) {
 #pragma unroll
@@ -242,12 +249,13 @@ __device__ __forceinline__ void row_sum2(float& a, float& b, float2* sh, int& ph
         b += __shfl_xor_sync(0xffffffffu, b, o);
     }
     if constexpr (TPR > 32) {
-        constexpr int NW = TPR / 32, kWarps = block_of(TPR) / 32;
+        constexpr int NW = TPR / 32, kWarps = bwd_block(TPR) / 32;
         const int warp = threadIdx.x >> 5, w0 = warp / NW * NW;
         float2* buf = sh + phase * kWarps;  // two buffers: one barrier for each row
         phase ^= 1;
         if ((threadIdx.x & 31) == 0) buf[warp] = make_float2(a, b);
-        __syncthreads();
+        // the row's own threads only: the rows of a block do not wait for one another
+        asm volatile("bar.sync %0, %1;" ::"r"((int)threadIdx.x / TPR + 1), "n"(TPR) : "memory");
         a = b = 0.f;
 #pragma unroll
         for (int i = 0; i < NW; ++i) {
@@ -258,9 +266,10 @@ __device__ __forceinline__ void row_sum2(float& a, float& b, float2* sh, int& ph
 }
 
 template <typename T, typename TY, int TPR, int NV, bool VEC>
-__global__ void __launch_bounds__(block_of(TPR)) rmsnorm_bwd_kernel(const NormBwdParams p) {
-    constexpr int kThreads = block_of(TPR), kRows = kThreads / TPR;
+__global__ void __launch_bounds__(bwd_block(TPR), bwd_blocks(TPR)) rmsnorm_bwd_kernel(const NormBwdParams p) {
+    constexpr int kThreads = bwd_block(TPR), kRows = kThreads / TPR;
     __shared__ float2 sh[2 * kThreads / 32];
+    extern __shared__ __align__(16) float columns[];  // [C], where rows share the block
     int phase = 0;
     const int lane = threadIdx.x % TPR;
     const long long group = (long long)blockIdx.x * kRows + threadIdx.x / TPR;
@@ -290,11 +299,12 @@ __global__ void __launch_bounds__(block_of(TPR)) rmsnorm_bwd_kernel(const NormBw
             }
         }
     };
-    const int trips = (int)((p.rows + groups - 1) / groups);  // the same for every thread of the block
+    // lanes of one warp that hold different rows make the same trips (the sums are taken by whole warps)
+    const int trips = (int)((p.rows + groups - 1) / groups);
     long long row = group;
+    if (row < p.rows) load(row);
     for (int k = 0; k < trips; ++k, row += groups) {
         const bool live = row < p.rows;
-        if (live) load(row);
         float a = 0.f, b = 0.f;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
@@ -312,9 +322,10 @@ __global__ void __launch_bounds__(block_of(TPR)) rmsnorm_bwd_kernel(const NormBw
         if (!live) continue;
         const float rstd = rsqrtf(fmaf(a, p.inv_c, p.eps));
         const float back = rstd * rstd * rstd * (b * p.inv_c);  // rstd mean(w dy n) n = this times t
+        Lane<T, 8, VEC> out[NV];
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const int c = (v * TPR + lane) * 8, n = p.C - c;
+            const int n = p.C - (v * TPR + lane) * 8;
             if (n > 0) {
                 float dx[8];
 #pragma unroll
@@ -327,60 +338,72 @@ __global__ void __launch_bounds__(block_of(TPR)) rmsnorm_bwd_kernel(const NormBw
 #pragma unroll
                     for (int j = 0; j < 8; ++j) dx[j] += sv[v].get(j);
                 }
-                tv[v].set(dx);
-                tv[v].store(static_cast<T*>(p.dx) + row * p.lddx + c, n);
+                out[v].set(dx);
             }
+        }
+        if (row + groups < p.rows) load(row + groups);  // on its way while this row is written
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int c = (v * TPR + lane) * 8, n = p.C - c;
+            if (n > 0) out[v].store(static_cast<T*>(p.dx) + row * p.lddx + c, n);
         }
     }
     if (!p.dw) return;
+    // the block's sums, group after group, then one line of partial sums to a block
+    float* const part = p.part + (long long)blockIdx.x * p.C;
+    for (int g = 0; g < kRows; ++g) {
+        if (threadIdx.x / TPR == g) {
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        const int c = (v * TPR + lane) * 8;
+            for (int v = 0; v < NV; ++v) {
+                const int c = (v * TPR + lane) * 8;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (c + j < p.C) p.part[group * p.C + c + j] = acc[v][j];
+                for (int j = 0; j < 8; ++j)
+                    if (c + j < p.C) {
+                        const float s = g > 0 ? columns[c + j] + acc[v][j] : acc[v][j];
+                        if (g + 1 < kRows) columns[c + j] = s;
+                        else part[c + j] = s;
+                    }
+            }
+        }
+        if (g + 1 < kRows) __syncthreads();
     }
 }
 
-// dw[c] = sum of the groups' partial sums, in order: a warp's lanes take 32
-// columns, the block's 32 warps every 32nd group.
-constexpr int kFoldWarps = 32;
-__global__ void __launch_bounds__(kFoldWarps * 32) fold_columns_kernel(const float* __restrict__ part,
-                                                                      float* __restrict__ dw, int groups, int C) {
-    __shared__ float sh[kFoldWarps][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+// dw[c] = sum of the blocks' partial sums, in a fixed order: 16 columns to a
+// block, each 64 threads' sums of every 64th line.
+constexpr int kFoldColumns = 16, kFoldThreads = 1024, kFoldLines = kFoldThreads / kFoldColumns;
+__global__ void __launch_bounds__(kFoldThreads) fold_columns_kernel(const float* __restrict__ part,
+                                                                   float* __restrict__ dw, int lines, int C) {
+    __shared__ float sh[kFoldThreads / 32][kFoldColumns];
+    const int col = threadIdx.x % kFoldColumns, line = threadIdx.x / kFoldColumns;
+    const int c = blockIdx.x * kFoldColumns + col;
     float a = 0.f;
     if (c < C) {
 #pragma unroll 8
-        for (int g = warp; g < groups; g += kFoldWarps) a += part[(size_t)g * C + c];
+        for (int g = line; g < lines; g += kFoldLines) a += part[(size_t)g * C + c];
     }
-    sh[warp][lane] = a;
+    a += __shfl_down_sync(0xffffffffu, a, 16);  // the warp's second line of threads
+    if ((threadIdx.x & 31) < kFoldColumns) sh[threadIdx.x >> 5][col] = a;
     __syncthreads();
-    if (warp == 0 && c < C) {
+    if (threadIdx.x < kFoldColumns && c < C) {
+        a = 0.f;
 #pragma unroll
-        for (int i = 1; i < kFoldWarps; ++i) a += sh[i][lane];
+        for (int i = 0; i < kFoldThreads / 32; ++i) a += sh[i][col];
         dw[c] = a;
     }
 }
 
-// Blocks of the gradient's grid: what an SM holds, at most one for each run of rows.
-constexpr int kBwdThreadsPerSM = 1024;
+// Blocks of the gradient's grid: what the SMs hold, at most one for each run of rows.
 struct BwdPlan {
     int tpr, nv, rows_per_block, blocks;
 };
 BwdPlan bwd_plan(long long rows, int C) {
     BwdPlan b;
-    if (C <= 64) { b.tpr = 8; b.nv = 1; }
-    else if (C <= 128) { b.tpr = 8; b.nv = 2; }
-    else if (C <= 256) { b.tpr = 16; b.nv = 2; }
-    else if (C <= 512) { b.tpr = 32; b.nv = 2; }
-    else if (C <= 1024) { b.tpr = 64; b.nv = 2; }
-    else if (C <= 2048) { b.tpr = 128; b.nv = 2; }
-    else if (C <= 4096) { b.tpr = 256; b.nv = 2; }
-    else if (C <= 8192) { b.tpr = 512; b.nv = 2; }
-    else { b.tpr = 512; b.nv = 4; }
-    b.rows_per_block = block_of(b.tpr) / b.tpr;
-    const long long most = (long long)sm_count() * (kBwdThreadsPerSM / block_of(b.tpr));
+    b.nv = C <= 8192 ? 1 : 2;
+    b.tpr = 8;
+    while (b.tpr * b.nv * 8 < C) b.tpr *= 2;
+    b.rows_per_block = bwd_block(b.tpr) / b.tpr;
+    const long long most = (long long)sm_count() * bwd_blocks(b.tpr);
     const long long need = (rows + b.rows_per_block - 1) / b.rows_per_block;
     b.blocks = (int)(need < most ? need : most);
     return b;
@@ -388,24 +411,26 @@ BwdPlan bwd_plan(long long rows, int C) {
 
 template <typename T, typename TY, int TPR, int NV>
 cudaError_t launch_bwd(const NormBwdParams& p, int blocks, bool vec, cudaStream_t s) {
-    if (vec) rmsnorm_bwd_kernel<T, TY, TPR, NV, true><<<blocks, block_of(TPR), 0, s>>>(p);
-    else rmsnorm_bwd_kernel<T, TY, TPR, NV, false><<<blocks, block_of(TPR), 0, s>>>(p);
+    const size_t smem = p.dw && TPR < bwd_block(TPR) ? (size_t)p.C * 4 : 0;
+    if (vec) rmsnorm_bwd_kernel<T, TY, TPR, NV, true><<<blocks, bwd_block(TPR), smem, s>>>(p);
+    else rmsnorm_bwd_kernel<T, TY, TPR, NV, false><<<blocks, bwd_block(TPR), smem, s>>>(p);
     note_launches(1);
     return cudaGetLastError();
 }
 
 template <typename T, typename TY>
 cudaError_t pick_bwd(const NormBwdParams& p, const BwdPlan& b, bool vec, cudaStream_t s) {
-    switch (b.tpr * 8 + b.nv) {
-        case 8 * 8 + 1: return launch_bwd<T, TY, 8, 1>(p, b.blocks, vec, s);
-        case 8 * 8 + 2: return launch_bwd<T, TY, 8, 2>(p, b.blocks, vec, s);
-        case 16 * 8 + 2: return launch_bwd<T, TY, 16, 2>(p, b.blocks, vec, s);
-        case 32 * 8 + 2: return launch_bwd<T, TY, 32, 2>(p, b.blocks, vec, s);
-        case 64 * 8 + 2: return launch_bwd<T, TY, 64, 2>(p, b.blocks, vec, s);
-        case 128 * 8 + 2: return launch_bwd<T, TY, 128, 2>(p, b.blocks, vec, s);
-        case 256 * 8 + 2: return launch_bwd<T, TY, 256, 2>(p, b.blocks, vec, s);
-        case 512 * 8 + 2: return launch_bwd<T, TY, 512, 2>(p, b.blocks, vec, s);
-        default: return launch_bwd<T, TY, 512, 4>(p, b.blocks, vec, s);
+    switch (b.tpr) {
+        case 8: return launch_bwd<T, TY, 8, 1>(p, b.blocks, vec, s);
+        case 16: return launch_bwd<T, TY, 16, 1>(p, b.blocks, vec, s);
+        case 32: return launch_bwd<T, TY, 32, 1>(p, b.blocks, vec, s);
+        case 64: return launch_bwd<T, TY, 64, 1>(p, b.blocks, vec, s);
+        case 128: return launch_bwd<T, TY, 128, 1>(p, b.blocks, vec, s);
+        case 256: return launch_bwd<T, TY, 256, 1>(p, b.blocks, vec, s);
+        case 512: return launch_bwd<T, TY, 512, 1>(p, b.blocks, vec, s);
+        default:
+            return b.nv == 1 ? launch_bwd<T, TY, 1024, 1>(p, b.blocks, vec, s)
+                             : launch_bwd<T, TY, 1024, 2>(p, b.blocks, vec, s);
     }
 }
 
@@ -470,7 +495,7 @@ extern "C" size_t hla2_rmsnorm_backward_workspace(long long rows, int C) {
     using namespace hla2;
     if (rows <= 0 || rows > 0x7fffffffLL || C <= 0 || C > kMaxC) return 0;
     const BwdPlan b = bwd_plan(rows, C);
-    return ((size_t)b.blocks * b.rows_per_block * C * 4 + 255) & ~size_t(255);
+    return ((size_t)b.blocks * C * 4 + 255) & ~size_t(255);
 }
 
 extern "C" int hla2_rmsnorm_backward(const void* S, const void* dY, const void* W, const void* dS, void* dX, float* dW,
@@ -489,9 +514,8 @@ extern "C" int hla2_rmsnorm_backward(const void* S, const void* dY, const void* 
         !row_ok(dX, ld[3], C, es) || !aligned_elem(W, wsz) || !aligned_elem(dW, 4))
         return set_error(HLA2_ERR_INVALID, "%s: a row stride below C=%d or a pointer not aligned to its element", what, C);
     const BwdPlan b = bwd_plan(rows, C);
-    const int groups = b.blocks * b.rows_per_block;
-    if (dW && (!workspace || ws_bytes < (size_t)groups * C * 4))
-        return set_error(HLA2_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", what, ws_bytes, (size_t)groups * C * 4);
+    if (dW && (!workspace || ws_bytes < (size_t)b.blocks * C * 4))
+        return set_error(HLA2_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", what, ws_bytes, (size_t)b.blocks * C * 4);
     if (dW && reinterpret_cast<uintptr_t>(workspace) % 16) return set_error(HLA2_ERR_INVALID, "%s: workspace not 16-byte aligned", what);
     const bool vec = C % 8 == 0 && row_vec(S, ld[0], es, 16) && row_vec(dY, ld[1], os, 16) &&
                      row_vec(dS, ld[2], es, 16) && row_vec(dX, ld[3], es, 16) &&
@@ -504,7 +528,7 @@ extern "C" int hla2_rmsnorm_backward(const void* S, const void* dY, const void* 
     else
         e = out_dtype == HLA2_DTYPE_BF16 ? pick_bwd<float, bf16>(p, b, vec, s) : pick_bwd<float, float>(p, b, vec, s);
     if (e == cudaSuccess && dW) {
-        fold_columns_kernel<<<(C + 31) / 32, kFoldWarps * 32, 0, s>>>(p.part, dW, groups, C);
+        fold_columns_kernel<<<(C + kFoldColumns - 1) / kFoldColumns, kFoldThreads, 0, s>>>(p.part, dW, b.blocks, C);
         note_launches(1);
         e = cudaGetLastError();
     }
