@@ -63,12 +63,7 @@ gated_scan_kernel(const GateParams p) {
                 runs[r][ch] = m;
                 m = then(m, f);
             }
-            if (p.words) {
-                publish_tile(p, lb, row, n, ch, m);
-                publish_group(p, lb, row, n, ch, m);
-                h = enter_tile(p, lb, row, n, ch, h);
-                publish_state(p, lb, row, n, ch, pass(m, h));
-            }
+            if (p.words) h = join_tile(p, lb, row, n, ch, m, h);
             entering[ch] = h;
             if (p.carry && ch < p.d) p.carry[((long long)row * p.tiles + n) * p.d + ch] = h;
             __syncthreads();  // what enters each run is there
@@ -153,46 +148,18 @@ gated_scan_kernel(const GateParams p) {
 //            their own, so that no group's map waits behind a joiner's waits;
 //   writers  walk the runs again and write the outputs.
 // Every wait is bounded in time, as in the other kernels of this library.
-constexpr int kJoin = 2;
-constexpr int kAhead = 1;
 
 template <typename T, bool SHARED, int LANES>
 struct PipeLayout {
     static constexpr int CB = LANES * kCh, RUNS = kData / LANES, TILE = RUNS * kTok;
     static constexpr uint32_t kTileBytes = TILE * CB * sizeof(T);  // of x, and of the gates
     static constexpr uint32_t kMaps = RUNS * CB * 8;
+    static constexpr int kJoiners = CB / kJoinCh;  // threads of a set of joiners
     static constexpr uint32_t kStage = kTileBytes * (SHARED ? 1 : 2) + kMaps;
     static constexpr int kStages = 225 * 1024 / kStage > 8 ? 8 : 225 * 1024 / kStage;
     static constexpr uint32_t kBytes = kStage * kStages + 128;  // and alignment to 128 bytes
-    static constexpr int kThreads = 32 + kData + kJoin * CB + CB + kData;
+    static constexpr int kThreads = 32 + kData + (kJoin + 1) * kJoiners + kData;
 };
-
-__device__ __forceinline__ void mbar_arrive(uint32_t a) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(a) : "memory");
-}
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t mbar) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
-        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(mbar)
-        : "memory");
-}
-
-__device__ __forceinline__ void tma_prefetch_l2_4d(const CUtensorMap* map, int x, int y, int z, int w) {
-    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global [%0, {%1, %2, %3, %4}];"
-                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w)
-                 : "memory");
-}
-
-// four channels of one token in shared memory, as fp32
-__device__ __forceinline__ void four(const float* p, float (&v)[4]) {
-    const float4 a = *reinterpret_cast<const float4*>(p);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-}
-__device__ __forceinline__ void four(const bf16* p, float (&v)[4]) {
-    const uint2 a = *reinterpret_cast<const uint2*>(p);
-    v[0] = __uint_as_float(a.x << 16); v[1] = __uint_as_float(a.x & 0xffff0000u);
-    v[2] = __uint_as_float(a.y << 16); v[3] = __uint_as_float(a.y & 0xffff0000u);
-}
 
 template <typename T, bool SIG, bool SHARED, int LANES>
 __global__ void __launch_bounds__(PipeLayout<T, SHARED, LANES>::kThreads, 1)
@@ -224,8 +191,8 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
         for (int s = 0; s < S; ++s) {
             mbar_init(full(s), 1);
             mbar_init(mapped(s), CB / 32);
-            mbar_init(joined(s), CB / 32);
-            mbar_init(empty(s), kData / 32 + CB / 32);
+            mbar_init(joined(s), LY::kJoiners / 32);
+            mbar_init(empty(s), kData / 32 + LY::kJoiners / 32);
             mbar_init(runs(s), kData / 32);
             mbar_init(known(s), 1);
         }
@@ -236,7 +203,7 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
         if (abort_flag) return false;
         if (mbar_try(bar, parity)) return true;
         const unsigned long long t0 = globaltimer();
-        while (!mbar_try(bar, parity)) {
+        while (!mbar_try_long(bar, parity)) {
             if (abort_flag) return false;
             if (globaltimer() - t0 > 2 * kGateWaitNs) {  // longer than the joiners' own waits
                 abort_flag = 1;
@@ -299,26 +266,37 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
         if (abort_flag && !loads.settle()) atomicExch(p.status, (int)kDevWaitTimeout);
         return;
     }
-    if (warp >= 1 + kData / 32 && warp < 1 + kData / 32 + kJoin * (CB / 32)) {  // joiners
-        const int j = (warp - 1 - kData / 32) / (CB / 32);
-        const int ch = tid - 32 - kData - j * CB;
+    constexpr int kFirstJoiner = 32 + kData, kFirstGrouper = kFirstJoiner + kJoin * LY::kJoiners;
+    if (tid >= kFirstJoiner && tid < kFirstGrouper) {  // joiners
+        const int j = (tid - kFirstJoiner) / LY::kJoiners;
+        const int ch = (tid - kFirstJoiner - j * LY::kJoiners) * kJoinCh;
         for (unsigned i = (unsigned)j;; i += kJoin) {
             const int s = (int)(i % S);
             if (!wait(known(s), (i / S) & 1u)) return;
             const unsigned k = tile_of_stage[s];
             if (k != kEnd) {
                 place(k, n, row, b, hd);
-                float h = p.state_in && ch < p.d ? p.state_in[(long long)row * p.d + ch] : 0.f;
-                if (p.words) h = enter_tile(p, lb, row, n, ch, h);  // while the tile is loaded and mapped
-                if (p.carry && ch < p.d) p.carry[((long long)row * p.tiles + n) * p.d + ch] = h;
-                if (!wait(mapped(s), (i / S) & 1u)) return;
-                if (p.words) publish_state(p, lb, row, n, ch, pass(total[s][ch], h));
-                float2* m = maps(s) + ch;
+                float h[kJoinCh];
 #pragma unroll
-                for (int r = 0; r < RUNS; ++r) {
-                    const float2 f = m[r * CB];
-                    m[r * CB].x = h;
-                    h = pass(f, h);
+                for (int q = 0; q < kJoinCh; ++q)
+                    h[q] = p.state_in && ch + q < p.d ? p.state_in[(long long)row * p.d + ch + q] : 0.f;
+                if (p.words) enter_tile(p, lb, row, n, ch, h);  // while the tile is loaded and mapped
+                if (p.carry) {
+#pragma unroll
+                    for (int q = 0; q < kJoinCh; ++q)
+                        if (ch + q < p.d) p.carry[((long long)row * p.tiles + n) * p.d + ch + q] = h[q];
+                }
+                if (!wait(mapped(s), (i / S) & 1u)) return;
+#pragma unroll
+                for (int q = 0; q < kJoinCh; ++q) {
+                    if (p.words) publish_state(p, lb, row, n, ch + q, pass(total[s][ch + q], h[q]));
+                    float2* m = maps(s) + ch + q;
+#pragma unroll
+                    for (int r = 0; r < RUNS; ++r) {
+                        const float2 f = m[r * CB];
+                        m[r * CB].x = h[q];
+                        h[q] = pass(f, h[q]);
+                    }
                 }
             }
             __syncwarp();
@@ -326,14 +304,16 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
             if (k == kEnd) return;
         }
     }
-    if (warp >= 1 + kData / 32 && warp < 1 + kData / 32 + (kJoin + 1) * (CB / 32)) {  // groupers
-        const int ch = tid - 32 - kData - kJoin * CB;
+    if (tid >= kFirstGrouper && tid < kFirstGrouper + LY::kJoiners) {  // groupers
+        const int ch = (tid - kFirstGrouper) * kJoinCh;
         for (unsigned i = 0;; ++i) {
             const int s = (int)(i % S);
             if (!wait(mapped(s), (i / S) & 1u)) return;
             const unsigned k = tile_of_stage[s];
             if (k == kEnd) return;
-            const float2 m = total[s][ch];
+            float2 m[kJoinCh];
+#pragma unroll
+            for (int q = 0; q < kJoinCh; ++q) m[q] = total[s][ch + q];
             __syncwarp();
             if ((tid & 31) == 0) mbar_arrive(empty(s));
             place(k, n, row, b, hd);
@@ -349,8 +329,7 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
     for (unsigned i = 0;; ++i) {
         const int s = (int)(i % S);
         const uint32_t phase = (i / S) & 1u;
-        if (!mapper && !wait(joined(s), phase)) return;
-        if (!wait(full(s), phase)) return;
+        if (!wait(mapper ? known(s) : joined(s), phase)) return;
         const unsigned k = tile_of_stage[s];
         if (k == kEnd) {
             if (!mapper) return;
@@ -361,6 +340,16 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
         place(k, n, row, b, hd);
         const int t0 = n * TILE + run * kTok;
         const int nt = nc > 0 ? min(kTok, p.T - t0) : 0;
+        unsigned resets = 0;  // asked for while the tile is loaded
+        if (p.reset) {
+            if (mapper) {
+                resets = run_resets<LANES>(p.reset + (long long)b * p.T, t0, p.T);
+                if (lane == 0) reset_bits[s][run] = resets;
+            } else {
+                resets = reset_bits[s][run];
+            }
+        }
+        if (!wait(full(s), phase)) return;
         const T* xs = sx(s) + run * kTok * p.d + c;
         const T* gs = sg(s) + run * kTok * p.d + c;
         const T* gp = static_cast<const T*>(p.g) + b * p.sg[0] + hd * p.sg[1] + t0 * p.sg[2];
@@ -382,35 +371,28 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
             }
         };
         if (mapper) {
-            unsigned resets = 0;
-            if (p.reset) {
-                const unsigned char* rp = p.reset + (long long)b * p.T + t0;
-#pragma unroll
-                for (int i2 = 0; i2 < kTok; ++i2)
-                    if (i2 < min(kTok, p.T - t0) && rp[i2]) resets |= 1u << i2;
-                if (lane == 0) reset_bits[s][run] = resets;
-            }
             float A[kCh], X[kCh];
 #pragma unroll
             for (int j = 0; j < kCh; ++j) { A[j] = 1.f; X[j] = 0.f; }
-            auto walk = [&](auto plain) {  // plain: a whole run without resets
+            auto walk = [&](auto whole, auto clean) {  // a whole run; one without resets
 #pragma unroll
                 for (int i2 = 0; i2 < kTok; ++i2)
-                    if (plain || i2 < nt) {
+                    if (whole || i2 < nt) {
                         float xv[kCh], ga[NG];
                         four(xs + i2 * p.d, xv);
                         gates(i2, ga);
 #pragma unroll
                         for (int j = 0; j < kCh; ++j) {
                             const float z = ga[SHARED ? 0 : j];
-                            if (!plain && ((resets >> i2) & 1u)) X[j] = 0.f;
+                            if (!clean && ((resets >> i2) & 1u)) X[j] = 0.f;
                             X[j] = SIG ? fmaf(z, xv[j] - X[j], X[j]) : fmaf(z, X[j], xv[j]);
                             A[j] = SIG ? fmaf(-z, A[j], A[j]) : z * A[j];
                         }
                     }
             };
-            if (nt == kTok && resets == 0) walk(std::true_type{});
-            else walk(std::false_type{});
+            if (nt == kTok && resets == 0) walk(std::true_type{}, std::true_type{});
+            else if (nt == kTok) walk(std::true_type{}, std::false_type{});
+            else walk(std::false_type{}, std::false_type{});
             float4* m4 = reinterpret_cast<float4*>(maps(s) + run * CB + c);
 #pragma unroll
             for (int j = 0; j < kCh; ++j) A[j] = resets ? cut() : A[j] + 0.f;
@@ -429,23 +411,22 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
                 if ((tid & 31) == 0) mbar_arrive(mapped(s));
             }
         } else {
-            const unsigned resets = p.reset ? reset_bits[s][run] : 0u;
             float h[kCh];
             const float4* m4 = reinterpret_cast<const float4*>(maps(s) + run * CB + c);
             const float4 lo = m4[0], hi = m4[1];
             h[0] = lo.x; h[1] = lo.z; h[2] = hi.x; h[3] = hi.z;
             const long long off = b * p.so[0] + hd * p.so[1] + t0 * p.so[2] + c;
-            auto walk = [&](auto plain, auto* o) {
+            auto walk = [&](auto whole, auto clean, auto* o) {
 #pragma unroll
                 for (int i2 = 0; i2 < kTok; ++i2)
-                    if (plain || i2 < nt) {
+                    if (whole || i2 < nt) {
                         float xv[kCh], ga[NG];
                         four(xs + i2 * p.d, xv);
                         gates(i2, ga);
 #pragma unroll
                         for (int j = 0; j < kCh; ++j) {
                             const float z = ga[SHARED ? 0 : j];
-                            if (!plain && ((resets >> i2) & 1u)) h[j] = 0.f;
+                            if (!clean && ((resets >> i2) & 1u)) h[j] = 0.f;
                             h[j] = SIG ? fmaf(z, xv[j] - h[j], h[j]) : fmaf(z, h[j], xv[j]);
                         }
                         Lane<std::remove_pointer_t<decltype(o)>, kCh, true> ov;
@@ -453,39 +434,19 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
                         ov.store(o + off + i2 * p.so[2], nc);
                     }
             };
-            if (nt == kTok && resets == 0) {
-                if (p.out_bf16) walk(std::true_type{}, static_cast<bf16*>(p.o));
-                else walk(std::true_type{}, static_cast<float*>(p.o));
-            } else if (nt > 0) {
-                if (p.out_bf16) walk(std::false_type{}, static_cast<bf16*>(p.o));
-                else walk(std::false_type{}, static_cast<float*>(p.o));
-            }
+            auto go = [&](auto* o) {
+                if (nt == kTok && resets == 0) walk(std::true_type{}, std::true_type{}, o);
+                else if (nt == kTok) walk(std::true_type{}, std::false_type{}, o);
+                else walk(std::false_type{}, std::false_type{}, o);
+            };
+            if (p.out_bf16) go(static_cast<bf16*>(p.o));
+            else go(static_cast<float*>(p.o));
             __syncwarp();
             if ((tid & 31) == 0) mbar_arrive(empty(s));
             if (p.state_out && nt > 0 && t0 + nt == p.T)
                 *reinterpret_cast<float4*>(p.state_out + (long long)row * p.d + c) = make_float4(h[0], h[1], h[2], h[3]);
         }
     }
-}
-
-// A map of a strided [B][H][T][d] tensor, box of TILE tokens; false where its
-// strides or address do not allow bulk tensor copies.
-bool gate_map(CUtensorMap* m, const void* base, int es, const long long (&s)[3], int B, int H, int T, int d, int tile) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn || (reinterpret_cast<uintptr_t>(base) & 15u) || (d * es) % 16) return false;
-    const int sizes[3] = {T, H, B};
-    const long long st[3] = {s[2], s[1], s[0]};
-    cuuint64_t strides[3];
-    for (int i = 0; i < 3; ++i) {
-        strides[i] = (cuuint64_t)(sizes[i] == 1 ? (long long)d * es : st[i] * es);  // a single index needs none
-        if (sizes[i] > 1 && (st[i] <= 0 || (st[i] * es) % 16 || st[i] * es >= (1LL << 40))) return false;
-    }
-    const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)T, (cuuint64_t)H, (cuuint64_t)B};
-    const cuuint32_t box[4] = {(cuuint32_t)d, (cuuint32_t)tile, 1, 1}, step[4] = {1, 1, 1, 1};
-    return fn(m, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4,
-              const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
-           CUDA_SUCCESS;
 }
 
 // One token: a read and a write of the state and of the token's n d values are

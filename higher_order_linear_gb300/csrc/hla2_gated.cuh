@@ -146,43 +146,63 @@ __device__ __forceinline__ void publish_tile(const GateParams& p, const Lookback
     if (n + 1 < lb.tiles) st_pair(p.words + lb.tile_map(row, n) + ch, m);
 }
 
-// Publishes one channel of the map of the group that tile n ends, if it ends one.
-__device__ __forceinline__ void publish_group(const GateParams& p, const Lookback& lb, int row, int n, int ch, float2 m) {
-    if (kSuper == 1 || n % kGroup != kGroup - 1 || n + 1 == lb.tiles) return;
-    u64 w[kGroup - 1];
+// The rest is done for N channels by one thread (ch, ch + 1, ..): what it needs of
+// each is asked for before any is waited for.
+
+// Publishes the map of the group that tile n, of map `m`, ends, if it ends one.
+template <int N>
+__device__ __forceinline__ void publish_group(const GateParams& p, const Lookback& lb, int row, int n, int ch,
+                                              const float2 (&m)[N]) {
+    if (n % kGroup != kGroup - 1 || n + 1 == lb.tiles) return;
+    u64 w[N][kGroup - 1];
     const u64* const tiles = p.words + lb.tile_map(row, n - (kGroup - 1)) + ch;
-    ask_words(tiles, lb.cb, kGroup - 1, w);
-    wait_words(p, tiles, lb.cb, w);
-    float2 all = as_pair(w[0]);
 #pragma unroll
-    for (int i = 1; i < kGroup - 1; ++i) all = then(all, as_pair(w[i]));
-    st_pair(p.words + lb.group_map(row, n / kGroup) + ch, then(all, m));
+    for (int q = 0; q < N; ++q) ask_words(tiles + q, lb.cb, kGroup - 1, w[q]);
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+        wait_words(p, tiles + q, lb.cb, w[q]);
+        float2 all = as_pair(w[q][0]);
+#pragma unroll
+        for (int i = 1; i < kGroup - 1; ++i) all = then(all, as_pair(w[q][i]));
+        st_pair(p.words + lb.group_map(row, n / kGroup) + ch + q, then(all, m[q]));
+    }
 }
 
-// The state that enters the tile, for one channel.  `start`: the state that enters
-// the sequence.
-__device__ __forceinline__ float enter_tile(const GateParams& p, const Lookback& lb, int row, int n, int ch,
-                                            float start) {
+// h: in, the state that enters the sequence; out, the state that enters tile n.
+template <int N>
+__device__ __forceinline__ void enter_tile(const GateParams& p, const Lookback& lb, int row, int n, int ch,
+                                           float (&h)[N]) {
     const int g = n / kGroup, s = g / kSuper;
     const int nt = n % kGroup, ng = g % kSuper;  // tiles before this one in its group, groups before it in the super-group
-    u64 w[kGroup - 1], v[kSuper > 1 ? kSuper - 1 : 1], u[1];
+    u64 w[N][kGroup - 1], v[N][kSuper - 1], u[N][1];
     const u64* const state = p.words + lb.super_state(row, s) + ch;
     const u64* const groups = p.words + lb.group_map(row, g - ng) + ch;
     const u64* const tiles = p.words + lb.tile_map(row, n - nt) + ch;
-    ask_words(state, 0, s > 0 ? 1 : 0, u);
-    ask_words(groups, lb.cb, ng, v);
-    ask_words(tiles, lb.cb, nt, w);
-    wait_words(p, state, 0, u);
-    wait_words(p, groups, lb.cb, v);
-    wait_words(p, tiles, lb.cb, w);
-    float h = s > 0 ? as_pair(u[0]).x : start;
 #pragma unroll
-    for (int i = 0; i < kSuper - 1; ++i)
-        if (i < ng) h = pass(as_pair(v[i]), h);
+    for (int q = 0; q < N; ++q) ask_words(state + q, 0, s > 0 ? 1 : 0, u[q]);
 #pragma unroll
-    for (int i = 0; i < kGroup - 1; ++i)
-        if (i < nt) h = pass(as_pair(w[i]), h);
-    return h;
+    for (int q = 0; q < N; ++q) ask_words(groups + q, lb.cb, ng, v[q]);
+#pragma unroll
+    for (int q = 0; q < N; ++q) ask_words(tiles + q, lb.cb, nt, w[q]);
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+        wait_words(p, state + q, 0, u[q]);
+        if (s > 0) h[q] = as_pair(u[q][0]).x;
+    }
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+        wait_words(p, groups + q, lb.cb, v[q]);
+#pragma unroll
+        for (int i = 0; i < kSuper - 1; ++i)
+            if (i < ng) h[q] = pass(as_pair(v[q][i]), h[q]);
+    }
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+        wait_words(p, tiles + q, lb.cb, w[q]);
+#pragma unroll
+        for (int i = 0; i < kGroup - 1; ++i)
+            if (i < nt) h[q] = pass(as_pair(w[q][i]), h[q]);
+    }
 }
 
 // Publishes the state `h` after tile n where the tile ends a super-group.
@@ -190,6 +210,18 @@ __device__ __forceinline__ void publish_state(const GateParams& p, const Lookbac
     constexpr int kLong = kGroup * kSuper;
     if (n % kLong == kLong - 1 && n + 1 < lb.tiles)
         st_pair(p.words + lb.super_state(row, n / kLong + 1) + ch, make_float2(h, 0.f));
+}
+
+// One channel's part in the register kernels: publishes the tile's map, returns the state that enters it.
+__device__ __forceinline__ float join_tile(const GateParams& p, const Lookback& lb, int row, int n, int ch, float2 m,
+                                           float start) {
+    publish_tile(p, lb, row, n, ch, m);
+    const float2 one[1] = {m};
+    publish_group(p, lb, row, n, ch, one);
+    float h[1] = {start};
+    enter_tile(p, lb, row, n, ch, h);
+    publish_state(p, lb, row, n, ch, pass(m, h[0]));
+    return h[0];
 }
 
 // The tiles of a block, by ticket where tiles wait for one another.  The
@@ -231,6 +263,58 @@ struct Run {
     }
     __device__ __forceinline__ bool reset(int i) const { return (resets >> i) & 1u; }
 };
+
+// ---- the pipelined kernels ---------------------------------------------------
+constexpr int kJoin = 2;    // sets of joiners, every kJoin-th tile each
+constexpr int kJoinCh = 1;  // channels of a joiner's thread
+constexpr int kAhead = 1;   // tickets taken ahead, their tiles on the way to L2
+
+// Like mbar_try, but the thread may sleep for up to 2 us in one try: the waiting
+// warps' own instructions took a third of the issue slots without it.
+__device__ __forceinline__ bool mbar_try_long(uint32_t a, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(a), "r"(parity), "r"(2000u)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t a) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(a) : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t mbar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(mbar)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_prefetch_l2_4d(const CUtensorMap* map, int x, int y, int z, int w) {
+    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global [%0, {%1, %2, %3, %4}];"
+                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w)
+                 : "memory");
+}
+
+// The resets of a run of kTok tokens from t0 on, as bits, for the LANES lanes of a
+// warp that share the run: each of the first kTok loads one byte.
+template <int LANES>
+__device__ __forceinline__ unsigned run_resets(const unsigned char* rp, int t0, int T) {
+    const int lane = threadIdx.x & 31, i = lane % LANES;
+    const bool r = i < kTok && t0 + i < T && rp[t0 + i];
+    return (__ballot_sync(0xffffffffu, r) >> (lane - i)) & ((1u << kTok) - 1u);
+}
+
+// four channels of one token in shared memory, as fp32
+__device__ __forceinline__ void four(const float* p, float (&v)[4]) {
+    const float4 a = *reinterpret_cast<const float4*>(p);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+}
+__device__ __forceinline__ void four(const bf16* p, float (&v)[4]) {
+    const uint2 a = *reinterpret_cast<const uint2*>(p);
+    v[0] = __uint_as_float(a.x << 16); v[1] = __uint_as_float(a.x & 0xffff0000u);
+    v[2] = __uint_as_float(a.y << 16); v[3] = __uint_as_float(a.y & 0xffff0000u);
+}
 
 // ------------------------------------------------------------ host side ----
 template <typename F>
@@ -319,6 +403,26 @@ cudaError_t by_lanes(int d, F&& f) {
 template <typename F>
 cudaError_t by_bool(bool v, F&& f) {
     return v ? f(std::true_type{}) : f(std::false_type{});
+}
+
+// A map of a strided [B][H][T][d] tensor, box of TILE tokens; false where its
+// strides or address do not allow bulk tensor copies.
+bool gate_map(CUtensorMap* m, const void* base, int es, const long long (&s)[3], int B, int H, int T, int d, int tile) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn || (reinterpret_cast<uintptr_t>(base) & 15u) || (d * es) % 16) return false;
+    const int sizes[3] = {T, H, B};
+    const long long st[3] = {s[2], s[1], s[0]};
+    cuuint64_t strides[3];
+    for (int i = 0; i < 3; ++i) {
+        strides[i] = (cuuint64_t)(sizes[i] == 1 ? (long long)d * es : st[i] * es);  // a single index needs none
+        if (sizes[i] > 1 && (st[i] <= 0 || (st[i] * es) % 16 || st[i] * es >= (1LL << 40))) return false;
+    }
+    const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)T, (cuuint64_t)H, (cuuint64_t)B};
+    const cuuint32_t box[4] = {(cuuint32_t)d, (cuuint32_t)tile, 1, 1}, step[4] = {1, 1, 1, 1};
+    return fn(m, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4,
+              const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
 }
 
 }  // namespace

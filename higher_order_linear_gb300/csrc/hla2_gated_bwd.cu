@@ -41,20 +41,13 @@ gated_scan_bwd_kernel(const GateParams p) {
                 back[r][ch] = m;
                 m = then(m, f);
             }
-            if (p.words) {
-                publish_tile(p, lb, row, n, ch, m);
-                publish_group(p, lb, row, n, ch, m);
-            }
 #pragma unroll 8
             for (int r = 0; r < RUNS; ++r) {
                 const float2 f = fwd[r][ch];
                 fwd[r][ch].x = h;
                 h = pass(f, h);
             }
-            if (p.words) {
-                mu = enter_tile(p, lb, row, n, ch, mu);
-                publish_state(p, lb, row, n, ch, pass(m, mu));
-            }
+            if (p.words) mu = join_tile(p, lb, row, n, ch, m, mu);
             entering[ch] = mu;
             __syncthreads();
             k = slot;
@@ -179,6 +172,379 @@ gated_scan_bwd_kernel(const GateParams p) {
     }
 }
 
+
+// ---- the pipelined gradient (16-bit x and gates) --------------------------------
+// The forward's pipeline (hla2_gated.cu) over tiles of x, gates and dh.  A run's
+// entry is (A, X, Y); the joiners wait for the mu behind the tile and read the
+// kept state that enters it, and leave in X and Y what enters each run from
+// either side.  A writer's thread walks its run forwards, leaving h_{t-1} in
+// shared memory and the gates in registers, and then backwards.
+template <typename TO, bool SHARED, int LANES>
+struct BackLayout {
+    static constexpr int CB = LANES * kCh, RUNS = kData / LANES, TILE = RUNS * kTok;
+    static constexpr uint32_t kTileBytes = TILE * CB * 2, kUpBytes = TILE * CB * sizeof(TO);
+    static constexpr uint32_t kPlane = RUNS * CB * 4;  // of A, of X, of Y
+    static constexpr uint32_t kStage = kTileBytes * (SHARED ? 1 : 2) + kUpBytes + 3 * kPlane;
+    static constexpr uint32_t kBefore = kTok * kData * 16;
+    static constexpr int kFit = (int)((222 * 1024 - kBefore) / kStage);
+    static constexpr int kStages = kFit > 6 ? 6 : kFit;
+    static constexpr uint32_t kBytes = kStage * kStages + kBefore + 128;
+    static constexpr int kJoiners = CB / kJoinCh;
+    static constexpr int kThreads = 32 + kData + (kJoin + 1) * kJoiners + kData;
+};
+
+template <typename TO, bool SIG, bool SHARED, int LANES>
+__global__ void __launch_bounds__(BackLayout<TO, SHARED, LANES>::kThreads, 1)
+gated_pipe_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mg,
+                      const __grid_constant__ CUtensorMap mu_, const GateParams p) {
+    using T = bf16;
+    using LY = BackLayout<TO, SHARED, LANES>;
+    constexpr int CB = LY::CB, RUNS = LY::RUNS, TILE = LY::TILE, S = LY::kStages, NG = SHARED ? 1 : kCh;
+    constexpr unsigned kEnd = 0xffffffffu;
+    extern __shared__ __align__(128) unsigned char raw[];
+    __shared__ __align__(8) unsigned long long bars[6 * S];
+    static_assert(S >= kJoin, "the ends of the tickets take a stage for each group of joiners");
+    __shared__ unsigned tile_of_stage[S], reset_bits[S][RUNS];
+    __shared__ float2 total[S][CB];
+    __shared__ volatile int abort_flag;
+    unsigned char* const base = raw + ((128u - (smem_u32(raw) & 127u)) & 127u);
+    float4* const before = reinterpret_cast<float4*>(base + (size_t)LY::kStage * S);  // [kTok][kData]: h_{t-1}
+    const int tid = threadIdx.x, warp = tid >> 5;
+    auto full = [&](int s) { return smem_u32(&bars[s]); };
+    auto mapped = [&](int s) { return smem_u32(&bars[S + s]); };
+    auto joined = [&](int s) { return smem_u32(&bars[2 * S + s]); };
+    auto empty = [&](int s) { return smem_u32(&bars[3 * S + s]); };
+    auto runs = [&](int s) { return smem_u32(&bars[4 * S + s]); };
+    auto known = [&](int s) { return smem_u32(&bars[5 * S + s]); };
+    auto stage = [&](int s) { return base + (size_t)s * LY::kStage; };
+    constexpr uint32_t kG = LY::kTileBytes, kUp = kG * (SHARED ? 1 : 2), kMapA = kUp + LY::kUpBytes;
+    auto plane = [&](int s, int which) { return reinterpret_cast<float*>(stage(s) + kMapA + which * LY::kPlane); };
+    if (tid == 0) {
+        abort_flag = 0;
+        for (int s = 0; s < S; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(mapped(s), CB / 32);
+            mbar_init(joined(s), LY::kJoiners / 32);
+            mbar_init(empty(s), kData / 32 + LY::kJoiners / 32);
+            mbar_init(runs(s), kData / 32);
+            mbar_init(known(s), 1);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+        if (abort_flag) return false;
+        if (mbar_try(bar, parity)) return true;
+        const unsigned long long t0 = globaltimer();
+        while (!mbar_try_long(bar, parity)) {
+            if (abort_flag) return false;
+            if (globaltimer() - t0 > 2 * kGateWaitNs) {  // longer than the joiners' own waits
+                abort_flag = 1;
+                atomicExch(p.status, (int)kDevWaitTimeout);
+                return false;
+            }
+        }
+        return true;
+    };
+    const int rows = p.B * p.H;
+    const Lookback lb(rows, p.tiles, CB);
+    auto place = [&](unsigned k, int& n, int& row, int& b, int& hd) {
+        n = (int)(k / (unsigned)rows);
+        row = (int)(k - (unsigned)n * (unsigned)rows);
+        b = row / p.H;
+        hd = row - b * p.H;
+    };
+    int n, row, b, hd;
+
+    if (warp == 0) {  // loader
+        if (tid != 0) return;
+        Tickets tickets{reinterpret_cast<unsigned*>(p.words), nullptr};
+        LoadLedger<S> loads(full(0));
+        unsigned ahead[kAhead + 1];
+        auto take = [&](unsigned last, bool first) -> unsigned {
+            const unsigned k = first && !p.words ? blockIdx.x : tickets.take(last);
+            if (kAhead > 0 && k < p.total) {
+                place(k, n, row, b, hd);
+                const int t = (p.tiles - 1 - n) * TILE;
+                tma_prefetch_l2_4d(&mx, 0, t, hd, b);
+                if (!SHARED) tma_prefetch_l2_4d(&mg, 0, t, hd, b);
+                tma_prefetch_l2_4d(&mu_, 0, t, hd, b);
+            }
+            return k;
+        };
+#pragma unroll
+        for (int i = 0; i <= kAhead; ++i) ahead[i] = take(i > 0 ? ahead[i > 0 ? i - 1 : 0] : 0u, i == 0);
+        int ends = 0;
+        for (unsigned i = 0; ends < kJoin; ++i) {
+            const int s = (int)(i % S);
+            const unsigned k = ahead[0];
+            if (!wait(empty(s), ((i / S) & 1u) ^ 1u)) break;
+            if (k >= p.total) {  // one end to each group of joiners
+                tile_of_stage[s] = kEnd;
+                mbar_arrive(known(s));
+                mbar_arrive(full(s));
+                ++ends;
+                continue;
+            }
+            tile_of_stage[s] = k;
+            mbar_arrive(known(s));
+            place(k, n, row, b, hd);
+            const int t = (p.tiles - 1 - n) * TILE;
+            loads.note(s);
+            mbar_expect_tx(full(s), (uint32_t)(TILE * p.d) * (2u * (SHARED ? 1u : 2u) + (uint32_t)sizeof(TO)));
+            tma_load_4d(smem_u32(stage(s)), &mx, 0, t, hd, b, full(s));
+            if (!SHARED) tma_load_4d(smem_u32(stage(s) + kG), &mg, 0, t, hd, b, full(s));
+            tma_load_4d(smem_u32(stage(s) + kUp), &mu_, 0, t, hd, b, full(s));
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) ahead[j] = ahead[j + 1];
+            ahead[kAhead] = take(ahead[kAhead], false);
+        }
+        if (abort_flag && !loads.settle()) atomicExch(p.status, (int)kDevWaitTimeout);
+        return;
+    }
+    constexpr int kFirstJoiner = 32 + kData, kFirstGrouper = kFirstJoiner + kJoin * LY::kJoiners;
+    if (tid >= kFirstJoiner && tid < kFirstGrouper) {  // joiners
+        const int j = (tid - kFirstJoiner) / LY::kJoiners;
+        const int ch = (tid - kFirstJoiner - j * LY::kJoiners) * kJoinCh;
+        for (unsigned i = (unsigned)j;; i += kJoin) {
+            const int s = (int)(i % S);
+            if (!wait(known(s), (i / S) & 1u)) return;
+            const unsigned k = tile_of_stage[s];
+            if (k != kEnd) {
+                place(k, n, row, b, hd);
+                float mu[kJoinCh], h[kJoinCh];
+#pragma unroll
+                for (int q = 0; q < kJoinCh; ++q) {
+                    const bool in = ch + q < p.d;
+                    mu[q] = p.dstate_out && in ? p.dstate_out[(long long)row * p.d + ch + q] : 0.f;
+                    h[q] = in ? p.carry[((long long)row * p.tiles + (p.tiles - 1 - n)) * p.d + ch + q] : 0.f;
+                }
+                if (p.words) enter_tile(p, lb, row, n, ch, mu);  // while the tile is loaded and mapped
+                if (!wait(mapped(s), (i / S) & 1u)) return;
+#pragma unroll
+                for (int q = 0; q < kJoinCh; ++q) {
+                    if (p.words) publish_state(p, lb, row, n, ch + q, pass(total[s][ch + q], mu[q]));
+                    const float* A = plane(s, 0) + ch + q;
+                    float *X = plane(s, 1) + ch + q, *Y = plane(s, 2) + ch + q;
+#pragma unroll
+                    for (int r = 0; r < RUNS; ++r) {
+                        const float2 f = make_float2(A[r * CB], X[r * CB]);
+                        X[r * CB] = h[q];
+                        h[q] = pass(f, h[q]);
+                    }
+#pragma unroll
+                    for (int r = RUNS - 1; r >= 0; --r) {
+                        const float2 f = make_float2(A[r * CB], Y[r * CB]);
+                        Y[r * CB] = mu[q];
+                        mu[q] = pass(f, mu[q]);
+                    }
+                }
+            }
+            __syncwarp();
+            if ((tid & 31) == 0) mbar_arrive(joined(s));
+            if (k == kEnd) return;
+        }
+    }
+    if (tid >= kFirstGrouper && tid < kFirstGrouper + LY::kJoiners) {  // groupers
+        const int ch = (tid - kFirstGrouper) * kJoinCh;
+        for (unsigned i = 0;; ++i) {
+            const int s = (int)(i % S);
+            if (!wait(mapped(s), (i / S) & 1u)) return;
+            const unsigned k = tile_of_stage[s];
+            if (k == kEnd) return;
+            float2 m[kJoinCh];
+#pragma unroll
+            for (int q = 0; q < kJoinCh; ++q) m[q] = total[s][ch + q];
+            __syncwarp();
+            if ((tid & 31) == 0) mbar_arrive(empty(s));
+            place(k, n, row, b, hd);
+            if (p.words) publish_group(p, lb, row, n, ch, m);
+        }
+    }
+    const bool mapper = warp < 1 + kData / 32;
+    const int at = mapper ? tid - 32 : tid - (LY::kThreads - kData);
+    const int lane = at % LANES, run = at / LANES;
+    const int c = lane * kCh, nc = p.d - c;
+    int ends = 0;
+    for (unsigned i = 0;; ++i) {
+        const int s = (int)(i % S);
+        const uint32_t phase = (i / S) & 1u;
+        if (!wait(mapper ? known(s) : joined(s), phase)) return;
+        const unsigned k = tile_of_stage[s];
+        if (k == kEnd) {
+            if (!mapper) return;
+            if (at < CB && (tid & 31) == 0) mbar_arrive(mapped(s));
+            if (++ends == kJoin) return;
+            continue;
+        }
+        place(k, n, row, b, hd);
+        const int t0 = (p.tiles - 1 - n) * TILE + run * kTok;
+        const int nt = nc > 0 ? min(kTok, p.T - t0) : 0;
+        unsigned resets = 0;  // asked for while the tile is loaded
+        if (p.reset) {
+            if (mapper) {
+                resets = run_resets<LANES>(p.reset + (long long)b * p.T, t0, p.T);
+                if (lane == 0) reset_bits[s][run] = resets;
+            } else {
+                resets = reset_bits[s][run];
+            }
+        }
+        if (!wait(full(s), phase)) return;
+        const T* xs = reinterpret_cast<const T*>(stage(s)) + run * kTok * p.d + c;
+        const T* gs = reinterpret_cast<const T*>(stage(s) + kG) + run * kTok * p.d + c;
+        const TO* us = reinterpret_cast<const TO*>(stage(s) + kUp) + run * kTok * p.d + c;
+        const T* gp = static_cast<const T*>(p.g) + b * p.sg[0] + hd * p.sg[1] + t0 * p.sg[2];
+        float gl[SHARED ? kTok : 1];
+        if (SHARED) {
+#pragma unroll
+            for (int i2 = 0; i2 < kTok; ++i2)
+                if (i2 < nt) gl[i2] = to_f32(gp[i2 * p.sg[2]]);
+        }
+        auto gates = [&](int i2, float (&ga)[NG]) {
+            if constexpr (SHARED) {
+                ga[0] = SIG ? keep_out(gl[i2]) : gl[i2];
+            } else {
+                four(gs + i2 * p.d, ga);
+                if (SIG) {
+#pragma unroll
+                    for (int j = 0; j < kCh; ++j) ga[j] = keep_out(ga[j]);
+                }
+            }
+        };
+        if (mapper) {
+            // (A, X) forwards; Y = sum over the run of dh_t times the decays a_t .. of its beginning
+            float A[kCh], X[kCh], Y[kCh];
+#pragma unroll
+            for (int j = 0; j < kCh; ++j) { A[j] = 1.f; X[j] = 0.f; Y[j] = 0.f; }
+            auto walk = [&](auto whole, auto clean) {  // a whole run; one without resets
+                bool open = true;  // no reset so far
+#pragma unroll
+                for (int i2 = 0; i2 < kTok; ++i2)
+                    if (whole || i2 < nt) {
+                        float xv[kCh], uv[kCh], ga[NG];
+                        four(xs + i2 * p.d, xv);
+                        four(us + i2 * p.d, uv);
+                        gates(i2, ga);
+                        if (!clean && ((resets >> i2) & 1u)) open = false;
+#pragma unroll
+                        for (int j = 0; j < kCh; ++j) {
+                            const float z = ga[SHARED ? 0 : j];
+                            if (!clean && ((resets >> i2) & 1u)) X[j] = 0.f;
+                            X[j] = SIG ? fmaf(z, xv[j] - X[j], X[j]) : fmaf(z, X[j], xv[j]);
+                            A[j] = SIG ? fmaf(-z, A[j], A[j]) : z * A[j];
+                            if (clean || open) Y[j] = fmaf(A[j], uv[j], Y[j]);
+                        }
+                    }
+            };
+            if (nt == kTok && resets == 0) walk(std::true_type{}, std::true_type{});
+            else if (nt == kTok) walk(std::true_type{}, std::false_type{});
+            else walk(std::false_type{}, std::false_type{});
+            const int o = run * CB + c;
+            if (resets) {
+#pragma unroll
+                for (int j = 0; j < kCh; ++j) A[j] = cut();
+            } else {
+#pragma unroll
+                for (int j = 0; j < kCh; ++j) A[j] += 0.f;
+            }
+            *reinterpret_cast<float4*>(plane(s, 0) + o) = make_float4(A[0], A[1], A[2], A[3]);
+            *reinterpret_cast<float4*>(plane(s, 1) + o) = make_float4(X[0], X[1], X[2], X[3]);
+            *reinterpret_cast<float4*>(plane(s, 2) + o) = make_float4(Y[0], Y[1], Y[2], Y[3]);
+            __syncwarp();
+            if ((tid & 31) == 0) mbar_arrive(runs(s));
+            if (at < CB) {  // one channel of the tile's map of mu, from its last run to its first
+                if (!wait(runs(s), phase)) return;
+                const float *pA = plane(s, 0) + at, *pY = plane(s, 2) + at;
+                float2 m = make_float2(pA[(RUNS - 1) * CB], pY[(RUNS - 1) * CB]);
+#pragma unroll
+                for (int r = RUNS - 2; r >= 0; --r) m = then(m, make_float2(pA[r * CB], pY[r * CB]));
+                if (p.words) publish_tile(p, lb, row, n, at, m);
+                total[s][at] = m;
+                __syncwarp();
+                if ((tid & 31) == 0) mbar_arrive(mapped(s));
+            }
+        } else {
+            float h[kCh], mu[kCh];
+            four(plane(s, 1) + run * CB + c, h);
+            four(plane(s, 2) + run * CB + c, mu);
+            T* const dxp = static_cast<T*>(p.dx) + b * p.sdx[0] + hd * p.sdx[1] + t0 * p.sdx[2] + c;
+            T* const dgp = static_cast<T*>(p.dg) + b * p.sdg[0] + hd * p.sdg[1] + t0 * p.sdg[2] + (SHARED ? 0 : c);
+            auto walk = [&](auto whole, auto clean) {
+                float z[kTok][NG];
+#pragma unroll
+                for (int i2 = 0; i2 < kTok; ++i2)
+                    if (whole || i2 < nt) {
+                        float xv[kCh];
+                        four(xs + i2 * p.d, xv);
+                        gates(i2, z[i2]);
+                        if (!clean && ((resets >> i2) & 1u)) {
+#pragma unroll
+                            for (int j = 0; j < kCh; ++j) h[j] = 0.f;
+                        }
+                        before[i2 * kData + at] = make_float4(h[0], h[1], h[2], h[3]);
+#pragma unroll
+                        for (int j = 0; j < kCh; ++j) {
+                            const float ga = z[i2][SHARED ? 0 : j];
+                            h[j] = SIG ? fmaf(ga, xv[j] - h[j], h[j]) : fmaf(ga, h[j], xv[j]);
+                        }
+                    }
+#pragma unroll
+                for (int i2 = kTok - 1; i2 >= 0; --i2) {
+                    const bool live = whole || i2 < nt;
+                    float gx[kCh], gg[kCh];
+                    if (live) {
+                        float xv[kCh], uv[kCh];
+                        four(xs + i2 * p.d, xv);
+                        four(us + i2 * p.d, uv);
+                        const float4 hb4 = before[i2 * kData + at];
+                        const float hb[kCh] = {hb4.x, hb4.y, hb4.z, hb4.w};
+#pragma unroll
+                        for (int j = 0; j < kCh; ++j) {
+                            const float ga = z[i2][SHARED ? 0 : j], lam = uv[j] + mu[j];
+                            if (SIG) {
+                                gx[j] = ga * lam;
+                                mu[j] = fmaf(-ga, lam, lam);
+                                gg[j] = ga * mu[j] * (hb[j] - xv[j]);
+                            } else {
+                                gx[j] = lam;
+                                gg[j] = lam * hb[j];
+                                mu[j] = ga * lam;
+                            }
+                            if (!clean && ((resets >> i2) & 1u)) mu[j] = 0.f;
+                        }
+                        Lane<T, kCh, true> ov;
+                        ov.set(gx);
+                        ov.store(dxp + i2 * p.sdx[2], nc);
+                    }
+                    if constexpr (SHARED) {  // the sum over the token's channels
+                        float sum = 0.f;
+#pragma unroll
+                        for (int j = 0; j < kCh; ++j) sum += live ? gg[j] : 0.f;
+#pragma unroll
+                        for (int w = LANES / 2; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+                        if (live && lane == 0) dgp[i2 * p.sdg[2]] = from_f32<T>(sum);
+                    } else if (live) {
+                        Lane<T, kCh, true> ov;
+                        ov.set(gg);
+                        ov.store(dgp + i2 * p.sdg[2], nc);
+                    }
+                }
+            };
+            // the same path for a warp's lanes: a shared gate's gradient is summed over them
+            const bool whole = __all_sync(0xffffffffu, nt == kTok), clean = __all_sync(0xffffffffu, resets == 0);
+            if (whole && clean) walk(std::true_type{}, std::true_type{});
+            else if (whole) walk(std::true_type{}, std::false_type{});
+            else walk(std::false_type{}, std::false_type{});
+            __syncwarp();
+            if ((tid & 31) == 0) mbar_arrive(empty(s));
+            if (p.dstate_in && nt > 0 && t0 == 0) {
+#pragma unroll
+                for (int j = 0; j < kCh; ++j) p.dstate_in[(long long)row * p.d + c + j] = mu[j];
+            }
+        }
+    }
+}
+
 }  // namespace
 }  // namespace hla2
 
@@ -216,18 +582,40 @@ extern "C" int hla2_gated_scan_backward(const void* X, const void* G, const unsi
                      (gate_shared || (aligned_to(G, es, p.sg, 3, kCh * es) && aligned_to(dG, es, p.sdg, 3, kCh * es)));
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = begin_lookback(p, lanes * kCh, workspace, s);
+    CUtensorMap mx{}, mg{}, mu{};
+    const bool pipe = dtype == HLA2_DTYPE_BF16 && vec && gate_map(&mx, X, es, p.sx, B, H, T, d, tile) &&
+                      (gate_shared || gate_map(&mg, G, es, p.sg, B, H, T, d, tile)) &&
+                      gate_map(&mu, dO, os, p.sdo, B, H, T, d, tile);
     if (e == cudaSuccess) e = by_types(dtype, out_dtype, [&](auto tin, auto tout) {
         return by_form(form, gate_shared, [&](auto sig, auto shared) {
-            return by_lanes(d, [&](auto ln) { return by_bool(vec, [&](auto v) {
-                auto kernel = gated_scan_bwd_kernel<decltype(tin), decltype(tout), decltype(sig)::value,
-                                                    decltype(shared)::value, decltype(ln)::value, decltype(v)::value>;
-                constexpr int threads = block_threads(decltype(ln)::value);
-                constexpr size_t smem = (size_t)kTok * kData * sizeof(float4);
+            return by_lanes(d, [&](auto ln) {
+                using T_ = decltype(tin);
+                using TO = decltype(tout);
+                constexpr bool SIG = decltype(sig)::value, SHARED = decltype(shared)::value;
+                constexpr int LANES = decltype(ln)::value;
                 unsigned blocks = 0;
-                if (cudaError_t e2 = persistent_blocks(reinterpret_cast<const void*>(kernel), threads, smem, p.total, &blocks)) return e2;
-                kernel<<<blocks, threads, smem, s>>>(p);
-                return cudaGetLastError();
-            }); });
+                if constexpr (std::is_same<T_, bf16>::value) {
+                    if (pipe) {
+                        using LY = BackLayout<TO, SHARED, LANES>;
+                        auto kernel = gated_pipe_bwd_kernel<TO, SIG, SHARED, LANES>;
+                        if (cudaError_t e2 = persistent_blocks(reinterpret_cast<const void*>(kernel), LY::kThreads,
+                                                               LY::kBytes, p.total, &blocks)) return e2;
+                        kernel<<<blocks, LY::kThreads, LY::kBytes, s>>>(mx, mg, mu, p);
+                        return cudaGetLastError();
+                    }
+                }
+                // wide accesses only for fp32: 16-bit operands that allow them took the pipeline
+                return by_bool(vec && std::is_same<T_, float>::value, [&](auto v) {
+                    constexpr bool VEC = decltype(v)::value && std::is_same<T_, float>::value;
+                    constexpr int threads = block_threads(LANES);
+                    constexpr size_t smem = (size_t)kTok * kData * sizeof(float4);
+                    auto kernel = gated_scan_bwd_kernel<T_, TO, SIG, SHARED, LANES, VEC>;
+                    if (cudaError_t e2 = persistent_blocks(reinterpret_cast<const void*>(kernel), threads, smem,
+                                                           p.total, &blocks)) return e2;
+                    kernel<<<blocks, threads, smem, s>>>(p);
+                    return cudaGetLastError();
+                });
+            });
         });
     });
     note_launches(1);
