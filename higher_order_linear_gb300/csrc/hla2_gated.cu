@@ -166,11 +166,11 @@ __global__ void __launch_bounds__(PipeLayout<T, SHARED, LANES>::kThreads, 1)
 gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mg, const GateParams p) {
     using LY = PipeLayout<T, SHARED, LANES>;
     constexpr int CB = LY::CB, RUNS = LY::RUNS, TILE = LY::TILE, S = LY::kStages;
-    constexpr unsigned kEnd = 0xffffffffu;
     extern __shared__ __align__(128) unsigned char raw[];
     __shared__ __align__(8) unsigned long long bars[6 * S];
     static_assert(S >= kJoin, "the ends of the tickets take a stage for each group of joiners");
-    __shared__ unsigned tile_of_stage[S], reset_bits[S][RUNS];
+    __shared__ TileInfo info[S];
+    __shared__ unsigned reset_bits[S][RUNS];
     __shared__ float2 total[S][CB];
     __shared__ volatile int abort_flag;
     unsigned char* const base = raw + ((128u - (smem_u32(raw) & 127u)) & 127u);
@@ -221,10 +221,9 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
         b = row / p.H;
         hd = row - b * p.H;
     };
-    int n, row, b, hd;
-
     if (warp == 0) {  // loader
         if (tid != 0) return;
+        int n, row, b, hd;
         Tickets tickets{reinterpret_cast<unsigned*>(p.words), nullptr};
         LoadLedger<S> loads(full(0));
         // tickets taken ahead, their tiles on the way to L2
@@ -241,20 +240,22 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
 #pragma unroll
         for (int i = 0; i <= kAhead; ++i) ahead[i] = take(i > 0 ? ahead[i > 0 ? i - 1 : 0] : 0u, i == 0);
         int ends = 0;
-        for (unsigned i = 0; ends < kJoin; ++i) {
-            const int s = (int)(i % S);
+        for (Ring<S, 1> at(0); ends < kJoin; at.next()) {
+            const int s = at.s;
             const unsigned k = ahead[0];
-            if (!wait(empty(s), ((i / S) & 1u) ^ 1u)) break;
+            if (!wait(empty(s), at.phase ^ 1u)) break;
             if (k >= p.total) {  // one end to each group of joiners
-                tile_of_stage[s] = kEnd;
+                info[s].n = -1;
                 mbar_arrive(known(s));
                 mbar_arrive(full(s));
                 ++ends;
                 continue;
             }
-            tile_of_stage[s] = k;
-            mbar_arrive(known(s));
             place(k, n, row, b, hd);
+            const long long t = (long long)n * TILE;
+            info[s] = TileInfo{n, row, b, n * TILE, (long long)b * p.T, b * p.sg[0] + hd * p.sg[1] + t * p.sg[2],
+                               b * p.so[0] + hd * p.so[1] + t * p.so[2], 0};
+            mbar_arrive(known(s));
             loads.note(s);
             mbar_expect_tx(full(s), (uint32_t)(TILE * p.d * sizeof(T)) * (SHARED ? 1u : 2u));
             tma_load_4d(smem_u32(sx(s)), &mx, 0, n * TILE, hd, b, full(s));
@@ -270,23 +271,22 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
     if (tid >= kFirstJoiner && tid < kFirstGrouper) {  // joiners
         const int j = (tid - kFirstJoiner) / LY::kJoiners;
         const int ch = (tid - kFirstJoiner - j * LY::kJoiners) * kJoinCh;
-        for (unsigned i = (unsigned)j;; i += kJoin) {
-            const int s = (int)(i % S);
-            if (!wait(known(s), (i / S) & 1u)) return;
-            const unsigned k = tile_of_stage[s];
-            if (k != kEnd) {
-                place(k, n, row, b, hd);
+        for (Ring<S, kJoin> at(j);; at.next()) {
+            const int s = at.s;
+            if (!wait(known(s), at.phase)) return;
+            const int n = info[s].n, row = info[s].row;
+            if (n >= 0) {
                 float h[kJoinCh];
 #pragma unroll
                 for (int q = 0; q < kJoinCh; ++q)
                     h[q] = p.state_in && ch + q < p.d ? p.state_in[(long long)row * p.d + ch + q] : 0.f;
-                if (p.words) enter_tile(p, lb, row, n, ch, h);  // while the tile is loaded and mapped
+                const auto own = [&] { return wait(mapped(s), at.phase); };
+                if (!(p.words ? enter_tile(p, lb, row, n, ch, h, own) : own())) return;
                 if (p.carry) {
 #pragma unroll
                     for (int q = 0; q < kJoinCh; ++q)
                         if (ch + q < p.d) p.carry[((long long)row * p.tiles + n) * p.d + ch + q] = h[q];
                 }
-                if (!wait(mapped(s), (i / S) & 1u)) return;
 #pragma unroll
                 for (int q = 0; q < kJoinCh; ++q) {
                     if (p.words) publish_state(p, lb, row, n, ch + q, pass(total[s][ch + q], h[q]));
@@ -301,22 +301,21 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
             }
             __syncwarp();
             if ((tid & 31) == 0) mbar_arrive(joined(s));
-            if (k == kEnd) return;
+            if (n < 0) return;
         }
     }
     if (tid >= kFirstGrouper && tid < kFirstGrouper + LY::kJoiners) {  // groupers
         const int ch = (tid - kFirstGrouper) * kJoinCh;
-        for (unsigned i = 0;; ++i) {
-            const int s = (int)(i % S);
-            if (!wait(mapped(s), (i / S) & 1u)) return;
-            const unsigned k = tile_of_stage[s];
-            if (k == kEnd) return;
+        for (Ring<S, 1> at(0);; at.next()) {
+            const int s = at.s;
+            if (!wait(mapped(s), at.phase)) return;
+            const int n = info[s].n, row = info[s].row;
+            if (n < 0) return;
             float2 m[kJoinCh];
 #pragma unroll
             for (int q = 0; q < kJoinCh; ++q) m[q] = total[s][ch + q];
             __syncwarp();
             if ((tid & 31) == 0) mbar_arrive(empty(s));
-            place(k, n, row, b, hd);
             if (p.words) publish_group(p, lb, row, n, ch, m);
         }
     }
@@ -326,24 +325,23 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
     const int c = lane * kCh, nc = p.d - c;
     constexpr int NG = SHARED ? 1 : kCh;
     int ends = 0;
-    for (unsigned i = 0;; ++i) {
-        const int s = (int)(i % S);
-        const uint32_t phase = (i / S) & 1u;
+    for (Ring<S, 1> ring(0);; ring.next()) {
+        const int s = ring.s;
+        const uint32_t phase = ring.phase;
         if (!wait(mapper ? known(s) : joined(s), phase)) return;
-        const unsigned k = tile_of_stage[s];
-        if (k == kEnd) {
+        const int n = info[s].n;
+        if (n < 0) {
             if (!mapper) return;
             if (at < CB && (tid & 31) == 0) mbar_arrive(mapped(s));
             if (++ends == kJoin) return;
             continue;
         }
-        place(k, n, row, b, hd);
-        const int t0 = n * TILE + run * kTok;
+        const int t0 = info[s].t0 + run * kTok;
         const int nt = nc > 0 ? min(kTok, p.T - t0) : 0;
         unsigned resets = 0;  // asked for while the tile is loaded
         if (p.reset) {
             if (mapper) {
-                resets = run_resets<LANES>(p.reset + (long long)b * p.T, t0, p.T);
+                resets = run_resets<LANES>(p.reset + info[s].reset, t0, p.T);
                 if (lane == 0) reset_bits[s][run] = resets;
             } else {
                 resets = reset_bits[s][run];
@@ -352,7 +350,7 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
         if (!wait(full(s), phase)) return;
         const T* xs = sx(s) + run * kTok * p.d + c;
         const T* gs = sg(s) + run * kTok * p.d + c;
-        const T* gp = static_cast<const T*>(p.g) + b * p.sg[0] + hd * p.sg[1] + t0 * p.sg[2];
+        const T* gp = static_cast<const T*>(p.g) + info[s].g + run * kTok * p.sg[2];
         float gl[SHARED ? kTok : 1];
         if (SHARED) {
 #pragma unroll
@@ -405,7 +403,7 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
                 float2 m = maps(s)[at];
 #pragma unroll
                 for (int r = 1; r < RUNS; ++r) m = then(m, maps(s)[r * CB + at]);
-                if (p.words) publish_tile(p, lb, row, n, at, m);
+                if (p.words) publish_tile(p, lb, info[s].row, n, at, m);
                 total[s][at] = m;
                 __syncwarp();
                 if ((tid & 31) == 0) mbar_arrive(mapped(s));
@@ -415,7 +413,7 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
             const float4* m4 = reinterpret_cast<const float4*>(maps(s) + run * CB + c);
             const float4 lo = m4[0], hi = m4[1];
             h[0] = lo.x; h[1] = lo.z; h[2] = hi.x; h[3] = hi.z;
-            const long long off = b * p.so[0] + hd * p.so[1] + t0 * p.so[2] + c;
+            const long long off = info[s].o + run * kTok * p.so[2] + c;
             auto walk = [&](auto whole, auto clean, auto* o) {
 #pragma unroll
                 for (int i2 = 0; i2 < kTok; ++i2)
@@ -441,6 +439,7 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
             };
             if (p.out_bf16) go(static_cast<bf16*>(p.o));
             else go(static_cast<float*>(p.o));
+            const int row = info[s].row;
             __syncwarp();
             if ((tid & 31) == 0) mbar_arrive(empty(s));
             if (p.state_out && nt > 0 && t0 + nt == p.T)

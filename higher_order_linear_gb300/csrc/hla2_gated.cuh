@@ -169,9 +169,13 @@ __device__ __forceinline__ void publish_group(const GateParams& p, const Lookbac
 }
 
 // h: in, the state that enters the sequence; out, the state that enters tile n.
-template <int N>
-__device__ __forceinline__ void enter_tile(const GateParams& p, const Lookback& lb, int row, int n, int ch,
-                                           float (&h)[N]) {
+// `mapped()` is called between the first look at the words and the waiting for
+// those that are missing: it waits for the tile's own map (false: give up), by
+// which time the tiles before it have theirs too; polling from the start took
+// more of the L2's bandwidth than the data.
+template <int N, typename F>
+__device__ __forceinline__ bool enter_tile(const GateParams& p, const Lookback& lb, int row, int n, int ch,
+                                           float (&h)[N], F&& mapped) {
     const int g = n / kGroup, s = g / kSuper;
     const int nt = n % kGroup, ng = g % kSuper;  // tiles before this one in its group, groups before it in the super-group
     u64 w[N][kGroup - 1], v[N][kSuper - 1], u[N][1];
@@ -179,30 +183,26 @@ __device__ __forceinline__ void enter_tile(const GateParams& p, const Lookback& 
     const u64* const groups = p.words + lb.group_map(row, g - ng) + ch;
     const u64* const tiles = p.words + lb.tile_map(row, n - nt) + ch;
 #pragma unroll
-    for (int q = 0; q < N; ++q) ask_words(state + q, 0, s > 0 ? 1 : 0, u[q]);
-#pragma unroll
-    for (int q = 0; q < N; ++q) ask_words(groups + q, lb.cb, ng, v[q]);
-#pragma unroll
-    for (int q = 0; q < N; ++q) ask_words(tiles + q, lb.cb, nt, w[q]);
+    for (int q = 0; q < N; ++q) {
+        ask_words(state + q, 0, s > 0 ? 1 : 0, u[q]);
+        ask_words(groups + q, lb.cb, ng, v[q]);
+        ask_words(tiles + q, lb.cb, nt, w[q]);
+    }
+    if (!mapped()) return false;
 #pragma unroll
     for (int q = 0; q < N; ++q) {
         wait_words(p, state + q, 0, u[q]);
         if (s > 0) h[q] = as_pair(u[q][0]).x;
-    }
-#pragma unroll
-    for (int q = 0; q < N; ++q) {
         wait_words(p, groups + q, lb.cb, v[q]);
 #pragma unroll
         for (int i = 0; i < kSuper - 1; ++i)
             if (i < ng) h[q] = pass(as_pair(v[q][i]), h[q]);
-    }
-#pragma unroll
-    for (int q = 0; q < N; ++q) {
         wait_words(p, tiles + q, lb.cb, w[q]);
 #pragma unroll
         for (int i = 0; i < kGroup - 1; ++i)
             if (i < nt) h[q] = pass(as_pair(w[q][i]), h[q]);
     }
+    return true;
 }
 
 // Publishes the state `h` after tile n where the tile ends a super-group.
@@ -219,7 +219,7 @@ __device__ __forceinline__ float join_tile(const GateParams& p, const Lookback& 
     const float2 one[1] = {m};
     publish_group(p, lb, row, n, ch, one);
     float h[1] = {start};
-    enter_tile(p, lb, row, n, ch, h);
+    enter_tile(p, lb, row, n, ch, h, [] { return true; });
     publish_state(p, lb, row, n, ch, pass(m, h[0]));
     return h[0];
 }
@@ -268,6 +268,29 @@ struct Run {
 constexpr int kJoin = 2;    // sets of joiners, every kJoin-th tile each
 constexpr int kJoinCh = 1;  // channels of a joiner's thread
 constexpr int kAhead = 1;   // tickets taken ahead, their tiles on the way to L2
+
+// A tile in a stage, worked out once by the loader: n counts tiles in the order of
+// the walk (-1: there is no further tile); t0 is its first token; the offsets are
+// those of the tile's first element in each strided operand that is not loaded by
+// tensor copies.
+struct TileInfo {
+    int n, row, b, t0;
+    long long reset, g, o, o2;
+};
+// A role's place in the ring of stages.
+template <int S, int STEP>
+struct Ring {
+    int s;
+    uint32_t phase;
+    __device__ explicit Ring(int first) : s(first), phase(0) {}
+    __device__ void next() {
+        s += STEP;
+        if (s >= S) {
+            s -= S;
+            phase ^= 1u;
+        }
+    }
+};
 
 // Like mbar_try, but the thread may sleep for up to 2 us in one try: the waiting
 // warps' own instructions took a third of the issue slots without it.

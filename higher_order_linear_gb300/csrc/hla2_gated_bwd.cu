@@ -200,11 +200,11 @@ gated_pipe_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
     using T = bf16;
     using LY = BackLayout<TO, SHARED, LANES>;
     constexpr int CB = LY::CB, RUNS = LY::RUNS, TILE = LY::TILE, S = LY::kStages, NG = SHARED ? 1 : kCh;
-    constexpr unsigned kEnd = 0xffffffffu;
     extern __shared__ __align__(128) unsigned char raw[];
     __shared__ __align__(8) unsigned long long bars[6 * S];
     static_assert(S >= kJoin, "the ends of the tickets take a stage for each group of joiners");
-    __shared__ unsigned tile_of_stage[S], reset_bits[S][RUNS];
+    __shared__ TileInfo info[S];
+    __shared__ unsigned reset_bits[S][RUNS];
     __shared__ float2 total[S][CB];
     __shared__ volatile int abort_flag;
     unsigned char* const base = raw + ((128u - (smem_u32(raw) & 127u)) & 127u);
@@ -254,10 +254,9 @@ gated_pipe_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
         b = row / p.H;
         hd = row - b * p.H;
     };
-    int n, row, b, hd;
-
     if (warp == 0) {  // loader
         if (tid != 0) return;
+        int n, row, b, hd;
         Tickets tickets{reinterpret_cast<unsigned*>(p.words), nullptr};
         LoadLedger<S> loads(full(0));
         unsigned ahead[kAhead + 1];
@@ -275,21 +274,22 @@ gated_pipe_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
 #pragma unroll
         for (int i = 0; i <= kAhead; ++i) ahead[i] = take(i > 0 ? ahead[i > 0 ? i - 1 : 0] : 0u, i == 0);
         int ends = 0;
-        for (unsigned i = 0; ends < kJoin; ++i) {
-            const int s = (int)(i % S);
+        for (Ring<S, 1> at(0); ends < kJoin; at.next()) {
+            const int s = at.s;
             const unsigned k = ahead[0];
-            if (!wait(empty(s), ((i / S) & 1u) ^ 1u)) break;
+            if (!wait(empty(s), at.phase ^ 1u)) break;
             if (k >= p.total) {  // one end to each group of joiners
-                tile_of_stage[s] = kEnd;
+                info[s].n = -1;
                 mbar_arrive(known(s));
                 mbar_arrive(full(s));
                 ++ends;
                 continue;
             }
-            tile_of_stage[s] = k;
-            mbar_arrive(known(s));
             place(k, n, row, b, hd);
             const int t = (p.tiles - 1 - n) * TILE;
+            info[s] = TileInfo{n, row, b, t, (long long)b * p.T, b * p.sg[0] + hd * p.sg[1] + t * p.sg[2],
+                               b * p.sdx[0] + hd * p.sdx[1] + t * p.sdx[2], b * p.sdg[0] + hd * p.sdg[1] + t * p.sdg[2]};
+            mbar_arrive(known(s));
             loads.note(s);
             mbar_expect_tx(full(s), (uint32_t)(TILE * p.d) * (2u * (SHARED ? 1u : 2u) + (uint32_t)sizeof(TO)));
             tma_load_4d(smem_u32(stage(s)), &mx, 0, t, hd, b, full(s));
@@ -306,12 +306,11 @@ gated_pipe_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
     if (tid >= kFirstJoiner && tid < kFirstGrouper) {  // joiners
         const int j = (tid - kFirstJoiner) / LY::kJoiners;
         const int ch = (tid - kFirstJoiner - j * LY::kJoiners) * kJoinCh;
-        for (unsigned i = (unsigned)j;; i += kJoin) {
-            const int s = (int)(i % S);
-            if (!wait(known(s), (i / S) & 1u)) return;
-            const unsigned k = tile_of_stage[s];
-            if (k != kEnd) {
-                place(k, n, row, b, hd);
+        for (Ring<S, kJoin> at(j);; at.next()) {
+            const int s = at.s;
+            if (!wait(known(s), at.phase)) return;
+            const int n = info[s].n, row = info[s].row;
+            if (n >= 0) {
                 float mu[kJoinCh], h[kJoinCh];
 #pragma unroll
                 for (int q = 0; q < kJoinCh; ++q) {
@@ -319,8 +318,8 @@ gated_pipe_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
                     mu[q] = p.dstate_out && in ? p.dstate_out[(long long)row * p.d + ch + q] : 0.f;
                     h[q] = in ? p.carry[((long long)row * p.tiles + (p.tiles - 1 - n)) * p.d + ch + q] : 0.f;
                 }
-                if (p.words) enter_tile(p, lb, row, n, ch, mu);  // while the tile is loaded and mapped
-                if (!wait(mapped(s), (i / S) & 1u)) return;
+                const auto own = [&] { return wait(mapped(s), at.phase); };
+                if (!(p.words ? enter_tile(p, lb, row, n, ch, mu, own) : own())) return;
 #pragma unroll
                 for (int q = 0; q < kJoinCh; ++q) {
                     if (p.words) publish_state(p, lb, row, n, ch + q, pass(total[s][ch + q], mu[q]));
@@ -342,22 +341,21 @@ gated_pipe_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
             }
             __syncwarp();
             if ((tid & 31) == 0) mbar_arrive(joined(s));
-            if (k == kEnd) return;
+            if (n < 0) return;
         }
     }
     if (tid >= kFirstGrouper && tid < kFirstGrouper + LY::kJoiners) {  // groupers
         const int ch = (tid - kFirstGrouper) * kJoinCh;
-        for (unsigned i = 0;; ++i) {
-            const int s = (int)(i % S);
-            if (!wait(mapped(s), (i / S) & 1u)) return;
-            const unsigned k = tile_of_stage[s];
-            if (k == kEnd) return;
+        for (Ring<S, 1> at(0);; at.next()) {
+            const int s = at.s;
+            if (!wait(mapped(s), at.phase)) return;
+            const int n = info[s].n, row = info[s].row;
+            if (n < 0) return;
             float2 m[kJoinCh];
 #pragma unroll
             for (int q = 0; q < kJoinCh; ++q) m[q] = total[s][ch + q];
             __syncwarp();
             if ((tid & 31) == 0) mbar_arrive(empty(s));
-            place(k, n, row, b, hd);
             if (p.words) publish_group(p, lb, row, n, ch, m);
         }
     }
@@ -366,24 +364,23 @@ gated_pipe_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
     const int lane = at % LANES, run = at / LANES;
     const int c = lane * kCh, nc = p.d - c;
     int ends = 0;
-    for (unsigned i = 0;; ++i) {
-        const int s = (int)(i % S);
-        const uint32_t phase = (i / S) & 1u;
+    for (Ring<S, 1> ring(0);; ring.next()) {
+        const int s = ring.s;
+        const uint32_t phase = ring.phase;
         if (!wait(mapper ? known(s) : joined(s), phase)) return;
-        const unsigned k = tile_of_stage[s];
-        if (k == kEnd) {
+        const int n = info[s].n;
+        if (n < 0) {
             if (!mapper) return;
             if (at < CB && (tid & 31) == 0) mbar_arrive(mapped(s));
             if (++ends == kJoin) return;
             continue;
         }
-        place(k, n, row, b, hd);
-        const int t0 = (p.tiles - 1 - n) * TILE + run * kTok;
+        const int t0 = info[s].t0 + run * kTok;
         const int nt = nc > 0 ? min(kTok, p.T - t0) : 0;
         unsigned resets = 0;  // asked for while the tile is loaded
         if (p.reset) {
             if (mapper) {
-                resets = run_resets<LANES>(p.reset + (long long)b * p.T, t0, p.T);
+                resets = run_resets<LANES>(p.reset + info[s].reset, t0, p.T);
                 if (lane == 0) reset_bits[s][run] = resets;
             } else {
                 resets = reset_bits[s][run];
@@ -393,7 +390,7 @@ gated_pipe_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
         const T* xs = reinterpret_cast<const T*>(stage(s)) + run * kTok * p.d + c;
         const T* gs = reinterpret_cast<const T*>(stage(s) + kG) + run * kTok * p.d + c;
         const TO* us = reinterpret_cast<const TO*>(stage(s) + kUp) + run * kTok * p.d + c;
-        const T* gp = static_cast<const T*>(p.g) + b * p.sg[0] + hd * p.sg[1] + t0 * p.sg[2];
+        const T* gp = static_cast<const T*>(p.g) + info[s].g + run * kTok * p.sg[2];
         float gl[SHARED ? kTok : 1];
         if (SHARED) {
 #pragma unroll
@@ -458,7 +455,7 @@ gated_pipe_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
                 float2 m = make_float2(pA[(RUNS - 1) * CB], pY[(RUNS - 1) * CB]);
 #pragma unroll
                 for (int r = RUNS - 2; r >= 0; --r) m = then(m, make_float2(pA[r * CB], pY[r * CB]));
-                if (p.words) publish_tile(p, lb, row, n, at, m);
+                if (p.words) publish_tile(p, lb, info[s].row, n, at, m);
                 total[s][at] = m;
                 __syncwarp();
                 if ((tid & 31) == 0) mbar_arrive(mapped(s));
@@ -467,8 +464,8 @@ gated_pipe_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
             float h[kCh], mu[kCh];
             four(plane(s, 1) + run * CB + c, h);
             four(plane(s, 2) + run * CB + c, mu);
-            T* const dxp = static_cast<T*>(p.dx) + b * p.sdx[0] + hd * p.sdx[1] + t0 * p.sdx[2] + c;
-            T* const dgp = static_cast<T*>(p.dg) + b * p.sdg[0] + hd * p.sdg[1] + t0 * p.sdg[2] + (SHARED ? 0 : c);
+            T* const dxp = static_cast<T*>(p.dx) + info[s].o + run * kTok * p.sdx[2] + c;
+            T* const dgp = static_cast<T*>(p.dg) + info[s].o2 + run * kTok * p.sdg[2] + (SHARED ? 0 : c);
             auto walk = [&](auto whole, auto clean) {
                 float z[kTok][NG];
 #pragma unroll
@@ -535,6 +532,7 @@ gated_pipe_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
             if (whole && clean) walk(std::true_type{}, std::true_type{});
             else if (whole) walk(std::true_type{}, std::false_type{});
             else walk(std::false_type{}, std::false_type{});
+            const int row = info[s].row;
             __syncwarp();
             if ((tid & 31) == 0) mbar_arrive(empty(s));
             if (p.dstate_in && nt > 0 && t0 == 0) {
