@@ -154,24 +154,26 @@ struct PipeLayout {
     static constexpr int CB = LANES * kCh, RUNS = kData / LANES, TILE = RUNS * kTok;
     static constexpr uint32_t kTileBytes = TILE * CB * sizeof(T);  // of x, and of the gates
     static constexpr uint32_t kMaps = RUNS * CB * 8;
-    static constexpr int kJoiners = CB / kJoinCh;  // threads of a set of joiners
-    static constexpr uint32_t kStage = kTileBytes * (SHARED ? 1 : 2) + kMaps;
-    static constexpr int kStages = 225 * 1024 / kStage > 8 ? 8 : 225 * 1024 / kStage;
-    static constexpr uint32_t kBytes = kStage * kStages + 128;  // and alignment to 128 bytes
-    static constexpr int kThreads = 32 + kData + (kJoin + 1) * kJoiners + kData;
+    static constexpr uint32_t kStage = kTileBytes * (SHARED ? 1 : 2);
+    // The maps of a tile live from its mapping to its writing, a part of the time
+    // that its data does: they have a ring of their own, of fewer slots.
+    static constexpr int kSlots = sizeof(T) == 2 ? 4 : 2;
+    static constexpr int kFit = (int)((225 * 1024 - kMaps * kSlots) / kStage);
+    static constexpr int kStages = kFit > 8 ? 8 : kFit;
+    static constexpr uint32_t kBytes = kStage * kStages + kMaps * kSlots + 128;  // and alignment to 128 bytes
+    static constexpr int kThreads = 32 + kData + (kJoin + 1) * CB + kData;
 };
 
 template <typename T, bool SIG, bool SHARED, int LANES>
 __global__ void __launch_bounds__(PipeLayout<T, SHARED, LANES>::kThreads, 1)
 gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mg, const GateParams p) {
     using LY = PipeLayout<T, SHARED, LANES>;
-    constexpr int CB = LY::CB, RUNS = LY::RUNS, TILE = LY::TILE, S = LY::kStages;
+    constexpr int CB = LY::CB, RUNS = LY::RUNS, TILE = LY::TILE, S = LY::kStages, M = LY::kSlots;
     extern __shared__ __align__(128) unsigned char raw[];
-    __shared__ __align__(8) unsigned long long bars[6 * S];
+    __shared__ __align__(8) unsigned long long bars[5 * S + 2 * M];
     static_assert(S >= kJoin, "the ends of the tickets take a stage for each group of joiners");
     __shared__ TileInfo info[S];
     __shared__ unsigned reset_bits[S][RUNS];
-    __shared__ float2 total[S][CB];
     __shared__ volatile int abort_flag;
     unsigned char* const base = raw + ((128u - (smem_u32(raw) & 127u)) & 127u);
     const int tid = threadIdx.x, warp = tid >> 5;
@@ -179,46 +181,35 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
     auto mapped = [&](int s) { return smem_u32(&bars[S + s]); };      // its runs' maps and its own are there
     auto joined = [&](int s) { return smem_u32(&bars[2 * S + s]); };  // the states that enter its runs are there
     auto empty = [&](int s) { return smem_u32(&bars[3 * S + s]); };   // its outputs are written
-    auto known = [&](int s) { return smem_u32(&bars[5 * S + s]); };   // the stage's next tile is known
-    auto runs = [&](int s) { return smem_u32(&bars[4 * S + s]); };    // every mapper's runs are mapped
+    auto known = [&](int s) { return smem_u32(&bars[4 * S + s]); };   // the stage's next tile is known
     auto sx = [&](int s) { return reinterpret_cast<T*>(base + (size_t)s * LY::kStage); };
     auto sg = [&](int s) { return reinterpret_cast<T*>(base + (size_t)s * LY::kStage + LY::kTileBytes); };
-    auto maps = [&](int s) {
-        return reinterpret_cast<float2*>(base + (size_t)s * LY::kStage + LY::kTileBytes * (SHARED ? 1 : 2));
-    };
+    auto maps = [&](int m) { return reinterpret_cast<float2*>(base + (size_t)S * LY::kStage + m * LY::kMaps); };
+    auto runs = [&](int m) { return smem_u32(&bars[5 * S + m]); };      // every mapper's runs are mapped
+    auto taken = [&](int m) { return smem_u32(&bars[5 * S + M + m]); };  // the slot's maps have been read
     if (tid == 0) {
         abort_flag = 0;
         for (int s = 0; s < S; ++s) {
             mbar_init(full(s), 1);
             mbar_init(mapped(s), CB / 32);
-            mbar_init(joined(s), LY::kJoiners / 32);
-            mbar_init(empty(s), kData / 32 + LY::kJoiners / 32);
-            mbar_init(runs(s), kData / 32);
+            mbar_init(joined(s), CB / 32);
+            mbar_init(empty(s), kData / 32);
             mbar_init(known(s), 1);
+        }
+        for (int m = 0; m < M; ++m) {
+            mbar_init(runs(m), kData / 32);
+            mbar_init(taken(m), kData / 32);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
-    auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
-        if (abort_flag) return false;
-        if (mbar_try(bar, parity)) return true;
-        const unsigned long long t0 = globaltimer();
-        while (!mbar_try_long(bar, parity)) {
-            if (abort_flag) return false;
-            if (globaltimer() - t0 > 2 * kGateWaitNs) {  // longer than the joiners' own waits
-                abort_flag = 1;
-                atomicExch(p.status, (int)kDevWaitTimeout);
-                return false;
-            }
-        }
-        return true;
-    };
+    auto wait = [&](uint32_t bar, uint32_t parity) { return bar_wait(bar, parity, &abort_flag, p.status); };
     const int rows = p.B * p.H;
     const Lookback lb(rows, p.tiles, CB);
     auto place = [&](unsigned k, int& n, int& row, int& b, int& hd) {
-        n = (int)(k / (unsigned)rows);
+        n = (int)quotient(k, p.per_rows);
         row = (int)(k - (unsigned)n * (unsigned)rows);
-        b = row / p.H;
+        b = (int)quotient((unsigned)row, p.per_h);
         hd = row - b * p.H;
     };
     if (warp == 0) {  // loader
@@ -226,23 +217,20 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
         int n, row, b, hd;
         Tickets tickets{reinterpret_cast<unsigned*>(p.words), nullptr};
         LoadLedger<S> loads(full(0));
-        // tickets taken ahead, their tiles on the way to L2
-        unsigned ahead[kAhead + 1];
-        auto take = [&](unsigned last, bool first) -> unsigned {
-            const unsigned k = first && !p.words ? blockIdx.x : tickets.take(last);
-            if (kAhead > 0 && k < p.total) {
-                place(k, n, row, b, hd);
-                tma_prefetch_l2_4d(&mx, 0, n * TILE, hd, b);
-                if (!SHARED) tma_prefetch_l2_4d(&mg, 0, n * TILE, hd, b);
-            }
-            return k;
+        // Tickets come in order, so the tiles of the rounds ahead are known: each block
+        // asks L2 for as many tiles as it loads, whichever block will load them.
+        auto ask = [&](unsigned long long k) {
+            if (k >= p.total) return;
+            place((unsigned)k, n, row, b, hd);
+            tma_prefetch_l2_4d(&mx, 0, n * TILE, hd, b);
+            if (!SHARED) tma_prefetch_l2_4d(&mg, 0, n * TILE, hd, b);
         };
-#pragma unroll
-        for (int i = 0; i <= kAhead; ++i) ahead[i] = take(i > 0 ? ahead[i > 0 ? i - 1 : 0] : 0u, i == 0);
+        for (int r = 1; r < kFar; ++r) ask((unsigned long long)r * gridDim.x + blockIdx.x);
+        unsigned next = p.words ? tickets.take(0) : blockIdx.x;
         int ends = 0;
         for (Ring<S, 1> at(0); ends < kJoin; at.next()) {
             const int s = at.s;
-            const unsigned k = ahead[0];
+            const unsigned k = next;
             if (!wait(empty(s), at.phase ^ 1u)) break;
             if (k >= p.total) {  // one end to each group of joiners
                 info[s].n = -1;
@@ -260,63 +248,63 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
             mbar_expect_tx(full(s), (uint32_t)(TILE * p.d * sizeof(T)) * (SHARED ? 1u : 2u));
             tma_load_4d(smem_u32(sx(s)), &mx, 0, n * TILE, hd, b, full(s));
             if (!SHARED) tma_load_4d(smem_u32(sg(s)), &mg, 0, n * TILE, hd, b, full(s));
-#pragma unroll
-            for (int j = 0; j < kAhead; ++j) ahead[j] = ahead[j + 1];
-            ahead[kAhead] = take(ahead[kAhead], false);
+            ask((unsigned long long)kFar * gridDim.x + k);
+            // a ticket held longer than it must be holds up the tiles after it in its row
+            next = tickets.take(k);
         }
         if (abort_flag && !loads.settle()) atomicExch(p.status, (int)kDevWaitTimeout);
         return;
     }
-    constexpr int kFirstJoiner = 32 + kData, kFirstGrouper = kFirstJoiner + kJoin * LY::kJoiners;
-    if (tid >= kFirstJoiner && tid < kFirstGrouper) {  // joiners
-        const int j = (tid - kFirstJoiner) / LY::kJoiners;
-        const int ch = (tid - kFirstJoiner - j * LY::kJoiners) * kJoinCh;
-        for (Ring<S, kJoin> at(j);; at.next()) {
+    constexpr int kFirstJoiner = 32 + kData, kFirstComposer = kFirstJoiner + kJoin * CB;
+    if (tid >= kFirstJoiner && tid < kFirstComposer) {  // joiners
+        const int j = (tid - kFirstJoiner) / CB, ch = tid - kFirstJoiner - j * CB;
+        Ring<M, kJoin> slot(j);
+        for (Ring<S, kJoin> at(j);; at.next(), slot.next()) {
             const int s = at.s;
             if (!wait(known(s), at.phase)) return;
             const int n = info[s].n, row = info[s].row;
             if (n >= 0) {
-                float h[kJoinCh];
-#pragma unroll
-                for (int q = 0; q < kJoinCh; ++q)
-                    h[q] = p.state_in && ch + q < p.d ? p.state_in[(long long)row * p.d + ch + q] : 0.f;
+                const float start = p.state_in && ch < p.d ? p.state_in[(long long)row * p.d + ch] : 0.f;
                 const auto own = [&] { return wait(mapped(s), at.phase); };
-                if (!(p.words ? enter_tile(p, lb, row, n, ch, h, own) : own())) return;
-                if (p.carry) {
+                float h = start;
+                if (!(p.words ? enter_tile(p, lb, row, n, ch, start, h, own) : own())) return;
+                if (p.carry && ch < p.d) p.carry[((long long)row * p.tiles + n) * p.d + ch] = h;
+                float2* m = maps(slot.s) + ch;
+                float2 f[RUNS];
 #pragma unroll
-                    for (int q = 0; q < kJoinCh; ++q)
-                        if (ch + q < p.d) p.carry[((long long)row * p.tiles + n) * p.d + ch + q] = h[q];
+                for (int r = 0; r < RUNS; ++r) f[r] = m[r * CB];
+#pragma unroll
+                for (int r = 0; r < RUNS; ++r) {
+                    const float after = pass(f[r], h);
+                    f[r].x = h;
+                    h = after;
                 }
+                if (p.words) publish_state(p, lb, row, n, ch, h);  // first: tiles of other blocks wait for it
 #pragma unroll
-                for (int q = 0; q < kJoinCh; ++q) {
-                    if (p.words) publish_state(p, lb, row, n, ch + q, pass(total[s][ch + q], h[q]));
-                    float2* m = maps(s) + ch + q;
-#pragma unroll
-                    for (int r = 0; r < RUNS; ++r) {
-                        const float2 f = m[r * CB];
-                        m[r * CB].x = h[q];
-                        h[q] = pass(f, h[q]);
-                    }
-                }
+                for (int r = 0; r < RUNS; ++r) m[r * CB].x = f[r].x;
             }
             __syncwarp();
             if ((tid & 31) == 0) mbar_arrive(joined(s));
             if (n < 0) return;
         }
     }
-    if (tid >= kFirstGrouper && tid < kFirstGrouper + LY::kJoiners) {  // groupers
-        const int ch = (tid - kFirstGrouper) * kJoinCh;
-        for (Ring<S, 1> at(0);; at.next()) {
+    if (tid >= kFirstComposer && tid < kFirstComposer + CB) {  // composers
+        const int ch = tid - kFirstComposer;
+        Ring<M, 1> slot(0);
+        for (Ring<S, 1> at(0);; at.next(), slot.next()) {
             const int s = at.s;
-            if (!wait(mapped(s), at.phase)) return;
+            if (!wait(known(s), at.phase)) return;
             const int n = info[s].n, row = info[s].row;
             if (n < 0) return;
-            float2 m[kJoinCh];
+            if (!wait(runs(slot.s), slot.phase)) return;
+            if (p.words && n + 1 < p.tiles) {
+                float2 m = maps(slot.s)[ch];
 #pragma unroll
-            for (int q = 0; q < kJoinCh; ++q) m[q] = total[s][ch + q];
+                for (int r = 1; r < RUNS; ++r) m = then(m, maps(slot.s)[r * CB + ch]);
+                publish_tile(p, lb, row, n, ch, m);
+            }
             __syncwarp();
-            if ((tid & 31) == 0) mbar_arrive(empty(s));
-            if (p.words) publish_group(p, lb, row, n, ch, m);
+            if ((tid & 31) == 0) mbar_arrive(mapped(s));
         }
     }
     const bool mapper = warp < 1 + kData / 32;
@@ -324,18 +312,13 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
     const int lane = at % LANES, run = at / LANES;
     const int c = lane * kCh, nc = p.d - c;
     constexpr int NG = SHARED ? 1 : kCh;
-    int ends = 0;
-    for (Ring<S, 1> ring(0);; ring.next()) {
+    Ring<M, 1> slot(0);
+    for (Ring<S, 1> ring(0);; ring.next(), slot.next()) {
         const int s = ring.s;
         const uint32_t phase = ring.phase;
         if (!wait(mapper ? known(s) : joined(s), phase)) return;
         const int n = info[s].n;
-        if (n < 0) {
-            if (!mapper) return;
-            if (at < CB && (tid & 31) == 0) mbar_arrive(mapped(s));
-            if (++ends == kJoin) return;
-            continue;
-        }
+        if (n < 0) return;
         const int t0 = info[s].t0 + run * kTok;
         const int nt = nc > 0 ? min(kTok, p.T - t0) : 0;
         unsigned resets = 0;  // asked for while the tile is loaded
@@ -391,28 +374,21 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
             if (nt == kTok && resets == 0) walk(std::true_type{}, std::true_type{});
             else if (nt == kTok) walk(std::true_type{}, std::false_type{});
             else walk(std::false_type{}, std::false_type{});
-            float4* m4 = reinterpret_cast<float4*>(maps(s) + run * CB + c);
+            if (!wait(taken(slot.s), slot.phase ^ 1u)) return;
+            float4* m4 = reinterpret_cast<float4*>(maps(slot.s) + run * CB + c);
 #pragma unroll
             for (int j = 0; j < kCh; ++j) A[j] = resets ? cut() : A[j] + 0.f;
             m4[0] = make_float4(A[0], X[0], A[1], X[1]);
             m4[1] = make_float4(A[2], X[2], A[3], X[3]);
             __syncwarp();
-            if ((tid & 31) == 0) mbar_arrive(runs(s));
-            if (at < CB) {  // one channel of the tile's map
-                if (!wait(runs(s), phase)) return;
-                float2 m = maps(s)[at];
-#pragma unroll
-                for (int r = 1; r < RUNS; ++r) m = then(m, maps(s)[r * CB + at]);
-                if (p.words) publish_tile(p, lb, info[s].row, n, at, m);
-                total[s][at] = m;
-                __syncwarp();
-                if ((tid & 31) == 0) mbar_arrive(mapped(s));
-            }
+            if ((tid & 31) == 0) mbar_arrive(runs(slot.s));
         } else {
             float h[kCh];
-            const float4* m4 = reinterpret_cast<const float4*>(maps(s) + run * CB + c);
+            const float4* m4 = reinterpret_cast<const float4*>(maps(slot.s) + run * CB + c);
             const float4 lo = m4[0], hi = m4[1];
             h[0] = lo.x; h[1] = lo.z; h[2] = hi.x; h[3] = hi.z;
+            __syncwarp();
+            if ((tid & 31) == 0) mbar_arrive(taken(slot.s));
             const long long off = info[s].o + run * kTok * p.so[2] + c;
             auto walk = [&](auto whole, auto clean, auto* o) {
 #pragma unroll

@@ -15,8 +15,7 @@ namespace {
 constexpr int kTok = 8;         // tokens of a run
 constexpr int kCh = 4;          // channels of a thread
 constexpr int kData = 256;      // threads that share a tile: one to a run and four channels
-constexpr int kGroup = 8;       // tiles to a group
-constexpr int kSuper = 4;       // groups to a super-group
+constexpr int kGroup = 8;       // tiles to a group: a state is published at the end of each
 constexpr unsigned long long kGateWaitNs = 2000000000ull;  // bounded waits: 2 s
 
 // Lanes that share a token: they cover 4 channels each, d <= 4 lanes.
@@ -38,6 +37,7 @@ struct GateParams {
     unsigned long long* words;
     int tiles, out_bf16;
     unsigned total;  // rows * tiles
+    unsigned long long per_rows, per_h;  // 2^64 / rows and 2^64 / H, for quotients
     int* status;
 };
 
@@ -65,24 +65,25 @@ __device__ __forceinline__ float2 then(float2 a, float2 b) {
     return make_float2(is_cut(b.x) || is_cut(a.x) ? cut() : a.x * b.x + 0.f, pass(b, a.y));
 }
 
+// x / y for the y whose 2^64 / y (rounded up; 0 stands for y = 1) is `per`
+__device__ __forceinline__ unsigned quotient(unsigned x, unsigned long long per) {
+    return per ? (unsigned)__umul64hi((unsigned long long)x, per) : x;
+}
+
 // ---- the workspace -----------------------------------------------------------
 // A ticket word and a word that says that a wait ran out; then the maps of the
-// tiles and of the groups (A, X for each of a row's channels), then the states
-// that enter the super-groups (h, 0).  Each pair is one 64-bit word, written and
-// read whole, so it is its own flag: the words are set to all ones before the
-// launch, which no pair is (arithmetic gives one NaN, 0x7fffffff), and whoever
-// needs one reads it until it is something else.
+// tiles (A, X for each of a row's channels), then the states that enter the groups
+// (h, 0).  Each pair is one 64-bit word, written and read whole, so it is its own
+// flag: the words are set to all ones before the launch, which no pair is
+// (arithmetic gives one NaN, 0x7fffffff), and whoever needs one reads it until it
+// is something else.
 struct Lookback {
-    int rows, tiles, groups, supers, cb;  // cb: channels of a map
+    int rows, tiles, groups, cb;  // cb: channels of a map
     __host__ __device__ Lookback(int rows, int tiles, int cb)
-        : rows(rows), tiles(tiles), groups((tiles + kGroup - 1) / kGroup),
-          supers((groups + kSuper - 1) / kSuper), cb(cb) {}
+        : rows(rows), tiles(tiles), groups((tiles + kGroup - 1) / kGroup), cb(cb) {}
     __host__ __device__ size_t tile_map(int r, int t) const { return 1 + ((size_t)r * tiles + t) * cb; }
-    __host__ __device__ size_t group_map(int r, int g) const { return tile_map(rows, 0) + ((size_t)r * groups + g) * cb; }
-    __host__ __device__ size_t super_state(int r, int s) const {
-        return group_map(rows, 0) + ((size_t)r * supers + s) * cb;
-    }
-    __host__ __device__ size_t words() const { return super_state(rows, 0); }
+    __host__ __device__ size_t state(int r, int g) const { return tile_map(rows, 0) + ((size_t)r * groups + g) * cb; }
+    __host__ __device__ size_t words() const { return state(rows, 0); }
 };
 
 using u64 = unsigned long long;
@@ -146,82 +147,44 @@ __device__ __forceinline__ void publish_tile(const GateParams& p, const Lookback
     if (n + 1 < lb.tiles) st_pair(p.words + lb.tile_map(row, n) + ch, m);
 }
 
-// The rest is done for N channels by one thread (ch, ch + 1, ..): what it needs of
-// each is asked for before any is waited for.
-
-// Publishes the map of the group that tile n, of map `m`, ends, if it ends one.
-template <int N>
-__device__ __forceinline__ void publish_group(const GateParams& p, const Lookback& lb, int row, int n, int ch,
-                                              const float2 (&m)[N]) {
-    if (n % kGroup != kGroup - 1 || n + 1 == lb.tiles) return;
-    u64 w[N][kGroup - 1];
-    const u64* const tiles = p.words + lb.tile_map(row, n - (kGroup - 1)) + ch;
-#pragma unroll
-    for (int q = 0; q < N; ++q) ask_words(tiles + q, lb.cb, kGroup - 1, w[q]);
-#pragma unroll
-    for (int q = 0; q < N; ++q) {
-        wait_words(p, tiles + q, lb.cb, w[q]);
-        float2 all = as_pair(w[q][0]);
-#pragma unroll
-        for (int i = 1; i < kGroup - 1; ++i) all = then(all, as_pair(w[q][i]));
-        st_pair(p.words + lb.group_map(row, n / kGroup) + ch + q, then(all, m[q]));
-    }
-}
-
-// h: in, the state that enters the sequence; out, the state that enters tile n.
-// `mapped()` is called between the first look at the words and the waiting for
-// those that are missing: it waits for the tile's own map (false: give up), by
-// which time the tiles before it have theirs too; polling from the start took
-// more of the L2's bandwidth than the data.
-template <int N, typename F>
-__device__ __forceinline__ bool enter_tile(const GateParams& p, const Lookback& lb, int row, int n, int ch,
-                                           float (&h)[N], F&& mapped) {
-    const int g = n / kGroup, s = g / kSuper;
-    const int nt = n % kGroup, ng = g % kSuper;  // tiles before this one in its group, groups before it in the super-group
-    u64 w[N][kGroup - 1], v[N][kSuper - 1], u[N][1];
-    const u64* const state = p.words + lb.super_state(row, s) + ch;
-    const u64* const groups = p.words + lb.group_map(row, g - ng) + ch;
+// The state that enters tile n, for one channel; `start` is the one that enters the
+// sequence.  `mapped()` is called between the first look at the words and the
+// waiting for those that are missing: it waits for the tile's own map (false: give
+// up), by which time the tiles before it have theirs too; polling from the start
+// took more of the L2's bandwidth than the data.
+template <typename F>
+__device__ __forceinline__ bool enter_tile(const GateParams& p, const Lookback& lb, int row, int n, int ch, float start,
+                                           float& h, F&& mapped) {
+    const int g = n / kGroup, nt = n % kGroup;  // nt: tiles before this one in its group
+    u64 w[kGroup - 1], u[1];
+    const u64* const state = p.words + lb.state(row, g) + ch;
     const u64* const tiles = p.words + lb.tile_map(row, n - nt) + ch;
-#pragma unroll
-    for (int q = 0; q < N; ++q) {
-        ask_words(state + q, 0, s > 0 ? 1 : 0, u[q]);
-        ask_words(groups + q, lb.cb, ng, v[q]);
-        ask_words(tiles + q, lb.cb, nt, w[q]);
-    }
+    ask_words(state, 0, g > 0 ? 1 : 0, u);
+    ask_words(tiles, lb.cb, nt, w);
     if (!mapped()) return false;
+    wait_words(p, state, 0, u);
+    wait_words(p, tiles, lb.cb, w);
+    h = g > 0 ? as_pair(u[0]).x : start;
 #pragma unroll
-    for (int q = 0; q < N; ++q) {
-        wait_words(p, state + q, 0, u[q]);
-        if (s > 0) h[q] = as_pair(u[q][0]).x;
-        wait_words(p, groups + q, lb.cb, v[q]);
-#pragma unroll
-        for (int i = 0; i < kSuper - 1; ++i)
-            if (i < ng) h[q] = pass(as_pair(v[q][i]), h[q]);
-        wait_words(p, tiles + q, lb.cb, w[q]);
-#pragma unroll
-        for (int i = 0; i < kGroup - 1; ++i)
-            if (i < nt) h[q] = pass(as_pair(w[q][i]), h[q]);
-    }
+    for (int i = 0; i < kGroup - 1; ++i)
+        if (i < nt) h = pass(as_pair(w[i]), h);
     return true;
 }
 
-// Publishes the state `h` after tile n where the tile ends a super-group.
+// Publishes the state `h` after tile n where the tile ends a group.
 __device__ __forceinline__ void publish_state(const GateParams& p, const Lookback& lb, int row, int n, int ch, float h) {
-    constexpr int kLong = kGroup * kSuper;
-    if (n % kLong == kLong - 1 && n + 1 < lb.tiles)
-        st_pair(p.words + lb.super_state(row, n / kLong + 1) + ch, make_float2(h, 0.f));
+    if (n % kGroup == kGroup - 1 && n + 1 < lb.tiles)
+        st_pair(p.words + lb.state(row, n / kGroup + 1) + ch, make_float2(h, 0.f));
 }
 
 // One channel's part in the register kernels: publishes the tile's map, returns the state that enters it.
 __device__ __forceinline__ float join_tile(const GateParams& p, const Lookback& lb, int row, int n, int ch, float2 m,
                                            float start) {
     publish_tile(p, lb, row, n, ch, m);
-    const float2 one[1] = {m};
-    publish_group(p, lb, row, n, ch, one);
-    float h[1] = {start};
-    enter_tile(p, lb, row, n, ch, h, [] { return true; });
-    publish_state(p, lb, row, n, ch, pass(m, h[0]));
-    return h[0];
+    float h;
+    enter_tile(p, lb, row, n, ch, start, h, [] { return true; });
+    publish_state(p, lb, row, n, ch, pass(m, h));
+    return h;
 }
 
 // The tiles of a block, by ticket where tiles wait for one another.  The
@@ -266,8 +229,8 @@ struct Run {
 
 // ---- the pipelined kernels ---------------------------------------------------
 constexpr int kJoin = 2;    // sets of joiners, every kJoin-th tile each
-constexpr int kJoinCh = 1;  // channels of a joiner's thread
-constexpr int kAhead = 1;   // tickets taken ahead, their tiles on the way to L2
+constexpr int kFar = 2;     // tiles are asked into L2 this many rounds of the grid ahead
+constexpr unsigned kNapNs = 40;
 
 // A tile in a stage, worked out once by the loader: n counts tiles in the order of
 // the walk (-1: there is no further tile); t0 is its first token; the offsets are
@@ -292,16 +255,27 @@ struct Ring {
     }
 };
 
-// Like mbar_try, but the thread may sleep for up to 2 us in one try: the waiting
-// warps' own instructions took a third of the issue slots without it.
-__device__ __forceinline__ bool mbar_try_long(uint32_t a, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(a), "r"(parity), "r"(2000u)
-        : "memory");
-    return ok != 0;
+// Waits on a barrier of the block, at most 2 x kGateWaitNs (longer than a joiner
+// waits for other blocks); false when that ran out, or when another wait of the
+// block did.  Between two tries the warp sleeps: twenty waiting warps that only
+// tried again took more issue slots than the work.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
+    if (mbar_try(bar, parity)) return *abort_flag == 0;
+    unsigned long long t0 = 0;
+    for (unsigned tries = 1;; ++tries) {
+        __nanosleep(kNapNs);
+        if (mbar_try(bar, parity)) return *abort_flag == 0;
+        if (tries % 64 == 0) {
+            if (*abort_flag) return false;
+            const unsigned long long now = globaltimer();
+            if (t0 == 0) t0 = now;
+            if (now - t0 > 2 * kGateWaitNs) {
+                *abort_flag = 1;
+                atomicExch(status, (int)kDevWaitTimeout);
+                return false;
+            }
+        }
+    }
 }
 __device__ __forceinline__ void mbar_arrive(uint32_t a) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(a) : "memory");
@@ -411,6 +385,9 @@ cudaError_t persistent_blocks(const void* kernel, int threads, size_t smem, unsi
 cudaError_t begin_lookback(GateParams& p, int cb, void* workspace, cudaStream_t s) {
     p.total = (unsigned)((long long)p.B * p.H * p.tiles);
     p.status = device_status_word();
+    const auto per = [](unsigned long long y) { return y == 1 ? 0ull : ~0ull / y + 1; };
+    p.per_rows = per((unsigned long long)p.B * p.H);
+    p.per_h = per((unsigned long long)p.H);
     if (p.tiles <= 1) return cudaSuccess;
     p.words = static_cast<unsigned long long*>(workspace);
     return cudaMemsetAsync(p.words, 0xff, Lookback(p.B * p.H, p.tiles, cb).words() * 8, s);

@@ -189,8 +189,7 @@ struct BackLayout {
     static constexpr int kFit = (int)((222 * 1024 - kBefore) / kStage);
     static constexpr int kStages = kFit > 6 ? 6 : kFit;
     static constexpr uint32_t kBytes = kStage * kStages + kBefore + 128;
-    static constexpr int kJoiners = CB / kJoinCh;
-    static constexpr int kThreads = 32 + kData + (kJoin + 1) * kJoiners + kData;
+    static constexpr int kThreads = 32 + kData + (kJoin + 1) * CB + kData;
 };
 
 template <typename TO, bool SIG, bool SHARED, int LANES>
@@ -205,7 +204,6 @@ gated_pipe_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
     static_assert(S >= kJoin, "the ends of the tickets take a stage for each group of joiners");
     __shared__ TileInfo info[S];
     __shared__ unsigned reset_bits[S][RUNS];
-    __shared__ float2 total[S][CB];
     __shared__ volatile int abort_flag;
     unsigned char* const base = raw + ((128u - (smem_u32(raw) & 127u)) & 127u);
     float4* const before = reinterpret_cast<float4*>(base + (size_t)LY::kStage * S);  // [kTok][kData]: h_{t-1}
@@ -224,34 +222,21 @@ gated_pipe_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
         for (int s = 0; s < S; ++s) {
             mbar_init(full(s), 1);
             mbar_init(mapped(s), CB / 32);
-            mbar_init(joined(s), LY::kJoiners / 32);
-            mbar_init(empty(s), kData / 32 + LY::kJoiners / 32);
+            mbar_init(joined(s), CB / 32);
+            mbar_init(empty(s), kData / 32);
             mbar_init(runs(s), kData / 32);
             mbar_init(known(s), 1);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
-    auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
-        if (abort_flag) return false;
-        if (mbar_try(bar, parity)) return true;
-        const unsigned long long t0 = globaltimer();
-        while (!mbar_try_long(bar, parity)) {
-            if (abort_flag) return false;
-            if (globaltimer() - t0 > 2 * kGateWaitNs) {  // longer than the joiners' own waits
-                abort_flag = 1;
-                atomicExch(p.status, (int)kDevWaitTimeout);
-                return false;
-            }
-        }
-        return true;
-    };
+    auto wait = [&](uint32_t bar, uint32_t parity) { return bar_wait(bar, parity, &abort_flag, p.status); };
     const int rows = p.B * p.H;
     const Lookback lb(rows, p.tiles, CB);
     auto place = [&](unsigned k, int& n, int& row, int& b, int& hd) {
-        n = (int)(k / (unsigned)rows);
+        n = (int)quotient(k, p.per_rows);
         row = (int)(k - (unsigned)n * (unsigned)rows);
-        b = row / p.H;
+        b = (int)quotient((unsigned)row, p.per_h);
         hd = row - b * p.H;
     };
     if (warp == 0) {  // loader
@@ -259,24 +244,21 @@ gated_pipe_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
         int n, row, b, hd;
         Tickets tickets{reinterpret_cast<unsigned*>(p.words), nullptr};
         LoadLedger<S> loads(full(0));
-        unsigned ahead[kAhead + 1];
-        auto take = [&](unsigned last, bool first) -> unsigned {
-            const unsigned k = first && !p.words ? blockIdx.x : tickets.take(last);
-            if (kAhead > 0 && k < p.total) {
-                place(k, n, row, b, hd);
-                const int t = (p.tiles - 1 - n) * TILE;
-                tma_prefetch_l2_4d(&mx, 0, t, hd, b);
-                if (!SHARED) tma_prefetch_l2_4d(&mg, 0, t, hd, b);
-                tma_prefetch_l2_4d(&mu_, 0, t, hd, b);
-            }
-            return k;
+        // Tickets come in order, so the tiles of the rounds ahead are known: each block
+        // asks L2 for as many tiles as it loads, whichever block will load them.
+        auto ask = [&](unsigned long long k) {
+            if (k >= p.total) return;
+            place((unsigned)k, n, row, b, hd);
+            tma_prefetch_l2_4d(&mx, 0, (p.tiles - 1 - n) * TILE, hd, b);
+            if (!SHARED) tma_prefetch_l2_4d(&mg, 0, (p.tiles - 1 - n) * TILE, hd, b);
+            tma_prefetch_l2_4d(&mu_, 0, (p.tiles - 1 - n) * TILE, hd, b);
         };
-#pragma unroll
-        for (int i = 0; i <= kAhead; ++i) ahead[i] = take(i > 0 ? ahead[i > 0 ? i - 1 : 0] : 0u, i == 0);
+        for (int r = 1; r < kFar; ++r) ask((unsigned long long)r * gridDim.x + blockIdx.x);
+        unsigned next = p.words ? tickets.take(0) : blockIdx.x;
         int ends = 0;
         for (Ring<S, 1> at(0); ends < kJoin; at.next()) {
             const int s = at.s;
-            const unsigned k = ahead[0];
+            const unsigned k = next;
             if (!wait(empty(s), at.phase ^ 1u)) break;
             if (k >= p.total) {  // one end to each group of joiners
                 info[s].n = -1;
@@ -295,48 +277,48 @@ gated_pipe_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
             tma_load_4d(smem_u32(stage(s)), &mx, 0, t, hd, b, full(s));
             if (!SHARED) tma_load_4d(smem_u32(stage(s) + kG), &mg, 0, t, hd, b, full(s));
             tma_load_4d(smem_u32(stage(s) + kUp), &mu_, 0, t, hd, b, full(s));
-#pragma unroll
-            for (int j = 0; j < kAhead; ++j) ahead[j] = ahead[j + 1];
-            ahead[kAhead] = take(ahead[kAhead], false);
+            ask((unsigned long long)kFar * gridDim.x + k);
+            // a ticket held longer than it must be holds up the tiles after it in its row
+            next = tickets.take(k);
         }
         if (abort_flag && !loads.settle()) atomicExch(p.status, (int)kDevWaitTimeout);
         return;
     }
-    constexpr int kFirstJoiner = 32 + kData, kFirstGrouper = kFirstJoiner + kJoin * LY::kJoiners;
-    if (tid >= kFirstJoiner && tid < kFirstGrouper) {  // joiners
-        const int j = (tid - kFirstJoiner) / LY::kJoiners;
-        const int ch = (tid - kFirstJoiner - j * LY::kJoiners) * kJoinCh;
+    constexpr int kFirstJoiner = 32 + kData, kFirstComposer = kFirstJoiner + kJoin * CB;
+    if (tid >= kFirstJoiner && tid < kFirstComposer) {  // joiners
+        const int j = (tid - kFirstJoiner) / CB, ch = tid - kFirstJoiner - j * CB;
         for (Ring<S, kJoin> at(j);; at.next()) {
             const int s = at.s;
             if (!wait(known(s), at.phase)) return;
             const int n = info[s].n, row = info[s].row;
             if (n >= 0) {
-                float mu[kJoinCh], h[kJoinCh];
-#pragma unroll
-                for (int q = 0; q < kJoinCh; ++q) {
-                    const bool in = ch + q < p.d;
-                    mu[q] = p.dstate_out && in ? p.dstate_out[(long long)row * p.d + ch + q] : 0.f;
-                    h[q] = in ? p.carry[((long long)row * p.tiles + (p.tiles - 1 - n)) * p.d + ch + q] : 0.f;
+                float start = 0.f, h = 0.f;
+                if (ch < p.d) {
+                    if (p.dstate_out) start = p.dstate_out[(long long)row * p.d + ch];
+                    h = p.carry[((long long)row * p.tiles + (p.tiles - 1 - n)) * p.d + ch];
                 }
                 const auto own = [&] { return wait(mapped(s), at.phase); };
-                if (!(p.words ? enter_tile(p, lb, row, n, ch, mu, own) : own())) return;
+                float mu = start;
+                if (!(p.words ? enter_tile(p, lb, row, n, ch, start, mu, own) : own())) return;
+                float2 f[RUNS];
+                float *X = plane(s, 1) + ch, *Y = plane(s, 2) + ch;
 #pragma unroll
-                for (int q = 0; q < kJoinCh; ++q) {
-                    if (p.words) publish_state(p, lb, row, n, ch + q, pass(total[s][ch + q], mu[q]));
-                    const float* A = plane(s, 0) + ch + q;
-                    float *X = plane(s, 1) + ch + q, *Y = plane(s, 2) + ch + q;
+                for (int r = 0; r < RUNS; ++r) f[r] = make_float2(plane(s, 0)[r * CB + ch], Y[r * CB]);
 #pragma unroll
-                    for (int r = 0; r < RUNS; ++r) {
-                        const float2 f = make_float2(A[r * CB], X[r * CB]);
-                        X[r * CB] = h[q];
-                        h[q] = pass(f, h[q]);
-                    }
+                for (int r = RUNS - 1; r >= 0; --r) {
+                    const float after = pass(f[r], mu);
+                    f[r].y = mu;
+                    mu = after;
+                }
+                if (p.words) publish_state(p, lb, row, n, ch, mu);  // first: tiles of other blocks wait for it
 #pragma unroll
-                    for (int r = RUNS - 1; r >= 0; --r) {
-                        const float2 f = make_float2(A[r * CB], Y[r * CB]);
-                        Y[r * CB] = mu[q];
-                        mu[q] = pass(f, mu[q]);
-                    }
+                for (int r = 0; r < RUNS; ++r) Y[r * CB] = f[r].y;
+#pragma unroll
+                for (int r = 0; r < RUNS; ++r) f[r].y = X[r * CB];
+#pragma unroll
+                for (int r = 0; r < RUNS; ++r) {
+                    X[r * CB] = h;
+                    h = pass(f[r], h);
                 }
             }
             __syncwarp();
@@ -344,37 +326,35 @@ gated_pipe_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
             if (n < 0) return;
         }
     }
-    if (tid >= kFirstGrouper && tid < kFirstGrouper + LY::kJoiners) {  // groupers
-        const int ch = (tid - kFirstGrouper) * kJoinCh;
+    if (tid >= kFirstComposer && tid < kFirstComposer + CB) {  // composers
+        const int ch = tid - kFirstComposer;
         for (Ring<S, 1> at(0);; at.next()) {
             const int s = at.s;
-            if (!wait(mapped(s), at.phase)) return;
+            if (!wait(known(s), at.phase)) return;
             const int n = info[s].n, row = info[s].row;
             if (n < 0) return;
-            float2 m[kJoinCh];
+            if (!wait(runs(s), at.phase)) return;
+            if (p.words && n + 1 < p.tiles) {
+                const float *A = plane(s, 0) + ch, *Y = plane(s, 2) + ch;
+                float2 m = make_float2(A[(RUNS - 1) * CB], Y[(RUNS - 1) * CB]);
 #pragma unroll
-            for (int q = 0; q < kJoinCh; ++q) m[q] = total[s][ch + q];
+                for (int r = RUNS - 2; r >= 0; --r) m = then(m, make_float2(A[r * CB], Y[r * CB]));
+                publish_tile(p, lb, row, n, ch, m);
+            }
             __syncwarp();
-            if ((tid & 31) == 0) mbar_arrive(empty(s));
-            if (p.words) publish_group(p, lb, row, n, ch, m);
+            if ((tid & 31) == 0) mbar_arrive(mapped(s));
         }
     }
     const bool mapper = warp < 1 + kData / 32;
     const int at = mapper ? tid - 32 : tid - (LY::kThreads - kData);
     const int lane = at % LANES, run = at / LANES;
     const int c = lane * kCh, nc = p.d - c;
-    int ends = 0;
     for (Ring<S, 1> ring(0);; ring.next()) {
         const int s = ring.s;
         const uint32_t phase = ring.phase;
         if (!wait(mapper ? known(s) : joined(s), phase)) return;
         const int n = info[s].n;
-        if (n < 0) {
-            if (!mapper) return;
-            if (at < CB && (tid & 31) == 0) mbar_arrive(mapped(s));
-            if (++ends == kJoin) return;
-            continue;
-        }
+        if (n < 0) return;
         const int t0 = info[s].t0 + run * kTok;
         const int nt = nc > 0 ? min(kTok, p.T - t0) : 0;
         unsigned resets = 0;  // asked for while the tile is loaded
@@ -449,17 +429,6 @@ gated_pipe_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
             *reinterpret_cast<float4*>(plane(s, 2) + o) = make_float4(Y[0], Y[1], Y[2], Y[3]);
             __syncwarp();
             if ((tid & 31) == 0) mbar_arrive(runs(s));
-            if (at < CB) {  // one channel of the tile's map of mu, from its last run to its first
-                if (!wait(runs(s), phase)) return;
-                const float *pA = plane(s, 0) + at, *pY = plane(s, 2) + at;
-                float2 m = make_float2(pA[(RUNS - 1) * CB], pY[(RUNS - 1) * CB]);
-#pragma unroll
-                for (int r = RUNS - 2; r >= 0; --r) m = then(m, make_float2(pA[r * CB], pY[r * CB]));
-                if (p.words) publish_tile(p, lb, info[s].row, n, at, m);
-                total[s][at] = m;
-                __syncwarp();
-                if ((tid & 31) == 0) mbar_arrive(mapped(s));
-            }
         } else {
             float h[kCh], mu[kCh];
             four(plane(s, 1) + run * CB + c, h);
