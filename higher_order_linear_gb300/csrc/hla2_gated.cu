@@ -161,14 +161,15 @@ struct PipeLayout {
     static constexpr int kFit = (int)((225 * 1024 - kMaps * kSlots) / kStage);
     static constexpr int kStages = kFit > 8 ? 8 : kFit;
     static constexpr uint32_t kBytes = kStage * kStages + kMaps * kSlots + 128;  // and alignment to 128 bytes
-    static constexpr int kThreads = 32 + kData + (kJoin + 1) * CB + kData;
+    static constexpr int kJoin = kSlots < kMostJoin ? kSlots : kMostJoin;
+    static constexpr int kThreads = 32 + kData + kJoin * CB + CB / 2 + kData;
 };
 
 template <typename T, bool SIG, bool SHARED, int LANES>
 __global__ void __launch_bounds__(PipeLayout<T, SHARED, LANES>::kThreads, 1)
 gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mg, const GateParams p) {
     using LY = PipeLayout<T, SHARED, LANES>;
-    constexpr int CB = LY::CB, RUNS = LY::RUNS, TILE = LY::TILE, S = LY::kStages, M = LY::kSlots;
+    constexpr int CB = LY::CB, RUNS = LY::RUNS, TILE = LY::TILE, S = LY::kStages, M = LY::kSlots, kJoin = LY::kJoin;
     extern __shared__ __align__(128) unsigned char raw[];
     __shared__ __align__(8) unsigned long long bars[5 * S + 2 * M];
     static_assert(S >= kJoin, "the ends of the tickets take a stage for each group of joiners");
@@ -191,7 +192,7 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
         abort_flag = 0;
         for (int s = 0; s < S; ++s) {
             mbar_init(full(s), 1);
-            mbar_init(mapped(s), CB / 32);
+            mbar_init(mapped(s), CB / 64);
             mbar_init(joined(s), CB / 32);
             mbar_init(empty(s), kData / 32);
             mbar_init(known(s), 1);
@@ -266,30 +267,37 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
             if (n >= 0) {
                 const float start = p.state_in && ch < p.d ? p.state_in[(long long)row * p.d + ch] : 0.f;
                 const auto own = [&] { return wait(mapped(s), at.phase); };
-                float h = start;
-                if (!(p.words ? enter_tile(p, lb, row, n, ch, start, h, own) : own())) return;
-                if (p.carry && ch < p.d) p.carry[((long long)row * p.tiles + n) * p.d + ch] = h;
-                float2* m = maps(slot.s) + ch;
                 float2 f[RUNS];
+                u64 w[kGroup - 1];
+                if (!(p.words ? maps_before(p, lb, row, n, ch, w, own) : own())) return;
+                float2* m = maps(slot.s) + ch;
 #pragma unroll
                 for (int r = 0; r < RUNS; ++r) f[r] = m[r * CB];
+                float h = start;
+                if (p.words && ends_group(lb, n)) {
+                    float2 all = compose(w, kGroup - 1);
+#pragma unroll
+                    for (int r = 0; r < RUNS; ++r) all = then(all, f[r]);
+                    h = group_state(p, lb, row, n, ch, start);
+                    publish_state(p, lb, row, n, ch, pass(all, h));  // first: tiles of other blocks wait for it
+                } else if (p.words) {
+                    h = group_state(p, lb, row, n, ch, start);
+                }
+                if (p.words) h = pass_all(w, n % kGroup, h);
+                if (p.carry && ch < p.d) p.carry[((long long)row * p.tiles + n) * p.d + ch] = h;
 #pragma unroll
                 for (int r = 0; r < RUNS; ++r) {
-                    const float after = pass(f[r], h);
-                    f[r].x = h;
-                    h = after;
+                    m[r * CB].x = h;
+                    h = pass(f[r], h);
                 }
-                if (p.words) publish_state(p, lb, row, n, ch, h);  // first: tiles of other blocks wait for it
-#pragma unroll
-                for (int r = 0; r < RUNS; ++r) m[r * CB].x = f[r].x;
             }
             __syncwarp();
             if ((tid & 31) == 0) mbar_arrive(joined(s));
             if (n < 0) return;
         }
     }
-    if (tid >= kFirstComposer && tid < kFirstComposer + CB) {  // composers
-        const int ch = tid - kFirstComposer;
+    if (tid >= kFirstComposer && tid < kFirstComposer + CB / 2) {  // composers: two channels to a thread
+        const int ch = (tid - kFirstComposer) * 2;
         Ring<M, 1> slot(0);
         for (Ring<S, 1> at(0);; at.next(), slot.next()) {
             const int s = at.s;
@@ -298,10 +306,15 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
             if (n < 0) return;
             if (!wait(runs(slot.s), slot.phase)) return;
             if (p.words && n + 1 < p.tiles) {
-                float2 m = maps(slot.s)[ch];
+                float2 m[2];
 #pragma unroll
-                for (int r = 1; r < RUNS; ++r) m = then(m, maps(slot.s)[r * CB + ch]);
-                publish_tile(p, lb, row, n, ch, m);
+                for (int r = 0; r < RUNS; ++r) {
+                    const float4 f = *reinterpret_cast<const float4*>(maps(slot.s) + r * CB + ch);
+                    m[0] = r ? then(m[0], make_float2(f.x, f.y)) : make_float2(f.x, f.y);
+                    m[1] = r ? then(m[1], make_float2(f.z, f.w)) : make_float2(f.z, f.w);
+                }
+                publish_tile(p, lb, row, n, ch, m[0]);
+                publish_tile(p, lb, row, n, ch + 1, m[1]);
             }
             __syncwarp();
             if ((tid & 31) == 0) mbar_arrive(mapped(s));

@@ -147,42 +147,63 @@ __device__ __forceinline__ void publish_tile(const GateParams& p, const Lookback
     if (n + 1 < lb.tiles) st_pair(p.words + lb.tile_map(row, n) + ch, m);
 }
 
-// The state that enters tile n, for one channel; `start` is the one that enters the
-// sequence.  `mapped()` is called between the first look at the words and the
-// waiting for those that are missing: it waits for the tile's own map (false: give
-// up), by which time the tiles before it have theirs too; polling from the start
+// What enters tile n, for one channel.  First the maps w of the tiles of its group
+// before it: `mapped()` is called between the first look at their words and the
+// waiting for those that are missing; it waits for the tile's own map (false: give
+// up), by which time the tiles before it have theirs too.  Polling from the start
 // took more of the L2's bandwidth than the data.
 template <typename F>
-__device__ __forceinline__ bool enter_tile(const GateParams& p, const Lookback& lb, int row, int n, int ch, float start,
-                                           float& h, F&& mapped) {
-    const int g = n / kGroup, nt = n % kGroup;  // nt: tiles before this one in its group
-    u64 w[kGroup - 1], u[1];
-    const u64* const state = p.words + lb.state(row, g) + ch;
+__device__ __forceinline__ bool maps_before(const GateParams& p, const Lookback& lb, int row, int n, int ch,
+                                            u64 (&w)[kGroup - 1], F&& mapped) {
+    const int nt = n % kGroup;
     const u64* const tiles = p.words + lb.tile_map(row, n - nt) + ch;
-    ask_words(state, 0, g > 0 ? 1 : 0, u);
     ask_words(tiles, lb.cb, nt, w);
     if (!mapped()) return false;
-    wait_words(p, state, 0, u);
     wait_words(p, tiles, lb.cb, w);
-    h = g > 0 ? as_pair(u[0]).x : start;
+    return true;
+}
+__device__ __forceinline__ float2 compose(const u64 (&w)[kGroup - 1], int nt) {
+    float2 m = make_float2(1.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kGroup - 1; ++i)
+        if (i < nt) m = then(m, as_pair(w[i]));
+    return m;
+}
+__device__ __forceinline__ float pass_all(const u64 (&w)[kGroup - 1], int nt, float h) {
 #pragma unroll
     for (int i = 0; i < kGroup - 1; ++i)
         if (i < nt) h = pass(as_pair(w[i]), h);
-    return true;
+    return h;
+}
+// Then the state that enters the group (`start` enters the sequence), waited for
+// last: from group to group only this passes, so the tile that ends a group has
+// composed all that it can before it comes.
+__device__ __forceinline__ float group_state(const GateParams& p, const Lookback& lb, int row, int n, int ch,
+                                             float start) {
+    const int g = n / kGroup;
+    if (g == 0) return start;
+    u64 u[1];
+    const u64* const state = p.words + lb.state(row, g) + ch;
+    ask_words(state, 0, 1, u);
+    wait_words(p, state, 0, u);
+    return as_pair(u[0]).x;
 }
 
+__device__ __forceinline__ bool ends_group(const Lookback& lb, int n) {
+    return n % kGroup == kGroup - 1 && n + 1 < lb.tiles;
+}
 // Publishes the state `h` after tile n where the tile ends a group.
 __device__ __forceinline__ void publish_state(const GateParams& p, const Lookback& lb, int row, int n, int ch, float h) {
-    if (n % kGroup == kGroup - 1 && n + 1 < lb.tiles)
-        st_pair(p.words + lb.state(row, n / kGroup + 1) + ch, make_float2(h, 0.f));
+    if (ends_group(lb, n)) st_pair(p.words + lb.state(row, n / kGroup + 1) + ch, make_float2(h, 0.f));
 }
 
 // One channel's part in the register kernels: publishes the tile's map, returns the state that enters it.
 __device__ __forceinline__ float join_tile(const GateParams& p, const Lookback& lb, int row, int n, int ch, float2 m,
                                            float start) {
     publish_tile(p, lb, row, n, ch, m);
-    float h;
-    enter_tile(p, lb, row, n, ch, start, h, [] { return true; });
+    u64 w[kGroup - 1];
+    maps_before(p, lb, row, n, ch, w, [] { return true; });
+    const float h = pass_all(w, n % kGroup, group_state(p, lb, row, n, ch, start));
     publish_state(p, lb, row, n, ch, pass(m, h));
     return h;
 }
@@ -228,7 +249,7 @@ struct Run {
 };
 
 // ---- the pipelined kernels ---------------------------------------------------
-constexpr int kJoin = 2;    // sets of joiners, every kJoin-th tile each
+constexpr int kMostJoin = 3;  // sets of joiners, every so-many-th tile each
 constexpr int kFar = 2;     // tiles are asked into L2 this many rounds of the grid ahead
 constexpr unsigned kNapNs = 40;
 

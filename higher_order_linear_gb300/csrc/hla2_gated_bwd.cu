@@ -189,7 +189,8 @@ struct BackLayout {
     static constexpr int kFit = (int)((222 * 1024 - kBefore) / kStage);
     static constexpr int kStages = kFit > 6 ? 6 : kFit;
     static constexpr uint32_t kBytes = kStage * kStages + kBefore + 128;
-    static constexpr int kThreads = 32 + kData + (kJoin + 1) * CB + kData;
+    static constexpr int kJoin = kStages < kMostJoin ? kStages : kMostJoin;
+    static constexpr int kThreads = 32 + kData + kJoin * CB + CB / 2 + kData;
 };
 
 template <typename TO, bool SIG, bool SHARED, int LANES>
@@ -198,7 +199,7 @@ gated_pipe_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
                       const __grid_constant__ CUtensorMap mu_, const GateParams p) {
     using T = bf16;
     using LY = BackLayout<TO, SHARED, LANES>;
-    constexpr int CB = LY::CB, RUNS = LY::RUNS, TILE = LY::TILE, S = LY::kStages, NG = SHARED ? 1 : kCh;
+    constexpr int CB = LY::CB, RUNS = LY::RUNS, TILE = LY::TILE, S = LY::kStages, kJoin = LY::kJoin, NG = SHARED ? 1 : kCh;
     extern __shared__ __align__(128) unsigned char raw[];
     __shared__ __align__(8) unsigned long long bars[6 * S];
     static_assert(S >= kJoin, "the ends of the tickets take a stage for each group of joiners");
@@ -221,7 +222,7 @@ gated_pipe_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
         abort_flag = 0;
         for (int s = 0; s < S; ++s) {
             mbar_init(full(s), 1);
-            mbar_init(mapped(s), CB / 32);
+            mbar_init(mapped(s), CB / 64);
             mbar_init(joined(s), CB / 32);
             mbar_init(empty(s), kData / 32);
             mbar_init(runs(s), kData / 32);
@@ -298,27 +299,34 @@ gated_pipe_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
                     h = p.carry[((long long)row * p.tiles + (p.tiles - 1 - n)) * p.d + ch];
                 }
                 const auto own = [&] { return wait(mapped(s), at.phase); };
-                float mu = start;
-                if (!(p.words ? enter_tile(p, lb, row, n, ch, start, mu, own) : own())) return;
                 float2 f[RUNS];
+                u64 w[kGroup - 1];
+                if (!(p.words ? maps_before(p, lb, row, n, ch, w, own) : own())) return;
                 float *X = plane(s, 1) + ch, *Y = plane(s, 2) + ch;
 #pragma unroll
-                for (int r = 0; r < RUNS; ++r) f[r] = make_float2(plane(s, 0)[r * CB + ch], Y[r * CB]);
-#pragma unroll
-                for (int r = RUNS - 1; r >= 0; --r) {
-                    const float after = pass(f[r], mu);
-                    f[r].y = mu;
-                    mu = after;
-                }
-                if (p.words) publish_state(p, lb, row, n, ch, mu);  // first: tiles of other blocks wait for it
-#pragma unroll
-                for (int r = 0; r < RUNS; ++r) Y[r * CB] = f[r].y;
-#pragma unroll
-                for (int r = 0; r < RUNS; ++r) f[r].y = X[r * CB];
+                for (int r = 0; r < RUNS; ++r) f[r] = make_float2(plane(s, 0)[r * CB + ch], X[r * CB]);
 #pragma unroll
                 for (int r = 0; r < RUNS; ++r) {
                     X[r * CB] = h;
                     h = pass(f[r], h);
+                }
+#pragma unroll
+                for (int r = 0; r < RUNS; ++r) f[r].y = Y[r * CB];
+                float mu = start;
+                if (p.words && ends_group(lb, n)) {
+                    float2 all = compose(w, kGroup - 1);
+#pragma unroll
+                    for (int r = RUNS - 1; r >= 0; --r) all = then(all, f[r]);
+                    mu = group_state(p, lb, row, n, ch, start);
+                    publish_state(p, lb, row, n, ch, pass(all, mu));  // first: tiles of other blocks wait for it
+                } else if (p.words) {
+                    mu = group_state(p, lb, row, n, ch, start);
+                }
+                if (p.words) mu = pass_all(w, n % kGroup, mu);
+#pragma unroll
+                for (int r = RUNS - 1; r >= 0; --r) {
+                    Y[r * CB] = mu;
+                    mu = pass(f[r], mu);
                 }
             }
             __syncwarp();
@@ -326,8 +334,8 @@ gated_pipe_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
             if (n < 0) return;
         }
     }
-    if (tid >= kFirstComposer && tid < kFirstComposer + CB) {  // composers
-        const int ch = tid - kFirstComposer;
+    if (tid >= kFirstComposer && tid < kFirstComposer + CB / 2) {  // composers: two channels to a thread
+        const int ch = (tid - kFirstComposer) * 2;
         for (Ring<S, 1> at(0);; at.next()) {
             const int s = at.s;
             if (!wait(known(s), at.phase)) return;
@@ -336,10 +344,16 @@ gated_pipe_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
             if (!wait(runs(s), at.phase)) return;
             if (p.words && n + 1 < p.tiles) {
                 const float *A = plane(s, 0) + ch, *Y = plane(s, 2) + ch;
-                float2 m = make_float2(A[(RUNS - 1) * CB], Y[(RUNS - 1) * CB]);
+                float2 m[2];
 #pragma unroll
-                for (int r = RUNS - 2; r >= 0; --r) m = then(m, make_float2(A[r * CB], Y[r * CB]));
-                publish_tile(p, lb, row, n, ch, m);
+                for (int r = RUNS - 1; r >= 0; --r) {  // from the tile's last run to its first
+                    const float2 a = *reinterpret_cast<const float2*>(A + r * CB);
+                    const float2 y = *reinterpret_cast<const float2*>(Y + r * CB);
+                    m[0] = r < RUNS - 1 ? then(m[0], make_float2(a.x, y.x)) : make_float2(a.x, y.x);
+                    m[1] = r < RUNS - 1 ? then(m[1], make_float2(a.y, y.y)) : make_float2(a.y, y.y);
+                }
+                publish_tile(p, lb, row, n, ch, m[0]);
+                publish_tile(p, lb, row, n, ch + 1, m[1]);
             }
             __syncwarp();
             if ((tid & 31) == 0) mbar_arrive(mapped(s));
