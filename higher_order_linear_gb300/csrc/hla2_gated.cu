@@ -162,7 +162,7 @@ struct PipeLayout {
     static constexpr int kStages = kFit > 8 ? 8 : kFit;
     static constexpr uint32_t kBytes = kStage * kStages + kMaps * kSlots + 128;  // and alignment to 128 bytes
     static constexpr int kJoin = kSlots < kMostJoin ? kSlots : kMostJoin;
-    static constexpr int kThreads = 32 + kData + kJoin * CB + CB / 2 + kData;
+    static constexpr int kThreads = 32 + kData + kJoin * CB + kComposers + kData;
 };
 
 template <typename T, bool SIG, bool SHARED, int LANES>
@@ -192,7 +192,7 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
         abort_flag = 0;
         for (int s = 0; s < S; ++s) {
             mbar_init(full(s), 1);
-            mbar_init(mapped(s), CB / 64);
+            mbar_init(mapped(s), kComposers / 32);
             mbar_init(joined(s), CB / 32);
             mbar_init(empty(s), kData / 32);
             mbar_init(known(s), 1);
@@ -296,8 +296,9 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
             if (n < 0) return;
         }
     }
-    if (tid >= kFirstComposer && tid < kFirstComposer + CB / 2) {  // composers: two channels to a thread
-        const int ch = (tid - kFirstComposer) * 2;
+    if (tid >= kFirstComposer && tid < kFirstComposer + kComposers) {  // composers: N channels to a thread
+        constexpr int N = CB / kComposers;
+        const int ch = (tid - kFirstComposer) * N;
         Ring<M, 1> slot(0);
         for (Ring<S, 1> at(0);; at.next(), slot.next()) {
             const int s = at.s;
@@ -306,15 +307,16 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
             if (n < 0) return;
             if (!wait(runs(slot.s), slot.phase)) return;
             if (p.words && n + 1 < p.tiles) {
-                float2 m[2];
+                float2 m[N];
 #pragma unroll
-                for (int r = 0; r < RUNS; ++r) {
-                    const float4 f = *reinterpret_cast<const float4*>(maps(slot.s) + r * CB + ch);
-                    m[0] = r ? then(m[0], make_float2(f.x, f.y)) : make_float2(f.x, f.y);
-                    m[1] = r ? then(m[1], make_float2(f.z, f.w)) : make_float2(f.z, f.w);
-                }
-                publish_tile(p, lb, row, n, ch, m[0]);
-                publish_tile(p, lb, row, n, ch + 1, m[1]);
+                for (int r = 0; r < RUNS; ++r)
+#pragma unroll
+                    for (int q = 0; q < N; ++q) {
+                        const float2 f = maps(slot.s)[r * CB + ch + q];
+                        m[q] = r ? then(m[q], f) : f;
+                    }
+#pragma unroll
+                for (int q = 0; q < N; ++q) publish_tile(p, lb, row, n, ch + q, m[q]);
             }
             __syncwarp();
             if ((tid & 31) == 0) mbar_arrive(mapped(s));

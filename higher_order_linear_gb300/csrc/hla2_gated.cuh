@@ -249,6 +249,7 @@ struct Run {
 };
 
 // ---- the pipelined kernels ---------------------------------------------------
+constexpr int kComposers = 64;
 constexpr int kMostJoin = 3;  // sets of joiners, every so-many-th tile each
 constexpr int kFar = 2;     // tiles are asked into L2 this many rounds of the grid ahead
 constexpr unsigned kNapNs = 40;

@@ -190,7 +190,7 @@ struct BackLayout {
     static constexpr int kStages = kFit > 6 ? 6 : kFit;
     static constexpr uint32_t kBytes = kStage * kStages + kBefore + 128;
     static constexpr int kJoin = kStages < kMostJoin ? kStages : kMostJoin;
-    static constexpr int kThreads = 32 + kData + kJoin * CB + CB / 2 + kData;
+    static constexpr int kThreads = 32 + kData + kJoin * CB + kComposers + kData;
 };
 
 template <typename TO, bool SIG, bool SHARED, int LANES>
@@ -222,7 +222,7 @@ gated_pipe_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
         abort_flag = 0;
         for (int s = 0; s < S; ++s) {
             mbar_init(full(s), 1);
-            mbar_init(mapped(s), CB / 64);
+            mbar_init(mapped(s), kComposers / 32);
             mbar_init(joined(s), CB / 32);
             mbar_init(empty(s), kData / 32);
             mbar_init(runs(s), kData / 32);
@@ -334,8 +334,9 @@ gated_pipe_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
             if (n < 0) return;
         }
     }
-    if (tid >= kFirstComposer && tid < kFirstComposer + CB / 2) {  // composers: two channels to a thread
-        const int ch = (tid - kFirstComposer) * 2;
+    if (tid >= kFirstComposer && tid < kFirstComposer + kComposers) {  // composers: N channels to a thread
+        constexpr int N = CB / kComposers;
+        const int ch = (tid - kFirstComposer) * N;
         for (Ring<S, 1> at(0);; at.next()) {
             const int s = at.s;
             if (!wait(known(s), at.phase)) return;
@@ -344,16 +345,16 @@ gated_pipe_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
             if (!wait(runs(s), at.phase)) return;
             if (p.words && n + 1 < p.tiles) {
                 const float *A = plane(s, 0) + ch, *Y = plane(s, 2) + ch;
-                float2 m[2];
+                float2 m[N];
 #pragma unroll
-                for (int r = RUNS - 1; r >= 0; --r) {  // from the tile's last run to its first
-                    const float2 a = *reinterpret_cast<const float2*>(A + r * CB);
-                    const float2 y = *reinterpret_cast<const float2*>(Y + r * CB);
-                    m[0] = r < RUNS - 1 ? then(m[0], make_float2(a.x, y.x)) : make_float2(a.x, y.x);
-                    m[1] = r < RUNS - 1 ? then(m[1], make_float2(a.y, y.y)) : make_float2(a.y, y.y);
-                }
-                publish_tile(p, lb, row, n, ch, m[0]);
-                publish_tile(p, lb, row, n, ch + 1, m[1]);
+                for (int r = RUNS - 1; r >= 0; --r)  // from the tile's last run to its first
+#pragma unroll
+                    for (int q = 0; q < N; ++q) {
+                        const float2 f = make_float2(A[r * CB + q], Y[r * CB + q]);
+                        m[q] = r < RUNS - 1 ? then(m[q], f) : f;
+                    }
+#pragma unroll
+                for (int q = 0; q < N; ++q) publish_tile(p, lb, row, n, ch + q, m[q]);
             }
             __syncwarp();
             if ((tid & 31) == 0) mbar_arrive(mapped(s));
