@@ -9,6 +9,7 @@ missing or cannot be loaded, every call raises: there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -538,7 +539,17 @@ def hla2_decay_step(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: to
 _GATE_FORMS = {"sigmoid": 0, "decay": 1}
 _CODES = {torch.float32: HLA2_DTYPE_F32, torch.bfloat16: HLA2_DTYPE_BF16}
 _F32 = torch.float32
-_LL3, _LL4, _LL9, _LL14, _LL15 = (ctypes.c_longlong * n for n in (3, 4, 9, 14, 15))
+
+
+@functools.lru_cache(maxsize=256)
+def _longs(*values):
+    """Strides as the C entries take them (read only: the same values share one array)."""
+    return (ctypes.c_longlong * len(values))(*values)
+
+
+@functools.lru_cache(maxsize=64)
+def _ints(*values):
+    return (ctypes.c_int * len(values))(*values)
 
 
 class _NoGuard:
@@ -691,7 +702,7 @@ def hla2_gated_scan(X: torch.Tensor, G: torch.Tensor, O: torch.Tensor | None = N
         workspace, nws = _gated_work(L, workspace, B, H, T, d, dev)
         rc = L.hla2_gated_scan(X.data_ptr(), G.data_ptr(), _ptr(reset), _ptr(state_in), O.data_ptr(),
                                _ptr(state_out), _ptr(carry), B, H, T, d,
-                               _LL9(*X.stride()[:3], *G.stride()[:3], *O.stride()[:3]), fcode, shared, code, ocode,
+                               _longs(*X.stride()[:3], *G.stride()[:3], *O.stride()[:3]), fcode, shared, code, ocode,
                                _ptr(workspace), nws, _raw(dev, stream))
     if rc:
         _check(rc, "hla2_gated_scan")
@@ -731,7 +742,7 @@ def hla2_gated_scan_backward(X: torch.Tensor, G: torch.Tensor, dO: torch.Tensor,
         workspace, nws = _gated_work(L, workspace, B, H, T, d, dev)
         rc = L.hla2_gated_scan_backward(X.data_ptr(), G.data_ptr(), _ptr(reset), carry.data_ptr(), dO.data_ptr(),
                                         _ptr(dstate_out), dX.data_ptr(), dG.data_ptr(), _ptr(dstate_in), B, H, T, d,
-                                        _LL15(*X.stride()[:3], *G.stride()[:3], *dO.stride()[:3], *dX.stride()[:3],
+                                        _longs(*X.stride()[:3], *G.stride()[:3], *dO.stride()[:3], *dX.stride()[:3],
                                               *dG.stride()[:3]), fcode, shared, code, ocode, _ptr(workspace), nws,
                                         _raw(dev, stream))
     if rc:
@@ -785,7 +796,7 @@ def hla2_gated_step(state: torch.Tensor, x: torch.Tensor, g: torch.Tensor, o: to
             o = torch.empty(shape, device=dev, dtype=out_dtype)
         rc = L.hla2_gated_step(state.data_ptr(), x.data_ptr(), g.data_ptr(), o.data_ptr(),
                                None if state_out is None else state_out.data_ptr(), n, d,
-                               _LL3(x.stride(0), g.stride(0), o.stride(0)), fcode, g.dim() == 1, _CODES[dt], ocode,
+                               _longs(x.stride(0), g.stride(0), o.stride(0)), fcode, g.dim() == 1, _CODES[dt], ocode,
                                _raw(dev, stream))
     if rc:
         _check(rc, "hla2_gated_step")
@@ -947,7 +958,7 @@ def hla2_rmsnorm_backward(S: torch.Tensor, dY: torch.Tensor, weight: torch.Tenso
                 workspace = torch.empty(L.hla2_rmsnorm_backward_workspace(rows, C), device=dev, dtype=torch.uint8)
             nws = workspace.numel() * workspace.element_size()
         rc = L.hla2_rmsnorm_backward(S.data_ptr(), dY.data_ptr(), wptr, _ptr(dS), dX.data_ptr(), _ptr(dW), rows, C,
-                                     _LL4(lds, ldy, ldd, _rows(dX, "dX")), eps, code, wcode, ycode, _ptr(workspace),
+                                     _longs(lds, ldy, ldd, _rows(dX, "dX")), eps, code, wcode, ycode, _ptr(workspace),
                                      nws, _raw(dev, stream))
     if rc:
         _check(rc, "hla2_rmsnorm_backward")
@@ -996,9 +1007,15 @@ def hla2_rotary(Q: torch.Tensor, pos: torch.Tensor, freq: torch.Tensor, sections
     ``interleaved``.  OQ and OK may be Q and K; those not given take the memory
     order of their input.  Returns (OQ, OK)."""
     sections = tuple(sections)
-    _rotary_checks(Q, pos, freq, sections, K, OQ, OK)
-    B, H, T, d = Q.shape
-    dev, axes = Q.device, len(sections)
+    shape, dt, dev, axes = Q.shape, Q.dtype, Q.device, len(sections)
+    if not (Q.is_cuda and len(shape) == 4 and dt in _CODES and Q.stride(3) == 1 and OQ is None and OK is None and
+            pos.dtype is torch.int32 and pos.shape == (axes, shape[0], shape[2]) and pos.is_contiguous() and
+            pos.device == dev and freq.dtype is _F32 and freq.shape == (sum(sections),) and freq.is_contiguous() and
+            freq.device == dev and
+            (K is None or (K.dtype is dt and K.device == dev and K.dim() == 4 and K.stride(3) == 1 and
+                           K.shape[0] == shape[0] and K.shape[2:] == shape[2:]))):
+        _rotary_checks(Q, pos, freq, sections, K, OQ, OK)
+    B, H, T, d = shape
     L = _lib or lib()
     with _guard(dev, stream):
         if OQ is None:
@@ -1007,16 +1024,16 @@ def hla2_rotary(Q: torch.Tensor, pos: torch.Tensor, freq: torch.Tensor, sections
         pb = sp[1] if len(sp) == 3 else 0
         if K is None:
             HK, pk, po = 0, None, None
-            st = _LL14(sq[0], sq[1], sq[2], so[0], so[1], so[2], 0, 0, 0, 0, 0, 0, sp[0], pb)
+            st = _longs(sq[0], sq[1], sq[2], so[0], so[1], so[2], 0, 0, 0, 0, 0, 0, sp[0], pb)
         else:
             if OK is None:
                 OK = torch.empty_like(K)
             HK, pk, po = K.shape[1], K.data_ptr(), OK.data_ptr()
             sk, sl = K.stride(), OK.stride()
-            st = _LL14(sq[0], sq[1], sq[2], so[0], so[1], so[2], sk[0], sk[1], sk[2], sl[0], sl[1], sl[2], sp[0], pb)
+            st = _longs(sq[0], sq[1], sq[2], so[0], so[1], so[2], sk[0], sk[1], sk[2], sl[0], sl[1], sl[2], sp[0], pb)
         rc = L.hla2_rotary(Q.data_ptr(), OQ.data_ptr(), pk, po, pos.data_ptr(), freq.data_ptr(), B, H, HK, T, d,
-                           2 * freq.numel(), axes, (ctypes.c_int * axes)(*sections), bool(interleaved), bool(inverse),
-                           st, _CODES[Q.dtype], _raw(dev, stream))
+                           2 * freq.numel(), axes, _ints(*sections), bool(interleaved), bool(inverse),
+                           st, _CODES[dt], _raw(dev, stream))
     if rc:
         _check(rc, "hla2_rotary")
     return OQ, OK
