@@ -189,7 +189,7 @@ struct BackLayout {
     static constexpr int kFit = (int)((222 * 1024 - kBefore) / kStage);
     static constexpr int kStages = kFit > 6 ? 6 : kFit;
     static constexpr uint32_t kBytes = kStage * kStages + kBefore + 128;
-    static constexpr int kJoin = kStages < kMostJoin ? kStages : kMostJoin;
+    static constexpr int kJoin = 2;  // a third set would take registers that the writers need
     static constexpr int kThreads = 32 + kData + kJoin * CB + kComposers + kData;
 };
 
