@@ -13,30 +13,40 @@
 //   decay:   dx = lam,    dg = lam h_{t-1}
 //   sigmoid: dx = z lam,  dg = z (1 - z) lam (h_{t-1} - x)
 //
-// One pass over the data.  A run of tokens maps the state before it to the
-// state after it by h -> A h + X, and such maps compose, so a tile of tokens
-// can be read once, long before the state that enters it is known:
-//   - a block holds a tile in registers: a thread 4 channels of kTok tokens, a
-//     "run"; the runs' maps are composed in shared memory;
-//   - the tile's map goes to the workspace; the state that enters the tile is
-//     the state that entered its super-group of 128 tiles, passed through the
-//     maps of the groups of 8 tiles, then of the tiles, before it; warps of their
-//     own do this, so that no thread holds its tokens and these maps at once;
-//   - every thread then walks its tokens again, from registers, from the state
-//     that enters its run.
-// Tiles are taken by ticket, all heads' first tiles first, so whoever waits
-// waits for a tile that a running block holds.  Which maps are composed, and in
-// which order, depends on the tile's place alone: the same call gives the same
-// bits, whatever the timing.  The last tile of a group publishes the group's
-// map and the last of a super-group the state after it, so a tile reads at most
-// 22 maps and one state, and the only chain along the sequence has one link for
-// each 128 tiles.
+// One pass over the data.  A run of tokens maps the state before it to the state
+// after it by h -> A h + X, and such maps compose, so a tile of tokens can be read
+// once, long before the state that enters it is known: the maps of its runs are
+// composed to the tile's, which goes to the workspace; the state that enters the
+// tile is the state that entered its group of 8 tiles, passed through the maps of
+// the tiles before it in the group; and the tokens are walked again, on chip, from
+// the state that enters each run.
+//
+// Tiles are taken by ticket, all heads' first tiles first, so whoever waits waits
+// for a tile that a running block holds.  Which maps are passed, and in which
+// order, depends on the tile's place alone: the same call gives the same bits,
+// whatever the timing.  Along the sequence one state for each group is handed on.
+//
+// What bounds it.  Forward of 1 x 16 x 65536 x 128, 16-bit in, 32-bit out (1.07 GB,
+// 158 us at the copy bandwidth of 6.8 TB/s): 185 us, 0.85 of it; 16-bit out
+// (0.81 GB, 118 us): 164 us.  An earlier stand of the pipeline took 170 us with the
+// waits between blocks left out: they cost the rest, by the way of a state from
+// group to group, about 1.3 us a hop through L2, and by the maps to be read for
+// each tile (groups of 6 tiles took 215 us where 8 took 200, 12 211 and 16 237, all
+// before the last two steps below).  Steps, same sizes: a
+// thread to a channel, token by token, 34.7 ms; tiles in registers, flags beside
+// the maps, 0.78 ms; a map that is its own flag 0.48 ms; tiles by bulk copies into
+// a ring and a warp to a role 0.33 ms; the gate as a power of two and a reciprocal
+// 0.24 ms; joiners apart from composers, three sets of them, 0.20 ms; the state
+// waited for last and handed on first 0.185 ms.
 #include "hla2_gated.cuh"
 
 namespace hla2 {
 namespace {
 
-// ---- forward -----------------------------------------------------------------
+// ---- forward in registers: operands that bulk tensor copies do not take ---------
+// (strides or addresses that are no multiple of 16 bytes).  A block holds a tile in
+// registers, 4 channels of 8 tokens to a thread; warps of their own join tiles, so
+// that no thread holds its tokens and the maps of other tiles at once.
 // LANES x 4 channels to a token, kData / LANES runs of kTok tokens to a tile.
 template <typename T, bool SIG, bool SHARED, int LANES>
 __global__ void __launch_bounds__(block_threads(LANES), 1)
@@ -141,11 +151,12 @@ gated_scan_kernel(const GateParams p) {
 // of a block wait for the states that enter them while others are loaded,
 // mapped and written.  Warps have one role each and meet on mbarriers:
 //   loader   takes tickets and loads tiles of x (and gates) by bulk tensor copies;
-//   mappers  form the maps of the tile's runs, compose and publish the tile's map;
-//   joiners  (kJoin sets, every kJoin-th tile each) find the state that enters
-//            the tile and from it the state that enters each run;
-//   groupers publish the maps of the groups that the block's tiles end: warps of
-//            their own, so that no group's map waits behind a joiner's waits;
+//   mappers  form the maps of the tile's runs;
+//   composers compose them to the tile's map and publish it;
+//   joiners  (three sets, every third tile each: one waits about 3 us for other
+//            blocks, a tile has 1.5 us) find the state that enters the tile, hand on
+//            the one that leaves a group, and leave in each run's entry the state
+//            that enters it;
 //   writers  walk the runs again and write the outputs.
 // Every wait is bounded in time, as in the other kernels of this library.
 
