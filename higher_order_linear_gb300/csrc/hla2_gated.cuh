@@ -5,6 +5,7 @@
 
 #include <map>
 #include <mutex>
+#include <new>
 
 #include "hla2_layer.cuh"
 #include "hla2_tc_common.cuh"
@@ -395,8 +396,11 @@ cudaError_t persistent_blocks(const void* kernel, int threads, size_t smem, unsi
         int per_sm = 0;
         if (cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem)) return e;
         fit = (unsigned)(per_sm > 0 ? per_sm : 1) * (unsigned)sm_count();
-        std::lock_guard<std::mutex> lk(mu);
-        known[{kernel, dev}] = fit;
+        try {
+            std::lock_guard<std::mutex> lk(mu);
+            known[{kernel, dev}] = fit;
+        } catch (const std::bad_alloc&) {  // not remembered: nothing leaves a C entry as an exception
+        }
     }
     *blocks = total < fit ? total : fit;
     return cudaSuccess;

@@ -17,7 +17,9 @@
 // for tiles of other blocks 2.6, writing 1.7) and shared memory holds three, so one
 // leaves every 2.5 to 2.9 us against 1.8 us for its bytes; a launch of 13 tiles to
 // an SM also pays for the filling and emptying of that pipeline.  In registers,
-// without the ring: 95 us.
+// without the ring: about 85 us.  Tried and left out: a fourth stage, with h_{t-1} in
+// the place of the 16-bit x and gate (62 us: the writers then keep x and the gates as
+// loaded, and spill more than they gain).
 #include "hla2_gated.cuh"
 
 namespace hla2 {
