@@ -20,7 +20,7 @@ struct Lane;
 
 template <int N>
 struct Lane<bf16, N, true> {
-    static_assert(N == 2 || N == 4 || N % 8 == 0, "whole accesses");
+    static_assert(N == 4 || N % 8 == 0, "whole accesses");
     static constexpr int W = N / 2;  // 32-bit words
     uint32_t w[W];
     __device__ __forceinline__ void load(const bf16* p, int) {
@@ -28,10 +28,8 @@ struct Lane<bf16, N, true> {
 #pragma unroll
             for (int i = 0; i < N / 8; ++i)
                 *reinterpret_cast<uint4*>(w + 4 * i) = __ldcs(reinterpret_cast<const uint4*>(p) + i);
-        } else if constexpr (N == 4) {
-            *reinterpret_cast<uint2*>(w) = __ldcs(reinterpret_cast<const uint2*>(p));
         } else {
-            w[0] = __ldcs(reinterpret_cast<const unsigned int*>(p));
+            *reinterpret_cast<uint2*>(w) = __ldcs(reinterpret_cast<const uint2*>(p));
         }
     }
     __device__ __forceinline__ float get(int i) const {
@@ -49,10 +47,8 @@ struct Lane<bf16, N, true> {
 #pragma unroll
             for (int i = 0; i < N / 8; ++i)
                 reinterpret_cast<uint4*>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-        } else if constexpr (N == 4) {
-            *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
         } else {
-            *reinterpret_cast<uint32_t*>(p) = w[0];
+            *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
         }
     }
 };
