@@ -12,8 +12,8 @@
 //
 // HBM bounds it.  16384 rows of 2048 with a residual, 16 bits (268 MB): 41.6 us,
 // 0.95 of the copy bandwidth (6.8 TB/s); 2^20 rows of 128, fp32 to 16 bits (805 MB):
-// 116 us, 1.02; 8 bits, 8191 rows of 8192 (470 MB): 76 us, 0.91, with 256 threads of
-// 32 elements to a row (512 of 16: 91 us, 1024 of 8: 153 us: a barrier holds up more
+// 116 us, 1.02; 8 bits, 8191 rows of 8192 (470 MB): 74 us, 0.94, with 256 threads of
+// 32 elements to a row (512 of 16 took 91 us, 1024 of 8 153 us, when this took 76: a barrier holds up more
 // of the SM).  16 rows of 2048 take 2.7 us, a launch.
 //
 // The maximum is taken over the bit patterns of |t w| as whole numbers, which
@@ -157,12 +157,16 @@ __global__ void __launch_bounds__(block_of(TPR)) rmsnorm_kernel(const NormParams
     if (!live) return;
     const float rstd = rsqrtf(fmaf(ss, p.inv_c, p.eps));  // 2 ulp; a root and a quotient took 30 instructions a row
     if constexpr (Q8) {
-        const float top = __uint_as_float(m) * rstd;
-        const float scale = top == 0.f ? 1.f : top / 448.f;
+        // The codes are those of y / scale = 448 t w / max|t w|: the root cancels, and where the
+        // quotient stands between two codes (16-bit operands often give such) it is exact, which
+        // fp32's y and scale lose.  The quotient is the product with the reciprocal, corrected by
+        // its remainder (Markstein's division).  Rows beyond 2^+-100 are scaled by a power of two,
+        // so that neither the reciprocal nor 448 t w leaves fp32's range.
+        const float most = __uint_as_float(m);
+        const float scale = most == 0.f ? 1.f : most * rstd / 448.f;
         if (lane == 0) p.scale[row] = scale;
-        // y / scale as a product, unless the reciprocal of a tiny scale overflows
-        const bool tiny = scale < 1e-37f;
-        const float inv = 1.f / scale;
+        const float by = most > 0x1p100f ? 0x1p-64f : most < 0x1p-100f ? 0x1p64f : 1.f;
+        const float den = most == 0.f ? 1.f : most * by, inv = 1.f / den;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int c = (v * TPR + lane) * 8, n = p.C - c;
@@ -170,8 +174,8 @@ __global__ void __launch_bounds__(block_of(TPR)) rmsnorm_kernel(const NormParams
                 float q[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float y = t[v][j] * rstd;
-                    q[j] = tiny ? y / scale : y * inv;
+                    const float num = t[v][j] * (448.f * by), first = num * inv;
+                    q[j] = fmaf(fmaf(-first, den, num), inv, first);
                 }
                 unsigned char* o = static_cast<unsigned char*>(p.y) + row * p.ldy + c;
                 const uint32_t a = e4m3x4(q[0], q[1], q[2], q[3]), b = e4m3x4(q[4], q[5], q[6], q[7]);

@@ -442,7 +442,8 @@ HLA2_API int hla2_rmsnorm(const void* X, const void* R, const void* W, void* S, 
 
 /*
  * The same norm with an 8-bit output: row r of Y is stored as
- *   Q = e4m3(Y / scale[r]) (round to nearest even, saturating),
+ *   Q = e4m3(Y / scale[r]) (round to nearest even), taken as
+ *       e4m3(448 t W / max|t W|), where ties are those of the exact quotient,
  *   scale[r] = max|Y_r| / 448, or 1 for a row of zeros.
  * A row that holds NaN or inf has a NaN or infinite scale and NaN in those places.
  *   Q [rows][C] bytes, row stride ldq;  scale [rows] fp32.

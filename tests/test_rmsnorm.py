@@ -111,6 +111,39 @@ def test_q8_special_rows():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rows,C", [(400, 64), (300, 100), (200, 127), (90, 1000), (60, 2048), (40, 8192), (15, 16384), (11, 9001)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_q8_codes_are_those_of_the_exact_quotient(rows, C, dtype):
+    """Q = e4m3(y / scale) = e4m3(448 t w / max|t w|), ties to even.  t and w of 8 bits make t w a number of 16
+    bits and 448 t w one of 19: either the quotient stands between two codes exactly, or it is 2^-21 of itself
+    and more from there, which fp32 tells.  So every code is the definition's."""
+    g = torch.Generator().manual_seed(33)
+    for by in (1.0, 2.0 ** -50, 2.0 ** 50, 2.0 ** -104, 2.0 ** 105):
+        x = (torch.randn(rows, C, generator=g) * torch.exp(torch.randn(rows, 1, generator=g))).to(torch.bfloat16) * by
+        w = (1 + 0.1 * torch.randn(C, generator=g)).to(torch.bfloat16)
+        q, scale, _ = hla2.hla2_rmsnorm_q8(x.to(dtype).cuda(), w.to(dtype).cuda())
+        tw = x.double() * w.double()
+        top = tw.abs().amax(-1, keepdim=True)
+        ref = (448 * tw / top).float().to(torch.float8_e4m3fn)
+        assert torch.equal(q.cpu().float(), ref.float())
+
+
+@pytest.mark.gpu
+def test_q8_of_rows_whose_scale_leaves_the_range():
+    """A scale that underflows, a row of zeros without eps: no NaN, and Q * scale is the row's (zero) value."""
+    C = 96
+    x = torch.zeros(3, C)
+    x[0, ::2] = 1e-45
+    x[1, ::3] = -3e-44
+    q, scale, _ = hla2.hla2_rmsnorm_q8(x.cuda(), eps=1.0)
+    q, scale = q.float().cpu(), scale.cpu()
+    assert torch.isfinite(q).all() and (q[x == 0] == 0).all() and (scale >= 0).all() and (scale[:2] < 1e-45).all()
+    assert scale[2] == 1
+    q, scale, _ = hla2.hla2_rmsnorm_q8(x[2:].cuda(), eps=0.0)
+    assert (q.float() == 0).all() and (scale == 1).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("rows,C", SIZES + [(3000, 64), (2500, 128), (1500, 1024), (700, 2048), (400, 4096), (300, 8192)])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_backward(rows, C, dtype):
