@@ -337,7 +337,8 @@ __global__ void __launch_bounds__(bwd_block(TPR), bwd_blocks(TPR)) rmsnorm_bwd_k
         row_sum2<TPR>(a, b, sh, phase);
         if (!live) continue;
         const float rstd = rsqrtf(fmaf(a, p.inv_c, p.eps));
-        const float back = rstd * rstd * rstd * (b * p.inv_c);  // rstd mean(w dy n) n = this times t
+        // rstd mean(w dy n): of dx's own size, where a power of rstd alone leaves fp32's range
+        const float back = rstd * (rstd * (b * p.inv_c));
         Lane<T, 8, VEC> out[NV];
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
@@ -347,7 +348,7 @@ __global__ void __launch_bounds__(bwd_block(TPR), bwd_blocks(TPR)) rmsnorm_bwd_k
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const float t = tv[v].get(j), dy = rstd * yv[v].get(j);
-                    dx[j] = fmaf(w[v][j], dy, -(t * back));
+                    dx[j] = fmaf(w[v][j], dy, -((t * rstd) * back));
                     acc[v][j] = fmaf(dy, t, acc[v][j]);
                 }
                 if (p.ds) {

@@ -433,7 +433,9 @@ HLA2_API int hla2_gated_step(float* state, const void* x, const void* g, void* o
  *   S     t rounded to dtype, the new residual stream (optional, may be X or R);
  *   Y     [rows][C] out_dtype.
  *   ldx, ldr, lds, ldy: row strides in elements, at least C.
- * The norm is taken of t before its rounding.  Sums are fp32.
+ * The norm is taken of t before its rounding.  Sums are fp32, of t^2 too: a row's
+ * values stay below about 1e18 (and, with eps = 0, its root mean square above
+ * 1e-18), here and in the calls below.
  * Errors: HLA2_ERR_INVALID, HLA2_ERR_UNSUPPORTED (C > 16384, types).
  */
 HLA2_API int hla2_rmsnorm(const void* X, const void* R, const void* W, void* S, void* Y, long long rows, int C,

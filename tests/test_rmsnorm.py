@@ -171,6 +171,30 @@ def test_backward(rows, C, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("C", [96, 256, 1000, 2048, 12288])
+@pytest.mark.parametrize("size,eps", [(1e14, 1e-6), (1e15, 1e-6), (1e16, 1e-6), (1e17, 1e-6), (1e-9, 0.0), (1e-13, 0.0),
+                                      (1e-16, 0.0), (1e15, 0.0), (1e-3, 1e-6), (1e-13, 1e-12)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_gradient_of_large_and_small_rows(C, size, eps, dtype):
+    """The bounds of test_backward, at sizes where a power of the rows' reciprocal root leaves fp32's range."""
+    rows = 9
+    g = torch.Generator().manual_seed(14)
+    t = (torch.randn(rows, C, generator=g) * size).to(dtype)
+    w = (1 + 0.2 * torch.randn(C, generator=g)).to(dtype)
+    # a gradient along the row itself, where the projection takes most of it away, and one across it
+    for dy in (torch.randn(rows, C, generator=g).to(dtype), (t.double() / size).to(dtype)):
+        dx, dw = hla2.hla2_rmsnorm_backward(t.cuda(), dy.cuda(), w.cuda(), eps=eps)
+        td, yd = t.double(), dy.double()
+        rstd = 1 / (td.square().mean(-1, keepdim=True) + eps).sqrt()
+        n, gw = td * rstd, yd * w.double()
+        ref = rstd * (gw - n * (gw * n).mean(-1, keepdim=True))
+        top = rstd * (gw.abs().amax(-1, keepdim=True) + n.abs().amax(-1, keepdim=True) * (gw * n).abs().mean(-1, keepdim=True))
+        assert torch.isfinite(dx).all() and (excess(dx, ref, F32 * top) <= F32 * top).all()
+        terms = yd * n
+        assert ((dw.double().cpu() - terms.sum(0)).abs() <= 1e-5 * terms.abs().sum(0).max()).all()
+
+
+@pytest.mark.gpu
 def test_gradient_against_differences():
     """Central differences of the 64-bit norm (their own error is about 1e-8)."""
     rows, C, eps = 2, 6, 1e-4
