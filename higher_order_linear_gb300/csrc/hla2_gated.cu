@@ -489,7 +489,7 @@ extern "C" size_t hla2_gated_scan_workspace(int B, int H, int T, int d) {
     using namespace hla2;
     if (B <= 0 || H <= 0 || T <= 0 || d <= 0 || d > 128 || (long long)B * H > 65535) return 0;
     const int lanes = lanes_of(d), rows = B * H;
-    return (lookback_bytes(rows, (T + tile_of(lanes) - 1) / tile_of(lanes), lanes * kCh) + 255) & ~size_t(255);
+    return (lookback_bytes(rows, (T + tile_of(lanes) - 1) / tile_of(lanes), lanes * kCh, d) + 255) & ~size_t(255);
 }
 
 extern "C" size_t hla2_gated_scan_carry_len(int T, int d) {
@@ -511,6 +511,7 @@ extern "C" int hla2_gated_scan(const void* X, const void* G, const unsigned char
     if (!aligned_elem(X, es) || !aligned_elem(G, es) || !aligned_elem(O, os) || !aligned_elem(state_in, 4) ||
         !aligned_elem(state_out, 4) || !aligned_elem(carry, 4))
         return set_error(HLA2_ERR_INVALID, "%s: pointer not aligned to its element", what);
+    if (int rc = check_states(what, state_in, state_out, (size_t)B * H * d)) return rc;
     const size_t need = hla2_gated_scan_workspace(B, H, T, d);
     if (need && (!workspace || ws_bytes < need))
         return set_error(HLA2_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", what, ws_bytes, need);
@@ -526,6 +527,7 @@ extern "C" int hla2_gated_scan(const void* X, const void* G, const unsigned char
     p.tiles = (T + tile - 1) / tile;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = begin_lookback(p, lanes * kCh, workspace, s);
+    if (e == cudaSuccess) e = begin_states(p, lanes * kCh, workspace, &p.state_in, state_out, s);
     p.out_bf16 = out_dtype == HLA2_DTYPE_BF16;
     CUtensorMap mx{}, mg{};
     const bool pipe = gate_map(&mx, X, es, p.sx, B, H, T, d, tile) &&

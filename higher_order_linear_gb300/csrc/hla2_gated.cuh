@@ -371,9 +371,18 @@ void take_strides(long long (&s)[3], const long long* strides, int i, int H, int
 }
 
 
-size_t lookback_bytes(int rows, int tiles, int cb) {
+// The words, then room for the states that enter the sequences (begin_states).
+size_t lookback_bytes(int rows, int tiles, int cb, int d) {
     if (tiles <= 1) return 0;
-    return Lookback(rows, tiles, cb).words() * 8;
+    return Lookback(rows, tiles, cb).words() * 8 + (size_t)rows * d * 4;
+}
+
+// The state that a call leaves may take the place of the one that enters, but not a part of it.
+int check_states(const char* what, const float* in, const float* out, size_t n) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(in), b = reinterpret_cast<uintptr_t>(out), bytes = n * 4;
+    if (in && out && a != b && a < b + bytes && b < a + bytes)
+        return set_error(HLA2_ERR_INVALID, "%s: the state after overlaps the state before without being it", what);
+    return HLA2_OK;
 }
 
 // Blocks of a kernel that fit the device at once, at most one to a tile.  What
@@ -416,6 +425,19 @@ cudaError_t begin_lookback(GateParams& p, int cb, void* workspace, cudaStream_t 
     if (p.tiles <= 1) return cudaSuccess;
     p.words = static_cast<unsigned long long*>(workspace);
     return cudaMemsetAsync(p.words, 0xff, Lookback(p.B * p.H, p.tiles, cb).words() * 8, s);
+}
+
+// Where a call leaves its last state in the place of the one that enters, the tiles
+// read a copy: a row's last tile waits for the other tiles' maps only, so it may be
+// written before a tile of the first group has read what enters.  A row of one tile
+// reads its state before it writes.
+cudaError_t begin_states(const GateParams& p, int cb, void* workspace, const float** in, const float* out, cudaStream_t s) {
+    if (!*in || *in != out || p.tiles <= 1) return cudaSuccess;
+    const int rows = p.B * p.H;
+    float* const copy = reinterpret_cast<float*>(static_cast<u64*>(workspace) + Lookback(rows, p.tiles, cb).words());
+    const float* const from = *in;
+    *in = copy;
+    return cudaMemcpyAsync(copy, from, (size_t)rows * p.d * 4, cudaMemcpyDeviceToDevice, s);
 }
 
 template <int N>

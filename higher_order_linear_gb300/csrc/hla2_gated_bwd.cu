@@ -561,6 +561,7 @@ extern "C" int hla2_gated_scan_backward(const void* X, const void* G, const unsi
     if (!aligned_elem(X, es) || !aligned_elem(G, es) || !aligned_elem(dX, es) || !aligned_elem(dG, es) ||
         !aligned_elem(dO, os) || !aligned_elem(carry, 4) || !aligned_elem(dstate_out, 4) || !aligned_elem(dstate_in, 4))
         return set_error(HLA2_ERR_INVALID, "%s: pointer not aligned to its element", what);
+    if (int rc = check_states(what, dstate_out, dstate_in, (size_t)B * H * d)) return rc;
     const size_t need = hla2_gated_scan_workspace(B, H, T, d);
     if (need && (!workspace || ws_bytes < need))
         return set_error(HLA2_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", what, ws_bytes, need);
@@ -582,6 +583,7 @@ extern "C" int hla2_gated_scan_backward(const void* X, const void* G, const unsi
                      (gate_shared || (aligned_to(G, es, p.sg, 3, kCh * es) && aligned_to(dG, es, p.sdg, 3, kCh * es)));
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = begin_lookback(p, lanes * kCh, workspace, s);
+    if (e == cudaSuccess) e = begin_states(p, lanes * kCh, workspace, &p.dstate_out, dstate_in, s);
     CUtensorMap mx{}, mg{}, mu{};
     const bool pipe = dtype == HLA2_DTYPE_BF16 && vec && gate_map(&mx, X, es, p.sx, B, H, T, d, tile) &&
                       (gate_shared || gate_map(&mg, G, es, p.sg, B, H, T, d, tile)) &&

@@ -683,7 +683,7 @@ def hla2_gated_scan(X: torch.Tensor, G: torch.Tensor, O: torch.Tensor | None = N
 
     ``form`` "sigmoid": a = sigmoid(G), u = (1 - a) X;  "decay": a = G, u = X.
     ``reset`` [B,T] bool: a document begins there (h_{t-1} counts as zero).
-    ``state_in`` / ``state_out`` [B,H,d] fp32: h before and after.
+    ``state_in`` / ``state_out`` [B,H,d] fp32: h before and after (one tensor may be both).
     ``carry`` [B,H,hla2_gated_scan_carry_len(T, d)] fp32 keeps what
     hla2_gated_scan_backward needs."""
     B, H, T, d, code, fcode, shared = _gated_inputs(X, G, form, reset)
@@ -717,7 +717,7 @@ def hla2_gated_scan_backward(X: torch.Tensor, G: torch.Tensor, dO: torch.Tensor,
     """Gradients (dX, dG) of hla2_gated_scan over the same X, G, ``form`` and
     ``reset``; ``carry`` is what that call kept.  dO [B,H,T,d] is the gradient
     of O, ``dstate_out`` that of state_out; ``dstate_in`` [B,H,d] fp32 receives
-    that of state_in.  A shared gate's dG [B,H,T] is summed over the channels."""
+    that of state_in (one tensor may be both).  A shared gate's dG [B,H,T] is summed over the channels."""
     B, H, T, d, code, fcode, shared = _gated_inputs(X, G, form, reset)
     dev = X.device
     _operand(dO, "dO", dev, shape=X.shape)

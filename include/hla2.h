@@ -375,7 +375,8 @@ enum { HLA2_GATE_SIGMOID = 0, HLA2_GATE_DECAY = 1 };
  *              (a document begins at t), even when it is inf or NaN.
  *   state_in   optional [B][H][d] fp32, h before the first token (else zero).
  *   O          [B][H][T][d], out_dtype.
- *   state_out  optional [B][H][d] fp32, h after the last token.
+ *   state_out  optional [B][H][d] fp32, h after the last token; may be state_in
+ *              (a sequence in pieces), but not overlap it otherwise.
  *   carry      optional [B][H][hla2_gated_scan_carry_len(T, d)] fp32: the
  *              states entering each tile of tokens, kept for the backward.
  *   strides    NULL, or nine values: X (b, h, t), G (b, h, t), O (b, h, t).
@@ -405,7 +406,8 @@ HLA2_API int hla2_gated_scan(const void* X, const void* G, const unsigned char* 
  *   carry       as written by the forward over the same X, G, reset, state_in.
  *   dO          [B][H][T][d], out_dtype.      dstate_out  optional [B][H][d] fp32.
  *   dX, dG      like X and G (dtype); a shared gate's dG is the sum over the
- *               head's channels.              dstate_in   optional [B][H][d] fp32.
+ *               head's channels.              dstate_in   optional [B][H][d] fp32; may
+ *               be dstate_out, but not overlap it otherwise.
  *   strides     NULL, or fifteen values: X, G, dO, dX, dG (b, h, t each).
  * Workspace and errors as for the forward.
  */

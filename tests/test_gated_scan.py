@@ -412,7 +412,60 @@ def test_steps_continue_a_scan():
         assert rel(o.view(B, H, d), ref[:, :, t], ref.abs().max()) < F32
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("dtype,B,H,T,d", [(torch.bfloat16, 1, 16, 2000, 128), (torch.bfloat16, 2, 30, 700, 64),
+                                           (torch.float32, 3, 50, 130, 80), (torch.float32, 1, 1, 9000, 33),
+                                           (torch.bfloat16, 2, 2, 50, 16)])
+def test_states_in_place(form, dtype, B, H, T, d):
+    """One tensor as the state before and after, and one as the gradients of both: the same bits as with two."""
+    x, gate = make(B, H, T, d, dtype, form, False, 81)
+    g = torch.Generator().manual_seed(82)
+    h0, dl = torch.randn(B, H, d, generator=g).cuda(), torch.randn(B, H, d, generator=g).cuda()
+    do = torch.randn(B, H, T, d, generator=g).to(dtype).cuda()
+    xc, gc = x.cuda(), gate.cuda()
+    last, first = torch.empty_like(h0), torch.empty_like(h0)
+    carry = torch.empty(B, H, hla2.hla2_gated_scan_carry_len(T, d), device="cuda")
+    o = hla2.hla2_gated_scan(xc, gc, form=form, state_in=h0, state_out=last, carry=carry)
+    dx, dg = hla2.hla2_gated_scan_backward(xc, gc, do, carry, form=form, dstate_out=dl, dstate_in=first)
+    assert rel(o, forward64(x, gate, form, None, h0.cpu())) < F32
+    for _ in range(20):
+        state, grad = h0.clone(), dl.clone()
+        o2 = hla2.hla2_gated_scan(xc, gc, form=form, state_in=state, state_out=state)
+        assert torch.equal(o2, o) and torch.equal(state, last)
+        dx2, dg2 = hla2.hla2_gated_scan_backward(xc, gc, do, carry, form=form, dstate_out=grad, dstate_in=grad)
+        assert torch.equal(dx2, dx) and torch.equal(dg2, dg) and torch.equal(grad, first)
+
+
+@pytest.mark.gpu
+def test_a_sequence_in_pieces():
+    """Pieces of one sequence, the state handed on in place."""
+    B, H, d, cuts = 2, 3, 64, [0, 1, 300, 301, 1500, 2000]
+    x, gate = make(B, H, cuts[-1], d, torch.bfloat16, "sigmoid", False, 83)
+    xc, gc = x.cuda(), gate.cuda()
+    state = torch.zeros(B, H, d, device="cuda")
+    o = [hla2.hla2_gated_scan(xc[:, :, a:b], gc[:, :, a:b], state_in=state, state_out=state) for a, b in zip(cuts, cuts[1:])]
+    ref = forward64(x, gate, "sigmoid")
+    assert rel(torch.cat(o, 2), ref) < F32 and rel(state, ref[:, :, -1], ref.abs().max()) < F32
+
+
 # ---------------------------------------------------------------- refusals ----
+def test_states_that_overlap_are_refused():
+    import ctypes
+    L = hla2.lib()
+    p = lambda a: ctypes.c_void_p(a)
+    B, H, T, d = 2, 3, 8, 16
+    size = B * H * d * 4
+    for off in (4, 16, size - 4, -4, 4 - size):
+        assert L.hla2_gated_scan(p(4096), p(4096), None, p(65536), p(4096), p(65536 + off), None, B, H, T, d, None, 0, 0,
+                                 0, 0, None, 0, None) == hla2.HLA2_ERR_INVALID
+        assert "overlap" in hla2.hla2_last_error_detail()
+        assert L.hla2_gated_scan_backward(p(4096), p(4096), None, p(4096), p(4096), p(65536), p(4096), p(4096),
+                                          p(65536 + off), B, H, T, d, None, 0, 0, 0, 0, None, 0,
+                                          None) == hla2.HLA2_ERR_INVALID
+        assert "overlap" in hla2.hla2_last_error_detail()
+
+
 def test_binding_refuses():
     x, g = torch.zeros(2, 3, 8, 4), torch.zeros(2, 3, 8, 4)
     f, bw = hla2.hla2_gated_scan, hla2.hla2_gated_scan_backward
