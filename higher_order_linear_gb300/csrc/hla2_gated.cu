@@ -526,6 +526,8 @@ extern "C" int hla2_gated_scan(const void* X, const void* G, const unsigned char
     const int lanes = lanes_of(d), tile = tile_of(lanes);
     p.tiles = (T + tile - 1) / tile;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    p.status = device_status_word();  // where a wait that runs out is reported
+    if (!p.status) return set_error(HLA2_ERR_LAUNCH, "%s: cannot resolve the device status word", what);
     cudaError_t e = begin_lookback(p, lanes * kCh, workspace, s);
     if (e == cudaSuccess) e = begin_states(p, lanes * kCh, workspace, &p.state_in, state_out, s);
     p.out_bf16 = out_dtype == HLA2_DTYPE_BF16;

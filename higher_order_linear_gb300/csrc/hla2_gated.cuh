@@ -418,7 +418,6 @@ cudaError_t persistent_blocks(const void* kernel, int threads, size_t smem, unsi
 // Sets the workspace's words to "nothing yet".
 cudaError_t begin_lookback(GateParams& p, int cb, void* workspace, cudaStream_t s) {
     p.total = (unsigned)((long long)p.B * p.H * p.tiles);
-    p.status = device_status_word();
     const auto per = [](unsigned long long y) { return y == 1 ? 0ull : ~0ull / y + 1; };
     p.per_rows = per((unsigned long long)p.B * p.H);
     p.per_h = per((unsigned long long)p.H);

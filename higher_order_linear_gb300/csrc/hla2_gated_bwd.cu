@@ -582,6 +582,8 @@ extern "C" int hla2_gated_scan_backward(const void* X, const void* G, const unsi
                      aligned_to(dO, os, p.sdo, 3, kCh * os) &&
                      (gate_shared || (aligned_to(G, es, p.sg, 3, kCh * es) && aligned_to(dG, es, p.sdg, 3, kCh * es)));
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    p.status = device_status_word();  // where a wait that runs out is reported
+    if (!p.status) return set_error(HLA2_ERR_LAUNCH, "%s: cannot resolve the device status word", what);
     cudaError_t e = begin_lookback(p, lanes * kCh, workspace, s);
     if (e == cudaSuccess) e = begin_states(p, lanes * kCh, workspace, &p.dstate_out, dstate_in, s);
     CUtensorMap mx{}, mg{}, mu{};

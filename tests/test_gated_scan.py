@@ -466,6 +466,29 @@ def test_states_that_overlap_are_refused():
         assert "overlap" in hla2.hla2_last_error_detail()
 
 
+def test_no_launch_without_a_status_word():
+    """Where the device's status word cannot be had (here: no device at all), the scan and its gradient say so
+    before they launch anything that would report through it."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import ctypes
+from higher_order_linear_gb300 import hla2
+L = hla2.lib()
+p = ctypes.c_void_p(4096)
+for T in (8, 1000):
+    n = hla2.hla2_gated_scan_workspace(1, 1, T, 16)
+    for call in (lambda: L.hla2_gated_scan(p, p, None, None, p, None, None, 1, 1, T, 16, None, 0, 0, 0, 0, p, n, None),
+                 lambda: L.hla2_gated_scan_backward(p, p, None, p, p, None, p, p, None, 1, 1, T, 16, None, 0, 0, 0, 0,
+                                                    p, n, None)):
+        assert call() == hla2.HLA2_ERR_LAUNCH
+        assert "status word" in hla2.hla2_last_error_detail(), hla2.hla2_last_error_detail()
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run([sys.executable, "-c", code], cwd=root, env=dict(os.environ, CUDA_VISIBLE_DEVICES=""), check=True)
+
+
 def test_binding_refuses():
     x, g = torch.zeros(2, 3, 8, 4), torch.zeros(2, 3, 8, 4)
     f, bw = hla2.hla2_gated_scan, hla2.hla2_gated_scan_backward
