@@ -108,7 +108,7 @@ gated_scan_kernel(const GateParams p) {
                 }
             }
 #pragma unroll
-        for (int j = 0; j < kCh; ++j) runs[run][c + j] = make_float2(in.resets ? cut() : A[j] + 0.f, X[j]);
+        for (int j = 0; j < kCh; ++j) runs[run][c + j] = make_float2(in.resets ? cut() : no_cut(A[j]), X[j]);
         __syncthreads();
         __syncthreads();
         k = slot;
@@ -403,7 +403,7 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
             if (!wait(taken(slot.s), slot.phase ^ 1u)) return;
             float4* m4 = reinterpret_cast<float4*>(maps(slot.s) + run * CB + c);
 #pragma unroll
-            for (int j = 0; j < kCh; ++j) A[j] = resets ? cut() : A[j] + 0.f;
+            for (int j = 0; j < kCh; ++j) A[j] = resets ? cut() : no_cut(A[j]);
             m4[0] = make_float4(A[0], X[0], A[1], X[1]);
             m4[1] = make_float4(A[2], X[2], A[3], X[3]);
             __syncwarp();

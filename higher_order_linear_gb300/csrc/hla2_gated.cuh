@@ -57,13 +57,16 @@ __device__ __forceinline__ float keep_out(float g) {
 
 // ---- maps h -> A h + X -------------------------------------------------------
 // A run that holds a reset forgets what entered it: its A is -0, which nothing
-// else is (products that are zero are made +0), and then only X counts.
+// else is (a product that is zero is made +0, by an addition that may not be
+// contracted with it: an fma of a negative product that underflows is -0), and then
+// only X counts.
 __device__ __forceinline__ float cut() { return __uint_as_float(0x80000000u); }
 __device__ __forceinline__ bool is_cut(float A) { return __float_as_uint(A) == 0x80000000u; }
+__device__ __forceinline__ float no_cut(float A) { return __fadd_rn(A, 0.f); }
 __device__ __forceinline__ float pass(float2 m, float h) { return is_cut(m.x) ? m.y : fmaf(m.x, h, m.y); }
 // first `a`, then `b`
 __device__ __forceinline__ float2 then(float2 a, float2 b) {
-    return make_float2(is_cut(b.x) || is_cut(a.x) ? cut() : a.x * b.x + 0.f, pass(b, a.y));
+    return make_float2(is_cut(b.x) || is_cut(a.x) ? cut() : no_cut(__fmul_rn(a.x, b.x)), pass(b, a.y));
 }
 
 // x / y for the y whose 2^64 / y (rounded up; 0 stands for y = 1) is `per`

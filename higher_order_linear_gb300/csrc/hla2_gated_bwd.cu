@@ -114,7 +114,7 @@ gated_scan_bwd_kernel(const GateParams p) {
             }
 #pragma unroll
         for (int j = 0; j < kCh; ++j) {
-            const float a = in.resets ? cut() : A[j] + 0.f;
+            const float a = in.resets ? cut() : no_cut(A[j]);
             fwd[run][c + j] = make_float2(a, X[j]);
             back[run][c + j] = make_float2(a, Y[j]);
         }
@@ -455,7 +455,7 @@ gated_pipe_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
                 for (int j = 0; j < kCh; ++j) A[j] = cut();
             } else {
 #pragma unroll
-                for (int j = 0; j < kCh; ++j) A[j] += 0.f;
+                for (int j = 0; j < kCh; ++j) A[j] = no_cut(A[j]);
             }
             *reinterpret_cast<float4*>(plane(s, 0) + o) = make_float4(A[0], A[1], A[2], A[3]);
             *reinterpret_cast<float4*>(plane(s, 1) + o) = make_float4(X[0], X[1], X[2], X[3]);

@@ -259,6 +259,34 @@ def test_nothing_passes_a_reset(form, bad, at):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("dtype,d", [(torch.float32, 64), (torch.float32, 128), (torch.float32, 33),
+                                     (torch.bfloat16, 64), (torch.bfloat16, 128), (torch.bfloat16, 20)])
+def test_nan_stays_without_a_reset(dtype, d, shared):
+    """Decays of both signs whose products underflow: NaN in a state reaches every later token (0 * NaN is NaN),
+    and in a gradient every earlier one, up to a reset and not beyond."""
+    B, H, T, cut = 1, 3, 6000, 4500
+    g = torch.Generator().manual_seed(91)
+    shape = (B, H, T) if shared else (B, H, T, d)
+    gate = ((0.2 + 0.3 * torch.rand(shape, generator=g)) * torch.where(torch.rand(shape, generator=g) < 0.5, -1.0, 1.0)).to(dtype)
+    x = torch.randn(B, H, T, d, generator=g).to(dtype).cuda()
+    h0 = torch.full((B, H, d), float("nan"), device="cuda")
+    r = torch.zeros(B, T, dtype=torch.bool)
+    r[:, cut] = True
+    carry = torch.empty(B, H, hla2.hla2_gated_scan_carry_len(T, d), device="cuda")
+    o = hla2.hla2_gated_scan(x, gate.cuda(), form="decay", state_in=h0, reset=r.cuda())
+    assert torch.isnan(o[:, :, :cut]).all() and torch.isfinite(o[:, :, cut:]).all()
+    hla2.hla2_gated_scan(x, gate.cuda(), form="decay", reset=r.cuda(), carry=carry)
+    d0 = torch.empty(B, H, d, device="cuda")
+    dx, dg = hla2.hla2_gated_scan_backward(x, gate.cuda(), x, carry, form="decay", reset=r.cuda(), dstate_out=h0, dstate_in=d0)
+    assert torch.isfinite(dx[:, :, :cut]).all() and torch.isnan(dx[:, :, cut:]).all()
+    assert torch.isfinite(d0).all()
+    hla2.hla2_gated_scan(x, gate.cuda(), form="decay", carry=carry)
+    dx, dg = hla2.hla2_gated_scan_backward(x, gate.cuda(), x, carry, form="decay", dstate_out=h0, dstate_in=d0)
+    assert torch.isnan(dx).all() and torch.isnan(dg).all() and torch.isnan(d0).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("form", FORMS)
 def test_gradient_against_differences(form):
     """Central differences of the 64-bit forward: their own error is about eps^2 = 1e-8."""
