@@ -3,15 +3,15 @@
 //
 //   h_t = a_t h_{t-1} + u_t
 //   decay:   a = g, u = x
-//   sigmoid: a = 1 / (1 + e^-g), u = (1 - a) x, taken as h += z (x - h) with
-//            z = 1 - a = e^-g / (1 + e^-g): z keeps its relative precision where
-//            a is next to 1, which is where the memory is long.
+//   sigmoid: a = 1 / (1 + e^-g), u = z x, z = 1 - a = 1 / (1 + e^g): each of a and
+//            z keeps its relative precision, z where a is next to 1 (a long memory)
+//            and a where it is next to 0 (what a closing gate leaves).
 // A reset at t makes h_{t-1} zero there (chosen, not multiplied: nothing of an
 // earlier document passes, not even inf or NaN).
 //
 // Gradient, lam_t = dh_t + a_{t+1} lam_{t+1}:
 //   decay:   dx = lam,    dg = lam h_{t-1}
-//   sigmoid: dx = z lam,  dg = z (1 - z) lam (h_{t-1} - x)
+//   sigmoid: dx = z lam,  dg = a z lam (h_{t-1} - x)
 //
 // One pass over the data.  A run of tokens maps the state before it to the state
 // after it by h -> A h + X, and such maps compose, so a tile of tokens can be read
@@ -28,7 +28,7 @@
 //
 // What bounds it.  Forward of 1 x 16 x 65536 x 128, 16-bit in, 32-bit out (1.07 GB,
 // 158 us at the copy bandwidth of 6.8 TB/s): 185 us, 0.85 of it; 16-bit out
-// (0.81 GB, 118 us): 164 us.  An earlier stand of the pipeline took 170 us with the
+// (0.81 GB, 118 us): 171 us.  An earlier stand of the pipeline took 170 us with the
 // waits between blocks left out: they cost the rest, by the way of a state from
 // group to group, about 1.3 us a hop through L2, and by the maps to be read for
 // each tile (groups of 6 tiles took 215 us where 8 took 200, 12 211 and 16 237, all
@@ -90,7 +90,7 @@ gated_scan_kernel(const GateParams p) {
         const int nt = nc > 0 ? min(kTok, p.T - t0) : 0;  // tokens of this thread, none where <= 0
         Run<T, SHARED, false> in;
         in.load(p, b, hd, t0, c, nc, nt);
-        float gate[kTok][NG];  // z of the sigmoid, a of the decay
+        float gate[kTok][NG];
         float A[kCh], X[kCh];
 #pragma unroll
         for (int j = 0; j < kCh; ++j) { A[j] = 1.f; X[j] = 0.f; }
@@ -98,13 +98,13 @@ gated_scan_kernel(const GateParams p) {
         for (int i = 0; i < kTok; ++i)
             if (i < nt) {
 #pragma unroll
-                for (int j = 0; j < NG; ++j) gate[i][j] = SIG ? keep_out(in.g[i].get(j)) : in.g[i].get(j);
+                for (int j = 0; j < NG; ++j) gate[i][j] = SIG ? sigmoid_gate(in.g[i].get(j)) : in.g[i].get(j);
 #pragma unroll
                 for (int j = 0; j < kCh; ++j) {
                     const float ga = gate[i][SHARED ? 0 : j], xv = in.x[i].get(j);
                     if (in.reset(i)) X[j] = 0.f;
-                    X[j] = SIG ? fmaf(ga, xv - X[j], X[j]) : fmaf(ga, X[j], xv);
-                    A[j] = SIG ? fmaf(-ga, A[j], A[j]) : ga * A[j];
+                    X[j] = next_state<SIG>(ga, X[j], xv);
+                    A[j] = decayed<SIG>(ga, A[j]);
                 }
             }
 #pragma unroll
@@ -124,7 +124,7 @@ gated_scan_kernel(const GateParams p) {
                     for (int j = 0; j < kCh; ++j) {
                         const float ga = gate[i][SHARED ? 0 : j], xv = in.x[i].get(j);
                         if (in.reset(i)) h[j] = 0.f;
-                        h[j] = SIG ? fmaf(ga, xv - h[j], h[j]) : fmaf(ga, h[j], xv);
+                        h[j] = next_state<SIG>(ga, h[j], xv);
                     }
                     if (p.out_bf16) {
                         Lane<bf16, kCh, false> ov;
@@ -186,6 +186,7 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
     static_assert(S >= kJoin, "the ends of the tickets take a stage for each group of joiners");
     __shared__ TileInfo info[S];
     __shared__ unsigned reset_bits[S][RUNS];
+    __shared__ unsigned wide[S][kData / 32];  // lanes whose runs leave the range of Powers, for each warp
     __shared__ volatile int abort_flag;
     unsigned char* const base = raw + ((128u - (smem_u32(raw) & 127u)) & 127u);
     const int tid = threadIdx.x, warp = tid >> 5;
@@ -366,40 +367,76 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
             for (int i2 = 0; i2 < kTok; ++i2)
                 if (i2 < nt) gl[i2] = to_f32(gp[i2 * p.sg[2]]);
         }
-        auto gates = [&](int i2, float (&ga)[NG]) {
-            if constexpr (SHARED) {
-                ga[0] = SIG ? keep_out(gl[i2]) : gl[i2];
-            } else {
-                four(gs + i2 * p.d, ga);
-                if (SIG) {
-#pragma unroll
-                    for (int j = 0; j < kCh; ++j) ga[j] = keep_out(ga[j]);
-                }
+        // e^g where by_power, else a gate as next_state() takes it
+        auto gates_of = [&](int i2, float (&ga)[NG]) {
+            if constexpr (SHARED) ga[0] = gl[i2];
+            else four(gs + i2 * p.d, ga);
+        };
+        auto gates = [&](int i2, float (&ga)[NG], bool by_power) {  // e^g, or gates as next_state() takes them
+            gates_of(i2, ga);
+            if (!SIG) return;
+            if (by_power) {
+                gate_powers(ga);
+                return;
             }
+#pragma unroll
+            for (int j = 0; j < NG; ++j) ga[j] = sigmoid_gate(ga[j]);
         };
         if (mapper) {
             float A[kCh], X[kCh];
+            // whole: a run of kTok tokens; clean: one without resets
+            auto walk = [&](auto whole, auto clean) {
 #pragma unroll
-            for (int j = 0; j < kCh; ++j) { A[j] = 1.f; X[j] = 0.f; }
-            auto walk = [&](auto whole, auto clean) {  // a whole run; one without resets
+                for (int j = 0; j < kCh; ++j) { A[j] = 1.f; X[j] = 0.f; }
 #pragma unroll
                 for (int i2 = 0; i2 < kTok; ++i2)
                     if (whole || i2 < nt) {
                         float xv[kCh], ga[NG];
                         four(xs + i2 * p.d, xv);
-                        gates(i2, ga);
+                        gates(i2, ga, false);
 #pragma unroll
                         for (int j = 0; j < kCh; ++j) {
-                            const float z = ga[SHARED ? 0 : j];
+                            const float gate = ga[SHARED ? 0 : j];
                             if (!clean && ((resets >> i2) & 1u)) X[j] = 0.f;
-                            X[j] = SIG ? fmaf(z, xv[j] - X[j], X[j]) : fmaf(z, X[j], xv[j]);
-                            A[j] = SIG ? fmaf(-z, A[j], A[j]) : z * A[j];
+                            X[j] = next_state<SIG>(gate, X[j], xv[j]);
+                            A[j] = decayed<SIG>(gate, A[j]);
                         }
                     }
             };
-            if (nt == kTok && resets == 0) walk(std::true_type{}, std::true_type{});
-            else if (nt == kTok) walk(std::true_type{}, std::false_type{});
-            else walk(std::false_type{}, std::false_type{});
+            auto powers = [&](auto whole, auto clean) {  // false: out of range
+                Powers<NG> w;
+#pragma unroll
+                for (int j = 0; j < kCh; ++j) X[j] = 0.f;
+#pragma unroll
+                for (int i2 = 0; i2 < kTok; ++i2)
+                    if (whole || i2 < nt) {
+                        float xv[kCh], E[NG];
+                        four(xs + i2 * p.d, xv);
+                        gates(i2, E, true);
+                        if (!clean && ((resets >> i2) & 1u)) fill(X, 0.f);
+                        w.token(E, X, xv);
+                    }
+                bool in = true;
+#pragma unroll
+                for (int j = 0; j < kCh; ++j) {
+                    float per;
+                    in = w.close(SHARED ? 0 : j, A[j], per) && fabsf(X[j]) < INFINITY && in;
+                    X[j] *= per;
+                }
+                return in;
+            };
+            using yes = std::true_type;
+            using no = std::false_type;
+            if constexpr (SIG) {
+                const bool in = nt == kTok && resets == 0 ? powers(yes{}, yes{}) : nt == kTok ? powers(yes{}, no{}) : powers(no{}, no{});
+                if (!in) walk(no{}, no{});
+                const unsigned out = __ballot_sync(0xffffffffu, !in);
+                if ((tid & 31) == 0) wide[s][at >> 5] = out;
+            } else {
+                if (nt == kTok && resets == 0) walk(yes{}, yes{});
+                else if (nt == kTok) walk(yes{}, no{});
+                else walk(no{}, no{});
+            }
             if (!wait(taken(slot.s), slot.phase ^ 1u)) return;
             float4* m4 = reinterpret_cast<float4*>(maps(slot.s) + run * CB + c);
 #pragma unroll
@@ -416,18 +453,19 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
             __syncwarp();
             if ((tid & 31) == 0) mbar_arrive(taken(slot.s));
             const long long off = info[s].o + run * kTok * p.so[2] + c;
-            auto walk = [&](auto whole, auto clean, auto* o) {
+            auto walk = [&](auto whole, auto clean, auto by_power, auto* o) {
 #pragma unroll
                 for (int i2 = 0; i2 < kTok; ++i2)
                     if (whole || i2 < nt) {
                         float xv[kCh], ga[NG];
                         four(xs + i2 * p.d, xv);
-                        gates(i2, ga);
+                        gates(i2, ga, by_power);
+                        if (!clean && ((resets >> i2) & 1u)) fill(h, 0.f);
+                        if (by_power) {
+                            next_by_power(ga, h, xv);
+                        } else {
 #pragma unroll
-                        for (int j = 0; j < kCh; ++j) {
-                            const float z = ga[SHARED ? 0 : j];
-                            if (!clean && ((resets >> i2) & 1u)) h[j] = 0.f;
-                            h[j] = SIG ? fmaf(z, xv[j] - h[j], h[j]) : fmaf(z, h[j], xv[j]);
+                            for (int j = 0; j < kCh; ++j) h[j] = next_state<SIG>(ga[SHARED ? 0 : j], h[j], xv[j]);
                         }
                         Lane<std::remove_pointer_t<decltype(o)>, kCh, true> ov;
                         ov.set(h);
@@ -435,9 +473,13 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
                     }
             };
             auto go = [&](auto* o) {
-                if (nt == kTok && resets == 0) walk(std::true_type{}, std::true_type{}, o);
-                else if (nt == kTok) walk(std::true_type{}, std::false_type{}, o);
-                else walk(std::false_type{}, std::false_type{}, o);
+                using power = std::integral_constant<bool, SIG>;
+                using yes = std::true_type;
+                using no = std::false_type;
+                if (SIG && wide[s][at >> 5]) walk(no{}, no{}, no{}, o);
+                else if (nt == kTok && resets == 0) walk(yes{}, yes{}, power{}, o);
+                else if (nt == kTok) walk(yes{}, no{}, power{}, o);
+                else walk(no{}, no{}, power{}, o);
             };
             if (p.out_bf16) go(static_cast<bf16*>(p.o));
             else go(static_cast<float*>(p.o));
@@ -472,7 +514,7 @@ __global__ void __launch_bounds__(256) gated_step_kernel(const float* state, con
 #pragma unroll
     for (int j = 0; j < N; ++j) {
         const float gate = SHARED ? gate0 : gv.get(j);
-        out[j] = SIG ? fmaf(keep_out(gate), xv.get(j) - h.get(j), h.get(j)) : fmaf(gate, h.get(j), xv.get(j));
+        out[j] = next_state<SIG>(SIG ? sigmoid_gate(gate) : gate, h.get(j), xv.get(j));
     }
     h.set(out);
     h.store(state_out + row * d + c, N);

@@ -42,17 +42,192 @@ struct GateParams {
     int* status;
 };
 
-// z = 1 - a = 1 / (1 + e^g) of the sigmoid gate: 1 where e^g is zero, 0 where it is
-// inf, NaN for NaN.  The power of two and the reciprocal are the approximate
-// instructions (2 ulp and 1 ulp) without their handling of subnormal numbers,
-// which the sum with 1 swallows; a z below 2^-126 becomes 0.
-__device__ __forceinline__ float keep_out(float g) {
+// The sigmoid gate is kept as the smaller of a = 1 / (1 + e^-g) and z = 1 - a, which
+// is c = e / (1 + e) with e = e^-|g|, and its sign says which: c where it is a (g < 0),
+// -c where it is z.  Either end keeps its relative precision: the long memory where a
+// is next to 1, and what is left of the state and of the gate's gradient where a is
+// next to 0.  Held as z alone, a = 1 - z was off by 1e-2 of itself at g = -12 and
+// zero from -17 on.
+//
+// The power of two and the reciprocal are the approximate instructions (2 ulp and
+// 1 ulp) without their handling of subnormal numbers: a c below 2^-126 is 0.  The
+// rounding of g log2(e) adds |g| 2^-24 of c: what half a unit in the last place of an
+// fp32 g makes of c, and 2^-15 of that for a 16-bit g.
+__device__ __forceinline__ float sigmoid_gate(float g) {
     constexpr float kLog2e = 1.4426950408889634f;
-    const float t = g * kLog2e;
-    float e, z;
+    const float t = fabsf(g) * -kLog2e;
+    float e, r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(z) : "f"(1.f + e));
-    return z;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return __uint_as_float(__float_as_uint(e * r) | (~__float_as_uint(g) & 0x80000000u));
+}
+__device__ __forceinline__ bool holds_z(float gate) { return (int)__float_as_uint(gate) < 0; }
+
+// What a gate (a itself in the decay form) does to a state and to a decay.  The sigmoid
+// form is a step from the nearer of x and h towards the other: x + a (h - x) or
+// h + z (x - h).
+template <bool SIG>
+__device__ __forceinline__ float next_state(float gate, float h, float x) {
+    return SIG ? fmaf(gate, h - x, holds_z(gate) ? h : x) : fmaf(gate, h, x);
+}
+template <bool SIG>
+__device__ __forceinline__ float decayed(float gate, float v) {  // a v
+    return SIG ? fmaf(gate, v, holds_z(gate) ? v : 0.f) : gate * v;
+}
+// One token of the gradient: lam = dh + mu -> dx, dg and the mu that reaches h_{t-1}.
+template <bool SIG>
+__device__ __forceinline__ void back_token(float gate, float lam, float before, float x, float& dx, float& dg, float& mu) {
+    if (SIG) {
+        const bool z = holds_z(gate);
+        mu = fmaf(gate, lam, z ? lam : 0.f);    // a lam
+        dx = fmaf(-gate, lam, z ? 0.f : lam);   // z lam
+        dg = fabsf(gate) * (z ? mu : dx) * (before - x);
+    } else {
+        dx = lam;
+        dg = lam * before;
+        mu = gate * lam;
+    }
+}
+
+// The pipelined kernels take the sigmoid gate as E = e^g, a = E / (1 + E), z = 1 / (1 + E):
+// positive factors alone, so both keep their relative precision, and a run's map needs
+// one quotient in all.  Over the tokens of a run D = prod (1 + E), P = prod E, and
+//   X = N / D,  N -> E N + x D;      A = P / D = 1 - Q / D,  Q -> E Q + D;
+// A is taken from the smaller of P and Q, so that a long memory's 1 - A is good to its
+// own size and not to A's.  For the gradient Y = M / D, M -> (1 + E) M + P dh.
+// Where a product leaves fp32's range (gates above 8 at every token of a run and more,
+// inf, NaN) the run is walked with sigmoid_gate() instead.  Per element and token this
+// takes 7 operations in the map and 7 in the walk that writes; sigmoid_gate() and its
+// selections took 12 and 10, which made the scan of 65536 x 16 x 128 240 us.
+// Two elements to an instruction where there are pairs (f32x2) halve that again.
+template <int N, typename F1, typename F2>
+__device__ __forceinline__ void by_pairs(float (&o)[N], const float (&a)[N], const float (&b)[N], const float (&c)[N],
+                                         F1&& one, F2&& two) {
+    if constexpr (N % 2 == 0) {
+#pragma unroll
+        for (int j = 0; j < N; j += 2) {
+            unsigned long long x, y, z, r;
+            asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a[j]), "f"(a[j + 1]));
+            asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b[j]), "f"(b[j + 1]));
+            asm("mov.b64 %0, {%1, %2};" : "=l"(z) : "f"(c[j]), "f"(c[j + 1]));
+            r = two(x, y, z);
+            asm("mov.b64 {%0, %1}, %2;" : "=f"(o[j]), "=f"(o[j + 1]) : "l"(r));
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) o[j] = one(a[j], b[j], c[j]);
+    }
+}
+template <int N>
+__device__ __forceinline__ void fmas(float (&o)[N], const float (&a)[N], const float (&b)[N], const float (&c)[N]) {
+    using u = unsigned long long;
+    by_pairs(o, a, b, c, [](float x, float y, float z) { return fmaf(x, y, z); },
+             [](u x, u y, u z) { u r; asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z)); return r; });
+}
+template <int N>
+__device__ __forceinline__ void products(float (&o)[N], const float (&a)[N], const float (&b)[N]) {
+    using u = unsigned long long;
+    by_pairs(o, a, b, b, [](float x, float y, float) { return x * y; },
+             [](u x, u y, u) { u r; asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y)); return r; });
+}
+template <int N>
+__device__ __forceinline__ void sums(float (&o)[N], const float (&a)[N], const float (&b)[N]) {
+    using u = unsigned long long;
+    by_pairs(o, a, b, b, [](float x, float y, float) { return x + y; },
+             [](u x, u y, u) { u r; asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y)); return r; });
+}
+template <int N>
+__device__ __forceinline__ void fill(float (&o)[N], float v) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) o[j] = v;
+}
+// a gate shared by the channels, or one for each, for all of them
+template <int N, int NG>
+__device__ __forceinline__ void each(float (&o)[N], const float (&g)[NG]) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) o[j] = g[NG == 1 ? 0 : j];
+}
+
+template <int N>
+__device__ __forceinline__ void gate_powers(float (&g)[N]) {  // e^g
+    float l[N];
+    fill(l, 1.4426950408889634f);
+    products(g, g, l);
+#pragma unroll
+    for (int j = 0; j < N; ++j) asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(g[j]) : "f"(g[j]));
+}
+__device__ __forceinline__ float reciprocal(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+template <int N>
+__device__ __forceinline__ void keeps(float (&z)[N], const float (&E)[N]) {  // 1 / (1 + E)
+    float one[N];
+    fill(one, 1.f);
+    sums(z, E, one);
+#pragma unroll
+    for (int j = 0; j < N; ++j) z[j] = reciprocal(z[j]);
+}
+template <int NG>
+struct Powers {
+    float D[NG], P[NG], Q[NG];
+    __device__ __forceinline__ Powers() {
+        fill(D, 1.f);
+        fill(P, 1.f);
+        fill(Q, 0.f);
+    }
+    // a token: X is N, Y is M; u counts where `open`
+    __device__ __forceinline__ void token(const float (&E)[NG], float (&X)[kCh], const float (&x)[kCh]) {
+        float e[kCh], d[kCh];
+        each(e, E);
+        each(d, D);
+        products(d, d, x);
+        fmas(X, e, X, d);
+        fmas(Q, E, Q, D);
+        fmas(D, D, E, D);
+        products(P, P, E);
+    }
+    __device__ __forceinline__ void back_token(const float (&E)[NG], float (&Y)[kCh], const float (&u)[kCh], bool open) {
+        float e[kCh], q[kCh];
+        each(e, E);
+        each(q, P);
+        fmas(Y, Y, e, Y);
+        if (open) fmas(Y, q, u, Y);
+    }
+    // A and 1 / D of gate j; false where the products may have left the range
+    __device__ __forceinline__ bool close(int j, float& A, float& per) const {
+        per = reciprocal(D[j]);
+        A = P[j] < Q[j] ? P[j] * per : fmaf(-Q[j], per, 1.f);
+        return D[j] < 0x1p100f;
+    }
+};
+// A token with E: h -> a h + z x
+template <int NG>
+__device__ __forceinline__ void next_by_power(const float (&E)[NG], float (&h)[kCh], const float (&x)[kCh]) {
+    float z[NG], a[NG], zs[kCh], as[kCh];
+    keeps(z, E);
+    products(a, E, z);
+    each(zs, z);
+    each(as, a);
+    products(zs, zs, x);
+    fmas(h, as, h, zs);
+}
+// One token of the gradient: lam = u + mu -> dx = z lam, mu = a lam, dg = a z lam (before - x)
+template <int NG>
+__device__ __forceinline__ void back_by_power(const float (&E)[NG], const float (&u)[kCh], const float (&before)[kCh],
+                                              const float (&x)[kCh], float (&dx)[kCh], float (&dg)[kCh], float (&mu)[kCh]) {
+    float z[NG], zs[kCh], es[kCh], minus[kCh];
+    keeps(z, E);
+    each(zs, z);
+    each(es, E);
+    sums(mu, u, mu);
+    products(dx, zs, mu);
+    products(mu, es, dx);
+    products(dg, zs, mu);
+    fill(minus, -1.f);
+    fmas(minus, x, minus, before);
+    products(dg, dg, minus);
 }
 
 // ---- maps h -> A h + X -------------------------------------------------------

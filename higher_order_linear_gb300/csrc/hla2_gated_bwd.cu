@@ -2,7 +2,7 @@
 //
 //   lam_t = dh_t + a_{t+1} lam_{t+1}
 //   decay:   dx = lam,    dg = lam h_{t-1}
-//   sigmoid: dx = z lam,  dg = z (1 - z) lam (h_{t-1} - x),  z = 1 - a
+//   sigmoid: dx = z lam,  dg = a z lam (h_{t-1} - x),  z = 1 - a
 //
 // The forward's walk from the last tile to the first, for mu_t = a_t lam_t, the part
 // of the gradient that reaches h_{t-1}: mu_t = a_t (dh_t + mu_{t+1}), so a run maps
@@ -12,8 +12,9 @@
 // need no rounding to 16 bits, and reading x costs what reading h would.
 //
 // What bounds it.  4 x 16 x 4096 x 64, 16 bits (168 MB, 25 us at the copy
-// bandwidth): 56 us; with the forward (100 MB, 15 us) of 36 us a training pass
-// takes 93 us.  A tile is on chip for about 7 us (loads 0.8, mapping 1.0, waiting
+// bandwidth): 61 us; with the forward (100 MB, 15 us) of 38 us a training pass
+// takes 99 us (93 with the gate as z alone, whose 1 - z loses what a closing gate
+// leaves; 129 with sigmoid_gate() throughout).  A tile is on chip for about 7 us (loads 0.8, mapping 1.0, waiting
 // for tiles of other blocks 2.6, writing 1.7) and shared memory holds three, so one
 // leaves every 2.5 to 2.9 us against 1.8 us for its bytes; a launch of 13 tiles to
 // an SM also pays for the filling and emptying of that pipeline.  In registers,
@@ -94,13 +95,13 @@ gated_scan_bwd_kernel(const GateParams p) {
         for (int i = 0; i < kTok; ++i)
             if (i < nt) {
 #pragma unroll
-                for (int j = 0; j < NG; ++j) gate[i][j] = SIG ? keep_out(in.g[i].get(j)) : in.g[i].get(j);
+                for (int j = 0; j < NG; ++j) gate[i][j] = SIG ? sigmoid_gate(in.g[i].get(j)) : in.g[i].get(j);
 #pragma unroll
                 for (int j = 0; j < kCh; ++j) {
                     const float ga = gate[i][SHARED ? 0 : j], xv = in.x[i].get(j);
                     if (in.reset(i)) X[j] = 0.f;
-                    X[j] = SIG ? fmaf(ga, xv - X[j], X[j]) : fmaf(ga, X[j], xv);
-                    A[j] = SIG ? fmaf(-ga, A[j], A[j]) : ga * A[j];
+                    X[j] = next_state<SIG>(ga, X[j], xv);
+                    A[j] = decayed<SIG>(ga, A[j]);
                 }
             }
 #pragma unroll
@@ -109,7 +110,7 @@ gated_scan_bwd_kernel(const GateParams p) {
 #pragma unroll
                 for (int j = 0; j < kCh; ++j) {
                     const float ga = gate[i][SHARED ? 0 : j], lam = dh[i].get(j) + Y[j];
-                    Y[j] = in.reset(i) ? 0.f : SIG ? fmaf(-ga, lam, lam) : ga * lam;
+                    Y[j] = in.reset(i) ? 0.f : decayed<SIG>(ga, lam);
                 }
             }
 #pragma unroll
@@ -139,7 +140,7 @@ gated_scan_bwd_kernel(const GateParams p) {
 #pragma unroll
                     for (int j = 0; j < kCh; ++j) {
                         const float ga = gate[i][SHARED ? 0 : j], xv = in.x[i].get(j);
-                        h[j] = SIG ? fmaf(ga, xv - h[j], h[j]) : fmaf(ga, h[j], xv);
+                        h[j] = next_state<SIG>(ga, h[j], xv);
                     }
                 }
         }
@@ -155,15 +156,8 @@ gated_scan_bwd_kernel(const GateParams p) {
 #pragma unroll
                 for (int j = 0; j < kCh; ++j) {
                     const float ga = gate[i][SHARED ? 0 : j], lam = dh[i].get(j) + mu[j];
-                    if (SIG) {
-                        gx[j] = ga * lam;
-                        gg[j] = fmaf(-ga, gx[j], gx[j]) * (hb[j] - in.x[i].get(j));
-                        mu[j] = in.reset(i) ? 0.f : fmaf(-ga, lam, lam);
-                    } else {
-                        gx[j] = lam;
-                        gg[j] = lam * hb[j];
-                        mu[j] = in.reset(i) ? 0.f : ga * lam;
-                    }
+                    back_token<SIG>(ga, lam, hb[j], in.x[i].get(j), gx[j], gg[j], mu[j]);
+                    if (in.reset(i)) mu[j] = 0.f;
                 }
                 Lane<T, kCh, VEC> ov;
                 ov.set(gx);
@@ -223,6 +217,7 @@ gated_pipe_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
     static_assert(S >= kJoin, "the ends of the tickets take a stage for each group of joiners");
     __shared__ TileInfo info[S];
     __shared__ unsigned reset_bits[S][RUNS];
+    __shared__ unsigned wide[S][kData / 32];  // lanes whose runs leave the range of Powers, for each warp
     __shared__ volatile int abort_flag;
     unsigned char* const base = raw + ((128u - (smem_u32(raw) & 127u)) & 127u);
     float4* const before = reinterpret_cast<float4*>(base + (size_t)LY::kStage * S);  // [kTok][kData]: h_{t-1}
@@ -410,45 +405,86 @@ gated_pipe_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
             for (int i2 = 0; i2 < kTok; ++i2)
                 if (i2 < nt) gl[i2] = to_f32(gp[i2 * p.sg[2]]);
         }
-        auto gates = [&](int i2, float (&ga)[NG]) {
-            if constexpr (SHARED) {
-                ga[0] = SIG ? keep_out(gl[i2]) : gl[i2];
-            } else {
-                four(gs + i2 * p.d, ga);
-                if (SIG) {
-#pragma unroll
-                    for (int j = 0; j < kCh; ++j) ga[j] = keep_out(ga[j]);
-                }
+        // e^g where by_power, else a gate as next_state() takes it
+        auto gates_of = [&](int i2, float (&ga)[NG]) {
+            if constexpr (SHARED) ga[0] = gl[i2];
+            else four(gs + i2 * p.d, ga);
+        };
+        auto gates = [&](int i2, float (&ga)[NG], bool by_power) {  // e^g, or gates as next_state() takes them
+            gates_of(i2, ga);
+            if (!SIG) return;
+            if (by_power) {
+                gate_powers(ga);
+                return;
             }
+#pragma unroll
+            for (int j = 0; j < NG; ++j) ga[j] = sigmoid_gate(ga[j]);
         };
         if (mapper) {
             // (A, X) forwards; Y = sum over the run of dh_t times the decays a_t .. of its beginning
             float A[kCh], X[kCh], Y[kCh];
-#pragma unroll
-            for (int j = 0; j < kCh; ++j) { A[j] = 1.f; X[j] = 0.f; Y[j] = 0.f; }
-            auto walk = [&](auto whole, auto clean) {  // a whole run; one without resets
+            // whole: a run of kTok tokens; clean: one without resets
+            auto walk = [&](auto whole, auto clean) {
                 bool open = true;  // no reset so far
+#pragma unroll
+                for (int j = 0; j < kCh; ++j) { A[j] = 1.f; X[j] = 0.f; Y[j] = 0.f; }
 #pragma unroll
                 for (int i2 = 0; i2 < kTok; ++i2)
                     if (whole || i2 < nt) {
                         float xv[kCh], uv[kCh], ga[NG];
                         four(xs + i2 * p.d, xv);
                         four(us + i2 * p.d, uv);
-                        gates(i2, ga);
+                        gates(i2, ga, false);
                         if (!clean && ((resets >> i2) & 1u)) open = false;
 #pragma unroll
                         for (int j = 0; j < kCh; ++j) {
-                            const float z = ga[SHARED ? 0 : j];
+                            const float gate = ga[SHARED ? 0 : j];
                             if (!clean && ((resets >> i2) & 1u)) X[j] = 0.f;
-                            X[j] = SIG ? fmaf(z, xv[j] - X[j], X[j]) : fmaf(z, X[j], xv[j]);
-                            A[j] = SIG ? fmaf(-z, A[j], A[j]) : z * A[j];
+                            X[j] = next_state<SIG>(gate, X[j], xv[j]);
+                            A[j] = decayed<SIG>(gate, A[j]);
                             if (clean || open) Y[j] = fmaf(A[j], uv[j], Y[j]);
                         }
                     }
             };
-            if (nt == kTok && resets == 0) walk(std::true_type{}, std::true_type{});
-            else if (nt == kTok) walk(std::true_type{}, std::false_type{});
-            else walk(std::false_type{}, std::false_type{});
+            auto powers = [&](auto whole, auto clean) {  // false: out of range
+                Powers<NG> w;
+                bool open = true;
+#pragma unroll
+                for (int j = 0; j < kCh; ++j) X[j] = Y[j] = 0.f;
+#pragma unroll
+                for (int i2 = 0; i2 < kTok; ++i2)
+                    if (whole || i2 < nt) {
+                        float xv[kCh], uv[kCh], E[NG];
+                        four(xs + i2 * p.d, xv);
+                        four(us + i2 * p.d, uv);
+                        gates(i2, E, true);
+                        if (!clean && ((resets >> i2) & 1u)) open = false;
+                        if (!clean && ((resets >> i2) & 1u)) fill(X, 0.f);
+                        w.token(E, X, xv);
+                        w.back_token(E, Y, uv, clean || open);
+                    }
+                bool in = true;
+#pragma unroll
+                for (int j = 0; j < kCh; ++j) {
+                    float per;
+                    in = w.close(SHARED ? 0 : j, A[j], per) && fabsf(X[j]) < INFINITY && fabsf(Y[j]) < INFINITY && in;
+                    X[j] *= per;
+                    Y[j] *= per;
+                }
+                return in;
+            };
+            using yes = std::true_type;
+            using no = std::false_type;
+            if constexpr (SIG) {
+                const bool in = nt == kTok && resets == 0 ? powers(yes{}, yes{}) : nt == kTok ? powers(yes{}, no{}) : powers(no{}, no{});
+                if (!in) walk(no{}, no{});
+                const unsigned out = __ballot_sync(0xffffffffu, !in);
+                if ((tid & 31) == 0) wide[s][at >> 5] = out;
+            } else {
+                if (nt == kTok && resets == 0) walk(yes{}, yes{});
+                else if (nt == kTok) walk(yes{}, no{});
+                else walk(no{}, no{});
+            }
             const int o = run * CB + c;
             if (resets) {
 #pragma unroll
@@ -468,23 +504,24 @@ gated_pipe_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
             four(plane(s, 2) + run * CB + c, mu);
             T* const dxp = static_cast<T*>(p.dx) + info[s].o + run * kTok * p.sdx[2] + c;
             T* const dgp = static_cast<T*>(p.dg) + info[s].o2 + run * kTok * p.sdg[2] + (SHARED ? 0 : c);
-            auto walk = [&](auto whole, auto clean) {
+            auto walk = [&](auto whole, auto clean, auto by_power) {
                 float z[kTok][NG];
 #pragma unroll
                 for (int i2 = 0; i2 < kTok; ++i2)
                     if (whole || i2 < nt) {
                         float xv[kCh];
                         four(xs + i2 * p.d, xv);
-                        gates(i2, z[i2]);
+                        gates(i2, z[i2], by_power);
                         if (!clean && ((resets >> i2) & 1u)) {
 #pragma unroll
                             for (int j = 0; j < kCh; ++j) h[j] = 0.f;
                         }
                         before[i2 * kData + at] = make_float4(h[0], h[1], h[2], h[3]);
+                        if (by_power) {
+                            next_by_power(z[i2], h, xv);
+                        } else {
 #pragma unroll
-                        for (int j = 0; j < kCh; ++j) {
-                            const float ga = z[i2][SHARED ? 0 : j];
-                            h[j] = SIG ? fmaf(ga, xv[j] - h[j], h[j]) : fmaf(ga, h[j], xv[j]);
+                            for (int j = 0; j < kCh; ++j) h[j] = next_state<SIG>(z[i2][SHARED ? 0 : j], h[j], xv[j]);
                         }
                     }
 #pragma unroll
@@ -497,20 +534,14 @@ gated_pipe_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
                         four(us + i2 * p.d, uv);
                         const float4 hb4 = before[i2 * kData + at];
                         const float hb[kCh] = {hb4.x, hb4.y, hb4.z, hb4.w};
+                        if (by_power) {
+                            back_by_power(z[i2], uv, hb, xv, gx, gg, mu);
+                        } else {
 #pragma unroll
-                        for (int j = 0; j < kCh; ++j) {
-                            const float ga = z[i2][SHARED ? 0 : j], lam = uv[j] + mu[j];
-                            if (SIG) {
-                                gx[j] = ga * lam;
-                                mu[j] = fmaf(-ga, lam, lam);
-                                gg[j] = ga * mu[j] * (hb[j] - xv[j]);
-                            } else {
-                                gx[j] = lam;
-                                gg[j] = lam * hb[j];
-                                mu[j] = ga * lam;
-                            }
-                            if (!clean && ((resets >> i2) & 1u)) mu[j] = 0.f;
+                            for (int j = 0; j < kCh; ++j)
+                                back_token<SIG>(z[i2][SHARED ? 0 : j], uv[j] + mu[j], hb[j], xv[j], gx[j], gg[j], mu[j]);
                         }
+                        if (!clean && ((resets >> i2) & 1u)) fill(mu, 0.f);
                         Lane<T, kCh, true> ov;
                         ov.set(gx);
                         ov.store(dxp + i2 * p.sdx[2], nc);
@@ -531,9 +562,13 @@ gated_pipe_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
             };
             // the same path for a warp's lanes: a shared gate's gradient is summed over them
             const bool whole = __all_sync(0xffffffffu, nt == kTok), clean = __all_sync(0xffffffffu, resets == 0);
-            if (whole && clean) walk(std::true_type{}, std::true_type{});
-            else if (whole) walk(std::true_type{}, std::false_type{});
-            else walk(std::false_type{}, std::false_type{});
+            using power = std::integral_constant<bool, SIG>;
+            using yes = std::true_type;
+            using no = std::false_type;
+            if (SIG && wide[s][at >> 5]) walk(no{}, no{}, no{});
+            else if (whole && clean) walk(yes{}, yes{}, power{});
+            else if (whole) walk(yes{}, no{}, power{});
+            else walk(no{}, no{}, power{});
             const int row = info[s].row;
             __syncwarp();
             if ((tid & 31) == 0) mbar_arrive(empty(s));

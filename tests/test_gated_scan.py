@@ -236,6 +236,93 @@ def test_extreme_gates(form):
     assert rel(dx, rx) < F32 and rel(dg, rg) < F32
 
 
+def gate_slack(g):
+    """How far a and z = 1 - a of a sigmoid gate may each be off, of themselves: the rounding of g log2(e) moves the
+    exponent by |g| 2^-24 (and the constant's own by a quarter of that); the power of two has 2 ulp, the sum with 1
+    a half, the reciprocal 1, their product a half: 4 ulp of 2^-23."""
+    return g.double().abs() * 1.25 * 2.0 ** -24 + 4 * 2.0 ** -23
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d", [(torch.float32, 64), (torch.float32, 128), (torch.float32, 33),
+                                     (torch.bfloat16, 64), (torch.bfloat16, 128), (torch.bfloat16, 33)])
+@pytest.mark.parametrize("shared", [False, True])
+def test_both_ends_of_a_gate_keep_their_precision(dtype, d, shared):
+    """One token, from h = 1 with x = 0 (h is a) and from 0 with x = 1 (h is z), and the gradients z, a z and a:
+    each of its own size, however small."""
+    n = 161
+    g = torch.linspace(-80, 80, n, dtype=torch.float64).to(dtype)
+    gate = g.view(1, n, 1) if shared else g.view(1, n, 1, 1).expand(1, n, 1, d).contiguous()
+    a, z = torch.sigmoid(g.double()), torch.sigmoid(-g.double())
+    slack = gate_slack(g)
+    zero, one = torch.zeros(1, n, 1, d, dtype=dtype, device="cuda"), torch.ones(1, n, 1, d, dtype=dtype, device="cuda")
+    h1 = torch.ones(1, n, d, device="cuda")
+    gc = gate.cuda()
+
+    def near(got, ref, times=1.0):
+        ref, tol = ref.view(1, n, 1, 1), (times * slack * ref).view(1, n, 1, 1)
+        assert (excess(got.view(1, n, 1, -1), ref, tol) <= tol).all()
+
+    carry = torch.empty(1, n, hla2.hla2_gated_scan_carry_len(1, d), device="cuda")
+    near(hla2.hla2_gated_scan(one, gc), z)
+    near(hla2.hla2_gated_scan(zero, gc, state_in=h1, carry=carry), a)
+    d0 = torch.empty(1, n, d, device="cuda")
+    dx, dg = hla2.hla2_gated_scan_backward(zero, gc, one, carry, dstate_in=d0)
+    near(dx, z, 2)  # z is 1 - a or a is 1 - z: a rounding more
+    near(d0, a, 2)
+    near(dg, d * a * z if shared else a * z, 4 + d / 16 if shared else 4)
+    state = h1.view(n, d).clone()
+    sg = gc.view(n) if shared else gc.view(n, d)
+    near(hla2.hla2_gated_step(state, zero.view(n, d), sg), a)
+    near(hla2.hla2_gated_step(torch.zeros_like(state), one.view(n, d), sg), z)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d,T", [(torch.float32, 64, 700), (torch.float32, 33, 700), (torch.bfloat16, 64, 700),
+                                       (torch.bfloat16, 128, 700), (torch.bfloat16, 128, 2100)])
+def test_closing_gates_over_many_tokens(dtype, d, T):
+    """Gates from closed to open, and positive values over several powers of ten: each token's result is good to its
+    own size.  err, the relative error of h, goes by err' = w err + (gate's) + 2 roundings, w the part of h' that comes
+    from h; twice that for the roundings of the maps of runs and tiles.  mu goes the same way, backwards; dG holds a
+    difference h - x, whose error is that of both."""
+    B, H = 1, 2
+    gen = torch.Generator().manual_seed(95)
+    gate = (-14 + 18 * torch.rand(B, H, T, d, generator=gen)).to(dtype)
+    x = torch.exp(3 * torch.randn(B, H, T, d, generator=gen)).to(dtype)
+    do = torch.exp(3 * torch.randn(B, H, T, d, generator=gen))
+    h0 = torch.full((B, H, d), 1e6)
+    g = gate.double()
+    a, z, slack = torch.sigmoid(g), torch.sigmoid(-g), gate_slack(gate) + 2 * 2.0 ** -24
+    h, err, hs, errs, before = h0.double(), torch.zeros(B, H, d, dtype=torch.float64), [], [], []
+    befe = []
+    for t in range(T):
+        before.append(h)
+        befe.append(err)
+        new = a[:, :, t] * h + z[:, :, t] * x[:, :, t].double()
+        err = a[:, :, t] * h / new * err + slack[:, :, t]
+        h = new
+        hs.append(h)
+        errs.append(err)
+    ref, err = torch.stack(hs, 2), torch.stack(errs, 2)
+    before, befe = torch.stack(before, 2), torch.stack(befe, 2)
+    carry = torch.empty(B, H, hla2.hla2_gated_scan_carry_len(T, d), device="cuda")
+    o = hla2.hla2_gated_scan(x.cuda(), gate.cuda(), state_in=h0.cuda(), carry=carry)
+    assert ((o.double().cpu() - ref).abs() <= 2 * err * ref).all()
+    dx, dg = hla2.hla2_gated_scan_backward(x.cuda(), gate.cuda(), do.cuda(), carry)
+    mu, me = torch.zeros(B, H, d, dtype=torch.float64), torch.zeros(B, H, d, dtype=torch.float64)
+    lam, le = torch.empty_like(ref), torch.empty_like(ref)
+    for t in range(T - 1, -1, -1):
+        lam[:, :, t] = do[:, :, t].double() + mu
+        le[:, :, t] = me * mu / lam[:, :, t] + 2.0 ** -24
+        mu = a[:, :, t] * lam[:, :, t]
+        me = le[:, :, t] + slack[:, :, t]
+    tol = 2 * (le + slack) * z * lam
+    assert (excess(dx, z * lam, tol) <= tol).all()
+    size = a * z * lam
+    tol = 2 * size * ((le + 2 * slack) * (before - x.double()).abs() + (befe + 2.0 ** -24) * before + 2.0 ** -24 * x.double())
+    assert (excess(dg, size * (before - x.double()), tol) <= tol).all()
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("form", FORMS)
 @pytest.mark.parametrize("bad", [float("inf"), float("nan")])
