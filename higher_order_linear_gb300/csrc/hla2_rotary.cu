@@ -21,8 +21,9 @@
 // The angle is reduced in revolutions: freq / (2 pi) is carried as a sum of two
 // fp32 numbers, its product with the position as a sum of two more (the
 // rounding error of a product comes from one fma), and the nearest whole
-// number is subtracted exactly; positions of 2^24 and more go through fp64.
-// So the angle is good to fp32 at every position.
+// number is subtracted exactly; positions of 2^24 and more, and angles of 2^23 and
+// more, go through sums of two fp64 numbers.  So the angle is good to fp32 at every
+// position and frequency.
 #include <cstdlib>
 
 #include "hla2_layer.cuh"
@@ -53,9 +54,11 @@ struct RotParams {
 constexpr double kInvTwoPi = 0.15915494309189533577;
 constexpr float kInvTwoPiHi = (float)kInvTwoPi;
 constexpr float kInvTwoPiLo = (float)(kInvTwoPi - (double)kInvTwoPiHi);
+constexpr double kInvTwoPiRest = -9.839338337591243477019410e-18;  // 1 / (2 pi) less kInvTwoPi
 
-// pos * (hi + lo) less the nearest whole number, for a whole |pos| < 2^24: the
-// pair holds about 48 bits, so the result is off by less than 2^-26 of a turn
+// pos * (hi + lo) less the nearest whole number, of fewer than 2^21 turns of a whole
+// |pos| < 2^24: the pair holds about 48 bits, so the result is off by less than 2^-26
+// of a turn
 __device__ __forceinline__ float turn_fraction(float pos, float hi, float lo) {
     const float p = pos * hi;
     const float e = fmaf(pos, hi, -p) + pos * lo;
@@ -67,11 +70,13 @@ __device__ __forceinline__ void turn_of(int ps, float f, float& si, float& co) {
     const float hi = f * kInvTwoPiHi;
     const float lo = fmaf(f, kInvTwoPiHi, -hi) + f * kInvTwoPiLo;
     float r;
-    if (ps > -(1 << 24) && ps < (1 << 24)) {
+    if (ps > -(1 << 24) && ps < (1 << 24) && fabsf((float)ps * f) < 0x1p23f) {
         r = turn_fraction((float)ps, hi, lo);
-    } else {  // beyond what 48 bits of revolutions resolve
-        const double turns = (double)ps * ((double)f * kInvTwoPi);
-        r = (float)(turns - rint(turns));
+    } else {  // beyond what 48 bits of revolutions resolve: the same in fp64, 106 bits
+        const double dh = (double)f * kInvTwoPi, dl = fma((double)f, kInvTwoPi, -dh) + (double)f * kInvTwoPiRest;
+        const double p = ps * dh, e = fma((double)ps, dh, -p) + ps * dl;
+        const double t = (p - rint(p)) + e;
+        r = (float)(t - rint(t));
     }
     sincospif(2.f * r, &si, &co);
 }

@@ -385,7 +385,7 @@ enum { HLA2_GATE_SIGMOID = 0, HLA2_GATE_DECAY = 1 };
  * All sums are fp32.  Tokens are joined in a fixed order: the same call gives
  * the same bits.  |a_t| is meant to be at most 1; with larger decays the
  * product of the decays of any 1024 tokens in a row must stay finite.  Of the
- * sigmoid form's a and 1 - a each is good to (|g| + 8) 2^-24 of itself, down to
+ * sigmoid form's a and 1 - a each is good to (1.25 |g| + 8) 2^-24 of itself, down to
  * 2^-126.  An inf in x or in the state is inf or NaN from its token on, until a
  * reset.
  * Errors: HLA2_ERR_INVALID, HLA2_ERR_UNSUPPORTED (d > 128, B*H > 65535,
@@ -485,8 +485,10 @@ HLA2_API int hla2_rmsnorm_backward(const void* S, const void* dY, const void* W,
  *   sections  naxes (1..4) positive counts on the host, adding up to rot/2.
  *   interleaved  pair p is channels (2p, 2p + 1); else (p, p + rot/2).
  *   strides   NULL, or fourteen values: Q, OQ, K, OK (b, h, t each), pos (axis, b).
- * The angle is reduced exactly (its error does not grow with the position).
- * Errors: HLA2_ERR_INVALID, HLA2_ERR_UNSUPPORTED (d > 128, types).
+ * The angle is reduced exactly: its error grows neither with the position nor
+ * with the frequency.
+ * Errors: HLA2_ERR_INVALID, HLA2_ERR_UNSUPPORTED (d > 128, B*(H+HK) > 65535,
+ * B*T > 2^31, types).
  */
 HLA2_API int hla2_rotary(const void* Q, void* OQ, const void* K, void* OK, const int* pos, const float* freq, int B,
                          int H, int HK, int T, int d, int rot, int naxes, const int* sections, int interleaved,

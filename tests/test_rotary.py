@@ -92,6 +92,28 @@ def test_far_positions(start):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("scale", [1.0, 7.0, 300.0, 1e4, 1e6, 1e9])
+@pytest.mark.parametrize("start", [0, 5000, 1 << 20, (1 << 23) - 25, (1 << 24) - 25, (1 << 31) - 50, -(1 << 31)])
+def test_large_frequencies(scale, start):
+    """Frequencies above 1: angles of up to 3e18 radians, reduced in whole numbers (1 / 2 pi to 60
+    digits); the bound of every other position."""
+    from fractions import Fraction
+    inv = Fraction(159154943091895335768883763372514362034459645740456448747667, 10 ** 60)
+    T, pairs = 20, 8
+    g = torch.Generator().manual_seed(9)
+    x = torch.randn(1, 1, T, 2 * pairs, generator=g)
+    f = (scale * (0.5 + torch.rand(pairs, generator=g))).float()
+    pos = (torch.arange(T, dtype=torch.int64) + start).to(torch.int32)
+    out, _ = hla2.hla2_rotary(x.cuda(), pos.view(1, 1, T).cuda(), f.cuda(), (pairs,))
+    turns = [[float((Fraction(int(p)) * Fraction(float(v)) * inv) % 1) for v in f] for p in pos]
+    ang = 2 * torch.pi * torch.tensor(turns, dtype=torch.float64)
+    a, b = x.double()[0, 0, :, :pairs], x.double()[0, 0, :, pairs:]
+    ref = torch.cat([a * torch.cos(ang) - b * torch.sin(ang), a * torch.sin(ang) + b * torch.cos(ang)], -1)
+    size = (a * a + b * b).sqrt().repeat(1, 2)
+    assert ((out.double().cpu()[0, 0] - ref).abs() <= F32 * size).all()
+
+
+@pytest.mark.gpu
 def test_inverse_undoes_the_turn_and_shared_positions():
     g = torch.Generator().manual_seed(5)
     q = torch.randn(2, 4, 60, 128, generator=g).cuda()
