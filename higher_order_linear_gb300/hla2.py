@@ -617,6 +617,13 @@ def _out_code(dtype) -> int:
     return code
 
 
+def _like(t: torch.Tensor, dtype=None) -> torch.Tensor:
+    """An output in t's memory order, its last dimension contiguous (t's elements may overlap, as in
+    sliding windows: then the order is not always t's)."""
+    o = torch.empty_like(t, dtype=dtype)
+    return o if o.stride(-1) == 1 or t.shape[-1] == 1 else torch.empty(t.shape, device=t.device, dtype=o.dtype)
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -698,7 +705,7 @@ def hla2_gated_scan(X: torch.Tensor, G: torch.Tensor, O: torch.Tensor | None = N
     L = _lib or lib()
     with _guard(dev, stream):
         if O is None:
-            O = torch.empty_like(X, dtype=out_dtype)
+            O = _like(X, out_dtype)
         workspace, nws = _gated_work(L, workspace, B, H, T, d, dev)
         rc = L.hla2_gated_scan(X.data_ptr(), G.data_ptr(), _ptr(reset), _ptr(state_in), O.data_ptr(),
                                _ptr(state_out), _ptr(carry), B, H, T, d,
@@ -736,9 +743,9 @@ def hla2_gated_scan_backward(X: torch.Tensor, G: torch.Tensor, dO: torch.Tensor,
     L = _lib or lib()
     with _guard(dev, stream):
         if dX is None:
-            dX = torch.empty_like(X)
+            dX = _like(X)
         if dG is None:
-            dG = torch.empty_like(G)
+            dG = torch.empty_like(G) if shared else _like(G)
         workspace, nws = _gated_work(L, workspace, B, H, T, d, dev)
         rc = L.hla2_gated_scan_backward(X.data_ptr(), G.data_ptr(), _ptr(reset), carry.data_ptr(), dO.data_ptr(),
                                         _ptr(dstate_out), dX.data_ptr(), dG.data_ptr(), _ptr(dstate_in), B, H, T, d,
@@ -1019,7 +1026,7 @@ def hla2_rotary(Q: torch.Tensor, pos: torch.Tensor, freq: torch.Tensor, sections
     L = _lib or lib()
     with _guard(dev, stream):
         if OQ is None:
-            OQ = torch.empty_like(Q)
+            OQ = _like(Q)
         sq, so, sp = Q.stride(), OQ.stride(), pos.stride()
         pb = sp[1] if len(sp) == 3 else 0
         if K is None:
@@ -1027,7 +1034,7 @@ def hla2_rotary(Q: torch.Tensor, pos: torch.Tensor, freq: torch.Tensor, sections
             st = _longs(sq[0], sq[1], sq[2], so[0], so[1], so[2], 0, 0, 0, 0, 0, 0, sp[0], pb)
         else:
             if OK is None:
-                OK = torch.empty_like(K)
+                OK = _like(K)
             HK, pk, po = K.shape[1], K.data_ptr(), OK.data_ptr()
             sk, sl = K.stride(), OK.stride()
             st = _longs(sq[0], sq[1], sq[2], so[0], so[1], so[2], sk[0], sk[1], sk[2], sl[0], sl[1], sl[2], sp[0], pb)

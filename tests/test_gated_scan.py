@@ -435,6 +435,39 @@ def test_strided_and_unaligned_operands(dtype):
             assert (t[..., :off] == 7).all() and (t[..., off + d:] == 7).all()
 
 
+def windows(T, d, seed, dtype=torch.float32, step=1):
+    """[1, 2, T, d] whose rows are windows of d elements, `step` apart, of one sequence for each head."""
+    base = torch.randn(2, (T - 1) * step + d, generator=torch.Generator().manual_seed(seed)).to(dtype)
+    return base.as_strided((1, 2, T, d), (0, base.stride(0), step, 1))
+
+
+def test_outputs_are_laid_out_for_the_kernels():
+    """An output of the binding's own has a contiguous last dimension, whatever its input's strides."""
+    for T, d, step in ((8, 16, 1), (16, 16, 1), (20, 16, 1), (3, 16, 5), (1, 16, 1), (5, 1, 1)):
+        x = windows(T, d, 1, step=step)
+        for o in (hla2._like(x), hla2._like(x, torch.bfloat16)):
+            assert o.shape == x.shape and (d == 1 or o.stride(-1) == 1) \
+                and o.untyped_storage().nbytes() == o.numel() * o.element_size()
+    y = torch.zeros(2, 5, 3, 8).transpose(1, 2)
+    assert hla2._like(y).stride() == y.stride()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,d,step", [(8, 16, 1), (40, 64, 1), (300, 16, 4)])
+def test_overlapping_inputs(T, d, step):
+    """Sliding windows as inputs: elements that are in several places."""
+    x, gate = windows(T, d, 43, step=step), windows(T, d, 44, step=step)
+    dev = lambda t: t.as_strided((2, t.stride(1)), (t.stride(1), 1)).cuda().as_strided(t.shape, t.stride())
+    xc, gc = dev(x), dev(gate)
+    assert torch.equal(xc.cpu(), x)
+    carry = torch.empty(1, 2, hla2.hla2_gated_scan_carry_len(T, d), device="cuda")
+    assert rel(hla2.hla2_gated_scan(xc, gc, carry=carry), forward64(x, gate, "sigmoid")) < F32
+    do = windows(T, d, 45, step=step)
+    dx, dg = hla2.hla2_gated_scan_backward(xc, gc, dev(do), carry)
+    rx, rg, _ = backward64(x, gate, do, "sigmoid")
+    assert rel(dx, rx) < F32 and rel(dg, rg) < F32
+
+
 @pytest.mark.gpu
 def test_offsets_beyond_32_bits():
     """Tokens whose element offset passes 2^31."""

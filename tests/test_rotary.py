@@ -160,6 +160,23 @@ def test_strided_slices_and_gaps(dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,d,step", [(8, 16, 1), (40, 64, 1), (300, 16, 4)])
+def test_overlapping_inputs(T, d, step):
+    """Sliding windows as inputs: elements that are in several places, strides that leave no order of their own."""
+    base = torch.randn(3, (T - 1) * step + d, generator=torch.Generator().manual_seed(10))
+    strides = (0, base.stride(0), step, 1)
+    q, k = base.as_strided((1, 2, T, d), strides), base.as_strided((1, 2, T, d), strides, base.stride(0))
+    dev = base.cuda()
+    pos = torch.arange(T, dtype=torch.int32).view(1, 1, T)
+    f = freqs(d // 2)
+    oq, ok = hla2.hla2_rotary(dev.as_strided((1, 2, T, d), strides), pos.cuda(), f.cuda(), (d // 2,),
+                              K=dev.as_strided((1, 2, T, d), strides, dev.stride(0)))
+    for got, x in ((oq, q), (ok, k)):
+        ref, size = turn64(x, pos, f, (d // 2,), False, False)
+        assert (excess(got, ref, F32 * size) <= F32 * size + 1e-30).all()
+
+
+@pytest.mark.gpu
 def test_offsets_beyond_32_bits_and_streams():
     T, ld, d = 70000, 32768, 16
     base = torch.empty((T, ld), device="cuda", dtype=torch.bfloat16)
