@@ -531,14 +531,13 @@ extern "C" size_t hla2_gated_scan_workspace(int B, int H, int T, int d) {
     using namespace hla2;
     if (B <= 0 || H <= 0 || T <= 0 || d <= 0 || d > 128 || (long long)B * H > 65535) return 0;
     const int lanes = lanes_of(d), rows = B * H;
-    return (lookback_bytes(rows, (T + tile_of(lanes) - 1) / tile_of(lanes), lanes * kCh, d) + 255) & ~size_t(255);
+    return (lookback_bytes(rows, tiles_of(T, tile_of(lanes)), lanes * kCh, d) + 255) & ~size_t(255);
 }
 
 extern "C" size_t hla2_gated_scan_carry_len(int T, int d) {
     using namespace hla2;
     if (T <= 0 || d <= 0 || d > 128) return 0;
-    const int kept = tile_of(lanes_of(d));
-    return (size_t)((T + kept - 1) / kept) * d;
+    return (size_t)tiles_of(T, tile_of(lanes_of(d))) * d;
 }
 
 extern "C" int hla2_gated_scan(const void* X, const void* G, const unsigned char* reset, const float* state_in, void* O,
@@ -566,7 +565,7 @@ extern "C" int hla2_gated_scan(const void* X, const void* G, const unsigned char
     take_strides(p.sg, strides, 1, H, T, gate_shared ? 1 : d);
     take_strides(p.so, strides, 2, H, T, d);
     const int lanes = lanes_of(d), tile = tile_of(lanes);
-    p.tiles = (T + tile - 1) / tile;
+    p.tiles = tiles_of(T, tile);
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     p.status = device_status_word();  // where a wait that runs out is reported
     if (!p.status) return set_error(HLA2_ERR_LAUNCH, "%s: cannot resolve the device status word", what);

@@ -23,6 +23,8 @@ constexpr unsigned long long kGateWaitNs = 2000000000ull;  // bounded waits: 2 s
 __host__ __device__ constexpr int lanes_of(int d) { return d <= 64 ? 16 : 32; }
 // Tokens of a tile: a state is kept for the gradient at the start of each.
 __host__ __device__ constexpr int tile_of(int lanes) { return kData / lanes * kTok; }
+// Tiles of T > 0 tokens; T may be any int.
+__host__ __device__ constexpr int tiles_of(int T, int tile) { return (T - 1) / tile + 1; }
 // Threads of a block of the register kernels: those that hold the tile, and a warp for each 32 channels that joins tiles.
 __host__ __device__ constexpr int block_threads(int lanes) { return kData + lanes * kCh; }
 

@@ -612,7 +612,7 @@ extern "C" int hla2_gated_scan_backward(const void* X, const void* G, const unsi
     take_strides(p.sdx, strides, 3, H, T, d);
     take_strides(p.sdg, strides, 4, H, T, gate_shared ? 1 : d);
     const int lanes = lanes_of(d), tile = tile_of(lanes);
-    p.tiles = (T + tile - 1) / tile;
+    p.tiles = tiles_of(T, tile);
     const bool vec = d % kCh == 0 && aligned_to(X, es, p.sx, 3, kCh * es) && aligned_to(dX, es, p.sdx, 3, kCh * es) &&
                      aligned_to(dO, os, p.sdo, 3, kCh * os) &&
                      (gate_shared || (aligned_to(G, es, p.sg, 3, kCh * es) && aligned_to(dG, es, p.sdg, 3, kCh * es)));

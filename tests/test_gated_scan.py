@@ -614,6 +614,14 @@ def test_states_that_overlap_are_refused():
         assert "overlap" in hla2.hla2_last_error_detail()
 
 
+def test_sizes_up_to_the_largest_int():
+    for T in (1, 63, 64, 65, 128, 129, 1 << 30, 2 ** 31 - 129, 2 ** 31 - 64, 2 ** 31 - 1):
+        for d, tile, channels in ((16, 128, 64), (64, 128, 64), (65, 64, 128), (128, 64, 128)):
+            tiles = -(-T // tile)
+            assert hla2.hla2_gated_scan_carry_len(T, d) == tiles * d
+            assert hla2.hla2_gated_scan_workspace(1, 1, T, d) >= (tiles * channels * 8 if tiles > 1 else 0)
+
+
 def test_no_launch_without_a_status_word():
     """Where the device's status word cannot be had (here: no device at all), the scan and its gradient say so
     before they launch anything that would report through it."""
