@@ -614,6 +614,7 @@ extern "C" int hla2_gated_step(float* state, const void* x, const void* g, void*
     if (!aligned_elem(state, 4) || !aligned_elem(state_out, 4) || !aligned_elem(x, es) || !aligned_elem(g, es) ||
         !aligned_elem(o, os))
         return set_error(HLA2_ERR_INVALID, "%s: pointer not aligned to its element", what);
+    if (int rc = check_states(what, state, state_out, (size_t)n * d)) return rc;
     if (!state_out) state_out = state;
     const long long ldx = ld ? ld[0] : d, ldg = ld ? ld[1] : gate_shared ? 1 : d, ldo = ld ? ld[2] : d;
     const bool vec = d % 4 == 0 && aligned_to(state, 4, nullptr, 0, 16) && aligned_to(state_out, 4, nullptr, 0, 16) &&

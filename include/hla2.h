@@ -421,7 +421,8 @@ HLA2_API int hla2_gated_scan_backward(const void* X, const void* G, const unsign
 /*
  * One token of the recurrence for n heads: h = a state + u, o = h.
  *   state [n][d] fp32;  x [n][d], g [n][d] (or [n] when gate_shared), dtype;
- *   o [n][d], out_dtype;  state_out [n][d] fp32, or NULL to update in place.
+ *   o [n][d], out_dtype;  state_out [n][d] fp32, or NULL to update in place; it
+ *   may be state, but not overlap it otherwise.
  *   ld: row strides of x, g and o, or NULL for dense; the states are dense.
  * Errors as for the forward (n <= 0: HLA2_ERR_INVALID).
  */

@@ -612,6 +612,9 @@ def test_states_that_overlap_are_refused():
                                           p(65536 + off), B, H, T, d, None, 0, 0, 0, 0, None, 0,
                                           None) == hla2.HLA2_ERR_INVALID
         assert "overlap" in hla2.hla2_last_error_detail()
+        assert L.hla2_gated_step(p(65536), p(4096), p(4096), p(4096), p(65536 + off), B * H, d, None, 0, 0, 0, 0,
+                                 None) == hla2.HLA2_ERR_INVALID
+        assert "overlap" in hla2.hla2_last_error_detail()
 
 
 def test_sizes_up_to_the_largest_int():
