@@ -435,6 +435,125 @@ def test_strided_and_unaligned_operands(dtype):
             assert (t[..., :off] == 7).all() and (t[..., off + d:] == 7).all()
 
 
+def check_large(B, H, T, d, dtype, out_dtype, form, shared, reset, seed, layout="bthd"):
+    """check(), with the 64-bit recurrences on the GPU, all heads at once."""
+    x, gate = make(B, H, T, d, dtype, form, shared, seed, layout)
+    r = resets(reset, B, T)
+    gen = torch.Generator().manual_seed(seed + 7)
+    h0, dl = torch.randn(B, H, d, generator=gen), torch.randn(B, H, d, generator=gen)
+    do = torch.randn(B, H, T, d, generator=gen).to(out_dtype)
+    xc, gc, doc, h0c, dlc = x.cuda(), gate.cuda(), do.cuda(), h0.cuda(), dl.cuda()
+    rc = None if r is None else r.cuda()
+    a, u = gates64(xc, gc, form)
+    z = torch.sigmoid(-(gc.double()[..., None] if shared else gc.double())) if form == "sigmoid" else None
+    keep = torch.ones(B, T, dtype=torch.bool, device="cuda") if rc is None else ~rc
+    h, hs, before = h0c.double(), torch.empty_like(u), torch.empty_like(u)
+    for t in range(T):
+        h = torch.where(keep[:, t, None, None], h, 0.0)
+        before[:, :, t] = h
+        h = a[:, :, t] * h + u[:, :, t]
+        hs[:, :, t] = h
+    mu, lam = dlc.double(), torch.empty_like(u)
+    for t in range(T - 1, -1, -1):
+        lam[:, :, t] = doc[:, :, t].double() + mu
+        mu = torch.where(keep[:, t, None, None], a[:, :, t] * lam[:, :, t], 0.0)
+    rx = z * lam if form == "sigmoid" else lam
+    rg = lam * a * z * (before - xc.double()) if form == "sigmoid" else lam * before
+    carry = torch.full((B, H, hla2.hla2_gated_scan_carry_len(T, d)), float("nan"), device="cuda")
+    last, d0 = torch.empty_like(h0c), torch.empty_like(h0c)
+    o = hla2.hla2_gated_scan(xc, gc, form=form, reset=rc, state_in=h0c, state_out=last, carry=carry, out_dtype=out_dtype)
+    dx, dg = hla2.hla2_gated_scan_backward(xc, gc, doc, carry, form=form, reset=rc, dstate_out=dlc, dstate_in=d0)
+    assert rel(o, hs.cpu()) < F32 and rel(last, h.cpu(), hs.abs().max()) < F32
+    assert rel(dx, rx.cpu()) < F32 and rel(d0, mu.cpu(), max(mu.abs().max(), rx.abs().max())) < F32
+    if shared:
+        assert rel(dg, rg.sum(-1).cpu(), rg.abs().sum(-1).max()) < F32
+    else:
+        assert rel(dg, rg.cpu()) < F32
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("dtype,out", [(torch.bfloat16, torch.bfloat16), (torch.bfloat16, torch.float32),
+                                       (torch.float32, torch.float32)])
+@pytest.mark.parametrize("B,H,T,d,reset", [(2, 40, 2500, 64, "random"), (1, 20, 3001, 128, "random"),
+                                           (3, 25, 1200, 80, "edges"), (1, 64, 2000, 128, "none")])
+def test_many_tiles_to_a_block(form, shared, dtype, out, B, H, T, d, reset):
+    """940 to 2048 tiles, 6 to 14 for each SM of a GB300: every ring of stages is used again, with the resets, maps
+    and flags that its stages hold, in each direction and with both layouts of gates."""
+    check_large(B, H, T, d, dtype, out, form, shared, reset, 101)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d", [(torch.bfloat16, 64), (torch.bfloat16, 128), (torch.float32, 64)])
+@pytest.mark.parametrize("shared", [False, True])
+def test_runs_beyond_the_range_of_products(dtype, d, shared):
+    """Gates and inputs, here and there, whose products over a few tokens leave fp32's range, beside ordinary ones, in
+    both directions."""
+    B, H, T = 1, 40, 1500
+    g = torch.Generator().manual_seed(103)
+    shape = (B, H, T) if shared else (B, H, T, d)
+    gate = 2 + 1.5 * torch.randn(shape, generator=g)
+    odd = torch.rand(shape, generator=g)
+    for i, v in enumerate((15.0, 40.0, 90.0, 1e4, -1e4, -90.0, float("inf"), -float("inf"))):
+        gate[(odd >= 0.004 * i) & (odd < 0.004 * (i + 1))] = v
+    gate[:, :, 700:800] += 12  # a stretch that hardly forgets
+    gate = gate.to(dtype)
+    x = torch.randn(B, H, T, d, generator=g).to(dtype)
+    do = torch.randn(B, H, T, d, generator=g).to(dtype)
+    carry = torch.empty(B, H, hla2.hla2_gated_scan_carry_len(T, d), device="cuda")
+    ref = forward64(x, gate, "sigmoid")
+    assert rel(hla2.hla2_gated_scan(x.cuda(), gate.cuda(), carry=carry), ref) < F32
+    dx, dg = hla2.hla2_gated_scan_backward(x.cuda(), gate.cuda(), do.cuda(), carry)
+    rx, rg, _ = backward64(x, gate, do, "sigmoid")
+    assert rel(dx, rx) < F32
+    assert (rel(dg, rg.sum(-1), rg.abs().sum(-1).max()) if shared else rel(dg, rg)) < F32
+    by = 2.0 ** 100  # inputs that many times as large: so is every result
+    assert rel(hla2.hla2_gated_scan(x.cuda() * by, gate.cuda()) / by, ref) < F32
+
+
+@pytest.mark.gpu
+def test_graph_replays_on_new_values():
+    """A graph of the scan, its gradient and the step, replayed on inputs changed in place, with the workspaces as the
+    replay before left them (tickets and maps of other inputs)."""
+    B, H, T, d = 2, 3, 3000, 64
+    sets = [[t.cuda() for t in make(B, H, T, d, torch.bfloat16, "sigmoid", False, 111 + i)] for i in range(3)]
+    x, gate = (t.clone() for t in sets[0])
+    do = torch.randn(B, H, T, d, generator=torch.Generator().manual_seed(112)).cuda()
+    o, dx, dg = torch.empty(x.shape, device="cuda"), torch.empty_like(x), torch.empty_like(gate)
+    n = hla2.hla2_gated_scan_workspace(B, H, T, d)
+    w1, w2 = (torch.empty(n, device="cuda", dtype=torch.uint8) for _ in range(2))
+    carry = torch.zeros(B, H, hla2.hla2_gated_scan_carry_len(T, d), device="cuda")
+    state, so = torch.zeros(B * H, d, device="cuda"), torch.empty(B * H, d, device="cuda")
+    xt, gt = (t[:, :, 5].reshape(B * H, d).clone() for t in (x, gate))
+
+    def calls():
+        hla2.hla2_gated_scan(x, gate, O=o, carry=carry, state_in=state.view(B, H, d), state_out=state.view(B, H, d),
+                             workspace=w1)
+        hla2.hla2_gated_scan_backward(x, gate, do, carry, dX=dx, dG=dg, workspace=w2)
+        hla2.hla2_gated_step(state, xt, gt, o=so)
+
+    calls()  # loads the kernels
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    state.zero_()
+    follow = torch.zeros(B, H, d, device="cuda")
+    for k in (0, 1, 2, 1):
+        x.copy_(sets[k][0])
+        gate.copy_(sets[k][1])
+        xt.copy_(x[:, :, 5].reshape(B * H, d))
+        gt.copy_(gate[:, :, 5].reshape(B * H, d))
+        graph.replay()
+        kept = torch.empty_like(carry)
+        ref = hla2.hla2_gated_scan(x, gate, carry=kept, state_in=follow, state_out=follow)
+        rx, rg = hla2.hla2_gated_scan_backward(x, gate, do, kept)
+        rs = hla2.hla2_gated_step(follow.view(B * H, d), xt, gt)
+        assert torch.equal(o, ref) and torch.equal(dx, rx) and torch.equal(dg, rg)
+        assert torch.equal(so, rs) and torch.equal(state, follow.view(B * H, d))
+
+
 def windows(T, d, seed, dtype=torch.float32, step=1):
     """[1, 2, T, d] whose rows are windows of d elements, `step` apart, of one sequence for each head."""
     base = torch.randn(2, (T - 1) * step + d, generator=torch.Generator().manual_seed(seed)).to(dtype)

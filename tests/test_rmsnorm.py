@@ -255,6 +255,29 @@ def test_offsets_beyond_32_bits_and_streams():
     close(y, norm64(x, None, None)[1], F32)
 
 
+@pytest.mark.gpu
+def test_graph_replays_on_new_values():
+    """A graph of the norms, as a decoding loop would keep it, on inputs changed in place."""
+    rows, C = 16, 512
+    g = torch.Generator().manual_seed(31)
+    sets = [[torch.randn(rows, C, generator=g).to(torch.bfloat16).cuda() for _ in range(3)] for _ in range(3)]
+    x, r, dy = (t.clone() for t in sets[0])
+    w = (1 + 0.1 * torch.randn(C, generator=g)).to(torch.bfloat16).cuda()
+    calls = lambda: (*hla2.hla2_rmsnorm(x, w, residual=r), *hla2.hla2_rmsnorm_q8(x, w, residual=r),
+                     *hla2.hla2_rmsnorm_backward(x, dy, w, dS=r))
+    calls()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = calls()
+    for s in sets:
+        for to, value in zip((x, r, dy), s):
+            to.copy_(value)
+        graph.replay()
+        for a, b in zip(held, calls()):
+            assert torch.equal(a.float(), b.float())
+
+
 # ---------------------------------------------------------------- refusals ----
 def test_binding_refuses():
     x = torch.zeros(4, 8)

@@ -192,6 +192,27 @@ def test_offsets_beyond_32_bits_and_streams():
     assert (excess(o, ref, F32 * size) <= F32 * size + 1e-30).all()
 
 
+@pytest.mark.gpu
+def test_graph_replays_on_new_values():
+    """A graph of single tokens, as a decoding loop would keep it, on positions and values changed in place."""
+    g = torch.Generator().manual_seed(12)
+    q, k = torch.randn(8, 1, 16, 64, generator=g).cuda().transpose(1, 2), torch.randn(8, 1, 4, 64, generator=g).cuda().transpose(1, 2)
+    pos, f = torch.zeros(3, 8, 1, dtype=torch.int32, device="cuda"), freqs(32).cuda()
+    call = lambda: hla2.hla2_rotary(q, pos, f, (12, 10, 10), K=k)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = call()
+    for step in range(3):
+        pos.copy_(torch.randint(0, 5000, pos.shape, generator=g, dtype=torch.int32))
+        q.copy_(torch.randn(q.shape, generator=g))
+        k.copy_(torch.randn(k.shape, generator=g))
+        graph.replay()
+        for a, b in zip(held, call()):
+            assert torch.equal(a, b)
+
+
 # ---------------------------------------------------------------- refusals ----
 def test_binding_refuses():
     q, pos, f = torch.zeros(2, 3, 5, 8), torch.zeros(1, 2, 5, dtype=torch.int32), torch.zeros(4)
