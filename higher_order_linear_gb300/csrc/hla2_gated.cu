@@ -28,7 +28,7 @@
 //
 // What bounds it.  Forward of 1 x 16 x 65536 x 128, 16-bit in, 32-bit out (1.07 GB,
 // 158 us at the copy bandwidth of 6.8 TB/s): 185 us, 0.85 of it; 16-bit out
-// (0.81 GB, 118 us): 171 us.  An earlier stand of the pipeline took 170 us with the
+// (0.81 GB, 118 us): 174 us.  An earlier stand of the pipeline took 170 us with the
 // waits between blocks left out: they cost the rest, by the way of a state from
 // group to group, about 1.3 us a hop through L2, and by the maps to be read for
 // each tile (groups of 6 tiles took 215 us where 8 took 200, 12 211 and 16 237, all
@@ -338,7 +338,7 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
     const int at = mapper ? tid - 32 : tid - (LY::kThreads - kData);
     const int lane = at % LANES, run = at / LANES;
     const int c = lane * kCh, nc = p.d - c;
-    constexpr int NG = SHARED ? 1 : kCh;
+    constexpr int NG = SHARED ? 2 : kCh;
     Ring<M, 1> slot(0);
     for (Ring<S, 1> ring(0);; ring.next(), slot.next()) {
         const int s = ring.s;
@@ -369,14 +369,14 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
         }
         // e^g where by_power, else a gate as next_state() takes it
         auto gates_of = [&](int i2, float (&ga)[NG]) {
-            if constexpr (SHARED) ga[0] = gl[i2];
+            if constexpr (SHARED) ga[0] = ga[1] = gl[i2];
             else four(gs + i2 * p.d, ga);
         };
         auto gates = [&](int i2, float (&ga)[NG], bool by_power) {  // e^g, or gates as next_state() takes them
             gates_of(i2, ga);
             if (!SIG) return;
             if (by_power) {
-                gate_powers(ga);
+                gate_powers(ga, mapper);
                 return;
             }
 #pragma unroll
@@ -388,7 +388,7 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
             auto walk = [&](auto whole, auto clean) {
 #pragma unroll
                 for (int j = 0; j < kCh; ++j) { A[j] = 1.f; X[j] = 0.f; }
-#pragma unroll
+#pragma unroll(SIG && !SHARED ? 1 : kTok)
                 for (int i2 = 0; i2 < kTok; ++i2)
                     if (whole || i2 < nt) {
                         float xv[kCh], ga[NG];
@@ -416,12 +416,23 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
                         if (!clean && ((resets >> i2) & 1u)) fill(X, 0.f);
                         w.token(E, X, xv);
                     }
-                bool in = true;
+                bool in = true, surely = true;
 #pragma unroll
                 for (int j = 0; j < kCh; ++j) {
-                    float per;
-                    in = w.close(SHARED ? 0 : j, A[j], per) && fabsf(X[j]) < INFINITY && in;
+                    const float per = w.close(j % NG, A[j]);
+                    surely = surely && w.D[j % NG] < kSurely;
+                    in = in && w.D[j % NG] < kPerhaps && fabsf(X[j]) < INFINITY;
                     X[j] *= per;
+                }
+                if (in && !surely) {
+#pragma unroll(SHARED ? kTok : 1)
+                    for (int i2 = 0; i2 < kTok; ++i2)
+                        if (i2 < nt) {
+                            float ga[NG];
+                            gates_of(i2, ga);
+#pragma unroll
+                            for (int j = 0; j < NG; ++j) in = in && ga[j] < kLargestGate;
+                        }
                 }
                 return in;
             };
@@ -454,7 +465,7 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
             if ((tid & 31) == 0) mbar_arrive(taken(slot.s));
             const long long off = info[s].o + run * kTok * p.so[2] + c;
             auto walk = [&](auto whole, auto clean, auto by_power, auto* o) {
-#pragma unroll
+#pragma unroll(!SIG || SHARED || by_power ? kTok : 1)
                 for (int i2 = 0; i2 < kTok; ++i2)
                     if (whole || i2 < nt) {
                         float xv[kCh], ga[NG];

@@ -97,66 +97,69 @@ __device__ __forceinline__ void back_token(float gate, float lam, float before, 
 //   X = N / D,  N -> E N + x D;      A = P / D = 1 - Q / D,  Q -> E Q + D;
 // A is taken from the smaller of P and Q, so that a long memory's 1 - A is good to its
 // own size and not to A's.  For the gradient Y = M / D, M -> (1 + E) M + P dh.
-// Where a product leaves fp32's range (gates above 8 at every token of a run and more,
-// inf, NaN) the run is walked with sigmoid_gate() instead.  Per element and token this
-// takes 7 operations in the map and 7 in the walk that writes; sigmoid_gate() and its
-// selections took 12 and 10, which made the scan of 65536 x 16 x 128 240 us.
-// Two elements to an instruction where there are pairs (f32x2) halve that again.
-template <int N, typename F1, typename F2>
-__device__ __forceinline__ void by_pairs(float (&o)[N], const float (&a)[N], const float (&b)[N], const float (&c)[N],
-                                         F1&& one, F2&& two) {
-    if constexpr (N % 2 == 0) {
+// Every token's E and 1 are scaled by 2^-6: D then holds for gates of 14 at every token
+// of a run, and an A below 2^-78 loses bits.  A run of larger gates, or with inf or NaN,
+// is walked with sigmoid_gate() instead.  Scan of 65536 x 16 x 128 with gates of
+// 2 +- 1.5: 184 us, 9: 188, 12: 212, 14: 345 (unscaled, 9: 510).  Per element and token this takes 7.5 operations in the map and 7 in the
+// walk that writes; sigmoid_gate() and its selections took 12 and 10, which made the
+// scan of 65536 x 16 x 128 240 us.
+// Two elements to an instruction (f32x2) halve that again.
+template <int N, typename F>
+__device__ __forceinline__ void by_pairs(float (&o)[N], const float (&a)[N], const float (&b)[N], const float (&c)[N], F&& f) {
+    static_assert(N % 2 == 0, "pairs");
 #pragma unroll
-        for (int j = 0; j < N; j += 2) {
-            unsigned long long x, y, z, r;
-            asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a[j]), "f"(a[j + 1]));
-            asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b[j]), "f"(b[j + 1]));
-            asm("mov.b64 %0, {%1, %2};" : "=l"(z) : "f"(c[j]), "f"(c[j + 1]));
-            r = two(x, y, z);
-            asm("mov.b64 {%0, %1}, %2;" : "=f"(o[j]), "=f"(o[j + 1]) : "l"(r));
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < N; ++j) o[j] = one(a[j], b[j], c[j]);
+    for (int j = 0; j < N; j += 2) {
+        unsigned long long x, y, z;
+        asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a[j]), "f"(a[j + 1]));
+        asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b[j]), "f"(b[j + 1]));
+        asm("mov.b64 %0, {%1, %2};" : "=l"(z) : "f"(c[j]), "f"(c[j + 1]));
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(o[j]), "=f"(o[j + 1]) : "l"(f(x, y, z)));
     }
 }
 template <int N>
 __device__ __forceinline__ void fmas(float (&o)[N], const float (&a)[N], const float (&b)[N], const float (&c)[N]) {
     using u = unsigned long long;
-    by_pairs(o, a, b, c, [](float x, float y, float z) { return fmaf(x, y, z); },
-             [](u x, u y, u z) { u r; asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z)); return r; });
+    by_pairs(o, a, b, c, [](u x, u y, u z) { u r; asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z)); return r; });
 }
 template <int N>
 __device__ __forceinline__ void products(float (&o)[N], const float (&a)[N], const float (&b)[N]) {
     using u = unsigned long long;
-    by_pairs(o, a, b, b, [](float x, float y, float) { return x * y; },
-             [](u x, u y, u) { u r; asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y)); return r; });
+    by_pairs(o, a, b, b, [](u x, u y, u) { u r; asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y)); return r; });
 }
 template <int N>
 __device__ __forceinline__ void sums(float (&o)[N], const float (&a)[N], const float (&b)[N]) {
     using u = unsigned long long;
-    by_pairs(o, a, b, b, [](float x, float y, float) { return x + y; },
-             [](u x, u y, u) { u r; asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y)); return r; });
+    by_pairs(o, a, b, b, [](u x, u y, u) { u r; asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y)); return r; });
 }
 template <int N>
 __device__ __forceinline__ void fill(float (&o)[N], float v) {
 #pragma unroll
     for (int j = 0; j < N; ++j) o[j] = v;
 }
-// a gate shared by the channels, or one for each, for all of them
+// Gates of a token: one for each channel, or a shared one twice, which is the pair that
+// every pair of channels takes (formed for each use, the moves made the scan of
+// 65536 x 16 x 128 with a shared gate 190 us for 174).
 template <int N, int NG>
 __device__ __forceinline__ void each(float (&o)[N], const float (&g)[NG]) {
+    static_assert(NG == N || NG == 2, "gates of the channels, or a pair");
 #pragma unroll
-    for (int j = 0; j < N; ++j) o[j] = g[NG == 1 ? 0 : j];
+    for (int j = 0; j < N; ++j) o[j] = g[j % NG];
 }
 
+// e^g, or e^g 2^-6 where `scaled`
+constexpr float kGateScale = 0x1p-6f;
 template <int N>
-__device__ __forceinline__ void gate_powers(float (&g)[N]) {  // e^g
-    float l[N];
+__device__ __forceinline__ void gate_powers(float (&g)[N], bool scaled) {
+    float l[N], shift[N];
     fill(l, 1.4426950408889634f);
-    products(g, g, l);
+    fill(shift, -6.f);
+    if (scaled) fmas(g, g, l, shift);
+    else products(g, g, l);
 #pragma unroll
-    for (int j = 0; j < N; ++j) asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(g[j]) : "f"(g[j]));
+    for (int j = 0; j < N; ++j) {
+        if (N == 2 && j) g[j] = g[0];
+        else asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(g[j]) : "f"(g[j]));
+    }
 }
 __device__ __forceinline__ float reciprocal(float v) {
     float r;
@@ -169,7 +172,7 @@ __device__ __forceinline__ void keeps(float (&z)[N], const float (&E)[N]) {  // 
     fill(one, 1.f);
     sums(z, E, one);
 #pragma unroll
-    for (int j = 0; j < N; ++j) z[j] = reciprocal(z[j]);
+    for (int j = 0; j < N; ++j) z[j] = N == 2 && j ? z[0] : reciprocal(z[j]);
 }
 template <int NG>
 struct Powers {
@@ -179,31 +182,40 @@ struct Powers {
         fill(P, 1.f);
         fill(Q, 0.f);
     }
-    // a token: X is N, Y is M; u counts where `open`
+    // a token, E scaled: X is N
     __device__ __forceinline__ void token(const float (&E)[NG], float (&X)[kCh], const float (&x)[kCh]) {
-        float e[kCh], d[kCh];
+        float e[kCh], d[kCh], one[NG];
+        fill(one, kGateScale);
+        products(one, one, D);
         each(e, E);
-        each(d, D);
+        each(d, one);
         products(d, d, x);
         fmas(X, e, X, d);
-        fmas(Q, E, Q, D);
-        fmas(D, D, E, D);
+        fmas(Q, E, Q, one);
+        fmas(D, D, E, one);
         products(P, P, E);
     }
-    __device__ __forceinline__ void back_token(const float (&E)[NG], float (&Y)[kCh], const float (&u)[kCh], bool open) {
-        float e[kCh], q[kCh];
+    // Y is M; u counts where `open`
+    __device__ __forceinline__ void back_token(const float (&E)[NG], float (&Y)[kCh], const float (&u)[kCh], bool open) const {
+        float e[kCh], q[kCh], one[kCh];
         each(e, E);
         each(q, P);
-        fmas(Y, Y, e, Y);
+        fill(one, kGateScale);
+        products(one, one, Y);
+        fmas(Y, Y, e, one);
         if (open) fmas(Y, q, u, Y);
     }
-    // A and 1 / D of gate j; false where the products may have left the range
-    __device__ __forceinline__ bool close(int j, float& A, float& per) const {
-        per = reciprocal(D[j]);
+    // A of gate j; returns 1 / D
+    __device__ __forceinline__ float close(int j, float& A) const {
+        const float per = reciprocal(D[j]);
         A = P[j] < Q[j] ? P[j] * per : fmaf(-Q[j], per, 1.f);
-        return D[j] < 0x1p100f;
+        return per;
     }
 };
+// Ranges of the D of a run of kTok tokens: below the first no E is above 2^126, below
+// the second the products hold, but each E must be looked at.
+constexpr float kSurely = 0x1p78f, kPerhaps = 0x1p120f, kLargestGate = 83.f;  // e^83 < 2^120
+
 // A token with E: h -> a h + z x
 template <int NG>
 __device__ __forceinline__ void next_by_power(const float (&E)[NG], float (&h)[kCh], const float (&x)[kCh]) {

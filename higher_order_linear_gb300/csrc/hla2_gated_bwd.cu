@@ -12,15 +12,15 @@
 // need no rounding to 16 bits, and reading x costs what reading h would.
 //
 // What bounds it.  4 x 16 x 4096 x 64, 16 bits (168 MB, 25 us at the copy
-// bandwidth): 61 us; with the forward (100 MB, 15 us) of 38 us a training pass
-// takes 99 us (93 with the gate as z alone, whose 1 - z loses what a closing gate
-// leaves; 129 with sigmoid_gate() throughout).  A tile is on chip for about 7 us (loads 0.8, mapping 1.0, waiting
-// for tiles of other blocks 2.6, writing 1.7) and shared memory holds three, so one
-// leaves every 2.5 to 2.9 us against 1.8 us for its bytes; a launch of 13 tiles to
-// an SM also pays for the filling and emptying of that pipeline.  In registers,
-// without the ring: about 85 us.  Tried and left out: a fourth stage, with h_{t-1} in
-// the place of the 16-bit x and gate (62 us: the writers then keep x and the gates as
-// loaded, and spill more than they gain).
+// bandwidth): 58 us; with the forward (100 MB, 15 us) of 35 us a training pass
+// takes 93 us (129 with sigmoid_gate() throughout).  A tile is on chip for about 7 us
+// (loads 0.8, mapping 1.0, waiting for tiles of other blocks 2.6, writing 1.7) and
+// shared memory holds three, so one leaves every 2.5 to 2.9 us against 1.8 us for its
+// bytes; a launch of 13 tiles to an SM also pays for the filling and emptying of that
+// pipeline.  In registers, without the ring and with wide accesses: about 85 us.  Tried
+// and left out, when the writers still kept a run's gates: a fourth stage, with h_{t-1}
+// in the place of the 16-bit x and gate (62 us for 56: they then kept x as loaded too,
+// and spilled more than the stage gave).
 #include "hla2_gated.cuh"
 
 namespace hla2 {
@@ -201,7 +201,7 @@ struct BackLayout {
     static constexpr int kFit = (int)((222 * 1024 - kBefore) / kStage);
     static constexpr int kStages = kFit > 6 ? 6 : kFit;
     static constexpr uint32_t kBytes = kStage * kStages + kBefore + 128;
-    static constexpr int kJoin = 2;  // a third set would take registers that the writers need
+    static constexpr int kJoin = 2;  // as many as the smallest ring has stages
     static constexpr int kThreads = 32 + kData + kJoin * CB + kComposers + kData;
 };
 
@@ -211,7 +211,7 @@ gated_pipe_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
                       const __grid_constant__ CUtensorMap mu_, const GateParams p) {
     using T = bf16;
     using LY = BackLayout<TO, SHARED, LANES>;
-    constexpr int CB = LY::CB, RUNS = LY::RUNS, TILE = LY::TILE, S = LY::kStages, kJoin = LY::kJoin, NG = SHARED ? 1 : kCh;
+    constexpr int CB = LY::CB, RUNS = LY::RUNS, TILE = LY::TILE, S = LY::kStages, kJoin = LY::kJoin, NG = SHARED ? 2 : kCh;
     extern __shared__ __align__(128) unsigned char raw[];
     __shared__ __align__(8) unsigned long long bars[6 * S];
     static_assert(S >= kJoin, "the ends of the tickets take a stage for each group of joiners");
@@ -407,14 +407,14 @@ gated_pipe_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
         }
         // e^g where by_power, else a gate as next_state() takes it
         auto gates_of = [&](int i2, float (&ga)[NG]) {
-            if constexpr (SHARED) ga[0] = gl[i2];
+            if constexpr (SHARED) ga[0] = ga[1] = gl[i2];
             else four(gs + i2 * p.d, ga);
         };
         auto gates = [&](int i2, float (&ga)[NG], bool by_power) {  // e^g, or gates as next_state() takes them
             gates_of(i2, ga);
             if (!SIG) return;
             if (by_power) {
-                gate_powers(ga);
+                gate_powers(ga, mapper);
                 return;
             }
 #pragma unroll
@@ -428,7 +428,7 @@ gated_pipe_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
                 bool open = true;  // no reset so far
 #pragma unroll
                 for (int j = 0; j < kCh; ++j) { A[j] = 1.f; X[j] = 0.f; Y[j] = 0.f; }
-#pragma unroll
+#pragma unroll(SIG && !SHARED ? 1 : kTok)
                 for (int i2 = 0; i2 < kTok; ++i2)
                     if (whole || i2 < nt) {
                         float xv[kCh], uv[kCh], ga[NG];
@@ -463,13 +463,24 @@ gated_pipe_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
                         w.token(E, X, xv);
                         w.back_token(E, Y, uv, clean || open);
                     }
-                bool in = true;
+                bool in = true, surely = true;
 #pragma unroll
                 for (int j = 0; j < kCh; ++j) {
-                    float per;
-                    in = w.close(SHARED ? 0 : j, A[j], per) && fabsf(X[j]) < INFINITY && fabsf(Y[j]) < INFINITY && in;
+                    const float per = w.close(j % NG, A[j]);
+                    surely = surely && w.D[j % NG] < kSurely;
+                    in = in && w.D[j % NG] < kPerhaps && fabsf(X[j]) < INFINITY && fabsf(Y[j]) < INFINITY;
                     X[j] *= per;
                     Y[j] *= per;
+                }
+                if (in && !surely) {
+#pragma unroll(SHARED ? kTok : 1)
+                    for (int i2 = 0; i2 < kTok; ++i2)
+                        if (i2 < nt) {
+                            float ga[NG];
+                            gates_of(i2, ga);
+#pragma unroll
+                            for (int j = 0; j < NG; ++j) in = in && ga[j] < kLargestGate;
+                        }
                 }
                 return in;
             };
@@ -504,24 +515,38 @@ gated_pipe_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
             four(plane(s, 2) + run * CB + c, mu);
             T* const dxp = static_cast<T*>(p.dx) + info[s].o + run * kTok * p.sdx[2] + c;
             T* const dgp = static_cast<T*>(p.dg) + info[s].o2 + run * kTok * p.sdg[2] + (SHARED ? 0 : c);
+            // A gate for each channel is formed on either way from the tile: kept, the run's 32
+            // went to local memory (63 us for 58).  Shared ones are formed once.
             auto walk = [&](auto whole, auto clean, auto by_power) {
-                float z[kTok][NG];
+                if (SHARED && SIG) {
+#pragma unroll
+                    for (int i2 = 0; i2 < kTok; ++i2)
+                        if (whole || i2 < nt) {
+                            float ga[NG];
+                            gates(i2, ga, by_power);
+                            gl[SHARED ? i2 : 0] = ga[0];
+                        }
+                }
+                auto formed = [&](int i2, float (&ga)[NG]) {
+                    if (SHARED) gates_of(i2, ga);
+                    else gates(i2, ga, by_power);
+                };
 #pragma unroll
                 for (int i2 = 0; i2 < kTok; ++i2)
                     if (whole || i2 < nt) {
-                        float xv[kCh];
+                        float xv[kCh], ga[NG];
                         four(xs + i2 * p.d, xv);
-                        gates(i2, z[i2], by_power);
+                        formed(i2, ga);
                         if (!clean && ((resets >> i2) & 1u)) {
 #pragma unroll
                             for (int j = 0; j < kCh; ++j) h[j] = 0.f;
                         }
                         before[i2 * kData + at] = make_float4(h[0], h[1], h[2], h[3]);
                         if (by_power) {
-                            next_by_power(z[i2], h, xv);
+                            next_by_power(ga, h, xv);
                         } else {
 #pragma unroll
-                            for (int j = 0; j < kCh; ++j) h[j] = next_state<SIG>(z[i2][SHARED ? 0 : j], h[j], xv[j]);
+                            for (int j = 0; j < kCh; ++j) h[j] = next_state<SIG>(ga[SHARED ? 0 : j], h[j], xv[j]);
                         }
                     }
 #pragma unroll
@@ -529,17 +554,18 @@ gated_pipe_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
                     const bool live = whole || i2 < nt;
                     float gx[kCh], gg[kCh];
                     if (live) {
-                        float xv[kCh], uv[kCh];
+                        float xv[kCh], uv[kCh], ga[NG];
                         four(xs + i2 * p.d, xv);
                         four(us + i2 * p.d, uv);
+                        formed(i2, ga);
                         const float4 hb4 = before[i2 * kData + at];
                         const float hb[kCh] = {hb4.x, hb4.y, hb4.z, hb4.w};
                         if (by_power) {
-                            back_by_power(z[i2], uv, hb, xv, gx, gg, mu);
+                            back_by_power(ga, uv, hb, xv, gx, gg, mu);
                         } else {
 #pragma unroll
                             for (int j = 0; j < kCh; ++j)
-                                back_token<SIG>(z[i2][SHARED ? 0 : j], uv[j] + mu[j], hb[j], xv[j], gx[j], gg[j], mu[j]);
+                                back_token<SIG>(ga[SHARED ? 0 : j], uv[j] + mu[j], hb[j], xv[j], gx[j], gg[j], mu[j]);
                         }
                         if (!clean && ((resets >> i2) & 1u)) fill(mu, 0.f);
                         Lane<T, kCh, true> ov;

@@ -386,7 +386,7 @@ enum { HLA2_GATE_SIGMOID = 0, HLA2_GATE_DECAY = 1 };
  * the same bits.  |a_t| is meant to be at most 1; with larger decays the
  * product of the decays of any 1024 tokens in a row must stay finite.  Of the
  * sigmoid form's a and 1 - a each is good to (1.25 |g| + 8) 2^-24 of itself, down to
- * 2^-126.  An inf in x or in the state is inf or NaN from its token on, until a
+ * 2^-120.  An inf in x or in the state is inf or NaN from its token on, until a
  * reset.
  * Errors: HLA2_ERR_INVALID, HLA2_ERR_UNSUPPORTED (d > 128, B*H > 65535,
  * unknown form or type), HLA2_ERR_WORKSPACE, HLA2_ERR_LAUNCH.
