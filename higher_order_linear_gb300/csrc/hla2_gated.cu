@@ -439,7 +439,9 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
             using yes = std::true_type;
             using no = std::false_type;
             if constexpr (SIG) {
-                const bool in = nt == kTok && resets == 0 ? powers(yes{}, yes{}) : nt == kTok ? powers(yes{}, no{}) : powers(no{}, no{});
+                const bool in = nt == kTok && resets == 0 ? powers(yes{}, yes{})
+                                : nt == kTok              ? powers(yes{}, no{})
+                                                          : powers(no{}, no{});
                 if (!in) walk(no{}, no{});
                 const unsigned out = __ballot_sync(0xffffffffu, !in);
                 if ((tid & 31) == 0) wide[s][at >> 5] = out;

@@ -14,7 +14,7 @@
 // 0.95 of the copy bandwidth (6.8 TB/s); 2^20 rows of 128, fp32 to 16 bits (805 MB):
 // 116 us, 1.02; 8 bits, 8191 rows of 8192 (470 MB): 74 us, 0.94, with 256 threads of
 // 32 elements to a row (512 of 16 took 91 us, 1024 of 8 153 us, when this took 76: a barrier holds up more
-// of the SM).  16 rows of 2048 take 2.7 us, a launch.
+// of the SM).  16 rows of 2048 take 2.4 us, a launch.
 //
 // The maximum is taken over the bit patterns of |t w| as whole numbers, which
 // order like the values with NaN above inf, so a NaN reaches the scale.
@@ -215,6 +215,17 @@ cudaError_t launch_norm(const NormParams& p, bool vec, cudaStream_t s) {
     return cudaGetLastError();
 }
 
+// Threads to a row x steps of 8 elements, each against its neighbours on 0.5 GB of
+// 16-bit rows with a residual (us; 79 for its bytes; C = 128: fp32 in, 118; 2048: 39.5):
+//   C = 64:    8 x 1  79.5, 16 x 1 105 (half its lanes idle)
+//   C = 128:  16 x 1 115.4, 8 x 2 120.8
+//   C = 256:  32 x 1  79.4, 16 x 2 79.5, 8 x 4 80.1
+//   C = 512:  32 x 2  80.2, 64 x 1 79.9, 16 x 4 81.1
+//   C = 1024: 128 x 1 80.0, 64 x 2 80.0, 32 x 4 81.0
+//   C = 2048: 256 x 1 41.6, 128 x 2 42.0, 64 x 4 42.9
+//   C = 4096: 256 x 2 80.1, 512 x 1 80.9, 128 x 4 81.2
+//   C = 16384: 512 x 4 82.4, 1024 x 2 94.4
+// and C = 8192 above.  Up to 512 a row stays in one warp, whose sum needs no barrier.
 template <typename T, int OUT>
 cudaError_t pick_norm(const NormParams& p, bool vec, cudaStream_t s) {
     const int C = p.C;
@@ -237,11 +248,13 @@ cudaError_t pick_norm(const NormParams& p, bool vec, cudaStream_t s) {
 // workspace, and a second kernel adds the blocks' in order, so the result does
 // not depend on timing.
 //
-// 16384 x 2048, 16 bits (268 MB, 39.5 us at the copy bandwidth): 53 us, of which the
+// 16384 x 2048, 16 bits (268 MB, 39.5 us at the copy bandwidth): 54 us, of which the
 // second kernel 5.5.  The first one's instructions bound it as much as HBM does
 // (about 29 for each element, the reductions' among them): 8 elements to a thread
 // with the next row's loads in flight take 47 us, 16 elements, whose sums and weights
-// leave registers for half the threads, 54 us or more.
+// leave registers for half the threads, 54 us or more.  Rows beyond 8192 have to take 16
+// all the same, 1024 threads to a row, and go to local memory: 2048 x 12288 82 us, its
+// bytes 30.  The fp32 norm of heads, 2^18 rows of 64 with a 16-bit dy: 45 us, bytes 25.
 struct NormBwdParams {
     const void *t, *dy, *w, *ds;
     void* dx;

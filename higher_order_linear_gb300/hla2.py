@@ -534,8 +534,9 @@ def hla2_decay_step(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: to
 # The gated linear recurrence, the root-mean-square norm and the rotary
 # positions.  Their tensors may be strided (the last dimension contiguous).
 # A decoding step makes these calls on a few kilobytes, where the call itself is
-# the cost: each first asks in one expression whether the arguments are the
-# ordinary ones, and only otherwise goes through the checks one by one.
+# the cost: the step, the norms and the rotary call first ask in one expression
+# whether the arguments are the ordinary ones (dense, outputs not given, a gate for
+# each channel), and only otherwise go through the checks one by one.
 _GATE_FORMS = {"sigmoid": 0, "decay": 1}
 _CODES = {torch.float32: HLA2_DTYPE_F32, torch.bfloat16: HLA2_DTYPE_BF16}
 _F32 = torch.float32
