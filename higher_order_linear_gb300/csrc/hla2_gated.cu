@@ -367,7 +367,6 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
             for (int i2 = 0; i2 < kTok; ++i2)
                 if (i2 < nt) gl[i2] = to_f32(gp[i2 * p.sg[2]]);
         }
-        // e^g where by_power, else a gate as next_state() takes it
         auto gates_of = [&](int i2, float (&ga)[NG]) {
             if constexpr (SHARED) ga[0] = ga[1] = gl[i2];
             else four(gs + i2 * p.d, ga);
@@ -416,24 +415,25 @@ gated_pipe_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
                         if (!clean && ((resets >> i2) & 1u)) fill(X, 0.f);
                         w.token(E, X, xv);
                     }
-                bool in = true, surely = true;
+                float d = 0.f, top = 0.f, low = INFINITY, any = 0.f;
+                span(w.D, d, any);
+                span(X, top, low);
+                bool in = d < kPerhaps && top < INFINITY;
+                if (in && !(d < kSurely && low >= kSmall)) {  // looked at closer
+                    float gate = 0.f, x = 0.f;
+#pragma unroll 1
+                    for (int i2 = 0; i2 < nt; ++i2) {
+                        float xv[kCh], ga[NG];
+                        four(xs + i2 * p.d, xv);
+                        span(xv, x, any);
+                        if constexpr (SHARED) ga[0] = ga[1] = to_f32(gp[i2 * p.sg[2]]);
+                        else four(gs + i2 * p.d, ga);
 #pragma unroll
-                for (int j = 0; j < kCh; ++j) {
-                    const float per = w.close(j % NG, A[j]);
-                    surely = surely && w.D[j % NG] < kSurely;
-                    in = in && w.D[j % NG] < kPerhaps && fabsf(X[j]) < INFINITY;
-                    X[j] *= per;
+                        for (int j = 0; j < NG; ++j) gate = fmaxf(gate, ga[j]);
+                    }
+                    in = gate < kLargestGate && (x == 0.f || x >= kSmallInput);
                 }
-                if (in && !surely) {
-#pragma unroll(SHARED ? kTok : 1)
-                    for (int i2 = 0; i2 < kTok; ++i2)
-                        if (i2 < nt) {
-                            float ga[NG];
-                            gates_of(i2, ga);
-#pragma unroll
-                            for (int j = 0; j < NG; ++j) in = in && ga[j] < kLargestGate;
-                        }
-                }
+                w.close(X, A);
                 return in;
             };
             using yes = std::true_type;

@@ -98,8 +98,8 @@ __device__ __forceinline__ void back_token(float gate, float lam, float before, 
 // A is taken from the smaller of P and Q, so that a long memory's 1 - A is good to its
 // own size and not to A's.  For the gradient Y = M / D, M -> (1 + E) M + P dh.
 // Every token's E and 1 are scaled by 2^-6: D then holds for gates of 14 at every token
-// of a run, and an A below 2^-78 loses bits.  A run of larger gates, or with inf or NaN,
-// is walked with sigmoid_gate() instead.  Scan of 65536 x 16 x 128 with gates of
+// of a run, and an A below 2^-78 loses bits.  A run of larger gates, with inf or NaN, or
+// of inputs all below 2^-74 is walked with sigmoid_gate() instead.  Scan of 65536 x 16 x 128 with gates of
 // 2 +- 1.5: 184 us, 9: 188, 12: 212, 14: 345 (unscaled, 9: 510).  Per element and token
 // this takes 7.5 operations in the map and 7 in the walk that writes; sigmoid_gate() and
 // its selections took 12 and 10, which made that scan 240 us.
@@ -205,16 +205,41 @@ struct Powers {
         fmas(Y, Y, e, one);
         if (open) fmas(Y, q, u, Y);
     }
-    // A of gate j; returns 1 / D
-    __device__ __forceinline__ float close(int j, float& A) const {
-        const float per = reciprocal(D[j]);
-        A = P[j] < Q[j] ? P[j] * per : fmaf(-Q[j], per, 1.f);
-        return per;
+    // N becomes X, and A is formed
+    __device__ __forceinline__ void close(float (&X)[kCh], float (&A)[kCh]) const {
+        float per[NG], a[NG], all[kCh];
+#pragma unroll
+        for (int j = 0; j < NG; ++j) {
+            per[j] = NG == 2 && j ? per[0] : reciprocal(D[j]);
+            a[j] = P[j] < Q[j] ? P[j] * per[j] : fmaf(-Q[j], per[j], 1.f);
+        }
+        each(A, a);
+        each(all, per);
+        products(X, X, all);
+    }
+    __device__ __forceinline__ void close_back(float (&Y)[kCh]) const {  // M becomes Y
+        float per[NG], all[kCh];
+#pragma unroll
+        for (int j = 0; j < NG; ++j) per[j] = NG == 2 && j ? per[0] : reciprocal(D[j]);
+        each(all, per);
+        products(Y, Y, all);
     }
 };
+// The largest and the smallest of |v| and what top and low are; NaN stays.
+template <int N>
+__device__ __forceinline__ void span(const float (&v)[N], float& top, float& low) {
+#pragma unroll
+    for (int j = 0; j < N; j += 2) {
+        asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(top) : "f"(v[j]), "f"(v[j + 1]));
+        asm("min.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(low) : "f"(v[j]), "f"(v[j + 1]));
+    }
+}
 // Ranges of the D of a run of kTok tokens: below the first no E is above 2^126, below
 // the second the products hold, but each E must be looked at.
 constexpr float kSurely = 0x1p78f, kPerhaps = 0x1p120f, kLargestGate = 83.f;  // e^83 < 2^120
+// At the other end N, M >= 2^-48 of X, Y.  Below the first of these they may lose 2^-149
+// a token, 2^-98 of X and Y: a run's inputs above the second are 2^24 times that.
+constexpr float kSmall = 0x1p-78f, kSmallInput = 0x1p-74f;
 
 // A token with E: h -> a h + z x
 template <int NG>

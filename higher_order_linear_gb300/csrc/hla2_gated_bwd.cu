@@ -12,8 +12,8 @@
 // need no rounding to 16 bits, and reading x costs what reading h would.
 //
 // What bounds it.  4 x 16 x 4096 x 64, 16 bits (168 MB, 25 us at the copy
-// bandwidth): 58 us; with the forward (100 MB, 15 us) of 35 us a training pass
-// takes 93 us (129 with sigmoid_gate() throughout).  A tile is on chip for about 7 us
+// bandwidth): 60 us; with the forward (100 MB, 15 us) of 36 us a training pass
+// takes 94 us (129 with sigmoid_gate() throughout).  A tile is on chip for about 7 us
 // (loads 0.8, mapping 1.0, waiting for tiles of other blocks 2.6, writing 1.7) and
 // shared memory holds three, so one leaves every 2.5 to 2.9 us against 1.8 us for its
 // bytes; a launch of 13 tiles to an SM also pays for the filling and emptying of that
@@ -405,7 +405,6 @@ gated_pipe_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
             for (int i2 = 0; i2 < kTok; ++i2)
                 if (i2 < nt) gl[i2] = to_f32(gp[i2 * p.sg[2]]);
         }
-        // e^g where by_power, else a gate as next_state() takes it
         auto gates_of = [&](int i2, float (&ga)[NG]) {
             if constexpr (SHARED) ga[0] = ga[1] = gl[i2];
             else four(gs + i2 * p.d, ga);
@@ -463,25 +462,29 @@ gated_pipe_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
                         w.token(E, X, xv);
                         w.back_token(E, Y, uv, clean || open);
                     }
-                bool in = true, surely = true;
+                float d = 0.f, top = 0.f, low = INFINITY, any = 0.f;
+                span(w.D, d, any);
+                span(X, top, low);
+                span(Y, top, low);
+                bool in = d < kPerhaps && top < INFINITY;
+                if (in && !(d < kSurely && low >= kSmall)) {  // looked at closer
+                    float gate = 0.f, x = 0.f, u = 0.f;
+#pragma unroll 1
+                    for (int i2 = 0; i2 < nt; ++i2) {
+                        float xv[kCh], ga[NG];
+                        four(xs + i2 * p.d, xv);
+                        span(xv, x, any);
+                        four(us + i2 * p.d, xv);
+                        span(xv, u, any);
+                        if constexpr (SHARED) ga[0] = ga[1] = to_f32(gp[i2 * p.sg[2]]);
+                        else four(gs + i2 * p.d, ga);
 #pragma unroll
-                for (int j = 0; j < kCh; ++j) {
-                    const float per = w.close(j % NG, A[j]);
-                    surely = surely && w.D[j % NG] < kSurely;
-                    in = in && w.D[j % NG] < kPerhaps && fabsf(X[j]) < INFINITY && fabsf(Y[j]) < INFINITY;
-                    X[j] *= per;
-                    Y[j] *= per;
+                        for (int j = 0; j < NG; ++j) gate = fmaxf(gate, ga[j]);
+                    }
+                    in = gate < kLargestGate && (x == 0.f || x >= kSmallInput) && (u == 0.f || u >= kSmallInput);
                 }
-                if (in && !surely) {
-#pragma unroll(SHARED ? kTok : 1)
-                    for (int i2 = 0; i2 < kTok; ++i2)
-                        if (i2 < nt) {
-                            float ga[NG];
-                            gates_of(i2, ga);
-#pragma unroll
-                            for (int j = 0; j < NG; ++j) in = in && ga[j] < kLargestGate;
-                        }
-                }
+                w.close(X, A);
+                w.close_back(Y);
                 return in;
             };
             using yes = std::true_type;

@@ -513,6 +513,35 @@ def test_runs_beyond_the_range_of_products(dtype, d, shared):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d", [(torch.float32, 64), (torch.float32, 33), (torch.bfloat16, 64), (torch.bfloat16, 128)])
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("level", [-6.0, -2.0, 2.0, 9.0])
+def test_inputs_of_any_size(dtype, d, shared, level):
+    """The recurrence is linear in x, and its gradient in dO: inputs times a power of two give results times that, to
+    the bounds of ordinary ones, beside runs of zeros and ordinary inputs too."""
+    B, H, T = 1, 4, 600
+    g = torch.Generator().manual_seed(107)
+    gate = (level + 1.5 * torch.randn((B, H, T) if shared else (B, H, T, d), generator=g)).to(dtype)
+    x = torch.randn(B, H, T, d, generator=g).to(dtype)
+    do = torch.randn(B, H, T, d, generator=g).to(dtype)
+    x[:, :, 200:290], do[:, :, 250:340] = 0, 0
+    gc = gate.cuda()
+    ref = forward64(x, gate, "sigmoid")
+    rx, rg, _ = backward64(x, gate, do, "sigmoid")
+    if shared:
+        rg, den = rg.sum(-1), rg.abs().sum(-1).max()
+    for by in (1.0, 2.0 ** -60, 2.0 ** -80, 2.0 ** -100, 2.0 ** 100):
+        xs, ds = (x.float() * by).to(dtype).cuda(), (do.float() * by).to(dtype).cuda()
+        carry = torch.empty(B, H, hla2.hla2_gated_scan_carry_len(T, d), device="cuda")
+        assert rel(hla2.hla2_gated_scan(xs, gc, carry=carry).double() / by, ref) < F32
+        hla2.hla2_gated_scan(x.cuda(), gc, carry=carry)
+        dx, dg = hla2.hla2_gated_scan_backward(x.cuda(), gc, ds, carry)
+        scale = lambda t: (t.double() / by).to(dtype)  # exact: a power of two
+        assert rel(scale(dx), rx) < F32
+        assert (rel(scale(dg), rg, den) if shared else rel(scale(dg), rg)) < F32
+
+
+@pytest.mark.gpu
 def test_graph_replays_on_new_values():
     """A graph of the scan, its gradient and the step, replayed on inputs changed in place, with the workspaces as the
     replay before left them (tickets and maps of other inputs)."""
