@@ -99,10 +99,11 @@ __device__ __forceinline__ void back_token(float gate, float lam, float before, 
 // own size and not to A's.  For the gradient Y = M / D, M -> (1 + E) M + P dh.
 // Every token's E and 1 are scaled by 2^-6: D then holds for gates of 14 at every token
 // of a run, and an A below 2^-78 loses bits.  A run of larger gates, with inf or NaN, or
-// of inputs all below 2^-74 is walked with sigmoid_gate() instead.  Scan of 65536 x 16 x 128 with gates of
-// 2 +- 1.5: 184 us, 9: 188, 12: 212, 14: 345 (unscaled, 9: 510).  Per element and token
-// this takes 7.5 operations in the map and 7 in the walk that writes; sigmoid_gate() and
-// its selections took 12 and 10, which made that scan 240 us.
+// of inputs all below 2^-74 is walked with sigmoid_gate() instead.  Scan of
+// 65536 x 16 x 128 with gates of 2 +- 1.5: 184 us, 9: 186, 12: 208, 14: 348 (unscaled,
+// 9: 510).  Per element and token this takes 7.5 operations in the map and 7 in the walk
+// that writes; sigmoid_gate() and its selections took 12 and 10, which made that scan
+// 240 us.
 // Two elements to an instruction (f32x2) halve that again.
 template <int N, typename F>
 __device__ __forceinline__ void by_pairs(float (&o)[N], const float (&a)[N], const float (&b)[N], const float (&c)[N], F&& f) {
