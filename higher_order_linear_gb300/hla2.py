@@ -113,6 +113,14 @@ def lib() -> ctypes.CDLL:
             L.hla2_gated_scan_backward.restype = i
             L.hla2_gated_step.argtypes = [vp, vp, vp, vp, vp, i, i, pll, i, i, i, i, vp]
             L.hla2_gated_step.restype = i
+            L.hla2_linear_workspace.argtypes = [i, i, i, i, i]
+            L.hla2_linear_workspace.restype = sz
+            L.hla2_linear_forward.argtypes = [vp] * 8 + [i, i, i, i, i, pll, i, vp, sz, vp]
+            L.hla2_linear_forward.restype = i
+            L.hla2_linear_backward.argtypes = [vp] * 12 + [i, i, i, i, i, pll, i, vp, sz, vp]
+            L.hla2_linear_backward.restype = i
+            L.hla2_linear_step.argtypes = [vp] * 7 + [i, i, i, i, pll, i, vp]
+            L.hla2_linear_step.restype = i
             L.hla2_rmsnorm.argtypes = [vp, vp, vp, vp, vp, ll, i, ll, ll, ll, ll, f, i, i, i, vp]
             L.hla2_rmsnorm.restype = i
             L.hla2_rmsnorm_q8.argtypes = [vp, vp, vp, vp, vp, vp, ll, i, ll, ll, ll, ll, f, i, i, vp]
@@ -808,6 +816,163 @@ def hla2_gated_step(state: torch.Tensor, x: torch.Tensor, g: torch.Tensor, o: to
                                _raw(dev, stream))
     if rc:
         _check(rc, "hla2_gated_step")
+    return o
+
+
+def hla2_linear_workspace(B: int, H: int, T: int, d: int, dv: int) -> int:
+    return int(lib().hla2_linear_workspace(B, H, T, d, dv))
+
+
+def _linear_inputs(Q, K, V, gamma, lengths, workspace, **states):
+    """Checks shared by the linear attention's forward and backward; returns (B, H, T, d, dv, dtype code)."""
+    for name, t in (("Q", Q), ("K", K), ("V", V)):
+        _operand(t, name, None if t is Q else Q.device)
+        if t.dim() != 4:
+            raise ValueError("expected Q, K [B,H,T,d] and V [B,H,T,dv]")
+        _last_dense(t, name)
+    if K.shape != Q.shape or V.shape[:3] != Q.shape[:3]:
+        raise ValueError("expected Q, K [B,H,T,d] and V [B,H,T,dv]")
+    if not (Q.dtype == K.dtype == V.dtype):
+        raise ValueError(f"Q, K, V must share a dtype (got {Q.dtype}, {K.dtype}, {V.dtype})")
+    code = _dtype_code(Q)
+    B, H, T, d = Q.shape
+    dv, dev = V.shape[-1], Q.device
+    _operand(gamma, "gamma", dev, _F32, (H,), dense=True)
+    if lengths is not None:
+        _operand(lengths, "lengths", dev, torch.int32, (B,), dense=True)
+    for name, t in states.items():
+        if t is not None:
+            _operand(t, name, dev, _F32, (B, H, d, dv), dense=True)
+    if workspace is not None:
+        _operand(workspace, "workspace", dev, dense=True)
+    return B, H, T, d, dv, code
+
+
+def _linear_work(L, workspace, B, H, T, d, dv, dev):
+    if workspace is not None:
+        return workspace, workspace.numel() * workspace.element_size()
+    need = L.hla2_linear_workspace(B, H, T, d, dv)
+    return (torch.empty(need, device=dev, dtype=torch.uint8) if need else None), need
+
+
+def hla2_linear_forward(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, gamma: torch.Tensor,
+                        O: torch.Tensor | None = None, lengths: torch.Tensor | None = None,
+                        state_in: torch.Tensor | None = None, state_out: torch.Tensor | None = None,
+                        workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """First-order linear attention with a decay for each head,
+    S_t = gamma_h S_{t-1} + k_t v_t^T, o_t = S_t^T q_t: Q, K [B,H,T,d], V
+    [B,H,T,dv] fp32 or bf16 (the last dimension contiguous), gamma [H] fp32 in
+    [0, 1] -> O [B,H,T,dv] of the inputs' dtype, in V's memory order when it is
+    not given.
+
+    ``lengths`` [B] int32: the tokens of each sequence; what stands behind them is
+    not used and O is left as it was there.
+    ``state_in`` / ``state_out`` [B,H,d,dv] fp32: S before and after (one tensor may be both);
+    decoding goes on with hla2_linear_step."""
+    B, H, T, d, dv, code = _linear_inputs(Q, K, V, gamma, lengths, workspace, state_in=state_in, state_out=state_out)
+    dev = _cuda_device(Q, "Q")
+    if O is not None:
+        _output(O, "O", dev, Q.dtype, V.shape)
+    L = _lib or lib()
+    with _guard(dev, stream):
+        if O is None:
+            O = _like(V)
+        workspace, nws = _linear_work(L, workspace, B, H, T, d, dv, dev)
+        rc = L.hla2_linear_forward(Q.data_ptr(), K.data_ptr(), V.data_ptr(), gamma.data_ptr(), _ptr(lengths),
+                                   _ptr(state_in), O.data_ptr(), _ptr(state_out), B, H, T, d, dv,
+                                   _longs(*Q.stride()[:3], *K.stride()[:3], *V.stride()[:3], *O.stride()[:3]), code,
+                                   _ptr(workspace), nws, _raw(dev, stream))
+    if rc:
+        _check(rc, "hla2_linear_forward")
+    return O
+
+
+def hla2_linear_backward(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, gamma: torch.Tensor, dO: torch.Tensor,
+                         dQ: torch.Tensor | None = None, dK: torch.Tensor | None = None,
+                         dV: torch.Tensor | None = None, lengths: torch.Tensor | None = None,
+                         state_in: torch.Tensor | None = None, dstate_out: torch.Tensor | None = None,
+                         dstate_in: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """Gradients (dQ, dK, dV) of hla2_linear_forward over the same Q, K, V, gamma,
+    ``lengths`` and ``state_in``.  dO [B,H,T,dv] is the gradient of O,
+    ``dstate_out`` that of state_out; ``dstate_in`` [B,H,d,dv] fp32 receives that of
+    state_in (it may be dstate_out).  Behind a sequence's end the gradients are zero.
+    gamma is not differentiated."""
+    B, H, T, d, dv, code = _linear_inputs(Q, K, V, gamma, lengths, workspace, state_in=state_in,
+                                          dstate_out=dstate_out, dstate_in=dstate_in)
+    dev = _cuda_device(Q, "Q")
+    _operand(dO, "dO", dev, Q.dtype, V.shape)
+    _last_dense(dO, "dO")
+    for name, t, like in (("dQ", dQ, Q), ("dK", dK, K), ("dV", dV, V)):
+        if t is not None:
+            _output(t, name, dev, Q.dtype, like.shape)
+    L = _lib or lib()
+    with _guard(dev, stream):
+        dQ = _like(Q) if dQ is None else dQ
+        dK = _like(K) if dK is None else dK
+        dV = _like(V) if dV is None else dV
+        workspace, nws = _linear_work(L, workspace, B, H, T, d, dv, dev)
+        rc = L.hla2_linear_backward(Q.data_ptr(), K.data_ptr(), V.data_ptr(), gamma.data_ptr(), _ptr(lengths),
+                                    _ptr(state_in), dO.data_ptr(), _ptr(dstate_out), dQ.data_ptr(), dK.data_ptr(),
+                                    dV.data_ptr(), _ptr(dstate_in), B, H, T, d, dv,
+                                    _longs(*(st for t in (Q, K, V, dO, dQ, dK, dV) for st in t.stride()[:3])), code,
+                                    _ptr(workspace), nws, _raw(dev, stream))
+    if rc:
+        _check(rc, "hla2_linear_backward")
+    return dQ, dK, dV
+
+
+def _linear_step_checks(state, q, k, v, gamma, o, state_out):
+    _operand(q, "q")
+    if q.dim() != 2:
+        raise ValueError("hla2_linear_step: expected q, k [n,d] and v [n,dv]")
+    dev = q.device
+    _operand(k, "k", dev, q.dtype, q.shape)
+    _operand(v, "v", dev, q.dtype)
+    if v.dim() != 2 or v.shape[0] != q.shape[0]:
+        raise ValueError("hla2_linear_step: expected q, k [n,d] and v [n,dv]")
+    _dtype_code(q)
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _last_dense(t, name)
+    shape = (*q.shape, v.shape[1])
+    _operand(state, "state", dev, _F32, shape, dense=True)
+    if state_out is not None:
+        _operand(state_out, "state_out", dev, _F32, shape, dense=True)
+    _operand(gamma, "gamma", dev, _F32, dense=True)
+    if gamma.dim() != 1 or not gamma.numel() or q.shape[0] % gamma.numel():
+        raise ValueError("gamma must be [H] with the number of heads n a multiple of H")
+    if o is not None:
+        _output(o, "o", dev, q.dtype, v.shape)
+    _cuda_device(q, "q")
+
+
+def hla2_linear_step(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gamma: torch.Tensor,
+                     o: torch.Tensor | None = None, state_out: torch.Tensor | None = None,
+                     stream=None) -> torch.Tensor:
+    """One token of the linear attention for n heads: state [n,d,dv] fp32, q, k
+    [n,d], v [n,dv] (fp32 or bf16), gamma [H] with n a multiple of H (head i decays
+    by gamma[i % H]) -> o [n,dv] of the inputs' dtype.  The state is updated in
+    place, or left and the new one written to ``state_out``."""
+    shape, dt, dev = q.shape, q.dtype, q.device
+    if not (q.is_cuda and q.is_contiguous() and len(shape) == 2 and dt in _CODES and o is None and
+            k.shape == shape and k.dtype is dt and k.device == dev and k.is_contiguous() and
+            v.dtype is dt and v.device == dev and v.is_contiguous() and len(v.shape) == 2 and
+            v.shape[0] == shape[0] and state.shape == (*shape, v.shape[1]) and state.dtype is _F32 and
+            state.device == dev and state.is_contiguous() and gamma.dtype is _F32 and gamma.device == dev and
+            gamma.dim() == 1 and gamma.is_contiguous() and gamma.shape[0] and not shape[0] % gamma.shape[0] and
+            (state_out is None or (state_out.shape == state.shape and state_out.dtype is _F32 and
+                                   state_out.device == dev and state_out.is_contiguous()))):
+        _linear_step_checks(state, q, k, v, gamma, o, state_out)
+    n, d = shape
+    L = _lib or lib()
+    with _guard(dev, stream):
+        if o is None:
+            o = torch.empty(v.shape, device=dev, dtype=dt)
+        rc = L.hla2_linear_step(state.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), gamma.data_ptr(),
+                                o.data_ptr(), None if state_out is None else state_out.data_ptr(), n, gamma.shape[0],
+                                d, v.shape[1], _longs(q.stride(0), k.stride(0), v.stride(0), o.stride(0)), _CODES[dt],
+                                _raw(dev, stream))
+    if rc:
+        _check(rc, "hla2_linear_step")
     return o
 
 

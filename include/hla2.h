@@ -431,6 +431,69 @@ HLA2_API int hla2_gated_step(float* state, const void* x, const void* g, void* o
                              hla2_stream_t stream);
 
 /*
+ * First-order linear attention with a decay for each head:
+ *   S_t = g_h S_{t-1} + k_t v_t^T,   o_t = S_t^T q_t
+ *       = sum_{j<=t} g_h^(t-j) (q_t.k_j) v_j + g_h^(t+1) state_in^T q_t.
+ *   Q, K [B][H][T][d], V, O [B][H][T][dv], dtype, 1 <= d, dv <= 128.
+ *   gamma      [H] fp32 on the device, each in [0, 1] (0: only the token itself;
+ *              1: none).  It is not differentiated.
+ *   lengths    optional [B] int32 on the device: sequence b has lengths[b] tokens
+ *              (taken into 0..T).  What stands behind them in Q, K, V is not used,
+ *              whatever it is, and O is left as it was there.
+ *   state_in, state_out  optional [B][H][d][dv] fp32: S before the first and after
+ *              the last token; they may be one tensor, but not overlap otherwise.
+ *   strides    NULL, or twelve values: Q, K, V, O (b, h, t each), in elements; a
+ *              head's channels are contiguous.  O may not be one of the inputs.
+ *   workspace  hla2_linear_workspace(...) bytes, 16-byte aligned, not initialised;
+ *              NULL when that is 0.  It serves one call at a time.
+ * fp32 inputs are computed in fp32.  bf16 inputs of 16-byte steps (widths, strides
+ * and pointers) run on the tensor cores: there the scores within a block of 128
+ * tokens and the state that enters the block are rounded to bf16 where they are
+ * multiplied; the state itself is kept in fp32.  An infinity or NaN in a token's k
+ * or v reaches all outputs of its block of 128 tokens, the earlier ones too, and
+ * those behind.  Sums are joined in a fixed order: the same call gives the same bits.
+ * Errors: HLA2_ERR_INVALID, HLA2_ERR_UNSUPPORTED (d or dv > 128, B*H > 65535,
+ * type), HLA2_ERR_WORKSPACE, HLA2_ERR_LAUNCH.
+ */
+HLA2_API size_t hla2_linear_workspace(int B, int H, int T, int d, int dv);
+HLA2_API int hla2_linear_forward(const void* Q, const void* K, const void* V, const float* gamma, const int* lengths,
+                                 const float* state_in, void* O, float* state_out, int B, int H, int T, int d, int dv,
+                                 const long long* strides, int dtype, void* workspace, size_t ws_bytes,
+                                 hla2_stream_t stream);
+
+/*
+ * Gradients of hla2_linear_forward.  With G_t the gradient of S_t,
+ * G_t = q_t dO_t^T + g G_{t+1}, dstate_out added at the last token:
+ *   dQ_t = S_t dO_t,   dK_t = G_t v_t,   dV_t = G_t^T k_t,   dstate_in = g G_0.
+ *   dO, dV [B][H][T][dv], dQ, dK [B][H][T][d], dtype.
+ *   state_in    as for the forward;  dstate_out, dstate_in  optional
+ *               [B][H][d][dv] fp32.  dstate_in may be dstate_out or state_in, but not
+ *               overlap them otherwise.
+ *   lengths     as for the forward; dQ, dK and dV are zero behind a sequence's end.
+ *   strides     NULL, or twenty-one values: Q, K, V, dO, dQ, dK, dV (b, h, t each).
+ * No output may be an input or another output.  Workspace and errors as for the forward.
+ */
+HLA2_API int hla2_linear_backward(const void* Q, const void* K, const void* V, const float* gamma, const int* lengths,
+                                  const float* state_in, const void* dO, const float* dstate_out, void* dQ, void* dK,
+                                  void* dV, float* dstate_in, int B, int H, int T, int d, int dv,
+                                  const long long* strides, int dtype, void* workspace, size_t ws_bytes,
+                                  hla2_stream_t stream);
+
+/*
+ * One token for n heads: S = g S + k v^T, o = S^T q.
+ *   state [n][d][dv] fp32;  q, k [n][d], v, o [n][dv], dtype;  gamma [H], n a
+ *   multiple of H: head i decays by gamma[i % H].
+ *   state_out [n][d][dv] fp32, or NULL to update in place; it may be state, but not
+ *   overlap it otherwise.
+ *   ld: row strides of q, k, v and o, or NULL for dense; the states are dense.
+ * Errors: HLA2_ERR_INVALID, HLA2_ERR_UNSUPPORTED (d or dv > 128, n > 65535, type),
+ * HLA2_ERR_LAUNCH.
+ */
+HLA2_API int hla2_linear_step(float* state, const void* q, const void* k, const void* v, const float* gamma, void* o,
+                              float* state_out, int n, int H, int d, int dv, const long long* ld, int dtype,
+                              hla2_stream_t stream);
+
+/*
  * Root-mean-square norm of rows, with the residual's addition:
  *   t = X + R,   Y = t / sqrt(mean(t^2) + eps) * W.
  *   X, R  [rows][C] dtype (R optional);   W  [C], wdtype (NULL: ones);
