@@ -1,0 +1,707 @@
+// hla2_gnorm.cu -- group norm, channels last, with an activation or a gate, and
+// its gradient.
+//
+//   x [N][L][C], G groups of cg = C / G channels; mean and variance over a
+//   sample's L positions and a group's channels:
+//   n = (x - mean) / sqrt(var + eps),  z = n w + b,
+//   y = act(z), or z act(gate);  act: identity or silu.
+// Gradient, with dz = dy act'(z) (or dy act(gate)) and t = dz w:
+//   dx = rstd (t - mean(t) - n mean(t n)),  dw = sum dz n,  db = sum dz,
+//   dgate = dy z act'(gate).
+//
+// Two forms.  A unit (a sample's group, L cg values) of up to 2048 values stays
+// in the registers of up to 256 threads, eight values each: x crosses HBM once, the
+// variance is taken about the mean.  Larger units are summed by channel over
+// runs of positions (moments about the run's first position, so that a large mean
+// costs nothing), folded in a second launch and read again by a third.
+#include "hla2_layer.cuh"
+
+namespace hla2 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kUnit = kThreads * 8;  // the most values of a unit in registers
+constexpr int kMaxChannels = 16384;
+constexpr int kFwdBlocks = 4, kBwdBlocks = 2;  // blocks of units in registers that an SM holds
+
+struct View {
+    const void* p;
+    long long sn, sl;  // strides of samples and positions
+};
+
+struct GNormParams {
+    View x, z, dy;  // input, gate (p null: none), gradient of the output
+    void *y, *dz;   // output (dx in the gradient), gradient of the gate
+    long long yn, yl, dzn, dzl;
+    const void *w, *b;  // [C], wdtype, or null
+    float* stats;       // [N][G][2]: mean and reciprocal deviation
+    float* part;        // gradient and large units: partial sums
+    float* dw;          // [2][C] in the gradient: dw, then db
+    long long N;
+    int L, C, G, cg, wdtype;
+    bool silu;
+    float eps;
+    // units in registers: threads to a unit, units of one sample to a block, samples to a block
+    int tpr, gpb, spb;
+    // large units: runs of `run` positions, `runs` of them
+    int run, runs;
+};
+
+__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+// the activation and its slope
+__device__ __forceinline__ float act(float x, bool silu) { return silu ? x * sigmoid(x) : x; }
+__device__ __forceinline__ void act_slope(float x, bool silu, float& v, float& s) {
+    if (silu) {
+        const float g = sigmoid(x);
+        v = x * g;
+        s = fmaf(v, 1.f - g, g);
+    } else {
+        v = x;
+        s = 1.f;
+    }
+}
+__device__ __forceinline__ float weight_at(const void* w, int wdtype, int c, float none) {
+    if (!w) return none;
+    return wdtype == HLA2_DTYPE_F32 ? __ldg(static_cast<const float*>(w) + c)
+                                    : __bfloat162float(static_cast<const bf16*>(w)[c]);
+}
+// eight channels in a row, from a 16-byte step on
+__device__ __forceinline__ void weights8(const void* w, int wdtype, int c, float none, float (&v)[8]) {
+    if (!w) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = none;
+    } else if (wdtype == HLA2_DTYPE_F32) {
+        const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(w) + c);
+        const float4 a = __ldg(q), b = __ldg(q + 1);
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    } else {
+        const uint4 a = __ldg(reinterpret_cast<const uint4*>(static_cast<const bf16*>(w) + c));
+        const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[2 * j] = __uint_as_float(u[j] << 16);
+            v[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
+        }
+    }
+}
+
+// Where the eight values of a thread are: VEC, eight channels in a row of one
+// position; else every tpr-th value of the unit.
+template <bool VEC>
+struct Spots {
+    int pos[VEC ? 1 : 8], ch[VEC ? 1 : 8], n;
+    __device__ __forceinline__ Spots(int lane, int tpr, int values, int cg) {
+        n = 0;
+        if (VEC) {
+            const int e = lane * 8;
+            pos[0] = e / cg;
+            ch[0] = e - pos[0] * cg;
+            n = e < values ? 8 : 0;
+        } else {
+#pragma unroll
+            for (int j = 0; j < (VEC ? 1 : 8); ++j) {
+                const int e = lane + j * tpr;
+                pos[j] = e / cg;
+                ch[j] = e - pos[j] * cg;
+                n += e < values;
+            }
+        }
+    }
+    __device__ __forceinline__ int channel(int j) const { return VEC ? ch[0] + j : ch[VEC ? 0 : j]; }
+    __device__ __forceinline__ void weights(const void* w, int wdtype, int c0, float none, float (&v)[8]) const {
+        if constexpr (VEC) {
+            if (n) weights8(w, wdtype, c0 + ch[0], none, v);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = j < n ? weight_at(w, wdtype, c0 + ch[j], none) : 0.f;
+        }
+    }
+    // eight values as they lie in memory
+    template <typename T>
+    struct Raw {
+        Lane<T, 8, VEC> l;
+        __device__ __forceinline__ float get(int j) const { return l.get(j); }
+    };
+    template <typename T>
+    __device__ __forceinline__ void load(const T* p, long long sl, Raw<T>& r) const {
+        if constexpr (VEC) {
+            if (n) r.l.load(p + pos[0] * sl + ch[0], 8);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j < n) r.l.v[j] = p[pos[j] * sl + ch[j]];
+        }
+    }
+    template <typename T>
+    __device__ __forceinline__ void store(T* p, long long sl, const float (&v)[8]) const {
+        if constexpr (VEC) {
+            Lane<T, 8, true> l;
+            l.set(v);
+            if (n) l.store(p + pos[0] * sl + ch[0], 8);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j < n) p[pos[j] * sl + ch[j]] = from_f32<T>(v[j]);
+        }
+    }
+};
+
+// Sums over a unit's threads; sh: two rows of kThreads / 32, used alternately.
+__device__ __forceinline__ void unit_sum(float& a, float& b, int tpr, float2* sh) {
+    for (int o = min(tpr, 32) >> 1; o > 0; o >>= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+        b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
+    if (tpr > 32) {
+        const int warp = threadIdx.x >> 5, nw = tpr >> 5, w0 = warp / nw * nw;
+        if ((threadIdx.x & 31) == 0) sh[warp] = make_float2(a, b);
+        __syncthreads();
+        a = b = 0.f;
+        for (int i = 0; i < nw; ++i) {
+            a += sh[w0 + i].x;
+            b += sh[w0 + i].y;
+        }
+    }
+}
+
+// --------------------------------------------- units in registers ----
+// A block keeps its groups and takes every gridDim.x-th run of samples: its
+// weights stay in registers, and the next samples' values are on their way.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kThreads, VEC ? kFwdBlocks : 2) gnorm_unit_kernel(const GNormParams p) {
+    __shared__ float2 sh[2][kThreads / 32];
+    const int unit = threadIdx.x / p.tpr, lane = threadIdx.x % p.tpr;
+    const int s = unit / p.gpb, g = blockIdx.y * p.gpb + unit % p.gpb;
+    const int values = p.L * p.cg, c0 = g * p.cg;
+    const bool mine = s < p.spb && g < p.G;
+    const Spots<VEC> at(lane, p.tpr, mine ? values : 0, p.cg);
+    const float inv = 1.f / (float)values;
+    typename Spots<VEC>::template Raw<T> xr, zr;
+    auto fetch = [&](long long n) {
+        if (n >= p.N) return;
+        at.load(static_cast<const T*>(p.x.p) + n * p.x.sn + c0, p.x.sl, xr);
+        if (p.z.p) at.load(static_cast<const T*>(p.z.p) + n * p.z.sn + c0, p.z.sl, zr);
+    };
+    long long n = (long long)blockIdx.x * p.spb + s;
+    const long long step = (long long)gridDim.x * p.spb;
+    fetch(n);
+    float w[8], b[8];
+    at.weights(p.w, p.wdtype, c0, 1.f, w);
+    at.weights(p.b, p.wdtype, c0, 0.f, b);
+    for (long long n0 = (long long)blockIdx.x * p.spb; n0 < p.N; n0 += step, n += step) {
+        float x[8], z[8], sum = 0.f, none = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < at.n) {
+                x[j] = xr.get(j);
+                z[j] = p.z.p ? zr.get(j) : 0.f;
+                if (n < p.N) sum += x[j];
+            }
+        fetch(n + step);
+        unit_sum(sum, none, p.tpr, sh[0]);
+        const float mean = sum * inv;
+        float sq = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < at.n) {
+                x[j] -= mean;
+                sq = fmaf(x[j], x[j], sq);
+            }
+        unit_sum(sq, none, p.tpr, sh[1]);
+        if (!mine || n >= p.N) continue;
+        const float rstd = 1.f / sqrtf(fmaf(sq, inv, p.eps));
+        if (p.stats && lane == 0) *reinterpret_cast<float2*>(p.stats + (n * p.G + g) * 2) = make_float2(mean, rstd);
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < at.n) {
+                const float v = fmaf(x[j] * rstd, w[j], b[j]);
+                y[j] = p.z.p ? v * act(z[j], p.silu) : act(v, p.silu);
+            }
+        at.store(static_cast<T*>(p.y) + n * p.yn + c0, p.yl, y);
+    }
+}
+
+// The gradient.  A block keeps its groups and takes every gridDim.x-th run of
+// samples, so that a thread's channels stay its own and dw and db add up in
+// registers; then the block's threads add theirs, one line of sums to a block.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kThreads, VEC ? kBwdBlocks : 1) gnorm_unit_bwd_kernel(const GNormParams p) {
+    __shared__ float2 sh[2][kThreads / 32];
+    extern __shared__ float2 sums[];  // [unit of the block][value]
+    const int unit = threadIdx.x / p.tpr, lane = threadIdx.x % p.tpr;
+    const int s = unit / p.gpb, g = blockIdx.y * p.gpb + unit % p.gpb;
+    const int values = p.L * p.cg, c0 = g * p.cg;
+    const bool mine = s < p.spb && g < p.G;
+    const Spots<VEC> at(lane, p.tpr, mine ? values : 0, p.cg);
+    const float inv = 1.f / (float)values;
+    typename Spots<VEC>::template Raw<T> xr, yr, zr;
+    float2 sr = make_float2(0.f, 0.f);
+    auto fetch = [&](long long n) {
+        if (!mine || n >= p.N) return;
+        at.load(static_cast<const T*>(p.x.p) + n * p.x.sn + c0, p.x.sl, xr);
+        at.load(static_cast<const T*>(p.dy.p) + n * p.dy.sn + c0, p.dy.sl, yr);
+        if (p.z.p) at.load(static_cast<const T*>(p.z.p) + n * p.z.sn + c0, p.z.sl, zr);
+        sr = __ldg(reinterpret_cast<const float2*>(p.stats + (n * p.G + g) * 2));
+    };
+    const long long step = (long long)gridDim.x * p.spb;
+    fetch((long long)blockIdx.x * p.spb + s);
+    float w[8], b[8], dw[8] = {}, db[8] = {};
+    at.weights(p.w, p.wdtype, c0, 1.f, w);
+    at.weights(p.b, p.wdtype, c0, 0.f, b);
+    int turn = 0;
+    for (long long n0 = (long long)blockIdx.x * p.spb; n0 < p.N; n0 += step, turn ^= 1) {
+        const long long n = n0 + s;
+        const bool live = mine && n < p.N;
+        float x[8], dy[8], z[8], dgate[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (live && j < at.n) {
+                x[j] = xr.get(j);
+                dy[j] = yr.get(j);
+                z[j] = p.z.p ? zr.get(j) : 0.f;
+            }
+        const float2 st = sr;
+        fetch(n + step);
+        float m1 = 0.f, m2 = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (live && j < at.n) {
+                x[j] = (x[j] - st.x) * st.y;
+                const float v = fmaf(x[j], w[j], b[j]);
+                float value, slope;
+                act_slope(p.z.p ? z[j] : v, p.silu, value, slope);
+                dgate[j] = dy[j] * v * slope;
+                const float d = dy[j] * (p.z.p ? value : slope);
+                db[j] += d;
+                dw[j] = fmaf(d, x[j], dw[j]);
+                dy[j] = d * w[j];
+                m1 += dy[j];
+                m2 = fmaf(dy[j], x[j], m2);
+            }
+        unit_sum(m1, m2, p.tpr, sh[turn]);
+        if (!live) continue;
+        m1 *= inv;
+        m2 *= inv;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < at.n) x[j] = st.y * (dy[j] - m1 - x[j] * m2);
+        at.store(static_cast<T*>(p.y) + n * p.yn + c0, p.yl, x);
+        if (p.z.p) at.store(static_cast<T*>(p.dz) + n * p.dzn + c0, p.dzl, dgate);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (j < at.n) sums[unit * values + at.pos[VEC ? 0 : j] * p.cg + at.channel(j)] = make_float2(dw[j], db[j]);
+    __syncthreads();
+    float* const line = p.part + (long long)blockIdx.x * 2 * p.C;
+    const int width = min(p.gpb, p.G - (int)blockIdx.y * p.gpb) * p.cg;
+    for (int c = threadIdx.x; c < width; c += kThreads) {
+        const int u = c / p.cg, ch = c - u * p.cg;
+        float a = 0.f, d = 0.f;
+        for (int i = 0; i < p.spb; ++i)
+            for (int l = 0; l < p.L; ++l) {
+                const float2 v = sums[(i * p.gpb + u) * values + l * p.cg + ch];
+                a += v.x;
+                d += v.y;
+            }
+        line[blockIdx.y * p.gpb * p.cg + c] = a;
+        line[p.C + blockIdx.y * p.gpb * p.cg + c] = d;
+    }
+}
+
+// ------------------------------------------------------ large units ----
+// A block takes one run of positions of one sample and up to 2048 channels, a
+// thread eight of them and every rows-th position.
+struct RunSpot {
+    long long n;
+    int l0, l1, c, cols, rows, row, live;
+};
+__device__ __forceinline__ RunSpot run_spot(const GNormParams& p) {
+    RunSpot r;
+    r.cols = min((p.C + 7) / 8, kThreads);  // threads along the channels
+    r.n = blockIdx.x / p.runs;
+    r.l0 = (int)(blockIdx.x % p.runs) * p.run;
+    r.l1 = min(r.l0 + p.run, p.L);
+    r.rows = kThreads / r.cols;
+    r.row = threadIdx.x / r.cols;
+    r.c = (blockIdx.y * kThreads + threadIdx.x % r.cols) * 8;
+    r.live = r.row < r.rows ? min(8, p.C - r.c) : 0;
+    return r;
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ void load8(const T* p, int n, float (&v)[8]) {
+    Lane<T, 8, VEC> l;
+    l.load(p, n);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = l.get(j);
+}
+// a block's rows added in order: two sums of each channel
+__device__ __forceinline__ bool add_rows(const RunSpot& r, float (&a)[8], float (&b)[8], float2 (*sh)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sh[threadIdx.x][j] = make_float2(a[j], b[j]);
+    __syncthreads();
+    if (r.row != 0 || r.live <= 0) return false;
+    for (int i = 1; i < r.rows; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float2 v = sh[threadIdx.x + i * r.cols][j];
+            a[j] += v.x;
+            b[j] += v.y;
+        }
+    return true;
+}
+
+// GRAD: sums of dz and dz n of each channel; else mean and sum of squares about it.
+template <typename T, bool VEC, bool GRAD>
+__global__ void __launch_bounds__(kThreads) gnorm_sums_kernel(const GNormParams p) {
+    __shared__ float2 sh[kThreads][8];
+    const RunSpot r = run_spot(p);
+    float a[8] = {}, q[8] = {}, pivot[8], w[8], b[8], mean[8], rstd[8];
+    if (r.live > 0) {
+        const T* x = static_cast<const T*>(p.x.p) + r.n * p.x.sn + r.c;
+        if (!GRAD) load8<T, VEC>(x + (long long)r.l0 * p.x.sl, r.live, pivot);
+        else
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int c = min(r.c + j, p.C - 1);
+                const float2 st = __ldg(reinterpret_cast<const float2*>(p.stats) + r.n * p.G + c / p.cg);
+                mean[j] = st.x;
+                rstd[j] = st.y;
+                w[j] = weight_at(p.w, p.wdtype, c, 1.f);
+                b[j] = weight_at(p.b, p.wdtype, c, 0.f);
+            }
+#pragma unroll 2
+        for (int l = r.l0 + r.row; l < r.l1; l += r.rows) {
+            float v[8];
+            load8<T, VEC>(x + l * p.x.sl, r.live, v);
+            if (!GRAD) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float d = v[j] - pivot[j];
+                    a[j] += d;
+                    q[j] = fmaf(d, d, q[j]);
+                }
+            } else {
+                float dy[8], z[8];
+                load8<T, VEC>(static_cast<const T*>(p.dy.p) + r.n * p.dy.sn + l * p.dy.sl + r.c, r.live, dy);
+                if (p.z.p) load8<T, VEC>(static_cast<const T*>(p.z.p) + r.n * p.z.sn + l * p.z.sl + r.c, r.live, z);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float n = (v[j] - mean[j]) * rstd[j];
+                    float value, slope;
+                    act_slope(p.z.p ? z[j] : fmaf(n, w[j], b[j]), p.silu, value, slope);
+                    const float d = dy[j] * (p.z.p ? value : slope);
+                    a[j] = fmaf(d, n, a[j]);
+                    q[j] += d;
+                }
+            }
+        }
+    }
+    if (!add_rows(r, a, q, sh)) return;
+    float* const line = p.part + (long long)blockIdx.x * 2 * p.C + r.c;
+    const float inv = 1.f / (float)(r.l1 - r.l0);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (j < r.live) {
+            line[j] = GRAD ? a[j] : fmaf(a[j], inv, pivot[j]);
+            line[p.C + j] = GRAD ? q[j] : fmaxf(q[j] - a[j] * a[j] * inv, 0.f);
+        }
+}
+
+__device__ __forceinline__ double block_sum(double v, double* sh) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) v += sh[i];
+    return v;
+}
+
+// A group's runs and channels folded: mean and reciprocal deviation, or (GRAD)
+// the means of t and t n, which go behind the partial sums.
+template <bool GRAD>
+__global__ void __launch_bounds__(kThreads) gnorm_fold_kernel(const GNormParams p, float* out) {
+    __shared__ double sh[kThreads / 32];
+    const long long n = blockIdx.x / p.G;
+    const int g = (int)(blockIdx.x % p.G), items = p.runs * p.cg;
+    const float* const part = p.part + n * p.runs * 2 * p.C + g * p.cg;
+    const double count = (double)p.L * p.cg;
+    double a = 0, q = 0;
+    for (int i = threadIdx.x; i < items; i += kThreads) {
+        const int k = i / p.cg, c = i - k * p.cg;
+        const float* v = part + (long long)k * 2 * p.C + c;
+        if (GRAD) {
+            const double w = weight_at(p.w, p.wdtype, g * p.cg + c, 1.f);
+            a += w * v[p.C];
+            q += w * v[0];
+        } else {
+            a += (double)min(p.run, p.L - k * p.run) * v[0];
+        }
+    }
+    a = block_sum(a, sh) / count;
+    if (!GRAD)
+        for (int i = threadIdx.x; i < items; i += kThreads) {
+            const int k = i / p.cg, c = i - k * p.cg;
+            const float* v = part + (long long)k * 2 * p.C + c;
+            const double d = v[0] - a;
+            q += v[p.C] + (double)min(p.run, p.L - k * p.run) * d * d;
+        }
+    q = block_sum(q, sh) / count;
+    if (threadIdx.x == 0)
+        *reinterpret_cast<float2*>(out + 2 * (long long)blockIdx.x) =
+            make_float2((float)a, GRAD ? (float)q : (float)(1.0 / sqrt(q + (double)p.eps)));
+}
+
+// y, or (GRAD) dx and dgate; means: the gradient's, [N][G][2]
+template <typename T, bool VEC, bool GRAD>
+__global__ void __launch_bounds__(kThreads) gnorm_apply_kernel(const GNormParams p, const float* means) {
+    const RunSpot r = run_spot(p);
+    if (r.live <= 0) return;
+    float w[8], b[8], mean[8], rstd[8], m1[8], m2[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int c = min(r.c + j, p.C - 1);
+        const float2 st = __ldg(reinterpret_cast<const float2*>(p.stats) + r.n * p.G + c / p.cg);
+        mean[j] = st.x;
+        rstd[j] = st.y;
+        w[j] = weight_at(p.w, p.wdtype, c, 1.f);
+        b[j] = weight_at(p.b, p.wdtype, c, 0.f);
+        if (GRAD) {
+            const float2 m = __ldg(reinterpret_cast<const float2*>(means) + r.n * p.G + c / p.cg);
+            m1[j] = m.x;
+            m2[j] = m.y;
+        }
+    }
+#pragma unroll 2
+    for (int l = r.l0 + r.row; l < r.l1; l += r.rows) {
+        float x[8], z[8], dy[8];
+        load8<T, VEC>(static_cast<const T*>(p.x.p) + r.n * p.x.sn + l * p.x.sl + r.c, r.live, x);
+        if (p.z.p) load8<T, VEC>(static_cast<const T*>(p.z.p) + r.n * p.z.sn + l * p.z.sl + r.c, r.live, z);
+        if (GRAD) load8<T, VEC>(static_cast<const T*>(p.dy.p) + r.n * p.dy.sn + l * p.dy.sl + r.c, r.live, dy);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float n = (x[j] - mean[j]) * rstd[j], v = fmaf(n, w[j], b[j]);
+            if (!GRAD) {
+                x[j] = p.z.p ? v * act(z[j], p.silu) : act(v, p.silu);
+            } else {
+                float value, slope;
+                act_slope(p.z.p ? z[j] : v, p.silu, value, slope);
+                const float t = dy[j] * (p.z.p ? value : slope) * w[j];
+                z[j] = dy[j] * v * slope;
+                x[j] = rstd[j] * (t - m1[j] - n * m2[j]);
+            }
+        }
+        Lane<T, 8, VEC> o;
+        o.set(x);
+        o.store(static_cast<T*>(p.y) + r.n * p.yn + l * p.yl + r.c, r.live);
+        if (GRAD && p.z.p) {
+            o.set(z);
+            o.store(static_cast<T*>(p.dz) + r.n * p.dzn + l * p.dzl + r.c, r.live);
+        }
+    }
+}
+
+// dw and db: the lines of partial sums added in a fixed order, 16 columns to a
+// block, each 64 threads' sums of every 64th line.
+constexpr int kFoldColumns = 16, kFoldThreads = 1024, kFoldLines = kFoldThreads / kFoldColumns;
+__global__ void __launch_bounds__(kFoldThreads) gnorm_lines_kernel(const float* __restrict__ part,
+                                                                   float* __restrict__ out, long long lines, int width) {
+    __shared__ float sh[kFoldThreads / 32][kFoldColumns];
+    const int col = threadIdx.x % kFoldColumns, line = threadIdx.x / kFoldColumns;
+    const int c = blockIdx.x * kFoldColumns + col;
+    float a = 0.f;
+    if (c < width) {
+#pragma unroll 8
+        for (long long g = line; g < lines; g += kFoldLines) a += part[g * width + c];
+    }
+    a += __shfl_down_sync(0xffffffffu, a, 16);
+    if ((threadIdx.x & 31) < kFoldColumns) sh[threadIdx.x >> 5][col] = a;
+    __syncthreads();
+    if (threadIdx.x < kFoldColumns && c < width) {
+        a = 0.f;
+#pragma unroll
+        for (int i = 0; i < kFoldThreads / 32; ++i) a += sh[i][col];
+        out[c] = a;
+    }
+}
+
+// ------------------------------------------------------------------ host ----
+struct GPlan {
+    bool unit;
+    int tpr, gpb, spb, blocks;  // units in registers; blocks along the samples in the gradient
+    int run, runs;
+    long long lines;     // of partial sums
+    size_t part, means;  // floats of partial sums; of the gradient's means behind them
+};
+
+GPlan gnorm_plan(long long N, int L, int C, int G, bool grad) {
+    GPlan g{};
+    const int cg = C / G;
+    g.unit = (long long)L * cg <= kUnit;
+    if (g.unit) {
+        g.tpr = 1;
+        while (g.tpr * 8 < L * cg) g.tpr *= 2;
+        const int units = kThreads / g.tpr;
+        g.gpb = G < units ? G : units;
+        g.spb = units / g.gpb;
+        const int across = (G + g.gpb - 1) / g.gpb;
+        const long long need = (N + g.spb - 1) / g.spb, most = ((long long)(grad ? kBwdBlocks : kFwdBlocks) * sm_count() + across - 1) / across;
+        g.blocks = (int)(need < most ? need : most);
+        g.lines = g.blocks;
+        g.part = grad ? (size_t)g.lines * 2 * C : 0;
+        return g;
+    }
+    const int across = (C + kUnit - 1) / kUnit;
+    // enough blocks to fill the SMs several times, runs of 16 positions or more
+    long long runs = (8LL * sm_count() + N * across - 1) / (N * across);
+    if (runs > (L + 15) / 16) runs = (L + 15) / 16;
+    if (runs < 1) runs = 1;
+    g.run = (int)((L + runs - 1) / runs);
+    g.runs = (L + g.run - 1) / g.run;
+    g.lines = N * g.runs;
+    g.part = (size_t)g.lines * 2 * C;
+    g.means = (size_t)N * G * 2;
+    return g;
+}
+
+int check_gnorm(const char* what, long long N, int L, int C, int G, float eps, int dtype, int wdtype, int act) {
+    if (N <= 0 || L <= 0 || C <= 0 || G <= 0 || C % G)
+        return set_error(HLA2_ERR_INVALID, "%s: sizes must be positive and C a multiple of G (N=%lld L=%d C=%d G=%d)", what, N, L, C, G);
+    if (C > kMaxChannels) return set_error(HLA2_ERR_UNSUPPORTED, "%s: C=%d exceeds %d", what, C, kMaxChannels);
+    if (N > 0x7fffffffLL || N * L > 0x7fffffffLL || N * G > 0x7fffffffLL)
+        return set_error(HLA2_ERR_UNSUPPORTED, "%s: N*L or N*G exceeds 2^31 - 1 (N=%lld L=%d G=%d)", what, N, L, G);
+    if (!known_dtype(dtype) || !known_dtype(wdtype)) return set_error(HLA2_ERR_UNSUPPORTED, "%s: unknown dtype", what);
+    if (act != HLA2_ACT_NONE && act != HLA2_ACT_SILU) return set_error(HLA2_ERR_UNSUPPORTED, "%s: unknown activation %d", what, act);
+    if (!(eps >= 0.f)) return set_error(HLA2_ERR_INVALID, "%s: eps must not be negative", what);
+    return HLA2_OK;
+}
+
+int check_gws(const char* what, size_t need, const void* ws, size_t bytes) {
+    if (need && (!ws || bytes < need)) return set_error(HLA2_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", what, bytes, need);
+    if (need && reinterpret_cast<uintptr_t>(ws) % 16) return set_error(HLA2_ERR_INVALID, "%s: workspace not 16-byte aligned", what);
+    return HLA2_OK;
+}
+size_t gnorm_bytes(const GPlan& g) { return ((g.part + g.means) * 4 + 255) & ~size_t(255); }
+
+// what the kernels take 16 bytes of at a time
+bool wide(const void* p, long long sn, long long sl, long long N, int L, int es) {
+    if (!p) return true;
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (N == 1 || sn * es % 16 == 0) && (L == 1 || sl * es % 16 == 0);
+}
+
+template <bool GRAD>
+cudaError_t run_gnorm(GNormParams p, const GPlan& g, int dtype, bool vec, cudaStream_t s) {
+    auto typed = [&](auto t, auto v) {
+        using T = decltype(t);
+        constexpr bool VEC = decltype(v)::value;
+        if (g.unit) {
+            const unsigned across = (p.G + g.gpb - 1) / g.gpb;
+            if (GRAD)
+                gnorm_unit_bwd_kernel<T, VEC><<<dim3(g.blocks, across), kThreads,
+                                                (size_t)g.spb * g.gpb * p.L * p.cg * sizeof(float2), s>>>(p);
+            else
+                gnorm_unit_kernel<T, VEC><<<dim3(g.blocks, across), kThreads, 0, s>>>(p);
+            note_launches(1);
+            return cudaGetLastError();
+        }
+        const dim3 grid((unsigned)(p.N * g.runs), (p.C + kUnit - 1) / kUnit);
+        float* const means = p.part + g.part;
+        float* const folded = GRAD || !p.stats ? means : p.stats;
+        gnorm_sums_kernel<T, VEC, GRAD><<<grid, kThreads, 0, s>>>(p);
+        gnorm_fold_kernel<GRAD><<<(unsigned)(p.N * p.G), kThreads, 0, s>>>(p, folded);
+        if (!GRAD) p.stats = folded;
+        gnorm_apply_kernel<T, VEC, GRAD><<<grid, kThreads, 0, s>>>(p, means);
+        note_launches(3);
+        return cudaGetLastError();
+    };
+    cudaError_t e;
+    if (dtype == HLA2_DTYPE_BF16) e = vec ? typed(bf16{}, std::true_type{}) : typed(bf16{}, std::false_type{});
+    else e = vec ? typed(float{}, std::true_type{}) : typed(float{}, std::false_type{});
+    if (GRAD && e == cudaSuccess && p.dw) {
+        gnorm_lines_kernel<<<(2 * p.C + kFoldColumns - 1) / kFoldColumns, kFoldThreads, 0, s>>>(p.part, p.dw, g.lines, 2 * p.C);
+        note_launches(1);
+        e = cudaGetLastError();
+    }
+    return e;
+}
+
+}  // namespace
+}  // namespace hla2
+
+extern "C" size_t hla2_groupnorm_workspace(long long N, int L, int C, int G, int backward) {
+    using namespace hla2;
+    if (check_gnorm("groupnorm_workspace", N, L, C, G, 0.f, HLA2_DTYPE_F32, HLA2_DTYPE_F32, HLA2_ACT_NONE)) return 0;
+    return gnorm_bytes(gnorm_plan(N, L, C, G, backward != 0));
+}
+
+extern "C" int hla2_groupnorm(const void* X, const void* W, const void* Bias, const void* gate, void* Y, float* stats,
+                              long long N, int L, int C, int G, const long long* strides, float eps, int act, int dtype,
+                              int wdtype, void* workspace, size_t ws_bytes, hla2_stream_t stream) {
+    using namespace hla2;
+    const char* what = "groupnorm";
+    if (int rc = check_gnorm(what, N, L, C, G, eps, dtype, wdtype, act)) return rc;
+    if (!X || !Y) return set_error(HLA2_ERR_INVALID, "%s: null pointer", what);
+    const int es = dtype_size(dtype), wsz = dtype_size(wdtype);
+    if (!aligned_elem(X, es) || !aligned_elem(gate, es) || !aligned_elem(Y, es) || !aligned_elem(W, wsz) ||
+        !aligned_elem(Bias, wsz) || !aligned_elem(stats, 8))
+        return set_error(HLA2_ERR_INVALID, "%s: pointer not aligned to its element", what);
+    const GPlan g = gnorm_plan(N, L, C, G, false);
+    if (int rc = check_gws(what, gnorm_bytes(g), workspace, ws_bytes)) return rc;
+    const long long dense[2] = {(long long)L * C, C};
+    auto st = [&](int i, int k) { return strides ? strides[2 * i + k] : dense[k]; };
+    GNormParams p{};
+    p.x = {X, st(0, 0), st(0, 1)};
+    p.z = {gate, st(1, 0), st(1, 1)};
+    p.y = Y; p.yn = st(2, 0); p.yl = st(2, 1);
+    p.w = W; p.b = Bias; p.wdtype = wdtype; p.stats = stats; p.part = static_cast<float*>(workspace);
+    p.N = N; p.L = L; p.C = C; p.G = G; p.cg = C / G; p.silu = act == HLA2_ACT_SILU; p.eps = eps;
+    p.tpr = g.tpr; p.gpb = g.gpb; p.spb = g.spb; p.run = g.run; p.runs = g.runs;
+    const bool vec = (g.unit ? p.cg : C) % 8 == 0 && wide(X, p.x.sn, p.x.sl, N, L, es) &&
+                     wide(gate, p.z.sn, p.z.sl, N, L, es) && wide(Y, p.yn, p.yl, N, L, es) &&
+                     wide(W, 0, 0, 1, 1, wsz) && wide(Bias, 0, 0, 1, 1, wsz);
+    const cudaError_t e = run_gnorm<false>(p, g, dtype, vec, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return set_error(HLA2_ERR_LAUNCH, "%s: %s", what, cudaGetErrorString(e));
+    return HLA2_OK;
+}
+
+extern "C" int hla2_groupnorm_backward(const void* X, const void* dY, const float* stats, const void* W,
+                                       const void* Bias, const void* gate, void* dX, void* dgate, float* dWB,
+                                       long long N, int L, int C, int G, const long long* strides, int act, int dtype,
+                                       int wdtype, void* workspace, size_t ws_bytes, hla2_stream_t stream) {
+    using namespace hla2;
+    const char* what = "groupnorm_backward";
+    if (int rc = check_gnorm(what, N, L, C, G, 0.f, dtype, wdtype, act)) return rc;
+    if (!X || !dY || !stats || !dX || (gate != nullptr) != (dgate != nullptr))
+        return set_error(HLA2_ERR_INVALID, "%s: null pointer, or one of gate and dgate without the other", what);
+    const int es = dtype_size(dtype), wsz = dtype_size(wdtype);
+    if (!aligned_elem(X, es) || !aligned_elem(dY, es) || !aligned_elem(gate, es) || !aligned_elem(dX, es) ||
+        !aligned_elem(dgate, es) || !aligned_elem(W, wsz) || !aligned_elem(Bias, wsz) || !aligned_elem(stats, 8) ||
+        !aligned_elem(dWB, 4))
+        return set_error(HLA2_ERR_INVALID, "%s: pointer not aligned to its element", what);
+    if (dX == dgate) return set_error(HLA2_ERR_INVALID, "%s: two outputs are one tensor", what);
+    const GPlan g = gnorm_plan(N, L, C, G, true);
+    if (int rc = check_gws(what, gnorm_bytes(g), workspace, ws_bytes)) return rc;
+    const long long dense[2] = {(long long)L * C, C};
+    auto st = [&](int i, int k) { return strides ? strides[2 * i + k] : dense[k]; };
+    GNormParams p{};
+    p.x = {X, st(0, 0), st(0, 1)};
+    p.dy = {dY, st(1, 0), st(1, 1)};
+    p.z = {gate, st(2, 0), st(2, 1)};
+    p.y = dX; p.yn = st(3, 0); p.yl = st(3, 1);
+    p.dz = dgate; p.dzn = st(4, 0); p.dzl = st(4, 1);
+    p.w = W; p.b = Bias; p.wdtype = wdtype; p.stats = const_cast<float*>(stats);
+    p.part = static_cast<float*>(workspace); p.dw = dWB;
+    p.N = N; p.L = L; p.C = C; p.G = G; p.cg = C / G; p.silu = act == HLA2_ACT_SILU;
+    p.tpr = g.tpr; p.gpb = g.gpb; p.spb = g.spb; p.run = g.run; p.runs = g.runs;
+    const bool vec = (g.unit ? p.cg : C) % 8 == 0 && wide(X, p.x.sn, p.x.sl, N, L, es) &&
+                     wide(dY, p.dy.sn, p.dy.sl, N, L, es) && wide(gate, p.z.sn, p.z.sl, N, L, es) &&
+                     wide(dX, p.yn, p.yl, N, L, es) && wide(dgate, p.dzn, p.dzl, N, L, es) && wide(W, 0, 0, 1, 1, wsz) &&
+                     wide(Bias, 0, 0, 1, 1, wsz);
+    const cudaError_t e = run_gnorm<true>(p, g, dtype, vec, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return set_error(HLA2_ERR_LAUNCH, "%s: %s", what, cudaGetErrorString(e));
+    return HLA2_OK;
+}

@@ -129,6 +129,12 @@ def lib() -> ctypes.CDLL:
             L.hla2_rmsnorm_backward_workspace.restype = sz
             L.hla2_rmsnorm_backward.argtypes = [vp, vp, vp, vp, vp, vp, ll, i, pll, f, i, i, i, vp, sz, vp]
             L.hla2_rmsnorm_backward.restype = i
+            L.hla2_groupnorm_workspace.argtypes = [ll, i, i, i, i]
+            L.hla2_groupnorm_workspace.restype = sz
+            L.hla2_groupnorm.argtypes = [vp] * 6 + [ll, i, i, i, pll, f, i, i, i, vp, sz, vp]
+            L.hla2_groupnorm.restype = i
+            L.hla2_groupnorm_backward.argtypes = [vp] * 9 + [ll, i, i, i, pll, i, i, i, vp, sz, vp]
+            L.hla2_groupnorm_backward.restype = i
             L.hla2_rotary.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, pi, i, i, pll, i, vp]
             L.hla2_rotary.restype = i
             _lib = L
@@ -1136,6 +1142,149 @@ def hla2_rmsnorm_backward(S: torch.Tensor, dY: torch.Tensor, weight: torch.Tenso
     if rc:
         _check(rc, "hla2_rmsnorm_backward")
     return dX, dW
+
+
+_ACTIVATIONS = {"none": 0, "silu": 1}
+
+
+def hla2_groupnorm_workspace(N: int, L: int, C: int, groups: int, backward: bool = False) -> int:
+    return int(lib().hla2_groupnorm_workspace(N, L, C, groups, int(bool(backward))))
+
+
+def _group_view(t, shape):
+    """Strides of samples and positions of [N, C] or [N, L, C]."""
+    if t is None:
+        return 0, 0
+    st = t.stride()
+    return (st[0], st[1]) if len(shape) == 3 else (st[0], 0)
+
+
+def _group_checks(X, groups, weight, bias, gate, stats, workspace, **like):
+    """The checks of the group norm's inputs, one by one."""
+    _operand(X, "X")
+    if X.dim() not in (2, 3):
+        raise ValueError("expected X [N,C] or [N,L,C]")
+    _dtype_code(X)
+    dev, C = X.device, X.shape[-1]
+    _last_dense(X, "X")
+    if groups < 1 or C % groups:
+        raise ValueError(f"groups must divide the {C} channels, got {groups}")
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None:
+            _operand(t, name, dev, shape=(C,), dense=True)
+            _dtype_code(t)
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise ValueError(f"weight and bias must share a dtype (got {weight.dtype}, {bias.dtype})")
+    if gate is not None:
+        _operand(gate, "gate", dev, X.dtype, X.shape)
+        _last_dense(gate, "gate")
+    if stats is not None:
+        _operand(stats, "stats", dev, _F32, (X.shape[0], groups, 2), dense=True)
+    if workspace is not None:
+        _operand(workspace, "workspace", dev, dense=True)
+    for name, t in like.items():
+        if t is not None:
+            _output(t, name, dev, X.dtype, X.shape)
+    _cuda_device(X, "X")
+
+
+def _group_inputs(X, groups, weight, bias, gate, stats):
+    """(N, L, C, dtype code, weights' dtype code, activation code) where all arguments are the ordinary ones."""
+    shape, dt, dev = X.shape, X.dtype, X.device
+    return (X.is_cuda and len(shape) in (2, 3) and dt in _CODES and X.is_contiguous() and groups >= 1 and
+            not shape[-1] % groups and
+            all(t is None or (t.dtype in _CODES and t.shape == shape[-1:] and t.device == dev and t.is_contiguous())
+                for t in (weight, bias)) and
+            (weight is None or bias is None or weight.dtype is bias.dtype) and
+            (gate is None or (gate.dtype is dt and gate.shape == shape and gate.device == dev and
+                              gate.is_contiguous())) and
+            (stats is None or (stats.dtype is _F32 and stats.shape == (shape[0], groups, 2) and
+                               stats.device == dev and stats.is_contiguous())))
+
+
+def _activation(name) -> int:
+    code = _ACTIVATIONS.get(name)
+    if code is None:
+        raise ValueError(f"unknown activation {name!r}: one of {sorted(_ACTIVATIONS)}")
+    return code
+
+
+def _group_work(L, workspace, N, P, C, groups, backward, dev):
+    if workspace is not None:
+        return workspace, workspace.numel() * workspace.element_size()
+    need = L.hla2_groupnorm_workspace(N, P, C, groups, backward)
+    return (torch.empty(need, device=dev, dtype=torch.uint8) if need else None), need
+
+
+def hla2_groupnorm(X: torch.Tensor, groups: int, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                   gate: torch.Tensor | None = None, activation: str = "none", Y: torch.Tensor | None = None,
+                   stats: torch.Tensor | None = None, eps: float = 1e-5, workspace: torch.Tensor | None = None,
+                   stream=None) -> torch.Tensor:
+    """Group norm, channels last: X [N,L,C] (statistics over a sample's L positions
+    and a group's C / groups channels) or [N,C] (L = 1: the groups of each row, as
+    behind an attention layer with a group for each head), fp32 or bf16 -> Y like
+    X.  z = (X - mean) / sqrt(var + eps) * weight + bias;  Y = act(z), or
+    z * act(gate) with a ``gate`` like X;  ``activation`` "none" or "silu".
+    weight, bias [C] fp32 or bf16.  ``stats`` [N,groups,2] fp32 keeps what
+    hla2_groupnorm_backward needs.  Y may be X or gate."""
+    acode = _activation(activation)
+    if Y is not None or workspace is not None or not _group_inputs(X, groups, weight, bias, gate, stats):
+        _group_checks(X, groups, weight, bias, gate, stats, workspace, Y=Y)
+    dev, shape = X.device, X.shape
+    N, C = shape[0], shape[-1]
+    P = shape[1] if len(shape) == 3 else 1
+    wcode = _CODES[weight.dtype if weight is not None else bias.dtype if bias is not None else _F32]
+    L = _lib or lib()
+    with _guard(dev, stream):
+        if Y is None:
+            Y = _like(X)
+        workspace, nws = _group_work(L, workspace, N, P, C, groups, 0, dev)
+        rc = L.hla2_groupnorm(X.data_ptr(), _ptr(weight), _ptr(bias), _ptr(gate), Y.data_ptr(), _ptr(stats), N, P, C,
+                              groups, _longs(*_group_view(X, shape), *_group_view(gate, shape), *_group_view(Y, shape)),
+                              eps, acode, _CODES[X.dtype], wcode, _ptr(workspace), nws, _raw(dev, stream))
+    if rc:
+        _check(rc, "hla2_groupnorm")
+    return Y
+
+
+def hla2_groupnorm_backward(X: torch.Tensor, dY: torch.Tensor, stats: torch.Tensor, weight: torch.Tensor | None = None,
+                            bias: torch.Tensor | None = None, gate: torch.Tensor | None = None,
+                            activation: str = "none", dX: torch.Tensor | None = None,
+                            dgate: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """Gradients of hla2_groupnorm at X, with the ``stats`` [N,groups,2] that the
+    forward kept and its weight, bias, gate and activation: (dX, dW, dB, dgate), dX
+    and dgate in X's dtype (dgate None without a gate), dW and dB [C] fp32.  dX may
+    be dY or X, dgate may be gate."""
+    acode = _activation(activation)
+    groups = stats.shape[1] if isinstance(stats, torch.Tensor) and stats.dim() == 3 else 0
+    if not groups:
+        raise ValueError("expected stats [N,groups,2]")
+    if not (dX is dgate is workspace is None and _group_inputs(X, groups, weight, bias, gate, stats) and
+            dY.dtype is X.dtype and dY.shape == X.shape and dY.device == X.device and dY.is_contiguous()):
+        if gate is None and dgate is not None:
+            raise ValueError("dgate without a gate")
+        _group_checks(X, groups, weight, bias, gate, stats, workspace, dX=dX, dgate=dgate)
+        _operand(dY, "dY", X.device, X.dtype, X.shape)
+        _last_dense(dY, "dY")
+    dev, shape = X.device, X.shape
+    N, C = shape[0], shape[-1]
+    P = shape[1] if len(shape) == 3 else 1
+    wcode = _CODES[weight.dtype if weight is not None else bias.dtype if bias is not None else _F32]
+    L = _lib or lib()
+    with _guard(dev, stream):
+        if dX is None:
+            dX = _like(X)
+        if gate is not None and dgate is None:
+            dgate = _like(gate)
+        dwb = torch.empty((2, C), device=dev, dtype=_F32)
+        workspace, nws = _group_work(L, workspace, N, P, C, groups, 1, dev)
+        rc = L.hla2_groupnorm_backward(X.data_ptr(), dY.data_ptr(), stats.data_ptr(), _ptr(weight), _ptr(bias),
+                                       _ptr(gate), dX.data_ptr(), _ptr(dgate), dwb.data_ptr(), N, P, C, groups,
+                                       _longs(*(v for t in (X, dY, gate, dX, dgate) for v in _group_view(t, shape))),
+                                       acode, _CODES[X.dtype], wcode, _ptr(workspace), nws, _raw(dev, stream))
+    if rc:
+        _check(rc, "hla2_groupnorm_backward")
+    return dX, dwb[0], dwb[1], dgate
 
 
 def _rotary_checks(Q, pos, freq, sections, K, OQ, OK):

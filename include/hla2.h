@@ -64,6 +64,9 @@ enum {
 
 enum { HLA2_DTYPE_F32 = 0, HLA2_DTYPE_BF16 = 1 };
 
+/* Activations of hla2_groupnorm: the identity, x / (1 + exp(-x)). */
+enum { HLA2_ACT_NONE = 0, HLA2_ACT_SILU = 1 };
+
 /*
  * Bytes of device workspace hla2_forward needs for this problem (valid for
  * either value of `normalized`).  Returns 0 for sizes hla2_forward rejects.
@@ -535,6 +538,46 @@ HLA2_API size_t hla2_rmsnorm_backward_workspace(long long rows, int C);
 HLA2_API int hla2_rmsnorm_backward(const void* S, const void* dY, const void* W, const void* dS, void* dX, float* dW,
                                    long long rows, int C, const long long* ld, float eps, int dtype, int wdtype,
                                    int out_dtype, void* workspace, size_t ws_bytes, hla2_stream_t stream);
+
+/*
+ * Group norm, channels last, with an activation or a gate:
+ *   n = (X - mean) / sqrt(var + eps),  z = n W + Bias,
+ *   Y = act(z), or z act(gate) where there is a gate.
+ * Mean and variance are taken over a sample's L positions and a group's C / G
+ * channels (L = 1: each row's groups by themselves, as behind an attention layer
+ * with one group for each head).
+ *   X, gate, Y  [N][L][C] dtype (gate optional; Y may be X or gate);
+ *   W, Bias     [C] wdtype (NULL: ones, zeros);
+ *   stats       optional [N][G][2] fp32, 8-byte aligned: mean and 1 / sqrt(var + eps),
+ *               which the gradient takes;
+ *   strides     NULL, or six values: X, gate, Y (sample, position each), in elements.
+ *   act         HLA2_ACT_NONE or HLA2_ACT_SILU.
+ *   workspace   hla2_groupnorm_workspace(..., 0) bytes, 16-byte aligned, not
+ *               initialised; NULL when that is 0.  It serves one call at a time.
+ * All sums are fp32 or 64 bits, in a fixed order; the variance is that of the values about their mean.
+ * Values stay below about 1e18.
+ * Errors: HLA2_ERR_INVALID (G not a divisor of C among them), HLA2_ERR_UNSUPPORTED
+ * (C > 16384, N*L or N*G > 2^31 - 1, types), HLA2_ERR_WORKSPACE, HLA2_ERR_LAUNCH.
+ */
+HLA2_API size_t hla2_groupnorm_workspace(long long N, int L, int C, int G, int backward);
+HLA2_API int hla2_groupnorm(const void* X, const void* W, const void* Bias, const void* gate, void* Y, float* stats,
+                            long long N, int L, int C, int G, const long long* strides, float eps, int act, int dtype,
+                            int wdtype, void* workspace, size_t ws_bytes, hla2_stream_t stream);
+
+/*
+ * Gradients of hla2_groupnorm at X and the forward's stats.  With dz = dY act'(z)
+ * (dY act(gate) where there is a gate) and t = dz W, means over a sample's group:
+ *   dX = rstd (t - mean(t) - n mean(t n)),   dgate = dY z act'(gate),
+ *   dWB[0][c] = sum of dz n (W's gradient),  dWB[1][c] = sum of dz (Bias's).
+ *   dY, dX, dgate [N][L][C] dtype (dgate with a gate only); dX may be dY or X, and
+ *   dgate may be gate;  dWB  optional [2][C] fp32.
+ *   strides     NULL, or ten values: X, dY, gate, dX, dgate (sample, position each).
+ *   workspace   hla2_groupnorm_workspace(..., 1) bytes.
+ */
+HLA2_API int hla2_groupnorm_backward(const void* X, const void* dY, const float* stats, const void* W,
+                                     const void* Bias, const void* gate, void* dX, void* dgate, float* dWB,
+                                     long long N, int L, int C, int G, const long long* strides, int act, int dtype,
+                                     int wdtype, void* workspace, size_t ws_bytes, hla2_stream_t stream);
 
 /*
  * Rotary positions with several axes, on queries and (optionally) keys.
