@@ -40,7 +40,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) lin_walk_kernel(const LinWalk
     if (tid <= kTokens) pw[tid] = (float)power(g, tid);
     const size_t R = (size_t)p.da * p.dc;
     // the state that enters
-    const float* rec = OUT && p.nseg > 1 ? p.rec + ((size_t)bh * p.nseg + w) * R : nullptr;
+    const float* rec = OUT && p.nseg > 1 ? p.rec + ((size_t)bh * (p.nseg + 1) + w) * R : nullptr;
     for (int e = tid; e < D * D; e += kWalkThreads) {
         const int r = e / D, c = e % D;
         float v = 0.f;
@@ -189,9 +189,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1) lin_walk_kernel(const LinWalk
     }
     __syncthreads();
     if (!OUT) {
-        float* dst = p.rec + ((size_t)bh * p.nseg + w + 1) * R;
+        float* dst = p.rec + ((size_t)bh * (p.nseg + 1) + w + 1) * R;
         for (int e = tid; e < (int)R; e += kWalkThreads) dst[e] = sS[e / p.dc * D + e % p.dc];
-    } else if (p.s_out && w == p.nseg - 1) {
+    } else if (p.s_out && p.nseg == 1) {
         for (int e = tid; e < (int)R; e += kWalkThreads) {
             const int r = e / p.dc, c = e % p.dc;
             p.s_out[(size_t)bh * R + r * p.out_r + c * p.out_c] = sS[r * D + c];
@@ -200,28 +200,28 @@ __global__ void __launch_bounds__(kWalkThreads, 1) lin_walk_kernel(const LinWalk
 }
 
 // The states that enter the segments, in place: slot 0 is the state before the
-// first, slot w + 1 becomes g^(tokens of w) slot w + (its own sum).  A thread
-// for each element; the loads do not wait for the sums.
-__global__ void __launch_bounds__(256) lin_scan_kernel(const LinWalk p, int chunk) {
+// first, slot w + 1 becomes g^(tokens of w) slot w + (its own sum); `segments`
+// have one.  A thread for each element; the loads do not wait for the sums.
+__global__ void __launch_bounds__(256) lin_scan_kernel(const LinWalk p, int chunk, int segments) {
     const int R = p.da * p.dc, e = blockIdx.x * 256 + threadIdx.x, bh = blockIdx.y;
     __shared__ float f[256];
     const int len = length_of(p, bh / p.H);
     const double g = (double)__ldg(p.gamma + bh % p.H);
-    float* const rec = p.rec + (size_t)bh * p.nseg * R + e;
+    float* const rec = p.rec + (size_t)bh * (p.nseg + 1) * R + e;
     float acc = 0.f;
     if (e < R) {
         if (p.s_in) acc = p.s_in[(size_t)bh * R + (e / p.dc) * p.in_r + (e % p.dc) * p.in_c];
         rec[0] = acc;
     }
-    for (int base = 0; base < p.nseg - 1; base += 256) {
+    for (int base = 0; base < segments; base += 256) {
         const int w = base + threadIdx.x;
-        if (w < p.nseg - 1) {
+        if (w < segments) {
             const int seg = p.rev ? p.nseg - 1 - w : w;
             const long long t0 = (long long)seg * p.seglen * chunk, t1 = t0 + (long long)p.seglen * chunk;
             f[threadIdx.x] = (float)power(g, (int)max(0LL, min(t1, (long long)len) - t0));
         }
         __syncthreads();
-        const int m = min(256, p.nseg - 1 - base);
+        const int m = min(256, segments - base);
         if (e < R) {
 #pragma unroll 8
             for (int i = 0; i < m; ++i) {
@@ -232,6 +232,7 @@ __global__ void __launch_bounds__(256) lin_scan_kernel(const LinWalk p, int chun
         }
         __syncthreads();
     }
+    if (e < R && p.s_out) p.s_out[(size_t)bh * R + (e / p.dc) * p.out_r + (e % p.dc) * p.out_c] = acc;
 }
 
 // Zeros in the rows behind each sequence's end (the gradients there).
@@ -339,7 +340,7 @@ cudaError_t launch_simple(const LinWalk& w, bool states, cudaStream_t s) {
     const int bytes = SimpleLayout<D>::kBytes;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    kernel<<<dim3(states ? w.nseg - 1 : w.nseg, w.B * w.H), kWalkThreads, bytes, s>>>(w);
+    kernel<<<dim3(states ? lin_state_segments(w) : w.nseg, w.B * w.H), kWalkThreads, bytes, s>>>(w);
     note_launches(1);
     return cudaGetLastError();
 }
@@ -357,7 +358,7 @@ cudaError_t run_walk(LinWalk w, int dtype, cudaStream_t s) {
     };
     if (w.nseg > 1) {
         if (cudaError_t e = walk(true)) return e;
-        lin_scan_kernel<<<dim3((w.da * w.dc + 255) / 256, w.B * w.H), 256, 0, s>>>(w, chunk);
+        lin_scan_kernel<<<dim3((w.da * w.dc + 255) / 256, w.B * w.H), 256, 0, s>>>(w, chunk, lin_state_segments(w));
         note_launches(1);
         if (cudaError_t e = cudaGetLastError()) return e;
     }
@@ -394,7 +395,7 @@ size_t walk_bytes(int B, int H, int T, int d, int dv) {
     for (int chunk : {kLinTcChunk, kTokens}) {
         int nseg, seglen, nchunk;
         plan_segments(B * H, T, chunk, &nseg, &seglen, &nchunk);
-        if (nseg > 1) most = max(most, (size_t)B * H * nseg * d * dv * 4);
+        if (nseg > 1) most = max(most, (size_t)B * H * (nseg + 1) * d * dv * 4);
     }
     return (most + 255) & ~size_t(255);
 }

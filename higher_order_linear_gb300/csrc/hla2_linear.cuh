@@ -9,10 +9,11 @@
 // dK = (v, dO, q) and dV = (k, q, dO) backwards, from the last state's gradient.
 //
 // A head's chunks are cut into nseg segments, a CTA each.  Walk index w counts
-// segments in walk order.  With more than one: every segment but the last
-// leaves its own sum (from zero) in slot w + 1 of the head's records, a scan
-// turns the slots into the states that enter the segments, and the second
-// walk starts from slot w.
+// segments in walk order.  With more than one: every segment (the last one
+// only where the last state is wanted) leaves its own sum (from zero) in slot
+// w + 1 of the head's records, a scan turns the slots into the states that
+// enter the segments and writes the last state, and the second walk starts from
+// slot w.  A single segment's walk writes the last state itself.
 #pragma once
 
 #include "hla2_layer.cuh"
@@ -29,11 +30,14 @@ struct LinWalk {
     const float* s_in;   // [BH][da * dc], element (r, c) at r in_r + c in_c; null: zero
     float* s_out;        // the same with out_r, out_c; null: not wanted
     long long in_r, in_c, out_r, out_c;
-    float* rec;  // [BH][nseg][da * dc] (nseg > 1)
+    float* rec;  // [BH][nseg + 1][da * dc] (nseg > 1)
     int nseg, seglen, nchunk;
     int rev;
     int* status;
 };
+
+// segments whose own sums are formed
+inline int lin_state_segments(const LinWalk& w) { return w.s_out ? w.nseg : w.nseg - 1; }
 
 // Tensor cores (hla2_linear_tc.cu): bf16, da and dc up to 128, rows and bases
 // of whole 16-byte steps.  chunks of 128 tokens.

@@ -13,13 +13,16 @@
 // Precision.  P~ and the copy of S that A is multiplied with are rounded to
 // bf16 (half a unit each, like the bf16 result itself).  S is fp32, in the
 // registers of the warps that update it: the tensor cores only form U, one
-// chunk's sum, from B~ as three bf16 terms (24 bits), so neither a rounded
-// decay nor a sum of many chunks in the accumulator costs it bits.
+// chunk's sum, so neither a rounded decay nor a sum of many chunks in the
+// accumulator costs it bits.  B~ is three bf16 terms (24 bits) where S leaves
+// the walk in fp32, two (16 bits, far below the copy's 8) where only the copy is used.
 //
-// Roles.  X warps (8): P from tensor memory, decayed, masked and packed back;
-// o_i from O1 and O2 to global memory.  Y warps (8): B~ in quarters of 32
-// tokens (first terms in place of B, the others in a ring of two slots), then S
-// and its bf16 copy.  One warp issues the products, one the loads.
+// Roles.  X warps (4): P from tensor memory, decayed, masked and packed back;
+// o_i from O1 and O2, through shared memory, to global memory.  Y warps (8): B~
+// in steps of 32 tokens (first terms in place of B, the others in a ring of two
+// slots), then S and its bf16 copy.  One warp issues the products, one the loads.
+// Four warps to a scheduler leave 128 registers to a thread, which S (64 of
+// them) needs: local memory would go to L2, shared memory takes all of L1.
 #include "hla2_linear.cuh"
 #include "hla2_tc_common.cuh"
 
@@ -45,39 +48,67 @@ __device__ __forceinline__ void tmem_store16(uint32_t taddr, const uint32_t (&r)
         : "memory");
 }
 
-constexpr int kQuarter = 32;  // tokens of B~ at a time
+// (a, b) op (c, d), two fp32 operations to an instruction
+struct Pair {
+    float x, y;
+};
+__device__ __forceinline__ unsigned long long bits(Pair a) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+    return r;
+}
+__device__ __forceinline__ Pair pair_of(unsigned long long v) {
+    Pair r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
+    return pair_of(r);
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+    return pair_of(r);
+}
+__device__ __forceinline__ Pair unpack_bf16(uint32_t w) { return {__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)}; }
+__device__ __forceinline__ Pair at(const uint32_t* r) { return {__uint_as_float(r[0]), __uint_as_float(r[1])}; }
 
 // Shared memory.  Tiles of A: NA, of B and C: NB; the ring's slots hold the
-// second and third terms of a quarter of B~.  At D = 64 the products' A operand
-// still has 128 rows: those past the tile's 64 columns read what follows it in
-// this allocation, and nobody reads their results.
-template <int D, bool OUT>
+// second (and third) terms of STEP tokens of B~; the stage a group of 64 output
+// columns of each X warp.  At D = 64 the products' A operand still has 128
+// rows: those past the tile's 64 columns read what follows it in this
+// allocation, and nobody reads their results.
+template <int D, bool OUT, int TERMS>
 struct TcLayout {
+    static constexpr int STEP = D == 128 && OUT && TERMS == 3 ? 16 : 32;
     static constexpr int NA = OUT ? (D == 64 ? 2 : 1) : 0, NB = OUT ? (D == 64 ? 3 : 2) : 3;
-    static constexpr uint32_t kTile = kL * D * 2, kPart = kQuarter * D * 2;
+    static constexpr uint32_t kTile = kL * D * 2, kPart = STEP * D * 2;
     static constexpr uint32_t A = 0, B = NA * kTile, C = B + NB * kTile, ring = C + NB * kTile;
-    static constexpr uint32_t S = ring + 4 * kPart, kBytes = S + (D == 64 || OUT ? D * D * 2 : 0);
+    static constexpr uint32_t S = ring + 2 * (TERMS - 1) * kPart;
+    static constexpr uint32_t stage = S + (D == 64 || OUT ? D * D * 2 : 0), kBytes = stage + (OUT ? 4 * 4096 : 0);
 };
 
 template <int D, bool OUT>
 struct TcRoles {
-    static constexpr int kX = OUT ? 8 : 0, kY = 8;
+    static constexpr int kX = OUT ? 4 : 0, kY = 8;
     static constexpr int kThreads = (kX + kY + 2) * 32;
     static constexpr int kState = D / 32 * 2;  // Y warps that hold rows of the state
 };
 
-template <int D, bool REV, bool OUT>
+template <int D, bool REV, bool OUT, int TERMS>
 __global__ void __launch_bounds__(TcRoles<D, OUT>::kThreads, 1)
 lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorMap mB,
               const __grid_constant__ CUtensorMap mC, const LinWalk p) {
-    using LY = TcLayout<D, OUT>;
+    using LY = TcLayout<D, OUT, TERMS>;
     using RO = TcRoles<D, OUT>;
-    constexpr int NA = LY::NA, NB = LY::NB;
+    constexpr int NA = LY::NA, NA1 = NA ? NA : 1, NB = LY::NB, STEP = LY::STEP, STEPS = kL / STEP;
     extern __shared__ __align__(1024) unsigned char dsm_raw[];
     // loads | buffers free | P ready, packed | ring filled, free | U ready, drained | S copy ready, read |
     // O ready, drained | last wait
     enum { LA, LB = LA + NA, LC = LB + NB, FA = LC + NB, FB = FA + NA, FC = FB + NB, CP = FC + NB, DP, KQ, RF = KQ + 2,
-           CU = RF + 2, DU, DS, CS, CO, DO, FIN, NBAR };
+           CU = RF + 2, DU = CU + 2, DS, CS, CO, DO, FIN, NBAR };
     __shared__ __align__(8) unsigned long long bars[NBAR];
     __shared__ __align__(16) float pw[kL + 4];  // g^0 .. g^128
     __shared__ __align__(16) float down[32];    // g^31 .. g^0
@@ -88,7 +119,6 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
     const bool xwarp = warp < RO::kX, ywarp = !xwarp && warp < RO::kX + RO::kY;
     const bool issuer = warp == RO::kX + RO::kY, loader = warp == RO::kX + RO::kY + 1;
     const int quarter = warp & 3, row = quarter * 32 + lane;  // lanes of tensor memory
-    const int part = (warp >> 2) & 1;                         // which half of the columns
     const int bh = blockIdx.y, w = blockIdx.x, seg = REV ? p.nseg - 1 - w : w;
     const int b = bh / p.H, h = bh % p.H;
     const int len = length_of(p, b);
@@ -98,10 +128,12 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
     auto tokens_of = [&](int it) { return min(kL, len - chunk_of(it) * kL); };
 
     const uint32_t dsm = (smem_u32(dsm_raw) + 1023u) & ~1023u;
-    auto tA = [&](int it) { return Tile{dsm + LY::A + (uint32_t)(it % (NA ? NA : 1)) * LY::kTile, kL}; };
+    auto tA = [&](int it) { return Tile{dsm + LY::A + (uint32_t)(it % NA1) * LY::kTile, kL}; };
     auto tB = [&](int it) { return Tile{dsm + LY::B + (uint32_t)(it % NB) * LY::kTile, kL}; };
     auto tC = [&](int it) { return Tile{dsm + LY::C + (uint32_t)(it % NB) * LY::kTile, kL}; };
-    auto tR = [&](int slot, int term) { return Tile{dsm + LY::ring + (uint32_t)(slot * 2 + term) * LY::kPart, kQuarter}; };
+    auto tR = [&](int slot, int term) {
+        return Tile{dsm + LY::ring + (uint32_t)(slot * (TERMS - 1) + term) * LY::kPart, STEP};
+    };
     const Tile tS{dsm + LY::S, D};
     auto bar = [&](int i) -> uint32_t { return smem_u32(&bars[i]); };
 
@@ -131,7 +163,9 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
-    const uint32_t tP = tmem, tO1 = tmem + 128, tO2 = tmem + 128 + D, tU = tmem + 128 + 2 * D;
+    // outputs: P | O1 | O2 | U;  states: U twice, by turns
+    const uint32_t tP = tmem, tO1 = tmem + 128, tO2 = tmem + 128 + D;
+    auto tU = [&](int it) -> uint32_t { return OUT ? tmem + 128 + 2 * D : tmem + 128 * (it & 1); };
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
 
     auto wait_bar = [&](int i, uint32_t parity) -> bool {
@@ -170,40 +204,41 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
                 if (OUT) {
                     // P, once the previous chunk's P~ C has read its columns
                     if (it > 0 && !wait_bar(CO, before)) break;
-                    if (!wait_bar(LA + it % (NA ? NA : 1), (uint32_t)(it / (NA ? NA : 1)) & 1) || !wait_bar(LB + sb, kb)) break;
+                    if (!wait_bar(LA + it % NA1, (uint32_t)(it / NA1) & 1) || !wait_bar(LB + sb, kb)) break;
                     tc_fence_after();
                     const Tile A = tA(it);
                     for (int ks = 0; ks < D / 16; ++ks) mma_bf16(tP, A.kmaj(ks), B.kmaj(ks), iPP, ks > 0);
                     mma_commit(bar(CP));
                 }
-                // U, a quarter of the tokens at a time as Y fills the ring
+                // U, a step of the tokens at a time as Y fills the ring, once its columns have been drained
                 if (!wait_bar(LC + sb, kb)) break;
-                if (it > 0 && !wait_bar(DU, before)) break;
+                if (OUT ? it > 0 && !wait_bar(DU, before) : it > 1 && !wait_bar(DU, ph)) break;
                 bool ok = true;
-                for (int q = 0; q < 4 && ok; ++q) {
-                    if (OUT && q == 2) {
-                        // O2 = A S beside Y's third quarter
+                for (int q = 0; q < STEPS && ok; ++q) {
+                    if (OUT && q == STEPS / 2) {
+                        // O2 = A S beside Y's second half
                         if (!wait_bar(DS, ph) || (it > 0 && !wait_bar(DO, before))) { ok = false; break; }
                         tc_fence_after();
                         const Tile A = tA(it);
                         for (int ks = 0; ks < D / 16; ++ks) mma_bf16(tO2, A.kmaj(ks), tS.mnmaj(ks), iAS, ks > 0);
                         mma_commit(bar(CS));
-                        mma_commit(bar(FA + it % (NA ? NA : 1)));
+                        mma_commit(bar(FA + it % NA1));
                     }
                     const int slot = q & 1;
-                    if (!wait_bar(KQ + slot, (uint32_t)((2 * it + (q >> 1)) & 1))) { ok = false; break; }
+                    if (!wait_bar(KQ + slot, (uint32_t)((STEPS / 2 * it + (q >> 1)) & 1))) { ok = false; break; }
                     tc_fence_after();
-                    const Tile mid = tR(slot, 0), lo = tR(slot, 1);
-                    for (int ks = 0; ks < 2; ++ks) {
-                        const uint64_t c = C.mnmaj(2 * q + ks);
-                        mma_bf16(tU, B.mnmaj(2 * q + ks), c, iBC, q + ks > 0);
-                        mma_bf16(tU, mid.mnmaj(ks), c, iBC, 1);
-                        mma_bf16(tU, lo.mnmaj(ks), c, iBC, 1);
+                    const uint32_t u = tU(it);
+                    for (int ks = 0; ks < STEP / 16; ++ks) {
+                        const int kk = q * (STEP / 16) + ks;
+                        const uint64_t c = C.mnmaj(kk);
+                        mma_bf16(u, B.mnmaj(kk), c, iBC, kk > 0);
+#pragma unroll
+                        for (int t = 0; t < TERMS - 1; ++t) mma_bf16(u, tR(slot, t).mnmaj(ks), c, iBC, 1);
                     }
                     mma_commit(bar(RF + slot));
                 }
                 if (!ok) break;
-                mma_commit(bar(CU));
+                mma_commit(bar(CU + (OUT ? 0 : it & 1)));
                 mma_commit(bar(FB + sb));
                 if (OUT) {
                     if (!wait_bar(DP, ph)) break;
@@ -232,7 +267,7 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
                 if (ub > 0 && !wait_bar(FC + sb, (uint32_t)(ub - 1) & 1)) break;
                 load(LC + sb, &mC, tC(it), it);
                 if (OUT) {
-                    const int sa = it % (NA ? NA : 1), ua = it / (NA ? NA : 1);
+                    const int sa = it % NA1, ua = it / NA1;
                     if (ua > 0 && !wait_bar(FA + sa, (uint32_t)(ua - 1) & 1)) break;
                     load(LA + sa, &mA, tA(it), it);
                 }
@@ -241,14 +276,15 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
         }
     } else if (OUT && xwarp) {
         bf16* const out = static_cast<bf16*>(p.o) + b * p.so[0] + h * p.so[1];
+        const uint32_t stage = dsm + LY::stage + (uint32_t)warp * 4096u;
         for (int it = 0; it < nchunks; ++it) {
             const uint32_t ph = it & 1;
             const int n = tokens_of(it);
             if (!wait_bar(CP, ph)) break;
             tc_fence_after();
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int col = (k == 0 ? part : 3 - part) * 32;  // both halves get a full and a short one
+            for (int k = 0; k < 4; ++k) {
+                const int col = 32 * k;
                 uint32_t hi[16];
                 const bool none = REV ? col < quarter * 32 : col > quarter * 32;
                 if (none) {
@@ -258,14 +294,15 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
                     uint32_t r[32];
                     tmem_ld32(tP + lane_off + col, r);
                     tmem_ld_wait();
-                    float v[32];
                     if (col == quarter * 32) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j) {
                             const int far = REV ? j - lane : lane - j;
                             const bool in = far >= 0 && (!REV || col + j < n);
-                            v[j] = in ? __uint_as_float(r[j]) * pw[in ? far : 0] : 0.f;
+                            r[j] = in ? __float_as_uint(__uint_as_float(r[j]) * pw[in ? far : 0]) : 0u;
                         }
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) hi[j] = pack_bf16(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
                     } else {
                         // the row's distance to the group's near edge, then the group's own powers
                         const float f = pw[REV ? col - row : row - col - 31];
@@ -273,14 +310,19 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
                         for (int j = 0; j < 32; j += 4) {
                             const float4 u = REV ? *reinterpret_cast<const float4*>(pw + j)
                                                  : *reinterpret_cast<const float4*>(down + j);
-                            const float uu[4] = {u.x, u.y, u.z, u.w};
+                            const Pair x = mul2(mul2(at(r + j), {f, f}), {u.x, u.y});
+                            const Pair y = mul2(mul2(at(r + j + 2), {f, f}), {u.z, u.w});
+                            hi[j / 2] = pack_bf16(x.x, x.y);
+                            hi[j / 2 + 1] = pack_bf16(y.x, y.y);
+                        }
+                        if (REV && col + 32 > n) {  // tokens behind the end: whatever they held
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                v[j + i] = !REV || col + j + i < n ? __uint_as_float(r[j + i]) * (f * uu[i]) : 0.f;
+                            for (int j = 0; j < 16; ++j) {
+                                if (col + 2 * j >= n) hi[j] = 0u;
+                                else if (col + 2 * j + 1 >= n) hi[j] &= 0xffffu;
+                            }
                         }
                     }
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) hi[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
                 }
                 tmem_store16(tP + lane_off + col, hi);
             }
@@ -290,36 +332,48 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
             if (!wait_bar(CO, ph)) break;
             tc_fence_after();
             const float f = row < n ? pw[REV ? n - 1 - row : row + 1] : 0.f;
-            bf16* const dst = out + (long long)(chunk_of(it) * kL + row) * p.so[2];
-            constexpr int G = D / 64;  // groups of 32 columns to a warp
+            const long long t0 = (long long)chunk_of(it) * kL + quarter * 32;
 #pragma unroll
-            for (int k = 0; k < G; ++k) {
-                const int col = (part * G + k) * 32;
-                uint32_t r1[32], r2[32];
-                tmem_ld32(tO1 + lane_off + col, r1);
-                tmem_ld32(tO2 + lane_off + col, r2);
-                tmem_ld_wait();
-                if (k == G - 1) {
-                    tc_fence_before();
-                    arrive(DO);
-                }
-                if (row < n) {
+            for (int g = 0; g < D / 64; ++g) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int col = 64 * g + 32 * k;
+                    uint32_t r1[32], r2[32];
+                    tmem_ld32(tO1 + lane_off + col, r1);
+                    tmem_ld32(tO2 + lane_off + col, r2);
+                    tmem_ld_wait();
+                    if (col == D - 32) {
+                        tc_fence_before();
+                        arrive(DO);
+                    }
 #pragma unroll
                     for (int j = 0; j < 32; j += 8) {
-                        if (col + j >= p.dc) break;
                         uint32_t o[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            o[i] = pack_bf16(fmaf(f, __uint_as_float(r2[j + 2 * i]), __uint_as_float(r1[j + 2 * i])),
-                                             fmaf(f, __uint_as_float(r2[j + 2 * i + 1]), __uint_as_float(r1[j + 2 * i + 1])));
-                        *reinterpret_cast<uint4*>(dst + col + j) = make_uint4(o[0], o[1], o[2], o[3]);
+                        for (int i = 0; i < 4; ++i) {
+                            const Pair v = fma2({f, f}, at(r2 + j + 2 * i), at(r1 + j + 2 * i));
+                            o[i] = pack_bf16(v.x, v.y);
+                        }
+                        st_shared_v4(stage + (uint32_t)lane * 128u + (uint32_t)(((4 * k + j / 8) ^ (lane & 7)) << 4), o[0],
+                                     o[1], o[2], o[3]);
                     }
                 }
+                // whole lines of 128 bytes to global memory, four rows at a time
+                __syncwarp();
+                const int c = 64 * g + (lane & 7) * 8;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int r = 4 * i + (lane >> 3);
+                    uint4 v;
+                    ld_shared_v4(stage + (uint32_t)r * 128u + (uint32_t)(((lane & 7) ^ (r & 7)) << 4), v.x, v.y, v.z, v.w);
+                    if (quarter * 32 + r < n && c < p.dc) *reinterpret_cast<uint4*>(out + (t0 + r) * p.so[2] + c) = v;
+                }
+                __syncwarp();
             }
         }
     } else if (ywarp) {
         constexpr int W = D / 2;  // columns of S to a thread
-        const int yw = warp - RO::kX;
+        const int yw = warp - RO::kX, part = yw >> 2;
         const bool holds = quarter < D / 32;
         const int scol = part * W;
         const size_t R = (size_t)p.da * p.dc;
@@ -330,7 +384,7 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
             const float* src = nullptr;
             long long step = 1;
             if (p.nseg > 1) {
-                src = p.rec + ((size_t)bh * p.nseg + w) * R + (size_t)row * p.dc;
+                src = p.rec + ((size_t)bh * (p.nseg + 1) + w) * R + (size_t)row * p.dc;
             } else if (p.s_in) {
                 src = p.s_in + (size_t)bh * R + row * p.in_r;
                 step = p.in_c;
@@ -351,79 +405,94 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
             fence_proxy_async();
             arrive(DS);
         };
+        auto update = [&](int it) -> bool {  // S of chunk it's end
+            if (!wait_bar(CU + (OUT ? 0 : it & 1), OUT ? (uint32_t)it & 1 : (uint32_t)(it >> 1) & 1)) return false;
+            tc_fence_after();
+            const float gn = pw[tokens_of(it)];
+#pragma unroll
+            for (int k = 0; k < W / 32; ++k) {
+                uint32_t r[32];
+                tmem_ld32(tU(it) + lane_off + scol + 32 * k, r);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 32; j += 2) {
+                    const Pair v = fma2({gn, gn}, {S[32 * k + j], S[32 * k + j + 1]}, at(r + j));
+                    S[32 * k + j] = v.x;
+                    S[32 * k + j + 1] = v.y;
+                }
+            }
+            tc_fence_before();
+            arrive(DU);
+            return true;
+        };
         if (OUT && holds && nchunks > 0) copy_state();
-        for (int it = 0; it < nchunks; ++it) {
+        // the thread's row of four, and its first column step of a tile's row
+        constexpr int ROWS4 = STEP / 4, ITEMS = ROWS4 * (D / 64) / RO::kY;
+        int it = 0;
+        for (; it < nchunks; ++it) {
             const uint32_t ph = it & 1;
             const int n = tokens_of(it), sb = it % NB;
             const uint32_t kb = (uint32_t)(it / NB) & 1;
             const Tile B = tB(it), C = tC(it);
-            if (!wait_bar(LB + sb, kb)) break;
+            if (!wait_bar(LB + sb, kb) || (OUT && !wait_bar(CP, ph))) break;  // A B^T has read B
             if (n < kL) {
-                // rows behind the end: zeros in C, whatever they hold (B~'s are zeros below)
+                // rows of C behind the end: zeros, whatever they hold
                 if (!wait_bar(LC + sb, kb)) break;
                 for (int i = (n << 3) + yw * 32 + lane; i < kL * 8; i += RO::kY * 32)
 #pragma unroll
                     for (int k = 0; k < D / 64; ++k) st_shared_v4(C.chunk(i >> 3, k, i & 7), 0u, 0u, 0u, 0u);
             }
-            if (OUT && !wait_bar(CP, ph)) break;  // A B^T has read B
             bool ok = true;
-            for (int q = 0; q < 4; ++q) {
-                const int slot = q & 1, use = 2 * it + (q >> 1);
+#pragma unroll 1
+            for (int q = 0; q < STEPS; ++q) {
+                const int slot = q & 1, use = STEPS / 2 * it + (q >> 1);
                 if (use > 0 && !wait_bar(RF + slot, (uint32_t)(use - 1) & 1)) { ok = false; break; }
-                const Tile mid = tR(slot, 0), lo = tR(slot, 1);
-                const int r = 4 * yw + (lane >> 3), t = kQuarter * q + r;
-                const bool live = t < n;
-                const float f = live ? pw[REV ? t + 1 : n - 1 - t] : 0.f;
 #pragma unroll
-                for (int k = 0; k < D / 64; ++k) {
+                for (int i = 0; i < ITEMS; ++i) {
+                    const int m = yw + RO::kY * i, r = 4 * (m % ROWS4) + (lane >> 3), k = m / ROWS4, t = STEP * q + r;
+                    const bool in = t < n;
+                    const float f = in ? pw[REV ? t + 1 : n - 1 - t] : 0.f;
                     const uint32_t a = B.chunk(t, k, lane & 7);
                     uint32_t x[4], y[4], z[4];
                     ld_shared_v4(a, x[0], x[1], x[2], x[3]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float u = live ? __uint_as_float(x[i] << 16) * f : 0.f;
-                        const float v = live ? __uint_as_float(x[i] & 0xffff0000u) * f : 0.f;
-                        const __nv_bfloat162 h0 = __floats2bfloat162_rn(u, v);
-                        const float u1 = u - __low2float(h0), v1 = v - __high2float(h0);
-                        const __nv_bfloat162 h1 = __floats2bfloat162_rn(u1, v1);
-                        x[i] = *reinterpret_cast<const uint32_t*>(&h0);
-                        y[i] = *reinterpret_cast<const uint32_t*>(&h1);
-                        z[i] = pack_bf16(u1 - __low2float(h1), v1 - __high2float(h1));
+                    for (int j = 0; j < 4; ++j) {
+                        Pair u = mul2(unpack_bf16(in ? x[j] : 0u), {f, f});
+                        x[j] = pack_bf16(u.x, u.y);
+                        u = fma2(unpack_bf16(x[j]), {-1.f, -1.f}, u);
+                        y[j] = pack_bf16(u.x, u.y);
+                        if (TERMS == 3) {
+                            u = fma2(unpack_bf16(y[j]), {-1.f, -1.f}, u);
+                            z[j] = pack_bf16(u.x, u.y);
+                        }
                     }
                     st_shared_v4(a, x[0], x[1], x[2], x[3]);
-                    st_shared_v4(mid.chunk(r, k, lane & 7), y[0], y[1], y[2], y[3]);
-                    st_shared_v4(lo.chunk(r, k, lane & 7), z[0], z[1], z[2], z[3]);
+                    st_shared_v4(tR(slot, 0).chunk(r, k, lane & 7), y[0], y[1], y[2], y[3]);
+                    if (TERMS == 3) st_shared_v4(tR(slot, 1).chunk(r, k, lane & 7), z[0], z[1], z[2], z[3]);
                 }
                 fence_proxy_async();
                 arrive(KQ + slot);
             }
             if (!ok) break;
             if (holds) {
-                if (!wait_bar(CU, ph)) break;
-                tc_fence_after();
-                const float gn = pw[n];
-#pragma unroll
-                for (int k = 0; k < W / 32; ++k) {
-                    uint32_t r[32];
-                    tmem_ld32(tU + lane_off + scol + 32 * k, r);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) S[32 * k + j] = fmaf(gn, S[32 * k + j], __uint_as_float(r[j]));
-                }
-                tc_fence_before();
-                arrive(DU);
-                if (OUT && it + 1 < nchunks) {
-                    if (!wait_bar(CS, ph)) break;  // A S has read the copy
-                    copy_state();
+                if (OUT) {
+                    if (!update(it)) break;
+                    if (it + 1 < nchunks) {
+                        if (!wait_bar(CS, ph)) break;  // A S has read the copy
+                        copy_state();
+                    }
+                } else if (it > 0 && !update(it - 1)) {  // the previous chunk's, beside this one's products
+                    break;
                 }
             }
         }
+        if (!OUT && holds && it == nchunks && nchunks > 0) update(nchunks - 1);
         // (a wait that ran out leaves here too: the status word says so)
         float* dst = nullptr;
         long long step = 1;
         if (!OUT) {
-            dst = p.rec + ((size_t)bh * p.nseg + w + 1) * R + (size_t)row * p.dc;
-        } else if (p.s_out && w == p.nseg - 1) {
+            dst = p.rec + ((size_t)bh * (p.nseg + 1) + w + 1) * R + (size_t)row * p.dc;
+        } else if (p.s_out && p.nseg == 1) {
             dst = p.s_out + (size_t)bh * R + row * p.out_r;
             step = p.out_c;
         }
@@ -462,15 +531,23 @@ bool tile_map(CUtensorMap* m, const void* base, const long long (&s)[3], int B, 
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool REV, bool OUT>
+template <int D, bool REV, bool OUT, int TERMS>
 cudaError_t launch(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mc, const LinWalk& w,
                    cudaStream_t s) {
-    auto kernel = lin_tc_kernel<D, REV, OUT>;
-    const int bytes = (int)TcLayout<D, OUT>::kBytes + 1024;
+    auto kernel = lin_tc_kernel<D, REV, OUT, TERMS>;
+    const int bytes = (int)TcLayout<D, OUT, TERMS>::kBytes + 1024;
     if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) return e;
-    kernel<<<dim3(OUT ? w.nseg : w.nseg - 1, w.B * w.H), TcRoles<D, OUT>::kThreads, bytes, s>>>(ma, mb, mc, w);
+    kernel<<<dim3(OUT ? w.nseg : lin_state_segments(w), w.B * w.H), TcRoles<D, OUT>::kThreads, bytes, s>>>(ma, mb, mc, w);
     note_launches(1);
     return cudaGetLastError();
+}
+
+// states: three terms.  outputs: three where the walk itself leaves the last state.
+template <int D, bool REV>
+cudaError_t pick(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mc, const LinWalk& w, bool states,
+                 cudaStream_t s) {
+    if (states) return launch<D, REV, false, 3>(ma, mb, mc, w, s);
+    return w.s_out && w.nseg == 1 ? launch<D, REV, true, 3>(ma, mb, mc, w, s) : launch<D, REV, true, 2>(ma, mb, mc, w, s);
 }
 
 }  // namespace
@@ -486,13 +563,8 @@ cudaError_t launch_lin_tc(const LinWalk& w, bool states, cudaStream_t s) {
     if (!tile_map(&mb, w.b, w.sb, w.B, w.H, w.T, w.da) || !tile_map(&mc, w.c, w.sc, w.B, w.H, w.T, w.dc) ||
         (!states && !tile_map(&ma, w.a, w.sa, w.B, w.H, w.T, w.da)))
         return cudaErrorInvalidValue;
-    const bool small = w.da <= 64 && w.dc <= 64;
-    if (states) {
-        if (small) return w.rev ? launch<64, true, false>(ma, mb, mc, w, s) : launch<64, false, false>(ma, mb, mc, w, s);
-        return w.rev ? launch<128, true, false>(ma, mb, mc, w, s) : launch<128, false, false>(ma, mb, mc, w, s);
-    }
-    if (small) return w.rev ? launch<64, true, true>(ma, mb, mc, w, s) : launch<64, false, true>(ma, mb, mc, w, s);
-    return w.rev ? launch<128, true, true>(ma, mb, mc, w, s) : launch<128, false, true>(ma, mb, mc, w, s);
+    if (w.da <= 64 && w.dc <= 64) return w.rev ? pick<64, true>(ma, mb, mc, w, states, s) : pick<64, false>(ma, mb, mc, w, states, s);
+    return w.rev ? pick<128, true>(ma, mb, mc, w, states, s) : pick<128, false>(ma, mb, mc, w, states, s);
 }
 
 }  // namespace hla2
