@@ -17,12 +17,14 @@
 // accumulator costs it bits.  B~ is three bf16 terms (24 bits) where S leaves
 // the walk in fp32, two (16 bits, far below the copy's 8) where only the copy is used.
 //
-// Roles.  X warps (4): P from tensor memory, decayed, masked and packed back;
-// o_i from O1 and O2, through shared memory, to global memory.  Y warps (8): B~
-// in steps of 32 tokens (first terms in place of B, the others in a ring of two
-// slots), then S and its bf16 copy.  One warp issues the products, one the loads.
-// Four warps to a scheduler leave 128 registers to a thread, which S (64 of
-// them) needs: local memory would go to L2, shared memory takes all of L1.
+// Roles.  X warps (4): P from tensor memory, decayed, masked and packed back.
+// O warps (4): o_i from O1 and O2, through shared memory, to global memory.  Y
+// warps (16): B~ in steps of 16 to 64 tokens (first terms in place of B, the others in a
+// ring of two slots), then S and its bf16 copy.  One warp issues the products, one the loads.  Nothing may spill: local
+// memory would go to L2, shared memory takes all of L1.  The issuer orders a
+// chunk's products so that what the next chunk waits for comes early: A S (A's
+// tile is loaded again), half of U, P~ C, the rest of U and the next chunk's
+// scores, which are there when Y has updated S.
 #include "hla2_linear.cuh"
 #include "hla2_tc_common.cuh"
 
@@ -46,6 +48,15 @@ __device__ __forceinline__ void tmem_store16(uint32_t taddr, const uint32_t (&r)
         ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
           "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
+}
+
+// 16 columns of this thread's lane
+__device__ __forceinline__ void tmem_load16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
 }
 
 // (a, b) op (c, d), two fp32 operations to an instruction
@@ -75,6 +86,43 @@ __device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
 __device__ __forceinline__ Pair unpack_bf16(uint32_t w) { return {__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)}; }
 __device__ __forceinline__ Pair at(const uint32_t* r) { return {__uint_as_float(r[0]), __uint_as_float(r[1])}; }
 
+// What the issuing warp does, all lanes together: the values stay uniform, so
+// that descriptors are formed and products issued without a detour through
+// each lane's registers (one lane alone took 140 clocks a product).
+__device__ __forceinline__ void mma_warp(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n elect.sync _|q, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n"
+        ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_warp_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n elect.sync _|q, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
+        ::"r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void commit_warp(uint32_t mbar) {
+    asm volatile(
+        "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(mbar)
+        : "memory");
+}
+// A number of tries in a row (each may suspend the warp for a while)
+__device__ __forceinline__ bool mbar_tries(uint32_t a, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p, r;\n .reg .u32 n;\n mov.u32 n, 0;\n"
+        "AGAIN:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra DONE;\n"
+        " add.u32 n, n, 1;\n setp.lt.u32 r, n, 64;\n @r bra AGAIN;\n"
+        "DONE:\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(a), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // Shared memory.  Tiles of A: NA, of B and C: NB; the ring's slots hold the
 // second (and third) terms of STEP tokens of B~; the stage a group of 64 output
 // columns of each X warp.  At D = 64 the products' A operand still has 128
@@ -82,7 +130,8 @@ __device__ __forceinline__ Pair at(const uint32_t* r) { return {__uint_as_float(
 // allocation, and nobody reads their results.
 template <int D, bool OUT, int TERMS>
 struct TcLayout {
-    static constexpr int STEP = D == 128 && OUT && TERMS == 3 ? 16 : 32;
+    static constexpr int STEP = D == 64 ? 64 : OUT && TERMS == 3 ? 16 : 32;
+    static constexpr int PER = STEP / 4 * (D / 64);  // items of 4 tokens by 64 channels in a step, one to a warp
     static constexpr int NA = OUT ? (D == 64 ? 2 : 1) : 0, NB = OUT ? (D == 64 ? 3 : 2) : 3;
     static constexpr uint32_t kTile = kL * D * 2, kPart = STEP * D * 2;
     static constexpr uint32_t A = 0, B = NA * kTile, C = B + NB * kTile, ring = C + NB * kTile;
@@ -92,9 +141,11 @@ struct TcLayout {
 
 template <int D, bool OUT>
 struct TcRoles {
-    static constexpr int kX = OUT ? 4 : 0, kY = 8;
-    static constexpr int kThreads = (kX + kY + 2) * 32;
-    static constexpr int kState = D / 32 * 2;  // Y warps that hold rows of the state
+    static constexpr int kX = OUT ? 4 : 0, kO = kX, kY = 16;
+    static constexpr int kY0 = kX + kO, kIssuer = kY0 + kY, kLoader = kIssuer + 1;
+    static constexpr int kThreads = (kLoader + 1) * 32;
+    static constexpr int kParts = kY / 4;           // Y warps to 32 rows of the state
+    static constexpr int kState = D / 32 * kParts;  // Y warps that hold rows of the state
 };
 
 template <int D, bool REV, bool OUT, int TERMS>
@@ -103,12 +154,12 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
               const __grid_constant__ CUtensorMap mC, const LinWalk p) {
     using LY = TcLayout<D, OUT, TERMS>;
     using RO = TcRoles<D, OUT>;
-    constexpr int NA = LY::NA, NA1 = NA ? NA : 1, NB = LY::NB, STEP = LY::STEP, STEPS = kL / STEP;
+    constexpr int NA = LY::NA, NA1 = NA ? NA : 1, NB = LY::NB, STEP = LY::STEP, STEPS = kL / STEP, PER = LY::PER;
     extern __shared__ __align__(1024) unsigned char dsm_raw[];
-    // loads | buffers free | P ready, packed | ring filled, free | U ready, drained | S copy ready, read |
-    // O ready, drained | last wait
-    enum { LA, LB = LA + NA, LC = LB + NB, FA = LC + NB, FB = FA + NA, FC = FB + NB, CP = FC + NB, DP, KQ, RF = KQ + 2,
-           CU = RF + 2, DU = CU + 2, DS, CS, CO, DO, FIN, NBAR };
+    // loads | A read (O2 = A S done) | a chunk's last product done (B and C free, U ready) | P ready, packed |
+    // ring filled, free | U drained | S copy ready | O ready (P's columns free), drained | last wait
+    enum { LA, LB = LA + NA, LC = LB + NB, FA = LC + NB, FB = FA + NA1, CP = FB + NB, DP, KQ, RF = KQ + 2, DU = RF + 2,
+           DS = DU + 2, CO, DO, FIN, NBAR };
     __shared__ __align__(8) unsigned long long bars[NBAR];
     __shared__ __align__(16) float pw[kL + 4];  // g^0 .. g^128
     __shared__ __align__(16) float down[32];    // g^31 .. g^0
@@ -116,14 +167,14 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
     __shared__ volatile int abort_flag;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const bool xwarp = warp < RO::kX, ywarp = !xwarp && warp < RO::kX + RO::kY;
-    const bool issuer = warp == RO::kX + RO::kY, loader = warp == RO::kX + RO::kY + 1;
+    const bool xwarp = warp < RO::kX, owarp = !xwarp && warp < RO::kY0, ywarp = warp >= RO::kY0 && warp < RO::kIssuer;
+    const bool issuer = warp == RO::kIssuer, loader = warp == RO::kLoader;
     const int quarter = warp & 3, row = quarter * 32 + lane;  // lanes of tensor memory
     const int bh = blockIdx.y, w = blockIdx.x, seg = REV ? p.nseg - 1 - w : w;
     const int b = bh / p.H, h = bh % p.H;
     const int len = length_of(p, b);
     const int c0 = seg * p.seglen, c1 = min(min(c0 + p.seglen, p.nchunk), (len + kL - 1) / kL);
-    const int nchunks = max(0, c1 - c0);
+    int nchunks = max(0, c1 - c0);
     auto chunk_of = [&](int it) { return REV ? c1 - 1 - it : c0 + it; };
     auto tokens_of = [&](int it) { return min(kL, len - chunk_of(it) * kL); };
 
@@ -142,8 +193,8 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
         for (int i = 0; i < NBAR; ++i) {
             uint32_t count = 1;
             if (i == DP || i == DO) count = OUT ? RO::kX : 1;
-            if (i == KQ || i == KQ + 1) count = RO::kY;
-            if (i == DU || i == DS) count = RO::kState;
+            if (i == KQ || i == KQ + 1) count = PER;
+            if (i == DU || i == DU + 1 || i == DS) count = RO::kState;
             mbar_init(bar(i), count);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -162,7 +213,12 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = tmem_slot;
+    // all of tensor memory was taken, so it begins at column 0; anything else is reported and nothing is done
+    constexpr uint32_t tmem = 0;
+    if (tmem_slot != tmem) {
+        if (tid == 0) atomicExch(p.status, (int)kDevTmemAlloc);
+        nchunks = 0;
+    }
     // outputs: P | O1 | O2 | U;  states: U twice, by turns
     const uint32_t tP = tmem, tO1 = tmem + 128, tO2 = tmem + 128 + D;
     auto tU = [&](int it) -> uint32_t { return OUT ? tmem + 128 + 2 * D : tmem + 128 * (it & 1); };
@@ -170,7 +226,6 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
 
     auto wait_bar = [&](int i, uint32_t parity) -> bool {
         const uint32_t a = bar(i);
-        if (abort_flag) return false;
         if (mbar_try(a, parity)) return true;
         const unsigned long long t0 = globaltimer();
         while (!mbar_try(a, parity)) {
@@ -193,63 +248,105 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
     constexpr uint32_t iBC = idesc_bf16(128, D, true, true);      // B~^T C: both along the tokens
 
     if (issuer) {
-        if (lane == 0) {
-            // packed pairs of tokens 16 ks.. of P~ (each group of 32 columns packed into its first 16)
-            auto packed = [](int ks) -> uint32_t { return (uint32_t)(32 * (ks / 2) + 8 * (ks % 2)); };
-            for (int it = 0; it < nchunks; ++it) {
-                const uint32_t ph = it & 1, before = ph ^ 1;
-                const int sb = it % NB;
-                const uint32_t kb = (uint32_t)(it / NB) & 1;
-                const Tile B = tB(it), C = tC(it);
-                if (OUT) {
-                    // P, once the previous chunk's P~ C has read its columns
-                    if (it > 0 && !wait_bar(CO, before)) break;
-                    if (!wait_bar(LA + it % NA1, (uint32_t)(it / NA1) & 1) || !wait_bar(LB + sb, kb)) break;
-                    tc_fence_after();
-                    const Tile A = tA(it);
-                    for (int ks = 0; ks < D / 16; ++ks) mma_bf16(tP, A.kmaj(ks), B.kmaj(ks), iPP, ks > 0);
-                    mma_commit(bar(CP));
-                }
-                // U, a step of the tokens at a time as Y fills the ring, once its columns have been drained
-                if (!wait_bar(LC + sb, kb)) break;
-                if (OUT ? it > 0 && !wait_bar(DU, before) : it > 1 && !wait_bar(DU, ph)) break;
-                bool ok = true;
-                for (int q = 0; q < STEPS && ok; ++q) {
-                    if (OUT && q == STEPS / 2) {
-                        // O2 = A S beside Y's second half
-                        if (!wait_bar(DS, ph) || (it > 0 && !wait_bar(DO, before))) { ok = false; break; }
-                        tc_fence_after();
-                        const Tile A = tA(it);
-                        for (int ks = 0; ks < D / 16; ++ks) mma_bf16(tO2, A.kmaj(ks), tS.mnmaj(ks), iAS, ks > 0);
-                        mma_commit(bar(CS));
-                        mma_commit(bar(FA + it % NA1));
+        // as wait_bar, the whole warp with one answer
+        auto wait_warp = [&](int i, uint32_t parity) -> bool {
+            const uint32_t a = bar(i);
+            bool ok = mbar_tries(a, parity);
+            if (!__all_sync(0xffffffffu, ok)) {
+                const unsigned long long t0 = globaltimer();
+                while (!ok && !abort_flag) {
+                    ok = mbar_tries(a, parity);
+                    if (!ok && globaltimer() - t0 > kWaitNs) {
+                        abort_flag = 1;
+                        atomicExch(p.status, (int)kDevWaitTimeout);
                     }
-                    const int slot = q & 1;
-                    if (!wait_bar(KQ + slot, (uint32_t)((STEPS / 2 * it + (q >> 1)) & 1))) { ok = false; break; }
-                    tc_fence_after();
-                    const uint32_t u = tU(it);
-                    for (int ks = 0; ks < STEP / 16; ++ks) {
-                        const int kk = q * (STEP / 16) + ks;
-                        const uint64_t c = C.mnmaj(kk);
-                        mma_bf16(u, B.mnmaj(kk), c, iBC, kk > 0);
-#pragma unroll
-                        for (int t = 0; t < TERMS - 1; ++t) mma_bf16(u, tR(slot, t).mnmaj(ks), c, iBC, 1);
-                    }
-                    mma_commit(bar(RF + slot));
                 }
-                if (!ok) break;
-                mma_commit(bar(CU + (OUT ? 0 : it & 1)));
-                mma_commit(bar(FB + sb));
-                if (OUT) {
-                    if (!wait_bar(DP, ph)) break;
-                    tc_fence_after();
-                    for (int ks = 0; ks < kL / 16; ++ks) mma_bf16_tmem_a(tO1, tP + packed(ks), C.mnmaj(ks), iAS, ks > 0);
-                    mma_commit(bar(CO));
-                }
-                mma_commit(bar(FC + sb));
+                __syncwarp();
             }
-            if (!mma_wait_all(bar(FIN))) atomicExch(p.status, (int)kDevWaitTimeout);
+            return __all_sync(0xffffffffu, ok) != 0;
+        };
+        // packed pairs of tokens 16 ks.. of P~ (each group of 32 columns packed into its first 16)
+        auto packed = [](int ks) -> uint32_t { return (uint32_t)(32 * (ks / 2) + 8 * (ks % 2)); };
+        // a tile's descriptors: its first one, then steps along the channels (16 of them) or the rows (16)
+        constexpr uint32_t kBlock = kL * 128u;
+        auto along = [](uint64_t first, int ks) { return first + (uint64_t)((((ks >> 2) * kBlock) + (ks & 3) * 32u) >> 4); };
+        auto down_rows = [](uint64_t first, int ks) { return first + (uint64_t)(ks * 128); };
+        int sa = 0, sb = 0;         // stages of A, of B and C
+        uint32_t pa = 0, pb = 0;    // and their phases
+        const uint64_t dS = sdesc(dsm + LY::S, D * 128u, 1024u);
+        auto scores = [&](int it) -> bool {  // P of chunk `it`, once P~ C of the one before has read its columns
+            if (it > 0 && !wait_warp(CO, (uint32_t)(it - 1) & 1)) return false;
+            if (!wait_warp(LA + sa, pa) || !wait_warp(LB + sb, pb)) return false;
+            tc_fence_after();
+            const uint64_t dA = sdesc(dsm + LY::A + (uint32_t)sa * LY::kTile, 16u, 1024u);
+            const uint64_t dB = sdesc(dsm + LY::B + (uint32_t)sb * LY::kTile, 16u, 1024u);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) mma_warp(tP, along(dA, ks), along(dB, ks), iPP, ks > 0);
+            commit_warp(bar(CP));
+            return true;
+        };
+        bool ok = !OUT || nchunks == 0 || scores(0);
+        for (int it = 0; it < nchunks && ok; ++it) {
+            const uint32_t ph = it & 1, before = ph ^ 1;
+            const uint64_t dA = sdesc(dsm + LY::A + (uint32_t)sa * LY::kTile, 16u, 1024u);
+            const uint64_t dB = sdesc(dsm + LY::B + (uint32_t)sb * LY::kTile, kBlock, 1024u);
+            const uint64_t dC = sdesc(dsm + LY::C + (uint32_t)sb * LY::kTile, kBlock, 1024u);
+            ok = false;  // until the chunk's last product is issued
+            // O2 = A S first: A's tile is the next one to be filled again
+            if (OUT) {
+                if (!wait_warp(DS, ph) || (it > 0 && !wait_warp(DO, before))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) mma_warp(tO2, along(dA, ks), down_rows(dS, ks), iAS, ks > 0);
+                commit_warp(bar(FA + sa));
+            }
+            // U, a step of the tokens at a time as Y fills the ring, once its columns have been drained
+            if (!wait_warp(LC + sb, pb)) break;
+            if (OUT ? it > 0 && !wait_warp(DU, before)
+                    : it > 1 && !wait_warp(DU + (it & 1), (uint32_t)((it >> 1) - 1) & 1)) break;
+            const uint32_t u = tU(it);
+            bool all = true;
+#pragma unroll
+            for (int q = 0; q < STEPS; ++q) {
+                const int slot = q & 1;
+                all = all && wait_warp(KQ + slot, (uint32_t)((STEPS / 2 * it + q / 2) & 1));
+                if (!all) break;
+                tc_fence_after();
+#pragma unroll
+                for (int ks = 0; ks < STEP / 16; ++ks) {
+                    const int kk = q * (STEP / 16) + ks;
+                    mma_warp(u, down_rows(dB, kk), down_rows(dC, kk), iBC, kk > 0);
+#pragma unroll
+                    for (int t = 0; t < TERMS - 1; ++t)
+                        mma_warp(u, down_rows(sdesc(dsm + LY::ring + (uint32_t)(slot * (TERMS - 1) + t) * LY::kPart, STEP * 128u, 1024u), ks),
+                                 down_rows(dC, kk), iBC, 1);
+                }
+                commit_warp(bar(RF + slot));
+                if (OUT && q == STEPS / 2 - 1) {
+                    // O1 = P~ C, packed by X meanwhile
+                    all = wait_warp(DP, ph);
+                    if (!all) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int ks = 0; ks < kL / 16; ++ks) mma_warp_tmem_a(tO1, tP + packed(ks), down_rows(dC, ks), iAS, ks > 0);
+                    commit_warp(bar(CO));
+                }
+            }
+            if (!all) break;
+            commit_warp(bar(FB + sb));
+            if (++sb == NB) { sb = 0; pb ^= 1; }
+            if (++sa >= NA1) { sa = 0; pa ^= 1; }
+            ok = !OUT || it + 1 == nchunks || scores(it + 1);
         }
+        // no product may still run when the CTA gives its memory back, whatever ended the walk
+        commit_warp(bar(FIN));
+        const unsigned long long t0 = globaltimer();
+        while (!mbar_tries(bar(FIN), 0))
+            if (globaltimer() - t0 > kWaitNs) {
+                atomicExch(p.status, (int)kDevWaitTimeout);
+                break;
+            }
+        __syncwarp();
     } else if (loader) {
         if (lane == 0) {
             LoadLedger<NA + 2 * NB> loads(bar(0));
@@ -264,7 +361,6 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
                 const int sb = it % NB, ub = it / NB;
                 if (ub > 0 && !wait_bar(FB + sb, (uint32_t)(ub - 1) & 1)) break;
                 load(LB + sb, &mB, tB(it), it);
-                if (ub > 0 && !wait_bar(FC + sb, (uint32_t)(ub - 1) & 1)) break;
                 load(LC + sb, &mC, tC(it), it);
                 if (OUT) {
                     const int sa = it % NA1, ua = it / NA1;
@@ -275,8 +371,6 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
             if (!loads.settle()) atomicExch(p.status, (int)kDevWaitTimeout);
         }
     } else if (OUT && xwarp) {
-        bf16* const out = static_cast<bf16*>(p.o) + b * p.so[0] + h * p.so[1];
-        const uint32_t stage = dsm + LY::stage + (uint32_t)warp * 4096u;
         for (int it = 0; it < nchunks; ++it) {
             const uint32_t ph = it & 1;
             const int n = tokens_of(it);
@@ -329,51 +423,62 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
             tmem_st_wait();
             tc_fence_before();
             arrive(DP);
+        }
+    } else if (OUT && owarp) {
+        bf16* const out = static_cast<bf16*>(p.o) + b * p.so[0] + h * p.so[1];
+        const uint32_t stage = dsm + LY::stage + (uint32_t)quarter * 4096u;
+        for (int it = 0; it < nchunks; ++it) {
+            const uint32_t ph = it & 1;
+            const int n = tokens_of(it);
             if (!wait_bar(CO, ph)) break;
             tc_fence_after();
             const float f = row < n ? pw[REV ? n - 1 - row : row + 1] : 0.f;
-            const long long t0 = (long long)chunk_of(it) * kL + quarter * 32;
+            const int t0 = chunk_of(it) * kL + quarter * 32 + (lane >> 3);
+            bf16* const dst = out + (long long)t0 * p.so[2] + (lane & 7) * 8;
+            const int left = n - quarter * 32 - (lane >> 3);  // this lane's rows 0, 4, .. below it
 #pragma unroll
             for (int g = 0; g < D / 64; ++g) {
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int col = 64 * g + 32 * k;
-                    uint32_t r1[32], r2[32];
-                    tmem_ld32(tO1 + lane_off + col, r1);
-                    tmem_ld32(tO2 + lane_off + col, r2);
+                for (int k = 0; k < 4; ++k) {
+                    const int col = 64 * g + 16 * k;
+                    uint32_t r1[16], r2[16];
+                    tmem_load16(tO1 + lane_off + col, r1);
+                    tmem_load16(tO2 + lane_off + col, r2);
                     tmem_ld_wait();
-                    if (col == D - 32) {
+                    if (col == D - 16) {
                         tc_fence_before();
                         arrive(DO);
                     }
 #pragma unroll
-                    for (int j = 0; j < 32; j += 8) {
+                    for (int j = 0; j < 16; j += 8) {
                         uint32_t o[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const Pair v = fma2({f, f}, at(r2 + j + 2 * i), at(r1 + j + 2 * i));
                             o[i] = pack_bf16(v.x, v.y);
                         }
-                        st_shared_v4(stage + (uint32_t)lane * 128u + (uint32_t)(((4 * k + j / 8) ^ (lane & 7)) << 4), o[0],
+                        st_shared_v4(stage + (uint32_t)lane * 128u + (uint32_t)(((2 * k + j / 8) ^ (lane & 7)) << 4), o[0],
                                      o[1], o[2], o[3]);
                     }
                 }
                 // whole lines of 128 bytes to global memory, four rows at a time
                 __syncwarp();
-                const int c = 64 * g + (lane & 7) * 8;
+                bf16* to = dst + 64 * g;
+                const bool wide = 64 * g + (lane & 7) * 8 < p.dc;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int r = 4 * i + (lane >> 3);
                     uint4 v;
                     ld_shared_v4(stage + (uint32_t)r * 128u + (uint32_t)(((lane & 7) ^ (r & 7)) << 4), v.x, v.y, v.z, v.w);
-                    if (quarter * 32 + r < n && c < p.dc) *reinterpret_cast<uint4*>(out + (t0 + r) * p.so[2] + c) = v;
+                    if (wide && 4 * i < left) *reinterpret_cast<uint4*>(to) = v;
+                    to += 4 * p.so[2];
                 }
                 __syncwarp();
             }
         }
     } else if (ywarp) {
-        constexpr int W = D / 2;  // columns of S to a thread
-        const int yw = warp - RO::kX, part = yw >> 2;
+        constexpr int W = D / RO::kParts;  // columns of S to a thread
+        const int yw = warp - RO::kY0, part = yw >> 2;
         const bool holds = quarter < D / 32;
         const int scol = part * W;
         const size_t R = (size_t)p.da * p.dc;
@@ -406,28 +511,30 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
             arrive(DS);
         };
         auto update = [&](int it) -> bool {  // S of chunk it's end
-            if (!wait_bar(CU + (OUT ? 0 : it & 1), OUT ? (uint32_t)it & 1 : (uint32_t)(it >> 1) & 1)) return false;
+            if (!wait_bar(FB + it % NB, (uint32_t)(it / NB) & 1)) return false;
             tc_fence_after();
             const float gn = pw[tokens_of(it)];
 #pragma unroll
-            for (int k = 0; k < W / 32; ++k) {
-                uint32_t r[32];
-                tmem_ld32(tU(it) + lane_off + scol + 32 * k, r);
+            for (int k = 0; k < W / 16; ++k) {
+                uint32_t r[16];
+                tmem_load16(tU(it) + lane_off + scol + 16 * k, r);
                 tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 32; j += 2) {
-                    const Pair v = fma2({gn, gn}, {S[32 * k + j], S[32 * k + j + 1]}, at(r + j));
-                    S[32 * k + j] = v.x;
-                    S[32 * k + j + 1] = v.y;
+                for (int j = 0; j < 16; j += 2) {
+                    const Pair v = fma2({gn, gn}, {S[16 * k + j], S[16 * k + j + 1]}, at(r + j));
+                    S[16 * k + j] = v.x;
+                    S[16 * k + j + 1] = v.y;
                 }
             }
             tc_fence_before();
-            arrive(DU);
+            arrive(DU + (OUT ? 0 : it & 1));
             return true;
         };
         if (OUT && holds && nchunks > 0) copy_state();
-        // the thread's row of four, and its first column step of a tile's row
-        constexpr int ROWS4 = STEP / 4, ITEMS = ROWS4 * (D / 64) / RO::kY;
+        // an item of 4 tokens by 64 channels of a step; where a step has fewer items than there are warps, half
+        // the warps take every other step
+        constexpr int GROUPS = RO::kY / PER;
+        const int group = yw / PER, item = yw % PER, irow = 4 * (item % (STEP / 4)) + (lane >> 3), icol = item / (STEP / 4);
         int it = 0;
         for (; it < nchunks; ++it) {
             const uint32_t ph = it & 1;
@@ -438,38 +545,35 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
             if (n < kL) {
                 // rows of C behind the end: zeros, whatever they hold
                 if (!wait_bar(LC + sb, kb)) break;
-                for (int i = (n << 3) + yw * 32 + lane; i < kL * 8; i += RO::kY * 32)
+                // (by each group of warps, so that the arrivals of either say so)
+                for (int i = (n << 3) + item * 32 + lane; i < kL * 8; i += PER * 32)
 #pragma unroll
                     for (int k = 0; k < D / 64; ++k) st_shared_v4(C.chunk(i >> 3, k, i & 7), 0u, 0u, 0u, 0u);
             }
             bool ok = true;
 #pragma unroll 1
-            for (int q = 0; q < STEPS; ++q) {
-                const int slot = q & 1, use = STEPS / 2 * it + (q >> 1);
-                if (use > 0 && !wait_bar(RF + slot, (uint32_t)(use - 1) & 1)) { ok = false; break; }
+            for (int q = group; q < STEPS; q += GROUPS) {
+                const int slot = q & 1, use = STEPS / 2 * it + (q >> 1), t = STEP * q + irow;
+                const bool in = t < n;
+                const float f = in ? pw[REV ? t + 1 : n - 1 - t] : 0.f;
+                const uint32_t a = B.chunk(t, icol, lane & 7);
+                uint32_t x[4], y[4], z[4];
+                ld_shared_v4(a, x[0], x[1], x[2], x[3]);
 #pragma unroll
-                for (int i = 0; i < ITEMS; ++i) {
-                    const int m = yw + RO::kY * i, r = 4 * (m % ROWS4) + (lane >> 3), k = m / ROWS4, t = STEP * q + r;
-                    const bool in = t < n;
-                    const float f = in ? pw[REV ? t + 1 : n - 1 - t] : 0.f;
-                    const uint32_t a = B.chunk(t, k, lane & 7);
-                    uint32_t x[4], y[4], z[4];
-                    ld_shared_v4(a, x[0], x[1], x[2], x[3]);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        Pair u = mul2(unpack_bf16(in ? x[j] : 0u), {f, f});
-                        x[j] = pack_bf16(u.x, u.y);
-                        u = fma2(unpack_bf16(x[j]), {-1.f, -1.f}, u);
-                        y[j] = pack_bf16(u.x, u.y);
-                        if (TERMS == 3) {
-                            u = fma2(unpack_bf16(y[j]), {-1.f, -1.f}, u);
-                            z[j] = pack_bf16(u.x, u.y);
-                        }
+                for (int j = 0; j < 4; ++j) {
+                    Pair u = mul2(unpack_bf16(in ? x[j] : 0u), {f, f});
+                    x[j] = pack_bf16(u.x, u.y);
+                    u = fma2(unpack_bf16(x[j]), {-1.f, -1.f}, u);
+                    y[j] = pack_bf16(u.x, u.y);
+                    if (TERMS == 3) {
+                        u = fma2(unpack_bf16(y[j]), {-1.f, -1.f}, u);
+                        z[j] = pack_bf16(u.x, u.y);
                     }
-                    st_shared_v4(a, x[0], x[1], x[2], x[3]);
-                    st_shared_v4(tR(slot, 0).chunk(r, k, lane & 7), y[0], y[1], y[2], y[3]);
-                    if (TERMS == 3) st_shared_v4(tR(slot, 1).chunk(r, k, lane & 7), z[0], z[1], z[2], z[3]);
                 }
+                st_shared_v4(a, x[0], x[1], x[2], x[3]);
+                if (use > 0 && !wait_bar(RF + slot, (uint32_t)(use - 1) & 1)) { ok = false; break; }
+                st_shared_v4(tR(slot, 0).chunk(irow, icol, lane & 7), y[0], y[1], y[2], y[3]);
+                if (TERMS == 3) st_shared_v4(tR(slot, 1).chunk(irow, icol, lane & 7), z[0], z[1], z[2], z[3]);
                 fence_proxy_async();
                 arrive(KQ + slot);
             }
@@ -478,8 +582,7 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
                 if (OUT) {
                     if (!update(it)) break;
                     if (it + 1 < nchunks) {
-                        if (!wait_bar(CS, ph)) break;  // A S has read the copy
-                        copy_state();
+                        copy_state();  // (A S, issued before U, has read the copy)
                     }
                 } else if (it > 0 && !update(it - 1)) {  // the previous chunk's, beside this one's products
                     break;
@@ -506,7 +609,7 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
     __syncthreads();
     tc_fence_after();
     if (warp == 0)
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_slot), "r"(kTmemCols) : "memory");
 }
 
 // ------------------------------------------------------------------ host ----
