@@ -41,13 +41,11 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
-// 16 packed words of this thread's lane
-__device__ __forceinline__ void tmem_store16(uint32_t taddr, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
-        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-          "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
+// 8 packed words of this thread's lane
+__device__ __forceinline__ void tmem_store8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
 }
 
 // 16 columns of this thread's lane
@@ -162,7 +160,7 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
            DS = DU + 2, CO, DO, FIN, NBAR };
     __shared__ __align__(8) unsigned long long bars[NBAR];
     __shared__ __align__(16) float pw[kL + 4];  // g^0 .. g^128
-    __shared__ __align__(16) float down[32];    // g^31 .. g^0
+    __shared__ __align__(16) float down[16];    // g^15 .. g^0
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort_flag;
 
@@ -202,7 +200,7 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
     if (tid <= kL) {
         const float f = (float)power((double)__ldg(p.gamma + h), tid);
         pw[tid] = f;
-        if (tid < 32) down[31 - tid] = f;
+        if (tid < 16) down[15 - tid] = f;
     }
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
@@ -265,8 +263,6 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
             }
             return __all_sync(0xffffffffu, ok) != 0;
         };
-        // packed pairs of tokens 16 ks.. of P~ (each group of 32 columns packed into its first 16)
-        auto packed = [](int ks) -> uint32_t { return (uint32_t)(32 * (ks / 2) + 8 * (ks % 2)); };
         // a tile's descriptors: its first one, then steps along the channels (16 of them) or the rows (16)
         constexpr uint32_t kBlock = kL * 128u;
         auto along = [](uint64_t first, int ks) { return first + (uint64_t)((((ks >> 2) * kBlock) + (ks & 3) * 32u) >> 4); };
@@ -306,7 +302,7 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
                     : it > 1 && !wait_warp(DU + (it & 1), (uint32_t)((it >> 1) - 1) & 1)) break;
             const uint32_t u = tU(it);
             bool all = true;
-#pragma unroll
+#pragma unroll 1
             for (int q = 0; q < STEPS; ++q) {
                 const int slot = q & 1;
                 all = all && wait_warp(KQ + slot, (uint32_t)((STEPS / 2 * it + q / 2) & 1));
@@ -328,7 +324,7 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
                     if (!all) break;
                     tc_fence_after();
 #pragma unroll
-                    for (int ks = 0; ks < kL / 16; ++ks) mma_warp_tmem_a(tO1, tP + packed(ks), down_rows(dC, ks), iAS, ks > 0);
+                    for (int ks = 0; ks < kL / 16; ++ks) mma_warp_tmem_a(tO1, tP + 16 * ks, down_rows(dC, ks), iAS, ks > 0);
                     commit_warp(bar(CO));
                 }
             }
@@ -376,32 +372,30 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
             const int n = tokens_of(it);
             if (!wait_bar(CP, ph)) break;
             tc_fence_after();
+#pragma unroll 1
+            for (int col = 0; col < kL; col += 16) {  // each 16 columns packed into their first 8
+                const int gap = REV ? col - row : row - col - 15;  // the row's distance to the group's near edge
+                const int nearest = REV ? col - quarter * 32 - 16 : quarter * 32 - col;  // -16 or 0 on the diagonal
+                uint32_t hi[8];
+                if (nearest < -16 || (REV && col >= n)) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int col = 32 * k;
-                uint32_t hi[16];
-                const bool none = REV ? col < quarter * 32 : col > quarter * 32;
-                if (none) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) hi[j] = 0u;
+                    for (int j = 0; j < 8; ++j) hi[j] = 0u;
                 } else {
-                    uint32_t r[32];
-                    tmem_ld32(tP + lane_off + col, r);
+                    uint32_t r[16];
+                    tmem_load16(tP + lane_off + col, r);
                     tmem_ld_wait();
-                    if (col == quarter * 32) {
+                    if (nearest <= 0) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const int far = REV ? j - lane : lane - j;
-                            const bool in = far >= 0 && (!REV || col + j < n);
-                            r[j] = in ? __float_as_uint(__uint_as_float(r[j]) * pw[in ? far : 0]) : 0u;
+                        for (int j = 0; j < 16; ++j) {
+                            const int far = REV ? gap + j : gap + 15 - j;
+                            r[j] = far >= 0 ? __float_as_uint(__uint_as_float(r[j]) * pw[max(far, 0)]) : 0u;
                         }
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) hi[j] = pack_bf16(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+                        for (int j = 0; j < 8; ++j) hi[j] = pack_bf16(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
                     } else {
-                        // the row's distance to the group's near edge, then the group's own powers
-                        const float f = pw[REV ? col - row : row - col - 31];
+                        const float f = pw[gap];
 #pragma unroll
-                        for (int j = 0; j < 32; j += 4) {
+                        for (int j = 0; j < 16; j += 4) {
                             const float4 u = REV ? *reinterpret_cast<const float4*>(pw + j)
                                                  : *reinterpret_cast<const float4*>(down + j);
                             const Pair x = mul2(mul2(at(r + j), {f, f}), {u.x, u.y});
@@ -409,16 +403,16 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
                             hi[j / 2] = pack_bf16(x.x, x.y);
                             hi[j / 2 + 1] = pack_bf16(y.x, y.y);
                         }
-                        if (REV && col + 32 > n) {  // tokens behind the end: whatever they held
+                    }
+                    if (REV && col + 16 > n) {  // tokens behind the end: whatever they held
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                if (col + 2 * j >= n) hi[j] = 0u;
-                                else if (col + 2 * j + 1 >= n) hi[j] &= 0xffffu;
-                            }
+                        for (int j = 0; j < 8; ++j) {
+                            if (col + 2 * j >= n) hi[j] = 0u;
+                            else if (col + 2 * j + 1 >= n) hi[j] &= 0xffffu;
                         }
                     }
                 }
-                tmem_store16(tP + lane_off + col, hi);
+                tmem_store8(tP + lane_off + col, hi);
             }
             tmem_st_wait();
             tc_fence_before();
@@ -436,7 +430,7 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
             const int t0 = chunk_of(it) * kL + quarter * 32 + (lane >> 3);
             bf16* const dst = out + (long long)t0 * p.so[2] + (lane & 7) * 8;
             const int left = n - quarter * 32 - (lane >> 3);  // this lane's rows 0, 4, .. below it
-#pragma unroll
+#pragma unroll 1
             for (int g = 0; g < D / 64; ++g) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
