@@ -19,12 +19,12 @@
 //
 // Roles.  X warps (4): P from tensor memory, decayed, masked and packed back.
 // O warps (4): o_i from O1 and O2, through shared memory, to global memory.  Y
-// warps (16): B~ in steps of 16 to 64 tokens (first terms in place of B, the others in a
-// ring of two slots), then S and its bf16 copy.  One warp issues the products, one the loads.  Nothing may spill: local
-// memory would go to L2, shared memory takes all of L1.  The issuer orders a
-// chunk's products so that what the next chunk waits for comes early: A S (A's
-// tile is loaded again), half of U, P~ C, the rest of U and the next chunk's
-// scores, which are there when Y has updated S.
+// warps (16): B~ in steps of 16 to 64 tokens (first terms in place of B, the
+// others in a ring of two slots), then S and its bf16 copy.  Two warps issue
+// products, U and the other three, so that a wait in one chain does not hold up
+// the other; one warp loads.  Code is kept short and nothing may spill: seven
+// roles share the instruction caches, and local memory goes to L2 (shared memory
+// takes all of L1).
 #include "hla2_linear.cuh"
 #include "hla2_tc_common.cuh"
 
@@ -84,28 +84,10 @@ __device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
 __device__ __forceinline__ Pair unpack_bf16(uint32_t w) { return {__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)}; }
 __device__ __forceinline__ Pair at(const uint32_t* r) { return {__uint_as_float(r[0]), __uint_as_float(r[1])}; }
 
-// What the issuing warp does, all lanes together: the values stay uniform, so
-// that descriptors are formed and products issued without a detour through
-// each lane's registers (one lane alone took 140 clocks a product).
-__device__ __forceinline__ void mma_warp(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n .reg .pred p, q;\n elect.sync _|q, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
-        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n"
-        ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(acc)
-        : "memory");
-}
-__device__ __forceinline__ void mma_warp_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n .reg .pred p, q;\n elect.sync _|q, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
-        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
-        ::"r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
-        : "memory");
-}
-__device__ __forceinline__ void commit_warp(uint32_t mbar) {
-    asm volatile(
-        "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
-        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(mbar)
-        : "memory");
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+    return r != 0;
 }
 // A number of tries in a row (each may suspend the warp for a while)
 __device__ __forceinline__ bool mbar_tries(uint32_t a, uint32_t parity) {
@@ -140,8 +122,8 @@ struct TcLayout {
 template <int D, bool OUT>
 struct TcRoles {
     static constexpr int kX = OUT ? 4 : 0, kO = kX, kY = 16;
-    static constexpr int kY0 = kX + kO, kIssuer = kY0 + kY, kLoader = kIssuer + 1;
-    static constexpr int kThreads = (kLoader + 1) * 32;
+    static constexpr int kY0 = kX + kO, kStates = kY0 + kY, kLoader = kStates + 1, kOuts = kLoader + 1;
+    static constexpr int kThreads = (OUT ? kOuts + 1 : kOuts) * 32;
     static constexpr int kParts = kY / 4;           // Y warps to 32 rows of the state
     static constexpr int kState = D / 32 * kParts;  // Y warps that hold rows of the state
 };
@@ -154,10 +136,12 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
     using RO = TcRoles<D, OUT>;
     constexpr int NA = LY::NA, NA1 = NA ? NA : 1, NB = LY::NB, STEP = LY::STEP, STEPS = kL / STEP, PER = LY::PER;
     extern __shared__ __align__(1024) unsigned char dsm_raw[];
-    // loads | A read (O2 = A S done) | a chunk's last product done (B and C free, U ready) | P ready, packed |
-    // ring filled, free | U drained | S copy ready | O ready (P's columns free), drained | last wait
-    enum { LA, LB = LA + NA, LC = LB + NB, FA = LC + NB, FB = FA + NA1, CP = FB + NB, DP, KQ, RF = KQ + 2, DU = RF + 2,
-           DS = DU + 2, CO, DO, FIN, NBAR };
+    // A barrier's next phase never completes before everybody has seen this one: it takes an arrival that each waiter
+    // gives after its wait.  (P of the next chunk needs no arrival of Y, so its barriers go by turns.)
+    // loads | A read (O2 = A S done) | B and C read (by both issuers) | P ready, packed | ring filled, free |
+    // U ready, drained | S copy ready | O ready (P's columns free), drained | last waits
+    enum { LA, LB = LA + NA, LC = LB + NB, FA = LC + NB, FB = FA + NA1, CP = FB + NB, DP = CP + 2, KQ, RF = KQ + 2, CU = RF + 2,
+           DU = CU + 2, DS = DU + 2, CO, DO, FIN, NBAR = FIN + 2 };
     __shared__ __align__(8) unsigned long long bars[NBAR];
     __shared__ __align__(16) float pw[kL + 4];  // g^0 .. g^128
     __shared__ __align__(16) float down[16];    // g^15 .. g^0
@@ -165,8 +149,7 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
     __shared__ volatile int abort_flag;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const bool xwarp = warp < RO::kX, owarp = !xwarp && warp < RO::kY0, ywarp = warp >= RO::kY0 && warp < RO::kIssuer;
-    const bool issuer = warp == RO::kIssuer, loader = warp == RO::kLoader;
+    const bool xwarp = warp < RO::kX, owarp = !xwarp && warp < RO::kY0, ywarp = warp >= RO::kY0 && warp < RO::kStates;
     const int quarter = warp & 3, row = quarter * 32 + lane;  // lanes of tensor memory
     const int bh = blockIdx.y, w = blockIdx.x, seg = REV ? p.nseg - 1 - w : w;
     const int b = bh / p.H, h = bh % p.H;
@@ -191,6 +174,7 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
         for (int i = 0; i < NBAR; ++i) {
             uint32_t count = 1;
             if (i == DP || i == DO) count = OUT ? RO::kX : 1;
+            if (i >= FB && i < FB + NB) count = OUT ? 2 : 1;
             if (i == KQ || i == KQ + 1) count = PER;
             if (i == DU || i == DU + 1 || i == DS) count = RO::kState;
             mbar_init(bar(i), count);
@@ -241,109 +225,138 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
         if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar(i)) : "memory");
     };
 
+    // Zeros in the rows of C behind the end, whatever they hold, by warp `i` of `count`.  Y writes them before U, X
+    // before P~ C: neither set of products waits for the other's.
+    auto zero_behind = [&](const Tile& C, int n, int i, int count) {
+        for (int e = (n << 3) + i * 32 + lane; e < kL * 8; e += count * 32)
+#pragma unroll
+            for (int k = 0; k < D / 64; ++k) st_shared_v4(C.chunk(e >> 3, k, e & 7), 0u, 0u, 0u, 0u);
+    };
+
     constexpr uint32_t iPP = idesc_bf16(128, 128, false, false);  // A B^T: both along the channels
     constexpr uint32_t iAS = idesc_bf16(128, D, false, true);     // A S, P~ C: the second along its rows
     constexpr uint32_t iBC = idesc_bf16(128, D, true, true);      // B~^T C: both along the tokens
 
-    if (issuer) {
-        // as wait_bar, the whole warp with one answer
-        auto wait_warp = [&](int i, uint32_t parity) -> bool {
-            const uint32_t a = bar(i);
-            bool ok = mbar_tries(a, parity);
-            if (!__all_sync(0xffffffffu, ok)) {
-                const unsigned long long t0 = globaltimer();
-                while (!ok && !abort_flag) {
-                    ok = mbar_tries(a, parity);
-                    if (!ok && globaltimer() - t0 > kWaitNs) {
-                        abort_flag = 1;
-                        atomicExch(p.status, (int)kDevWaitTimeout);
-                    }
-                }
-                __syncwarp();
-            }
-            return __all_sync(0xffffffffu, ok) != 0;
-        };
-        // a tile's descriptors: its first one, then steps along the channels (16 of them) or the rows (16)
-        constexpr uint32_t kBlock = kL * 128u;
-        auto along = [](uint64_t first, int ks) { return first + (uint64_t)((((ks >> 2) * kBlock) + (ks & 3) * 32u) >> 4); };
-        auto down_rows = [](uint64_t first, int ks) { return first + (uint64_t)(ks * 128); };
-        int sa = 0, sb = 0;         // stages of A, of B and C
-        uint32_t pa = 0, pb = 0;    // and their phases
-        const uint64_t dS = sdesc(dsm + LY::S, D * 128u, 1024u);
-        auto scores = [&](int it) -> bool {  // P of chunk `it`, once P~ C of the one before has read its columns
-            if (it > 0 && !wait_warp(CO, (uint32_t)(it - 1) & 1)) return false;
-            if (!wait_warp(LA + sa, pa) || !wait_warp(LB + sb, pb)) return false;
-            tc_fence_after();
-            const uint64_t dA = sdesc(dsm + LY::A + (uint32_t)sa * LY::kTile, 16u, 1024u);
-            const uint64_t dB = sdesc(dsm + LY::B + (uint32_t)sb * LY::kTile, 16u, 1024u);
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) mma_warp(tP, along(dA, ks), along(dB, ks), iPP, ks > 0);
-            commit_warp(bar(CP));
-            return true;
-        };
-        bool ok = !OUT || nchunks == 0 || scores(0);
-        for (int it = 0; it < nchunks && ok; ++it) {
-            const uint32_t ph = it & 1, before = ph ^ 1;
-            const uint64_t dA = sdesc(dsm + LY::A + (uint32_t)sa * LY::kTile, 16u, 1024u);
-            const uint64_t dB = sdesc(dsm + LY::B + (uint32_t)sb * LY::kTile, kBlock, 1024u);
-            const uint64_t dC = sdesc(dsm + LY::C + (uint32_t)sb * LY::kTile, kBlock, 1024u);
-            ok = false;  // until the chunk's last product is issued
-            // O2 = A S first: A's tile is the next one to be filled again
-            if (OUT) {
-                if (!wait_warp(DS, ph) || (it > 0 && !wait_warp(DO, before))) break;
-                tc_fence_after();
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) mma_warp(tO2, along(dA, ks), down_rows(dS, ks), iAS, ks > 0);
-                commit_warp(bar(FA + sa));
-            }
-            // U, a step of the tokens at a time as Y fills the ring, once its columns have been drained
-            if (!wait_warp(LC + sb, pb)) break;
-            if (OUT ? it > 0 && !wait_warp(DU, before)
-                    : it > 1 && !wait_warp(DU + (it & 1), (uint32_t)((it >> 1) - 1) & 1)) break;
-            const uint32_t u = tU(it);
-            bool all = true;
-#pragma unroll 1
-            for (int q = 0; q < STEPS; ++q) {
-                const int slot = q & 1;
-                all = all && wait_warp(KQ + slot, (uint32_t)((STEPS / 2 * it + q / 2) & 1));
-                if (!all) break;
-                tc_fence_after();
-#pragma unroll
-                for (int ks = 0; ks < STEP / 16; ++ks) {
-                    const int kk = q * (STEP / 16) + ks;
-                    mma_warp(u, down_rows(dB, kk), down_rows(dC, kk), iBC, kk > 0);
-#pragma unroll
-                    for (int t = 0; t < TERMS - 1; ++t)
-                        mma_warp(u, down_rows(sdesc(dsm + LY::ring + (uint32_t)(slot * (TERMS - 1) + t) * LY::kPart, STEP * 128u, 1024u), ks),
-                                 down_rows(dC, kk), iBC, 1);
-                }
-                commit_warp(bar(RF + slot));
-                if (OUT && q == STEPS / 2 - 1) {
-                    // O1 = P~ C, packed by X meanwhile
-                    all = wait_warp(DP, ph);
-                    if (!all) break;
-                    tc_fence_after();
-#pragma unroll
-                    for (int ks = 0; ks < kL / 16; ++ks) mma_warp_tmem_a(tO1, tP + 16 * ks, down_rows(dC, ks), iAS, ks > 0);
-                    commit_warp(bar(CO));
+    // a tile's descriptors: its first one, then steps along the channels (16 of them) or the rows (16)
+    constexpr uint32_t kBlock = kL * 128u;
+    auto along = [](uint64_t first, int ks) { return first + (uint64_t)((((ks >> 2) * kBlock) + (ks & 3) * 32u) >> 4); };
+    auto down_rows = [](uint64_t first, int ks) { return first + (uint64_t)(ks * 128); };
+
+    // The issuing warps stay together: their values are uniform, so that descriptors are formed once for the warp
+    // (a single lane's way through its own registers took 180 clocks a product), and one lane issues each batch.
+    auto wait_warp = [&](int i, uint32_t parity) -> bool {
+        const uint32_t a = bar(i);
+        bool ok = mbar_tries(a, parity);
+        if (!__all_sync(0xffffffffu, ok)) {
+            const unsigned long long t0 = globaltimer();
+            while (!ok && !abort_flag) {
+                ok = mbar_tries(a, parity);
+                if (!ok && globaltimer() - t0 > kWaitNs) {
+                    abort_flag = 1;
+                    atomicExch(p.status, (int)kDevWaitTimeout);
                 }
             }
-            if (!all) break;
-            commit_warp(bar(FB + sb));
-            if (++sb == NB) { sb = 0; pb ^= 1; }
-            if (++sa >= NA1) { sa = 0; pa ^= 1; }
-            ok = !OUT || it + 1 == nchunks || scores(it + 1);
+            __syncwarp();
         }
-        // no product may still run when the CTA gives its memory back, whatever ended the walk
-        commit_warp(bar(FIN));
+        return __all_sync(0xffffffffu, ok) != 0;
+    };
+    // no product may still run when the CTA gives its memory back, whatever ended the walk
+    auto finish = [&](int i) {
+        if (elect_one()) mma_commit(bar(i));
+        __syncwarp();
         const unsigned long long t0 = globaltimer();
-        while (!mbar_tries(bar(FIN), 0))
+        while (!mbar_tries(bar(i), 0))
             if (globaltimer() - t0 > kWaitNs) {
                 atomicExch(p.status, (int)kDevWaitTimeout);
                 break;
             }
         __syncwarp();
-    } else if (loader) {
+    };
+
+    if (warp == RO::kStates) {
+        // U, a step of the tokens at a time as Y fills the ring, once its columns have been drained
+        int sb = 0;
+        uint32_t pb = 0;
+        for (int it = 0; it < nchunks; ++it) {
+            const uint64_t dB = sdesc(dsm + LY::B + (uint32_t)sb * LY::kTile, kBlock, 1024u);
+            const uint64_t dC = sdesc(dsm + LY::C + (uint32_t)sb * LY::kTile, kBlock, 1024u);
+            if (!wait_warp(LC + sb, pb)) break;
+            if (OUT ? it > 0 && !wait_warp(DU, (uint32_t)(it - 1) & 1)
+                    : it > 1 && !wait_warp(DU + (it & 1), (uint32_t)((it >> 1) - 1) & 1)) break;
+            const uint32_t u = tU(it);
+            bool ok = true;
+#pragma unroll
+            for (int q = 0; q < STEPS; ++q) {
+                const int slot = q & 1;
+                ok = ok && wait_warp(KQ + slot, (uint32_t)((STEPS / 2 * it + q / 2) & 1));
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int ks = 0; ks < STEP / 16; ++ks) {
+                        const int kk = q * (STEP / 16) + ks;
+                        mma_bf16(u, down_rows(dB, kk), down_rows(dC, kk), iBC, kk > 0);
+#pragma unroll
+                        for (int t = 0; t < TERMS - 1; ++t)
+                            mma_bf16(u, down_rows(sdesc(dsm + LY::ring + (uint32_t)(slot * (TERMS - 1) + t) * LY::kPart, STEP * 128u, 1024u), ks),
+                                     down_rows(dC, kk), iBC, 1);
+                    }
+                    mma_commit(bar(RF + slot));
+                    if (q == STEPS - 1) {
+                        mma_commit(bar(CU + (OUT ? 0 : it & 1)));
+                        mma_commit(bar(FB + sb));
+                    }
+                }
+                __syncwarp();
+            }
+            if (!ok) break;
+            if (++sb == NB) { sb = 0; pb ^= 1; }
+        }
+        finish(FIN);
+    } else if (OUT && warp == RO::kOuts) {
+        // P, O2, O1, with an issuer of their own: a wait of one chain of products does not hold up the other
+        const uint64_t dS = sdesc(dsm + LY::S, D * 128u, 1024u);
+        int sa = 0, sb = 0;
+        uint32_t pa = 0, pb = 0;
+        for (int it = 0; it < nchunks; ++it) {
+            const uint32_t ph = it & 1, before = ph ^ 1;
+            const uint64_t dA = sdesc(dsm + LY::A + (uint32_t)sa * LY::kTile, 16u, 1024u);
+            const uint64_t dB = sdesc(dsm + LY::B + (uint32_t)sb * LY::kTile, 16u, 1024u);
+            const uint64_t dC = sdesc(dsm + LY::C + (uint32_t)sb * LY::kTile, kBlock, 1024u);
+            // P, once the last chunk's P~ C has read its columns
+            if (it > 0 && !wait_warp(CO, before)) break;
+            if (!wait_warp(LA + sa, pa) || !wait_warp(LB + sb, pb)) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) mma_bf16(tP, along(dA, ks), along(dB, ks), iPP, ks > 0);
+                mma_commit(bar(CP + ph));
+            }
+            __syncwarp();
+            // O2 = A S, once the last chunk's outputs have been drained
+            if (!wait_warp(DS, ph) || (it > 0 && !wait_warp(DO, before))) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) mma_bf16(tO2, along(dA, ks), down_rows(dS, ks), iAS, ks > 0);
+                mma_commit(bar(FA + sa));
+            }
+            __syncwarp();
+            // O1 = P~ C
+            if (!wait_warp(LC + sb, pb) || !wait_warp(DP, ph)) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int ks = 0; ks < kL / 16; ++ks) mma_bf16_tmem_a(tO1, tP + 16 * ks, down_rows(dC, ks), iAS, ks > 0);
+                mma_commit(bar(CO));
+                mma_commit(bar(FB + sb));
+            }
+            __syncwarp();
+            if (++sb == NB) { sb = 0; pb ^= 1; }
+            if (++sa == NA1) { sa = 0; pa ^= 1; }
+        }
+        finish(FIN + 1);
+    } else if (warp == RO::kLoader) {
         if (lane == 0) {
             LoadLedger<NA + 2 * NB> loads(bar(0));
             auto load = [&](int l, const CUtensorMap* map, const Tile& t, int it) {
@@ -370,7 +383,7 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
         for (int it = 0; it < nchunks; ++it) {
             const uint32_t ph = it & 1;
             const int n = tokens_of(it);
-            if (!wait_bar(CP, ph)) break;
+            if (!wait_bar(CP + ph, (uint32_t)(it >> 1) & 1)) break;
             tc_fence_after();
 #pragma unroll 1
             for (int col = 0; col < kL; col += 16) {  // each 16 columns packed into their first 8
@@ -413,6 +426,11 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
                     }
                 }
                 tmem_store8(tP + lane_off + col, hi);
+            }
+            if (n < kL) {
+                if (!wait_bar(LC + it % NB, (uint32_t)(it / NB) & 1)) break;
+                zero_behind(tC(it), n, quarter, RO::kX);
+                fence_proxy_async();
             }
             tmem_st_wait();
             tc_fence_before();
@@ -505,7 +523,7 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
             arrive(DS);
         };
         auto update = [&](int it) -> bool {  // S of chunk it's end
-            if (!wait_bar(FB + it % NB, (uint32_t)(it / NB) & 1)) return false;
+            if (!wait_bar(CU + (OUT ? 0 : it & 1), OUT ? (uint32_t)it & 1 : (uint32_t)(it >> 1) & 1)) return false;
             tc_fence_after();
             const float gn = pw[tokens_of(it)];
 #pragma unroll
@@ -535,14 +553,10 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
             const int n = tokens_of(it), sb = it % NB;
             const uint32_t kb = (uint32_t)(it / NB) & 1;
             const Tile B = tB(it), C = tC(it);
-            if (!wait_bar(LB + sb, kb) || (OUT && !wait_bar(CP, ph))) break;  // A B^T has read B
+            if (!wait_bar(LB + sb, kb) || (OUT && !wait_bar(CP + ph, (uint32_t)(it >> 1) & 1))) break;  // A B^T has read B
             if (n < kL) {
-                // rows of C behind the end: zeros, whatever they hold
                 if (!wait_bar(LC + sb, kb)) break;
-                // (by each group of warps, so that the arrivals of either say so)
-                for (int i = (n << 3) + item * 32 + lane; i < kL * 8; i += PER * 32)
-#pragma unroll
-                    for (int k = 0; k < D / 64; ++k) st_shared_v4(C.chunk(i >> 3, k, i & 7), 0u, 0u, 0u, 0u);
+                zero_behind(C, n, item, PER);  // by each group of warps, so that the arrivals of either say so
             }
             bool ok = true;
 #pragma unroll 1
@@ -576,7 +590,8 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
                 if (OUT) {
                     if (!update(it)) break;
                     if (it + 1 < nchunks) {
-                        copy_state();  // (A S, issued before U, has read the copy)
+                        if (!wait_bar(FA + it % NA1, (uint32_t)(it / NA1) & 1)) break;  // A S has read the copy
+                        copy_state();
                     }
                 } else if (it > 0 && !update(it - 1)) {  // the previous chunk's, beside this one's products
                     break;
