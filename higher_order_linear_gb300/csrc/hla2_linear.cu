@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) lin_walk_kernel(const LinWalk
         const int r = e / D, c = e % D;
         float v = 0.f;
         if (OUT && r < p.da && c < p.dc) {
-            if (rec) v = rec[(size_t)r * p.dc + c];
+            if (rec) v = rec[r * p.rec_r + c * p.rec_c];
             else if (p.s_in) v = p.s_in[(size_t)bh * R + r * p.in_r + c * p.in_c];
         }
         sS[e] = v;
@@ -313,11 +313,11 @@ __global__ void __launch_bounds__(256) lin_step_kernel(const float* state, const
 }
 
 // ------------------------------------------------------------------ host ----
-// Segments per head, each a CTA that fills an SM: the count with the least time
+// Segments per head, each a CTA, `ctas` of which fill an SM: the count with the least time
 // of rounds of CTAs (a chunk is the unit; a CTA's start costs about one; the
 // states' pass reads half of what the second one moves).
-void plan_segments(int BH, int T, int chunk, int* nseg, int* seglen, int* nchunk) {
-    const int n = (T + chunk - 1) / chunk, sms = sm_count();
+void plan_segments(int BH, int T, int chunk, int ctas, int* nseg, int* seglen, int* nchunk) {
+    const int n = (T + chunk - 1) / chunk, sms = sm_count() * ctas;
     double best = 0;
     *nchunk = n; *nseg = 1; *seglen = n;
     for (int want = 1; want <= n && want <= 1024; ++want) {
@@ -345,24 +345,33 @@ cudaError_t launch_simple(const LinWalk& w, bool states, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-// One walk: the segments' states and their scan where there are several, then the outputs.
-cudaError_t run_walk(LinWalk w, int dtype, cudaStream_t s) {
+// The path and the segments of a walk.
+bool plan_walk(LinWalk& w, int dtype) {
     const bool tc = lin_tc_supported(w, dtype);
-    const int chunk = tc ? kLinTcChunk : kTokens;
-    plan_segments(w.B * w.H, w.T, chunk, &w.nseg, &w.seglen, &w.nchunk);
-    auto walk = [&](bool states) {
-        if (tc) return launch_lin_tc(w, states, s);
-        const bool small = w.da <= 64 && w.dc <= 64;
-        if (dtype == HLA2_DTYPE_BF16) return small ? launch_simple<bf16, 64>(w, states, s) : launch_simple<bf16, 128>(w, states, s);
-        return small ? launch_simple<float, 64>(w, states, s) : launch_simple<float, 128>(w, states, s);
-    };
-    if (w.nseg > 1) {
-        if (cudaError_t e = walk(true)) return e;
-        lin_scan_kernel<<<dim3((w.da * w.dc + 255) / 256, w.B * w.H), 256, 0, s>>>(w, chunk, lin_state_segments(w));
-        note_launches(1);
-        if (cudaError_t e = cudaGetLastError()) return e;
-    }
-    return walk(false);
+    plan_segments(w.B * w.H, w.T, tc ? kLinTcChunk : kTokens, tc ? lin_tc_ctas(w.da, w.dc) : 1, &w.nseg, &w.seglen, &w.nchunk);
+    w.rec_r = w.dc;
+    w.rec_c = 1;
+    return tc;
+}
+cudaError_t launch_walk(const LinWalk& w, int dtype, bool tc, bool states, cudaStream_t s) {
+    if (tc) return launch_lin_tc(w, states, s);
+    const bool small = w.da <= 64 && w.dc <= 64;
+    if (dtype == HLA2_DTYPE_BF16) return small ? launch_simple<bf16, 64>(w, states, s) : launch_simple<bf16, 128>(w, states, s);
+    return small ? launch_simple<float, 64>(w, states, s) : launch_simple<float, 128>(w, states, s);
+}
+// The states that enter the segments, where there are several (and the last state).
+cudaError_t enter_states(const LinWalk& w, int dtype, bool tc, cudaStream_t s) {
+    if (w.nseg == 1) return cudaSuccess;
+    if (cudaError_t e = launch_walk(w, dtype, tc, true, s)) return e;
+    lin_scan_kernel<<<dim3((w.da * w.dc + 255) / 256, w.B * w.H), 256, 0, s>>>(w, tc ? kLinTcChunk : kTokens,
+                                                                               lin_state_segments(w));
+    note_launches(1);
+    return cudaGetLastError();
+}
+cudaError_t run_walk(LinWalk w, int dtype, cudaStream_t s) {
+    const bool tc = plan_walk(w, dtype);
+    if (cudaError_t e = enter_states(w, dtype, tc, s)) return e;
+    return launch_walk(w, dtype, tc, false, s);
 }
 
 int check_linear(const char* what, int B, int H, int T, int d, int dv, int dtype) {
@@ -394,7 +403,7 @@ size_t walk_bytes(int B, int H, int T, int d, int dv) {
     size_t most = 0;
     for (int chunk : {kLinTcChunk, kTokens}) {
         int nseg, seglen, nchunk;
-        plan_segments(B * H, T, chunk, &nseg, &seglen, &nchunk);
+        plan_segments(B * H, T, chunk, chunk == kLinTcChunk ? lin_tc_ctas(d, dv) : 1, &nseg, &seglen, &nchunk);
         if (nseg > 1) most = max(most, (size_t)B * H * (nseg + 1) * d * dv * 4);
     }
     return (most + 255) & ~size_t(255);
@@ -495,18 +504,32 @@ extern "C" int hla2_linear_backward(const void* Q, const void* K, const void* V,
         w.s_in = s_in; w.s_out = s_out;
         w.in_r = transposed ? 1 : dv; w.in_c = transposed ? dv : 1;
         w.out_r = dv; w.out_c = 1;
-        cudaError_t e = run_walk(w, dtype, s);
-        if (e != cudaSuccess || !lengths) return e;
-        const dim3 grid(8, H, B);
-        if (dtype == HLA2_DTYPE_BF16) lin_tail_kernel<bf16><<<grid, 256, 0, s>>>(w);
-        else lin_tail_kernel<float><<<grid, 256, 0, s>>>(w);
-        note_launches(1);
-        return cudaGetLastError();
+        return w;
     };
-    // dV's walk, which writes dstate_in, last: dstate_in may be dstate_out or state_in
-    cudaError_t e = walk(g, v, k, dQ, 4, false, state_in, true, nullptr);
-    if (e == cudaSuccess) e = walk(v, g, q, dK, 5, true, dstate_out, true, nullptr);
-    if (e == cudaSuccess) e = walk(k, q, g, dV, 6, true, dstate_out, false, dstate_in);
+    LinWalk wq = walk(g, v, k, dQ, 4, false, state_in, true, nullptr);
+    LinWalk wk = walk(v, g, q, dK, 5, true, dstate_out, true, nullptr);
+    LinWalk wv = walk(k, q, g, dV, 6, true, dstate_out, false, dstate_in);
+    // dQ first, and dV, which writes dstate_in, after whatever reads dstate_out: dstate_in may be either state
+    cudaError_t e = run_walk(wq, dtype, s);
+    const bool tk = plan_walk(wk, dtype), tv = plan_walk(wv, dtype);
+    if (e == cudaSuccess && tk == tv && wv.nseg > 1) {
+        // the states of dK are those of dV, transposed
+        e = enter_states(wv, dtype, tv, s);
+        wk.rec_r = 1;
+        wk.rec_c = dv;
+        if (e == cudaSuccess) e = launch_walk(wk, dtype, tk, false, s);
+        if (e == cudaSuccess) e = launch_walk(wv, dtype, tv, false, s);
+    } else {
+        if (e == cudaSuccess) e = run_walk(wk, dtype, s);
+        if (e == cudaSuccess) e = run_walk(wv, dtype, s);
+    }
+    if (e == cudaSuccess && lengths)
+        for (const LinWalk& w : {wq, wk, wv}) {
+            if (dtype == HLA2_DTYPE_BF16) lin_tail_kernel<bf16><<<dim3(8, H, B), 256, 0, s>>>(w);
+            else lin_tail_kernel<float><<<dim3(8, H, B), 256, 0, s>>>(w);
+            note_launches(1);
+            if ((e = cudaGetLastError()) != cudaSuccess) break;
+        }
     if (e != cudaSuccess) return set_error(HLA2_ERR_LAUNCH, "%s: %s", what, cudaGetErrorString(e));
     return HLA2_OK;
 }

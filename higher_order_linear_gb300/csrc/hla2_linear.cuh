@@ -30,7 +30,8 @@ struct LinWalk {
     const float* s_in;   // [BH][da * dc], element (r, c) at r in_r + c in_c; null: zero
     float* s_out;        // the same with out_r, out_c; null: not wanted
     long long in_r, in_c, out_r, out_c;
-    float* rec;  // [BH][nseg + 1][da * dc] (nseg > 1)
+    float* rec;  // [BH][nseg + 1][da * dc] (nseg > 1), a state that enters has (r, c) at r rec_r + c rec_c
+    long long rec_r, rec_c;  // (dK's walk reads dV's states, transposed)
     int nseg, seglen, nchunk;
     int rev;
     int* status;
@@ -42,6 +43,7 @@ inline int lin_state_segments(const LinWalk& w) { return w.s_out ? w.nseg : w.ns
 // Tensor cores (hla2_linear_tc.cu): bf16, da and dc up to 128, rows and bases
 // of whole 16-byte steps.  chunks of 128 tokens.
 constexpr int kLinTcChunk = 128;
+inline int lin_tc_ctas(int da, int dc) { return da <= 64 && dc <= 64 ? 2 : 1; }  // to an SM
 bool lin_tc_supported(const LinWalk& w, int dtype);
 cudaError_t launch_lin_tc(const LinWalk& w, bool states, cudaStream_t s);
 

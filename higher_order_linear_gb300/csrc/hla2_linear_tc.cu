@@ -103,37 +103,39 @@ __device__ __forceinline__ bool mbar_tries(uint32_t a, uint32_t parity) {
     return ok != 0;
 }
 
-// Shared memory.  Tiles of A: NA, of B and C: NB; the ring's slots hold the
-// second (and third) terms of STEP tokens of B~; the stage a group of 64 output
-// columns of each X warp.  At D = 64 the products' A operand still has 128
-// rows: those past the tile's 64 columns read what follows it in this
-// allocation, and nobody reads their results.
+// Warps and shared memory.  Tiles of A: NA, of B and C: NB; the ring's slots hold
+// the second (and third) terms of STEP tokens of B~; the stage a group of SC
+// output columns of each O warp.  At D = 64 two CTAs share an SM: sixteen warps of
+// 64 registers each (X and O are the same four), half of tensor memory, and
+// half of shared memory; a walk of one chunk after another leaves gaps that the other
+// CTA fills.  At D = 64 the products' A operand still has 128 rows: those past
+// the tile's 64 columns read what follows it in this allocation, and nobody
+// reads their results.
 template <int D, bool OUT, int TERMS>
 struct TcLayout {
-    static constexpr int STEP = D == 64 ? 64 : OUT && TERMS == 3 ? 16 : 32;
-    static constexpr int PER = STEP / 4 * (D / 64);  // items of 4 tokens by 64 channels in a step, one to a warp
-    static constexpr int NA = OUT ? (D == 64 ? 2 : 1) : 0, NB = OUT ? (D == 64 ? 3 : 2) : 3;
-    static constexpr uint32_t kTile = kL * D * 2, kPart = STEP * D * 2;
-    static constexpr uint32_t A = 0, B = NA * kTile, C = B + NB * kTile, ring = C + NB * kTile;
-    static constexpr uint32_t S = ring + 2 * (TERMS - 1) * kPart;
-    static constexpr uint32_t stage = S + (D == 64 || OUT ? D * D * 2 : 0), kBytes = stage + (OUT ? 4 * 4096 : 0);
-};
-
-template <int D, bool OUT>
-struct TcRoles {
-    static constexpr int kX = OUT ? 4 : 0, kO = kX, kY = 16;
+    static constexpr int kCtas = D == 64 ? 2 : 1;
+    static constexpr int kX = OUT ? 4 : 0, kO = OUT && D == 128 ? 4 : 0, kY = D == 64 ? 8 : 16;
     static constexpr int kY0 = kX + kO, kStates = kY0 + kY, kLoader = kStates + 1, kOuts = kLoader + 1;
     static constexpr int kThreads = (OUT ? kOuts + 1 : kOuts) * 32;
     static constexpr int kParts = kY / 4;           // Y warps to 32 rows of the state
     static constexpr int kState = D / 32 * kParts;  // Y warps that hold rows of the state
+    static constexpr int kCols = D == 128 ? 512 : OUT ? 256 : 128;  // of tensor memory
+
+    static constexpr int STEP = OUT && TERMS == 3 ? 16 : 32;
+    static constexpr int PER = STEP / 4 * (D / 64);  // items of 4 tokens by 64 channels in a step, one to a warp
+    static constexpr int SC = D == 64 ? 32 : 64;
+    static constexpr int NA = OUT ? 1 : 0, NB = D == 128 && !OUT ? 3 : 2;
+    static constexpr uint32_t kTile = kL * D * 2, kPart = STEP * D * 2, kStage = 32 * SC * 2;
+    static constexpr uint32_t A = 0, B = NA * kTile, C = B + NB * kTile, ring = C + NB * kTile;
+    static constexpr uint32_t S = ring + 2 * (TERMS - 1) * kPart;
+    static constexpr uint32_t stage = S + (D == 64 || OUT ? D * D * 2 : 0), kBytes = stage + (OUT ? 4 * kStage : 0);
 };
 
 template <int D, bool REV, bool OUT, int TERMS>
-__global__ void __launch_bounds__(TcRoles<D, OUT>::kThreads, 1)
+__global__ void __launch_bounds__(TcLayout<D, OUT, TERMS>::kThreads, TcLayout<D, OUT, TERMS>::kCtas)
 lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorMap mB,
               const __grid_constant__ CUtensorMap mC, const LinWalk p) {
     using LY = TcLayout<D, OUT, TERMS>;
-    using RO = TcRoles<D, OUT>;
     constexpr int NA = LY::NA, NA1 = NA ? NA : 1, NB = LY::NB, STEP = LY::STEP, STEPS = kL / STEP, PER = LY::PER;
     extern __shared__ __align__(1024) unsigned char dsm_raw[];
     // A barrier's next phase never completes before everybody has seen this one: it takes an arrival that each waiter
@@ -149,7 +151,8 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
     __shared__ volatile int abort_flag;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const bool xwarp = warp < RO::kX, owarp = !xwarp && warp < RO::kY0, ywarp = warp >= RO::kY0 && warp < RO::kStates;
+    const bool xwarp = warp < LY::kX, owarp = LY::kO ? !xwarp && warp < LY::kY0 : xwarp;
+    const bool ywarp = warp >= LY::kY0 && warp < LY::kStates;
     const int quarter = warp & 3, row = quarter * 32 + lane;  // lanes of tensor memory
     const int bh = blockIdx.y, w = blockIdx.x, seg = REV ? p.nseg - 1 - w : w;
     const int b = bh / p.H, h = bh % p.H;
@@ -173,10 +176,10 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
         abort_flag = 0;
         for (int i = 0; i < NBAR; ++i) {
             uint32_t count = 1;
-            if (i == DP || i == DO) count = OUT ? RO::kX : 1;
+            if (i == DP || i == DO) count = OUT ? LY::kX : 1;
             if (i >= FB && i < FB + NB) count = OUT ? 2 : 1;
             if (i == KQ || i == KQ + 1) count = PER;
-            if (i == DU || i == DU + 1 || i == DS) count = RO::kState;
+            if (i == DU || i == DU + 1 || i == DS) count = LY::kState;
             mbar_init(bar(i), count);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -188,22 +191,18 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
     }
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
-                     "r"(kTmemCols)
+                     "r"(LY::kCols)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    // all of tensor memory was taken, so it begins at column 0; anything else is reported and nothing is done
-    constexpr uint32_t tmem = 0;
-    if (tmem_slot != tmem) {
-        if (tid == 0) atomicExch(p.status, (int)kDevTmemAlloc);
-        nchunks = 0;
-    }
-    // outputs: P | O1 | O2 | U;  states: U twice, by turns
-    const uint32_t tP = tmem, tO1 = tmem + 128, tO2 = tmem + 128 + D;
-    auto tU = [&](int it) -> uint32_t { return OUT ? tmem + 128 + 2 * D : tmem + 128 * (it & 1); };
+    const uint32_t tmem = tmem_slot;
+    // outputs: P | O2 | U | O1, which at D = 64 takes the half of P's columns that P~ leaves free; states: U
+    // twice, by turns
+    const uint32_t tP = tmem, tO2 = tmem + 128, tO1 = D == 64 ? tmem + 64 : tmem + 128 + 2 * D;
+    auto tU = [&](int it) -> uint32_t { return OUT ? tmem + 128 + D : tmem + D * (it & 1); };
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
 
     auto wait_bar = [&](int i, uint32_t parity) -> bool {
@@ -273,7 +272,7 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
         __syncwarp();
     };
 
-    if (warp == RO::kStates) {
+    if (warp == LY::kStates) {
         // U, a step of the tokens at a time as Y fills the ring, once its columns have been drained
         int sb = 0;
         uint32_t pb = 0;
@@ -313,7 +312,7 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
             if (++sb == NB) { sb = 0; pb ^= 1; }
         }
         finish(FIN);
-    } else if (OUT && warp == RO::kOuts) {
+    } else if (OUT && warp == LY::kOuts) {
         // P, O2, O1, with an issuer of their own: a wait of one chain of products does not hold up the other
         const uint64_t dS = sdesc(dsm + LY::S, D * 128u, 1024u);
         int sa = 0, sb = 0;
@@ -323,8 +322,8 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
             const uint64_t dA = sdesc(dsm + LY::A + (uint32_t)sa * LY::kTile, 16u, 1024u);
             const uint64_t dB = sdesc(dsm + LY::B + (uint32_t)sb * LY::kTile, 16u, 1024u);
             const uint64_t dC = sdesc(dsm + LY::C + (uint32_t)sb * LY::kTile, kBlock, 1024u);
-            // P, once the last chunk's P~ C has read its columns
-            if (it > 0 && !wait_warp(CO, before)) break;
+            // P, once the last chunk's P~ C has read its columns (and what it left there has been drained)
+            if (it > 0 && !wait_warp(D == 64 ? DO : CO, before)) break;
             if (!wait_warp(LA + sa, pa) || !wait_warp(LB + sb, pb)) break;
             tc_fence_after();
             if (elect_one()) {
@@ -334,7 +333,7 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
             }
             __syncwarp();
             // O2 = A S, once the last chunk's outputs have been drained
-            if (!wait_warp(DS, ph) || (it > 0 && !wait_warp(DO, before))) break;
+            if (!wait_warp(DS, ph) || (D == 128 && it > 0 && !wait_warp(DO, before))) break;
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
@@ -347,7 +346,7 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
-                for (int ks = 0; ks < kL / 16; ++ks) mma_bf16_tmem_a(tO1, tP + 16 * ks, down_rows(dC, ks), iAS, ks > 0);
+                for (int ks = 0; ks < kL / 16; ++ks) mma_bf16_tmem_a(tO1, tP + 8 * ks, down_rows(dC, ks), iAS, ks > 0);
                 mma_commit(bar(CO));
                 mma_commit(bar(FB + sb));
             }
@@ -356,7 +355,7 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
             if (++sa == NA1) { sa = 0; pa ^= 1; }
         }
         finish(FIN + 1);
-    } else if (warp == RO::kLoader) {
+    } else if (warp == LY::kLoader) {
         if (lane == 0) {
             LoadLedger<NA + 2 * NB> loads(bar(0));
             auto load = [&](int l, const CUtensorMap* map, const Tile& t, int it) {
@@ -379,80 +378,82 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
             }
             if (!loads.settle()) atomicExch(p.status, (int)kDevWaitTimeout);
         }
-    } else if (OUT && xwarp) {
-        for (int it = 0; it < nchunks; ++it) {
-            const uint32_t ph = it & 1;
-            const int n = tokens_of(it);
-            if (!wait_bar(CP + ph, (uint32_t)(it >> 1) & 1)) break;
-            tc_fence_after();
-#pragma unroll 1
-            for (int col = 0; col < kL; col += 16) {  // each 16 columns packed into their first 8
-                const int gap = REV ? col - row : row - col - 15;  // the row's distance to the group's near edge
-                const int nearest = REV ? col - quarter * 32 - 16 : quarter * 32 - col;  // -16 or 0 on the diagonal
-                uint32_t hi[8];
-                if (nearest < -16 || (REV && col >= n)) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) hi[j] = 0u;
-                } else {
-                    uint32_t r[16];
-                    tmem_load16(tP + lane_off + col, r);
-                    tmem_ld_wait();
-                    if (nearest <= 0) {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const int far = REV ? gap + j : gap + 15 - j;
-                            r[j] = far >= 0 ? __float_as_uint(__uint_as_float(r[j]) * pw[max(far, 0)]) : 0u;
-                        }
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) hi[j] = pack_bf16(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-                    } else {
-                        const float f = pw[gap];
-#pragma unroll
-                        for (int j = 0; j < 16; j += 4) {
-                            const float4 u = REV ? *reinterpret_cast<const float4*>(pw + j)
-                                                 : *reinterpret_cast<const float4*>(down + j);
-                            const Pair x = mul2(mul2(at(r + j), {f, f}), {u.x, u.y});
-                            const Pair y = mul2(mul2(at(r + j + 2), {f, f}), {u.z, u.w});
-                            hi[j / 2] = pack_bf16(x.x, x.y);
-                            hi[j / 2 + 1] = pack_bf16(y.x, y.y);
-                        }
-                    }
-                    if (REV && col + 16 > n) {  // tokens behind the end: whatever they held
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            if (col + 2 * j >= n) hi[j] = 0u;
-                            else if (col + 2 * j + 1 >= n) hi[j] &= 0xffffu;
-                        }
-                    }
-                }
-                tmem_store8(tP + lane_off + col, hi);
-            }
-            if (n < kL) {
-                if (!wait_bar(LC + it % NB, (uint32_t)(it / NB) & 1)) break;
-                zero_behind(tC(it), n, quarter, RO::kX);
-                fence_proxy_async();
-            }
-            tmem_st_wait();
-            tc_fence_before();
-            arrive(DP);
-        }
-    } else if (OUT && owarp) {
+    } else if (OUT && (xwarp || owarp)) {
         bf16* const out = static_cast<bf16*>(p.o) + b * p.so[0] + h * p.so[1];
-        const uint32_t stage = dsm + LY::stage + (uint32_t)quarter * 4096u;
+        const uint32_t stage = dsm + LY::stage + (uint32_t)quarter * LY::kStage;
         for (int it = 0; it < nchunks; ++it) {
             const uint32_t ph = it & 1;
             const int n = tokens_of(it);
+            if (xwarp) {
+                if (!wait_bar(CP + ph, (uint32_t)(it >> 1) & 1)) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int col = 0; col < kL; col += 16) {  // packed two to a column, from the first on
+                    const int gap = REV ? col - row : row - col - 15;  // the row's distance to the group's near edge
+                    const int nearest = REV ? col - quarter * 32 - 16 : quarter * 32 - col;  // -16 or 0 on the diagonal
+                    uint32_t hi[8];
+                    if (nearest < -16 || (REV && col >= n)) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) hi[j] = 0u;
+                    } else {
+                        uint32_t r[16];
+                        tmem_load16(tP + lane_off + col, r);
+                        tmem_ld_wait();
+                        if (nearest <= 0) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                const int far = REV ? gap + j : gap + 15 - j;
+                                r[j] = far >= 0 ? __float_as_uint(__uint_as_float(r[j]) * pw[max(far, 0)]) : 0u;
+                            }
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) hi[j] = pack_bf16(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+                        } else {
+                            const float f = pw[gap];
+#pragma unroll
+                            for (int j = 0; j < 16; j += 4) {
+                                const float4 u = REV ? *reinterpret_cast<const float4*>(pw + j)
+                                                     : *reinterpret_cast<const float4*>(down + j);
+                                const Pair x = mul2(mul2(at(r + j), {f, f}), {u.x, u.y});
+                                const Pair y = mul2(mul2(at(r + j + 2), {f, f}), {u.z, u.w});
+                                hi[j / 2] = pack_bf16(x.x, x.y);
+                                hi[j / 2 + 1] = pack_bf16(y.x, y.y);
+                            }
+                        }
+                        if (REV && col + 16 > n) {  // tokens behind the end: whatever they held
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                if (col + 2 * j >= n) hi[j] = 0u;
+                                else if (col + 2 * j + 1 >= n) hi[j] &= 0xffffu;
+                            }
+                        }
+                    }
+                    tmem_store8(tP + lane_off + col / 2, hi);
+                }
+                if (n < kL) {
+                    if (!wait_bar(LC + it % NB, (uint32_t)(it / NB) & 1)) break;
+                    zero_behind(tC(it), n, quarter, LY::kX);
+                    fence_proxy_async();
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                arrive(DP);
+            }
+            if (!owarp) continue;
             if (!wait_bar(CO, ph)) break;
             tc_fence_after();
             const float f = row < n ? pw[REV ? n - 1 - row : row + 1] : 0.f;
-            const int t0 = chunk_of(it) * kL + quarter * 32 + (lane >> 3);
-            bf16* const dst = out + (long long)t0 * p.so[2] + (lane & 7) * 8;
-            const int left = n - quarter * 32 - (lane >> 3);  // this lane's rows 0, 4, .. below it
+            // the lane's place in a line of SC columns, and its rows: row0, row0 + RI, ..
+            constexpr int CH = LY::SC / 8, RI = 32 / CH;
+            const int row0 = lane / CH, c8 = lane % CH, left = n - quarter * 32 - row0;
+            bf16* const dst = out + (long long)(chunk_of(it) * kL + quarter * 32 + row0) * p.so[2] + c8 * 8;
+            auto spot = [&](int r, int c) {  // 16 bytes c of row r, so that neither side's accesses collide
+                return stage + (uint32_t)r * (LY::SC * 2) + (uint32_t)((c ^ (CH == 8 ? r & 7 : (r >> 1) & 3)) << 4);
+            };
 #pragma unroll 1
-            for (int g = 0; g < D / 64; ++g) {
+            for (int g = 0; g < D / LY::SC; ++g) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int col = 64 * g + 16 * k;
+                for (int k = 0; k < LY::SC / 16; ++k) {
+                    const int col = LY::SC * g + 16 * k;
                     uint32_t r1[16], r2[16];
                     tmem_load16(tO1 + lane_off + col, r1);
                     tmem_load16(tO2 + lane_off + col, r2);
@@ -469,28 +470,26 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
                             const Pair v = fma2({f, f}, at(r2 + j + 2 * i), at(r1 + j + 2 * i));
                             o[i] = pack_bf16(v.x, v.y);
                         }
-                        st_shared_v4(stage + (uint32_t)lane * 128u + (uint32_t)(((2 * k + j / 8) ^ (lane & 7)) << 4), o[0],
-                                     o[1], o[2], o[3]);
+                        st_shared_v4(spot(lane, 2 * k + j / 8), o[0], o[1], o[2], o[3]);
                     }
                 }
-                // whole lines of 128 bytes to global memory, four rows at a time
+                // whole lines to global memory
                 __syncwarp();
-                bf16* to = dst + 64 * g;
-                const bool wide = 64 * g + (lane & 7) * 8 < p.dc;
+                bf16* to = dst + LY::SC * g;
+                const bool wide = LY::SC * g + c8 * 8 < p.dc;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int r = 4 * i + (lane >> 3);
+                for (int i = 0; i < CH; ++i) {
                     uint4 v;
-                    ld_shared_v4(stage + (uint32_t)r * 128u + (uint32_t)(((lane & 7) ^ (r & 7)) << 4), v.x, v.y, v.z, v.w);
-                    if (wide && 4 * i < left) *reinterpret_cast<uint4*>(to) = v;
-                    to += 4 * p.so[2];
+                    ld_shared_v4(spot(RI * i + row0, c8), v.x, v.y, v.z, v.w);
+                    if (wide && RI * i < left) *reinterpret_cast<uint4*>(to) = v;
+                    to += RI * p.so[2];
                 }
                 __syncwarp();
             }
         }
     } else if (ywarp) {
-        constexpr int W = D / RO::kParts;  // columns of S to a thread
-        const int yw = warp - RO::kY0, part = yw >> 2;
+        constexpr int W = D / LY::kParts;  // columns of S to a thread
+        const int yw = warp - LY::kY0, part = yw >> 2;
         const bool holds = quarter < D / 32;
         const int scol = part * W;
         const size_t R = (size_t)p.da * p.dc;
@@ -501,7 +500,8 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
             const float* src = nullptr;
             long long step = 1;
             if (p.nseg > 1) {
-                src = p.rec + ((size_t)bh * (p.nseg + 1) + w) * R + (size_t)row * p.dc;
+                src = p.rec + ((size_t)bh * (p.nseg + 1) + w) * R + (size_t)row * p.rec_r;
+                step = p.rec_c;
             } else if (p.s_in) {
                 src = p.s_in + (size_t)bh * R + row * p.in_r;
                 step = p.in_c;
@@ -545,7 +545,7 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
         if (OUT && holds && nchunks > 0) copy_state();
         // an item of 4 tokens by 64 channels of a step; where a step has fewer items than there are warps, half
         // the warps take every other step
-        constexpr int GROUPS = RO::kY / PER;
+        constexpr int GROUPS = LY::kY / PER;
         const int group = yw / PER, item = yw % PER, irow = 4 * (item % (STEP / 4)) + (lane >> 3), icol = item / (STEP / 4);
         int it = 0;
         for (; it < nchunks; ++it) {
@@ -618,7 +618,7 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
     __syncthreads();
     tc_fence_after();
     if (warp == 0)
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_slot), "r"(kTmemCols) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_slot), "r"(LY::kCols) : "memory");
 }
 
 // ------------------------------------------------------------------ host ----
@@ -647,9 +647,10 @@ template <int D, bool REV, bool OUT, int TERMS>
 cudaError_t launch(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mc, const LinWalk& w,
                    cudaStream_t s) {
     auto kernel = lin_tc_kernel<D, REV, OUT, TERMS>;
-    const int bytes = (int)TcLayout<D, OUT, TERMS>::kBytes + 1024;
+    using LY = TcLayout<D, OUT, TERMS>;
+    const int bytes = (int)LY::kBytes + 1024;
     if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) return e;
-    kernel<<<dim3(OUT ? w.nseg : lin_state_segments(w), w.B * w.H), TcRoles<D, OUT>::kThreads, bytes, s>>>(ma, mb, mc, w);
+    kernel<<<dim3(OUT ? w.nseg : lin_state_segments(w), w.B * w.H), LY::kThreads, bytes, s>>>(ma, mb, mc, w);
     note_launches(1);
     return cudaGetLastError();
 }
