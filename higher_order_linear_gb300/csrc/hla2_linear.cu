@@ -223,11 +223,17 @@ __global__ void __launch_bounds__(256) lin_scan_kernel(const LinWalk p, int chun
         __syncthreads();
         const int m = min(256, segments - base);
         if (e < R) {
-#pragma unroll 8
-            for (int i = 0; i < m; ++i) {
-                float* slot = rec + (size_t)(base + i + 1) * R;
-                acc = fmaf(f[i], acc, *slot);
-                *slot = acc;
+            for (int i0 = 0; i0 < m; i0 += 8) {  // eight loads on their way at a time
+                float* const slot = rec + (size_t)(base + i0 + 1) * R;
+                float own[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) own[i] = i0 + i < m ? slot[(size_t)i * R] : 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i0 + i < m) {
+                        acc = fmaf(f[i0 + i], acc, own[i]);
+                        slot[(size_t)i * R] = acc;
+                    }
             }
         }
         __syncthreads();

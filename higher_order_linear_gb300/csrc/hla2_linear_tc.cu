@@ -121,10 +121,11 @@ struct TcLayout {
     static constexpr int kState = D / 32 * kParts;  // Y warps that hold rows of the state
     static constexpr int kCols = D == 128 ? 512 : OUT ? 256 : 128;  // of tensor memory
 
-    static constexpr int STEP = OUT && TERMS == 3 ? 16 : 32;
-    static constexpr int PER = STEP / 4 * (D / 64);  // items of 4 tokens by 64 channels in a step, one to a warp
+    static constexpr int STEP = !OUT ? 64 : TERMS == 3 ? 16 : 32;
+    static constexpr int kItems = STEP / 4 * (D / 64);  // of 4 tokens by 64 channels in a step
+    static constexpr int PER = kItems < kY ? kItems : kY;  // warps that share a step, kItems / PER items each
     static constexpr int SC = D == 64 ? 32 : 64;
-    static constexpr int NA = OUT ? 1 : 0, NB = D == 128 && !OUT ? 3 : 2;
+    static constexpr int NA = OUT ? 1 : 0, NB = 2;
     static constexpr uint32_t kTile = kL * D * 2, kPart = STEP * D * 2, kStage = 32 * SC * 2;
     static constexpr uint32_t A = 0, B = NA * kTile, C = B + NB * kTile, ring = C + NB * kTile;
     static constexpr uint32_t S = ring + 2 * (TERMS - 1) * kPart;
@@ -136,7 +137,7 @@ __global__ void __launch_bounds__(TcLayout<D, OUT, TERMS>::kThreads, TcLayout<D,
 lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorMap mB,
               const __grid_constant__ CUtensorMap mC, const LinWalk p) {
     using LY = TcLayout<D, OUT, TERMS>;
-    constexpr int NA = LY::NA, NA1 = NA ? NA : 1, NB = LY::NB, STEP = LY::STEP, STEPS = kL / STEP, PER = LY::PER;
+    constexpr int NA = LY::NA, NA1 = NA ? NA : 1, NB = LY::NB, STEP = LY::STEP, STEPS = kL / STEP, PER = LY::PER, ITEMS = LY::kItems / PER;
     extern __shared__ __align__(1024) unsigned char dsm_raw[];
     // A barrier's next phase never completes before everybody has seen this one: it takes an arrival that each waiter
     // gives after its wait.  (P of the next chunk needs no arrival of Y, so its barriers go by turns.)
@@ -543,10 +544,10 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
             return true;
         };
         if (OUT && holds && nchunks > 0) copy_state();
-        // an item of 4 tokens by 64 channels of a step; where a step has fewer items than there are warps, half
-        // the warps take every other step
+        // items of 4 tokens by 64 channels of a step; where a step has fewer than there are warps, half the warps
+        // take every other step
         constexpr int GROUPS = LY::kY / PER;
-        const int group = yw / PER, item = yw % PER, irow = 4 * (item % (STEP / 4)) + (lane >> 3), icol = item / (STEP / 4);
+        const int group = yw / PER, item = yw % PER;
         int it = 0;
         for (; it < nchunks; ++it) {
             const uint32_t ph = it & 1;
@@ -561,27 +562,35 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
             bool ok = true;
 #pragma unroll 1
             for (int q = group; q < STEPS; q += GROUPS) {
-                const int slot = q & 1, use = STEPS / 2 * it + (q >> 1), t = STEP * q + irow;
-                const bool in = t < n;
-                const float f = in ? pw[REV ? t + 1 : n - 1 - t] : 0.f;
-                const uint32_t a = B.chunk(t, icol, lane & 7);
-                uint32_t x[4], y[4], z[4];
-                ld_shared_v4(a, x[0], x[1], x[2], x[3]);
+                const int slot = q & 1, use = STEPS / 2 * it + (q >> 1);
+                uint32_t x[ITEMS][4], y[ITEMS][4], z[ITEMS][4], place[ITEMS];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    Pair u = mul2(unpack_bf16(in ? x[j] : 0u), {f, f});
-                    x[j] = pack_bf16(u.x, u.y);
-                    u = fma2(unpack_bf16(x[j]), {-1.f, -1.f}, u);
-                    y[j] = pack_bf16(u.x, u.y);
-                    if (TERMS == 3) {
-                        u = fma2(unpack_bf16(y[j]), {-1.f, -1.f}, u);
-                        z[j] = pack_bf16(u.x, u.y);
+                for (int i = 0; i < ITEMS; ++i) {
+                    const int m = item + PER * i, r = 4 * (m % (STEP / 4)) + (lane >> 3), t = STEP * q + r;
+                    const uint32_t a = B.chunk(t, m / (STEP / 4), lane & 7);
+                    place[i] = tR(slot, 0).chunk(r, m / (STEP / 4), lane & 7);
+                    ld_shared_v4(a, x[i][0], x[i][1], x[i][2], x[i][3]);
+                    const bool in = t < n;
+                    const float f = in ? pw[REV ? t + 1 : n - 1 - t] : 0.f;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        Pair u = mul2(unpack_bf16(in ? x[i][j] : 0u), {f, f});
+                        x[i][j] = pack_bf16(u.x, u.y);
+                        u = fma2(unpack_bf16(x[i][j]), {-1.f, -1.f}, u);
+                        y[i][j] = pack_bf16(u.x, u.y);
+                        if (TERMS == 3) {
+                            u = fma2(unpack_bf16(y[i][j]), {-1.f, -1.f}, u);
+                            z[i][j] = pack_bf16(u.x, u.y);
+                        }
                     }
+                    st_shared_v4(a, x[i][0], x[i][1], x[i][2], x[i][3]);
                 }
-                st_shared_v4(a, x[0], x[1], x[2], x[3]);
                 if (use > 0 && !wait_bar(RF + slot, (uint32_t)(use - 1) & 1)) { ok = false; break; }
-                st_shared_v4(tR(slot, 0).chunk(irow, icol, lane & 7), y[0], y[1], y[2], y[3]);
-                if (TERMS == 3) st_shared_v4(tR(slot, 1).chunk(irow, icol, lane & 7), z[0], z[1], z[2], z[3]);
+#pragma unroll
+                for (int i = 0; i < ITEMS; ++i) {
+                    st_shared_v4(place[i], y[i][0], y[i][1], y[i][2], y[i][3]);
+                    if (TERMS == 3) st_shared_v4(place[i] + LY::kPart, z[i][0], z[i][1], z[i][2], z[i][3]);
+                }
                 fence_proxy_async();
                 arrive(KQ + slot);
             }
