@@ -14,8 +14,12 @@
 // bf16 (half a unit each, like the bf16 result itself).  S is fp32, in the
 // registers of the warps that update it: the tensor cores only form U, one
 // chunk's sum, so neither a rounded decay nor a sum of many chunks in the
-// accumulator costs it bits.  B~ is three bf16 terms (24 bits) where S leaves
-// the walk in fp32, two (16 bits, far below the copy's 8) where only the copy is used.
+// accumulator costs it bits.  B~ is a sum of bf16 terms: three (24 bits), split off
+// the fp32 product, where S leaves the walk in fp32; two (16 bits) where only
+// the copy of S is used, by packed bf16 operations alone: with g^.. = f1 + f2 in
+// bf16 pieces, h = rn(b f1) and m = rn(b f2 + (b f1 - h)), the error of a bf16
+// product being a bf16 number.  (Four such terms for 24 bits cost the tensor cores more
+// than they save: states of 65536 x 16 x 128 in 133 us instead of 119.)
 //
 // Roles.  X warps (4): P from tensor memory, decayed, masked and packed back.
 // O warps (4): o_i from O1 and O2, through shared memory, to global memory.  Y
@@ -48,6 +52,11 @@ __device__ __forceinline__ void tmem_store8(uint32_t taddr, const uint32_t (&r)[
                  : "memory");
 }
 
+__device__ __forceinline__ void tmem_load8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
 // 16 columns of this thread's lane
 __device__ __forceinline__ void tmem_load16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
@@ -82,6 +91,8 @@ __device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
     return pair_of(r);
 }
 __device__ __forceinline__ Pair unpack_bf16(uint32_t w) { return {__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)}; }
+__device__ __forceinline__ __nv_bfloat162 as_pair(uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); }
+__device__ __forceinline__ uint32_t as_word(__nv_bfloat162 v) { return *reinterpret_cast<const uint32_t*>(&v); }
 __device__ __forceinline__ Pair at(const uint32_t* r) { return {__uint_as_float(r[0]), __uint_as_float(r[1])}; }
 
 __device__ __forceinline__ bool elect_one() {
@@ -104,7 +115,7 @@ __device__ __forceinline__ bool mbar_tries(uint32_t a, uint32_t parity) {
 }
 
 // Warps and shared memory.  Tiles of A: NA, of B and C: NB; the ring's slots hold
-// the second (and third) terms of STEP tokens of B~; the stage a group of SC
+// the terms of STEP tokens of B~ but the first; the stage a group of SC
 // output columns of each O warp.  At D = 64 two CTAs share an SM: sixteen warps of
 // 64 registers each (X and O are the same four), half of tensor memory, and
 // half of shared memory; a walk of one chunk after another leaves gaps that the other
@@ -124,7 +135,7 @@ struct TcLayout {
     static constexpr int STEP = !OUT ? 64 : TERMS == 3 ? 16 : 32;
     static constexpr int kItems = STEP / 4 * (D / 64);  // of 4 tokens by 64 channels in a step
     static constexpr int PER = kItems < kY ? kItems : kY;  // warps that share a step, kItems / PER items each
-    static constexpr int SC = D == 64 ? 32 : 64;
+    static constexpr int SC = D == 128 && TERMS == 2 ? 64 : 32;
     static constexpr int NA = OUT ? 1 : 0, NB = 2;
     static constexpr uint32_t kTile = kL * D * 2, kPart = STEP * D * 2, kStage = 32 * SC * 2;
     static constexpr uint32_t A = 0, B = NA * kTile, C = B + NB * kTile, ring = C + NB * kTile;
@@ -148,6 +159,8 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
     __shared__ __align__(8) unsigned long long bars[NBAR];
     __shared__ __align__(16) float pw[kL + 4];  // g^0 .. g^128
     __shared__ __align__(16) float down[16];    // g^15 .. g^0
+    __shared__ uint32_t pieces[TERMS == 2 ? kL + 1 : 1];  // f1 (low half) and f2 of each power
+
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort_flag;
 
@@ -189,6 +202,10 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
         const float f = (float)power((double)__ldg(p.gamma + h), tid);
         pw[tid] = f;
         if (tid < 16) down[15 - tid] = f;
+        if (TERMS == 2) {
+            const bf16 f1 = __float2bfloat16_rn(f), f2 = __float2bfloat16_rn(f - __bfloat162float(f1));
+            pieces[tid] = (uint32_t)__bfloat16_as_ushort(f1) | (uint32_t)__bfloat16_as_ushort(f2) << 16;
+        }
     }
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
@@ -393,7 +410,7 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
                     const int gap = REV ? col - row : row - col - 15;  // the row's distance to the group's near edge
                     const int nearest = REV ? col - quarter * 32 - 16 : quarter * 32 - col;  // -16 or 0 on the diagonal
                     uint32_t hi[8];
-                    if (nearest < -16 || (REV && col >= n)) {
+                    if (nearest < -16) {
 #pragma unroll
                         for (int j = 0; j < 8; ++j) hi[j] = 0u;
                     } else {
@@ -412,23 +429,28 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
                             const float f = pw[gap];
 #pragma unroll
                             for (int j = 0; j < 16; j += 4) {
-                                const float4 u = REV ? *reinterpret_cast<const float4*>(pw + j)
-                                                     : *reinterpret_cast<const float4*>(down + j);
+                                const float4 u = *reinterpret_cast<const float4*>((REV ? pw : down) + j);
                                 const Pair x = mul2(mul2(at(r + j), {f, f}), {u.x, u.y});
                                 const Pair y = mul2(mul2(at(r + j + 2), {f, f}), {u.z, u.w});
                                 hi[j / 2] = pack_bf16(x.x, x.y);
                                 hi[j / 2 + 1] = pack_bf16(y.x, y.y);
                             }
                         }
-                        if (REV && col + 16 > n) {  // tokens behind the end: whatever they held
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                if (col + 2 * j >= n) hi[j] = 0u;
-                                else if (col + 2 * j + 1 >= n) hi[j] &= 0xffffu;
-                            }
-                        }
                     }
                     tmem_store8(tP + lane_off + col / 2, hi);
+                }
+                if (REV && n < kL) {
+                    // scores of tokens behind the end: zeros, whatever they held
+                    tmem_st_wait();
+#pragma unroll 1
+                    for (int col = n & ~15; col < kL; col += 16) {
+                        uint32_t hi[8];
+                        tmem_load8(tP + lane_off + col / 2, hi);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) hi[j] = col + 2 * j >= n ? 0u : col + 2 * j + 1 >= n ? hi[j] & 0xffffu : hi[j];
+                        tmem_store8(tP + lane_off + col / 2, hi);
+                    }
                 }
                 if (n < kL) {
                     if (!wait_bar(LC + it % NB, (uint32_t)(it / NB) & 1)) break;
@@ -563,34 +585,45 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
 #pragma unroll 1
             for (int q = group; q < STEPS; q += GROUPS) {
                 const int slot = q & 1, use = STEPS / 2 * it + (q >> 1);
-                uint32_t x[ITEMS][4], y[ITEMS][4], z[ITEMS][4], place[ITEMS];
+                uint32_t more[ITEMS][TERMS - 1][4], place[ITEMS];
 #pragma unroll
                 for (int i = 0; i < ITEMS; ++i) {
                     const int m = item + PER * i, r = 4 * (m % (STEP / 4)) + (lane >> 3), t = STEP * q + r;
                     const uint32_t a = B.chunk(t, m / (STEP / 4), lane & 7);
                     place[i] = tR(slot, 0).chunk(r, m / (STEP / 4), lane & 7);
-                    ld_shared_v4(a, x[i][0], x[i][1], x[i][2], x[i][3]);
+                    uint32_t x[4];
+                    ld_shared_v4(a, x[0], x[1], x[2], x[3]);
                     const bool in = t < n;
-                    const float f = in ? pw[REV ? t + 1 : n - 1 - t] : 0.f;
+                    const int far = in ? (REV ? t + 1 : n - 1 - t) : 0;
+                    if constexpr (TERMS == 2) {
+                        const uint32_t f12 = pieces[far];
+                        const __nv_bfloat162 f1 = as_pair(__byte_perm(f12, 0u, 0x1010)), f2 = as_pair(__byte_perm(f12, 0u, 0x3232));
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        Pair u = mul2(unpack_bf16(in ? x[i][j] : 0u), {f, f});
-                        x[i][j] = pack_bf16(u.x, u.y);
-                        u = fma2(unpack_bf16(x[i][j]), {-1.f, -1.f}, u);
-                        y[i][j] = pack_bf16(u.x, u.y);
-                        if (TERMS == 3) {
-                            u = fma2(unpack_bf16(y[i][j]), {-1.f, -1.f}, u);
-                            z[i][j] = pack_bf16(u.x, u.y);
+                        for (int j = 0; j < 4; ++j) {
+                            const __nv_bfloat162 v = as_pair(in ? x[j] : 0u), h1 = __hmul2_rn(v, f1);
+                            x[j] = as_word(h1);
+                            more[i][0][j] = as_word(__hfma2(v, f2, __hfma2(v, f1, __hneg2(h1))));
+                        }
+                    } else {
+                        const float f = pw[far];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            Pair u = mul2(unpack_bf16(in ? x[j] : 0u), {f, f});
+                            x[j] = pack_bf16(u.x, u.y);
+                            u = fma2(unpack_bf16(x[j]), {-1.f, -1.f}, u);
+                            more[i][0][j] = pack_bf16(u.x, u.y);
+                            u = fma2(unpack_bf16(more[i][0][j]), {-1.f, -1.f}, u);
+                            more[i][TERMS - 2][j] = pack_bf16(u.x, u.y);
                         }
                     }
-                    st_shared_v4(a, x[i][0], x[i][1], x[i][2], x[i][3]);
+                    st_shared_v4(a, x[0], x[1], x[2], x[3]);
                 }
                 if (use > 0 && !wait_bar(RF + slot, (uint32_t)(use - 1) & 1)) { ok = false; break; }
 #pragma unroll
-                for (int i = 0; i < ITEMS; ++i) {
-                    st_shared_v4(place[i], y[i][0], y[i][1], y[i][2], y[i][3]);
-                    if (TERMS == 3) st_shared_v4(place[i] + LY::kPart, z[i][0], z[i][1], z[i][2], z[i][3]);
-                }
+                for (int i = 0; i < ITEMS; ++i)
+#pragma unroll
+                    for (int t = 0; t < TERMS - 1; ++t)
+                        st_shared_v4(place[i] + t * LY::kPart, more[i][t][0], more[i][t][1], more[i][t][2], more[i][t][3]);
                 fence_proxy_async();
                 arrive(KQ + slot);
             }
