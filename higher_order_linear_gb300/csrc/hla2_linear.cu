@@ -201,17 +201,21 @@ __global__ void __launch_bounds__(kWalkThreads, 1) lin_walk_kernel(const LinWalk
 
 // The states that enter the segments, in place: slot 0 is the state before the
 // first, slot w + 1 becomes g^(tokens of w) slot w + (its own sum); `segments`
-// have one.  A thread for each element; the loads do not wait for the sums.
+// have one.  A thread
+// for each element (or four: N); the loads do not wait for the sums.
+template <int N>
 __global__ void __launch_bounds__(256) lin_scan_kernel(const LinWalk p, int chunk, int segments) {
-    const int R = p.da * p.dc, e = blockIdx.x * 256 + threadIdx.x, bh = blockIdx.y;
+    const int R = p.da * p.dc, e = (blockIdx.x * 256 + threadIdx.x) * N, bh = blockIdx.y;
     __shared__ float f[256];
     const int len = length_of(p, bh / p.H);
     const double g = (double)__ldg(p.gamma + bh % p.H);
     float* const rec = p.rec + (size_t)bh * (p.nseg + 1) * R + e;
-    float acc = 0.f;
+    Lane<float, 4, N == 4> acc;
+    auto first = [&](int j) { return p.s_in ? p.s_in[(size_t)bh * R + ((e + j) / p.dc) * p.in_r + ((e + j) % p.dc) * p.in_c] : 0.f; };
     if (e < R) {
-        if (p.s_in) acc = p.s_in[(size_t)bh * R + (e / p.dc) * p.in_r + (e % p.dc) * p.in_c];
-        rec[0] = acc;
+#pragma unroll
+        for (int j = 0; j < N; ++j) acc.v[j] = first(j);
+        acc.store(rec, N);
     }
     for (int base = 0; base < segments; base += 256) {
         const int w = base + threadIdx.x;
@@ -225,20 +229,26 @@ __global__ void __launch_bounds__(256) lin_scan_kernel(const LinWalk p, int chun
         if (e < R) {
             for (int i0 = 0; i0 < m; i0 += 8) {  // eight loads on their way at a time
                 float* const slot = rec + (size_t)(base + i0 + 1) * R;
-                float own[8];
+                Lane<float, 4, N == 4> own[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) own[i] = i0 + i < m ? slot[(size_t)i * R] : 0.f;
+                for (int i = 0; i < 8; ++i)
+                    if (i0 + i < m) own[i].load(slot + (size_t)i * R, N);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     if (i0 + i < m) {
-                        acc = fmaf(f[i0 + i], acc, own[i]);
-                        slot[(size_t)i * R] = acc;
+#pragma unroll
+                        for (int j = 0; j < N; ++j) acc.v[j] = fmaf(f[i0 + i], acc.v[j], own[i].v[j]);
+                        acc.store(slot + (size_t)i * R, N);
                     }
             }
         }
         __syncthreads();
     }
-    if (e < R && p.s_out) p.s_out[(size_t)bh * R + (e / p.dc) * p.out_r + (e % p.dc) * p.out_c] = acc;
+    if (e < R && p.s_out) {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            p.s_out[(size_t)bh * R + ((e + j) / p.dc) * p.out_r + ((e + j) % p.dc) * p.out_c] = acc.v[j];
+    }
 }
 
 // Zeros in the rows behind each sequence's end (the gradients there).
@@ -319,24 +329,35 @@ __global__ void __launch_bounds__(256) lin_step_kernel(const float* state, const
 }
 
 // ------------------------------------------------------------------ host ----
-// Segments per head, each a CTA, `ctas` of which fill an SM: the count with the least time
-// of rounds of CTAs (a chunk is the unit; a CTA's start costs about one; the
-// states' pass reads half of what the second one moves).
-void plan_segments(int BH, int T, int chunk, int ctas, int* nseg, int* seglen, int* nchunk) {
-    const int n = (T + chunk - 1) / chunk, sms = sm_count() * ctas;
+// Segments per head, each a CTA.  The count with the least time, in units of a
+// chunk of the output walk: rounds of CTAs, each its chunks and about one to
+// start; the states' walk, the scan and two more launches where there are several
+// segments.  Measured: a chunk takes 2.8 us on the tensor cores (1.25 times that with
+// two CTAs on the SM), the states' walk 0.6 of the output walk, the scan and the
+// launches 17 us; the CUDA cores take some 20 us for a chunk and 0.45 for its states.
+struct SegmentCost {
+    int ctas;  // to an SM
+    double shared, states, extra;
+};
+SegmentCost segment_cost(bool tc, int d, int dv) {
+    return tc ? SegmentCost{lin_tc_ctas(d, dv), 1.25, 0.6, 6.0} : SegmentCost{1, 1.0, 0.45, 0.5};
+}
+void plan_segments(int BH, int T, int chunk, const SegmentCost& c, int* nseg, int* seglen, int* nchunk) {
+    const int n = (T + chunk - 1) / chunk, sms = sm_count();
     double best = 0;
     *nchunk = n; *nseg = 1; *seglen = n;
     for (int want = 1; want <= n && want <= 1024; ++want) {
         const int len = (n + want - 1) / want, segs = (n + len - 1) / len;
         if (segs != want) continue;
-        const double rounds = (double)(((long long)BH * segs + sms - 1) / sms);
-        const double cost = rounds * (len + 1) * (segs > 1 ? 1.5 : 1.0) + (segs > 1 ? 2.0 + 0.05 * segs : 0.0);
+        const long long blocks = (long long)BH * segs, slots = (long long)sms * c.ctas;
+        double cost = (double)((blocks + slots - 1) / slots) * (len + 1) * (blocks > sms ? c.shared : 1.0);
+        if (segs > 1) cost = cost * (1.0 + c.states) + c.extra + 0.05 * segs;
         if (want == 1 || cost < best) {
             best = cost;
             *nseg = segs;
             *seglen = len;
         }
-        if ((long long)BH * want > 4LL * sms) break;
+        if (blocks > 4 * slots) break;
     }
 }
 
@@ -354,7 +375,7 @@ cudaError_t launch_simple(const LinWalk& w, bool states, cudaStream_t s) {
 // The path and the segments of a walk.
 bool plan_walk(LinWalk& w, int dtype) {
     const bool tc = lin_tc_supported(w, dtype);
-    plan_segments(w.B * w.H, w.T, tc ? kLinTcChunk : kTokens, tc ? lin_tc_ctas(w.da, w.dc) : 1, &w.nseg, &w.seglen, &w.nchunk);
+    plan_segments(w.B * w.H, w.T, tc ? kLinTcChunk : kTokens, segment_cost(tc, w.da, w.dc), &w.nseg, &w.seglen, &w.nchunk);
     w.rec_r = w.dc;
     w.rec_c = 1;
     return tc;
@@ -369,8 +390,9 @@ cudaError_t launch_walk(const LinWalk& w, int dtype, bool tc, bool states, cudaS
 cudaError_t enter_states(const LinWalk& w, int dtype, bool tc, cudaStream_t s) {
     if (w.nseg == 1) return cudaSuccess;
     if (cudaError_t e = launch_walk(w, dtype, tc, true, s)) return e;
-    lin_scan_kernel<<<dim3((w.da * w.dc + 255) / 256, w.B * w.H), 256, 0, s>>>(w, tc ? kLinTcChunk : kTokens,
-                                                                               lin_state_segments(w));
+    const int R = w.da * w.dc, per = R % 4 ? 256 : 1024;
+    auto scan = R % 4 ? lin_scan_kernel<1> : lin_scan_kernel<4>;
+    scan<<<dim3((R + per - 1) / per, w.B * w.H), 256, 0, s>>>(w, tc ? kLinTcChunk : kTokens, lin_state_segments(w));
     note_launches(1);
     return cudaGetLastError();
 }
@@ -409,7 +431,7 @@ size_t walk_bytes(int B, int H, int T, int d, int dv) {
     size_t most = 0;
     for (int chunk : {kLinTcChunk, kTokens}) {
         int nseg, seglen, nchunk;
-        plan_segments(B * H, T, chunk, chunk == kLinTcChunk ? lin_tc_ctas(d, dv) : 1, &nseg, &seglen, &nchunk);
+        plan_segments(B * H, T, chunk, segment_cost(chunk == kLinTcChunk, d, dv), &nseg, &seglen, &nchunk);
         if (nseg > 1) most = max(most, (size_t)B * H * (nseg + 1) * d * dv * 4);
     }
     return (most + 255) & ~size_t(255);
