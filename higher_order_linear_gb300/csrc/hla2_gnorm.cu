@@ -49,9 +49,11 @@ struct GNormParams {
 
 __device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
 // the activation and its slope
-__device__ __forceinline__ float act(float x, bool silu) { return silu ? x * sigmoid(x) : x; }
-__device__ __forceinline__ void act_slope(float x, bool silu, float& v, float& s) {
-    if (silu) {
+template <bool SILU>
+__device__ __forceinline__ float act(float x) { return SILU ? x * sigmoid(x) : x; }
+template <bool SILU>
+__device__ __forceinline__ void act_slope(float x, float& v, float& s) {
+    if (SILU) {
         const float g = sigmoid(x);
         v = x * g;
         s = fmaf(v, 1.f - g, g);
@@ -147,12 +149,15 @@ struct Spots {
     }
 };
 
-// Sums over a unit's threads; sh: two rows of kThreads / 32, used alternately.
+// Sums over a unit's threads (B: two of them); sh: two rows of kThreads / 32, used alternately.
+template <bool B>
 __device__ __forceinline__ void unit_sum(float& a, float& b, int tpr, float2* sh) {
-    for (int o = min(tpr, 32) >> 1; o > 0; o >>= 1) {
-        a += __shfl_xor_sync(0xffffffffu, a, o);
-        b += __shfl_xor_sync(0xffffffffu, b, o);
-    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        if (o < tpr) {
+            a += __shfl_xor_sync(0xffffffffu, a, o);
+            if (B) b += __shfl_xor_sync(0xffffffffu, b, o);
+        }
     if (tpr > 32) {
         const int warp = threadIdx.x >> 5, nw = tpr >> 5, w0 = warp / nw * nw;
         if ((threadIdx.x & 31) == 0) sh[warp] = make_float2(a, b);
@@ -160,7 +165,7 @@ __device__ __forceinline__ void unit_sum(float& a, float& b, int tpr, float2* sh
         a = b = 0.f;
         for (int i = 0; i < nw; ++i) {
             a += sh[w0 + i].x;
-            b += sh[w0 + i].y;
+            if (B) b += sh[w0 + i].y;
         }
     }
 }
@@ -168,20 +173,20 @@ __device__ __forceinline__ void unit_sum(float& a, float& b, int tpr, float2* sh
 // --------------------------------------------- units in registers ----
 // A block keeps its groups and takes every gridDim.x-th run of samples: its
 // weights stay in registers, and the next samples' values are on their way.
-template <typename T, bool VEC>
+template <typename T, bool VEC, bool GATE, bool SILU>
 __global__ void __launch_bounds__(kThreads, VEC ? kFwdBlocks : 2) gnorm_unit_kernel(const GNormParams p) {
     __shared__ float2 sh[2][kThreads / 32];
     const int unit = threadIdx.x / p.tpr, lane = threadIdx.x % p.tpr;
     const int s = unit / p.gpb, g = blockIdx.y * p.gpb + unit % p.gpb;
     const int values = p.L * p.cg, c0 = g * p.cg;
-    const bool mine = s < p.spb && g < p.G;
-    const Spots<VEC> at(lane, p.tpr, mine ? values : 0, p.cg);
+    const Spots<VEC> at(lane, p.tpr, s < p.spb && g < p.G ? values : 0, p.cg);
+    const bool mine = at.n > 0;
     const float inv = 1.f / (float)values;
-    typename Spots<VEC>::template Raw<T> xr, zr;
+    typename Spots<VEC>::template Raw<T> xr{}, zr{};
     auto fetch = [&](long long n) {
         if (n >= p.N) return;
         at.load(static_cast<const T*>(p.x.p) + n * p.x.sn + c0, p.x.sl, xr);
-        if (p.z.p) at.load(static_cast<const T*>(p.z.p) + n * p.z.sn + c0, p.z.sl, zr);
+        if (GATE) at.load(static_cast<const T*>(p.z.p) + n * p.z.sn + c0, p.z.sl, zr);
     };
     long long n = (long long)blockIdx.x * p.spb + s;
     const long long step = (long long)gridDim.x * p.spb;
@@ -190,35 +195,33 @@ __global__ void __launch_bounds__(kThreads, VEC ? kFwdBlocks : 2) gnorm_unit_ker
     at.weights(p.w, p.wdtype, c0, 1.f, w);
     at.weights(p.b, p.wdtype, c0, 0.f, b);
     for (long long n0 = (long long)blockIdx.x * p.spb; n0 < p.N; n0 += step, n += step) {
-        float x[8], z[8], sum = 0.f, none = 0.f;
+        float x[8], z[8], sum = 0.f, sq = 0.f, none = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < at.n) {
-                x[j] = xr.get(j);
-                z[j] = p.z.p ? zr.get(j) : 0.f;
-                if (n < p.N) sum += x[j];
-            }
+        for (int j = 0; j < 8; ++j) {
+            x[j] = VEC || j < at.n ? xr.get(j) : 0.f;
+            if (GATE) z[j] = VEC || j < at.n ? zr.get(j) : 0.f;
+            sum += x[j];
+        }
         fetch(n + step);
-        unit_sum(sum, none, p.tpr, sh[0]);
-        const float mean = sum * inv;
-        float sq = 0.f;
+        if (!mine) sum = 0.f;
+        unit_sum<false>(sum, none, p.tpr, sh[0]);
+        const float mean = sum / (float)values;  // (a quotient: equal values have their mean)
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < at.n) {
-                x[j] -= mean;
-                sq = fmaf(x[j], x[j], sq);
-            }
-        unit_sum(sq, none, p.tpr, sh[1]);
+        for (int j = 0; j < 8; ++j) {
+            x[j] -= mean;
+            if (VEC || j < at.n) sq = fmaf(x[j], x[j], sq);
+        }
+        if (!mine) sq = 0.f;
+        unit_sum<false>(sq, none, p.tpr, sh[1]);
         if (!mine || n >= p.N) continue;
         const float rstd = 1.f / sqrtf(fmaf(sq, inv, p.eps));
         if (p.stats && lane == 0) *reinterpret_cast<float2*>(p.stats + (n * p.G + g) * 2) = make_float2(mean, rstd);
         float y[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < at.n) {
-                const float v = fmaf(x[j] * rstd, w[j], b[j]);
-                y[j] = p.z.p ? v * act(z[j], p.silu) : act(v, p.silu);
-            }
+        for (int j = 0; j < 8; ++j) {
+            const float v = fmaf(x[j] * rstd, w[j], b[j]);
+            y[j] = GATE ? v * act<SILU>(z[j]) : act<SILU>(v);
+        }
         at.store(static_cast<T*>(p.y) + n * p.yn + c0, p.yl, y);
     }
 }
@@ -226,23 +229,23 @@ __global__ void __launch_bounds__(kThreads, VEC ? kFwdBlocks : 2) gnorm_unit_ker
 // The gradient.  A block keeps its groups and takes every gridDim.x-th run of
 // samples, so that a thread's channels stay its own and dw and db add up in
 // registers; then the block's threads add theirs, one line of sums to a block.
-template <typename T, bool VEC>
+template <typename T, bool VEC, bool GATE, bool SILU>
 __global__ void __launch_bounds__(kThreads, VEC ? kBwdBlocks : 1) gnorm_unit_bwd_kernel(const GNormParams p) {
     __shared__ float2 sh[2][kThreads / 32];
     extern __shared__ float2 sums[];  // [unit of the block][value]
     const int unit = threadIdx.x / p.tpr, lane = threadIdx.x % p.tpr;
     const int s = unit / p.gpb, g = blockIdx.y * p.gpb + unit % p.gpb;
     const int values = p.L * p.cg, c0 = g * p.cg;
-    const bool mine = s < p.spb && g < p.G;
-    const Spots<VEC> at(lane, p.tpr, mine ? values : 0, p.cg);
+    const Spots<VEC> at(lane, p.tpr, s < p.spb && g < p.G ? values : 0, p.cg);
+    const bool mine = at.n > 0;
     const float inv = 1.f / (float)values;
-    typename Spots<VEC>::template Raw<T> xr, yr, zr;
+    typename Spots<VEC>::template Raw<T> xr{}, yr{}, zr{};
     float2 sr = make_float2(0.f, 0.f);
     auto fetch = [&](long long n) {
         if (!mine || n >= p.N) return;
         at.load(static_cast<const T*>(p.x.p) + n * p.x.sn + c0, p.x.sl, xr);
         at.load(static_cast<const T*>(p.dy.p) + n * p.dy.sn + c0, p.dy.sl, yr);
-        if (p.z.p) at.load(static_cast<const T*>(p.z.p) + n * p.z.sn + c0, p.z.sl, zr);
+        if (GATE) at.load(static_cast<const T*>(p.z.p) + n * p.z.sn + c0, p.z.sl, zr);
         sr = __ldg(reinterpret_cast<const float2*>(p.stats + (n * p.G + g) * 2));
     };
     const long long step = (long long)gridDim.x * p.spb;
@@ -256,39 +259,39 @@ __global__ void __launch_bounds__(kThreads, VEC ? kBwdBlocks : 1) gnorm_unit_bwd
         const bool live = mine && n < p.N;
         float x[8], dy[8], z[8], dgate[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (live && j < at.n) {
-                x[j] = xr.get(j);
-                dy[j] = yr.get(j);
-                z[j] = p.z.p ? zr.get(j) : 0.f;
-            }
+        for (int j = 0; j < 8; ++j) {
+            const bool in = VEC || j < at.n;
+            x[j] = in ? xr.get(j) : 0.f;
+            dy[j] = in ? yr.get(j) : 0.f;
+            if (GATE) z[j] = in ? zr.get(j) : 0.f;
+        }
         const float2 st = sr;
         fetch(n + step);
         float m1 = 0.f, m2 = 0.f;
+        if (live)
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (live && j < at.n) {
+            for (int j = 0; j < 8; ++j) {
+                if (!VEC && j >= at.n) break;
                 x[j] = (x[j] - st.x) * st.y;
                 const float v = fmaf(x[j], w[j], b[j]);
                 float value, slope;
-                act_slope(p.z.p ? z[j] : v, p.silu, value, slope);
-                dgate[j] = dy[j] * v * slope;
-                const float d = dy[j] * (p.z.p ? value : slope);
+                act_slope<SILU>(GATE ? z[j] : v, value, slope);
+                if (GATE) dgate[j] = dy[j] * v * slope;
+                const float d = dy[j] * (GATE ? value : slope);
                 db[j] += d;
                 dw[j] = fmaf(d, x[j], dw[j]);
                 dy[j] = d * w[j];
                 m1 += dy[j];
                 m2 = fmaf(dy[j], x[j], m2);
             }
-        unit_sum(m1, m2, p.tpr, sh[turn]);
+        unit_sum<true>(m1, m2, p.tpr, sh[turn]);
         if (!live) continue;
         m1 *= inv;
         m2 *= inv;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < at.n) x[j] = st.y * (dy[j] - m1 - x[j] * m2);
+        for (int j = 0; j < 8; ++j) x[j] = st.y * (dy[j] - m1 - x[j] * m2);
         at.store(static_cast<T*>(p.y) + n * p.yn + c0, p.yl, x);
-        if (p.z.p) at.store(static_cast<T*>(p.dz) + n * p.dzn + c0, p.dzl, dgate);
+        if (GATE) at.store(static_cast<T*>(p.dz) + n * p.dzn + c0, p.dzl, dgate);
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -353,7 +356,7 @@ __device__ __forceinline__ bool add_rows(const RunSpot& r, float (&a)[8], float 
 }
 
 // GRAD: sums of dz and dz n of each channel; else mean and sum of squares about it.
-template <typename T, bool VEC, bool GRAD>
+template <typename T, bool VEC, bool GRAD, bool GATE, bool SILU>
 __global__ void __launch_bounds__(kThreads) gnorm_sums_kernel(const GNormParams p) {
     __shared__ float2 sh[kThreads][8];
     const RunSpot r = run_spot(p);
@@ -385,13 +388,13 @@ __global__ void __launch_bounds__(kThreads) gnorm_sums_kernel(const GNormParams 
             } else {
                 float dy[8], z[8];
                 load8<T, VEC>(static_cast<const T*>(p.dy.p) + r.n * p.dy.sn + l * p.dy.sl + r.c, r.live, dy);
-                if (p.z.p) load8<T, VEC>(static_cast<const T*>(p.z.p) + r.n * p.z.sn + l * p.z.sl + r.c, r.live, z);
+                if (GATE) load8<T, VEC>(static_cast<const T*>(p.z.p) + r.n * p.z.sn + l * p.z.sl + r.c, r.live, z);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const float n = (v[j] - mean[j]) * rstd[j];
                     float value, slope;
-                    act_slope(p.z.p ? z[j] : fmaf(n, w[j], b[j]), p.silu, value, slope);
-                    const float d = dy[j] * (p.z.p ? value : slope);
+                    act_slope<SILU>(GATE ? z[j] : fmaf(n, w[j], b[j]), value, slope);
+                    const float d = dy[j] * (GATE ? value : slope);
                     a[j] = fmaf(d, n, a[j]);
                     q[j] += d;
                 }
@@ -409,13 +412,23 @@ __global__ void __launch_bounds__(kThreads) gnorm_sums_kernel(const GNormParams 
         }
 }
 
-__device__ __forceinline__ double block_sum(double v, double* sh) {
+// A running sum with its rounding errors kept (64-bit sums would take 60 times as long here)
+struct LongSum {
+    float hi = 0.f, lo = 0.f;
+    __device__ __forceinline__ void add(float x) {
+        const float s = hi + x, t = s - hi;
+        lo += (hi - (s - t)) + (x - t);
+        hi = s;
+    }
+};
+__device__ __forceinline__ float block_sum(const LongSum& sum, float* sh) {
+    float v = sum.hi + sum.lo;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     __syncthreads();
     if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = 0;
+    v = 0.f;
 #pragma unroll
     for (int i = 0; i < kThreads / 32; ++i) v += sh[i];
     return v;
@@ -425,39 +438,38 @@ __device__ __forceinline__ double block_sum(double v, double* sh) {
 // the means of t and t n, which go behind the partial sums.
 template <bool GRAD>
 __global__ void __launch_bounds__(kThreads) gnorm_fold_kernel(const GNormParams p, float* out) {
-    __shared__ double sh[kThreads / 32];
+    __shared__ float sh[kThreads / 32];
     const long long n = blockIdx.x / p.G;
     const int g = (int)(blockIdx.x % p.G), items = p.runs * p.cg;
     const float* const part = p.part + n * p.runs * 2 * p.C + g * p.cg;
-    const double count = (double)p.L * p.cg;
-    double a = 0, q = 0;
+    const float count = (float)p.L * (float)p.cg;  // (divided by, so that equal values have their mean)
+    LongSum first, second;
     for (int i = threadIdx.x; i < items; i += kThreads) {
         const int k = i / p.cg, c = i - k * p.cg;
         const float* v = part + (long long)k * 2 * p.C + c;
         if (GRAD) {
-            const double w = weight_at(p.w, p.wdtype, g * p.cg + c, 1.f);
-            a += w * v[p.C];
-            q += w * v[0];
+            const float w = weight_at(p.w, p.wdtype, g * p.cg + c, 1.f);
+            first.add(w * v[p.C]);
+            second.add(w * v[0]);
         } else {
-            a += (double)min(p.run, p.L - k * p.run) * v[0];
+            first.add((float)min(p.run, p.L - k * p.run) * v[0]);
         }
     }
-    a = block_sum(a, sh) / count;
+    const float a = block_sum(first, sh) / count;
     if (!GRAD)
         for (int i = threadIdx.x; i < items; i += kThreads) {
             const int k = i / p.cg, c = i - k * p.cg;
             const float* v = part + (long long)k * 2 * p.C + c;
-            const double d = v[0] - a;
-            q += v[p.C] + (double)min(p.run, p.L - k * p.run) * d * d;
+            const float d = v[0] - a;
+            second.add(fmaf((float)min(p.run, p.L - k * p.run) * d, d, v[p.C]));
         }
-    q = block_sum(q, sh) / count;
+    const float q = block_sum(second, sh) / count;
     if (threadIdx.x == 0)
-        *reinterpret_cast<float2*>(out + 2 * (long long)blockIdx.x) =
-            make_float2((float)a, GRAD ? (float)q : (float)(1.0 / sqrt(q + (double)p.eps)));
+        *reinterpret_cast<float2*>(out + 2 * (long long)blockIdx.x) = make_float2(a, GRAD ? q : 1.f / sqrtf(q + p.eps));
 }
 
 // y, or (GRAD) dx and dgate; means: the gradient's, [N][G][2]
-template <typename T, bool VEC, bool GRAD>
+template <typename T, bool VEC, bool GRAD, bool GATE, bool SILU>
 __global__ void __launch_bounds__(kThreads) gnorm_apply_kernel(const GNormParams p, const float* means) {
     const RunSpot r = run_spot(p);
     if (r.live <= 0) return;
@@ -480,17 +492,17 @@ __global__ void __launch_bounds__(kThreads) gnorm_apply_kernel(const GNormParams
     for (int l = r.l0 + r.row; l < r.l1; l += r.rows) {
         float x[8], z[8], dy[8];
         load8<T, VEC>(static_cast<const T*>(p.x.p) + r.n * p.x.sn + l * p.x.sl + r.c, r.live, x);
-        if (p.z.p) load8<T, VEC>(static_cast<const T*>(p.z.p) + r.n * p.z.sn + l * p.z.sl + r.c, r.live, z);
+        if (GATE) load8<T, VEC>(static_cast<const T*>(p.z.p) + r.n * p.z.sn + l * p.z.sl + r.c, r.live, z);
         if (GRAD) load8<T, VEC>(static_cast<const T*>(p.dy.p) + r.n * p.dy.sn + l * p.dy.sl + r.c, r.live, dy);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float n = (x[j] - mean[j]) * rstd[j], v = fmaf(n, w[j], b[j]);
             if (!GRAD) {
-                x[j] = p.z.p ? v * act(z[j], p.silu) : act(v, p.silu);
+                x[j] = GATE ? v * act<SILU>(z[j]) : act<SILU>(v);
             } else {
                 float value, slope;
-                act_slope(p.z.p ? z[j] : v, p.silu, value, slope);
-                const float t = dy[j] * (p.z.p ? value : slope) * w[j];
+                act_slope<SILU>(GATE ? z[j] : v, value, slope);
+                const float t = dy[j] * (GATE ? value : slope) * w[j];
                 z[j] = dy[j] * v * slope;
                 x[j] = rstd[j] * (t - m1[j] - n * m2[j]);
             }
@@ -498,7 +510,7 @@ __global__ void __launch_bounds__(kThreads) gnorm_apply_kernel(const GNormParams
         Lane<T, 8, VEC> o;
         o.set(x);
         o.store(static_cast<T*>(p.y) + r.n * p.yn + l * p.yl + r.c, r.live);
-        if (GRAD && p.z.p) {
+        if (GRAD && GATE) {
             o.set(z);
             o.store(static_cast<T*>(p.dz) + r.n * p.dzn + l * p.dzl + r.c, r.live);
         }
@@ -556,8 +568,8 @@ GPlan gnorm_plan(long long N, int L, int C, int G, bool grad) {
         return g;
     }
     const int across = (C + kUnit - 1) / kUnit;
-    // enough blocks to fill the SMs several times, runs of 16 positions or more
-    long long runs = (8LL * sm_count() + N * across - 1) / (N * across);
+    // enough blocks to fill the SMs, runs of 16 positions or more
+    long long runs = (4LL * sm_count() + N * across - 1) / (N * across);
     if (runs > (L + 15) / 16) runs = (L + 15) / 16;
     if (runs < 1) runs = 1;
     g.run = (int)((L + runs - 1) / runs);
@@ -595,32 +607,37 @@ bool wide(const void* p, long long sn, long long sl, long long N, int L, int es)
 
 template <bool GRAD>
 cudaError_t run_gnorm(GNormParams p, const GPlan& g, int dtype, bool vec, cudaStream_t s) {
-    auto typed = [&](auto t, auto v) {
+    auto typed = [&](auto t, auto v, auto gate, auto silu) {
         using T = decltype(t);
-        constexpr bool VEC = decltype(v)::value;
+        constexpr bool VEC = decltype(v)::value, GATE = decltype(gate)::value, SILU = decltype(silu)::value;
         if (g.unit) {
-            const unsigned across = (p.G + g.gpb - 1) / g.gpb;
+            const dim3 grid(g.blocks, (p.G + g.gpb - 1) / g.gpb);
             if (GRAD)
-                gnorm_unit_bwd_kernel<T, VEC><<<dim3(g.blocks, across), kThreads,
-                                                (size_t)g.spb * g.gpb * p.L * p.cg * sizeof(float2), s>>>(p);
+                gnorm_unit_bwd_kernel<T, VEC, GATE, SILU><<<grid, kThreads, (size_t)g.spb * g.gpb * p.L * p.cg * sizeof(float2), s>>>(p);
             else
-                gnorm_unit_kernel<T, VEC><<<dim3(g.blocks, across), kThreads, 0, s>>>(p);
+                gnorm_unit_kernel<T, VEC, GATE, SILU><<<grid, kThreads, 0, s>>>(p);
             note_launches(1);
             return cudaGetLastError();
         }
         const dim3 grid((unsigned)(p.N * g.runs), (p.C + kUnit - 1) / kUnit);
         float* const means = p.part + g.part;
         float* const folded = GRAD || !p.stats ? means : p.stats;
-        gnorm_sums_kernel<T, VEC, GRAD><<<grid, kThreads, 0, s>>>(p);
+        gnorm_sums_kernel<T, VEC, GRAD, GATE, SILU><<<grid, kThreads, 0, s>>>(p);
         gnorm_fold_kernel<GRAD><<<(unsigned)(p.N * p.G), kThreads, 0, s>>>(p, folded);
         if (!GRAD) p.stats = folded;
-        gnorm_apply_kernel<T, VEC, GRAD><<<grid, kThreads, 0, s>>>(p, means);
+        gnorm_apply_kernel<T, VEC, GRAD, GATE, SILU><<<grid, kThreads, 0, s>>>(p, means);
         note_launches(3);
         return cudaGetLastError();
     };
+    using yes = std::true_type;
+    using no = std::false_type;
+    auto acted = [&](auto t, auto v) {
+        if (p.z.p) return p.silu ? typed(t, v, yes{}, yes{}) : typed(t, v, yes{}, no{});
+        return p.silu ? typed(t, v, no{}, yes{}) : typed(t, v, no{}, no{});
+    };
     cudaError_t e;
-    if (dtype == HLA2_DTYPE_BF16) e = vec ? typed(bf16{}, std::true_type{}) : typed(bf16{}, std::false_type{});
-    else e = vec ? typed(float{}, std::true_type{}) : typed(float{}, std::false_type{});
+    if (dtype == HLA2_DTYPE_BF16) e = vec ? acted(bf16{}, yes{}) : acted(bf16{}, no{});
+    else e = vec ? acted(float{}, yes{}) : acted(float{}, no{});
     if (GRAD && e == cudaSuccess && p.dw) {
         gnorm_lines_kernel<<<(2 * p.C + kFoldColumns - 1) / kFoldColumns, kFoldThreads, 0, s>>>(p.part, p.dw, g.lines, 2 * p.C);
         note_launches(1);
