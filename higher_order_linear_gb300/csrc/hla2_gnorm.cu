@@ -22,7 +22,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kUnit = kThreads * 8;  // the most values of a unit in registers
 constexpr int kMaxChannels = 16384;
-constexpr int kFwdBlocks = 4, kBwdBlocks = 2;  // blocks of units in registers that an SM holds
+constexpr int kFwdBlocks = 3, kBwdBlocks = 2;  // blocks of units in registers that an SM holds
+constexpr int kRunBlocks = 3;                  // and of runs of large units
 
 struct View {
     const void* p;
@@ -182,15 +183,17 @@ __global__ void __launch_bounds__(kThreads, VEC ? kFwdBlocks : 2) gnorm_unit_ker
     const Spots<VEC> at(lane, p.tpr, s < p.spb && g < p.G ? values : 0, p.cg);
     const bool mine = at.n > 0;
     const float inv = 1.f / (float)values;
-    typename Spots<VEC>::template Raw<T> xr{}, zr{};
-    auto fetch = [&](long long n) {
+    constexpr int AHEAD = VEC && sizeof(T) == 2 ? 2 : 1;  // samples on their way
+    typename Spots<VEC>::template Raw<T> xr[AHEAD]{}, zr[AHEAD]{};
+    auto fetch = [&](long long n, int k) {
         if (n >= p.N) return;
-        at.load(static_cast<const T*>(p.x.p) + n * p.x.sn + c0, p.x.sl, xr);
-        if (GATE) at.load(static_cast<const T*>(p.z.p) + n * p.z.sn + c0, p.z.sl, zr);
+        at.load(static_cast<const T*>(p.x.p) + n * p.x.sn + c0, p.x.sl, xr[k]);
+        if (GATE) at.load(static_cast<const T*>(p.z.p) + n * p.z.sn + c0, p.z.sl, zr[k]);
     };
     long long n = (long long)blockIdx.x * p.spb + s;
     const long long step = (long long)gridDim.x * p.spb;
-    fetch(n);
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) fetch(n + k * step, k);
     float w[8], b[8];
     at.weights(p.w, p.wdtype, c0, 1.f, w);
     at.weights(p.b, p.wdtype, c0, 0.f, b);
@@ -198,11 +201,16 @@ __global__ void __launch_bounds__(kThreads, VEC ? kFwdBlocks : 2) gnorm_unit_ker
         float x[8], z[8], sum = 0.f, sq = 0.f, none = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            x[j] = VEC || j < at.n ? xr.get(j) : 0.f;
-            if (GATE) z[j] = VEC || j < at.n ? zr.get(j) : 0.f;
+            x[j] = VEC || j < at.n ? xr[0].get(j) : 0.f;
+            if (GATE) z[j] = VEC || j < at.n ? zr[0].get(j) : 0.f;
             sum += x[j];
         }
-        fetch(n + step);
+#pragma unroll
+        for (int k = 1; k < AHEAD; ++k) {
+            xr[k - 1] = xr[k];
+            zr[k - 1] = zr[k];
+        }
+        fetch(n + AHEAD * step, AHEAD - 1);
         if (!mine) sum = 0.f;
         unit_sum<false>(sum, none, p.tpr, sh[0]);
         const float mean = sum / (float)values;  // (a quotient: equal values have their mean)
@@ -468,51 +476,77 @@ __global__ void __launch_bounds__(kThreads) gnorm_fold_kernel(const GNormParams 
         *reinterpret_cast<float2*>(out + 2 * (long long)blockIdx.x) = make_float2(a, GRAD ? q : 1.f / sqrtf(q + p.eps));
 }
 
-// y, or (GRAD) dx and dgate; means: the gradient's, [N][G][2]
+// y, or (GRAD) dx and dgate; means: the gradient's, [N][G][2].  A few positions on
+// their way to a thread at a time.
 template <typename T, bool VEC, bool GRAD, bool GATE, bool SILU>
-__global__ void __launch_bounds__(kThreads) gnorm_apply_kernel(const GNormParams p, const float* means) {
+__global__ void __launch_bounds__(kThreads, VEC ? (GRAD ? 2 : kRunBlocks) : 1) gnorm_apply_kernel(const GNormParams p, const float* means) {
     const RunSpot r = run_spot(p);
     if (r.live <= 0) return;
+    constexpr int M = sizeof(T) == 4 || GRAD || GATE ? 2 : 4;
     float w[8], b[8], mean[8], rstd[8], m1[8], m2[8];
+    if (VEC) {
+        weights8(p.w, p.wdtype, r.c, 1.f, w);
+        weights8(p.b, p.wdtype, r.c, 0.f, b);
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const int c = min(r.c + j, p.C - 1);
         const float2 st = __ldg(reinterpret_cast<const float2*>(p.stats) + r.n * p.G + c / p.cg);
         mean[j] = st.x;
         rstd[j] = st.y;
-        w[j] = weight_at(p.w, p.wdtype, c, 1.f);
-        b[j] = weight_at(p.b, p.wdtype, c, 0.f);
+        if (!VEC) {
+            w[j] = weight_at(p.w, p.wdtype, c, 1.f);
+            b[j] = weight_at(p.b, p.wdtype, c, 0.f);
+        }
+        if (!GRAD) w[j] *= st.y;
         if (GRAD) {
             const float2 m = __ldg(reinterpret_cast<const float2*>(means) + r.n * p.G + c / p.cg);
             m1[j] = m.x;
             m2[j] = m.y;
         }
     }
-#pragma unroll 2
-    for (int l = r.l0 + r.row; l < r.l1; l += r.rows) {
-        float x[8], z[8], dy[8];
-        load8<T, VEC>(static_cast<const T*>(p.x.p) + r.n * p.x.sn + l * p.x.sl + r.c, r.live, x);
-        if (GATE) load8<T, VEC>(static_cast<const T*>(p.z.p) + r.n * p.z.sn + l * p.z.sl + r.c, r.live, z);
-        if (GRAD) load8<T, VEC>(static_cast<const T*>(p.dy.p) + r.n * p.dy.sn + l * p.dy.sl + r.c, r.live, dy);
+    const T* const xp = static_cast<const T*>(p.x.p) + r.n * p.x.sn + r.c;
+    const T* const zp = static_cast<const T*>(p.z.p) + r.n * p.z.sn + r.c;
+    const T* const gp = static_cast<const T*>(p.dy.p) + r.n * p.dy.sn + r.c;
+    T* const yp = static_cast<T*>(p.y) + r.n * p.yn + r.c;
+    T* const dp = static_cast<T*>(p.dz) + r.n * p.dzn + r.c;
+    for (int l0 = r.l0 + r.row; l0 < r.l1; l0 += M * r.rows) {
+        Lane<T, 8, VEC> xv[M], zv[M], gv[M];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float n = (x[j] - mean[j]) * rstd[j], v = fmaf(n, w[j], b[j]);
-            if (!GRAD) {
-                x[j] = GATE ? v * act<SILU>(z[j]) : act<SILU>(v);
-            } else {
-                float value, slope;
-                act_slope<SILU>(GATE ? z[j] : v, value, slope);
-                const float t = dy[j] * (GATE ? value : slope) * w[j];
-                z[j] = dy[j] * v * slope;
-                x[j] = rstd[j] * (t - m1[j] - n * m2[j]);
+        for (int i = 0; i < M; ++i) {
+            const int l = l0 + i * r.rows;
+            if (l < r.l1) {
+                xv[i].load(xp + l * p.x.sl, r.live);
+                if (GATE) zv[i].load(zp + l * p.z.sl, r.live);
+                if (GRAD) gv[i].load(gp + l * p.dy.sl, r.live);
             }
         }
-        Lane<T, 8, VEC> o;
-        o.set(x);
-        o.store(static_cast<T*>(p.y) + r.n * p.yn + l * p.yl + r.c, r.live);
-        if (GRAD && GATE) {
-            o.set(z);
-            o.store(static_cast<T*>(p.dz) + r.n * p.dzn + l * p.dzl + r.c, r.live);
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+            const int l = l0 + i * r.rows;
+            if (l >= r.l1) break;
+            float x[8], z[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (!GRAD) {
+                    const float v = fmaf(xv[i].get(j) - mean[j], w[j], b[j]);
+                    x[j] = GATE ? v * act<SILU>(zv[i].get(j)) : act<SILU>(v);
+                } else {
+                    const float n = (xv[i].get(j) - mean[j]) * rstd[j], v = fmaf(n, w[j], b[j]);
+                    float value, slope;
+                    act_slope<SILU>(GATE ? zv[i].get(j) : v, value, slope);
+                    const float dy = gv[i].get(j), t = dy * (GATE ? value : slope) * w[j];
+                    z[j] = dy * v * slope;
+                    x[j] = rstd[j] * (t - m1[j] - n * m2[j]);
+                }
+            }
+            Lane<T, 8, VEC> o;
+            o.set(x);
+            o.store(yp + l * p.yl, r.live);
+            if (GRAD && GATE) {
+                o.set(z);
+                o.store(dp + l * p.dzl, r.live);
+            }
         }
     }
 }
@@ -569,7 +603,7 @@ GPlan gnorm_plan(long long N, int L, int C, int G, bool grad) {
     }
     const int across = (C + kUnit - 1) / kUnit;
     // enough blocks to fill the SMs, runs of 16 positions or more
-    long long runs = (4LL * sm_count() + N * across - 1) / (N * across);
+    long long runs = ((long long)kRunBlocks * sm_count() + N * across - 1) / (N * across);
     if (runs > (L + 15) / 16) runs = (L + 15) / 16;
     if (runs < 1) runs = 1;
     g.run = (int)((L + runs - 1) / runs);

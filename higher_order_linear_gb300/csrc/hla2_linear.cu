@@ -40,15 +40,20 @@ __global__ void __launch_bounds__(kWalkThreads, 1) lin_walk_kernel(const LinWalk
     if (tid <= kTokens) pw[tid] = (float)power(g, tid);
     const size_t R = (size_t)p.da * p.dc;
     // the state that enters
-    const float* rec = OUT && p.nseg > 1 ? p.rec + ((size_t)bh * (p.nseg + 1) + w) * R : nullptr;
-    for (int e = tid; e < D * D; e += kWalkThreads) {
-        const int r = e / D, c = e % D;
-        float v = 0.f;
-        if (OUT && r < p.da && c < p.dc) {
-            if (rec) v = rec[r * p.rec_r + c * p.rec_c];
-            else if (p.s_in) v = p.s_in[(size_t)bh * R + r * p.in_r + c * p.in_c];
+    {
+        const float* src = nullptr;
+        long long sr = 0, sc = 0;
+        if (OUT && p.nseg > 1) {
+            src = p.rec + ((size_t)bh * (p.nseg + 1) + w) * R; sr = p.rec_r; sc = p.rec_c;
+        } else if (OUT && p.s_in) {
+            src = p.s_in + (size_t)bh * R; sr = p.in_r; sc = p.in_c;
         }
-        sS[e] = v;
+        const bool turned = sr == 1 && sc != 1;  // neighbours in memory to neighbouring threads
+#pragma unroll 16
+        for (int i = 0; i < D * D / kWalkThreads; ++i) {
+            const int e = tid + i * kWalkThreads, r = turned ? e % D : e / D, c = turned ? e / D : e % D;
+            sS[r * D + c] = src && r < p.da && c < p.dc ? src[r * sr + c * sc] : 0.f;
+        }
     }
     const T* const ga = static_cast<const T*>(p.a) + b * p.sa[0] + h * p.sa[1];
     const T* const gb = static_cast<const T*>(p.b) + b * p.sb[0] + h * p.sb[1];
@@ -60,15 +65,34 @@ __global__ void __launch_bounds__(kWalkThreads, 1) lin_walk_kernel(const LinWalk
         const int n = min(kTokens, len - t0);
         if (n <= 0) continue;  // behind the sequence's end: all threads agree
         __syncthreads();
-        auto load = [&](float* dst, const T* src, long long st, int width) {
-            for (int e = tid; e < kTokens * D; e += kWalkThreads) {
-                const int r = e / D, c = e % D;
-                dst[r * LD + c] = r < n && c < width ? to_f32(src[(t0 + r) * st + c]) : 0.f;
+        // rows of four values at a time where they allow it, eight loads on their way to a thread
+        auto load = [&](float* dst, const T* src, long long st, int width, bool four) {
+            if (four) {
+                constexpr int RUN = D / 4, N = kTokens * RUN / kWalkThreads;
+                Lane<T, 4, true> v[N];
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    const int e = tid + k * kWalkThreads, r = e / RUN, c = e % RUN * 4;
+                    if (r < n && c < width) v[k].load(src + (t0 + r) * st + c, 4);
+                }
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    const int e = tid + k * kWalkThreads, r = e / RUN, c = e % RUN * 4;
+                    const bool in = r < n && c < width;
+                    *reinterpret_cast<float4*>(dst + r * LD + c) =
+                        in ? make_float4(v[k].get(0), v[k].get(1), v[k].get(2), v[k].get(3)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+            } else {
+#pragma unroll 8
+                for (int k = 0; k < kTokens * D / kWalkThreads; ++k) {
+                    const int e = tid + k * kWalkThreads, r = e / D, c = e % D;
+                    dst[r * LD + c] = r < n && c < width ? to_f32(src[(t0 + r) * st + c]) : 0.f;
+                }
             }
         };
-        if (OUT) load(sA, ga, p.sa[2], p.da);
-        load(sB, gb, p.sb[2], p.da);
-        load(sC, gc, p.sc[2], p.dc);
+        if (OUT) load(sA, ga, p.sa[2], p.da, p.fours & 1);
+        load(sB, gb, p.sb[2], p.da, p.fours & 2);
+        load(sC, gc, p.sc[2], p.dc, p.fours & 4);
         __syncthreads();
         if (OUT) {
             // P: rows 4 (tid / 16) .. + 3, columns tid % 16 + 16 q
@@ -378,6 +402,9 @@ bool plan_walk(LinWalk& w, int dtype) {
     plan_segments(w.B * w.H, w.T, tc ? kLinTcChunk : kTokens, segment_cost(tc, w.da, w.dc), &w.nseg, &w.seglen, &w.nchunk);
     w.rec_r = w.dc;
     w.rec_c = 1;
+    const int es = dtype_size(dtype);
+    auto four = [&](const void* ptr, const long long (&st)[3], int n) { return n % 4 == 0 && aligned_to(ptr, es, st, 3, 4 * es); };
+    w.fours = (four(w.a, w.sa, w.da) ? 1 : 0) | (four(w.b, w.sb, w.da) ? 2 : 0) | (four(w.c, w.sc, w.dc) ? 4 : 0);
     return tc;
 }
 cudaError_t launch_walk(const LinWalk& w, int dtype, bool tc, bool states, cudaStream_t s) {

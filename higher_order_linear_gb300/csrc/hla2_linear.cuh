@@ -34,6 +34,7 @@ struct LinWalk {
     long long rec_r, rec_c;  // (dK's walk reads dV's states, transposed)
     int nseg, seglen, nchunk;
     int rev;
+    int fours;  // CUDA cores: bits 0..2, a, b, c are read four values at a time
     int* status;
 };
 
