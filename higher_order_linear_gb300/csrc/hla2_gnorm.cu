@@ -48,7 +48,13 @@ struct GNormParams {
     int run, runs;
 };
 
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+// 1 / (1 + 2^(-x log2 e)): one power of two and one reciprocal, good to (1.5 |x| + 10) 2^-24 of itself
+__device__ __forceinline__ float sigmoid(float x) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return r;
+}
 // the activation and its slope
 template <bool SILU>
 __device__ __forceinline__ float act(float x) { return SILU ? x * sigmoid(x) : x; }
@@ -183,6 +189,7 @@ __global__ void __launch_bounds__(kThreads, VEC ? kFwdBlocks : 2) gnorm_unit_ker
     const Spots<VEC> at(lane, p.tpr, s < p.spb && g < p.G ? values : 0, p.cg);
     const bool mine = at.n > 0;
     const float inv = 1.f / (float)values;
+    const bool even = (values & (values - 1)) == 0;  // the reciprocal is exact
     constexpr int AHEAD = VEC && sizeof(T) == 2 ? 2 : 1;  // samples on their way
     typename Spots<VEC>::template Raw<T> xr[AHEAD]{}, zr[AHEAD]{};
     auto fetch = [&](long long n, int k) {
@@ -213,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, VEC ? kFwdBlocks : 2) gnorm_unit_ker
         fetch(n + AHEAD * step, AHEAD - 1);
         if (!mine) sum = 0.f;
         unit_sum<false>(sum, none, p.tpr, sh[0]);
-        const float mean = sum / (float)values;  // (a quotient: equal values have their mean)
+        const float mean = even ? sum * inv : sum / (float)values;  // (equal values have their mean)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             x[j] -= mean;
@@ -222,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, VEC ? kFwdBlocks : 2) gnorm_unit_ker
         if (!mine) sq = 0.f;
         unit_sum<false>(sq, none, p.tpr, sh[1]);
         if (!mine || n >= p.N) continue;
-        const float rstd = 1.f / sqrtf(fmaf(sq, inv, p.eps));
+        const float rstd = rsqrtf(fmaf(sq, inv, p.eps));
         if (p.stats && lane == 0) *reinterpret_cast<float2*>(p.stats + (n * p.G + g) * 2) = make_float2(mean, rstd);
         float y[8];
 #pragma unroll
