@@ -958,7 +958,7 @@ def hla2_linear_step(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: t
     [n,d], v [n,dv] (fp32 or bf16), gamma [H] with n a multiple of H (head i decays
     by gamma[i % H]) -> o [n,dv] of the inputs' dtype.  The state is updated in
     place, or left and the new one written to ``state_out``."""
-    shape, dt, dev = q.shape, q.dtype, q.device
+    shape, dt, dev, ld = q.shape, q.dtype, q.device, None
     if not (q.is_cuda and q.is_contiguous() and len(shape) == 2 and dt in _CODES and o is None and
             k.shape == shape and k.dtype is dt and k.device == dev and k.is_contiguous() and
             v.dtype is dt and v.device == dev and v.is_contiguous() and len(v.shape) == 2 and
@@ -968,6 +968,7 @@ def hla2_linear_step(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: t
             (state_out is None or (state_out.shape == state.shape and state_out.dtype is _F32 and
                                    state_out.device == dev and state_out.is_contiguous()))):
         _linear_step_checks(state, q, k, v, gamma, o, state_out)
+        ld = _longs(q.stride(0), k.stride(0), v.stride(0), v.shape[1] if o is None else o.stride(0))
     n, d = shape
     L = _lib or lib()
     with _guard(dev, stream):
@@ -975,7 +976,7 @@ def hla2_linear_step(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: t
             o = torch.empty(v.shape, device=dev, dtype=dt)
         rc = L.hla2_linear_step(state.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), gamma.data_ptr(),
                                 o.data_ptr(), None if state_out is None else state_out.data_ptr(), n, gamma.shape[0],
-                                d, v.shape[1], _longs(q.stride(0), k.stride(0), v.stride(0), o.stride(0)), _CODES[dt],
+                                d, v.shape[1], ld, _CODES[dt],
                                 _raw(dev, stream))
     if rc:
         _check(rc, "hla2_linear_step")
@@ -1188,14 +1189,13 @@ def _group_checks(X, groups, weight, bias, gate, stats, workspace, **like):
     _cuda_device(X, "X")
 
 
-def _group_inputs(X, groups, weight, bias, gate, stats):
-    """(N, L, C, dtype code, weights' dtype code, activation code) where all arguments are the ordinary ones."""
+def _group_plain(X, groups, weight, bias, gate, stats):
+    """Whether all arguments are the ordinary ones: dense, weight and bias of one type."""
     shape, dt, dev = X.shape, X.dtype, X.device
     return (X.is_cuda and len(shape) in (2, 3) and dt in _CODES and X.is_contiguous() and groups >= 1 and
-            not shape[-1] % groups and
-            all(t is None or (t.dtype in _CODES and t.shape == shape[-1:] and t.device == dev and t.is_contiguous())
-                for t in (weight, bias)) and
-            (weight is None or bias is None or weight.dtype is bias.dtype) and
+            not shape[-1] % groups and weight is not None and bias is not None and weight.dtype in _CODES and
+            weight.dtype is bias.dtype and weight.shape == bias.shape == shape[-1:] and
+            weight.device == bias.device == dev and weight.is_contiguous() and bias.is_contiguous() and
             (gate is None or (gate.dtype is dt and gate.shape == shape and gate.device == dev and
                               gate.is_contiguous())) and
             (stats is None or (stats.dtype is _F32 and stats.shape == (shape[0], groups, 2) and
@@ -1209,10 +1209,16 @@ def _activation(name) -> int:
     return code
 
 
-def _group_work(L, workspace, N, P, C, groups, backward, dev):
+@functools.lru_cache(maxsize=256)
+def _group_need(device, N, P, C, groups, backward):
+    """The workspace's bytes, asked once for each size on a device (its SM count is part of the answer)."""
+    return lib().hla2_groupnorm_workspace(N, P, C, groups, backward)
+
+
+def _group_work(workspace, N, P, C, groups, backward, dev):
     if workspace is not None:
         return workspace, workspace.numel() * workspace.element_size()
-    need = L.hla2_groupnorm_workspace(N, P, C, groups, backward)
+    need = _group_need(dev.index, N, P, C, groups, backward)
     return (torch.empty(need, device=dev, dtype=torch.uint8) if need else None), need
 
 
@@ -1227,9 +1233,10 @@ def hla2_groupnorm(X: torch.Tensor, groups: int, weight: torch.Tensor | None = N
     z * act(gate) with a ``gate`` like X;  ``activation`` "none" or "silu".
     weight, bias [C] fp32 or bf16.  ``stats`` [N,groups,2] fp32 keeps what
     hla2_groupnorm_backward needs.  Y may be X or gate."""
-    acode = _activation(activation)
-    if Y is not None or workspace is not None or not _group_inputs(X, groups, weight, bias, gate, stats):
+    acode, strides = _activation(activation), None
+    if Y is not None or workspace is not None or not _group_plain(X, groups, weight, bias, gate, stats):
         _group_checks(X, groups, weight, bias, gate, stats, workspace, Y=Y)
+        strides = 0
     dev, shape = X.device, X.shape
     N, C = shape[0], shape[-1]
     P = shape[1] if len(shape) == 3 else 1
@@ -1238,10 +1245,11 @@ def hla2_groupnorm(X: torch.Tensor, groups: int, weight: torch.Tensor | None = N
     with _guard(dev, stream):
         if Y is None:
             Y = _like(X)
-        workspace, nws = _group_work(L, workspace, N, P, C, groups, 0, dev)
+        if strides is not None:
+            strides = _longs(*_group_view(X, shape), *_group_view(gate, shape), *_group_view(Y, shape))
+        workspace, nws = _group_work(workspace, N, P, C, groups, 0, dev)
         rc = L.hla2_groupnorm(X.data_ptr(), _ptr(weight), _ptr(bias), _ptr(gate), Y.data_ptr(), _ptr(stats), N, P, C,
-                              groups, _longs(*_group_view(X, shape), *_group_view(gate, shape), *_group_view(Y, shape)),
-                              eps, acode, _CODES[X.dtype], wcode, _ptr(workspace), nws, _raw(dev, stream))
+                              groups, strides, eps, acode, _CODES[X.dtype], wcode, _ptr(workspace), nws, _raw(dev, stream))
     if rc:
         _check(rc, "hla2_groupnorm")
     return Y
@@ -1259,8 +1267,10 @@ def hla2_groupnorm_backward(X: torch.Tensor, dY: torch.Tensor, stats: torch.Tens
     groups = stats.shape[1] if isinstance(stats, torch.Tensor) and stats.dim() == 3 else 0
     if not groups:
         raise ValueError("expected stats [N,groups,2]")
-    if not (dX is dgate is workspace is None and _group_inputs(X, groups, weight, bias, gate, stats) and
+    strides = None
+    if not (dX is dgate is workspace is None and _group_plain(X, groups, weight, bias, gate, stats) and
             dY.dtype is X.dtype and dY.shape == X.shape and dY.device == X.device and dY.is_contiguous()):
+        strides = 0
         if gate is None and dgate is not None:
             raise ValueError("dgate without a gate")
         _group_checks(X, groups, weight, bias, gate, stats, workspace, dX=dX, dgate=dgate)
@@ -1277,14 +1287,16 @@ def hla2_groupnorm_backward(X: torch.Tensor, dY: torch.Tensor, stats: torch.Tens
         if gate is not None and dgate is None:
             dgate = _like(gate)
         dwb = torch.empty((2, C), device=dev, dtype=_F32)
-        workspace, nws = _group_work(L, workspace, N, P, C, groups, 1, dev)
+        if strides is not None:
+            strides = _longs(*(v for t in (X, dY, gate, dX, dgate) for v in _group_view(t, shape)))
+        workspace, nws = _group_work(workspace, N, P, C, groups, 1, dev)
         rc = L.hla2_groupnorm_backward(X.data_ptr(), dY.data_ptr(), stats.data_ptr(), _ptr(weight), _ptr(bias),
                                        _ptr(gate), dX.data_ptr(), _ptr(dgate), dwb.data_ptr(), N, P, C, groups,
-                                       _longs(*(v for t in (X, dY, gate, dX, dgate) for v in _group_view(t, shape))),
-                                       acode, _CODES[X.dtype], wcode, _ptr(workspace), nws, _raw(dev, stream))
+                                       strides, acode, _CODES[X.dtype], wcode, _ptr(workspace), nws, _raw(dev, stream))
     if rc:
         _check(rc, "hla2_groupnorm_backward")
-    return dX, dwb[0], dwb[1], dgate
+    dW, dB = dwb.unbind(0)
+    return dX, dW, dB, dgate
 
 
 def _rotary_checks(Q, pos, freq, sections, K, OQ, OK):
