@@ -449,11 +449,46 @@ __device__ __forceinline__ float block_sum(const LongSum& sum, float* sh) {
     return v;
 }
 
+// dw and db: the lines of partial sums added in a fixed order, 16 columns to a
+// block, each THREADS / 16 threads' sums of every (THREADS / 16)th line.
+constexpr int kFoldColumns = 16, kFoldThreads = 1024;
+template <int THREADS>
+__device__ __forceinline__ void fold_lines(const float* __restrict__ part, float* __restrict__ out, long long lines,
+                                           int width, int block, float (*sh)[kFoldColumns]) {
+    const int col = threadIdx.x % kFoldColumns, line = threadIdx.x / kFoldColumns;
+    const int c = block * kFoldColumns + col;
+    float a = 0.f;
+    if (c < width) {
+#pragma unroll 8
+        for (long long g = line; g < lines; g += THREADS / kFoldColumns) a += part[g * width + c];
+    }
+    a += __shfl_down_sync(0xffffffffu, a, 16);
+    if ((threadIdx.x & 31) < kFoldColumns) sh[threadIdx.x >> 5][col] = a;
+    __syncthreads();
+    if (threadIdx.x < kFoldColumns && c < width) {
+        a = 0.f;
+#pragma unroll
+        for (int i = 0; i < THREADS / 32; ++i) a += sh[i][col];
+        out[c] = a;
+    }
+}
+__global__ void __launch_bounds__(kFoldThreads) gnorm_lines_kernel(const float* __restrict__ part,
+                                                                   float* __restrict__ out, long long lines, int width) {
+    __shared__ float sh[kFoldThreads / 32][kFoldColumns];
+    fold_lines<kFoldThreads>(part, out, lines, width, blockIdx.x, sh);
+}
+
 // A group's runs and channels folded: mean and reciprocal deviation, or (GRAD)
-// the means of t and t n, which go behind the partial sums.
+// the means of t and t n, which go behind the partial sums.  The blocks behind the
+// groups' fold the gradient's lines.
 template <bool GRAD>
 __global__ void __launch_bounds__(kThreads) gnorm_fold_kernel(const GNormParams p, float* out) {
     __shared__ float sh[kThreads / 32];
+    if (GRAD && blockIdx.x >= p.N * p.G) {
+        __shared__ float columns[kThreads / 32][kFoldColumns];
+        fold_lines<kThreads>(p.part, p.dw, p.N * p.runs, 2 * p.C, (int)(blockIdx.x - p.N * p.G), columns);
+        return;
+    }
     const long long n = blockIdx.x / p.G;
     const int g = (int)(blockIdx.x % p.G), items = p.runs * p.cg;
     const float* const part = p.part + n * p.runs * 2 * p.C + g * p.cg;
@@ -558,30 +593,6 @@ __global__ void __launch_bounds__(kThreads, VEC ? (GRAD ? 2 : kRunBlocks) : 1) g
     }
 }
 
-// dw and db: the lines of partial sums added in a fixed order, 16 columns to a
-// block, each 64 threads' sums of every 64th line.
-constexpr int kFoldColumns = 16, kFoldThreads = 1024, kFoldLines = kFoldThreads / kFoldColumns;
-__global__ void __launch_bounds__(kFoldThreads) gnorm_lines_kernel(const float* __restrict__ part,
-                                                                   float* __restrict__ out, long long lines, int width) {
-    __shared__ float sh[kFoldThreads / 32][kFoldColumns];
-    const int col = threadIdx.x % kFoldColumns, line = threadIdx.x / kFoldColumns;
-    const int c = blockIdx.x * kFoldColumns + col;
-    float a = 0.f;
-    if (c < width) {
-#pragma unroll 8
-        for (long long g = line; g < lines; g += kFoldLines) a += part[g * width + c];
-    }
-    a += __shfl_down_sync(0xffffffffu, a, 16);
-    if ((threadIdx.x & 31) < kFoldColumns) sh[threadIdx.x >> 5][col] = a;
-    __syncthreads();
-    if (threadIdx.x < kFoldColumns && c < width) {
-        a = 0.f;
-#pragma unroll
-        for (int i = 0; i < kFoldThreads / 32; ++i) a += sh[i][col];
-        out[c] = a;
-    }
-}
-
 // ------------------------------------------------------------------ host ----
 struct GPlan {
     bool unit;
@@ -625,7 +636,7 @@ int check_gnorm(const char* what, long long N, int L, int C, int G, float eps, i
     if (N <= 0 || L <= 0 || C <= 0 || G <= 0 || C % G)
         return set_error(HLA2_ERR_INVALID, "%s: sizes must be positive and C a multiple of G (N=%lld L=%d C=%d G=%d)", what, N, L, C, G);
     if (C > kMaxChannels) return set_error(HLA2_ERR_UNSUPPORTED, "%s: C=%d exceeds %d", what, C, kMaxChannels);
-    if (N > 0x7fffffffLL || N * L > 0x7fffffffLL || N * G > 0x7fffffffLL)
+    if (N > 0x7fffffffLL || N * L > 0x7fffffffLL || N * G > 0x7fff0000LL)
         return set_error(HLA2_ERR_UNSUPPORTED, "%s: N*L or N*G exceeds 2^31 - 1 (N=%lld L=%d G=%d)", what, N, L, G);
     if (!known_dtype(dtype) || !known_dtype(wdtype)) return set_error(HLA2_ERR_UNSUPPORTED, "%s: unknown dtype", what);
     if (act != HLA2_ACT_NONE && act != HLA2_ACT_SILU) return set_error(HLA2_ERR_UNSUPPORTED, "%s: unknown activation %d", what, act);
@@ -664,7 +675,8 @@ cudaError_t run_gnorm(GNormParams p, const GPlan& g, int dtype, bool vec, cudaSt
         float* const means = p.part + g.part;
         float* const folded = GRAD || !p.stats ? means : p.stats;
         gnorm_sums_kernel<T, VEC, GRAD, GATE, SILU><<<grid, kThreads, 0, s>>>(p);
-        gnorm_fold_kernel<GRAD><<<(unsigned)(p.N * p.G), kThreads, 0, s>>>(p, folded);
+        const unsigned lines = GRAD && p.dw ? (2 * p.C + kFoldColumns - 1) / kFoldColumns : 0;
+        gnorm_fold_kernel<GRAD><<<(unsigned)(p.N * p.G) + lines, kThreads, 0, s>>>(p, folded);
         if (!GRAD) p.stats = folded;
         gnorm_apply_kernel<T, VEC, GRAD, GATE, SILU><<<grid, kThreads, 0, s>>>(p, means);
         note_launches(3);
@@ -679,7 +691,7 @@ cudaError_t run_gnorm(GNormParams p, const GPlan& g, int dtype, bool vec, cudaSt
     cudaError_t e;
     if (dtype == HLA2_DTYPE_BF16) e = vec ? acted(bf16{}, yes{}) : acted(bf16{}, no{});
     else e = vec ? acted(float{}, yes{}) : acted(float{}, no{});
-    if (GRAD && e == cudaSuccess && p.dw) {
+    if (GRAD && e == cudaSuccess && p.dw && g.unit) {
         gnorm_lines_kernel<<<(2 * p.C + kFoldColumns - 1) / kFoldColumns, kFoldThreads, 0, s>>>(p.part, p.dw, g.lines, 2 * p.C);
         note_launches(1);
         e = cudaGetLastError();
