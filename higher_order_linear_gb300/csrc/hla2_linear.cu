@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) lin_walk_kernel(const LinWalk
             // P: rows 4 (tid / 16) .. + 3, columns tid % 16 + 16 q
             const int r0 = tid / 16 * 4, q0 = tid % 16;
             float acc[4][4] = {};
-            for (int x = 0; x < D; x += 4) {
+            for (int x = 0; x < p.da; x += 4) {  // (zeros up to a whole step)
                 float4 a[4], bb[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) lin_walk_kernel(const LinWalk
             constexpr int TC = D / 4, RO = kTokens * TC / kWalkThreads;
             const int col = tid % TC * 4, row = tid / TC * RO;
             float o[RO][4] = {};
-            for (int x = 0; x < D; x += 4) {
+            for (int x = 0; x < p.da; x += 4) {
                 float4 s[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) s[q] = *reinterpret_cast<const float4*>(sS + (x + q) * D + col);
@@ -180,6 +180,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1) lin_walk_kernel(const LinWalk
         // S = g^n S + (B g^(..))^T C: NS x NS values to a thread, columns in steps of four
         constexpr int NS = D == 128 ? 8 : 4, TS = D / NS;
         const int x0 = tid / TS * NS, cc = tid % TS * 4;
+        const bool wide = NS == 4 || p.dc > 4 * TS;  // the second half of the columns
+        if (x0 >= p.da) continue;
         float acc[NS][NS];
         const float gn = pw[n];
 #pragma unroll
@@ -195,14 +197,20 @@ __global__ void __launch_bounds__(kWalkThreads, 1) lin_walk_kernel(const LinWalk
 #pragma unroll
             for (int q = 0; q < NS; q += 4) {
                 const float4 x = *reinterpret_cast<const float4*>(sB + j * LD + x0 + q);
-                const float4 y = *reinterpret_cast<const float4*>(sC + j * LD + cc + q * TS);
                 bv[q] = f * x.x; bv[q + 1] = f * x.y; bv[q + 2] = f * x.z; bv[q + 3] = f * x.w;
-                cv[q] = y.x; cv[q + 1] = y.y; cv[q + 2] = y.z; cv[q + 3] = y.w;
+                if (q == 0 || wide) {
+                    const float4 y = *reinterpret_cast<const float4*>(sC + j * LD + cc + q * TS);
+                    cv[q] = y.x; cv[q + 1] = y.y; cv[q + 2] = y.z; cv[q + 3] = y.w;
+                }
             }
 #pragma unroll
-            for (int r = 0; r < NS; ++r)
+            for (int q = 0; q < NS; q += 4)
+                if (q == 0 || wide) {
 #pragma unroll
-                for (int q = 0; q < NS; ++q) acc[r][q] = fmaf(bv[r], cv[q], acc[r][q]);
+                    for (int r = 0; r < NS; ++r)
+#pragma unroll
+                        for (int k = q; k < q + 4; ++k) acc[r][k] = fmaf(bv[r], cv[k], acc[r][k]);
+                }
         }
 #pragma unroll
         for (int r = 0; r < NS; ++r)
