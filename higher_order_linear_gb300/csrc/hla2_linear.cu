@@ -299,14 +299,14 @@ __global__ void __launch_bounds__(256) lin_tail_kernel(const LinWalk p) {
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) lin_step_kernel(const float* state, const T* q, const T* k, const T* v,
                                                        const float* gamma, T* o, float* state_out, int H, int d,
-                                                       int dv, int cols, long long ldq, long long ldk, long long ldv,
+                                                       int dv, int cols, int slices, long long ldq, long long ldk, long long ldv,
                                                        long long ldo) {
     constexpr int N = VEC ? 4 : 1;
     __shared__ float sq[128], sk[128];
     __shared__ float part[256 * N];
-    const int head = blockIdx.y, tid = threadIdx.x;
+    const int head = blockIdx.x / slices, tid = threadIdx.x;
     const int per = (cols + N - 1) / N;  // threads to a row
-    const int lines = 256 / per, line = tid / per, c = blockIdx.x * cols + tid % per * N;
+    const int lines = 256 / per, line = tid / per, c = blockIdx.x % slices * cols + tid % per * N;
     if (tid < d) {
         sq[tid] = to_f32(q[head * ldq + tid]);
         sk[tid] = to_f32(k[head * ldk + tid]);
@@ -375,7 +375,7 @@ SegmentCost segment_cost(bool tc, int d, int dv) {
     return tc ? SegmentCost{lin_tc_ctas(d, dv), 1.25, 0.6, 6.0} : SegmentCost{1, 1.0, 0.45, 0.5};
 }
 void plan_segments(int BH, int T, int chunk, const SegmentCost& c, int* nseg, int* seglen, int* nchunk) {
-    const int n = (T + chunk - 1) / chunk, sms = sm_count();
+    const int n = T / chunk + (T % chunk != 0), sms = sm_count();
     double best = 0;
     *nchunk = n; *nseg = 1; *seglen = n;
     for (int want = 1; want <= n && want <= 1024; ++want) {
@@ -605,7 +605,6 @@ extern "C" int hla2_linear_step(float* state, const void* q, const void* k, cons
     if (n <= 0 || H <= 0 || d <= 0 || dv <= 0 || n % H)
         return set_error(HLA2_ERR_INVALID, "%s: sizes must be positive and n a multiple of H (n=%d H=%d d=%d dv=%d)", what, n, H, d, dv);
     if (d > 128 || dv > 128) return set_error(HLA2_ERR_UNSUPPORTED, "%s: d=%d or dv=%d exceeds 128", what, d, dv);
-    if (n > 65535) return set_error(HLA2_ERR_UNSUPPORTED, "%s: n=%d exceeds 65535", what, n);
     if (!known_dtype(dtype)) return set_error(HLA2_ERR_UNSUPPORTED, "%s: unknown dtype %d", what, dtype);
     if (!state || !q || !k || !v || !gamma || !o) return set_error(HLA2_ERR_INVALID, "%s: null pointer", what);
     const int es = dtype_size(dtype);
@@ -619,14 +618,14 @@ extern "C" int hla2_linear_step(float* state, const void* q, const void* k, cons
     int cols = dv;
     while (cols > 16 && (long long)n * ((dv + cols - 1) / cols) < 2LL * sm_count()) cols = (cols + 1) / 2;
     if (vec) cols = (cols + 3) / 4 * 4;
-    const dim3 grid((dv + cols - 1) / cols, n);
+    const int slices = (dv + cols - 1) / cols;  // (several only of few heads)
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     auto go = [&](auto t) {
         using T = decltype(t);
         auto kernel = vec ? lin_step_kernel<T, true> : lin_step_kernel<T, false>;
-        kernel<<<grid, 256, 0, s>>>(state, static_cast<const T*>(q), static_cast<const T*>(k),
+        kernel<<<(unsigned)n * slices, 256, 0, s>>>(state, static_cast<const T*>(q), static_cast<const T*>(k),
                                     static_cast<const T*>(v), gamma, static_cast<T*>(o), state_out, H, d, dv, cols,
-                                    ldq, ldk, ldv, ldo);
+                                    slices, ldq, ldk, ldv, ldo);
     };
     if (dtype == HLA2_DTYPE_BF16) go(bf16{});
     else go(float{});

@@ -171,7 +171,7 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
     const int bh = blockIdx.y, w = blockIdx.x, seg = REV ? p.nseg - 1 - w : w;
     const int b = bh / p.H, h = bh % p.H;
     const int len = length_of(p, b);
-    const int c0 = seg * p.seglen, c1 = min(min(c0 + p.seglen, p.nchunk), (len + kL - 1) / kL);
+    const int c0 = seg * p.seglen, c1 = min(min(c0 + p.seglen, p.nchunk), len / kL + (len % kL != 0));
     int nchunks = max(0, c1 - c0);
     auto chunk_of = [&](int it) { return REV ? c1 - 1 - it : c0 + it; };
     auto tokens_of = [&](int it) { return min(kL, len - chunk_of(it) * kL); };

@@ -447,8 +447,9 @@ HLA2_API int hla2_gated_step(float* state, const void* x, const void* g, void* o
  *              the last token; they may be one tensor, but not overlap otherwise.
  *   strides    NULL, or twelve values: Q, K, V, O (b, h, t each), in elements; a
  *              head's channels are contiguous.  O may not be one of the inputs.
- *   workspace  hla2_linear_workspace(...) bytes, 16-byte aligned, not initialised;
- *              NULL when that is 0.  It serves one call at a time.
+ *   workspace  hla2_linear_workspace(...) bytes (asked with the device that runs the call
+ *              current), 16-byte aligned, not initialised; NULL when that is 0.  It
+ *              serves one call at a time.
  * fp32 inputs are computed in fp32.  bf16 inputs of 16-byte steps (widths, strides
  * and pointers) run on the tensor cores: there the scores within a block of 128
  * tokens and the state that enters the block are rounded to bf16 where they are
@@ -489,8 +490,7 @@ HLA2_API int hla2_linear_backward(const void* Q, const void* K, const void* V, c
  *   state_out [n][d][dv] fp32, or NULL to update in place; it may be state, but not
  *   overlap it otherwise.
  *   ld: row strides of q, k, v and o, or NULL for dense; the states are dense.
- * Errors: HLA2_ERR_INVALID, HLA2_ERR_UNSUPPORTED (d or dv > 128, n > 65535, type),
- * HLA2_ERR_LAUNCH.
+ * Errors: HLA2_ERR_INVALID, HLA2_ERR_UNSUPPORTED (d or dv > 128, type), HLA2_ERR_LAUNCH.
  */
 HLA2_API int hla2_linear_step(float* state, const void* q, const void* k, const void* v, const float* gamma, void* o,
                               float* state_out, int n, int H, int d, int dv, const long long* ld, int dtype,
