@@ -829,8 +829,8 @@ def hla2_linear_workspace(B: int, H: int, T: int, d: int, dv: int) -> int:
     return int(lib().hla2_linear_workspace(B, H, T, d, dv))
 
 
-def _linear_inputs(Q, K, V, gamma, lengths, workspace, **states):
-    """Checks shared by the linear attention's forward and backward; returns (B, H, T, d, dv, dtype code)."""
+def _linear_checks(Q, K, V, gamma):
+    """The checks of the linear attention's inputs, one by one."""
     for name, t in (("Q", Q), ("K", K), ("V", V)):
         _operand(t, name, None if t is Q else Q.device)
         if t.dim() != 4:
@@ -840,10 +840,20 @@ def _linear_inputs(Q, K, V, gamma, lengths, workspace, **states):
         raise ValueError("expected Q, K [B,H,T,d] and V [B,H,T,dv]")
     if not (Q.dtype == K.dtype == V.dtype):
         raise ValueError(f"Q, K, V must share a dtype (got {Q.dtype}, {K.dtype}, {V.dtype})")
-    code = _dtype_code(Q)
-    B, H, T, d = Q.shape
-    dv, dev = V.shape[-1], Q.device
-    _operand(gamma, "gamma", dev, _F32, (H,), dense=True)
+    _dtype_code(Q)
+    _operand(gamma, "gamma", Q.device, _F32, Q.shape[1:2], dense=True)
+
+
+def _linear_inputs(Q, K, V, gamma, lengths, workspace, **states):
+    """Checks shared by the linear attention's forward and backward; returns (B, H, T, d, dv, dtype code)."""
+    shape, vshape, dt, dev = Q.shape, V.shape, Q.dtype, Q.device
+    if not (Q.is_cuda and len(shape) == len(vshape) == 4 and K.shape == shape and vshape[:3] == shape[:3] and
+            dt in _CODES and K.dtype is dt and V.dtype is dt and K.device == dev and V.device == dev and
+            Q.stride(3) == K.stride(3) == V.stride(3) == 1 and gamma.dtype is _F32 and gamma.shape == shape[1:2] and
+            gamma.device == dev and gamma.is_contiguous()):
+        _linear_checks(Q, K, V, gamma)
+    B, H, T, d = shape
+    dv = vshape[3]
     if lengths is not None:
         _operand(lengths, "lengths", dev, torch.int32, (B,), dense=True)
     for name, t in states.items():
@@ -851,13 +861,19 @@ def _linear_inputs(Q, K, V, gamma, lengths, workspace, **states):
             _operand(t, name, dev, _F32, (B, H, d, dv), dense=True)
     if workspace is not None:
         _operand(workspace, "workspace", dev, dense=True)
-    return B, H, T, d, dv, code
+    return B, H, T, d, dv, _CODES[dt]
 
 
-def _linear_work(L, workspace, B, H, T, d, dv, dev):
+@functools.lru_cache(maxsize=256)
+def _linear_need(device, B, H, T, d, dv):
+    """The workspace's bytes, asked once for each size on a device (its SM count is part of the answer)."""
+    return lib().hla2_linear_workspace(B, H, T, d, dv)
+
+
+def _linear_work(workspace, B, H, T, d, dv, dev):
     if workspace is not None:
         return workspace, workspace.numel() * workspace.element_size()
-    need = L.hla2_linear_workspace(B, H, T, d, dv)
+    need = _linear_need(dev.index, B, H, T, d, dv)
     return (torch.empty(need, device=dev, dtype=torch.uint8) if need else None), need
 
 
@@ -883,7 +899,7 @@ def hla2_linear_forward(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, gamma
     with _guard(dev, stream):
         if O is None:
             O = _like(V)
-        workspace, nws = _linear_work(L, workspace, B, H, T, d, dv, dev)
+        workspace, nws = _linear_work(workspace, B, H, T, d, dv, dev)
         rc = L.hla2_linear_forward(Q.data_ptr(), K.data_ptr(), V.data_ptr(), gamma.data_ptr(), _ptr(lengths),
                                    _ptr(state_in), O.data_ptr(), _ptr(state_out), B, H, T, d, dv,
                                    _longs(*Q.stride()[:3], *K.stride()[:3], *V.stride()[:3], *O.stride()[:3]), code,
@@ -916,7 +932,7 @@ def hla2_linear_backward(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, gamm
         dQ = _like(Q) if dQ is None else dQ
         dK = _like(K) if dK is None else dK
         dV = _like(V) if dV is None else dV
-        workspace, nws = _linear_work(L, workspace, B, H, T, d, dv, dev)
+        workspace, nws = _linear_work(workspace, B, H, T, d, dv, dev)
         rc = L.hla2_linear_backward(Q.data_ptr(), K.data_ptr(), V.data_ptr(), gamma.data_ptr(), _ptr(lengths),
                                     _ptr(state_in), dO.data_ptr(), _ptr(dstate_out), dQ.data_ptr(), dK.data_ptr(),
                                     dV.data_ptr(), _ptr(dstate_in), B, H, T, d, dv,
