@@ -519,6 +519,10 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
         float S[W];
 #pragma unroll
         for (int j = 0; j < W; ++j) S[j] = 0.f;
+        // a row of a state that can be taken 16 bytes at a time (dc is a multiple of eight here)
+        auto whole_steps = [](const float* at, long long step) {
+            return step == 1 && reinterpret_cast<uintptr_t>(at) % 16 == 0;
+        };
         if (OUT && holds && row < p.da) {
             const float* src = nullptr;
             long long step = 1;
@@ -529,7 +533,14 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
                 src = p.s_in + (size_t)bh * R + row * p.in_r;
                 step = p.in_c;
             }
-            if (src) {
+            if (src && whole_steps(src, step)) {
+#pragma unroll
+                for (int j = 0; j < W; j += 4)
+                    if (scol + j < p.dc) {
+                        const float4 v = *reinterpret_cast<const float4*>(src + scol + j);
+                        S[j] = v.x; S[j + 1] = v.y; S[j + 2] = v.z; S[j + 3] = v.w;
+                    }
+            } else if (src) {
 #pragma unroll
                 for (int j = 0; j < W; ++j)
                     if (scol + j < p.dc) S[j] = src[(scol + j) * step];
@@ -651,9 +662,16 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
             step = p.out_c;
         }
         if (dst && holds && row < p.da) {
+            if (whole_steps(dst, step)) {
 #pragma unroll
-            for (int j = 0; j < W; ++j)
-                if (scol + j < p.dc) dst[(scol + j) * step] = S[j];
+                for (int j = 0; j < W; j += 4)
+                    if (scol + j < p.dc)
+                        *reinterpret_cast<float4*>(dst + scol + j) = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < W; ++j)
+                    if (scol + j < p.dc) dst[(scol + j) * step] = S[j];
+            }
         }
     }
     tc_fence_before();
