@@ -36,8 +36,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) lin_walk_kernel(const LinWalk
     const int bh = blockIdx.y, w = blockIdx.x, seg = p.rev ? p.nseg - 1 - w : w;
     const int b = bh / p.H, h = bh % p.H;
     const int len = length_of(p, b);
-    const double g = (double)__ldg(p.gamma + h);
-    if (tid <= kTokens) pw[tid] = (float)power(g, tid);
+    if (tid <= kTokens) pw[tid] = power(__ldg(p.gamma + h), tid);
     const size_t R = (size_t)p.da * p.dc;
     // the state that enters
     {
@@ -240,7 +239,7 @@ __global__ void __launch_bounds__(256) lin_scan_kernel(const LinWalk p, int chun
     const int R = p.da * p.dc, e = (blockIdx.x * 256 + threadIdx.x) * N, bh = blockIdx.y;
     __shared__ float f[256];
     const int len = length_of(p, bh / p.H);
-    const double g = (double)__ldg(p.gamma + bh % p.H);
+    const float g = __ldg(p.gamma + bh % p.H);
     float* const rec = p.rec + (size_t)bh * (p.nseg + 1) * R + e;
     Lane<float, 4, N == 4> acc;
     auto first = [&](int j) { return p.s_in ? p.s_in[(size_t)bh * R + ((e + j) / p.dc) * p.in_r + ((e + j) % p.dc) * p.in_c] : 0.f; };
@@ -254,7 +253,7 @@ __global__ void __launch_bounds__(256) lin_scan_kernel(const LinWalk p, int chun
         if (w < segments) {
             const int seg = p.rev ? p.nseg - 1 - w : w;
             const long long t0 = (long long)seg * p.seglen * chunk, t1 = t0 + (long long)p.seglen * chunk;
-            f[threadIdx.x] = (float)power(g, (int)max(0LL, min(t1, (long long)len) - t0));
+            f[threadIdx.x] = power(g, (int)max(0LL, min(t1, (long long)len) - t0));
         }
         __syncthreads();
         const int m = min(256, segments - base);

@@ -50,15 +50,23 @@ cudaError_t launch_lin_tc(const LinWalk& w, bool states, cudaStream_t s);
 
 namespace {
 
-// g^n, n >= 0 (g^0 = 1 for any g): by squaring in 64 bits, so that far powers
-// of decays next to one keep all 24 bits
-__device__ __forceinline__ double power(double g, int n) {
-    double r = 1.0;
+// g^n, n >= 0 (g^0 = 1 for any g), by squaring with sums of two fp32 numbers, so
+// that far powers of decays next to one keep all 24 bits (64-bit products are
+// 60 times as slow here, which a CTA's start would notice)
+struct Twofold {
+    float hi, lo;
+};
+__device__ __forceinline__ Twofold operator*(Twofold a, Twofold b) {
+    const float p = a.hi * b.hi, e = fmaf(a.hi, b.hi, -p) + fmaf(a.hi, b.lo, a.lo * b.hi), s = p + e;
+    return {s, e - (s - p)};
+}
+__device__ __forceinline__ float power(float g, int n) {
+    Twofold r{1.f, 0.f}, q{g, 0.f};
     for (; n; n >>= 1) {
-        if (n & 1) r *= g;
-        g *= g;
+        if (n & 1) r = r * q;
+        q = q * q;
     }
-    return r;
+    return r.hi;
 }
 __device__ __forceinline__ int length_of(const LinWalk& p, int b) {
     return p.lengths ? min(max(__ldg(p.lengths + b), 0), p.T) : p.T;

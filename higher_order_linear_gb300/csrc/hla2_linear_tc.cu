@@ -199,7 +199,7 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (tid <= kL) {
-        const float f = (float)power((double)__ldg(p.gamma + h), tid);
+        const float f = power(__ldg(p.gamma + h), tid);
         pw[tid] = f;
         if (tid < 16) down[15 - tid] = f;
         if (TERMS == 2) {
