@@ -110,16 +110,13 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
     return r != 0;
 }
-// A number of tries in a row (each may suspend the warp for a while)
-__device__ __forceinline__ bool mbar_tries(uint32_t a, uint32_t parity) {
+// One try that may suspend the warp for up to a millisecond: a waiting warp takes no issue slots from the others.
+__device__ __forceinline__ bool mbar_long_try(uint32_t a, uint32_t parity) {
     uint32_t ok;
     asm volatile(
-        "{\n .reg .pred p, r;\n .reg .u32 n;\n mov.u32 n, 0;\n"
-        "AGAIN:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra DONE;\n"
-        " add.u32 n, n, 1;\n setp.lt.u32 r, n, 64;\n @r bra AGAIN;\n"
-        "DONE:\n selp.u32 %0, 1, 0, p;\n}\n"
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
         : "=r"(ok)
-        : "r"(a), "r"(parity)
+        : "r"(a), "r"(parity), "r"(1000000u)
         : "memory");
     return ok != 0;
 }
@@ -170,7 +167,6 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
     __shared__ __align__(16) float pw[kL + 4];  // g^0 .. g^128
     __shared__ __align__(16) float down[16];    // g^15 .. g^0
     __shared__ uint32_t pieces[TERMS == 2 ? kL + 1 : 1];  // f1 (low half) and f2 of each power
-
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort_flag;
 
@@ -182,7 +178,7 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
     const int b = bh / p.H, h = bh % p.H;
     const int len = length_of(p, b);
     const int c0 = seg * p.seglen, c1 = min(min(c0 + p.seglen, p.nchunk), len / kL + (len % kL != 0));
-    int nchunks = max(0, c1 - c0);
+    const int nchunks = max(0, c1 - c0);
     auto chunk_of = [&](int it) { return REV ? c1 - 1 - it : c0 + it; };
     auto tokens_of = [&](int it) { return min(kL, len - chunk_of(it) * kL); };
 
@@ -235,9 +231,9 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
 
     auto wait_bar = [&](int i, uint32_t parity) -> bool {
         const uint32_t a = bar(i);
-        if (mbar_try(a, parity)) return true;
+        if (mbar_long_try(a, parity)) return true;
         const unsigned long long t0 = globaltimer();
-        while (!mbar_try(a, parity)) {
+        while (!mbar_long_try(a, parity)) {
             if (abort_flag) return false;
             if (globaltimer() - t0 > kWaitNs) {
                 abort_flag = 1;
@@ -273,11 +269,11 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
     // (a single lane's way through its own registers took 180 clocks a product), and one lane issues each batch.
     auto wait_warp = [&](int i, uint32_t parity) -> bool {
         const uint32_t a = bar(i);
-        bool ok = mbar_tries(a, parity);
+        bool ok = mbar_long_try(a, parity);
         if (!__all_sync(0xffffffffu, ok)) {
             const unsigned long long t0 = globaltimer();
             while (!ok && !abort_flag) {
-                ok = mbar_tries(a, parity);
+                ok = mbar_long_try(a, parity);
                 if (!ok && globaltimer() - t0 > kWaitNs) {
                     abort_flag = 1;
                     atomicExch(p.status, (int)kDevWaitTimeout);
@@ -292,7 +288,7 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
         if (elect_one()) mma_commit(bar(i));
         __syncwarp();
         const unsigned long long t0 = globaltimer();
-        while (!mbar_tries(bar(i), 0))
+        while (!mbar_long_try(bar(i), 0))
             if (globaltimer() - t0 > kWaitNs) {
                 atomicExch(p.status, (int)kDevWaitTimeout);
                 break;
