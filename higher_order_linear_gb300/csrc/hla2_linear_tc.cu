@@ -192,7 +192,18 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
     const Tile tS{dsm + LY::S, D};
     auto bar = [&](int i) -> uint32_t { return smem_u32(&bars[i]); };
 
-    if (tid == 0) {
+    // the loader's first lane sets up the barriers and sends for the first tiles at once; they are on their way while
+    // the others form the powers and take tensor memory
+    LoadLedger<NA + 2 * NB> loads(bar(0));
+    static_assert(NA <= NB, "the first turn of every slot is sent for below");
+    auto load = [&](int l, const CUtensorMap* map, const Tile& t, int it) {
+        loads.note(l);
+        mbar_expect_tx(bar(l), LY::kTile);
+#pragma unroll
+        for (int k = 0; k < D / 64; ++k)
+            tma_load_4d(t.base + k * t.block_bytes(), map, k * 64, chunk_of(it) * kL, h, b, bar(l));
+    };
+    if (warp == LY::kLoader && lane == 0) {
         abort_flag = 0;
         for (int i = 0; i < NBAR; ++i) {
             uint32_t count = 1;
@@ -203,6 +214,12 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
             mbar_init(bar(i), count);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_proxy_async();
+        for (int it = 0; it < NB && it < nchunks; ++it) {
+            load(LB + it, &mB, tB(it), it);
+            if (it < NA) load(LA + it, &mA, tA(it), it);
+            load(LC + it, &mC, tC(it), it);
+        }
     }
     if (tid <= kL) {
         const float f = power(__ldg(p.gamma + h), tid);
@@ -381,22 +398,16 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
         finish(FIN + 1);
     } else if (warp == LY::kLoader) {
         if (lane == 0) {
-            LoadLedger<NA + 2 * NB> loads(bar(0));
-            auto load = [&](int l, const CUtensorMap* map, const Tile& t, int it) {
-                loads.note(l);
-                mbar_expect_tx(bar(l), LY::kTile);
-#pragma unroll
-                for (int k = 0; k < D / 64; ++k)
-                    tma_load_4d(t.base + k * t.block_bytes(), map, k * 64, chunk_of(it) * kL, h, b, bar(l));
-            };
-            for (int it = 0; it < nchunks; ++it) {
+            for (int it = 1; it < nchunks; ++it) {
                 const int sb = it % NB, ub = it / NB;
-                if (ub > 0 && !wait_bar(FB + sb, (uint32_t)(ub - 1) & 1)) break;
-                load(LB + sb, &mB, tB(it), it);
-                load(LC + sb, &mC, tC(it), it);
-                if (OUT) {
+                if (it >= NB) {
+                    if (!wait_bar(FB + sb, (uint32_t)(ub - 1) & 1)) break;
+                    load(LB + sb, &mB, tB(it), it);
+                    load(LC + sb, &mC, tC(it), it);
+                }
+                if (OUT && it >= NA) {
                     const int sa = it % NA1, ua = it / NA1;
-                    if (ua > 0 && !wait_bar(FA + sa, (uint32_t)(ua - 1) & 1)) break;
+                    if (!wait_bar(FA + sa, (uint32_t)(ua - 1) & 1)) break;
                     load(LA + sa, &mA, tA(it), it);
                 }
             }
