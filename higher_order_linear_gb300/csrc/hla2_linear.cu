@@ -39,6 +39,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) lin_walk_kernel(const LinWalk
     const int b = bh / p.H, h = bh % p.H;
     const int len = length_of(p, b);
     if (tid <= kTokens) pw[tid] = power(__ldg(p.gamma + h), tid);
+    follow();
     const size_t R = (size_t)p.da * p.dc;
     // the state that enters
     {
@@ -245,18 +246,23 @@ __global__ void __launch_bounds__(256) lin_scan_kernel(const LinWalk p, int chun
     float* const rec = p.rec + (size_t)bh * (p.nseg + 1) * R + e;
     Lane<float, 4, N == 4> acc;
     auto first = [&](int j) { return p.s_in ? p.s_in[(size_t)bh * R + ((e + j) / p.dc) * p.in_r + ((e + j) % p.dc) * p.in_c] : 0.f; };
-    if (e < R) {
-#pragma unroll
-        for (int j = 0; j < N; ++j) acc.v[j] = first(j);
-        acc.store(rec, N);
-    }
-    for (int base = 0; base < segments; base += 256) {
+    auto powers = [&](int base) {
         const int w = base + threadIdx.x;
         if (w < segments) {
             const int seg = p.rev ? p.nseg - 1 - w : w;
             const long long t0 = (long long)seg * p.seglen * chunk, t1 = t0 + (long long)p.seglen * chunk;
             f[threadIdx.x] = power(g, (int)max(0LL, min(t1, (long long)len) - t0));
         }
+    };
+    powers(0);
+    follow();
+    if (e < R) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) acc.v[j] = first(j);
+        acc.store(rec, N);
+    }
+    for (int base = 0; base < segments; base += 256) {
+        if (base) powers(base);
         __syncthreads();
         const int m = min(256, segments - base);
         if (e < R) {
@@ -402,9 +408,8 @@ cudaError_t launch_simple(const LinWalk& w, bool states, cudaStream_t s) {
     const int bytes = SimpleLayout<D>::kBytes;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    kernel<<<dim3(states ? lin_state_segments(w) : w.nseg, w.B * w.H), kWalkThreads, bytes, s>>>(w);
-    note_launches(1);
-    return cudaGetLastError();
+    return launch_following(kernel, dim3(states ? lin_state_segments(w) : w.nseg, w.B * w.H), kWalkThreads, bytes, s,
+                            w.after, w);
 }
 
 // The path and the segments of a walk.
@@ -430,13 +435,13 @@ cudaError_t enter_states(const LinWalk& w, int dtype, bool tc, cudaStream_t s) {
     if (cudaError_t e = launch_walk(w, dtype, tc, true, s)) return e;
     const int R = w.da * w.dc, per = R % 4 ? 256 : 1024;
     auto scan = R % 4 ? lin_scan_kernel<1> : lin_scan_kernel<4>;
-    scan<<<dim3((R + per - 1) / per, w.B * w.H), 256, 0, s>>>(w, tc ? kLinTcChunk : kTokens, lin_state_segments(w));
-    note_launches(1);
-    return cudaGetLastError();
+    return launch_following(scan, dim3((R + per - 1) / per, w.B * w.H), 256, 0, s, true, w, tc ? kLinTcChunk : kTokens,
+                            lin_state_segments(w));
 }
 cudaError_t run_walk(LinWalk w, int dtype, cudaStream_t s) {
     const bool tc = plan_walk(w, dtype);
     if (cudaError_t e = enter_states(w, dtype, tc, s)) return e;
+    w.after |= w.nseg > 1;
     return launch_walk(w, dtype, tc, false, s);
 }
 
@@ -577,6 +582,7 @@ extern "C" int hla2_linear_backward(const void* Q, const void* K, const void* V,
     LinWalk wv = walk(k, q, g, dV, 6, true, dstate_out, false, dstate_in);
     // dQ first, and dV, which writes dstate_in, after whatever reads dstate_out: dstate_in may be either state
     cudaError_t e = run_walk(wq, dtype, s);
+    wk.after = wv.after = 1;
     const bool tk = plan_walk(wk, dtype), tv = plan_walk(wv, dtype);
     if (e == cudaSuccess && tk == tv && wv.nseg > 1) {
         // the states of dK are those of dV, transposed

@@ -236,6 +236,7 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    follow();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -727,9 +728,8 @@ cudaError_t launch(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorM
     using LY = TcLayout<D, OUT, TERMS>;
     const int bytes = (int)LY::kBytes + 1024;
     if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) return e;
-    kernel<<<dim3(OUT ? w.nseg : lin_state_segments(w), w.B * w.H), LY::kThreads, bytes, s>>>(ma, mb, mc, w);
-    note_launches(1);
-    return cudaGetLastError();
+    return launch_following(kernel, dim3(OUT ? w.nseg : lin_state_segments(w), w.B * w.H), LY::kThreads, bytes, s, w.after,
+                            ma, mb, mc, w);
 }
 
 // states: three terms.  outputs: three where the walk itself leaves the last state.
