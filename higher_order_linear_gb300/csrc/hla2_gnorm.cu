@@ -18,8 +18,9 @@
 // Measured, 16 bits: gated silu, 16384 rows of 2048 in 16 groups (203 MB), 41 us, 0.74
 // of the copy bandwidth, instructions (an element takes a power of two, a
 // reciprocal and some 25 more) and HBM together; its gradient on 1024 channels (170
-// MB) 31 us and 5.5 us for the lines of dw and db.  8 maps of 4096 x 512 with silu: 12,
-// 9 and 13 us for sums, fold and the second pass (67 MB: 10 us at the copy bandwidth).
+// MB) 41 us with the lines of dw and db (43 had the second launch waited for the
+// first's end).  8 maps of 4096 x 512 with silu: 31 us for sums, fold and the second pass
+// (67 MB: 10 us at the copy bandwidth; 37 had each launch waited for the last one's end).
 #include "hla2_layer.cuh"
 
 namespace hla2 {
@@ -254,6 +255,7 @@ template <typename T, bool VEC, bool GATE, bool SILU>
 __global__ void __launch_bounds__(kThreads, VEC ? kBwdBlocks : 1) gnorm_unit_bwd_kernel(const GNormParams p) {
     __shared__ float2 sh[2][kThreads / 32];
     extern __shared__ float2 sums[];  // [unit of the block][value]
+    follow();
     const int unit = threadIdx.x / p.tpr, lane = threadIdx.x % p.tpr;
     const int s = unit / p.gpb, g = blockIdx.y * p.gpb + unit % p.gpb;
     const int values = p.L * p.cg, c0 = g * p.cg;
@@ -380,6 +382,7 @@ __device__ __forceinline__ bool add_rows(const RunSpot& r, float (&a)[8], float 
 template <typename T, bool VEC, bool GRAD, bool GATE, bool SILU>
 __global__ void __launch_bounds__(kThreads) gnorm_sums_kernel(const GNormParams p) {
     __shared__ float2 sh[kThreads][8];
+    follow();
     const RunSpot r = run_spot(p);
     float a[8] = {}, q[8] = {}, pivot[8], w[8], b[8], mean[8], rstd[8];
     if (r.live > 0) {
@@ -459,7 +462,7 @@ __device__ __forceinline__ float block_sum(const LongSum& sum, float* sh) {
 // block, each THREADS / 16 threads' sums of every (THREADS / 16)th line.
 constexpr int kFoldColumns = 16, kFoldThreads = 1024;
 template <int THREADS>
-__device__ __forceinline__ void fold_lines(const float* __restrict__ part, float* __restrict__ out, long long lines,
+__device__ __forceinline__ void fold_lines(const float* part, float* out, long long lines,
                                            int width, int block, float (*sh)[kFoldColumns]) {
     const int col = threadIdx.x % kFoldColumns, line = threadIdx.x / kFoldColumns;
     const int c = block * kFoldColumns + col;
@@ -478,9 +481,10 @@ __device__ __forceinline__ void fold_lines(const float* __restrict__ part, float
         out[c] = a;
     }
 }
-__global__ void __launch_bounds__(kFoldThreads) gnorm_lines_kernel(const float* __restrict__ part,
-                                                                   float* __restrict__ out, long long lines, int width) {
+__global__ void __launch_bounds__(kFoldThreads) gnorm_lines_kernel(const float* part, float* out,
+                                                                   long long lines, int width) {
     __shared__ float sh[kFoldThreads / 32][kFoldColumns];
+    follow();
     fold_lines<kFoldThreads>(part, out, lines, width, blockIdx.x, sh);
 }
 
@@ -490,6 +494,7 @@ __global__ void __launch_bounds__(kFoldThreads) gnorm_lines_kernel(const float* 
 template <bool GRAD>
 __global__ void __launch_bounds__(kThreads) gnorm_fold_kernel(const GNormParams p, float* out) {
     __shared__ float sh[kThreads / 32];
+    follow();
     if (GRAD && blockIdx.x >= p.N * p.G) {
         __shared__ float columns[kThreads / 32][kFoldColumns];
         fold_lines<kThreads>(p.part, p.dw, p.N * p.runs, 2 * p.C, (int)(blockIdx.x - p.N * p.G), columns);
@@ -529,17 +534,21 @@ __global__ void __launch_bounds__(kThreads) gnorm_fold_kernel(const GNormParams 
 template <typename T, bool VEC, bool GRAD, bool GATE, bool SILU>
 __global__ void __launch_bounds__(kThreads, VEC ? (GRAD ? 2 : kRunBlocks) : 1) gnorm_apply_kernel(const GNormParams p, const float* means) {
     const RunSpot r = run_spot(p);
-    if (r.live <= 0) return;
+    if (r.live <= 0) {
+        follow();
+        return;
+    }
     constexpr int M = sizeof(T) == 4 || GRAD || GATE ? 2 : 4;
     float w[8], b[8], mean[8], rstd[8], m1[8], m2[8];
     if (VEC) {
         weights8(p.w, p.wdtype, r.c, 1.f, w);
         weights8(p.b, p.wdtype, r.c, 0.f, b);
     }
+    follow();
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const int c = min(r.c + j, p.C - 1);
-        const float2 st = __ldg(reinterpret_cast<const float2*>(p.stats) + r.n * p.G + c / p.cg);
+        const float2 st = *(reinterpret_cast<const float2*>(p.stats) + r.n * p.G + c / p.cg);
         mean[j] = st.x;
         rstd[j] = st.y;
         if (!VEC) {
@@ -548,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, VEC ? (GRAD ? 2 : kRunBlocks) : 1) g
         }
         if (!GRAD) w[j] *= st.y;
         if (GRAD) {
-            const float2 m = __ldg(reinterpret_cast<const float2*>(means) + r.n * p.G + c / p.cg);
+            const float2 m = *(reinterpret_cast<const float2*>(means) + r.n * p.G + c / p.cg);
             m1[j] = m.x;
             m2[j] = m.y;
         }
@@ -671,22 +680,23 @@ cudaError_t run_gnorm(GNormParams p, const GPlan& g, int dtype, bool vec, cudaSt
         if (g.unit) {
             const dim3 grid(g.blocks, (p.G + g.gpb - 1) / g.gpb);
             if (GRAD)
-                gnorm_unit_bwd_kernel<T, VEC, GATE, SILU><<<grid, kThreads, (size_t)g.spb * g.gpb * p.L * p.cg * sizeof(float2), s>>>(p);
-            else
-                gnorm_unit_kernel<T, VEC, GATE, SILU><<<grid, kThreads, 0, s>>>(p);
+                return launch_following(gnorm_unit_bwd_kernel<T, VEC, GATE, SILU>, grid, kThreads,
+                                        (size_t)g.spb * g.gpb * p.L * p.cg * sizeof(float2), s, false, p);
+            gnorm_unit_kernel<T, VEC, GATE, SILU><<<grid, kThreads, 0, s>>>(p);
             note_launches(1);
             return cudaGetLastError();
         }
         const dim3 grid((unsigned)(p.N * g.runs), (p.C + kUnit - 1) / kUnit);
         float* const means = p.part + g.part;
         float* const folded = GRAD || !p.stats ? means : p.stats;
-        gnorm_sums_kernel<T, VEC, GRAD, GATE, SILU><<<grid, kThreads, 0, s>>>(p);
+        cudaError_t e = launch_following(gnorm_sums_kernel<T, VEC, GRAD, GATE, SILU>, grid, kThreads, 0, s, false, p);
         const unsigned lines = GRAD && p.dw ? (2 * p.C + kFoldColumns - 1) / kFoldColumns : 0;
-        gnorm_fold_kernel<GRAD><<<(unsigned)(p.N * p.G) + lines, kThreads, 0, s>>>(p, folded);
+        if (e == cudaSuccess)
+            e = launch_following(gnorm_fold_kernel<GRAD>, dim3((unsigned)(p.N * p.G) + lines), kThreads, 0, s, true, p, folded);
         if (!GRAD) p.stats = folded;
-        gnorm_apply_kernel<T, VEC, GRAD, GATE, SILU><<<grid, kThreads, 0, s>>>(p, means);
-        note_launches(3);
-        return cudaGetLastError();
+        if (e == cudaSuccess)
+            e = launch_following(gnorm_apply_kernel<T, VEC, GRAD, GATE, SILU>, grid, kThreads, 0, s, true, p, means);
+        return e;
     };
     using yes = std::true_type;
     using no = std::false_type;
@@ -698,9 +708,8 @@ cudaError_t run_gnorm(GNormParams p, const GPlan& g, int dtype, bool vec, cudaSt
     if (dtype == HLA2_DTYPE_BF16) e = vec ? acted(bf16{}, yes{}) : acted(bf16{}, no{});
     else e = vec ? acted(float{}, yes{}) : acted(float{}, no{});
     if (GRAD && e == cudaSuccess && p.dw && g.unit) {
-        gnorm_lines_kernel<<<(2 * p.C + kFoldColumns - 1) / kFoldColumns, kFoldThreads, 0, s>>>(p.part, p.dw, g.lines, 2 * p.C);
-        note_launches(1);
-        e = cudaGetLastError();
+        e = launch_following(gnorm_lines_kernel, dim3((2 * p.C + kFoldColumns - 1) / kFoldColumns), kFoldThreads, 0, s, true,
+                             p.part, p.dw, g.lines, 2 * p.C);
     }
     return e;
 }

@@ -51,35 +51,6 @@ cudaError_t launch_lin_tc(const LinWalk& w, bool states, cudaStream_t s);
 
 namespace {
 
-// A call's kernels follow each other closely: each one's CTAs may start once all of the last one's have passed
-// follow(), and do there what needs only the caller's inputs.  Behind follow() the kernel before is complete, and
-// since that one lets nobody start before its own follow(), so are all the others: records, states and outputs are
-// read and written only behind it.  A call's first kernel starts like any other, after all the stream was given.
-// A CTA that finds room where an earlier one has ended also fills the gap a walk's last CTAs leave.  (Training,
-// plain launches and these: 4 x 4096 x 16 x 64 227 and 198 us, 16384 x 16 x 128 347 and 329, 2 x 1023 x 3 x 80 in
-// fp32 152 and 132.)
-__device__ __forceinline__ void follow() {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-template <typename... P, typename... A>
-cudaError_t launch_following(void (*kernel)(P...), dim3 grid, int threads, int bytes, cudaStream_t s, bool after,
-                             const A&... args) {
-    cudaLaunchAttribute early{};
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = bytes;
-    cfg.stream = s;
-    cfg.attrs = &early;
-    cfg.numAttrs = after ? 1 : 0;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
-    if (e == cudaSuccess) note_launches(1);
-    return e;
-}
-
 // g^n, n >= 0 (g^0 = 1 for any g), by squaring with sums of two fp32 numbers, so
 // that far powers of decays next to one keep all 24 bits (64-bit products are
 // 60 times as slow here, which a CTA's start would notice)
