@@ -357,3 +357,44 @@ def test_behind_linear_attention():
         err, ref = (got.double().cpu() - ref).detach(), ref.detach()
         # early rows have few terms and a norm of tiny deviations: errors against the 2-norm of everything
         assert float(err.norm() / ref.norm()) < 7 * 2.0 ** -8
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("shape", [(1000, 0, 64, 4), (5, 777, 240, 8), (2, 4096, 64, 4), (2, 0, 4500, 1)])
+def test_calls_in_a_row(shape, dtype, captured):
+    """Each call's inputs are what the call before has just written, all in one workspace: the bits of the same calls
+    with the device idle between them."""
+    x = {k: (v.cuda() if isinstance(v, torch.Tensor) else v) for k, v in make(*shape, dtype, True, F32).items()}
+    N, L, C, G = shape
+    need = max(hla2.hla2_groupnorm_workspace(N, max(L, 1), C, G, back) for back in (False, True))
+    ws = torch.full((max(need, 16),), 255, dtype=torch.uint8, device="cuda")
+    pause = lambda: None
+
+    def run():
+        a, dy, z, seen = x["x"], x["dy"], x["z"], []
+        for _ in range(3):
+            stats = torch.empty(N, G, 2, device="cuda")
+            y = hla2.hla2_groupnorm(a, G, x["w"], x["b"], gate=z, activation="silu", stats=stats, workspace=ws)
+            pause()
+            gr = hla2.hla2_groupnorm_backward(a, dy, stats, x["w"], x["b"], gate=z, activation="silu", workspace=ws)
+            pause()
+            seen += [y, stats, *gr]
+            a, dy = y, gr[0]
+        return seen
+
+    pause = torch.cuda.synchronize
+    want = run()
+    pause = lambda: None
+    if captured:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = run()
+        for _ in range(3):
+            g.replay()
+    else:
+        got = run()
+    torch.cuda.synchronize()
+    assert all(torch.isfinite(t).all() for t in want)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))

@@ -565,3 +565,44 @@ def test_captured(d):
             o = hla2.hla2_linear_forward(x["q"], x["k"], x["v"], x["gamma"], state_in=x["h0"], state_out=last)
             gr = hla2.hla2_linear_backward(x["q"], x["k"], x["v"], x["gamma"], x["do"], state_in=x["h0"], dstate_out=x["dlast"])
             assert all(torch.equal(a, b) for a, b in zip(out, (o, last, *gr)))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("dtype,B,H,T,d", [(BF, 1, 4, 6000, 128), (BF, 2, 40, 900, 64), (BF, 3, 2, 130, 64), (F32, 1, 3, 700, 40)])
+def test_calls_in_a_row(dtype, B, H, T, d, captured):
+    """Each call's inputs are what the call before has just written, all in one workspace: the bits of the same calls
+    with the device idle between them."""
+    x = dev(make(B, H, T, d, d, dtype))
+    ws = torch.full((max(hla2.hla2_linear_workspace(B, H, T, d, d), 16),), 255, dtype=torch.uint8, device="cuda")
+    pause = lambda: None
+
+    def run():
+        q, k, v, do, h, dh = (x[n] for n in ("q", "k", "v", "do", "h0", "dlast"))
+        seen = []
+        for _ in range(3):
+            last, first = torch.empty_like(h), torch.empty_like(h)
+            o = hla2.hla2_linear_forward(q, k, v, x["gamma"], state_in=h, state_out=last, workspace=ws)
+            pause()
+            gr = hla2.hla2_linear_backward(q, k, o, x["gamma"], do, state_in=last, dstate_out=dh, dstate_in=first, workspace=ws)
+            pause()
+            v, do, h, dh = o.div_(8), gr[2].div_(8), last.div_(8), first.div_(8)
+            pause()
+            seen += [o, last, first, *gr]
+        return seen
+
+    pause = torch.cuda.synchronize
+    want = run()
+    pause = lambda: None
+    if captured:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = run()
+        for _ in range(3):
+            g.replay()
+    else:
+        got = run()
+    torch.cuda.synchronize()
+    assert all(torch.isfinite(t).all() for t in want)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert hla2.hla2_device_status() == 0
