@@ -375,7 +375,8 @@ __global__ void __launch_bounds__(256) lin_step_kernel(const float* state, const
 // start; the states' walk, the scan and two more launches where there are several
 // segments.  Measured: a chunk takes 2.8 us on the tensor cores (1.25 times that with
 // two CTAs on the SM), the states' walk 0.6 of the output walk, the scan and the
-// launches 17 us; the CUDA cores take some 20 us for a chunk and 0.45 for its states.
+// launches 17 us (alone; the overlap of a call's kernels gives some back); the CUDA
+// cores take some 20 us for a chunk and 0.45 for its states.
 struct SegmentCost {
     int ctas;  // to an SM
     double shared, states, extra;

@@ -30,15 +30,16 @@
 // roles share the instruction caches, and local memory goes to L2 (shared memory
 // takes all of L1).
 //
-// Measured (device time, 16 heads, 16 bits).  65536 x 128: states 100 us, 537 MB at
-// 0.79 of the copy bandwidth; outputs 181 us, 1.07 GB at 0.88.  Shorter walks also
-// pay for their start and end: 16384 x 128, 33 us (0.61) and 57 us (0.70).  4 x 4096
-// x 64 (four segments of eight chunks a head): 21 us and 36 us, 0.47 and 0.54 of
-// the copy bandwidth were the tiles not in L2; the chain P, its packing, P~ C and the
-// drain takes 3.3 us a chunk, two CTAs to an SM.  Tried and slower: packing P in
-// groups of 32 columns or with the next group on its way (outputs of 65536 x 128 at a
-// stand of 196 us: 210, 207), a factor for P's columns, the state and the rows so
-// that both terms share one accumulator (211), four-term keys (above).
+// Measured (device time of a launch alone, 16 heads, 16 bits).  65536 x 128: states 97
+// us, 537 MB at 0.82 of the copy bandwidth; outputs 174 us, 1.07 GB at 0.91.  Shorter
+// walks also pay for their start and end: 16384 x 128, 31 us (0.64) and 54 us (0.73).
+// 4 x 4096 x 64 (four segments of eight chunks a head, three of them with states):
+// 21 us and 35 us, 0.36 and 0.57 of the copy bandwidth were the tiles not in L2; the
+// chain P, its packing, P~ C and the drain takes 3.3 us a chunk, two CTAs to an SM.
+// Tried and slower: packing P in groups of 32 columns or with the next group on its way
+// (outputs of 65536 x 128 at a stand of 196 us: 210, 207), a factor for P's columns, the
+// state and the rows so that both terms share one accumulator (201 at a stand of 176),
+// four-term keys (above).
 #include "hla2_linear.cuh"
 #include "hla2_tc_common.cuh"
 
