@@ -36,40 +36,40 @@ def listed():
     return [
         # ---- linear attention
         # decoding one sequence: 16 heads of 128, a call's latency
-        {"name": "linear step of 16 x 128", "op": "step", "n": 16, "H": 16, "d": 128, "dv": 128, "dtype": "bf16"},
+        {"name": "linear step, 16 heads of 128", "op": "step", "n": 16, "H": 16, "d": 128, "dv": 128, "dtype": "bf16"},
         # decoding a large batch: as many heads as the package's own decode workload
-        {"name": "linear step of 4096 x 128", "op": "step", "n": 4096, "H": 16, "d": 128, "dv": 128,
+        {"name": "linear step, 4096 heads of 128", "op": "step", "n": 4096, "H": 16, "d": 128, "dv": 128,
          "dtype": "f32"},
         # prefill of a long document, the sizes of the package's headline forward
-        {"name": "linear prefill of 65536 x 16 x 128", "op": "linear", "B": 1, "H": 16, "T": 65536, "d": 128,
+        {"name": "linear prefill, 65536 tokens, 16 x 128", "op": "linear", "B": 1, "H": 16, "T": 65536, "d": 128,
          "dv": 128, "dtype": "bf16", "layout": "bhtd", "state": True, "ragged": False},
         # prefill of a padded batch of prompts, projections laid out [B, T, H, d]
-        {"name": "linear prefill of 8 prompts x 16 x 64", "op": "linear", "B": 8, "H": 16, "T": 2048, "d": 64, "dv": 64,
+        {"name": "linear prefill, 8 prompts, 16 x 64", "op": "linear", "B": 8, "H": 16, "T": 2048, "d": 64, "dv": 64,
          "dtype": "bf16", "layout": "bthd", "state": True, "ragged": True},
         # training at the sizes of the package's normalised forward
-        {"name": "linear train of 4 x 4096 x 16 x 64", "op": "linear_train", "B": 4, "H": 16, "T": 4096, "d": 64,
+        {"name": "linear train, 4 x 4096, 16 x 64", "op": "linear_train", "B": 4, "H": 16, "T": 4096, "d": 64,
          "dv": 64, "dtype": "bf16", "layout": "bthd", "state": False, "ragged": False},
         # training on one long sequence in segments (a state comes in, its gradient goes back)
-        {"name": "linear train of 16384 x 16 x 128", "op": "linear_train", "B": 1, "H": 16, "T": 16384, "d": 128,
+        {"name": "linear train, 16384 tokens, 16 x 128", "op": "linear_train", "B": 1, "H": 16, "T": 16384, "d": 128,
          "dv": 128, "dtype": "bf16", "layout": "bhtd", "state": True, "ragged": False},
         # odd sizes in 32 bits, trained
-        {"name": "linear train of 2 x 1023 x 3 x 80 f32", "op": "linear_train", "B": 2, "H": 3, "T": 1023, "d": 80,
+        {"name": "linear train, 1023 tokens, 3 x 80, f32", "op": "linear_train", "B": 2, "H": 3, "T": 1023, "d": 80,
          "dv": 48, "dtype": "f32", "layout": "bthd", "state": True, "ragged": False},
         # ---- group norm
         # the norm of each head's output and its gate in prefill (16 heads of 128)
-        {"name": "group norm gated 16384 x 2048", "op": "gnorm", "N": 16384, "L": 1, "C": 2048, "G": 16,
+        {"name": "group norm gated, 16384 x 2048", "op": "gnorm", "N": 16384, "L": 1, "C": 2048, "G": 16,
          "dtype": "bf16", "act": "silu", "gate": True},
         # the same when decoding a batch of 16
-        {"name": "group norm gated 16 x 2048", "op": "gnorm", "N": 16, "L": 1, "C": 2048, "G": 16, "dtype": "bf16",
+        {"name": "group norm gated, 16 x 2048", "op": "gnorm", "N": 16, "L": 1, "C": 2048, "G": 16, "dtype": "bf16",
          "act": "silu", "gate": True},
         # channels-last feature maps of 64 x 64 positions, norm and activation
-        {"name": "group norm of 8 maps 4096 x 512", "op": "gnorm", "N": 8, "L": 4096, "C": 512, "G": 32,
+        {"name": "group norm, 8 maps of 4096 x 512", "op": "gnorm", "N": 8, "L": 4096, "C": 512, "G": 32,
          "dtype": "bf16", "act": "silu", "gate": False},
         # training: gradients of input, gate, weight and bias (16 heads of 64)
-        {"name": "group norm backward 16384 x 1024", "op": "gnorm_bwd", "N": 16384, "L": 1, "C": 1024, "G": 16,
+        {"name": "group norm backward, 16384 x 1024", "op": "gnorm_bwd", "N": 16384, "L": 1, "C": 1024, "G": 16,
          "dtype": "bf16", "act": "silu", "gate": True},
         # odd sizes in 32 bits: small feature maps, trained
-        {"name": "group norm backward 5 x 777 x 240 f32", "op": "gnorm_bwd", "N": 5, "L": 777, "C": 240, "G": 8,
+        {"name": "group norm backward, 5 x 777 x 240, f32", "op": "gnorm_bwd", "N": 5, "L": 777, "C": 240, "G": 8,
          "dtype": "f32", "act": "silu", "gate": False},
     ]
 
