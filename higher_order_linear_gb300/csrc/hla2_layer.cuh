@@ -165,5 +165,42 @@ inline bool aligned_to(const void* p, int esize, const long long* s, int n, int 
 }
 inline bool aligned_elem(const void* p, int esize) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)esize == 0; }
 
+// n rows of `width` bytes, `step` bytes apart.
+struct Rows {
+    const void* p;
+    long long n, step, width;
+};
+// Whether two sets of rows share a byte.  Rows of one step (slices of one tensor, or a single row on one side) are
+// compared at once, others row by row where the spans meet.
+inline bool rows_meet(Rows a, Rows b) {
+    if (!a.p || !b.p) return false;
+    auto first = [](Rows& r) {
+        long long at = (long long)reinterpret_cast<uintptr_t>(r.p);
+        if (r.step < 0) {
+            at += (r.n - 1) * r.step;
+            r.step = -r.step;
+        }
+        return at;
+    };
+    const long long pa = first(a), pb = first(b);
+    if (pa + (a.n - 1) * a.step + a.width <= pb || pb + (b.n - 1) * b.step + b.width <= pa) return false;
+    if (a.n == 1) a.step = b.step;
+    if (b.n == 1) b.step = a.step;
+    if (a.step == b.step) {
+        // row j of b lies d + (j - i) step behind row i of a: the least such distance above -b.width
+        const long long d = pb - pa, s = a.step;
+        if (s == 0 || (a.n == 1 && b.n == 1)) return true;
+        const long long least = -b.width - d, k = max((least < 0 ? -((-least + s - 1) / s) : least / s) + 1, 1 - a.n);
+        return k < b.n && d + k * s < a.width;
+    }
+    for (long long i = 0, j = 0; i < a.n && j < b.n;) {
+        const long long x = pa + i * a.step, y = pb + j * b.step;
+        if (x + a.width <= y) ++i;
+        else if (y + b.width <= x) ++j;
+        else return true;
+    }
+    return false;
+}
+
 }  // namespace
 }  // namespace hla2

@@ -624,6 +624,18 @@ extern "C" int hla2_linear_step(float* state, const void* q, const void* k, cons
     if (int rc = check_apart(what, state, state_out, (size_t)n * d * dv)) return rc;
     if (!state_out) state_out = state;
     const long long ldq = ld ? ld[0] : d, ldk = ld ? ld[1] : d, ldv = ld ? ld[2] : dv, ldo = ld ? ld[3] : dv;
+    // Few heads are cut into blocks that each read all of q and k and write their own columns: an output among the
+    // inputs would be read by one block before and by another after its writing.  v's columns are read by the
+    // block that writes them in o.
+    const Rows rq{q, n, ldq * es, (long long)d * es}, rk{k, n, ldk * es, (long long)d * es},
+        rv{v, n, ldv * es, (long long)dv * es}, ro{o, n, ldo * es, (long long)dv * es};
+    const long long all = (long long)n * d * dv * 4;
+    const Rows before{state, 1, all, all}, behind{state_out, 1, all, all};
+    if (rows_meet(ro, rq) || rows_meet(ro, rk) || (!(o == v && ldo == ldv) && rows_meet(ro, rv)))
+        return set_error(HLA2_ERR_INVALID, "%s: the output overlaps an input", what);
+    if (rows_meet(ro, before) || rows_meet(ro, behind) || rows_meet(rq, behind) || rows_meet(rk, behind) ||
+        rows_meet(rv, behind))
+        return set_error(HLA2_ERR_INVALID, "%s: a state overlaps the output or an input", what);
     const bool vec = dv % 4 == 0 && aligned_to(state, 4, nullptr, 0, 16) && aligned_to(state_out, 4, nullptr, 0, 16);
     int cols = dv;
     while (cols > 16 && (long long)n * ((dv + cols - 1) / cols) < 2LL * sm_count()) cols = (cols + 1) / 2;

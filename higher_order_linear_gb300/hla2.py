@@ -972,8 +972,9 @@ def hla2_linear_step(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: t
                      stream=None) -> torch.Tensor:
     """One token of the linear attention for n heads: state [n,d,dv] fp32, q, k
     [n,d], v [n,dv] (fp32 or bf16), gamma [H] with n a multiple of H (head i decays
-    by gamma[i % H]) -> o [n,dv] of the inputs' dtype.  The state is updated in
-    place, or left and the new one written to ``state_out``."""
+    by gamma[i % H]) -> o [n,dv] of the inputs' dtype (it may be v, but not overlap
+    an input otherwise).  The state is updated in place, or left and the new one
+    written to ``state_out``."""
     shape, dt, dev, ld = q.shape, q.dtype, q.device, None
     if not (q.is_cuda and q.is_contiguous() and len(shape) == 2 and dt in _CODES and o is None and
             k.shape == shape and k.dtype is dt and k.device == dev and k.is_contiguous() and

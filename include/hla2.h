@@ -489,8 +489,11 @@ HLA2_API int hla2_linear_backward(const void* Q, const void* K, const void* V, c
  *   multiple of H: head i decays by gamma[i % H].
  *   state_out [n][d][dv] fp32, or NULL to update in place; it may be state, but not
  *   overlap it otherwise.
+ *   o may be v (the same rows), but not overlap q, k, v or a state otherwise, nor may
+ *   the state that is written overlap q, k or v.
  *   ld: row strides of q, k, v and o, or NULL for dense; the states are dense.
- * Errors: HLA2_ERR_INVALID, HLA2_ERR_UNSUPPORTED (d or dv > 128, type), HLA2_ERR_LAUNCH.
+ * Errors: HLA2_ERR_INVALID (an overlap among them), HLA2_ERR_UNSUPPORTED (d or dv > 128,
+ * type), HLA2_ERR_LAUNCH.
  */
 HLA2_API int hla2_linear_step(float* state, const void* q, const void* k, const void* v, const float* gamma, void* o,
                               float* state_out, int n, int H, int d, int dv, const long long* ld, int dtype,

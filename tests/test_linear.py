@@ -274,7 +274,73 @@ def test_binding_refuses():
             pytest.fail(f"call {i} was taken")
 
 
+def step_code(s, q, k, v, o, so=None, ld=None, n=4, d=8, dv=8, dt=0):
+    import ctypes
+    ld = None if ld is None else (ctypes.c_longlong * 4)(*ld)
+    return hla2.lib().hla2_linear_step(*(None if t is None else ctypes.c_void_p(t) for t in (s, q, k, v, 1 << 16, o, so)), n, 1,
+                                       d, dv, ld, dt, None)
+
+
+def test_step_refuses_overlaps():
+    """Few heads are cut into blocks that each read q and k: an output among them would be read half written."""
+    s, q, k, v, o, so = (1 << 20) * 1, (1 << 20) * 2, (1 << 20) * 3, (1 << 20) * 4, (1 << 20) * 5, (1 << 20) * 6
+    n, d = 4, 8
+    state = n * d * d * 4
+    for kw in (dict(o=q), dict(o=k), dict(o=q + 4), dict(o=k - 4), dict(o=v + 4), dict(o=q + n * d * 4 - 4),
+               dict(o=s), dict(o=s + state - 4), dict(o=s - n * d * 4 + 4), dict(o=so), dict(so=q), dict(so=k - state + 4),
+               dict(so=v), dict(s=v, o=o, so=None), dict(o=v, ld=[8, 8, 8, 16]), dict(o=q + 4 * 4, ld=[64, 64, 64, 64], q=q - 8),
+               dict(o=q + 58 * 4, ld=[64, 8, 8, 57]), dict(o=q, ld=[0, 8, 8, 8])):
+        args = dict(dict(s=s, q=q, k=k, v=v, o=o, so=so), **kw)
+        assert step_code(**args) == hla2.HLA2_ERR_INVALID, kw
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="addresses that are none: what is not refused would be launched")
+def test_step_refuses_overlaps_and_nothing_else():
+    gen = torch.Generator().manual_seed(0)
+    pick = lambda lo, hi: int(torch.randint(lo, hi, (), generator=gen))
+    base = 1 << 20
+
+    def touched(p, step, width, n):
+        return {p + 4 * (i * step + c) for i in range(n) for c in range(width)}
+
+    seen = [0, 0]
+    for _ in range(3000):
+        n, d, dv = pick(1, 6), pick(1, 7), pick(1, 7)
+        lo, lq = pick(dv, 15), pick(0, 15)
+        if pick(0, 2):
+            lq = lo
+        o = base + 4 * pick(-40, 40)
+        meet = bool(touched(base, lq, d, n) & touched(o, lo, dv, n))
+        code = step_code(1 << 24, base, 1 << 25, 1 << 26, o, ld=[lq, 8, 8, lo], n=n, d=d, dv=dv)
+        assert code == (hla2.HLA2_ERR_INVALID if meet else hla2.HLA2_ERR_LAUNCH), (n, d, dv, lq, lo, o - base)
+        seen[meet] += 1
+    assert min(seen) > 300
+    assert step_code(1 << 24, base, 1 << 25, 1 << 26, 1 << 26) == hla2.HLA2_ERR_LAUNCH  # o is v
+
+
 # -------------------------------------------------------------- GPU tests ----
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,d", [(1, 128), (3, 64), (1000, 32)])
+def test_step_output_in_place_of_v(n, d):
+    gen = torch.Generator().manual_seed(n)
+    q, k, v = (torch.randn(n, d, generator=gen).cuda() for _ in range(3))
+    S, g = torch.randn(n, d, d, generator=gen).cuda(), torch.tensor([0.9], device="cuda")
+    want_state = torch.empty_like(S)
+    want = hla2.hla2_linear_step(S, q, k, v, g, state_out=want_state)
+    for o in (q, k, S[0, :n] if n <= d else q):
+        with pytest.raises(hla2.HLA2Error):
+            hla2.hla2_linear_step(S, q, k, v, g, o=o, state_out=torch.empty_like(S))
+    assert hla2.hla2_linear_step(S, q, k, v, g, o=v) is v
+    assert torch.equal(v, want) and torch.equal(S, want_state)
+    # q, k, v and o as slices of one buffer
+    room = torch.cat([q, k, want, torch.zeros_like(q)], 1)
+    parts = [room[:, i * d:(i + 1) * d] for i in range(4)]
+    S2 = S.clone()
+    want = hla2.hla2_linear_step(S, q, k, want, g)
+    hla2.hla2_linear_step(S2, *parts[:3], g, o=parts[3])
+    assert torch.equal(parts[3], want) and torch.equal(S2, S)
+
+
 SHAPES = [  # B, H, T, d, dv
     (1, 1, 1, 1, 1), (2, 3, 2, 16, 16), (1, 6, 63, 33, 20), (2, 2, 64, 64, 64), (1, 2, 65, 80, 48), (2, 2, 127, 64, 128),
     (1, 3, 128, 128, 128), (2, 1, 129, 128, 64), (3, 2, 300, 72, 72), (1, 2, 1000, 128, 128), (1, 3, 1025, 64, 64),
