@@ -12,8 +12,9 @@
 // Two forms.  A unit (a sample's group, L cg values) of up to 2048 values stays
 // in the registers of up to 256 threads, eight values each: x crosses HBM once, the
 // variance is taken about the mean.  Larger units are summed by channel over
-// runs of positions (moments about the run's first position, so that a large mean
-// costs nothing), folded in a second launch and read again by a third.
+// runs of positions (moments of a few positions at a time about one of them, joined, so that
+// neither a large mean nor an untypical value costs the others' digits), folded in a second launch
+// and read again by a third.
 //
 // Measured, 16 bits: gated silu, 16384 rows of 2048 in 16 groups (203 MB), 41 us, 0.74
 // of the copy bandwidth, instructions (an element takes a power of two, a
@@ -355,6 +356,99 @@ __device__ __forceinline__ RunSpot run_spot(const GNormParams& p) {
     r.live = r.row < r.rows ? min(8, p.C - r.c) : 0;
     return r;
 }
+// A running sum with its rounding errors kept (64-bit sums would take 60 times as long here)
+struct LongSum {
+    float hi = 0.f, lo = 0.f;
+    __device__ __forceinline__ void add(float x) {
+        const float s = hi + x, t = s - hi;
+        lo += (hi - (s - t)) + (x - t);
+        hi = s;
+    }
+    __device__ __forceinline__ float value() const { return hi + lo; }
+};
+// Mean and sum of squares about it of each channel of a run.  A thread takes its positions in pieces of kPiece, each
+// about its own first value, and joins them: with count n, mean and squares of what it has and m, mean + d, squares'
+// of a piece,  mean + d m / (n + m),  squares + squares' + d^2 n m / (n + m).  So a value far from the others
+// costs the digits of one piece, not of the run (a zero in front of 4096 values of 1000 +- 1 moved a variance by 2e-3
+// where the run was summed about it, by 4e-6 now), and long runs are sums of few levels.  What a thread has so
+// far waits in shared memory.
+constexpr int kPiece = 16;
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kThreads, VEC ? kRunBlocks : 2) gnorm_moments_kernel(const GNormParams p) {
+    __shared__ float4 sofar[8][kThreads];  // mean and squares, each as a LongSum
+    follow();
+    const RunSpot r = run_spot(p);
+    constexpr int M = sizeof(T) == 4 ? 2 : 4;  // positions on their way to a thread
+    const int len = r.l1 - r.l0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sofar[j][threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r.live > 0) {
+        const T* const x = static_cast<const T*>(p.x.p) + r.n * p.x.sn + r.l0 * p.x.sl + r.c;
+        float done = 0.f;
+#pragma unroll 1
+        for (int l0 = r.row; l0 < len; l0 += kPiece * r.rows) {
+            Lane<T, 8, VEC> pivot;
+            float a[8] = {}, q[8] = {};
+            const int m = min(kPiece, (len - l0 + r.rows - 1) / r.rows);
+#pragma unroll 1
+            for (int i0 = 0; i0 < m; i0 += M) {
+                Lane<T, 8, VEC> v[M];
+#pragma unroll
+                for (int i = 0; i < M; ++i)
+                    if (i0 + i < m) v[i].load(x + (l0 + (i0 + i) * r.rows) * p.x.sl, r.live);
+                if (i0 == 0) pivot = v[0];
+#pragma unroll
+                for (int i = 0; i < M; ++i) {
+                    if (i0 + i >= m) break;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float d = v[i].get(j) - pivot.get(j);
+                        a[j] += d;
+                        q[j] = fmaf(d, d, q[j]);
+                    }
+                }
+            }
+            const float inv = 1.f / (float)m, part = (float)m / (done + (float)m);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float4 f = sofar[j][threadIdx.x];
+                LongSum mean{f.x, f.y}, squares{f.z, f.w};
+                const float shift = a[j] * inv, d = (pivot.get(j) - mean.hi) + (shift - mean.lo);
+                squares.add(fmaf(d * d, done * part, fmaxf(fmaf(-a[j], shift, q[j]), 0.f)));
+                mean.add(d * part);
+                sofar[j][threadIdx.x] = make_float4(mean.hi, mean.lo, squares.hi, squares.lo);
+            }
+            done += (float)m;
+            asm volatile("" ::: "memory");  // (it is to wait there, not in registers)
+        }
+    }
+    __syncthreads();
+    // the block's rows, joined in order about the first one's mean: a channel to a thread
+    float* const line = p.part + (long long)blockIdx.x * 2 * p.C;
+    for (int e = threadIdx.x; e < r.cols * 8; e += kThreads) {
+        const int col = e % r.cols, j = e / r.cols, c = blockIdx.y * kUnit + col * 8 + j;
+        if (c >= p.C) continue;
+        const float4* const own = sofar[j] + col;  // row i at i cols
+        const int whole = len / r.rows, more = len % r.rows;
+        const float first = own->x + own->y;
+        LongSum moved, all;
+#pragma unroll 4
+        for (int i = 1; i < r.rows; ++i) {
+            const float4 f = own[i * r.cols];
+            moved.add((float)(whole + (i < more)) * ((f.x - first) + f.y));
+        }
+        const float middle = first + moved.value() / (float)len;
+#pragma unroll 4
+        for (int i = 0; i < r.rows; ++i) {
+            const float4 f = own[i * r.cols];
+            const float d = (f.x - middle) + f.y;
+            all.add(fmaf((float)(whole + (i < more)) * d, d, f.z + f.w));
+        }
+        line[c] = middle;
+        line[p.C + c] = all.value();
+    }
+}
+
 template <typename T, bool VEC>
 __device__ __forceinline__ void load8(const T* p, int n, float (&v)[8]) {
     Lane<T, 8, VEC> l;
@@ -378,75 +472,53 @@ __device__ __forceinline__ bool add_rows(const RunSpot& r, float (&a)[8], float 
     return true;
 }
 
-// GRAD: sums of dz and dz n of each channel; else mean and sum of squares about it.
-template <typename T, bool VEC, bool GRAD, bool GATE, bool SILU>
+// The gradient's sums of each channel of a run: dz n and dz.
+template <typename T, bool VEC, bool GATE, bool SILU>
 __global__ void __launch_bounds__(kThreads) gnorm_sums_kernel(const GNormParams p) {
     __shared__ float2 sh[kThreads][8];
     follow();
     const RunSpot r = run_spot(p);
-    float a[8] = {}, q[8] = {}, pivot[8], w[8], b[8], mean[8], rstd[8];
+    float a[8] = {}, q[8] = {}, w[8], b[8], mean[8], rstd[8];
     if (r.live > 0) {
         const T* x = static_cast<const T*>(p.x.p) + r.n * p.x.sn + r.c;
-        if (!GRAD) load8<T, VEC>(x + (long long)r.l0 * p.x.sl, r.live, pivot);
-        else
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int c = min(r.c + j, p.C - 1);
-                const float2 st = __ldg(reinterpret_cast<const float2*>(p.stats) + r.n * p.G + c / p.cg);
-                mean[j] = st.x;
-                rstd[j] = st.y;
-                w[j] = weight_at(p.w, p.wdtype, c, 1.f);
-                b[j] = weight_at(p.b, p.wdtype, c, 0.f);
-            }
+        for (int j = 0; j < 8; ++j) {
+            const int c = min(r.c + j, p.C - 1);
+            const float2 st = __ldg(reinterpret_cast<const float2*>(p.stats) + r.n * p.G + c / p.cg);
+            mean[j] = st.x;
+            rstd[j] = st.y;
+            w[j] = weight_at(p.w, p.wdtype, c, 1.f);
+            b[j] = weight_at(p.b, p.wdtype, c, 0.f);
+        }
 #pragma unroll 2
         for (int l = r.l0 + r.row; l < r.l1; l += r.rows) {
-            float v[8];
+            float v[8], dy[8], z[8];
             load8<T, VEC>(x + l * p.x.sl, r.live, v);
-            if (!GRAD) {
+            load8<T, VEC>(static_cast<const T*>(p.dy.p) + r.n * p.dy.sn + l * p.dy.sl + r.c, r.live, dy);
+            if (GATE) load8<T, VEC>(static_cast<const T*>(p.z.p) + r.n * p.z.sn + l * p.z.sl + r.c, r.live, z);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float d = v[j] - pivot[j];
-                    a[j] += d;
-                    q[j] = fmaf(d, d, q[j]);
-                }
-            } else {
-                float dy[8], z[8];
-                load8<T, VEC>(static_cast<const T*>(p.dy.p) + r.n * p.dy.sn + l * p.dy.sl + r.c, r.live, dy);
-                if (GATE) load8<T, VEC>(static_cast<const T*>(p.z.p) + r.n * p.z.sn + l * p.z.sl + r.c, r.live, z);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float n = (v[j] - mean[j]) * rstd[j];
-                    float value, slope;
-                    act_slope<SILU>(GATE ? z[j] : fmaf(n, w[j], b[j]), value, slope);
-                    const float d = dy[j] * (GATE ? value : slope);
-                    a[j] = fmaf(d, n, a[j]);
-                    q[j] += d;
-                }
+            for (int j = 0; j < 8; ++j) {
+                const float n = (v[j] - mean[j]) * rstd[j];
+                float value, slope;
+                act_slope<SILU>(GATE ? z[j] : fmaf(n, w[j], b[j]), value, slope);
+                const float d = dy[j] * (GATE ? value : slope);
+                a[j] = fmaf(d, n, a[j]);
+                q[j] += d;
             }
         }
     }
     if (!add_rows(r, a, q, sh)) return;
     float* const line = p.part + (long long)blockIdx.x * 2 * p.C + r.c;
-    const float inv = 1.f / (float)(r.l1 - r.l0);
 #pragma unroll
     for (int j = 0; j < 8; ++j)
         if (j < r.live) {
-            line[j] = GRAD ? a[j] : fmaf(a[j], inv, pivot[j]);
-            line[p.C + j] = GRAD ? q[j] : fmaxf(q[j] - a[j] * a[j] * inv, 0.f);
+            line[j] = a[j];
+            line[p.C + j] = q[j];
         }
 }
 
-// A running sum with its rounding errors kept (64-bit sums would take 60 times as long here)
-struct LongSum {
-    float hi = 0.f, lo = 0.f;
-    __device__ __forceinline__ void add(float x) {
-        const float s = hi + x, t = s - hi;
-        lo += (hi - (s - t)) + (x - t);
-        hi = s;
-    }
-};
 __device__ __forceinline__ float block_sum(const LongSum& sum, float* sh) {
-    float v = sum.hi + sum.lo;
+    float v = sum.value();
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     __syncthreads();
@@ -689,7 +761,9 @@ cudaError_t run_gnorm(GNormParams p, const GPlan& g, int dtype, bool vec, cudaSt
         const dim3 grid((unsigned)(p.N * g.runs), (p.C + kUnit - 1) / kUnit);
         float* const means = p.part + g.part;
         float* const folded = GRAD || !p.stats ? means : p.stats;
-        cudaError_t e = launch_following(gnorm_sums_kernel<T, VEC, GRAD, GATE, SILU>, grid, kThreads, 0, s, false, p);
+        cudaError_t e;
+        if constexpr (GRAD) e = launch_following(gnorm_sums_kernel<T, VEC, GATE, SILU>, grid, kThreads, 0, s, false, p);
+        else e = launch_following(gnorm_moments_kernel<T, VEC>, grid, kThreads, 0, s, false, p);
         const unsigned lines = GRAD && p.dw ? (2 * p.C + kFoldColumns - 1) / kFoldColumns : 0;
         if (e == cudaSuccess)
             e = launch_following(gnorm_fold_kernel<GRAD>, dim3((unsigned)(p.N * p.G) + lines), kThreads, 0, s, true, p, folded);

@@ -398,3 +398,13 @@ def test_calls_in_a_row(shape, dtype, captured):
     torch.cuda.synchronize()
     assert all(torch.isfinite(t).all() for t in want)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("shape", [(512, 4096, 8, 8), (460, 4100, 12, 3), (3, 70001, 16, 2)])
+def test_variance_behind_an_untypical_first_position(shape, dtype):
+    """Padding in front of values far from zero: the variance of a long run does not depend on its first value."""
+    x = make(*shape, dtype, False, F32, shift=1000.0)
+    x["x"][:, 0] = 0.0
+    check(x, "none", backward=False)
