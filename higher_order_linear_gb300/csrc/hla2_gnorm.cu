@@ -456,31 +456,21 @@ __device__ __forceinline__ void load8(const T* p, int n, float (&v)[8]) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = l.get(j);
 }
-// a block's rows added in order: two sums of each channel
-__device__ __forceinline__ bool add_rows(const RunSpot& r, float (&a)[8], float (&b)[8], float2 (*sh)[8]) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sh[threadIdx.x][j] = make_float2(a[j], b[j]);
-    __syncthreads();
-    if (r.row != 0 || r.live <= 0) return false;
-    for (int i = 1; i < r.rows; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float2 v = sh[threadIdx.x + i * r.cols][j];
-            a[j] += v.x;
-            b[j] += v.y;
-        }
-    return true;
-}
-
-// The gradient's sums of each channel of a run: dz n and dz.
+// The gradient's sums of each channel of a run: dz n and dz, in the same pieces (a thousand equal terms added one
+// after another are off by 160 roundings, all to one side).
 template <typename T, bool VEC, bool GATE, bool SILU>
 __global__ void __launch_bounds__(kThreads) gnorm_sums_kernel(const GNormParams p) {
-    __shared__ float2 sh[kThreads][8];
+    __shared__ float4 sofar[8][kThreads];  // two LongSums
     follow();
     const RunSpot r = run_spot(p);
-    float a[8] = {}, q[8] = {}, w[8], b[8], mean[8], rstd[8];
+    const int len = r.l1 - r.l0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sofar[j][threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r.live > 0) {
-        const T* x = static_cast<const T*>(p.x.p) + r.n * p.x.sn + r.c;
+        const T* const x = static_cast<const T*>(p.x.p) + r.n * p.x.sn + r.l0 * p.x.sl + r.c;
+        const T* const g = static_cast<const T*>(p.dy.p) + r.n * p.dy.sn + r.l0 * p.dy.sl + r.c;
+        const T* const gate = static_cast<const T*>(p.z.p) + r.n * p.z.sn + r.l0 * p.z.sl + r.c;
+        float w[8], b[8], mean[8], rstd[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int c = min(r.c + j, p.C - 1);
@@ -490,31 +480,52 @@ __global__ void __launch_bounds__(kThreads) gnorm_sums_kernel(const GNormParams 
             w[j] = weight_at(p.w, p.wdtype, c, 1.f);
             b[j] = weight_at(p.b, p.wdtype, c, 0.f);
         }
+#pragma unroll 1
+        for (int l0 = r.row; l0 < len; l0 += kPiece * r.rows) {
+            float a[8] = {}, q[8] = {};
+            const int end = min(len, l0 + kPiece * r.rows);
 #pragma unroll 2
-        for (int l = r.l0 + r.row; l < r.l1; l += r.rows) {
-            float v[8], dy[8], z[8];
-            load8<T, VEC>(x + l * p.x.sl, r.live, v);
-            load8<T, VEC>(static_cast<const T*>(p.dy.p) + r.n * p.dy.sn + l * p.dy.sl + r.c, r.live, dy);
-            if (GATE) load8<T, VEC>(static_cast<const T*>(p.z.p) + r.n * p.z.sn + l * p.z.sl + r.c, r.live, z);
+            for (int l = l0; l < end; l += r.rows) {
+                float v[8], dy[8], z[8];
+                load8<T, VEC>(x + l * p.x.sl, r.live, v);
+                load8<T, VEC>(g + l * p.dy.sl, r.live, dy);
+                if (GATE) load8<T, VEC>(gate + l * p.z.sl, r.live, z);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float n = (v[j] - mean[j]) * rstd[j];
+                    float value, slope;
+                    act_slope<SILU>(GATE ? z[j] : fmaf(n, w[j], b[j]), value, slope);
+                    const float d = dy[j] * (GATE ? value : slope);
+                    a[j] = fmaf(d, n, a[j]);
+                    q[j] += d;
+                }
+            }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float n = (v[j] - mean[j]) * rstd[j];
-                float value, slope;
-                act_slope<SILU>(GATE ? z[j] : fmaf(n, w[j], b[j]), value, slope);
-                const float d = dy[j] * (GATE ? value : slope);
-                a[j] = fmaf(d, n, a[j]);
-                q[j] += d;
+                const float4 f = sofar[j][threadIdx.x];
+                LongSum first{f.x, f.y}, second{f.z, f.w};
+                first.add(a[j]);
+                second.add(q[j]);
+                sofar[j][threadIdx.x] = make_float4(first.hi, first.lo, second.hi, second.lo);
             }
+            asm volatile("" ::: "memory");  // (they are to wait there, not in registers)
         }
     }
-    if (!add_rows(r, a, q, sh)) return;
-    float* const line = p.part + (long long)blockIdx.x * 2 * p.C + r.c;
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        if (j < r.live) {
-            line[j] = a[j];
-            line[p.C + j] = q[j];
+    __syncthreads();
+    float* const line = p.part + (long long)blockIdx.x * 2 * p.C;
+    for (int e = threadIdx.x; e < r.cols * 8; e += kThreads) {
+        const int col = e % r.cols, j = e / r.cols, c = blockIdx.y * kUnit + col * 8 + j;
+        if (c >= p.C) continue;
+        LongSum first, second;
+#pragma unroll 4
+        for (int i = 0; i < r.rows; ++i) {
+            const float4 f = sofar[j][col + i * r.cols];
+            first.add(f.x + f.y);
+            second.add(f.z + f.w);
         }
+        line[c] = first.value();
+        line[p.C + c] = second.value();
+    }
 }
 
 __device__ __forceinline__ float block_sum(const LongSum& sum, float* sh) {
@@ -538,11 +549,12 @@ __device__ __forceinline__ void fold_lines(const float* part, float* out, long l
                                            int width, int block, float (*sh)[kFoldColumns]) {
     const int col = threadIdx.x % kFoldColumns, line = threadIdx.x / kFoldColumns;
     const int c = block * kFoldColumns + col;
-    float a = 0.f;
+    LongSum sum;
     if (c < width) {
 #pragma unroll 8
-        for (long long g = line; g < lines; g += THREADS / kFoldColumns) a += part[g * width + c];
+        for (long long g = line; g < lines; g += THREADS / kFoldColumns) sum.add(part[g * width + c]);
     }
+    float a = sum.value();
     a += __shfl_down_sync(0xffffffffu, a, 16);
     if ((threadIdx.x & 31) < kFoldColumns) sh[threadIdx.x >> 5][col] = a;
     __syncthreads();

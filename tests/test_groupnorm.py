@@ -408,3 +408,27 @@ def test_variance_behind_an_untypical_first_position(shape, dtype):
     x = make(*shape, dtype, False, F32, shift=1000.0)
     x["x"][:, 0] = 0.0
     check(x, "none", backward=False)
+
+
+@pytest.mark.gpu
+def test_gradient_of_equal_terms_over_long_runs():
+    """dy and gate constant: t is its own mean, and n has none, so that dx is nothing but rounding however many
+    positions a thread adds.  What dx may be is formulas()' tolerance at w = 1: the terms of t's mean (30 u beside the
+    slope's own roundings, which are the same in all terms), n's mean times t's, and the products."""
+    N, L, C, G = 456, 2048, 2048, 8
+    gen = torch.Generator("cuda").manual_seed(0)
+    x = torch.empty(N, L, C, device="cuda").normal_(generator=gen)
+    dy, z = (torch.full((C,), v, device="cuda").expand(N, L, C) for v in (0.1, 0.3))
+    stats = torch.empty(N, G, 2, device="cuda")
+    hla2.hla2_groupnorm(x, G, gate=z, activation="silu", stats=stats, Y=torch.empty_like(x))
+    dx, dw, db, dgate = hla2.hla2_groupnorm_backward(x, dy, stats, gate=z, activation="silu")
+    t = float(torch.tensor(0.1).double() * torch.nn.functional.silu(torch.tensor(0.3).double()))
+    for i in (0, 200, N - 1):
+        mean, r = (s.repeat_interleave(C // G).double() for s in stats[i].unbind(-1))
+        n = ((x[i].double() - mean) * r).abs()
+        # n's own mean is 30 u of the largest |x|, which moves mean(t n) as much
+        top = float(x[i].abs().max())
+        slack = t * r * U * (30 + 80 + n * (30 * float(n.mean()) + 30 * top * float(r.max()) + 40))
+        assert bool((dx[i].double().abs() <= slack).all()), float((dx[i].double().abs() / slack).max())
+    # equal terms: a sum's error is that of its few levels
+    assert float((db.double() / (t * N * L) - 1).abs().max()) <= 60 * U
