@@ -349,7 +349,7 @@ __device__ __forceinline__ RunSpot run_spot(const GNormParams& p) {
     r.cols = min((p.C + 7) / 8, kThreads);  // threads along the channels
     r.n = blockIdx.x / p.runs;
     r.l0 = (int)(blockIdx.x % p.runs) * p.run;
-    r.l1 = min(r.l0 + p.run, p.L);
+    r.l1 = r.l0 + min(p.run, p.L - r.l0);  // (sums of positions may pass 2^31 - 1 next to the largest L)
     r.rows = kThreads / r.cols;
     r.row = threadIdx.x / r.cols;
     r.c = (blockIdx.y * kThreads + threadIdx.x % r.cols) * 8;
@@ -646,17 +646,18 @@ __global__ void __launch_bounds__(kThreads, VEC ? (GRAD ? 2 : kRunBlocks) : 1) g
             m2[j] = m.y;
         }
     }
-    const T* const xp = static_cast<const T*>(p.x.p) + r.n * p.x.sn + r.c;
-    const T* const zp = static_cast<const T*>(p.z.p) + r.n * p.z.sn + r.c;
-    const T* const gp = static_cast<const T*>(p.dy.p) + r.n * p.dy.sn + r.c;
-    T* const yp = static_cast<T*>(p.y) + r.n * p.yn + r.c;
-    T* const dp = static_cast<T*>(p.dz) + r.n * p.dzn + r.c;
-    for (int l0 = r.l0 + r.row; l0 < r.l1; l0 += M * r.rows) {
+    const T* const xp = static_cast<const T*>(p.x.p) + r.n * p.x.sn + r.l0 * p.x.sl + r.c;
+    const T* const zp = static_cast<const T*>(p.z.p) + r.n * p.z.sn + r.l0 * p.z.sl + r.c;
+    const T* const gp = static_cast<const T*>(p.dy.p) + r.n * p.dy.sn + r.l0 * p.dy.sl + r.c;
+    T* const yp = static_cast<T*>(p.y) + r.n * p.yn + r.l0 * p.yl + r.c;
+    T* const dp = static_cast<T*>(p.dz) + r.n * p.dzn + r.l0 * p.dzl + r.c;
+    const int len = r.l1 - r.l0;
+    for (int l0 = r.row; l0 < len; l0 += M * r.rows) {
         Lane<T, 8, VEC> xv[M], zv[M], gv[M];
 #pragma unroll
         for (int i = 0; i < M; ++i) {
             const int l = l0 + i * r.rows;
-            if (l < r.l1) {
+            if (l < len) {
                 xv[i].load(xp + l * p.x.sl, r.live);
                 if (GATE) zv[i].load(zp + l * p.z.sl, r.live);
                 if (GRAD) gv[i].load(gp + l * p.dy.sl, r.live);
@@ -665,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, VEC ? (GRAD ? 2 : kRunBlocks) : 1) g
 #pragma unroll
         for (int i = 0; i < M; ++i) {
             const int l = l0 + i * r.rows;
-            if (l >= r.l1) break;
+            if (l >= len) break;
             float x[8], z[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -721,10 +722,10 @@ GPlan gnorm_plan(long long N, int L, int C, int G, bool grad) {
     const int across = (C + kUnit - 1) / kUnit;
     // enough blocks to fill the SMs, runs of 16 positions or more
     long long runs = ((long long)kRunBlocks * sm_count() + N * across - 1) / (N * across);
-    if (runs > (L + 15) / 16) runs = (L + 15) / 16;
-    if (runs < 1) runs = 1;
+    const long long most = (L + 15LL) / 16;
+    if (runs > most) runs = most;
     g.run = (int)((L + runs - 1) / runs);
-    g.runs = (L + g.run - 1) / g.run;
+    g.runs = (int)((L + (long long)g.run - 1) / g.run);
     g.lines = N * g.runs;
     g.part = (size_t)g.lines * 2 * C;
     g.means = (size_t)N * G * 2;

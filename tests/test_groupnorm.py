@@ -188,6 +188,14 @@ def test_binding_refuses():
             pytest.fail(f"call {i} was taken")
 
 
+@pytest.mark.parametrize("L", [2 ** 30, 2 ** 31 - 5 * 10 ** 6, 2 ** 31 - 10 ** 6, 2 ** 31 - 16, 2 ** 31 - 15, 2 ** 31 - 1])
+def test_workspace_up_to_the_largest_length(L):
+    """A line of two sums for each run of one sample, as many runs as fill the SMs three times (of up to 200)."""
+    for backward in (False, True):
+        need = hla2.hla2_groupnorm_workspace(1, L, 1, 1, backward)
+        assert 100 * 8 < need <= 601 * 8 + 256
+
+
 # ------------------------------------------------------------------- GPU ----
 SHAPES = [  # N, L (0: two dimensions), C, G
     (1, 0, 1, 1), (3, 0, 8, 1), (2, 0, 30, 3), (5, 0, 240, 8), (7, 0, 2048, 16), (1000, 0, 64, 4), (4, 0, 2048, 1),
@@ -432,3 +440,33 @@ def test_gradient_of_equal_terms_over_long_runs():
         assert bool((dx[i].double().abs() <= slack).all()), float((dx[i].double().abs() / slack).max())
     # equal terms: a sum's error is that of its few levels
     assert float((db.double() / (t * N * L) - 1).abs().max()) <= 60 * U
+
+
+@pytest.mark.gpu
+def test_largest_length():
+    """2^31 - 1 positions: the ends of the last runs."""
+    L = 2 ** 31 - 1
+    gen = torch.Generator("cuda").manual_seed(0)
+    x = torch.empty(1, L, 1, device="cuda", dtype=BF).normal_(generator=gen)
+    pieces = x.view(-1).split(2 ** 28)
+    mean = sum(float(c.double().sum()) for c in pieces) / L
+    rstd = (sum(float((c.double() - mean).square().sum()) for c in pieces) / L + 1e-5) ** -0.5
+    stats = torch.empty(1, 1, 2, device="cuda")
+    y = hla2.hla2_groupnorm(x, 1, stats=stats)
+    top = float(x.abs().max())
+    assert abs(float(stats[0, 0, 0]) - mean) <= 30 * U * top
+    assert abs(float(stats[0, 0, 1]) - rstd) <= 60 * U * rstd * (1 + top * rstd)
+    for c, got in zip(pieces, y.view(-1).split(2 ** 28)):
+        n = (c.double() - mean) * rstd
+        slack = 30 * U * top * rstd + 44 * U * n.abs()
+        unit = torch.ldexp(torch.ones_like(n), torch.frexp((n.abs() + slack).clamp(min=2.0 ** -126)).exponent - 9)
+        assert bool(((got.double() - n).abs() <= slack + unit).all())
+        del n, slack, unit
+    dx, dw, db, _ = hla2.hla2_groupnorm_backward(x, y, stats)
+    # dy is y: the gradient is the rounding of y to bf16 alone, all along
+    for c, g in zip(pieces, dx.view(-1).split(2 ** 28)):
+        assert float(g.abs().max()) <= rstd * (2.0 ** -8 * (top - mean) * rstd * 2.5 + 1e-4)
+    # dw of the statistics that it was given: two roundings of n, pieces of sixteen terms, a few levels on top
+    mean, rstd = (float(v) for v in stats[0, 0])
+    want = sum(float(((c.double() - mean) * rstd * g.double()).sum()) for c, g in zip(pieces, y.view(-1).split(2 ** 28)))
+    assert abs(float(dw[0]) / want - 1) <= 40 * U
