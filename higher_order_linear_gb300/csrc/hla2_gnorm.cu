@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, VEC ? kFwdBlocks : 2) gnorm_unit_ker
     at.weights(p.w, p.wdtype, c0, 1.f, w);
     at.weights(p.b, p.wdtype, c0, 0.f, b);
     for (long long n0 = (long long)blockIdx.x * p.spb; n0 < p.N; n0 += step, n += step) {
-        float x[8], z[8], sum = 0.f, sq = 0.f, none = 0.f;
+        float x[8], z[8], sum = 0.f, sq = 0.f, rest = 0.f, none = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             x[j] = VEC || j < at.n ? xr[0].get(j) : 0.f;
@@ -228,16 +228,31 @@ __global__ void __launch_bounds__(kThreads, VEC ? kFwdBlocks : 2) gnorm_unit_ker
         fetch(n + AHEAD * step, AHEAD - 1);
         if (!mine) sum = 0.f;
         unit_sum<false>(sum, none, p.tpr, sh[0]);
-        const float mean = even ? sum * inv : sum / (float)values;  // (equal values have their mean)
+        // Equal values are their mean.  In 16 bits by themselves: 2048 of them add up exactly.  In 32 bits the
+        // sum has been rounded, and the mean of what is left is taken off as well.
+        constexpr bool TWICE = sizeof(T) == 4;
+        float mean = even ? sum * inv : sum / (float)values;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             x[j] -= mean;
-            if (VEC || j < at.n) sq = fmaf(x[j], x[j], sq);
+            if (VEC || j < at.n) {
+                sq = fmaf(x[j], x[j], sq);
+                if (TWICE) rest += x[j];
+            }
         }
-        if (!mine) sq = 0.f;
-        unit_sum<false>(sq, none, p.tpr, sh[1]);
+        if (!mine) sq = rest = 0.f;
+        unit_sum<TWICE>(sq, rest, p.tpr, sh[1]);
         if (!mine || n >= p.N) continue;
-        const float rstd = rsqrtf(fmaf(sq, inv, p.eps));
+        float var = sq * inv;
+        if (TWICE) {
+            rest *= inv;
+            mean += rest;
+            var = fmaf(-rest, rest, var);
+            if (var < 0.f) var = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] -= rest;
+        }
+        const float rstd = rsqrtf(var + p.eps);
         if (p.stats && lane == 0) *reinterpret_cast<float2*>(p.stats + (n * p.G + g) * 2) = make_float2(mean, rstd);
         float y[8];
 #pragma unroll
@@ -587,7 +602,8 @@ __global__ void __launch_bounds__(kThreads) gnorm_fold_kernel(const GNormParams 
     const long long n = blockIdx.x / p.G;
     const int g = (int)(blockIdx.x % p.G), items = p.runs * p.cg;
     const float* const part = p.part + n * p.runs * 2 * p.C + g * p.cg;
-    const float count = (float)p.L * (float)p.cg;  // (divided by, so that equal values have their mean)
+    const float count = (float)p.L * (float)p.cg;
+    const float about = GRAD ? 0.f : part[0];  // means are added about one of them: equal values are their mean
     LongSum first, second;
     for (int i = threadIdx.x; i < items; i += kThreads) {
         const int k = i / p.cg, c = i - k * p.cg;
@@ -597,10 +613,10 @@ __global__ void __launch_bounds__(kThreads) gnorm_fold_kernel(const GNormParams 
             first.add(w * v[p.C]);
             second.add(w * v[0]);
         } else {
-            first.add((float)min(p.run, p.L - k * p.run) * v[0]);
+            first.add((float)min(p.run, p.L - k * p.run) * (v[0] - about));
         }
     }
-    const float a = block_sum(first, sh) / count;
+    const float a = about + block_sum(first, sh) / count;
     if (!GRAD)
         for (int i = threadIdx.x; i < items; i += kThreads) {
             const int k = i / p.cg, c = i - k * p.cg;

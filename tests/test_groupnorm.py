@@ -470,3 +470,21 @@ def test_largest_length():
     mean, rstd = (float(v) for v in stats[0, 0])
     want = sum(float(((c.double() - mean) * rstd * g.double()).sum()) for c, g in zip(pieces, y.view(-1).split(2 ** 28)))
     assert abs(float(dw[0]) / want - 1) <= 40 * U
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", [(400, 0, 64, 4), (50, 0, 2048, 16), (30, 0, 90, 3), (20, 2, 2048, 2), (8, 1000, 32, 4), (3, 300, 45, 3)])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_equal_values_of_all_bits(shape, dtype):
+    """Equal values of 24 bits, another in each sample: n is zero but for what a first mean is off by (17 roundings: eight
+    values to a thread, eight levels, the quotient), which the second pass takes away to 17 roundings of itself."""
+    x = make(*shape, dtype, False, F32)
+    gen = torch.Generator().manual_seed(7)
+    v = (1000 + 1000 * torch.rand(shape[0], generator=gen)).to(dtype)
+    x["x"][:] = v.view(-1, *[1] * (x["x"].dim() - 1))
+    G = shape[3]
+    stats = torch.empty(shape[0], G, 2, device="cuda")
+    y = hla2.hla2_groupnorm(x["x"].cuda(), G, x["w"].cuda(), x["b"].cuda(), stats=stats).cpu().double()
+    assert torch.equal(stats[..., 0].cpu(), v.float()[:, None].expand(-1, G))
+    slack = (17 * U) ** 2 * 2000 * 1e-5 ** -0.5 * x["w"].double().abs() + U * x["b"].double().abs()
+    assert bool((excess(y.to(dtype) if dtype == BF else y, x["b"].double().expand(y.shape), slack) <= slack).all())
