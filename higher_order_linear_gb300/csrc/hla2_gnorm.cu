@@ -22,6 +22,8 @@
 // MB) 41 us with the lines of dw and db (43 had the second launch waited for the
 // first's end).  8 maps of 4096 x 512 with silu: 31 us for sums, fold and the second pass
 // (67 MB: 10 us at the copy bandwidth; 37 had each launch waited for the last one's end).
+#include <type_traits>
+
 #include "hla2_layer.cuh"
 
 namespace hla2 {
@@ -561,7 +563,7 @@ __device__ __forceinline__ float block_sum(const LongSum& sum, float* sh) {
 constexpr int kFoldColumns = 16, kFoldThreads = 1024;
 template <int THREADS>
 __device__ __forceinline__ void fold_lines(const float* part, float* out, long long lines,
-                                           int width, int block, float (*sh)[kFoldColumns]) {
+                                           int width, int block, bool add, float (*sh)[kFoldColumns]) {
     const int col = threadIdx.x % kFoldColumns, line = threadIdx.x / kFoldColumns;
     const int c = block * kFoldColumns + col;
     LongSum sum;
@@ -577,26 +579,26 @@ __device__ __forceinline__ void fold_lines(const float* part, float* out, long l
         a = 0.f;
 #pragma unroll
         for (int i = 0; i < THREADS / 32; ++i) a += sh[i][col];
-        out[c] = a;
+        out[c] = add ? out[c] + a : a;
     }
 }
 __global__ void __launch_bounds__(kFoldThreads) gnorm_lines_kernel(const float* part, float* out,
                                                                    long long lines, int width) {
     __shared__ float sh[kFoldThreads / 32][kFoldColumns];
     follow();
-    fold_lines<kFoldThreads>(part, out, lines, width, blockIdx.x, sh);
+    fold_lines<kFoldThreads>(part, out, lines, width, blockIdx.x, false, sh);
 }
 
 // A group's runs and channels folded: mean and reciprocal deviation, or (GRAD)
 // the means of t and t n, which go behind the partial sums.  The blocks behind the
-// groups' fold the gradient's lines.
+// groups' fold the gradient's lines (add: to those of the samples before).
 template <bool GRAD>
-__global__ void __launch_bounds__(kThreads) gnorm_fold_kernel(const GNormParams p, float* out) {
+__global__ void __launch_bounds__(kThreads) gnorm_fold_kernel(const GNormParams p, float* out, bool add) {
     __shared__ float sh[kThreads / 32];
     follow();
     if (GRAD && blockIdx.x >= p.N * p.G) {
         __shared__ float columns[kThreads / 32][kFoldColumns];
-        fold_lines<kThreads>(p.part, p.dw, p.N * p.runs, 2 * p.C, (int)(blockIdx.x - p.N * p.G), columns);
+        fold_lines<kThreads>(p.part, p.dw, p.N * p.runs, 2 * p.C, (int)(blockIdx.x - p.N * p.G), add, columns);
         return;
     }
     const long long n = blockIdx.x / p.G;
@@ -714,9 +716,15 @@ struct GPlan {
     bool unit;
     int tpr, gpb, spb, blocks;  // units in registers; blocks along the samples in the gradient
     int run, runs;
+    long long slab;      // large units: samples whose sums are held at a time
     long long lines;     // of partial sums
     size_t part, means;  // floats of partial sums; of the gradient's means behind them
 };
+
+// Large units take their samples in slabs whose partial sums have this many bytes at most (16384 blocks or more then).
+// A run of a wide row is one position, whose sums are twice the size of an fp32 row: 65536 x 16384 held 8.6 GB of
+// them.  (16384 x 8192 in 16 bits, of 1.07 GB: 1.91 ms at once, 2.00 by 256 MB, 2.23 by 64 MB.)
+constexpr size_t kPartBytes = size_t(256) << 20;
 
 GPlan gnorm_plan(long long N, int L, int C, int G, bool grad) {
     GPlan g{};
@@ -742,9 +750,11 @@ GPlan gnorm_plan(long long N, int L, int C, int G, bool grad) {
     if (runs > most) runs = most;
     g.run = (int)((L + runs - 1) / runs);
     g.runs = (int)((L + (long long)g.run - 1) / g.run);
-    g.lines = N * g.runs;
+    const long long fit = (long long)(kPartBytes / ((size_t)g.runs * 2 * C * 4));  // (one sample's runs are far below)
+    g.slab = N < fit ? N : fit;
+    g.lines = g.slab * g.runs;
     g.part = (size_t)g.lines * 2 * C;
-    g.means = (size_t)N * G * 2;
+    g.means = (size_t)g.slab * G * 2;
     return g;
 }
 
@@ -787,19 +797,35 @@ cudaError_t run_gnorm(GNormParams p, const GPlan& g, int dtype, bool vec, cudaSt
             note_launches(1);
             return cudaGetLastError();
         }
-        const dim3 grid((unsigned)(p.N * g.runs), (p.C + kUnit - 1) / kUnit);
         float* const means = p.part + g.part;
-        float* const folded = GRAD || !p.stats ? means : p.stats;
-        cudaError_t e;
-        if constexpr (GRAD) e = launch_following(gnorm_sums_kernel<T, VEC, GATE, SILU>, grid, kThreads, 0, s, false, p);
-        else e = launch_following(gnorm_moments_kernel<T, VEC>, grid, kThreads, 0, s, false, p);
         const unsigned lines = GRAD && p.dw ? (2 * p.C + kFoldColumns - 1) / kFoldColumns : 0;
-        if (e == cudaSuccess)
-            e = launch_following(gnorm_fold_kernel<GRAD>, dim3((unsigned)(p.N * p.G) + lines), kThreads, 0, s, true, p, folded);
-        if (!GRAD) p.stats = folded;
-        if (e == cudaSuccess)
-            e = launch_following(gnorm_apply_kernel<T, VEC, GRAD, GATE, SILU>, grid, kThreads, 0, s, true, p, means);
-        return e;
+        for (long long n0 = 0; n0 < p.N; n0 += g.slab) {
+            GNormParams q = p;
+            q.N = p.N - n0 < g.slab ? p.N - n0 : g.slab;
+            auto ahead = [&](auto* at, long long stride) {
+                using P = std::conditional_t<std::is_const_v<std::remove_pointer_t<decltype(at)>>, const T, T>;
+                return at ? static_cast<P*>(at) + n0 * stride : nullptr;
+            };
+            q.x.p = ahead(p.x.p, p.x.sn);
+            q.z.p = ahead(p.z.p, p.z.sn);
+            q.dy.p = ahead(p.dy.p, p.dy.sn);
+            q.y = ahead(p.y, p.yn);
+            q.dz = ahead(p.dz, p.dzn);
+            if (p.stats) q.stats = p.stats + n0 * p.G * 2;
+            float* const folded = GRAD || !p.stats ? means : q.stats;
+            const dim3 grid((unsigned)(q.N * g.runs), (p.C + kUnit - 1) / kUnit);
+            cudaError_t e;
+            if constexpr (GRAD) e = launch_following(gnorm_sums_kernel<T, VEC, GATE, SILU>, grid, kThreads, 0, s, n0 > 0, q);
+            else e = launch_following(gnorm_moments_kernel<T, VEC>, grid, kThreads, 0, s, n0 > 0, q);
+            if (e == cudaSuccess)
+                e = launch_following(gnorm_fold_kernel<GRAD>, dim3((unsigned)(q.N * p.G) + lines), kThreads, 0, s, true, q, folded,
+                                     n0 > 0);
+            if (!GRAD) q.stats = folded;
+            if (e == cudaSuccess)
+                e = launch_following(gnorm_apply_kernel<T, VEC, GRAD, GATE, SILU>, grid, kThreads, 0, s, true, q, means);
+            if (e != cudaSuccess) return e;
+        }
+        return cudaSuccess;
     };
     using yes = std::true_type;
     using no = std::false_type;

@@ -196,6 +196,14 @@ def test_workspace_up_to_the_largest_length(L):
         assert 100 * 8 < need <= 601 * 8 + 256
 
 
+@pytest.mark.parametrize("N,L,C,G", [(16384, 1, 8192, 1), (65536, 1, 16384, 1), (1 << 20, 1, 16384, 4), (1 << 20, 8, 512, 1),
+                                     (1000, 2000, 240, 8)])
+def test_workspace_of_many_samples(N, L, C, G):
+    """The partial sums of large units do not grow with the batch beyond 256 MB (and two means for each group)."""
+    for backward in (False, True):
+        assert 0 < hla2.hla2_groupnorm_workspace(N, L, C, G, backward) <= (256 << 20) * (1 + 2 * G / (2 * C)) + 256
+
+
 # ------------------------------------------------------------------- GPU ----
 SHAPES = [  # N, L (0: two dimensions), C, G
     (1, 0, 1, 1), (3, 0, 8, 1), (2, 0, 30, 3), (5, 0, 240, 8), (7, 0, 2048, 16), (1000, 0, 64, 4), (4, 0, 2048, 1),
@@ -488,3 +496,10 @@ def test_equal_values_of_all_bits(shape, dtype):
     assert torch.equal(stats[..., 0].cpu(), v.float()[:, None].expand(-1, G))
     slack = (17 * U) ** 2 * 2000 * 1e-5 ** -0.5 * x["w"].double().abs() + U * x["b"].double().abs()
     assert bool((excess(y.to(dtype) if dtype == BF else y, x["b"].double().expand(y.shape), slack) <= slack).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,gate", [(F32, False), (BF, True)])
+@pytest.mark.parametrize("shape", [(8400, 0, 4096, 1), (8300, 0, 4102, 1), (2100, 0, 16384, 4)])
+def test_more_samples_than_are_held_at_a_time(shape, dtype, gate):
+    check(make(*shape, dtype, gate, F32), "silu")
