@@ -503,3 +503,31 @@ def test_equal_values_of_all_bits(shape, dtype):
 @pytest.mark.parametrize("shape", [(8400, 0, 4096, 1), (8300, 0, 4102, 1), (2100, 0, 16384, 4)])
 def test_more_samples_than_are_held_at_a_time(shape, dtype, gate):
     check(make(*shape, dtype, gate, F32), "silu")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,shift", [(BF, 0), (BF, 1), (F32, 0)])
+@pytest.mark.parametrize("N,L,C,far", [(2, 1, 256, "sample"), (2, 300, 64, "sample"), (1, 3, 64, "position"), (1, 3, 4096, "position")])
+def test_offsets_beyond_32_bits(N, L, C, far, dtype, shift):
+    """Samples, or positions, more than 2^32 elements apart, in both forms."""
+    G, step = 2, 2 ** 32 + 64
+    x = make(N, L, C, G, dtype, True, F32)
+    size = L * C if far == "sample" else C
+    room = torch.empty(step * (N - 1 if far == "sample" else L - 1) + 5 * size + 64, device="cuda", dtype=dtype)
+
+    def place(i):
+        return room.as_strided((N, L, C), (step, C, 1) if far == "sample" else (64, step, 1), i * size + shift)
+
+    y = {k: (dev(v) if k != "G" else v) for k, v in x.items()}
+    for i, name in enumerate(("x", "dy", "z")):
+        y[name] = place(i).copy_(y[name])
+    check(x, "silu", y)
+    want = formulas(x, "silu")
+    stats = torch.empty(N, G, 2, device="cuda")
+    kw = dict(gate=y["z"], activation="silu")
+    near("y", hla2.hla2_groupnorm(y["x"], G, y["w"], y["b"], stats=stats, Y=place(3), **kw), want["y"])
+    dx, _, _, dgate = hla2.hla2_groupnorm_backward(y["x"], y["dy"], stats, y["w"], y["b"], dX=place(3), dgate=place(4), **kw)
+    near("dx", dx, want["dx"])
+    near("dgate", dgate, want["dgate"])
+    del room, y, dx, dgate
+    torch.cuda.empty_cache()

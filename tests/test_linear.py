@@ -672,3 +672,116 @@ def test_calls_in_a_row(dtype, B, H, T, d, captured):
     assert all(torch.isfinite(t).all() for t in want)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert hla2.hla2_device_status() == 0
+
+
+def backward_near(x, y, outs=None, lens=None):
+    """check_backward with outputs of the caller's, on tensor cores or off them one by one: the wider tolerance."""
+    B, H, T, d = x["q"].shape
+    dv = x["v"].shape[-1]
+    ls = [T] * B if lens is None else lens
+    d0 = torch.full((B, H, d, dv), float("nan"), device="cuda")
+    got = hla2.hla2_linear_backward(y["q"], y["k"], y["v"], y["gamma"], y["do"], *(outs or (None,) * 3), state_in=y["h0"],
+                                    lengths=None if lens is None else torch.tensor(lens, dtype=torch.int32).cuda(),
+                                    dstate_out=y["dlast"], dstate_in=d0)
+    for name, grad, args, width in (("dq", got[0], (x["do"], x["v"], x["k"], x["h0"].mT, ls), dv),
+                                    ("dk", got[1], (x["v"], x["do"], x["q"], x["dlast"].mT, ls, True), dv),
+                                    ("dv", got[2], (x["k"], x["q"], x["do"], x["dlast"], ls, True), d)):
+        ref, S, m2, m1, A = by_block(x["gamma"], *args)
+        near(grad, ref, m1, m2, width, T, True, name)
+        if name == "dv":
+            near(d0, S, A, None, d, T, True, "dstate_in")
+    return got
+
+
+def unaligned(t, off=1):
+    """The same values `off` elements behind a 16-byte step, rows and heads as far apart as t's."""
+    room = torch.empty(t.numel() + 8, device=t.device, dtype=t.dtype)
+    out = room[off:off + t.numel()].view(t.shape)
+    return out.copy_(t)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,H,T,d,dv", [(1, 2, 3000, 64, 64), (1, 1, 5000, 128, 96), (3, 40, 300, 64, 64)])
+@pytest.mark.parametrize("off", ["k", "v", "dk", "dv", "dq", "do"])
+def test_each_gradient_on_its_own_path(B, H, T, d, dv, off):
+    """One tensor of the call alone keeps the walks that touch it from the tensor cores; the others go on there, and
+    no walk takes the states of another's cut of the sequence."""
+    x = make(B, H, T, d, dv, BF)
+    y = dev(x)
+    outs = [torch.empty_like(y[n]) for n in "qkv"]
+    if off in y:
+        y[off] = unaligned(y[off])
+    else:
+        outs["qkv".index(off[1])] = unaligned(outs["qkv".index(off[1])])
+    backward_near(x, y, outs)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("T,d", [(70, 64), (3000, 128)])
+def test_states_off_their_step(T, d, dtype):
+    """States 4 bytes off a 16-byte step, with one segment and with several."""
+    x = make(1, 2, T, d, d, dtype)
+    y = dev(x)
+    want = torch.empty(1, 2, d, d, device="cuda")
+    o = hla2.hla2_linear_forward(y["q"], y["k"], y["v"], y["gamma"], state_in=y["h0"], state_out=want)
+    last = unaligned(want)
+    last.fill_(float("nan"))
+    o2 = hla2.hla2_linear_forward(y["q"], y["k"], y["v"], y["gamma"], state_in=unaligned(y["h0"]), state_out=last)
+    assert torch.equal(o, o2) and torch.equal(want, last)
+    args, d0 = (y["q"], y["k"], y["v"], y["gamma"], y["do"]), torch.empty_like(want)
+    grads = hla2.hla2_linear_backward(*args, state_in=y["h0"], dstate_out=y["dlast"], dstate_in=d0)
+    last.fill_(float("nan"))
+    again = hla2.hla2_linear_backward(*args, state_in=unaligned(y["h0"]), dstate_out=unaligned(y["dlast"]), dstate_in=last)
+    assert all(torch.equal(a, b) for a, b in zip((*grads, d0), (*again, last)))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,shift", [(BF, 0), (BF, 1), (F32, 0)])
+@pytest.mark.parametrize("far", ["batch", "token"])
+def test_offsets_beyond_32_bits(far, dtype, shift):
+    """Sequences, or tokens, more than 2^32 elements apart."""
+    B, H, T, d = (2, 2, 150, 16) if far == "batch" else (1, 2, 3, 16)
+    step = 2 ** 32 + 64
+    x = make(B, H, T, d, d, dtype)
+    y = dev(x)
+    size = H * T * d
+    room = torch.empty(step * (B - 1 if far == "batch" else T - 1) + 8 * size + 64, device="cuda", dtype=dtype)
+
+    def place(i):
+        strides = (step, T * d, d, 1) if far == "batch" else (1 << 20, d, step, 1)
+        return room.as_strided((B, H, T, d), strides, i * size + shift)
+
+    for i, name in enumerate(("q", "k", "v", "do")):
+        y[name] = place(i).copy_(y[name])
+    ref, _, m2, m1, _ = by_block(x["gamma"], x["q"], x["k"], x["v"], x["h0"], [T] * B)
+    o = hla2.hla2_linear_forward(y["q"], y["k"], y["v"], y["gamma"], O=place(4), state_in=y["h0"])
+    near(o, ref, m1, m2, d, T, True, "o")
+    backward_near(x, y, [place(i) for i in (5, 6, 7)])
+    del room, o, y
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_lengths_outside_the_sequence(dtype):
+    """Lengths are taken into 0..T."""
+    x = make(4, 2, 200, 32, 32, dtype)
+    y = dev(x)
+    args, states = (y["q"], y["k"], y["v"], y["gamma"]), [torch.empty(4, 2, 32, 32, device="cuda") for _ in range(4)]
+    outs = []
+    for lens, last, d0 in (([-3, 205, 2 ** 31 - 1, 100], *states[:2]), ([0, 200, 200, 100], *states[2:])):
+        ls = torch.tensor(lens, dtype=torch.int32).cuda()
+        o = torch.zeros(4, 2, 200, 32, device="cuda", dtype=dtype)
+        outs.append((hla2.hla2_linear_forward(*args, O=o, lengths=ls, state_in=y["h0"], state_out=last),
+                     *hla2.hla2_linear_backward(*args, y["do"], lengths=ls, state_in=y["h0"], dstate_out=y["dlast"], dstate_in=d0)))
+    assert all(torch.equal(a, b) for a, b in zip((*outs[0], *states[:2]), (*outs[1], *states[2:])))
+    assert torch.equal(states[0][0], y["h0"][0]) and torch.equal(states[1][0], y["dlast"][0])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_as_many_heads_as_there_may_be(dtype):
+    x = make(257, 255, 3, 8, 8, dtype)
+    check_forward(x)
+    check_backward(x)
