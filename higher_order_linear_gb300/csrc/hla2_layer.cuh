@@ -1,6 +1,6 @@
 // hla2_layer.cuh -- what the operators around the attention layer share
-// (hla2_gated.cu, hla2_norm.cu, hla2_rotary.cu): typed vector accesses and the
-// host-side checks of their entry points.
+// (hla2_gated*.cu, hla2_norm.cu, hla2_rotary.cu, hla2_linear*.cu, hla2_gnorm.cu): typed
+// vector accesses, launches in a row and the host-side checks of their entry points.
 #pragma once
 
 #include <cmath>
@@ -126,7 +126,7 @@ __device__ __forceinline__ bf16 from_f32<bf16>(float x) { return __float2bfloat1
 // caller's inputs.  Behind follow() the kernel before is complete, and since that one lets nobody start before its
 // own follow(), so are all the others: what the call's kernels hand on (never by read-only loads, which would allow
 // an old copy) and its outputs are touched only behind it.  Every kernel of the row has one; the first starts like
-// any other, after all the stream was given.  CTAs that find room where earlier ones have ended also fill the gap
+// any other, after all the stream was given, and so does whatever is launched behind the row in the usual way.  CTAs that find room where earlier ones have ended also fill the gap
 // that a kernel's last CTAs leave.  (Plain launches and these.  Training of the linear attention, 4 x 4096 x 16 x 64:
 // 227 and 198 us; 16384 x 16 x 128: 347 and 329; 2 x 1023 x 3 x 80 in fp32: 152 and 132.)
 __device__ __forceinline__ void follow() {

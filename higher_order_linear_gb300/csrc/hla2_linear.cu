@@ -373,8 +373,9 @@ __global__ void __launch_bounds__(256) lin_step_kernel(const float* state, const
 // Segments per head, each a CTA.  The count with the least time, in units of a
 // chunk of the output walk: rounds of CTAs, each its chunks and about one to
 // start; the states' walk, the scan and two more launches where there are several
-// segments.  Measured: a chunk takes 2.8 us on the tensor cores (1.25 times that with
-// two CTAs on the SM), the states' walk 0.6 of the output walk, the scan and the
+// segments.  Measured: a chunk takes 2.8 us on the tensor cores (1.25 times that where
+// CTAs are more than SMs: two share one up to width 64; above it the factor is a price
+// on further rounds that was not measured by itself), the states' walk 0.6 of the output walk, the scan and the
 // launches 17 us (alone; the overlap of a call's kernels gives some back); the CUDA
 // cores take some 20 us for a chunk and 0.45 for its states.
 struct SegmentCost {

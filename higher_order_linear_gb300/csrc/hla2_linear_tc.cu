@@ -48,14 +48,6 @@ namespace {
 
 static_assert(kL == kLinTcChunk, "a chunk is the M of the products");
 
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int t, int h, int b,
-                                            uint32_t mbar) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
-        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(t), "r"(h), "r"(b), "r"(mbar)
-        : "memory");
-}
-
 // 8 packed words of this thread's lane
 __device__ __forceinline__ void tmem_store8(uint32_t taddr, const uint32_t (&r)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
@@ -122,7 +114,7 @@ __device__ __forceinline__ bool mbar_long_try(uint32_t a, uint32_t parity) {
     return ok != 0;
 }
 
-// Warps and shared memory.  Tiles of A: NA, of B and C: NB; the ring's slots hold
+// Warps and shared memory.  One tile of A (outputs), NB of B and C; the ring's slots hold
 // the terms of STEP tokens of B~ but the first; the stage a group of SC
 // output columns of each O warp.  At D = 64 two CTAs share an SM: sixteen warps of
 // 64 registers each (X and O are the same four), half of tensor memory, and
@@ -144,9 +136,9 @@ struct TcLayout {
     static constexpr int kItems = STEP / 4 * (D / 64);  // of 4 tokens by 64 channels in a step
     static constexpr int PER = kItems < kY ? kItems : kY;  // warps that share a step, kItems / PER items each
     static constexpr int SC = D == 128 && TERMS == 2 ? 64 : 32;
-    static constexpr int NA = OUT ? 1 : 0, NB = 2;
+    static constexpr int NB = 2;
     static constexpr uint32_t kTile = kL * D * 2, kPart = STEP * D * 2, kStage = 32 * SC * 2;
-    static constexpr uint32_t A = 0, B = NA * kTile, C = B + NB * kTile, ring = C + NB * kTile;
+    static constexpr uint32_t A = 0, B = OUT ? kTile : 0, C = B + NB * kTile, ring = C + NB * kTile;
     static constexpr uint32_t S = ring + 2 * (TERMS - 1) * kPart;
     static constexpr uint32_t stage = S + (D == 64 || OUT ? D * D * 2 : 0), kBytes = stage + (OUT ? 4 * kStage : 0);
 };
@@ -156,13 +148,13 @@ __global__ void __launch_bounds__(TcLayout<D, OUT, TERMS>::kThreads, TcLayout<D,
 lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorMap mB,
               const __grid_constant__ CUtensorMap mC, const LinWalk p) {
     using LY = TcLayout<D, OUT, TERMS>;
-    constexpr int NA = LY::NA, NA1 = NA ? NA : 1, NB = LY::NB, STEP = LY::STEP, STEPS = kL / STEP, PER = LY::PER, ITEMS = LY::kItems / PER;
+    constexpr int NB = LY::NB, STEP = LY::STEP, STEPS = kL / STEP, PER = LY::PER, ITEMS = LY::kItems / PER;
     extern __shared__ __align__(1024) unsigned char dsm_raw[];
     // A barrier's next phase never completes before everybody has seen this one: it takes an arrival that each waiter
     // gives after its wait.  (P of the next chunk needs no arrival of Y, so its barriers go by turns.)
     // loads | A read (O2 = A S done) | B and C read (by both issuers) | P ready, packed | ring filled, free |
     // U ready, drained | S copy ready | O ready (P's columns free), drained | last waits
-    enum { LA, LB = LA + NA, LC = LB + NB, FA = LC + NB, FB = FA + NA1, CP = FB + NB, DP = CP + 2, KQ, RF = KQ + 2, CU = RF + 2,
+    enum { LA, LB, LC = LB + NB, FA = LC + NB, FB, CP = FB + NB, DP = CP + 2, KQ, RF = KQ + 2, CU = RF + 2,
            DU = CU + 2, DS = DU + 2, CO, DO, FIN, NBAR = FIN + 2 };
     __shared__ __align__(8) unsigned long long bars[NBAR];
     __shared__ __align__(16) float pw[kL + 4];  // g^0 .. g^128
@@ -184,7 +176,7 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
     auto tokens_of = [&](int it) { return min(kL, len - chunk_of(it) * kL); };
 
     const uint32_t dsm = (smem_u32(dsm_raw) + 1023u) & ~1023u;
-    auto tA = [&](int it) { return Tile{dsm + LY::A + (uint32_t)(it % NA1) * LY::kTile, kL}; };
+    const Tile tA{dsm + LY::A, kL};
     auto tB = [&](int it) { return Tile{dsm + LY::B + (uint32_t)(it % NB) * LY::kTile, kL}; };
     auto tC = [&](int it) { return Tile{dsm + LY::C + (uint32_t)(it % NB) * LY::kTile, kL}; };
     auto tR = [&](int slot, int term) {
@@ -195,8 +187,7 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
 
     // the loader's first lane sets up the barriers and sends for the first tiles at once; they are on their way while
     // the others form the powers and take tensor memory
-    LoadLedger<NA + 2 * NB> loads(bar(0));
-    static_assert(NA <= NB, "the first turn of every slot is sent for below");
+    LoadLedger<1 + 2 * NB> loads(bar(0));
     auto load = [&](int l, const CUtensorMap* map, const Tile& t, int it) {
         loads.note(l);
         mbar_expect_tx(bar(l), LY::kTile);
@@ -218,7 +209,7 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
         fence_proxy_async();
         for (int it = 0; it < NB && it < nchunks; ++it) {
             load(LB + it, &mB, tB(it), it);
-            if (it < NA) load(LA + it, &mA, tA(it), it);
+            if (OUT && it == 0) load(LA, &mA, tA, it);
             load(LC + it, &mC, tC(it), it);
         }
     }
@@ -358,16 +349,16 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
     } else if (OUT && warp == LY::kOuts) {
         // P, O2, O1, with an issuer of their own: a wait of one chain of products does not hold up the other
         const uint64_t dS = sdesc(dsm + LY::S, D * 128u, 1024u);
-        int sa = 0, sb = 0;
-        uint32_t pa = 0, pb = 0;
+        int sb = 0;
+        uint32_t pb = 0;
         for (int it = 0; it < nchunks; ++it) {
             const uint32_t ph = it & 1, before = ph ^ 1;
-            const uint64_t dA = sdesc(dsm + LY::A + (uint32_t)sa * LY::kTile, 16u, 1024u);
+            const uint64_t dA = sdesc(dsm + LY::A, 16u, 1024u);
             const uint64_t dB = sdesc(dsm + LY::B + (uint32_t)sb * LY::kTile, 16u, 1024u);
             const uint64_t dC = sdesc(dsm + LY::C + (uint32_t)sb * LY::kTile, kBlock, 1024u);
             // P, once the last chunk's P~ C has read its columns (and what it left there has been drained)
             if (it > 0 && !wait_warp(D == 64 ? DO : CO, before)) break;
-            if (!wait_warp(LA + sa, pa) || !wait_warp(LB + sb, pb)) break;
+            if (!wait_warp(LA, ph) || !wait_warp(LB + sb, pb)) break;
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
@@ -381,7 +372,7 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
             if (elect_one()) {
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) mma_bf16(tO2, along(dA, ks), down_rows(dS, ks), iAS, ks > 0);
-                mma_commit(bar(FA + sa));
+                mma_commit(bar(FA));
             }
             __syncwarp();
             // O1 = P~ C
@@ -395,7 +386,6 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
             }
             __syncwarp();
             if (++sb == NB) { sb = 0; pb ^= 1; }
-            if (++sa == NA1) { sa = 0; pa ^= 1; }
         }
         finish(FIN + 1);
     } else if (warp == LY::kLoader) {
@@ -407,10 +397,9 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
                     load(LB + sb, &mB, tB(it), it);
                     load(LC + sb, &mC, tC(it), it);
                 }
-                if (OUT && it >= NA) {
-                    const int sa = it % NA1, ua = it / NA1;
-                    if (!wait_bar(FA + sa, (uint32_t)(ua - 1) & 1)) break;
-                    load(LA + sa, &mA, tA(it), it);
+                if (OUT) {
+                    if (!wait_bar(FA, (uint32_t)(it - 1) & 1)) break;
+                    load(LA, &mA, tA, it);
                 }
             }
             if (!loads.settle()) atomicExch(p.status, (int)kDevWaitTimeout);
@@ -662,7 +651,7 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CU
                 if (OUT) {
                     if (!update(it)) break;
                     if (it + 1 < nchunks) {
-                        if (!wait_bar(FA + it % NA1, (uint32_t)(it / NA1) & 1)) break;  // A S has read the copy
+                        if (!wait_bar(FA, ph)) break;  // A S has read the copy
                         copy_state();
                     }
                 } else if (it > 0 && !update(it - 1)) {  // the previous chunk's, beside this one's products

@@ -453,7 +453,9 @@ HLA2_API int hla2_gated_step(float* state, const void* x, const void* g, void* o
  * fp32 inputs are computed in fp32.  bf16 inputs of 16-byte steps (widths, strides
  * and pointers) run on the tensor cores: there the scores within a block of 128
  * tokens and the state that enters the block are rounded to bf16 where they are
- * multiplied; the state itself is kept in fp32.  An infinity or NaN in a token's k
+ * multiplied, and what a block adds to a state keeps 16 bits of each decayed key (24
+ * where the state leaves the walk, so that the last bits of O may depend on whether
+ * state_out is given); the state itself is kept in fp32.  An infinity or NaN in a token's k
  * or v reaches all outputs of its block of 128 tokens, the earlier ones too, and
  * those behind.  Sums are joined in a fixed order: the same call gives the same bits.
  * Errors: HLA2_ERR_INVALID, HLA2_ERR_UNSUPPORTED (d or dv > 128, B*H > 65535,
@@ -557,10 +559,11 @@ HLA2_API int hla2_rmsnorm_backward(const void* S, const void* dY, const void* W,
  *   act         HLA2_ACT_NONE or HLA2_ACT_SILU.
  *   workspace   hla2_groupnorm_workspace(..., 0) bytes, 16-byte aligned, not
  *               initialised; NULL when that is 0.  It serves one call at a time.
- * All sums are fp32 or 64 bits, in a fixed order; the variance is that of the values about their mean.
- * Values stay below about 1e18.
+ * All sums are fp32, long ones in pieces or with their rounding errors kept, in a fixed order; the
+ * variance is that of the values about their mean.  Values stay below about 1e18.  silu counts as
+ * zero below -87.3, where it is above -1.1e-36.
  * Errors: HLA2_ERR_INVALID (G not a divisor of C among them), HLA2_ERR_UNSUPPORTED
- * (C > 16384, N*L or N*G > 2^31 - 1, types), HLA2_ERR_WORKSPACE, HLA2_ERR_LAUNCH.
+ * (C > 16384, N*L > 2^31 - 1, N*G > 2^31 - 2^16, types), HLA2_ERR_WORKSPACE, HLA2_ERR_LAUNCH.
  */
 HLA2_API size_t hla2_groupnorm_workspace(long long N, int L, int C, int G, int backward);
 HLA2_API int hla2_groupnorm(const void* X, const void* W, const void* Bias, const void* gate, void* Y, float* stats,
