@@ -888,7 +888,7 @@ def hla2_linear_forward(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, gamma
     not given.
 
     ``lengths`` [B] int32: the tokens of each sequence; what stands behind them is
-    not used and O is left as it was there.
+    not used and O is left as it was there (zeros when it is not given).
     ``state_in`` / ``state_out`` [B,H,d,dv] fp32: S before and after (one tensor may be both);
     decoding goes on with hla2_linear_step."""
     B, H, T, d, dv, code = _linear_inputs(Q, K, V, gamma, lengths, workspace, state_in=state_in, state_out=state_out)
@@ -898,7 +898,7 @@ def hla2_linear_forward(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, gamma
     L = _lib or lib()
     with _guard(dev, stream):
         if O is None:
-            O = _like(V)
+            O = _like(V) if lengths is None else _like(V).zero_()
         workspace, nws = _linear_work(workspace, B, H, T, d, dv, dev)
         rc = L.hla2_linear_forward(Q.data_ptr(), K.data_ptr(), V.data_ptr(), gamma.data_ptr(), _ptr(lengths),
                                    _ptr(state_in), O.data_ptr(), _ptr(state_out), B, H, T, d, dv,

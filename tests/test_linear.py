@@ -785,3 +785,31 @@ def test_as_many_heads_as_there_may_be(dtype):
     x = make(257, 255, 3, 8, 8, dtype)
     check_forward(x)
     check_backward(x)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_new_output_of_a_padded_batch_is_zero_behind_the_ends(dtype):
+    """Not what the memory held: a norm's weight gradient behind it sums over all rows."""
+    x = dev(make(3, 2, 500, 64, 64, dtype, "bthd"))
+    junk = torch.full_like(x["v"], float("nan"))
+    del junk  # what the next output of this size is made of
+    lens = torch.tensor([0, 130, 499], dtype=torch.int32).cuda()
+    o = hla2.hla2_linear_forward(x["q"], x["k"], x["v"], x["gamma"], lengths=lens, state_in=x["h0"])
+    assert bool(torch.isfinite(o).all()) and all(not bool(o[i, :, n:].any()) for i, n in enumerate((0, 130, 499)))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [40, 1500])
+def test_sliding_windows(T):
+    """Inputs whose rows overlap in memory: token t's channels begin eight behind token t - 1's."""
+    H, d = 2, 64
+    gen = torch.Generator().manual_seed(3)
+    flat = (torch.randn(4, H, 8 * T + d, generator=gen) * 0.3).to(BF)
+    cuda = flat.cuda()
+    wide = lambda t, i: t[i].as_strided((1, H, T, d), (t.stride(0), t.stride(1), 8, 1), t[i].storage_offset())
+    x = {**make(1, H, T, d, d, BF), **{n: wide(flat, i) for i, n in enumerate(("q", "k", "v", "do"))}}
+    y = {**dev(x), **{n: wide(cuda, i) for i, n in enumerate(("q", "k", "v", "do"))}}
+    check_forward(x, None, y)
+    backward_near(x, y)
+
