@@ -468,9 +468,11 @@ __device__ __forceinline__ void load8(const T* p, int n, float (&v)[8]) {
     for (int j = 0; j < 8; ++j) v[j] = l.get(j);
 }
 // The gradient's sums of each channel of a run: dz n and dz, in the same pieces (a thousand equal terms added one
-// after another are off by 160 roundings, all to one side).
+// after another are off by 160 roundings, all to one side).  Three blocks to an SM where 80 registers hold it without
+// spills, two elsewhere (gradient of 512 maps of 1024 x 256, silu without a gate: 336 us by two, 468 by three; of
+// 8 x 4096 x 512 with a gate: 66 by three, 68 by two).
 template <typename T, bool VEC, bool GATE, bool SILU>
-__global__ void __launch_bounds__(kThreads) gnorm_sums_kernel(const GNormParams p) {
+__global__ void __launch_bounds__(kThreads, VEC && sizeof(T) == 2 && (GATE || !SILU) ? kRunBlocks : 2) gnorm_sums_kernel(const GNormParams p) {
     __shared__ float4 sofar[8][kThreads];  // two LongSums
     follow();
     const RunSpot r = run_spot(p);
