@@ -188,6 +188,20 @@ __device__ __forceinline__ void unit_sum(float& a, float& b, int tpr, float2* sh
     }
 }
 
+// A running sum with its rounding errors kept (64-bit sums would take 60 times as long here)
+struct LongSum {
+    float hi = 0.f, lo = 0.f;
+    __device__ __forceinline__ void add(float x) {
+        const float s = hi + x, t = s - hi;
+        lo += (hi - (s - t)) + (x - t);
+        hi = s;
+    }
+    __device__ __forceinline__ float value() const { return hi + lo; }
+};
+// Long sums are taken in pieces of this many terms, and the pieces so: a thousand equal terms added one after another
+// are off by 160 roundings, all to one side.
+constexpr int kPiece = 16;
+
 // --------------------------------------------- units in registers ----
 // A block keeps its groups and takes every gridDim.x-th run of samples: its
 // weights stay in registers, and the next samples' values are on their way.
@@ -262,11 +276,11 @@ __global__ void __launch_bounds__(kThreads, VEC ? kFwdBlocks : 2) gnorm_unit_ker
 
 // The gradient.  A block keeps its groups and takes every gridDim.x-th run of
 // samples, so that a thread's channels stay its own and dw and db add up in
-// registers; then the block's threads add theirs, one line of sums to a block.
+// registers, a piece at a time; then the block's threads add theirs, one line of sums to a block.
 template <typename T, bool VEC, bool GATE, bool SILU>
 __global__ void __launch_bounds__(kThreads, VEC ? kBwdBlocks : 1) gnorm_unit_bwd_kernel(const GNormParams p) {
     __shared__ float2 sh[2][kThreads / 32];
-    extern __shared__ float2 sums[];  // [unit of the block][value]
+    __shared__ float4 sofar[8][kThreads];  // dw and db of a thread's values, each as a LongSum
     follow();
     const int unit = threadIdx.x / p.tpr, lane = threadIdx.x % p.tpr;
     const int s = unit / p.gpb, g = blockIdx.y * p.gpb + unit % p.gpb;
@@ -288,8 +302,22 @@ __global__ void __launch_bounds__(kThreads, VEC ? kBwdBlocks : 1) gnorm_unit_bwd
     float w[8], b[8], dw[8] = {}, db[8] = {};
     at.weights(p.w, p.wdtype, c0, 1.f, w);
     at.weights(p.b, p.wdtype, c0, 0.f, b);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sofar[j][threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto keep = [&]() {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float4 f = sofar[j][threadIdx.x];
+            LongSum first{f.x, f.y}, second{f.z, f.w};
+            first.add(dw[j]);
+            second.add(db[j]);
+            sofar[j][threadIdx.x] = make_float4(first.hi, first.lo, second.hi, second.lo);
+            dw[j] = db[j] = 0.f;
+        }
+    };
     int turn = 0;
-    for (long long n0 = (long long)blockIdx.x * p.spb; n0 < p.N; n0 += step, turn ^= 1) {
+    for (long long n0 = (long long)blockIdx.x * p.spb; n0 < p.N; n0 += step, ++turn) {
+        if (turn && turn % kPiece == 0) keep();
         const long long n = n0 + s;
         const bool live = mine && n < p.N;
         float x[8], dy[8], z[8], dgate[8];
@@ -319,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, VEC ? kBwdBlocks : 1) gnorm_unit_bwd
                 m1 += dy[j];
                 m2 = fmaf(dy[j], x[j], m2);
             }
-        unit_sum<true>(m1, m2, p.tpr, sh[turn]);
+        unit_sum<true>(m1, m2, p.tpr, sh[turn & 1]);
         if (!live) continue;
         m1 *= inv;
         m2 *= inv;
@@ -328,23 +356,22 @@ __global__ void __launch_bounds__(kThreads, VEC ? kBwdBlocks : 1) gnorm_unit_bwd
         at.store(static_cast<T*>(p.y) + n * p.yn + c0, p.yl, x);
         if (GATE) at.store(static_cast<T*>(p.dz) + n * p.dzn + c0, p.dzl, dgate);
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        if (j < at.n) sums[unit * values + at.pos[VEC ? 0 : j] * p.cg + at.channel(j)] = make_float2(dw[j], db[j]);
+    keep();
     __syncthreads();
     float* const line = p.part + (long long)blockIdx.x * 2 * p.C;
     const int width = min(p.gpb, p.G - (int)blockIdx.y * p.gpb) * p.cg;
     for (int c = threadIdx.x; c < width; c += kThreads) {
         const int u = c / p.cg, ch = c - u * p.cg;
-        float a = 0.f, d = 0.f;
+        LongSum first, second;
         for (int i = 0; i < p.spb; ++i)
             for (int l = 0; l < p.L; ++l) {
-                const float2 v = sums[(i * p.gpb + u) * values + l * p.cg + ch];
-                a += v.x;
-                d += v.y;
+                const int e = l * p.cg + ch, t = (i * p.gpb + u) * p.tpr;
+                const float4 f = VEC ? sofar[e % 8][t + e / 8] : sofar[e / p.tpr][t + e % p.tpr];
+                first.add(f.x + f.y);
+                second.add(f.z + f.w);
             }
-        line[blockIdx.y * p.gpb * p.cg + c] = a;
-        line[p.C + blockIdx.y * p.gpb * p.cg + c] = d;
+        line[blockIdx.y * p.gpb * p.cg + c] = first.value();
+        line[p.C + blockIdx.y * p.gpb * p.cg + c] = second.value();
     }
 }
 
@@ -367,23 +394,12 @@ __device__ __forceinline__ RunSpot run_spot(const GNormParams& p) {
     r.live = r.row < r.rows ? min(8, p.C - r.c) : 0;
     return r;
 }
-// A running sum with its rounding errors kept (64-bit sums would take 60 times as long here)
-struct LongSum {
-    float hi = 0.f, lo = 0.f;
-    __device__ __forceinline__ void add(float x) {
-        const float s = hi + x, t = s - hi;
-        lo += (hi - (s - t)) + (x - t);
-        hi = s;
-    }
-    __device__ __forceinline__ float value() const { return hi + lo; }
-};
 // Mean and sum of squares about it of each channel of a run.  A thread takes its positions in pieces of kPiece, each
 // about its own first value, and joins them: with count n, mean and squares of what it has and m, mean + d, squares'
 // of a piece,  mean + d m / (n + m),  squares + squares' + d^2 n m / (n + m).  So a value far from the others
 // costs the digits of one piece, not of the run (a zero in front of 4096 values of 1000 +- 1 moved a variance by 2e-3
 // where the run was summed about it, by 4e-6 now), and long runs are sums of few levels.  What a thread has so
 // far waits in shared memory.
-constexpr int kPiece = 16;
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads, VEC ? kRunBlocks : 2) gnorm_moments_kernel(const GNormParams p) {
     __shared__ float4 sofar[8][kThreads];  // mean and squares, each as a LongSum
@@ -467,8 +483,7 @@ __device__ __forceinline__ void load8(const T* p, int n, float (&v)[8]) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = l.get(j);
 }
-// The gradient's sums of each channel of a run: dz n and dz, in the same pieces (a thousand equal terms added one
-// after another are off by 160 roundings, all to one side).  Three blocks to an SM where 80 registers hold it without
+// The gradient's sums of each channel of a run: dz n and dz, in pieces.  Three blocks to an SM where 80 registers hold it without
 // spills, two elsewhere (gradient of 512 maps of 1024 x 256, silu without a gate: 336 us by two, 468 by three; of
 // 8 x 4096 x 512 with a gate: 66 by three, 68 by two).
 template <typename T, bool VEC, bool GATE, bool SILU>
@@ -787,8 +802,7 @@ cudaError_t run_gnorm(GNormParams p, const GPlan& g, int dtype, bool vec, cudaSt
         if (g.unit) {
             const dim3 grid(g.blocks, (p.G + g.gpb - 1) / g.gpb);
             if (GRAD)
-                return launch_following(gnorm_unit_bwd_kernel<T, VEC, GATE, SILU>, grid, kThreads,
-                                        (size_t)g.spb * g.gpb * p.L * p.cg * sizeof(float2), s, false, p);
+                return launch_following(gnorm_unit_bwd_kernel<T, VEC, GATE, SILU>, grid, kThreads, 0, s, false, p);
             gnorm_unit_kernel<T, VEC, GATE, SILU><<<grid, kThreads, 0, s>>>(p);
             note_launches(1);
             return cudaGetLastError();

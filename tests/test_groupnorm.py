@@ -531,3 +531,20 @@ def test_offsets_beyond_32_bits(N, L, C, far, dtype, shift):
     near("dgate", dgate, want["dgate"])
     del room, y, dx, dgate
     torch.cuda.empty_cache()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("C,G,L", [(2048, 1, 0), (700, 2, 0), (96, 12, 20)])
+def test_weight_gradients_of_equal_terms_over_many_rows(C, G, L):
+    """dz constant: db is its multiple, off by the error of a sum of few levels, however many rows a thread adds."""
+    N = 300000 * 2048 // (C * max(L, 1))
+    gen = torch.Generator("cuda").manual_seed(0)
+    shape = (N, L, C) if L else (N, C)
+    x = torch.empty(shape, device="cuda").normal_(generator=gen)
+    dy, z = (torch.full((C,), v, device="cuda").expand(shape) for v in (0.1, 0.3))
+    stats = torch.empty(N, G, 2, device="cuda")
+    hla2.hla2_groupnorm(x, G, gate=z, activation="silu", stats=stats, Y=torch.empty_like(x))
+    _, dw, db, _ = hla2.hla2_groupnorm_backward(x, dy, stats, gate=z, activation="silu")
+    t = float(torch.tensor(0.1).double() * torch.nn.functional.silu(torch.tensor(0.3).double()))
+    assert float((db.double() / (t * N * max(L, 1)) - 1).abs().max()) <= 60 * U
+    assert bool(torch.isfinite(dw).all())
