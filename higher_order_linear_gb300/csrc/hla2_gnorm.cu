@@ -440,7 +440,8 @@ __global__ void __launch_bounds__(kThreads, VEC ? kRunBlocks : 2) gnorm_moments_
                 const float4 f = sofar[j][threadIdx.x];
                 LongSum mean{f.x, f.y}, squares{f.z, f.w};
                 const float shift = a[j] * inv, d = (pivot.get(j) - mean.hi) + (shift - mean.lo);
-                squares.add(fmaf(d * d, done * part, fmaxf(fmaf(-a[j], shift, q[j]), 0.f)));
+                // (d is the value itself in the first piece: its square, which counts nothing there, is not formed)
+                squares.add(fmaf(d * part, d * done, fmaxf(fmaf(-a[j], shift, q[j]), 0.f)));
                 mean.add(d * part);
                 sofar[j][threadIdx.x] = make_float4(mean.hi, mean.lo, squares.hi, squares.lo);
             }

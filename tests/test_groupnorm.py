@@ -548,3 +548,12 @@ def test_weight_gradients_of_equal_terms_over_many_rows(C, G, L):
     t = float(torch.tensor(0.1).double() * torch.nn.functional.silu(torch.tensor(0.3).double()))
     assert float((db.double() / (t * N * max(L, 1)) - 1).abs().max()) <= 60 * U
     assert bool(torch.isfinite(dw).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", [(5, 0, 512, 4), (2, 2000, 32, 2), (500, 2100, 2, 2)])
+def test_mean_whose_square_overflows(shape):
+    """Deviations of 1e16 about 3e19: no square of a value itself is formed."""
+    x = make(*shape, F32, False, F32, shift=0.0)
+    x["x"] = x["x"] * 1e16 + 3e19
+    check(x, "none")
