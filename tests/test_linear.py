@@ -813,3 +813,34 @@ def test_sliding_windows(T):
     check_forward(x, None, y)
     backward_near(x, y)
 
+
+
+@pytest.mark.gpu
+def test_calls_at_once():
+    """Calls of several widths, types and operators on three streams, each with memory of its own: the bits of each alone."""
+    xs = [dev(make(B, H, T, d, d, dtype)) for B, H, T, d, dtype in
+          ((2, 8, 2100, 64, BF), (1, 4, 3000, 128, BF), (1, 3, 500, 40, F32))]
+
+    def run(x):
+        last, d0 = torch.empty_like(x["h0"]), torch.empty_like(x["h0"])
+        args = (x["q"], x["k"], x["v"], x["gamma"])
+        o = hla2.hla2_linear_forward(*args, state_in=x["h0"], state_out=last)
+        rows = o.transpose(1, 2).reshape(-1, o.shape[1] * o.shape[3])
+        stats = torch.empty(rows.shape[0], o.shape[1], 2, device="cuda")
+        n = hla2.hla2_groupnorm(rows, o.shape[1], gate=rows, activation="silu", stats=stats)
+        dx, dw, _, _ = hla2.hla2_groupnorm_backward(rows, n, stats, gate=rows, activation="silu")
+        return (o, last, n, dx, dw, *hla2.hla2_linear_backward(*args, x["do"], state_in=x["h0"], dstate_out=x["dlast"],
+                                                               dstate_in=d0), d0)
+
+    want = [run(x) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    seen = []
+    for _ in range(20):
+        for x, s in zip(xs, streams):
+            with torch.cuda.stream(s):
+                seen.append(run(x))
+    torch.cuda.synchronize()
+    for i, got in enumerate(seen):
+        assert all(torch.equal(a, b) for a, b in zip(got, want[i % 3]))
+    assert hla2.hla2_device_status() == 0
